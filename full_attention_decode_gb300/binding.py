@@ -82,6 +82,15 @@ class qwen35_gdn_state(C.Structure):
     _fields_ = [("conv_state", C.c_void_p), ("gdn_state", C.c_void_p)]
 
 
+class qwen35_cache_rows(C.Structure):
+    _fields_ = [("row_start", C.c_void_p), ("pos", C.c_void_p), ("n_seqs", C.c_uint32), ("n_rows", C.c_uint32),
+                ("num_blocks", C.c_uint32), ("reserved", C.c_uint32)]
+
+
+class qwen35_key_bounds(C.Structure):
+    _fields_ = [("lo_hi", C.c_void_p), ("block", C.c_uint32), ("reserved", C.c_uint32)]
+
+
 class qwen35_layer(C.Structure):
     _fields_ = [("kind", C.c_int32), ("fa", C.POINTER(qwen35_fa_layer)), ("kv", C.POINTER(qwen35_kv_cache)),
                 ("gdn", C.POINTER(qwen35_gdn_layer)), ("state", C.POINTER(qwen35_gdn_state))]
@@ -134,6 +143,18 @@ _SIGS = {
                                                   C.c_size_t, C.POINTER(qwen35_gdn_state), _P, _P, _U, _P]),
     "qwen35_prefill_step": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_layer), _U, _P, C.c_size_t,
                                       _P, _P, _U, _U, _P]),
+    "qwen35_cache_scratch_bytes": (C.c_size_t, [C.POINTER(qwen35_config), _U, _U, _U]),
+    "qwen35_cache_append": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
+                                      C.POINTER(qwen35_cache_rows), C.POINTER(qwen35_key_bounds), _P, _P, _P,
+                                      C.c_size_t, _P]),
+    "qwen35_cache_read": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
+                                    C.POINTER(qwen35_cache_rows), _P, _P, _P, C.c_size_t, _P]),
+    "qwen35_select_blocks": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
+                                       C.POINTER(qwen35_cache_rows), C.POINTER(qwen35_key_bounds), _P, _U, _U, _U,
+                                       _P, _P, C.c_size_t, _P]),
+    "qwen35_decode_attention": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
+                                          C.POINTER(qwen35_cache_rows), _P, _P, _U, _P, _U, _U, _P, _P, C.c_size_t,
+                                          _P]),
     "qwen35_debug_scratch_offset": (C.c_size_t, [C.POINTER(qwen35_config), C.c_int, C.c_char_p]),
     "qwen35_debug_stack_scratch_offset": (C.c_size_t, [C.POINTER(qwen35_config), C.c_char_p]),
     "qwen35_debug_stage_dump": (C.c_int, [C.c_int]),
@@ -355,6 +376,38 @@ def qwen35_lm_head_greedy(cfg, final_norm, lm_head, x, logits, token, scratch, s
                                        _ptr(token), _ptr(scratch), scratch.numel(), _stream(stream))
 
 
+def qwen35_cache_scratch_bytes(cfg: qwen35_config, capacity: int, block: int, max_rows: int) -> int:
+    return lib().qwen35_cache_scratch_bytes(C.byref(cfg), capacity, block, max_rows)
+
+
+def qwen35_cache_append(cfg, kv, rows, bounds, k, v, scratch, stream=None):
+    """rows: a DeviceRows; bounds: a DeviceKeyBounds, or None."""
+    return lib().qwen35_cache_append(C.byref(cfg), C.byref(kv), C.byref(rows.struct),
+                                     C.byref(bounds.struct) if bounds is not None else None, _ptr(k), _ptr(v),
+                                     _ptr(scratch), scratch.numel(), _stream(stream))
+
+
+def qwen35_cache_read(cfg, kv, rows, k, v, scratch, stream=None):
+    return lib().qwen35_cache_read(C.byref(cfg), C.byref(kv), C.byref(rows.struct), _ptr(k), _ptr(v), _ptr(scratch),
+                                   scratch.numel(), _stream(stream))
+
+
+def qwen35_select_blocks(cfg, kv, rows, bounds, q, blocks, scratch, n_first: int = 1, n_last: int = 1, stream=None):
+    """blocks: int32 [n_rows][num_kv_heads][n_select], written."""
+    return lib().qwen35_select_blocks(C.byref(cfg), C.byref(kv), C.byref(rows.struct), C.byref(bounds.struct), _ptr(q),
+                                      blocks.shape[-1], n_first, n_last, _ptr(blocks), _ptr(scratch), scratch.numel(),
+                                      _stream(stream))
+
+
+def qwen35_decode_attention(cfg, kv, rows, q, out, scratch, gate=None, gate_stride: int = 0, blocks=None,
+                            block: int = 0, stream=None):
+    """gate_stride 0: the gate's rows lie head_dim apart. blocks: int32 [n_rows][num_kv_heads][n_blocks], or None."""
+    return lib().qwen35_decode_attention(C.byref(cfg), C.byref(kv), C.byref(rows.struct), _ptr(q), _ptr(gate),
+                                         gate_stride or cfg.head_dim, _ptr(blocks),
+                                         blocks.shape[-1] if blocks is not None else 0, block, _ptr(out),
+                                         _ptr(scratch), scratch.numel(), _stream(stream))
+
+
 def qwen35_debug_scratch_offset(cfg, kind, name: str) -> int:
     return lib().qwen35_debug_scratch_offset(C.byref(cfg), kind, name.encode())
 
@@ -556,6 +609,27 @@ class DeviceKvPaged:
     def logical(self, which: str, b: int = 0) -> np.ndarray:
         from . import synth
         return synth.paged_gather(self.pool(which), self.table_np[b], self.block_tokens)
+
+
+class DeviceRows:
+    """The rows of a cache operator's call: pos [n_seqs] and row_start [n_seqs + 1] (or
+    None: one row a sequence), int32 device tensors that may change between calls."""
+
+    def __init__(self, pos, row_start=None, n_rows: int | None = None, num_blocks: int = 0):
+        self.pos, self.row_start = pos, row_start
+        n_seqs = pos.numel()
+        if row_start is not None and n_rows is None:
+            raise ValueError("n_rows is needed with row_start")
+        self.struct = qwen35_cache_rows(_ptr(row_start), pos.data_ptr(), n_seqs, n_seqs if n_rows is None else n_rows,
+                                        num_blocks, 0)
+
+
+class DeviceKeyBounds:
+    """Key bounds of a cache, bf16 (or int16 bits) [cache rows / block][Hkv][2][D]."""
+
+    def __init__(self, lo_hi, block: int):
+        self.lo_hi, self.block = lo_hi, block
+        self.struct = qwen35_key_bounds(lo_hi.data_ptr(), block, 0)
 
 
 class DeviceStateBatch:

@@ -13,6 +13,7 @@
 #include <new>
 
 #include "qwen35_decode.h"  // include/ (on the include path)
+#include "cache_ops.h"
 #include "common.cuh"
 #include "decode.h"
 #include "prefill.h"
@@ -1103,6 +1104,194 @@ int qwen35_prefill_step(const qwen35_config* cfg, const qwen35_layer* layers, ui
                                               : pf_gdn(c, L.gdn, L.state, xi, x_out);
   }
   return r;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- cache operators
+
+namespace {
+
+// Scratch of the cache operators: the status word, then their work space.
+constexpr size_t kCacheWork = 256;
+struct CacheNeed {
+  size_t scores, exact, most, total;
+};
+CacheNeed cache_need(uint32_t Hkv, uint32_t nblk, uint32_t n_rows) {
+  CacheNeed n = {};
+  const size_t items = (size_t)n_rows * Hkv;
+  auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+  n.exact = kCacheWork;
+  n.scores = n.exact + up(items * nblk * 8);
+  n.most = n.scores + up(items * nblk * 4);
+  n.total = n.most + up(items * 4);
+  return n;
+}
+
+// The head counts and dims the cache operators take (the other fields of the config
+// are not read).
+int cache_dims(const qwen35_config* c) {
+  if (!c || c->num_heads == 0 || c->num_kv_heads == 0 || c->num_heads % c->num_kv_heads)
+    return QWEN35_ERR_INVALID_ARGUMENT;
+  if (c->head_dim != 64 && c->head_dim != 128 && c->head_dim != 256) return QWEN35_ERR_UNSUPPORTED;
+  if (c->num_kv_heads > 8 || c->num_heads / c->num_kv_heads > q35c::kMaxGroup) return QWEN35_ERR_UNSUPPORTED;
+  return QWEN35_OK;
+}
+
+bool power_of_two(uint32_t x) { return x && !(x & (x - 1)); }
+uint32_t log2_of(uint32_t x) {
+  uint32_t s = 0;
+  while ((1u << s) < x) ++s;
+  return s;
+}
+
+// What every cache operator checks: dims, cache, rows, scratch.
+int cache_begin(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                uint32_t max_rows, void* scratch, size_t scratch_bytes, q35c::Cache& c, q35c::Rows& r) {
+  const int e = cache_dims(cfg);
+  if (e) return e;
+  if (!kv || !rows || !aligned16(kv->k) || !aligned16(kv->v) || kv->capacity == 0 || kv->capacity > (1u << 31))
+    return QWEN35_ERR_INVALID_ARGUMENT;
+  if (kv->dtype != QWEN35_KV_BF16 && kv->dtype != QWEN35_KV_TURBO8) return QWEN35_ERR_INVALID_ARGUMENT;
+  c = {};
+  c.k = static_cast<uint8_t*>(kv->k);
+  c.v = static_cast<uint8_t*>(kv->v);
+  c.capacity = kv->capacity;
+  c.Hkv = cfg->num_kv_heads;
+  c.D = cfg->head_dim;
+  if (kv->dtype == QWEN35_KV_TURBO8) {
+    if (!aligned16(kv->k_scales) || !aligned16(kv->v_scales)) return QWEN35_ERR_INVALID_ARGUMENT;
+    c.ks = kv->k_scales;
+    c.vs = kv->v_scales;
+    c.sstride = (c.Hkv * c.D / 16 + 7) / 8 * 8;
+  }
+  if (kv->block_table) {
+    const uint32_t bt = kv->block_tokens;
+    if (((uintptr_t)kv->block_table % 4) || bt < 8 || !power_of_two(bt) || kv->capacity % bt || rows->num_blocks == 0)
+      return QWEN35_ERR_INVALID_ARGUMENT;
+    c.btab = kv->block_table;
+    c.bt_shift = log2_of(bt);
+    c.num_blocks = rows->num_blocks;
+  }
+  if (rows->n_seqs == 0 || rows->n_rows == 0 || !rows->pos || ((uintptr_t)rows->pos % 4) ||
+      ((uintptr_t)rows->row_start % 4))
+    return QWEN35_ERR_INVALID_ARGUMENT;
+  if (!rows->row_start && rows->n_rows != rows->n_seqs) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (rows->n_seqs > q35c::kMaxSeqs || rows->n_rows > max_rows) return QWEN35_ERR_UNSUPPORTED;
+  r = {rows->row_start, rows->pos, rows->n_seqs, rows->n_rows};
+  if (!aligned16(scratch) || scratch_bytes < kCacheWork) return QWEN35_ERR_INVALID_ARGUMENT;
+  return QWEN35_OK;
+}
+
+// A selection block: a power of two of 16 to 1024 tokens that divides the capacity and a
+// paged cache's blocks.
+bool sel_block_ok(const qwen35_kv_cache* kv, uint32_t block) {
+  if (block < 16 || block > 1024 || !power_of_two(block) || kv->capacity % block) return false;
+  return !kv->block_table || kv->block_tokens % block == 0;
+}
+int bounds_ok(const qwen35_kv_cache* kv, const qwen35_key_bounds* b) {
+  return aligned16(b->lo_hi) && sel_block_ok(kv, b->block) ? QWEN35_OK : QWEN35_ERR_INVALID_ARGUMENT;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qwen35_cache_scratch_bytes(const qwen35_config* cfg, uint32_t capacity, uint32_t block, uint32_t max_rows) {
+  if (cache_dims(cfg) || capacity == 0 || max_rows == 0 || max_rows > q35c::kMaxRows) return 0;
+  if (block && (block < 16 || block > 1024 || !power_of_two(block))) return 0;
+  const uint32_t rows = max_rows < q35c::kMaxQueries ? max_rows : q35c::kMaxQueries;
+  return cache_need(cfg->num_kv_heads, block ? capacity / block : 0, rows).total;
+}
+
+int qwen35_cache_append(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                        const qwen35_key_bounds* bounds, const qwen35_bf16* k, const qwen35_bf16* v, void* scratch,
+                        size_t scratch_bytes, void* stream) {
+  q35c::Append a = {};
+  int r = cache_begin(cfg, kv, rows, q35c::kMaxRows, scratch, scratch_bytes, a.c, a.r);
+  if (r) return r;
+  if (!aligned16(k) || !aligned16(v)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (bounds) {
+    if ((r = bounds_ok(kv, bounds))) return r;
+    a.bounds = bounds->lo_hi;
+    a.blk_shift = log2_of(bounds->block);
+  }
+  if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  a.k = k;
+  a.v = v;
+  a.status = static_cast<int*>(scratch);
+  return cu(q35c::append(a, (cudaStream_t)stream));
+}
+
+int qwen35_cache_read(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                      qwen35_bf16* k, qwen35_bf16* v, void* scratch, size_t scratch_bytes, void* stream) {
+  q35c::Read a = {};
+  const int r = cache_begin(cfg, kv, rows, q35c::kMaxRows, scratch, scratch_bytes, a.c, a.r);
+  if (r) return r;
+  if (!aligned16(k) || !aligned16(v)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  a.k = k;
+  a.v = v;
+  a.status = static_cast<int*>(scratch);
+  return cu(q35c::read(a, (cudaStream_t)stream));
+}
+
+int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                         const qwen35_key_bounds* bounds, const qwen35_bf16* q, uint32_t n_select, uint32_t n_first,
+                         uint32_t n_last, int32_t* blocks, void* scratch, size_t scratch_bytes, void* stream) {
+  q35c::Select a = {};
+  int r = cache_begin(cfg, kv, rows, q35c::kMaxQueries, scratch, scratch_bytes, a.c, a.r);
+  if (r) return r;
+  if (!bounds) return QWEN35_ERR_INVALID_ARGUMENT;
+  if ((r = bounds_ok(kv, bounds))) return r;
+  if (!aligned16(q) || !blocks || ((uintptr_t)blocks % 4) || n_select == 0) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (n_select > kv->capacity / bounds->block) return QWEN35_ERR_INVALID_ARGUMENT;
+  a.nblk = kv->capacity / bounds->block;
+  const CacheNeed need = cache_need(a.c.Hkv, a.nblk, a.r.n_rows);
+  if (scratch_bytes < need.total) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  uint8_t* s = static_cast<uint8_t*>(scratch);
+  a.bounds = bounds->lo_hi;
+  a.q = q;
+  a.blocks = blocks;
+  a.scores = reinterpret_cast<float*>(s + need.scores);
+  a.exact = reinterpret_cast<double*>(s + need.exact);
+  a.most = reinterpret_cast<float*>(s + need.most);
+  a.H = cfg->num_heads;
+  a.blk_shift = log2_of(bounds->block);
+  a.n_select = n_select;
+  a.n_first = n_first;
+  a.n_last = n_last;
+  a.status = static_cast<int*>(scratch);
+  return cu(q35c::select(a, (cudaStream_t)stream));
+}
+
+int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                            const qwen35_bf16* q, const qwen35_bf16* gate, uint32_t gate_stride, const int32_t* blocks,
+                            uint32_t n_blocks, uint32_t block, qwen35_bf16* out, void* scratch, size_t scratch_bytes,
+                            void* stream) {
+  q35c::Attend a = {};
+  const int r = cache_begin(cfg, kv, rows, q35c::kMaxQueries, scratch, scratch_bytes, a.c, a.r);
+  if (r) return r;
+  if (!aligned16(q) || !aligned16(out)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (gate && (!aligned16(gate) || gate_stride < a.c.D || gate_stride % 8)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (blocks) {
+    if (((uintptr_t)blocks % 4) || !sel_block_ok(kv, block) || n_blocks == 0 || n_blocks > kv->capacity / block)
+      return QWEN35_ERR_INVALID_ARGUMENT;
+    a.blocks = blocks;
+    a.n_blocks = n_blocks;
+    a.blk_shift = log2_of(block);
+  } else if (n_blocks != 0) {
+    return QWEN35_ERR_INVALID_ARGUMENT;
+  }
+  if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  a.q = q;
+  a.gate = gate;
+  a.gate_stride = gate_stride;
+  a.out = out;
+  a.H = cfg->num_heads;
+  a.status = static_cast<int*>(scratch);
+  return cu(q35c::attend(a, (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -1,0 +1,48 @@
+// Where a call's rows and a cache's tokens are (device side of cache_ops.h). Whatever
+// the arrays in device memory hold, no address outside the cache is formed: a position
+// outside [0, capacity), a row count that runs backwards or a table entry outside the
+// pool makes the caller skip the access and set the range status.
+#pragma once
+
+#include "cache_ops.h"
+#include "common.cuh"
+
+namespace q35c {
+
+enum RowKind { kRowOk = 0, kRowSkip = 1, kRowBad = 2 };
+
+// Row r's sequence and position; kRowSkip for a row no sequence has.
+__device__ __forceinline__ RowKind locate(const Rows& w, uint32_t capacity, uint32_t r, uint32_t& seq, uint32_t& pos) {
+  int64_t i = 0;
+  if (!w.row_start) {
+    seq = r;
+  } else {
+    if ((int64_t)r < w.row_start[0] || (int64_t)r >= w.row_start[w.n_seqs]) return kRowSkip;
+    uint32_t lo = 0, hi = w.n_seqs;  // row_start[lo] <= r < row_start[hi]
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (w.row_start[mid] <= (int64_t)r) lo = mid;
+      else hi = mid;
+    }
+    seq = lo;
+    i = (int64_t)r - w.row_start[lo];
+  }
+  const int64_t p = (int64_t)w.pos[seq] + i;
+  if (w.pos[seq] < 0 || i < 0 || p >= (int64_t)capacity) return kRowBad;
+  pos = (uint32_t)p;
+  return kRowOk;
+}
+
+// The cache row of token t (< capacity) of a sequence; false for a block outside the pool.
+__device__ __forceinline__ bool cache_row(const Cache& c, uint32_t seq, uint32_t t, size_t& row) {
+  if (!c.btab) {
+    row = (size_t)seq * c.capacity + t;
+    return true;
+  }
+  const uint32_t blk = (uint32_t)c.btab[(size_t)seq * (c.capacity >> c.bt_shift) + (t >> c.bt_shift)];
+  if (blk >= c.num_blocks) return false;
+  row = ((size_t)blk << c.bt_shift) | (t & ((1u << c.bt_shift) - 1u));
+  return true;
+}
+
+}  // namespace q35c

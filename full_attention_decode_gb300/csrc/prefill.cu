@@ -11,11 +11,10 @@
 
 #include "common.cuh"
 #include "prefill.h"
+#include "turbo8.cuh"
 
 #include <algorithm>
 #include <type_traits>
-
-#include <cuda_fp16.h>
 
 namespace q35pf {
 using namespace q35;
@@ -356,18 +355,6 @@ __global__ void gemm_finish_kernel(const Gemm g, uint32_t splits) {
 
 // ------------------------------------------------------------------ norms
 
-// Eight bf16 values of a 16-byte word as floats, and back (round to nearest even).
-__device__ __forceinline__ void unpack8(const uint4 u, float* x) {
-  x[0] = bf16lo(u.x); x[1] = bf16hi(u.x); x[2] = bf16lo(u.y); x[3] = bf16hi(u.y);
-  x[4] = bf16lo(u.z); x[5] = bf16hi(u.z); x[6] = bf16lo(u.w); x[7] = bf16hi(u.w);
-}
-__device__ __forceinline__ uint4 pack8(const float* x) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) w[i] = (uint32_t)to_bf16(x[2 * i]) | ((uint32_t)to_bf16(x[2 * i + 1]) << 16);
-  return make_uint4(w[0], w[1], w[2], w[3]);
-}
-
 __device__ __forceinline__ float block_sum(float v, float* red) {
   v = warp_sum(v);
   const uint32_t warp = threadIdx.x >> 5, nw = blockDim.x >> 5;
@@ -458,16 +445,6 @@ __device__ __forceinline__ void wht_lanes(float* x, uint32_t lane, float norm) {
     }
 #pragma unroll
   for (int e = 0; e < EPL; ++e) x[e] *= norm;
-}
-__device__ __forceinline__ uint32_t e4m3_pair(float x0, float x1) {  // x0 in the low byte
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(x1), "f"(x0));
-  return r;
-}
-__device__ __forceinline__ float2 e4m3_pair_value(uint32_t two) {
-  uint32_t h2;
-  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)two));
-  return __half22float2(*reinterpret_cast<const __half2*>(&h2));
 }
 // Quantise the warp's row (bf16 values in x): per group of 16 elements (16 / EPL
 // lanes) scale = bf16(amax / 448), code = E4M3(x / scale) rounded to nearest even

@@ -434,6 +434,126 @@ QWEN35_API int qwen35_lm_head_greedy(const qwen35_config* cfg, const qwen35_bf16
                                      const qwen35_qweight* lm_head, const qwen35_bf16* x, qwen35_bf16* logits,
                                      int32_t* token, void* scratch, size_t scratch_bytes, void* stream);
 
+/* ---------------------------------------------------------------- cache operators
+ *
+ * What a serving loop does with KV caches outside the layer forwards, each call for
+ * any number of sequences: rows written to a cache and read back, blocks of a long
+ * cache chosen by a cheap score, and the attention of the new tokens over the whole
+ * cache or over the chosen blocks. One decode step of such a loop is
+ * qwen35_cache_append, (qwen35_select_blocks,) qwen35_decode_attention; a captured
+ * graph of them decodes on as the caller advances the positions in device memory.
+ * The pages keep the append and the attention inside forward_full_attention
+ * ("full_attention.rs") and leave sparse attention out; rounding, rotation and
+ * formats here are that forward's, so a cache may pass between these calls, the
+ * layer forwards and the prefill.
+ *
+ * Of the config only num_heads, num_kv_heads and head_dim are read: head_dim 64, 128
+ * or 256, at most 8 kv-heads of at most 16 q-heads each (UNSUPPORTED otherwise).
+ * The cache may be bf16 or Turbo8 and, unlike in the layer forwards, either may be
+ * paged: a paged Turbo8 cache has its codes in pools as a bf16 cache has its rows,
+ * its scales in pools [num_blocks][block_tokens][sstride]. A contiguous cache holds
+ * sequence b's rows at b * capacity, a paged one sequence b's table at
+ * b * (capacity / block_tokens). capacity: at most 2^31 tokens; a sequence's arrays
+ * may pass 2^32 bytes.
+ *
+ * Scratch: qwen35_cache_scratch_bytes, made with qwen35_scratch_init and not shared
+ * with the layer forwards. It belongs to one call at a time: calls (or replays of
+ * graphs that hold them) that overlap on the GPU need one each.
+ *
+ * The rows of a call: sequence b's tokens are rows [row_start[b], row_start[b + 1])
+ * of every [n_rows][...] argument, at positions pos[b], pos[b] + 1, ... (pos[b]: how
+ * many tokens the cache held before them). row_start NULL: one row a sequence
+ * (n_rows == n_seqs). A sequence may have no row (row_start[b + 1] ==
+ * row_start[b]); rows before row_start[0] or from row_start[n_seqs] on are left as they were.
+ * row_start [n_seqs + 1] and pos [n_seqs] lie in device memory and are read when the
+ * kernels run. A row whose position is outside [0, capacity), or whose token (any of
+ * its tokens, for the attention and the selection) lies in a block outside
+ * [0, num_blocks), sets QWEN35_ERR_DEVICE_RANGE in the status word; nothing outside
+ * the cache is touched, the row is skipped, or computed without that block.
+ * num_blocks: the pool's size (paged only). At most 4096 sequences; at most 2^20 rows
+ * for append and read, 4096 for selection and attention. Sequences of one call may
+ * share blocks that the call does not write. */
+typedef struct qwen35_cache_rows {
+    const int32_t* row_start;
+    const int32_t* pos;
+    uint32_t n_seqs, n_rows;
+    uint32_t num_blocks;
+    uint32_t reserved;
+} qwen35_cache_rows;
+
+/* Per selection block and kv-head, the smallest and the largest value of each key
+ * dimension over the block's tokens: lo_hi bf16 [cache rows / block][num_kv_heads][2]
+ * [head_dim] (lo, then hi), indexed by where the block lies in the cache arrays, so a
+ * block shared by sequences has one entry. block: tokens, a power of two of 16 to
+ * 1024 that divides capacity and, in a paged cache, block_tokens. The keys are the
+ * rows given to qwen35_cache_append (not rotated, before Turbo8 rounds them). */
+typedef struct qwen35_key_bounds {
+    qwen35_bf16* lo_hi;
+    uint32_t block;
+    uint32_t reserved;
+} qwen35_key_bounds;
+
+/* Scratch bytes for every call below with up to max_rows rows over caches of up to
+ * `capacity` tokens; block: tokens per selection block (0: no selection). 0 for
+ * dims or sizes the calls reject. */
+QWEN35_API size_t qwen35_cache_scratch_bytes(const qwen35_config* cfg, uint32_t capacity, uint32_t block,
+                                             uint32_t max_rows);
+
+/* Write rows to the cache: k, v bf16 [n_rows][num_kv_heads][head_dim] (keys already
+ * normed and rotated by position, as the cache keeps them). A bf16 cache takes them as they
+ * are; a Turbo8 cache takes bf16(WHT(x)) as codes and scales, bit for bit what the
+ * layer forwards append. bounds may be NULL; otherwise the bounds of every block that
+ * gets a row are brought up to date: a row at the first position of a block starts
+ * the block's bounds anew, other rows widen them (so the bounds are right while a
+ * sequence's rows come in order; a NaN never enters them unless a dimension has only
+ * NaN). Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
+QWEN35_API int qwen35_cache_append(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                                   const qwen35_key_bounds* bounds, const qwen35_bf16* k, const qwen35_bf16* v,
+                                   void* scratch, size_t scratch_bytes, void* stream);
+
+/* Read rows back: k, v bf16 [n_rows][num_kv_heads][head_dim], written. A bf16 cache's
+ * rows as they are; a Turbo8 cache's as bf16(WHT(scale * code)), the values they
+ * stand for in the basis they were given in. Errors as qwen35_cache_append. */
+QWEN35_API int qwen35_cache_read(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                                 qwen35_bf16* k, qwen35_bf16* v, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Choose blocks of the cache for every row and kv-head by the bounds: a row at
+ * position p sees blocks 0 .. p / block, and a block's score is the sum over the
+ * kv-head's q-heads of the largest q . k that a key inside the block's bounds could
+ * have, sum_h sum_d max(q_hd lo_d, q_hd hi_d). blocks int32 [n_rows][num_kv_heads]
+ * [n_select]: the n_select highest-scoring blocks in rising order, the lower index of
+ * equal scores, then -1 where fewer blocks are seen. The first n_first and the last
+ * n_last seen blocks come before all others. The choice is that of the exact
+ * scores: where 32-bit arithmetic cannot tell two blocks apart, 64 bits decide. A score
+ * that is not a number counts as -infinity. q bf16 [n_rows][num_heads][head_dim], in
+ * the basis of the rows given to qwen35_cache_append. n_select: 1 to
+ * capacity / block. Errors as qwen35_cache_append. */
+QWEN35_API int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                                    const qwen35_key_bounds* bounds, const qwen35_bf16* q, uint32_t n_select,
+                                    uint32_t n_first, uint32_t n_last, int32_t* blocks, void* scratch,
+                                    size_t scratch_bytes, void* stream);
+
+/* Attention of each row (position p) over its sequence's tokens [0, p], its own
+ * included (so after qwen35_cache_append of the same rows), softmax(q . k /
+ * sqrt(head_dim)) v per q-head, kv-head h / (num_heads / num_kv_heads):
+ *  - q, out bf16 [n_rows][num_heads][head_dim]; for a Turbo8 cache q is rotated and
+ *    the output rotated back inside.
+ *  - gate: NULL, or bf16, head h of row r at gate + (r * num_heads + h) * gate_stride
+ *    (gate_stride >= head_dim, a multiple of 8: the [Q_h | gate_h] rows of q_proj give
+ *    2 * head_dim): the output is multiplied by sigmoid(gate).
+ *  - blocks: NULL (n_blocks 0): every token; or int32 [n_rows][num_kv_heads][n_blocks]
+ *    as qwen35_select_blocks writes them: only the tokens [0, p] in the listed blocks of
+ *    `block` tokens (16 to 1024, a power of two that divides capacity and, in a paged
+ *    cache, block_tokens). An entry that is negative or behind the row's last
+ *    block counts as none, one listed twice counts twice; a row without a token gets zeros.
+ * Sums, maxima and weights are held in fp32 and the output rounded to bf16 once. Keys with
+ * an infinity or NaN spoil only rows that see them. out must not overlap an input. Errors
+ * as qwen35_cache_append. */
+QWEN35_API int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,
+                                       const qwen35_cache_rows* rows, const qwen35_bf16* q, const qwen35_bf16* gate,
+                                       uint32_t gate_stride, const int32_t* blocks, uint32_t n_blocks, uint32_t block,
+                                       qwen35_bf16* out, void* scratch, size_t scratch_bytes, void* stream);
+
 /* Byte offset inside a layer's scratch of a named intermediate the last forward of
  * that kind left there, or (size_t)-1 for an unknown name: the counterpart of the
  * intra_dump hook of "linear_attention.rs" (named buffers readable after a stream
