@@ -23,6 +23,8 @@ using namespace q35;
 namespace {
 
 constexpr int kMaxDevices = 64;
+// What qwen35_scratch_init zeroes: the status word and every kind of scratch's counters.
+constexpr size_t kScratchZeroed = 8192;
 int g_num_sms[kMaxDevices] = {0};
 
 int num_sms() {
@@ -420,7 +422,8 @@ size_t qwen35_stack_scratch_bytes(const qwen35_config* cfg) {
 
 int qwen35_scratch_init(void* scratch, size_t scratch_bytes, void* stream) {
   if (!aligned16(scratch) || scratch_bytes < 256) return QWEN35_ERR_INVALID_ARGUMENT;
-  return cudaMemsetAsync(scratch, 0, 256, (cudaStream_t)stream) == cudaSuccess ? QWEN35_OK : QWEN35_ERR_CUDA;
+  const size_t n = scratch_bytes < kScratchZeroed ? scratch_bytes : kScratchZeroed;
+  return cudaMemsetAsync(scratch, 0, n, (cudaStream_t)stream) == cudaSuccess ? QWEN35_OK : QWEN35_ERR_CUDA;
 }
 
 int qwen35_read_device_status(const void* scratch, int32_t* host_status, void* stream) {
@@ -1112,8 +1115,10 @@ int qwen35_prefill_step(const qwen35_config* cfg, const qwen35_layer* layers, ui
 
 namespace {
 
-// Scratch of the cache operators: the status word, then their work space.
-constexpr size_t kCacheWork = 256;
+// Scratch of the cache operators: the status word, the attention's counters (zero between
+// calls), then the work space, the attention's or the selection's.
+constexpr size_t kCacheTickets = 256, kCacheWork = kCacheTickets + q35c::kMaxCtas * 4;
+static_assert(kCacheWork <= kScratchZeroed, "the counters are zeroed by qwen35_scratch_init");
 struct CacheNeed {
   size_t scores, exact, most, total;
 };
@@ -1126,6 +1131,14 @@ CacheNeed cache_need(uint32_t Hkv, uint32_t nblk, uint32_t n_rows) {
   n.most = n.scores + up(items * nblk * 4);
   n.total = n.most + up(items * 4);
   return n;
+}
+// CTAs of an attention (two an SM), and its scratch: two parts of a split item for each.
+uint32_t attend_ctas() {
+  const uint32_t n = 2u * (uint32_t)num_sms();
+  return n < q35c::kMaxCtas ? n : q35c::kMaxCtas;
+}
+size_t attend_need(uint32_t group, uint32_t D) {
+  return kCacheWork + (size_t)2 * q35c::kMaxCtas * group * (D + 4) * 4;
 }
 
 // The head counts and dims the cache operators take (the other fields of the config
@@ -1179,7 +1192,7 @@ int cache_begin(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen3
   if (!rows->row_start && rows->n_rows != rows->n_seqs) return QWEN35_ERR_INVALID_ARGUMENT;
   if (rows->n_seqs > q35c::kMaxSeqs || rows->n_rows > max_rows) return QWEN35_ERR_UNSUPPORTED;
   r = {rows->row_start, rows->pos, rows->n_seqs, rows->n_rows};
-  if (!aligned16(scratch) || scratch_bytes < kCacheWork) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (!aligned16(scratch) || scratch_bytes < kCacheTickets) return QWEN35_ERR_INVALID_ARGUMENT;
   return QWEN35_OK;
 }
 
@@ -1201,7 +1214,9 @@ size_t qwen35_cache_scratch_bytes(const qwen35_config* cfg, uint32_t capacity, u
   if (cache_dims(cfg) || capacity == 0 || max_rows == 0 || max_rows > q35c::kMaxRows) return 0;
   if (block && (block < 16 || block > 1024 || !power_of_two(block))) return 0;
   const uint32_t rows = max_rows < q35c::kMaxQueries ? max_rows : q35c::kMaxQueries;
-  return cache_need(cfg->num_kv_heads, block ? capacity / block : 0, rows).total;
+  const size_t sel = cache_need(cfg->num_kv_heads, block ? capacity / block : 0, rows).total;
+  const size_t att = attend_need(cfg->num_heads / cfg->num_kv_heads, cfg->head_dim);
+  return sel > att ? sel : att;
 }
 
 int qwen35_cache_append(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
@@ -1284,7 +1299,14 @@ int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,
   } else if (n_blocks != 0) {
     return QWEN35_ERR_INVALID_ARGUMENT;
   }
+  const uint64_t tiles = blocks ? (uint64_t)n_blocks * (block / 16) : ((uint64_t)kv->capacity + 15) / 16;
+  if (tiles * a.r.n_rows * a.c.Hkv >= q35c::kMaxTiles) return QWEN35_ERR_UNSUPPORTED;
+  if (scratch_bytes < attend_need(cfg->num_heads / cfg->num_kv_heads, a.c.D)) return QWEN35_ERR_INVALID_ARGUMENT;
   if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  uint8_t* s = static_cast<uint8_t*>(scratch);
+  a.tickets = reinterpret_cast<uint32_t*>(s + kCacheTickets);
+  a.parts = reinterpret_cast<float*>(s + kCacheWork);
+  a.ctas = attend_ctas();
   a.q = q;
   a.gate = gate;
   a.gate_stride = gate_stride;

@@ -74,9 +74,15 @@ struct Attend {
   const uint16_t* gate;  // [n_rows][H] values of D, gate_stride apart, or null
   const int32_t* blocks; // [n_rows][Hkv][n_blocks], or null: every token
   uint16_t* out;         // [n_rows][H][D]
+  uint32_t* tickets;     // [ctas], zero between calls
+  float* parts;          // work [ctas][2][H / Hkv][D + 4]
+  uint32_t ctas;         // CTAs that fill the GPU
   uint32_t H, gate_stride, n_blocks, blk_shift;
   int* status;
 };
+constexpr uint32_t kMaxCtas = 320;  // two on each of up to 160 SMs
+// Tiles of 16 tokens that a call's rows and kv-heads may have in all.
+constexpr uint64_t kMaxTiles = 1ull << 31;
 cudaError_t attend(const Attend& a, cudaStream_t st);
 
 }  // namespace q35c

@@ -137,9 +137,11 @@ def test_selection_and_attention_arguments():
     assert select(16) == OK_BUT_NO_DEVICE
     assert select(0) == BAD and select(17) == BAD  # 256 / 16 blocks
     assert select(4, q=_Fake(0xB000002)) == BAD and select(4, blocks=_Fake(0xD000002, shape=(3, 1, 4))) == BAD
-    need = B.qwen35_cache_scratch_bytes(cfg, 256, 16, 3)
+    need = B.qwen35_cache_scratch_bytes(cfg, 1 << 20, 16, 3)  # the scores of 65536 blocks
+    kv.capacity = 1 << 20
     assert select(4, scratch=_Fake(0x9000000, need)) == OK_BUT_NO_DEVICE
-    assert select(4, scratch=_Fake(0x9000000, need - 1)) == BAD
+    assert select(4, scratch=_Fake(0x9000000, need - 256)) == BAD
+    kv.capacity = 256
 
     def attend(**kw):
         return B.qwen35_decode_attention(cfg, kv, rows, kw.pop("q", x), kw.pop("out", y), kw.pop("scratch", scr),
@@ -155,7 +157,19 @@ def test_selection_and_attention_arguments():
     assert attend(blocks=_Fake(0xD000002, shape=(3, 1, 4)), block=16) == BAD
     need = B.qwen35_cache_scratch_bytes(cfg, 256, 0, 3)
     assert attend(scratch=_Fake(0x9000000, need)) == OK_BUT_NO_DEVICE
-    assert attend(scratch=_Fake(0x9000008, need)) == BAD and attend(scratch=_Fake(0x9000000, 255)) == BAD
+    assert attend(scratch=_Fake(0x9000008, need)) == BAD and attend(scratch=_Fake(0x9000000, need - 1)) == BAD
+
+
+@no_device
+def test_attention_tile_limit():
+    """16-token tiles of all rows and kv-heads: below 2^31."""
+    cfg, scr, x = _cfg(num_heads=8, num_kv_heads=8), _Fake(0x9000000, 1 << 40), _Fake(0xB000000)
+    for rows, status in ((2, OK_BUT_NO_DEVICE), (3, UNSUPPORTED)):
+        r = _rows(n_seqs=rows, n_rows=rows)
+        assert B.qwen35_decode_attention(cfg, _kv(capacity=(1 << 31) - 16), r, x, x, scr, stream=0) == status
+        few = _Fake(0xD000000, shape=(rows, 8, 100))
+        assert B.qwen35_decode_attention(cfg, _kv(capacity=(1 << 31) - 16), r, x, x, scr, blocks=few, block=16,
+                                         stream=0) == OK_BUT_NO_DEVICE
 
 
 @no_device
@@ -169,9 +183,9 @@ def test_append_and_read_pointers():
 
 def test_scratch_sizes():
     c = _cfg()
-    small, large = B.qwen35_cache_scratch_bytes(c, 256, 16, 1), B.qwen35_cache_scratch_bytes(c, 4096, 16, 64)
+    small, large = B.qwen35_cache_scratch_bytes(c, 256, 16, 1), B.qwen35_cache_scratch_bytes(c, 1 << 17, 16, 64)
     assert 256 < small < large
-    assert B.qwen35_cache_scratch_bytes(c, 4096, 0, 64) < large  # no selection
+    assert B.qwen35_cache_scratch_bytes(c, 1 << 17, 0, 64) < large  # no selection
     assert B.qwen35_cache_scratch_bytes(c, 4096, 24, 64) == 0
     assert B.qwen35_cache_scratch_bytes(c, 4096, 16, 0) == 0 and B.qwen35_cache_scratch_bytes(c, 0, 16, 1) == 0
 
