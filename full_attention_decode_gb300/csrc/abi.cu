@@ -7,6 +7,7 @@
 // qwen35_decode_step. A launch is preceded by a memset of the scratch's tagged
 // words (the results CTAs hand each other), so a captured decode step is two graph
 // nodes.
+#include <algorithm>
 #include <cmath>
 #include <cstdlib>
 #include <cstring>
@@ -24,7 +25,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 // What qwen35_scratch_init zeroes: the status word and every kind of scratch's counters.
-constexpr size_t kScratchZeroed = 8192;
+constexpr size_t kScratchZeroed = 256 + (320 + 32768) * 4;
 int g_num_sms[kMaxDevices] = {0};
 
 int num_sms() {
@@ -1115,9 +1116,10 @@ int qwen35_prefill_step(const qwen35_config* cfg, const qwen35_layer* layers, ui
 
 namespace {
 
-// Scratch of the cache operators: the status word, the attention's counters (zero between
-// calls), then the work space, the attention's or the selection's.
-constexpr size_t kCacheTickets = 256, kCacheWork = kCacheTickets + q35c::kMaxCtas * 4;
+// Scratch of the cache operators: the status word, the attention's and the selection's counters
+// (zero between calls), then the work space, the one's or the other's.
+constexpr size_t kCacheTickets = 256, kSelTickets = kCacheTickets + q35c::kMaxCtas * 4;
+constexpr size_t kCacheWork = kSelTickets + q35c::kMaxItems * 4;
 static_assert(kCacheWork <= kScratchZeroed, "the counters are zeroed by qwen35_scratch_init");
 struct CacheNeed {
   size_t scores, exact, most, total;
@@ -1129,14 +1131,10 @@ CacheNeed cache_need(uint32_t Hkv, uint32_t nblk, uint32_t n_rows) {
   n.exact = kCacheWork;
   n.scores = n.exact + up(items * nblk * 8);
   n.most = n.scores + up(items * nblk * 4);
-  n.total = n.most + up(items * 4);
+  n.total = n.most + up((items + q35c::kMaxParts) * 4);
   return n;
 }
-// CTAs of an attention (two an SM), and its scratch: two parts of a split item for each.
-uint32_t attend_ctas() {
-  const uint32_t n = 2u * (uint32_t)num_sms();
-  return n < q35c::kMaxCtas ? n : q35c::kMaxCtas;
-}
+// Scratch of the attention: two parts of a split item for each CTA.
 size_t attend_need(uint32_t group, uint32_t D) {
   return kCacheWork + (size_t)2 * q35c::kMaxCtas * group * (D + 4) * 4;
 }
@@ -1272,6 +1270,8 @@ int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_cache* kv, co
   a.scores = reinterpret_cast<float*>(s + need.scores);
   a.exact = reinterpret_cast<double*>(s + need.exact);
   a.most = reinterpret_cast<float*>(s + need.most);
+  a.tickets = reinterpret_cast<uint32_t*>(s + kSelTickets);
+  a.ctas = std::min(8u * (uint32_t)num_sms(), q35c::kMaxParts);
   a.H = cfg->num_heads;
   a.blk_shift = log2_of(bounds->block);
   a.n_select = n_select;
@@ -1306,7 +1306,7 @@ int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,
   uint8_t* s = static_cast<uint8_t*>(scratch);
   a.tickets = reinterpret_cast<uint32_t*>(s + kCacheTickets);
   a.parts = reinterpret_cast<float*>(s + kCacheWork);
-  a.ctas = attend_ctas();
+  a.sms = (uint32_t)num_sms();
   a.q = q;
   a.gate = gate;
   a.gate_stride = gate_stride;

@@ -29,7 +29,10 @@ namespace q35c {
 using namespace q35;
 namespace {
 
-constexpr int kWarps = 4;  // warps of a CTA; two CTAs share an SM
+#ifndef ATT_WARPS
+#define ATT_WARPS 8
+#endif
+constexpr int kWarps = ATT_WARPS, kCtasPerSm = 8 / kWarps;
 constexpr int kAttnThreads = 32 * kWarps;
 
 // A ring slot: K or V of 16 tokens. Rows are padded by 16 bytes, which puts eight rows'
@@ -39,7 +42,7 @@ struct Slot {
   static constexpr int row = T8 ? D + 16 : 2 * D + 16;
   static constexpr int scales = T8 ? D / 16 * 2 : 0;  // a token's scales
   static constexpr int bytes = 16 * (row + scales);
-  static constexpr int n = T8 ? 5 : D == 256 ? 3 : 4;  // slots of a warp
+  static constexpr int n = D == 256 && !T8 ? 3 : 4;  // slots of a warp
 };
 // Shared memory of a CTA: the rings (reused to join the warps), Q's fragments, the warps'
 // maxima and sums, T8's transposed V scales, then the rows' first tiles.
@@ -48,7 +51,9 @@ struct Smem {
   using S = Slot<D, T8>;
   static constexpr int ring = kWarps * S::n * S::bytes;
   static constexpr int join = kWarps * 8 * NT * (D + 4) * 4;
-  static constexpr int big = ring > join ? ring : join;
+  static constexpr int weights = 24576;  // the parts' weights, behind their sums
+  static constexpr int parts = weights + 8 * NT * (int)kMaxCtas * 4;
+  static constexpr int big = ring > join ? (ring > parts ? ring : parts) : join > parts ? join : parts;
   static constexpr int qf = big;                                    // fragments, 8 or (T8) 16 bytes a lane
   static constexpr int ml = qf + (D / 16) * NT * 32 * (T8 ? 16 : 8);  // [warps + 1][2][16]
   static constexpr int vsc = ml + (kWarps + 1) * 2 * 16 * 4;
@@ -612,17 +617,32 @@ struct Attention {
       __stcg(reinterpret_cast<float4*>(to + threadIdx.x * (D + 4) + D),
              make_float4(ml[threadIdx.x], ml[16 + threadIdx.x], 0.f, 0.f));
   }
-  // The parts of CTAs c0 .. c1 added up in their order, as join_warps leaves its sums.
+  // The parts of CTAs c0 .. c1 added up, as join_warps leaves its sums: a thread has four dims of a head and,
+  // where there are fewer such columns than threads, every subs-th part. The order is fixed by c0 and c1.
   __device__ void join_parts(uint32_t c0, uint32_t c1) {
-    float* red = reinterpret_cast<float*>(sm);
+    float* red = reinterpret_cast<float*>(sm);  // [subs][group][D + 4]
     float* ml = reinterpret_cast<float*>(sm + M::ml) + kWarps * 32;
+    float* wt = reinterpret_cast<float*>(sm + M::weights);  // [group][parts]
+    const uint32_t n = c1 - c0 + 1;
     for (uint32_t h = warp; h < group; h += kWarps) {
       float mx = -INFINITY, sum = 0.f;
-      for (uint32_t c = c0 + lane; c <= c1; c += 32) mx = fmaxf(mx, __ldcg(part(c, c == c0) + h * (D + 4) + D));
+      constexpr int U = (kMaxCtas + 31) / 32;
+      float2 x[U];
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t c = c0 + lane + 32 * i;
+        x[i] = make_float2(-INFINITY, 0.f);
+        if (c <= c1) x[i] = __ldcg(reinterpret_cast<const float2*>(part(c, c == c0) + h * (D + 4) + D));
+      }
+#pragma unroll
+      for (int i = 0; i < U; ++i) mx = fmaxf(mx, x[i].x);
       mx = warp_max(mx);
-      for (uint32_t c = c0 + lane; c <= c1; c += 32) {
-        const float2 x = __ldcg(reinterpret_cast<const float2*>(part(c, c == c0) + h * (D + 4) + D));
-        sum += x.y * rescale(x.x, mx);
+#pragma unroll
+      for (int i = 0; i < U; ++i) {
+        const uint32_t c = lane + 32 * i;
+        const float f = rescale(x[i].x, mx);
+        if (c < n) wt[h * n + c] = f;
+        sum += x[i].y * f;
       }
       sum = warp_sum(sum);
       if (lane == 0) {
@@ -631,23 +651,50 @@ struct Attention {
       }
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < group * (D / 4); i += kAttnThreads) {
-      const uint32_t h = i / (D / 4), at = h * (D + 4) + 4 * (i % (D / 4));
-      const float mx = ml[h];
+    const uint32_t cols = group * (D / 4), subs = max(1u, kAttnThreads / cols);
+    for (uint32_t i = threadIdx.x; i < cols * subs; i += kAttnThreads) {
+      const uint32_t sub = i / cols, col = i % cols, h = col / (D / 4), at = h * (D + 4) + 4 * (col % (D / 4));
+      const float* w = wt + h * n;
+      const float* p0 = part(c0, 1) + at;  // CTA c0's part, then slot 0 of each CTA
+      const float* p = part(c0, 0) + at;
+      const size_t step = 2 * (size_t)(group * (D + 4));
       float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-      for (uint32_t c = c0; c <= c1; ++c) {
-        const float* p = part(c, c == c0);
-        const float f = rescale(__ldcg(p + h * (D + 4) + D), mx);
-        const float4 y = __ldcg(reinterpret_cast<const float4*>(p + at));
-        x.x = fmaf(y.x, f, x.x);
-        x.y = fmaf(y.y, f, x.y);
-        x.z = fmaf(y.z, f, x.z);
-        x.w = fmaf(y.w, f, x.w);
+      for (uint32_t k0 = sub; k0 < n; k0 += 16 * subs) {
+        float4 y[16];
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t c = k0 + k * subs;
+          y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (c < n) y[k] = __ldcg(reinterpret_cast<const float4*>(c ? p + c * step : p0));
+        }
+#pragma unroll
+        for (int k = 0; k < 16; ++k) {
+          const uint32_t c = k0 + k * subs;
+          const float f = c < n ? w[c] : 0.f;
+          x.x = fmaf(y[k].x, f, x.x);
+          x.y = fmaf(y[k].y, f, x.y);
+          x.z = fmaf(y[k].z, f, x.z);
+          x.w = fmaf(y[k].w, f, x.w);
+        }
       }
-      *reinterpret_cast<float4*>(red + at) = x;
+      *reinterpret_cast<float4*>(red + sub * group * (D + 4) + at) = x;
     }
     __syncthreads();
+    if (subs > 1) {
+      for (uint32_t col = threadIdx.x; col < cols; col += kAttnThreads) {
+        float* at = red + (col / (D / 4)) * (D + 4) + 4 * (col % (D / 4));
+        float4 x = *reinterpret_cast<float4*>(at);
+        for (uint32_t s = 1; s < subs; ++s) {
+          const float4 y = *reinterpret_cast<const float4*>(at + s * group * (D + 4));
+          x.x += y.x;
+          x.y += y.y;
+          x.z += y.z;
+          x.w += y.w;
+        }
+        *reinterpret_cast<float4*>(at) = x;
+      }
+      __syncthreads();
+    }
   }
 };
 
@@ -661,7 +708,7 @@ __device__ __forceinline__ uint32_t row_tiles(const Attend& a, uint32_t r, bool 
 }
 
 template <int D, int NT, bool T8>
-__global__ void __launch_bounds__(kAttnThreads, 2) attend_kernel(const __grid_constant__ Attend a) {
+__global__ void __launch_bounds__(kAttnThreads, kCtasPerSm) attend_kernel(const __grid_constant__ Attend a) {
   extern __shared__ __align__(128) uint8_t sm[];
   using A = Attention<D, NT, T8>;
   using M = Smem<D, NT, T8>;
@@ -757,7 +804,7 @@ cudaError_t launch(const Attend& a, cudaStream_t st) {
   if (e != cudaSuccess) return e;
   const uint64_t most = (uint64_t)a.r.n_rows * a.c.Hkv *
                         (a.blocks ? (uint64_t)a.n_blocks << (a.blk_shift - 4) : (a.c.capacity + 15) / 16);
-  const uint32_t grid = (uint32_t)std::min<uint64_t>(a.ctas, (most + kWarps - 1) / kWarps);
+  const uint32_t grid = (uint32_t)std::min<uint64_t>(std::min(a.sms * kCtasPerSm, kMaxCtas), (most + kWarps - 1) / kWarps);
   attend_kernel<D, NT, T8><<<grid, kAttnThreads, bytes, st>>>(a);
   return cudaGetLastError();
 }

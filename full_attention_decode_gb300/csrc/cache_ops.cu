@@ -12,121 +12,194 @@ constexpr uint32_t kThreads = 256;
 
 // ------------------------------------------------------------------ rows in and out
 
-// LPR = D / 8 lanes per (row, kv-head), eight elements a lane: 16-byte loads at every head
-// dim. Turbo8: r = bf16(WHT(x)), then codes and scales (quant8).
-template <int D, bool T8>
-__global__ void __launch_bounds__(kThreads) append_kernel(const Append a) {
+// A (row, kv-head) item of a call: where its cache row is. Every lane of a team asks.
+struct Item {
+  bool ok;
+  uint32_t g;
+  size_t row;
+};
+__device__ __forceinline__ Item find_item(const Rows& w, const Cache& c, size_t item, int* status) {
+  Item x = {false, 0, 0};
+  const uint32_t r = (uint32_t)(item / c.Hkv);
+  x.g = (uint32_t)(item % c.Hkv);
+  if (r >= w.n_rows) return x;
+  uint32_t seq, pos;
+  const RowKind kind = locate(w, c.capacity, r, seq, pos);
+  x.ok = kind == kRowOk && cache_row(c, seq, pos, x.row);
+  if (!x.ok && kind != kRowSkip) set_status(status, kStatusRange);
+  return x;
+}
+
+// A bf16 row: D / 8 lanes an item, 16 bytes a lane.
+template <int D>
+__device__ __forceinline__ void append_plain(const Append& a, uint32_t block) {
   constexpr int LPR = D / 8;
-  const size_t item = (blockIdx.x * (size_t)kThreads + threadIdx.x) / LPR;
-  const uint32_t lane = threadIdx.x & 31, l = lane % LPR;
-  const uint32_t r = (uint32_t)(item / a.c.Hkv), g = (uint32_t)(item % a.c.Hkv);
-  uint32_t seq = 0, pos = 0;
-  size_t row = 0;
-  RowKind kind = r < a.r.n_rows ? locate(a.r, a.c.capacity, r, seq, pos) : kRowSkip;
-  if (kind == kRowOk && !cache_row(a.c, seq, pos, row)) kind = kRowBad;
-  if (kind == kRowBad) set_status(a.status, kStatusRange);
-  const bool ok = kind == kRowOk;
-  const size_t src = item * D + 8 * l, dst = (row * a.c.Hkv + g) * D + 8 * l;
+  const size_t item = (block * (size_t)kThreads + threadIdx.x) / LPR;
+  const uint32_t l = threadIdx.x % LPR;
+  const Item x = find_item(a.r, a.c, item, a.status);
+  if (!x.ok) return;
+  const size_t src = item * D + 8 * l, dst = (x.row * a.c.Hkv + x.g) * D + 8 * l;
+  const uint4 k = *reinterpret_cast<const uint4*>(a.k + src), v = *reinterpret_cast<const uint4*>(a.v + src);
+  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.c.k) + dst) = k;
+  *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.c.v) + dst) = v;
+}
+
+// A Turbo8 row: four lanes an item and K or V, D / 4 elements a lane (wht_quad's layout).
+template <int D>
+__device__ __forceinline__ void append_turbo8(const Append& a, uint32_t block) {
+  constexpr int P = D / 32;  // pieces of eight elements
+  const size_t team = (block * (size_t)kThreads + threadIdx.x) / 4;
+  const uint32_t lane = threadIdx.x & 31, l = lane & 3;
+  const size_t item = team / 16 * 8 + team % 8;  // a warp's eight teams: eight items' K or V
+  const bool is_v = team & 8;
+  const Item w = find_item(a.r, a.c, item, a.status);
+  const uint16_t* src = (is_v ? a.v : a.k) + item * D + 8 * l;
+  float x[D / 4];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
+  for (int i = 0; i < P; ++i) {
     uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (ok) u = *reinterpret_cast<const uint4*>((p ? a.v : a.k) + src);
-    uint8_t* to = p ? a.c.v : a.c.k;
-    if constexpr (T8) {
-      float x[8];
-      unpack8(u, x);
-      wht8<LPR>(x, lane);
+    if (w.ok) u = *reinterpret_cast<const uint4*>(src + 32 * i);
+    unpack8(u, x + 8 * i);
+  }
+  wht_quad<D>(x, lane);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] = round_bf16(x[e]);
-      uint16_t sc;
-      const uint2 codes = quant8(x, sc);
-      if (ok) {
-        *reinterpret_cast<uint2*>(to + dst) = codes;
-        if (l % 2 == 0) (p ? a.c.vs : a.c.ks)[row * a.c.sstride + (g * D + 8 * l) / 16] = sc;
-      }
-    } else if (ok) {
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(to) + dst) = u;
+  for (int e = 0; e < D / 4; ++e) x[e] = round_bf16(x[e]);
+  uint8_t* to = (is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 8 * l;
+  uint16_t* sc = (is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16) + l / 2;
+#pragma unroll
+  for (int i = 0; i < P; ++i) {
+    uint16_t s;
+    const uint2 codes = quant8(x + 8 * i, s);
+    if (w.ok) {
+      *reinterpret_cast<uint2*>(to + 32 * i) = codes;
+      if (l % 2 == 0) sc[2 * i] = s;
     }
   }
 }
 
-// The key bounds: the first row of each (sequence, block) of the call folds the block's
-// rows; a block whose first token is among them starts anew.
+// The key bounds, one CTA per (span of rows, kv-head). A run is the call's rows of one block
+// of one sequence; the CTA that has its first row folds it, starting anew if that is
+// the block's first token. Warps (in teams of D / 8 lanes) take the run's rows in turn.
 template <int D>
-__global__ void __launch_bounds__(kThreads) bounds_kernel(const Append a) {
-  constexpr int LPR = D / 8;
-  const size_t item = (blockIdx.x * (size_t)kThreads + threadIdx.x) / LPR;
-  const uint32_t l = threadIdx.x % LPR;
-  const uint32_t r = (uint32_t)(item / a.c.Hkv), g = (uint32_t)(item % a.c.Hkv);
-  uint32_t seq, pos;
-  size_t row;
-  if (r >= a.r.n_rows || locate(a.r, a.c.capacity, r, seq, pos) != kRowOk || !cache_row(a.c, seq, pos, row)) return;
-  const uint32_t S = 1u << a.blk_shift, first = a.r.row_start ? (uint32_t)a.r.row_start[seq] : r;
-  if (r != first && pos % S != 0) return;
-  uint32_t last = a.r.row_start ? (uint32_t)a.r.row_start[seq + 1] : r + 1;  // rows [r, last) of the block
-  last = min(min(last, a.r.n_rows), r + (S - pos % S));
-  last = min(last, r + (a.c.capacity - pos));
-  uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D + 8 * l;
-  float lo[8], hi[8], x[8];
-  if (pos % S == 0) {
+__device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, uint32_t g, uint32_t span_rows) {
+  constexpr int LPR = D / 8, TEAMS = kThreads / LPR;
+  __shared__ float part[2][TEAMS][D];
+  const uint32_t l = threadIdx.x % LPR, team = threadIdx.x / LPR, S = 1u << a.blk_shift;
+  const uint32_t end = min(a.r.n_rows, (span + 1) * span_rows);
+  for (uint32_t r = span * span_rows; r < end;) {
+    uint32_t seq, pos;
+    size_t row;
+    const RowKind kind = locate(a.r, a.c.capacity, r, seq, pos);
+    if (kind != kRowOk || !cache_row(a.c, seq, pos, row)) {  // reported by the row's writer
+      ++r;
+      continue;
+    }
+    // the rows of this sequence from r on that lie in its block
+    int64_t last = a.r.row_start ? a.r.row_start[seq + 1] : (int64_t)r + 1;
+    last = min(min(last, (int64_t)a.r.n_rows), (int64_t)r + (S - pos % S));
+    last = min(last, (int64_t)r + (a.c.capacity - pos));
+    const uint32_t stop = (uint32_t)max(last, (int64_t)r + 1);
+    const bool fresh = pos % S == 0;
+    if (!fresh && a.r.row_start && (int64_t)r != a.r.row_start[seq]) {  // its first row is in an earlier span
+      r = stop;
+      continue;
+    }
+    float lo[8], hi[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       lo[e] = INFINITY;
       hi[e] = -INFINITY;
     }
-  } else {
-    unpack8(*reinterpret_cast<const uint4*>(b), lo);
-    unpack8(*reinterpret_cast<const uint4*>(b + D), hi);
-  }
-  for (uint32_t i = r; i < last; ++i) {
-    unpack8(*reinterpret_cast<const uint4*>(a.k + ((size_t)i * a.c.Hkv + g) * D + 8 * l), x);
+    const uint16_t* src = a.k + (size_t)g * D + 8 * l;
+#pragma unroll 4
+    for (uint32_t i = r + team; i < stop; i += TEAMS) {
+      float x[8];
+      unpack8(*reinterpret_cast<const uint4*>(src + (size_t)i * a.c.Hkv * D), x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      lo[e] = fminf(lo[e], x[e]);
-      hi[e] = fmaxf(hi[e], x[e]);
+      for (int e = 0; e < 8; ++e) {
+        lo[e] = fminf(lo[e], x[e]);
+        hi[e] = fmaxf(hi[e], x[e]);
+      }
     }
+    const uint32_t used = min(stop - r, (uint32_t)TEAMS);
+    if (team < used)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        part[0][team][8 * l + e] = lo[e];
+        part[1][team][8 * l + e] = hi[e];
+      }
+    __syncthreads();
+    uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D;
+    for (uint32_t i = threadIdx.x; i < 2 * D; i += kThreads) {
+      const uint32_t p = i / D, d = i % D;
+      float x = fresh ? (p ? -INFINITY : INFINITY) : bf16f(b[i]);
+      for (uint32_t t = 0; t < used; ++t) x = p ? fmaxf(x, part[1][t][d]) : fminf(x, part[0][t][d]);
+      b[i] = to_bf16(x);
+    }
+    __syncthreads();
+    r = stop;
   }
-  *reinterpret_cast<uint4*>(b) = pack8(lo);
-  *reinterpret_cast<uint4*>(b + D) = pack8(hi);
+}
+
+// CTAs [0, row_ctas) write rows, the others bring the bounds up to date.
+template <int D, bool T8>
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Append a, uint32_t row_ctas,
+                                                          uint32_t span_rows) {
+  if (blockIdx.x < row_ctas) {
+    if constexpr (T8) append_turbo8<D>(a, blockIdx.x);
+    else append_plain<D>(a, blockIdx.x);
+  } else {
+    const uint32_t i = blockIdx.x - row_ctas;
+    append_bounds<D>(a, i / a.c.Hkv, i % a.c.Hkv, span_rows);
+  }
 }
 
 template <int D, bool T8>
-__global__ void __launch_bounds__(kThreads) read_kernel(const Read a) {
-  constexpr int LPR = D / 8;
-  const size_t item = (blockIdx.x * (size_t)kThreads + threadIdx.x) / LPR;
-  const uint32_t lane = threadIdx.x & 31, l = lane % LPR;
-  const uint32_t r = (uint32_t)(item / a.c.Hkv), g = (uint32_t)(item % a.c.Hkv);
-  uint32_t seq = 0, pos = 0;
-  size_t row = 0;
-  RowKind kind = r < a.r.n_rows ? locate(a.r, a.c.capacity, r, seq, pos) : kRowSkip;
-  if (kind == kRowOk && !cache_row(a.c, seq, pos, row)) kind = kRowBad;
-  if (kind == kRowBad) set_status(a.status, kStatusRange);
-  const bool ok = kind == kRowOk;
-  const size_t dst = item * D + 8 * l, src = (row * a.c.Hkv + g) * D + 8 * l;
+__global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Read a) {
+  if constexpr (T8) {
+    constexpr int P = D / 32;
+    const size_t team = (blockIdx.x * (size_t)kThreads + threadIdx.x) / 4;
+    const uint32_t lane = threadIdx.x & 31, l = lane & 3;
+    const size_t item = team / 16 * 8 + team % 8;
+    const bool is_v = team & 8;
+    const Item w = find_item(a.r, a.c, item, a.status);
+    const uint8_t* from = (is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 8 * l;
+    const uint16_t* sc = (is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16) + l / 2;
+    float x[D / 4];
 #pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    const uint8_t* from = p ? a.c.v : a.c.k;
-    uint16_t* to = p ? a.v : a.k;
-    if constexpr (T8) {
+    for (int i = 0; i < P; ++i) {
       uint2 codes = make_uint2(0u, 0u);
-      float sc = 0.f;
-      if (ok) {
-        codes = *reinterpret_cast<const uint2*>(from + src);
-        sc = bf16f((p ? a.c.vs : a.c.ks)[row * a.c.sstride + (g * D + 8 * l) / 16]);
+      uint16_t s = 0;
+      if (w.ok) {
+        codes = *reinterpret_cast<const uint2*>(from + 32 * i);
+        s = sc[2 * i];
       }
-      float x[8];
-      dequant_codes8(codes, sc, x);
-      wht8<LPR>(x, lane);
-      if (ok) *reinterpret_cast<uint4*>(to + dst) = pack8(x);
-    } else if (ok) {
-      *reinterpret_cast<uint4*>(to + dst) =
-          *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(from) + src);
+      dequant_codes8(codes, bf16f(s), x + 8 * i);
     }
+    wht_quad<D>(x, lane);
+    uint16_t* to = (is_v ? a.v : a.k) + item * D + 8 * l;
+    if (w.ok)
+#pragma unroll
+      for (int i = 0; i < P; ++i) *reinterpret_cast<uint4*>(to + 32 * i) = pack8(x + 8 * i);
+  } else {
+    constexpr int LPR = D / 8;
+    const size_t item = (blockIdx.x * (size_t)kThreads + threadIdx.x) / LPR;
+    const uint32_t l = threadIdx.x % LPR;
+    const Item w = find_item(a.r, a.c, item, a.status);
+    if (!w.ok) return;
+    const size_t dst = item * D + 8 * l, src = (w.row * a.c.Hkv + w.g) * D + 8 * l;
+    const uint4 k = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.c.k) + src);
+    const uint4 v = *reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.c.v) + src);
+    *reinterpret_cast<uint4*>(a.k + dst) = k;
+    *reinterpret_cast<uint4*>(a.v + dst) = v;
   }
 }
 
-uint32_t item_blocks(const Rows& r, const Cache& c) {
-  const size_t lanes = (size_t)r.n_rows * c.Hkv * (c.D / 8);
+// CTAs that cover a call's rows: D / 8 lanes an item (K and V in turn), or four lanes for each of K and V
+// in whole warps of eight items.
+uint32_t row_ctas_of(const Rows& r, const Cache& c, bool t8) {
+  const size_t items = (size_t)r.n_rows * c.Hkv;
+  const size_t lanes = t8 ? (items + 7) / 8 * 64 : items * (c.D / 8);
   return (uint32_t)((lanes + kThreads - 1) / kThreads);
 }
 
@@ -151,71 +224,93 @@ __device__ __forceinline__ bool forced(const Select& a, uint32_t j, uint32_t n) 
   return j < a.n_first || (uint64_t)j + a.n_last >= n;
 }
 
-// Scores of the blocks a row sees: s_j = sum_d Q+_d hi_jd + Q-_d lo_jd with Q+ and Q- the sums
-// over the group's heads of q's positive and negative parts, the sum over the heads of the
-// largest q.k a key inside the bounds could have. One CTA per (row, kv-head) and
-// gridDim.x-th part of the blocks; LPR lanes a block.
+constexpr uint32_t kSelWarps = kThreads / 32;
+constexpr uint32_t kMine = 16;   // scores a thread holds in registers: 4096 blocks a CTA
+constexpr uint32_t kClose = 256;  // blocks scored again side by side
+
+// Sums over the group's heads of q's positive and negative parts, eight dims a lane.
 template <int D>
-__global__ void __launch_bounds__(kThreads) score_kernel(const Select a) {
-  constexpr int LPR = D / 8, PER = kThreads / LPR;
-  const uint32_t r = blockIdx.z, g = blockIdx.y, lane = threadIdx.x & 31, l = lane % LPR;
-  uint32_t seq, pos;
-  const RowKind kind = locate(a.r, a.c.capacity, r, seq, pos);
-  if (kind != kRowOk) {
-    if (kind == kRowBad) set_status(a.status, kStatusRange);
-    return;
-  }
-  const uint32_t n = (pos >> a.blk_shift) + 1;
-  if (n <= a.n_select) return;  // every block is taken
-  float up[8], dn[8];
+__device__ __forceinline__ void signed_sums(const Select& a, uint32_t r, uint32_t g, uint32_t l, float (&up)[8],
+                                            float (&dn)[8]) {
 #pragma unroll
   for (int e = 0; e < 8; ++e) up[e] = dn[e] = 0.f;
   const uint32_t group = a.H / a.c.Hkv;
+#pragma unroll 4
   for (uint32_t h = 0; h < group; ++h) {
     float x[8];
     unpack8(*reinterpret_cast<const uint4*>(a.q + ((size_t)r * a.H + g * group + h) * D + 8 * l), x);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      up[e] += fmaxf(x[e], 0.f);
-      dn[e] += fminf(x[e], 0.f);
-      if (x[e] != x[e]) up[e] = x[e];
+      up[e] += x[e] > 0.f || x[e] != x[e] ? x[e] : 0.f;
+      dn[e] += x[e] < 0.f ? x[e] : 0.f;
     }
   }
-  float* out = a.scores + ((size_t)r * a.c.Hkv + g) * a.nblk;
-  float most = 0.f;
-  for (uint32_t j0 = blockIdx.x * PER; j0 < n; j0 += gridDim.x * PER) {
-    const uint32_t j = j0 + threadIdx.x / LPR;
-    size_t row = 0;
-    const bool in = j < n, here = in && cache_row(a.c, seq, j << a.blk_shift, row);
-    if (in && !here) set_status(a.status, kStatusRange);
-    float s = 0.f, t = 0.f;
-    if (here) {
-      const uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D + 8 * l;
-      float lo[8], hi[8];
-      unpack8(*reinterpret_cast<const uint4*>(b), lo);
-      unpack8(*reinterpret_cast<const uint4*>(b + D), hi);
+}
+
+// Scores of blocks [j0, j1): s_j = sum_d Q+_d hi_jd + Q-_d lo_jd, with Q+ and Q- the sums over the
+// group's heads of q's positive and negative parts: the sum over the heads of the largest q.k that a key
+// inside the bounds could have. LPR lanes a block, four blocks of a lane in flight. Returns (in every
+// thread) sum_d Q+_d max_j|hi_jd| + |Q-_d| max_j|lo_jd|, which bounds every block's sum
+// of absolute terms; infinity where an infinity or NaN leaves no bound.
+template <int D>
+__device__ float score_blocks(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, uint32_t j0,
+                              uint32_t j1, float* out, float* tmp) {
+  constexpr int LPR = D / 8, PER = kThreads / LPR, U = 4;
+  const uint32_t l = threadIdx.x % LPR, team = threadIdx.x / LPR;
+  float up[8], dn[8], mh[8], ml[8];
+  signed_sums<D>(a, r, g, l, up, dn);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        s = fmaf(up[e], hi[e], s);
-        t = fmaf(up[e], fabsf(hi[e]), t);
-        s = fmaf(dn[e], lo[e], s);
-        t = fmaf(-dn[e], fabsf(lo[e]), t);
+  for (int e = 0; e < 8; ++e) mh[e] = ml[e] = 0.f;
+  bool wild = false;
+  for (uint32_t jb = j0; jb < j1; jb += PER * U) {
+    uint4 lo4[U], hi4[U];
+    bool here[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const uint32_t j = jb + u * PER + team;
+      size_t row = 0;
+      const bool in = j < j1;
+      here[u] = in && cache_row(a.c, seq, j << a.blk_shift, row);
+      if (in && !here[u]) set_status(a.status, kStatusRange);
+      lo4[u] = hi4[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (here[u]) {
+        const uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D + 8 * l;
+        lo4[u] = *reinterpret_cast<const uint4*>(b);
+        hi4[u] = *reinterpret_cast<const uint4*>(b + D);
       }
     }
 #pragma unroll
-    for (int o = LPR / 2; o > 0; o >>= 1) {
-      s += __shfl_xor_sync(0xffffffffu, s, o);
-      t += __shfl_xor_sync(0xffffffffu, t, o);
-    }
-    if (in && l == 0) out[j] = forced(a, j, n) ? INFINITY : here ? s : -INFINITY;
-    if (here && !forced(a, j, n)) most = t > most || t != t ? t : most;
-  }
-  // a NaN or an infinity: no bound on the rounding, every score is formed again
-  const bool wild = !(most < INFINITY);
-  most = wild ? INFINITY : most;
+    for (int u = 0; u < U; ++u) {
+      const uint32_t j = jb + u * PER + team;
+      float lo[8], hi[8], s = 0.f;
+      unpack8(lo4[u], lo);
+      unpack8(hi4[u], hi);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, o));
-  if (lane == 0) atomicMax(reinterpret_cast<int*>(a.most) + (size_t)r * a.c.Hkv + g, __float_as_int(most));
+      for (int e = 0; e < 8; ++e) {
+        s = fmaf(up[e], hi[e], s);
+        s = fmaf(dn[e], lo[e], s);
+        mh[e] = fmaxf(mh[e], fabsf(hi[e]));
+        ml[e] = fmaxf(ml[e], fabsf(lo[e]));
+      }
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      if (here[u]) wild |= !(fabsf(s) < INFINITY);
+      if (j < j1 && l == 0) __stcg(out + j, forced(a, j, n) ? INFINITY : here[u] ? s : -INFINITY);
+    }
+  }
+  float most = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) most += up[e] * mh[e] - dn[e] * ml[e];
+#pragma unroll
+  for (int o = LPR / 2; o > 0; o >>= 1) most += __shfl_xor_sync(0xffffffffu, most, o);
+  if (wild || !(most < INFINITY)) most = INFINITY;
+  most = warp_max(most);
+  if (threadIdx.x % 32 == 0) tmp[threadIdx.x / 32] = most;
+  __syncthreads();
+  most = tmp[0];
+  for (uint32_t w = 1; w < kSelWarps; ++w) most = fmaxf(most, tmp[w]);
+  __syncthreads();
+  return most;
 }
 
 // Block j's score in 64 bits, by one warp (the same value in every lane).
@@ -237,133 +332,263 @@ __device__ double exact_score(const Select& a, uint32_t r, uint32_t g, uint32_t 
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s;
+  return s > 1e300 ? 1e300 : s;  // an infinity stays below the blocks that always come first
 }
 
-template <typename F>
-__device__ __forceinline__ uint32_t block_count(uint32_t n, F&& is, uint32_t* tmp) {
-  uint32_t c = 0;
-  for (uint32_t j = threadIdx.x; j < n; j += kThreads) c += is(j) ? 1u : 0u;
+// The scores of an item, spread over one CTA: warp w has blocks [w span, (w + 1) span), lane l every 32nd
+// of them from l, the first kMine of a thread in registers.
+struct Scores {
+  const float* s;
+  uint32_t n, base, end, mine;  // base: this thread's first block; end: of its warp; mine: how many it has
+  uint32_t key[kMine];
+
+  __device__ void take(const float* scores, uint32_t count) {
+    const uint32_t span = (count + kThreads - 1) / kThreads * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    s = scores;
+    n = count;
+    end = (uint32_t)min((uint64_t)(warp + 1) * span, (uint64_t)count);
+    base = warp * span + lane;
+    mine = base < end ? (end - base + 31) / 32 : 0;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) c += __shfl_xor_sync(0xffffffffu, c, o);
+    for (uint32_t i = 0; i < kMine; ++i) key[i] = i < mine ? order_key(__ldcg(s + base + 32 * i)) : 0u;
+  }
+  // f(block, key) for this thread's blocks in order; every lane of a warp is called equally often (a key of
+  // 0 stands for no block: a score's key is above it).
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    const uint32_t w0 = base - (threadIdx.x & 31);
+    const uint32_t rounds = w0 < end ? (end - w0 + 31) / 32 : 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kMine; ++i)
+      if (i < rounds) f(base + 32 * i, key[i]);
+    for (uint32_t i = kMine; i < rounds; ++i) f(base + 32 * i, i < mine ? order_key(__ldcg(s + base + 32 * i)) : 0u);
+  }
+};
+
+// Sum over the CTA (the same in every thread); tmp: [2][kSelWarps], turn: alternates between calls.
+__device__ __forceinline__ uint32_t cta_sum(uint32_t x, uint32_t* tmp, uint32_t& turn) {
+  x = __reduce_add_sync(0xffffffffu, x);
+  uint32_t* t = tmp + turn * kSelWarps;
+  turn ^= 1;
+  if ((threadIdx.x & 31) == 0) t[threadIdx.x >> 5] = x;
   __syncthreads();
-  if ((threadIdx.x & 31) == 0) tmp[threadIdx.x >> 5] = c;
-  __syncthreads();
-  c = 0;
-  for (uint32_t w = 0; w < kThreads / 32; ++w) c += tmp[w];
-  return c;
+  x = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < kSelWarps; ++w) x += t[w];
+  return x;
 }
 
-// One CTA per (row, kv-head): the k-th largest of the 32-bit scores (radix selection, a byte a
-// pass), then which blocks the exact scores choose. Every s_j is within E of the exact t_j
-// (E = 48 2^-24 max_j sum|terms|: at most 15 additions in Q+-, 16 multiply-adds and 5
-// additions round). The k-th largest t is then within E of the k-th largest s, T: s_j > T + 2E
-// is in, s_j < T - 2E is out, and only what lies between is scored again in 64 bits.
+// Which blocks the exact scores choose, given 32-bit ones. Every s_j is within E of the exact t_j
+// (E = 48 2^-24 most: at most 15 additions in Q+-, 16 multiply-adds and 5 additions
+// round). The K-th largest t is then within E of the K-th largest s, T: s_j > T + 2E is in, s_j < T - 2E is
+// out, and only what lies between is scored again in 64 bits. T by bisection of the
+// scores' bits: a count over the CTA a step, until a step leaves exactly K.
 template <int D>
-__global__ void __launch_bounds__(kThreads) choose_kernel(const Select a) {
-  __shared__ uint32_t hist[256], tmp[kThreads / 32], s_pick[2], s_base[2];
-  const uint32_t r = blockIdx.y, g = blockIdx.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  uint32_t seq, pos;
-  if (locate(a.r, a.c.capacity, r, seq, pos) != kRowOk) return;
-  const uint32_t n = (pos >> a.blk_shift) + 1, K = a.n_select;
-  const size_t item = (size_t)r * a.c.Hkv + g;
+__device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item, float most) {
+  __shared__ uint32_t tmp[2 * kSelWarps], close_j[kClose], s_close;
+  __shared__ double close_t[kClose];
+  const uint32_t K = a.n_select, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   int32_t* out = a.blocks + item * K;
-  if (n <= K) {
-    for (uint32_t i = tid; i < K; i += kThreads) out[i] = i < n ? (int32_t)i : -1;
-    return;
-  }
-  const float* s = a.scores + item * a.nblk;
-  double* t = a.exact + item * a.nblk;
-  uint32_t prefix = 0, mask = 0, left = K;  // the left-th largest among keys with this prefix
-  for (int shift = 24; shift >= 0; shift -= 8) {
-    hist[tid] = 0;
-    __syncthreads();
-    for (uint32_t j = tid; j < n; j += kThreads) {
-      const uint32_t key = order_key(s[j]);
-      if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+  uint32_t turn = 0;
+  Scores sc;
+  sc.take(a.scores + item * a.nblk, n);
+  const auto count = [&](uint32_t from) {  // keys >= from
+    uint32_t c = 0;
+    sc.each([&](uint32_t, uint32_t k) { c += k >= from; });
+    return cta_sum(c, tmp, turn);
+  };
+  // low: the largest tried value with at least K keys from it up
+  uint32_t low = 1, high = 0xffffffffu, at_low = n;
+  while (at_low != K && high - low > 1) {
+    const uint32_t mid = low + (high - low) / 2, c = count(mid);
+    if (c >= K) {
+      low = mid;
+      at_low = c;
+    } else {
+      high = mid;
     }
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t b = 255, c = 0;
-      while (b > 0 && c + hist[b] < left) c += hist[b--];
-      s_pick[0] = b;
-      s_pick[1] = left - c;
-    }
-    __syncthreads();
-    prefix |= s_pick[0] << shift;
-    mask |= 255u << shift;
-    left = s_pick[1];
-    __syncthreads();
   }
-  const float T = key_value(prefix), E = 48.f * 5.9604645e-8f * a.most[item];
-  float lo = -INFINITY, hi = INFINITY;
+  uint32_t kth = 0xffffffffu;  // the smallest key from low up: the K-th largest's
+  sc.each([&](uint32_t, uint32_t k) {
+    if (k >= low) kth = min(kth, k);
+  });
+  kth = __reduce_min_sync(0xffffffffu, kth);
+  __syncthreads();
+  if (lane == 0) tmp[warp] = kth;
+  __syncthreads();
+  for (uint32_t w = 0; w < kSelWarps; ++w) kth = min(kth, tmp[w]);
+  __syncthreads();
+  const float T = key_value(kth), E = 48.f * 5.9604645e-8f * most;
+  uint32_t klo = 1, khi = 0xffffffffu;  // keys above khi are in, below klo out
   if (E < INFINITY) {
-    lo = isinf(T) ? T : __fadd_rd(T, -2.f * E);
-    hi = isinf(T) ? T : __fadd_ru(T, 2.f * E);
+    klo = order_key(isinf(T) ? T : __fadd_rd(T, -2.f * E));
+    khi = order_key(isinf(T) ? T : __fadd_ru(T, 2.f * E));
   }
-  const auto value = [&](uint32_t j) { return key_value(order_key(s[j])); };
-  const auto sure = [&](uint32_t j) { return value(j) > hi; };
-  const auto maybe = [&](uint32_t j) { return value(j) >= lo && value(j) <= hi; };
-  const uint32_t n_sure = block_count(n, sure, tmp), n_maybe = block_count(n, maybe, tmp), need = K - n_sure;
-  unsigned long long bar = 0;  // what lies between is in from this key up, `ties` of the equal ones
-  uint32_t ties = need;
-  const bool again = n_maybe != need;
-  if (again) {
-    for (uint32_t j0 = 0; j0 < n; j0 += kThreads) {
-      unsigned m = __ballot_sync(0xffffffffu, j0 + tid < n && maybe(j0 + tid));
+  uint32_t c1 = 0, c2 = 0;
+  sc.each([&](uint32_t, uint32_t k) {
+    c1 += k > khi;
+    c2 += k >= klo && k <= khi;
+  });
+  const uint32_t n_sure = cta_sum(c1, tmp, turn), n_close = cta_sum(c2, tmp, turn), need = K - n_sure;
+  const bool again = n_close != need, listed = n_close <= kClose;
+  unsigned long long bar = 0;  // (not listed) a close block is in from this key up, `ties` of the equal ones
+  uint32_t ties = 0;
+  double* t = a.exact + item * a.nblk;
+  if (again && listed) {
+    if (tid == 0) s_close = 0;
+    __syncthreads();
+    sc.each([&](uint32_t j, uint32_t k) {
+      if (k >= klo && k <= khi) close_j[atomicAdd(&s_close, 1u)] = j;
+    });
+    __syncthreads();
+    for (uint32_t i = warp; i < n_close; i += kSelWarps) {
+      const uint32_t j = close_j[i];
+      const double x = forced(a, j, n) ? (double)INFINITY : exact_score<D>(a, r, g, seq, j);
+      if (lane == 0) close_t[i] = x != x ? -(double)INFINITY : x;
+    }
+    __syncthreads();
+    // those that are in keep their place in the list, the others leave it
+    uint32_t mine = 0xffffffffu;
+    if (tid < n_close) {
+      uint32_t rank = 0;
+      const double x = close_t[tid];
+      for (uint32_t i = 0; i < n_close; ++i)
+        rank += close_t[i] > x || (close_t[i] == x && close_j[i] < close_j[tid]);
+      if (rank < need) mine = close_j[tid];
+    }
+    __syncthreads();
+    if (tid < n_close) close_j[tid] = mine;
+    __syncthreads();
+  } else if (again) {
+    // many equal or unbounded scores: all of them in 64 bits, then bisection of those bits
+    const uint32_t rounds = (n + kThreads - 1) / kThreads;
+    for (uint32_t i = 0; i < rounds; ++i) {
+      const uint32_t j0 = i * kThreads + warp * 32;
+      const uint32_t k = j0 + lane < n ? order_key(__ldcg(sc.s + j0 + lane)) : 0u;
+      unsigned m = __ballot_sync(0xffffffffu, k >= klo && k <= khi);
       while (m) {
-        const uint32_t j = j0 + warp * 32 + (__ffs(m) - 1);
+        const uint32_t j = j0 + (__ffs(m) - 1);
         m &= m - 1;
         const double x = forced(a, j, n) ? (double)INFINITY : exact_score<D>(a, r, g, seq, j);
-        if (lane == 0) t[j] = x;
+        if (lane == 0) __stcg(t + j, x);
       }
     }
     __syncthreads();
-    for (int bit = 63; bit >= 0; --bit) {  // the need-th largest key, bit by bit
+    const auto count64 = [&](unsigned long long from, bool above) {
+      uint32_t c = 0;
+      sc.each([&](uint32_t j, uint32_t k) {
+        if (k >= klo && k <= khi) {
+          const unsigned long long x = order_key(__ldcg(t + j));
+          c += above ? x > from : x >= from;
+        }
+      });
+      return cta_sum(c, tmp, turn);
+    };
+    for (int bit = 63; bit >= 0; --bit) {
       const unsigned long long c = bar | (1ull << bit);
-      if (block_count(n, [&](uint32_t j) { return maybe(j) && order_key(t[j]) >= c; }, tmp) >= need) bar = c;
+      if (count64(c, false) >= need) bar = c;
     }
-    ties = need - block_count(n, [&](uint32_t j) { return maybe(j) && order_key(t[j]) > bar; }, tmp);
+    ties = need - count64(bar, true);
   }
-  // in index order, the lower of equal ones first
-  if (tid < 2) s_base[tid] = 0;
+  // in index order, the lower of equal ones first: a warp's blocks are neighbours, so ranks come from
+  // ballots and the counts of the warps before
+  const auto is_in = [&](uint32_t j, uint32_t k, bool& eq) {
+    eq = false;
+    if (k > khi) return true;
+    if (k < klo) return false;
+    if (!again) return true;
+    if (listed) {
+      for (uint32_t i = 0; i < n_close; ++i)
+        if (close_j[i] == j) return true;
+      return false;
+    }
+    const unsigned long long x = order_key(__ldcg(t + j));
+    eq = x == bar;
+    return x > bar;
+  };
+  uint32_t eq_before = 0, n_in = 0, n_eq = 0;
+  if (again && !listed) {
+    sc.each([&](uint32_t j, uint32_t k) {
+      bool eq;
+      is_in(j, k, eq);
+      n_eq += eq;
+    });
+    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
+    __syncthreads();
+    if (lane == 0) tmp[warp] = n_eq;
+    __syncthreads();
+    for (uint32_t w = 0; w < warp; ++w) eq_before += tmp[w];
+    __syncthreads();
+  }
+  const auto flag = [&](uint32_t j, uint32_t k, uint32_t& rank) {  // rank: equal ones before
+    bool eq, in = is_in(j, k, eq);
+    const unsigned me = __ballot_sync(0xffffffffu, eq);
+    if (eq) in = rank + __popc(me & ((1u << lane) - 1u)) < ties;
+    rank += __popc(me);
+    return in;
+  };
+  uint32_t rank = eq_before;
+  sc.each([&](uint32_t j, uint32_t k) { n_in += __popc(__ballot_sync(0xffffffffu, flag(j, k, rank))); });
   __syncthreads();
-  for (uint32_t j0 = 0; j0 < n; j0 += kThreads) {
-    const uint32_t j = j0 + tid;
-    bool in = false, eq = false;
-    if (j < n) {
-      in = sure(j);
-      if (maybe(j)) {
-        if (!again) in = true;
-        else if (order_key(t[j]) > bar) in = true;
-        else eq = order_key(t[j]) == bar;
-      }
-    }
-    const unsigned me = __ballot_sync(0xffffffffu, eq), below = (1u << lane) - 1u;
-    if (lane == 0) tmp[warp] = __popc(me);
-    __syncthreads();
-    uint32_t rank = s_base[0] + __popc(me & below);
-    for (uint32_t w = 0; w < warp; ++w) rank += tmp[w];
-    if (eq && rank < ties) in = true;
-    uint32_t n_eq = 0;
-    for (uint32_t w = 0; w < kThreads / 32; ++w) n_eq += tmp[w];
-    __syncthreads();
-    const unsigned mi = __ballot_sync(0xffffffffu, in);
-    if (lane == 0) tmp[warp] = __popc(mi);
-    __syncthreads();
-    uint32_t at = s_base[1] + __popc(mi & below), n_in = 0;
-    for (uint32_t w = 0; w < kThreads / 32; ++w) {
-      if (w < warp) at += tmp[w];
-      n_in += tmp[w];
-    }
-    if (in && at < K) out[at] = (int32_t)j;
+  if (lane == 0) tmp[warp] = n_in;
+  __syncthreads();
+  uint32_t at = 0;
+  for (uint32_t w = 0; w < warp; ++w) at += tmp[w];
+  rank = eq_before;
+  sc.each([&](uint32_t j, uint32_t k) {
+    const bool in = flag(j, k, rank);
+    const unsigned m = __ballot_sync(0xffffffffu, in);
+    const uint32_t to = at + __popc(m & ((1u << lane) - 1u));
+    if (in && to < K) out[to] = (int32_t)j;
+    at += __popc(m);
+  });
+}
+
+// CTA x of a (row, kv-head) scores the x-th part of its blocks; the last of them to finish chooses.
+template <int D>
+__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Select a) {
+  __shared__ float tmp[kSelWarps];
+  __shared__ uint32_t s_last;
+  const uint32_t r = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
+  uint32_t seq, pos;
+  const RowKind kind = locate(a.r, a.c.capacity, r, seq, pos);
+  if (kind != kRowOk) {
+    if (kind == kRowBad) set_status(a.status, kStatusRange);
+    return;
+  }
+  const uint32_t n = (pos >> a.blk_shift) + 1, K = a.n_select;
+  const size_t item = (size_t)r * a.c.Hkv + g;
+  if (n <= K) {  // every block is taken
+    if (blockIdx.x == 0)
+      for (uint32_t i = tid; i < K; i += kThreads) a.blocks[item * K + i] = i < n ? (int32_t)i : -1;
+    return;
+  }
+  constexpr uint32_t PER = kThreads / (D / 8);
+  const uint32_t part = ((n + gridDim.x - 1) / gridDim.x + PER - 1) / PER * PER, parts = (n + part - 1) / part;
+  if (blockIdx.x >= parts) return;
+  float* most = a.most + item * gridDim.x;
+  float m = score_blocks<D>(a, r, g, seq, n, blockIdx.x * part, min(n, (blockIdx.x + 1) * part),
+                            a.scores + item * a.nblk, tmp);
+  if (parts > 1) {
+    __threadfence();
     __syncthreads();
     if (tid == 0) {
-      s_base[0] += n_eq;
-      s_base[1] += n_in;
+      __stcg(most + blockIdx.x, m);
+      __threadfence();
+      const uint32_t had = atomicAdd(a.tickets + item, 1u);
+      s_last = had == parts - 1;
+      if (had > parts - 1) set_status(a.status, kStatusInvalid);
+      if (had == parts - 1) a.tickets[item] = 0;
+      __threadfence();
     }
     __syncthreads();
+    if (!s_last) return;
+    m = 0.f;
+    for (uint32_t p = 0; p < parts; ++p) m = fmaxf(m, __ldcg(most + p));
+  } else {
+    __syncthreads();
   }
+  choose<D>(a, r, g, seq, n, item, m);
 }
 
 }  // namespace
@@ -377,38 +602,38 @@ __global__ void __launch_bounds__(kThreads) choose_kernel(const Select a) {
   }
 
 cudaError_t append(const Append& a, cudaStream_t st) {
-  const uint32_t blocks = item_blocks(a.r, a.c);
   const bool t8 = a.c.ks != nullptr;
-#define CALL(DD)                                                         \
-  if (t8) append_kernel<DD, true><<<blocks, kThreads, 0, st>>>(a);       \
-  else append_kernel<DD, false><<<blocks, kThreads, 0, st>>>(a);         \
-  if (a.bounds) bounds_kernel<DD><<<blocks, kThreads, 0, st>>>(a)
+  const uint32_t rows = row_ctas_of(a.r, a.c, t8);
+  const uint32_t span = a.r.row_start ? 1u << a.blk_shift : 1u;  // rows of a bounds CTA: about one block's
+  const uint32_t grid = rows + (a.bounds ? (a.r.n_rows + span - 1) / span * a.c.Hkv : 0);
+#define CALL(DD)                                                               \
+  if (t8) append_kernel<DD, true><<<grid, kThreads, 0, st>>>(a, rows, span);   \
+  else append_kernel<DD, false><<<grid, kThreads, 0, st>>>(a, rows, span)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
   return cudaGetLastError();
 }
 
 cudaError_t read(const Read& a, cudaStream_t st) {
-  const uint32_t blocks = item_blocks(a.r, a.c);
   const bool t8 = a.c.ks != nullptr;
-#define CALL(DD)                                                    \
-  if (t8) read_kernel<DD, true><<<blocks, kThreads, 0, st>>>(a);    \
-  else read_kernel<DD, false><<<blocks, kThreads, 0, st>>>(a)
+  const uint32_t grid = row_ctas_of(a.r, a.c, t8);
+#define CALL(DD)                                                   \
+  if (t8) read_kernel<DD, true><<<grid, kThreads, 0, st>>>(a);     \
+  else read_kernel<DD, false><<<grid, kThreads, 0, st>>>(a)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
   return cudaGetLastError();
 }
 
+uint32_t select_parts(uint32_t items, uint32_t nblk, uint32_t D, uint32_t ctas) {
+  // a CTA scores at least one pass of four blocks a team
+  const uint32_t per = kThreads / (D / 8) * 4;
+  return std::max(1u, std::min((nblk + per - 1) / per, ctas / items));
+}
+
 cudaError_t select(const Select& a, cudaStream_t st) {
-  const size_t items = (size_t)a.r.n_rows * a.c.Hkv;
-  cudaError_t e = cudaMemsetAsync(a.most, 0, items * 4, st);
-  if (e != cudaSuccess) return e;
-  const uint32_t per = kThreads / (a.c.D / 8);
-  const uint32_t parts = (uint32_t)std::min<size_t>((a.nblk + per - 1) / per, std::max<size_t>(1, 1216 / items));
-  const dim3 sg(parts, a.c.Hkv, a.r.n_rows), cg(a.c.Hkv, a.r.n_rows);
-#define CALL(DD)                                       \
-  score_kernel<DD><<<sg, kThreads, 0, st>>>(a);        \
-  choose_kernel<DD><<<cg, kThreads, 0, st>>>(a)
+  const dim3 grid(select_parts(a.r.n_rows * a.c.Hkv, a.nblk, a.c.D, a.ctas), a.c.Hkv, a.r.n_rows);
+#define CALL(DD) select_kernel<DD><<<grid, kThreads, 0, st>>>(a)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
   return cudaGetLastError();

@@ -61,11 +61,15 @@ struct Select {
   int32_t* blocks;    // [n_rows][Hkv][n_select]
   float* scores;      // work [n_rows * Hkv][nblk]
   double* exact;      // work, the same shape
-  float* most;        // work [n_rows * Hkv]: the largest sum of a block's absolute terms
+  float* most;        // work [n_rows * Hkv][parts]: bounds of the blocks' sums of absolute terms
+  uint32_t* tickets;  // [n_rows * Hkv], zero between calls
+  uint32_t ctas;      // CTAs that fill the GPU
   uint32_t H, blk_shift, nblk, n_select, n_first, n_last;
   int* status;
 };
 cudaError_t select(const Select& a, cudaStream_t st);
+constexpr uint32_t kMaxItems = 32768;  // kMaxQueries rows of 8 kv-heads
+constexpr uint32_t kMaxParts = 1024;   // parts of all items: at most one an item, or this many
 
 struct Attend {
   Cache c;
@@ -74,9 +78,9 @@ struct Attend {
   const uint16_t* gate;  // [n_rows][H] values of D, gate_stride apart, or null
   const int32_t* blocks; // [n_rows][Hkv][n_blocks], or null: every token
   uint16_t* out;         // [n_rows][H][D]
-  uint32_t* tickets;     // [ctas], zero between calls
-  float* parts;          // work [ctas][2][H / Hkv][D + 4]
-  uint32_t ctas;         // CTAs that fill the GPU
+  uint32_t* tickets;     // [kMaxCtas], zero between calls
+  float* parts;          // work [kMaxCtas][2][H / Hkv][D + 4]
+  uint32_t sms;          // of the GPU
   uint32_t H, gate_stride, n_blocks, blk_shift;
   int* status;
 };
