@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kMaxDevices = 64;
 // What qwen35_scratch_init zeroes: the status word and every kind of scratch's counters.
-constexpr size_t kScratchZeroed = 256 + (320 + 32768) * 4;
+constexpr size_t kScratchZeroed = 256 + (q35c::kMaxCtas + q35c::kMaxItems) * 4;
 int g_num_sms[kMaxDevices] = {0};
 
 int num_sms() {
@@ -381,7 +381,7 @@ int qwen35_init(void) {
       cudaDeviceGetAttribute(&coop, cudaDevAttrCooperativeLaunch, dev) != cudaSuccess)
     return QWEN35_ERR_CUDA;
   if (major != 10 || minor != 3 || !coop) return QWEN35_ERR_CUDA;  // built for sm_103a only
-  if (decode_set_attributes() != cudaSuccess) return QWEN35_ERR_CUDA;
+  if (decode_set_attributes() != cudaSuccess || q35c::attend_attributes() != cudaSuccess) return QWEN35_ERR_CUDA;
   g_num_sms[dev] = sms;
   return QWEN35_OK;
 }
@@ -1136,7 +1136,7 @@ CacheNeed cache_need(uint32_t Hkv, uint32_t nblk, uint32_t n_rows) {
 }
 // Scratch of the attention: two parts of a split item for each CTA.
 size_t attend_need(uint32_t group, uint32_t D) {
-  return kCacheWork + (size_t)2 * q35c::kMaxCtas * group * (D + 4) * 4;
+  return kCacheWork + (size_t)2 * q35c::kMaxCtas * std::max(group, 8u) * (D + 4) * 4;
 }
 
 // The head counts and dims the cache operators take (the other fields of the config
@@ -1271,7 +1271,7 @@ int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_cache* kv, co
   a.exact = reinterpret_cast<double*>(s + need.exact);
   a.most = reinterpret_cast<float*>(s + need.most);
   a.tickets = reinterpret_cast<uint32_t*>(s + kSelTickets);
-  a.ctas = std::min(8u * (uint32_t)num_sms(), q35c::kMaxParts);
+  a.ctas = std::min(2u * (uint32_t)num_sms(), q35c::kMaxParts);
   a.H = cfg->num_heads;
   a.blk_shift = log2_of(bounds->block);
   a.n_select = n_select;

@@ -1,13 +1,15 @@
 // Attention of new tokens over a KV cache (cache_ops.h): one launch for any number of
 // rows, split over the cache's length and joined.
 //
-// Per (row, kv-head), an item, softmax(q K^T / sqrt D) V for the kv-head's group of up to
-// 16 q-heads. The bytes of K and V bound it: each is read once for the whole group, by
-// asynchronous copies into shared memory, and the products run on matrix instructions
-// with the tokens as their rows (M = 16), the heads as their columns (N = 8), so that a
-// group of 4 costs one instruction per 16 tokens x 16 dims:
-//   S^T [16 tokens x 8 heads] += K [16 x 16 dims] Q^T [16 dims x 8], D / 16 times;
-//   O^T [16 dims x 8 heads] += V^T [16 dims x 16 tokens] P^T [16 tokens x 8], D / 16 times.
+// An item is a kv-head of one row, or of as many neighbouring rows of a sequence as
+// its group of q-heads leaves room for in eight columns (a group of 1: 8 rows, of 4: 2;
+// only without a list of blocks, which every row has of its own): softmax(q K^T /
+// sqrt D) V for the columns, (row, q-head) pairs. The bytes of K and V bound it: each is read once
+// for all columns, by asynchronous copies into shared memory, and the products run on
+// matrix instructions with the tokens as their rows (M = 16) and the columns as
+// theirs (N = 8), one instruction per 16 tokens x 16 dims:
+//   S^T [16 tokens x 8] += K [16 x 16 dims] Q^T [16 dims x 8], D / 16 times;
+//   O^T [16 dims x 8] += V^T [16 dims x 16 tokens] P^T [16 tokens x 8], D / 16 times.
 // A warp works alone: it has its own ring of K and V tiles of 16 tokens, its own running
 // maximum, sum and output, and meets the other warps only at the end of an item.
 //
@@ -17,9 +19,10 @@
 //
 // Roundings: bf16 K, V and q enter the products exactly, the weights P as hi + lo bf16
 // (2^-16 relative). Turbo8 codes enter as f16 (exact); the K scales multiply the fp32
-// products of their 16 dims; the rotated q enters as hi + lo f16 (2^-21); V = code * scale is
-// rounded to f16 (2^-12 relative: 12 bits to 11) with its tile's largest scale taken out as a power
-// of two, which is put into the weights, and those are rounded to f16 (2^-12).
+// products of their 16 dims; the rotated q enters as hi + lo f16 (2^-21). The weights are rounded to f16
+// (2^-12), multiplied by the V scales of each 16 dims and rounded to f16 again (2^-12); the
+// tile's largest scale goes into the exponent of the weights as a power of two, so that neither factor
+// leaves f16's range.
 #include "cache_ops.cuh"
 #include "turbo8.cuh"
 
@@ -29,38 +32,50 @@ namespace q35c {
 using namespace q35;
 namespace {
 
-#ifndef ATT_WARPS
-#define ATT_WARPS 8
+// Warps of a CTA, one CTA an SM.
+template <int D, int NT, bool T8>
+constexpr int warps_of() {
+#ifndef ATT_T8W
+#define ATT_T8W 8
 #endif
-constexpr int kWarps = ATT_WARPS, kCtasPerSm = 8 / kWarps;
-constexpr int kAttnThreads = 32 * kWarps;
+  return T8 && D * NT <= 256 ? ATT_T8W : 8;
+}
 
 // A ring slot: K or V of 16 tokens. Rows are padded by 16 bytes, which puts eight rows'
 // 16-byte pieces in different banks.
-template <int D, bool T8>
+template <int D, int NT, bool T8>
 struct Slot {
   static constexpr int row = T8 ? D + 16 : 2 * D + 16;
   static constexpr int scales = T8 ? D / 16 * 2 : 0;  // a token's scales
   static constexpr int bytes = 16 * (row + scales);
-  static constexpr int n = D == 256 && !T8 ? 3 : 4;  // slots of a warp
+  // slots of a warp, what shared memory holds up to 4 (K and V of two tiles)
+  static constexpr int n = D == 256 ? (T8 ? (warps_of<D, NT, T8>() == 16 ? 2 : warps_of<D, NT, T8>() == 12 ? 3 : 4) : 3) : 4;
 };
-// Shared memory of a CTA: the rings (reused to join the warps), Q's fragments, the warps'
-// maxima and sums, T8's transposed V scales, then the rows' first tiles.
+// Shared memory of a CTA: the rings (reused to join the warps), Q's fragments and (T8)
+// the rotated q, the warps' maxima and sums, T8's transposed V scales, then the rows' first tiles.
 template <int D, int NT, bool T8>
 struct Smem {
-  using S = Slot<D, T8>;
+  using S = Slot<D, NT, T8>;
+  static constexpr int kWarps = warps_of<D, NT, T8>();
   static constexpr int ring = kWarps * S::n * S::bytes;
   static constexpr int join = kWarps * 8 * NT * (D + 4) * 4;
   static constexpr int weights = 24576;  // the parts' weights, behind their sums
   static constexpr int parts = weights + 8 * NT * (int)kMaxCtas * 4;
   static constexpr int big = ring > join ? (ring > parts ? ring : parts) : join > parts ? join : parts;
   static constexpr int qf = big;                                    // fragments, 8 or (T8) 16 bytes a lane
-  static constexpr int ml = qf + (D / 16) * NT * 32 * (T8 ? 16 : 8);  // [warps + 1][2][16]
+  static constexpr int qs = qf + (D / 16) * NT * 32 * (T8 ? 16 : 8);  // [8 NT][D] fp32
+  static constexpr int ml = qs + (T8 ? 8 * NT * D * 4 : 0);           // [warps + 1][2][16]
   static constexpr int vsc = ml + (kWarps + 1) * 2 * 16 * 4;
-  static constexpr int misc = vsc + (T8 ? kWarps * (D / 16) * 32 : 0);
-  static constexpr int first = misc + 128;  // [n_rows + 1]
+  static constexpr int scale_row = D / 8 + 4;  // words, padded
+  static constexpr int misc = vsc + (T8 ? kWarps * scale_row * 16 : 0);
+  static constexpr int first = misc + 256;  // [n_rows + 1]
+  static_assert(kWarps <= 16 && 2 * kMaxSeqs * 4 + 4 <= big, "misc, the rows' places");
+  // misc: words 0-15 and 40-55 the warps' sums, 16 a flag, 20-35 (T8) q's powers of two
 };
 
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
 }
@@ -119,14 +134,27 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ float ex2(float x) {  // 2^x to 2^-22 relative; 0 below 2^-126
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
-__device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.f : exp2f(from - to); }
+__device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.f : ex2(from - to); }
 
-// One item's stretch in a CTA.
+__device__ __forceinline__ uint32_t count_up(uint32_t* p) {
+  uint32_t had;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(had) : "l"(p) : "memory");
+  return had;
+}
+
+// One item's stretch in a CTA: rows row .. row + rows - 1, the last at position pos.
 struct Segment {
-  uint32_t row, g, seq, pos;
+  uint32_t row, rows, g, seq, pos;
   uint32_t tiles;   // the item's tiles
   uint32_t t0, t1;  // this CTA's
+  size_t row0;         // contiguous: the sequence's first cache row
+  const int32_t* tab;  // paged: its table
 };
 
 // The first token of a tile and where its tokens lie: rows of tokens 0-7 and 8-15 (a
@@ -139,13 +167,16 @@ struct Tile {
 
 template <int D, int NT, bool T8>
 struct Attention {
-  using S = Slot<D, T8>;
+  using S = Slot<D, NT, T8>;
   using M = Smem<D, NT, T8>;
+  static constexpr int kWarps = M::kWarps, kAttnThreads = 32 * kWarps;
   const Attend& a;
   uint8_t* sm;
   uint32_t warp, lane, group;
+  uint32_t pack;  // the most rows of an item
   uint32_t ring;  // this warp's slots
   float m[NT][2], l[NT][2], o[D / 16][NT][4];
+  uint32_t later[NT][2];  // tokens of the item's last row that this column's row does not see
   float qscale[NT][2];  // log2(e) / sqrt(D), with T8's power of two of q
 
   // ---- where a tile's tokens are
@@ -165,101 +196,152 @@ struct Attention {
     if (token > s.pos) return x;
     x.token = (uint32_t)token;
     x.seen = min(16u, s.pos - x.token + 1);
-    bool ok = true;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-      if (8u * h < x.seen) {
-        x.in[h] = cache_row(a.c, s.seq, x.token + 8 * h, x.row[h]);
-        ok = ok && x.in[h];
-      }
-    if (!ok) set_status(a.status, kStatusRange);
+    if (s.tab) {
+      const uint32_t sh = a.c.bt_shift, mask = (1u << sh) - 1u, t8 = x.token + (x.seen > 8 ? 8 : 0);
+      const uint32_t b0 = (uint32_t)s.tab[x.token >> sh], b1 = (uint32_t)s.tab[t8 >> sh];
+      x.in[0] = b0 < a.c.num_blocks;
+      x.in[1] = b1 < a.c.num_blocks;
+      x.row[0] = ((size_t)b0 << sh) | (x.token & mask);
+      x.row[1] = ((size_t)b1 << sh) | ((x.token + 8) & mask);
+      if (!x.in[0] || !x.in[1]) set_status(a.status, kStatusRange);
+    } else {
+      x.in[0] = x.in[1] = true;
+      x.row[0] = s.row0 + x.token;
+      x.row[1] = x.row[0] + 8;
+    }
     return x;
   }
 
-  // ---- K (p = 0) or V of a tile into a slot; tokens the row does not see read as zero
+  // ---- K (p = 0) or V of a tile into a slot. Tokens no row sees read as zero; so do the V rows of
+  // tokens that only later rows of the item see (add_tail): their weight is 0 in the earlier rows' columns,
+  // and 0 times an infinity would spoil them.
   __device__ void load(const Segment& s, const Tile& x, int p, uint32_t slot) const {
+    const uint32_t last = s.pos + 1 - (p ? s.rows - 1 : 0);  // tokens below it
+    const uint32_t seen = x.seen ? min(x.seen, last > x.token ? last - x.token : 0u) : 0u;
     constexpr int C = (T8 ? D : 2 * D) / 16, R = 32 / C > 0 ? 32 / C : 1;  // 16-byte pieces of a row, rows a pass
     const uint8_t* base = p ? a.c.v : a.c.k;
-    const uint32_t dst = ring + slot * S::bytes;
-    const size_t stride = (size_t)a.c.Hkv * D * (T8 ? 1 : 2);
-    const uint32_t r0 = lane / C, c = lane % C;
+    const uint32_t stride = a.c.Hkv * D * (T8 ? 1 : 2), r0 = lane / C, c = lane % C;
+    const uint32_t dst = ring + slot * S::bytes, to = dst + r0 * S::row + c * 16;
+    const uint32_t within = r0 * stride + s.g * D * (T8 ? 1 : 2) + c * 16;
+    const uint8_t* p0 = base + x.row[0] * stride + within;
+    const uint8_t* p1 = base + x.row[1] * stride + within;
+    const bool full = seen == 16 && x.in[0] && x.in[1];
+    if (full) {
 #pragma unroll
-    for (int i = 0; i < 16 / R; ++i) {
-      const uint32_t r = i * R + r0, h = (i * R) / 8;
-      const bool in = r < x.seen && x.in[h];
-      const uint8_t* src = base + (x.row[h] + (r & 7)) * stride + (size_t)s.g * D * (T8 ? 1 : 2) + c * 16;
-      cp16(dst + r * S::row + c * 16, in ? src : base, in);
+      for (int i = 0; i < 8 / R; ++i) {
+        cp16(to + i * R * S::row, p0);
+        cp16(to + (8 + i * R) * S::row, p1);
+        p0 += R * stride;
+        p1 += R * stride;
+      }
+    } else {  // the last tile of an item
+#pragma unroll 1
+      for (int i = 0; i < 16 / R; ++i) {
+        const uint32_t r = i * R + r0;
+        const bool in = r < seen && (r & 8 ? x.in[1] : x.in[0]);
+        const uint8_t* src = r & 8 ? p1 + (i * R - 8) * (int)stride : p0 + i * R * stride;
+        cp16(to + i * R * S::row, in ? src : base, in);
+      }
     }
     if constexpr (T8) {
       constexpr int SB = S::scales, P = SB >= 16 ? SB / 16 : 1;  // pieces of a token's scales
       const uint8_t* sbase = reinterpret_cast<const uint8_t*>(p ? a.c.vs : a.c.ks);
       const uint32_t r = lane / P, c2 = lane % P;
       if (r < 16) {
-        const bool in = r < x.seen && (r & 8 ? x.in[1] : x.in[0]);
+        const bool in = r < seen && (r & 8 ? x.in[1] : x.in[0]);
         const size_t row = (r & 8 ? x.row[1] : x.row[0]) + (r & 7);
         const uint8_t* src = sbase + (row * a.c.sstride + s.g * (D / 16)) * 2 + c2 * 16;
-        const uint32_t to = dst + 16 * S::row + r * SB + c2 * 16;
-        if constexpr (SB >= 16) cp16(to, in ? src : sbase, in);
-        else cp8(to, in ? src : sbase, in);
+        const uint32_t sto = dst + 16 * S::row + r * SB + c2 * 16;
+        if constexpr (SB >= 16) cp16(sto, in ? src : sbase, in);
+        else cp8(sto, in ? src : sbase, in);
       }
     }
   }
 
-  // ---- q of an item as B fragments, [k-step][n-tile][lane]
-  __device__ void load_q(const Segment& s) {
-    float* qs = reinterpret_cast<float*>(sm);  // [8 NT][D] (the ring is empty)
-    const uint16_t* q = a.q + ((size_t)s.row * a.H + s.g * group) * D;
-    constexpr int LPR = D / 8;
-    int* qe = reinterpret_cast<int*>(sm + M::misc) + 8;  // [16]
-    for (uint32_t i = threadIdx.x; i < 8 * NT * LPR; i += kAttnThreads) {
-      const uint32_t h = i / LPR, c = i % LPR;
-      float x[8] = {};
-      if (h < group) unpack8(*reinterpret_cast<const uint4*>(q + h * D + 8 * c), x);
+  // ---- q of an item as B fragments, [k-step][n-tile][lane]; column c: row c / group, head c % group
+  __device__ __forceinline__ const uint16_t* q_at(const Segment& s, uint32_t col) const {
+    return a.q + ((size_t)(s.row + col / group) * a.H + s.g * group + col % group) * D;
+  }
+  // What a thread holds of q between its loads, which go ahead of the first copies, and their use.
+  static constexpr int kFrag = (D / 16) * NT * 32;  // fragments
+  static constexpr int kQ = T8 ? (8 * NT * (D / 8) + kAttnThreads - 1) / kAttnThreads
+                               : (kFrag + kAttnThreads - 1) / kAttnThreads;
+  struct QRegs {
+    uint4 u[kQ];  // T8: eight elements; bf16: a fragment's two words
+  };
+  __device__ QRegs fetch_q(const Segment& s) const {
+    const uint32_t cols = group * s.rows;
+    QRegs q;
+#pragma unroll
+    for (int k = 0; k < kQ; ++k) {
+      const uint32_t i = threadIdx.x + k * kAttnThreads;
+      q.u[k] = make_uint4(0u, 0u, 0u, 0u);
       if constexpr (T8) {
-        wht8<LPR>(x, lane);
-        float mx = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
-#pragma unroll
-        for (int w = 1; w < LPR; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        // |x| 2^-e below 2^15: e = exponent - 14
-        const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127 - 14, -100), 100);
-        const float f = mx > 0.f ? pow2(-e2) : 1.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] *= f;
-        if (c == 0) qe[h] = mx > 0.f ? e2 : 0;
+        const uint32_t h = i / (D / 8), c = i % (D / 8);
+        if (h < cols) q.u[k] = *reinterpret_cast<const uint4*>(q_at(s, h) + 8 * c);
+      } else {
+        const uint32_t ln = i & 31, nt = (i >> 5) % NT, kk = (i >> 5) / NT, col = 8 * nt + ln / 4, c = ln % 4;
+        if (i < kFrag && col < cols) {
+          const uint16_t* x = q_at(s, col) + 16 * kk + 2 * c;
+          q.u[k].x = *reinterpret_cast<const uint32_t*>(x);
+          q.u[k].y = *reinterpret_cast<const uint32_t*>(x + 8);
+        }
       }
+    }
+    return q;
+  }
+  __device__ void put_q(const QRegs& q) {
+    constexpr int LPR = D / 8;
+    float* qs = reinterpret_cast<float*>(sm + M::qs);
+    int* qe = reinterpret_cast<int*>(sm + M::misc) + 20;
 #pragma unroll
-      for (int e = 0; e < 8; ++e) qs[h * D + 8 * c + e] = x[e];
+    for (int k = 0; k < kQ; ++k) {
+      const uint32_t i = threadIdx.x + k * kAttnThreads;
+      if constexpr (T8) {
+        if (i < 8 * NT * LPR) {  // whole warps
+          const uint32_t h = i / LPR, c = i % LPR;
+          float x[8];
+          unpack8(q.u[k], x);
+          wht8<LPR>(x, lane);
+          float mx = 0.f;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+          for (int w = 1; w < LPR; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          // |x| 2^-e below 2^15: e = exponent - 14
+          const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127 - 14, -100), 100);
+          const float f = mx > 0.f ? pow2(-e2) : 1.f;
+          if (c == 0) qe[h] = mx > 0.f ? e2 : 0;
+#pragma unroll
+          for (int e = 0; e < 8; ++e) qs[h * D + 8 * c + e] = x[e] * f;
+        }
+      } else {
+        if (i < kFrag) *reinterpret_cast<uint2*>(sm + M::qf + i * 8) = make_uint2(q.u[k].x, q.u[k].y);
+      }
     }
     __syncthreads();
-    constexpr int N = (D / 16) * NT;
-    for (uint32_t i = threadIdx.x; i < N * 32; i += kAttnThreads) {
-      const uint32_t ln = i & 31, nt = (i >> 5) % NT, kk = (i >> 5) / NT;
-      const float* x = qs + (8 * nt + ln / 4) * D + 16 * kk;
-      const uint32_t c = ln % 4;
-      if constexpr (T8) {
+    if constexpr (T8) {
+      for (uint32_t i = threadIdx.x; i < kFrag; i += kAttnThreads) {
+        const uint32_t ln = i & 31, nt = (i >> 5) % NT, kk = (i >> 5) / NT, c = ln % 4;
         // a code word of 4 dims feeds both halves of the k-step: dims 4c, 4c+1 | 4c+2, 4c+3
+        const float4 x = *reinterpret_cast<const float4*>(qs + (8 * nt + ln / 4) * D + 16 * kk + 4 * c);
         uint32_t hi[2], lo[2];
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
-          const float u = x[4 * c + 2 * j], v = x[4 * c + 2 * j + 1];
+          const float u = j ? x.z : x.x, v = j ? x.w : x.y;
           hi[j] = pack_f16(u, v);
           const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
           lo[j] = pack_f16(u - f.x, v - f.y);
         }
         *reinterpret_cast<uint4*>(sm + M::qf + i * 16) = make_uint4(hi[0], hi[1], lo[0], lo[1]);
-      } else {
-        *reinterpret_cast<uint2*>(sm + M::qf + i * 8) =
-            make_uint2(pack_bf16(x[2 * c], x[2 * c + 1]), pack_bf16(x[2 * c + 8], x[2 * c + 9]));
       }
+      __syncthreads();
     }
     const float sl2 = 1.4426950408889634f / sqrtf((float)D);
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) qscale[nt][j] = T8 ? sl2 * pow2(qe[8 * nt + 2 * (lane % 4) + j]) : sl2;
-    __syncthreads();  // the ring is free
   }
 
   // ---- one tile: scores from its K slot
@@ -330,10 +412,11 @@ struct Attention {
     }
   }
 
-  // ---- T8: a tile's V scales, divided by 2^e, transposed to [dims group][token] f16; returns e
+  // ---- T8: a tile's V scales, divided by 2^e, as f16 pairs of tokens: word (c, g, h) has tokens 2c + 8h and
+  // 2c + 8h + 1 of dims group g; returns e
   __device__ int v_scales(uint32_t slot) const {
     const uint8_t* sc = sm + (ring - smem_addr(sm)) + slot * S::bytes + 16 * S::row;
-    uint16_t* t = reinterpret_cast<uint16_t*>(sm + M::vsc + warp * (D / 16) * 32);
+    uint16_t* t = reinterpret_cast<uint16_t*>(sm + M::vsc + warp * M::scale_row * 16);
     constexpr int PER = D / 32;  // scales a lane: half a token's
     const uint32_t tok = lane >> 1, g0 = (lane & 1) * PER;
     float f[PER], mx = 0.f;
@@ -344,17 +427,19 @@ struct Attention {
       f[i + 1] = bf16hi(u);
       mx = fmaxf(mx, fmaxf(f[i], f[i + 1]));
     }
-    mx = warp_max(mx);
+    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));  // scales are not negative
     const int e = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -60), 60) : -60;
     const float k = pow2(-e);
+    uint16_t* to = t + ((tok & 7) >> 1) * M::scale_row * 2 + g0 * 4 + (tok >> 3) * 2 + (tok & 1);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) t[(g0 + i) * 16 + tok] = __half_as_ushort(__float2half_rn(f[i] * k));
+    for (int i = 0; i < PER; ++i) to[i * 4] = __half_as_ushort(__float2half_rn(f[i] * k));
     __syncwarp();
     return e;
   }
 
-  // ---- one tile: weights from the scores, then the output from its V slot
-  __device__ void accumulate(uint32_t slot, float (&s)[NT][4], uint32_t seen) {
+  // ---- one tile: weights from the scores, then the output from its V slot; the last row sees `seen` tokens
+  // from the tile's first on
+  __device__ __forceinline__ int accumulate(uint32_t slot, float (&s)[NT][4], uint32_t seen) {
     const uint32_t r = lane >> 2;
     int ev = 0;
     if constexpr (T8) ev = v_scales(slot);
@@ -370,17 +455,17 @@ struct Attention {
           x0 += (float)ev;
           x1 += (float)ev;
         }
-        if (r >= seen) x0 = -INFINITY;
-        if (r + 8 >= seen) x1 = -INFINITY;
+        if (r + later[nt][j] >= seen) x0 = -INFINITY;
+        if (r + 8 + later[nt][j] >= seen) x1 = -INFINITY;
         float mx = fmaxf(x0, x1);
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
         const float mn = fmaxf(m[nt][j], mx), mu = mn == -INFINITY ? 0.f : mn;
-        corr[nt][j] = m[nt][j] == mn ? 1.f : exp2f(m[nt][j] - mu);
+        corr[nt][j] = m[nt][j] == mn ? 1.f : ex2(m[nt][j] - mu);
         grew |= m[nt][j] != mn;
         m[nt][j] = mn;
-        s[nt][j] = exp2f(x0 - mu);
-        s[nt][2 + j] = exp2f(x1 - mu);
+        s[nt][j] = ex2(x0 - mu);
+        s[nt][2 + j] = ex2(x1 - mu);
         const float sum = s[nt][j] + s[nt][2 + j];
         l[nt][j] = l[nt][j] * corr[nt][j] + (T8 ? sum * pow2(-ev) : sum);
       }
@@ -411,22 +496,21 @@ struct Attention {
     if constexpr (T8) {
       // matrices: tokens 0-7 and 8-15 of a group of 16 dims, then of the next
       const uint32_t at = v + (r8 + (q4 & 1) * 8) * S::row + (q4 >> 1) * 16;
-      const uint8_t* t = sm + M::vsc + warp * (D / 16) * 32 + (lane & 3) * 4;
+      const uint32_t* t = reinterpret_cast<const uint32_t*>(sm + M::vsc + warp * M::scale_row * 16) + (lane & 3) * M::scale_row;
 #pragma unroll
       for (int g2 = 0; g2 < D / 32; ++g2) {
         uint32_t w[4];
         ldsm4t(w, at + g2 * 32);
+        const uint4 c4 = *reinterpret_cast<const uint4*>(t + g2 * 4);  // two groups' scales of tokens 2c.. and 2c + 8..
 #pragma unroll
         for (int j = 0; j < 2; ++j) {
           const int g = 2 * g2 + j;
-          const uint32_t c0 = *reinterpret_cast<const uint32_t*>(t + g * 32);       // tokens 2c, 2c+1
-          const uint32_t c1 = *reinterpret_cast<const uint32_t*>(t + g * 32 + 16);  // tokens 2c+8, 2c+9
           // (dims 2r, 2r+1 of token 2c, then of 2c+1) -> (tokens 2c, 2c+1 of dim 2r, then of 2r+1)
           const uint32_t w0 = __byte_perm(w[2 * j], 0u, 0x3120), w1 = __byte_perm(w[2 * j + 1], 0u, 0x3120);
-          const uint32_t A[4] = {hmul2(e4m3_to_f16x2(w0), c0), hmul2(e4m3_to_f16x2(w0 >> 16), c0),
-                                 hmul2(e4m3_to_f16x2(w1), c1), hmul2(e4m3_to_f16x2(w1 >> 16), c1)};
+          const uint32_t A[4] = {e4m3_to_f16x2(w0), e4m3_to_f16x2(w0 >> 16), e4m3_to_f16x2(w1), e4m3_to_f16x2(w1 >> 16)};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma<true>(o[g][nt], A, ph[nt][0], ph[nt][1]);
+          for (int nt = 0; nt < NT; ++nt)
+            mma<true>(o[g][nt], A, hmul2(ph[nt][0], j ? c4.z : c4.x), hmul2(ph[nt][1], j ? c4.w : c4.y));
         }
       }
       __syncwarp();  // the transposed scales are free
@@ -443,16 +527,65 @@ struct Attention {
         }
       }
     }
+    return ev;
   }
 
-  // ---- the segment's tiles t0 + warp, t0 + warp + kWarps, ...
-  __device__ void walk(const Segment& s) {
+  // ---- the tokens of a tile that the item's first row does not see (the call's own later rows: at most
+  // seven): their V from the cache, weight times value in the columns that see them
+  __device__ void add_tail(const Segment& sg, uint32_t t, const float (&p)[NT][4], int ev) {
+    const Tile x = tile(sg, t);
+    const uint32_t first = sg.pos + 2 - sg.rows, r = lane >> 2;  // the first such token
+    for (uint32_t k = first > x.token ? first - x.token : 0u; k < x.seen; ++k) {
+      if (!(k & 8 ? x.in[1] : x.in[0])) continue;
+      const size_t row = (k & 8 ? x.row[1] : x.row[0]) + (k & 7);
+      const size_t at = (row * a.c.Hkv + sg.g) * D;
+      float w[NT][2];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const float lo = __shfl_sync(0xffffffffu, p[nt][j], (k & 7) * 4 + (lane & 3));
+          const float hi = __shfl_sync(0xffffffffu, p[nt][2 + j], (k & 7) * 4 + (lane & 3));
+          w[nt][j] = k & 8 ? hi : lo;
+        }
+#pragma unroll
+      for (int d = 0; d < D / 16; ++d) {
+        const uint32_t d0 = 16 * d + (T8 ? 2 * r : r), d1 = 16 * d + (T8 ? 2 * r + 1 : r + 8);
+        float v0, v1;
+        if constexpr (T8) {
+          const float sc = bf16f(a.c.vs[row * a.c.sstride + sg.g * (D / 16) + d]) * pow2(-ev);
+          const float2 v = e4m3_pair_value(*reinterpret_cast<const uint16_t*>(a.c.v + at + d0));
+          v0 = v.x * sc;
+          v1 = v.y * sc;
+        } else {
+          v0 = bf16f(reinterpret_cast<const uint16_t*>(a.c.v)[at + d0]);
+          v1 = bf16f(reinterpret_cast<const uint16_t*>(a.c.v)[at + d1]);
+        }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+            if (w[nt][j] != 0.f) {
+              o[d][nt][j] = fmaf(w[nt][j], v0, o[d][nt][j]);
+              o[d][nt][2 + j] = fmaf(w[nt][j], v1, o[d][nt][2 + j]);
+            }
+      }
+    }
+  }
+
+  // ---- this warp's tiles of a segment, t0 + warp, t0 + warp + kWarps, ...: K and V of each in turn through the
+  // ring, S::n half-tiles ahead. One loop for the start, where q is put in place, and the rest, so that the copies'
+  // code is there once: an SM runs it cold, and what it fetches shows in the small calls.
+  __device__ __forceinline__ void walk(const Segment& s, const QRegs& q) {
+    const uint32_t first = s.t0 + warp;
+    const int halves = first < s.t1 ? 2 * (int)((s.t1 - first + kWarps - 1) / kWarps) : 0;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         m[nt][j] = -INFINITY;
         l[nt][j] = 0.f;
+        later[nt][j] = s.rows - 1 - min((8 * nt + 2 * (lane & 3) + j) / group, s.rows - 1);
       }
 #pragma unroll
     for (int d = 0; d < D / 16; ++d)
@@ -460,47 +593,38 @@ struct Attention {
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[d][nt][i] = 0.f;
-    // slots hold K and V of tiles in turn; half-tile i of this warp: tile i / 2, V if odd.
-    // The copies run S::n half-tiles ahead; `ahead` is the tile they are at.
-    const uint32_t first = s.t0 + warp;
-    if (first >= s.t1) return;
-    const uint32_t n = (s.t1 - first + kWarps - 1) / kWarps, halves = 2 * n;
-    Tile ahead = tile(s, first), next = tile(s, first + kWarps);
-    uint32_t issued = 0, islot = 0;
-    auto issue = [&]() {
-      if (issued < halves) {
-        load(s, ahead, issued & 1, islot);
-        if (issued & 1) {  // the next tile's place, one tile before its copies
-          ahead = next;
-          next = tile(s, first + (issued / 2 + 2) * kWarps);
+    float sc[NT][4];
+    uint32_t slot = 0, seen = 0;  // the slot that is read now and refilled then
+    Tile ahead, next;             // the tile that is being copied, and the one after it, looked up half a tile ahead
+    next.seen = ahead.seen = 0;
+#pragma unroll 1
+    for (int h = -S::n - 2; h < max(halves, 1); ++h) {
+      if (h == 0) put_q(q);
+      if (h >= 0 && h < halves) {
+        cp_wait<S::n - 1>();
+        __syncwarp();
+        const uint32_t t = first + (h >> 1) * kWarps;
+        if (!(h & 1)) {
+          seen = seen_of(s, t);
+          if (seen) scores(slot, sc);
+        } else if (seen) {
+          const int ev = accumulate(slot, sc, seen);
+          if (seen < 16 + s.rows - 1 && s.rows > 1) add_tail(s, t, sc, ev);
         }
+        __syncwarp();  // this half-tile has been read by every lane
       }
-      cp_commit();
-      ++issued;
-      islot = islot + 1 == S::n ? 0 : islot + 1;
-    };
-    for (int i = 0; i < S::n; ++i) issue();
-    uint32_t slot = 0;
-    auto done = [&]() {  // this half-tile has been read by every lane
-      __syncwarp();
-      issue();
-      slot = slot + 1 == S::n ? 0 : slot + 1;
-    };
-    for (uint32_t tick = 0; tick < n; ++tick) {
-      const uint32_t seen = seen_of(s, first + tick * kWarps);
-      float sc[NT][4];
-      cp_wait<S::n - 1>();
-      __syncwarp();
-      if (seen) scores(slot, sc);
-      done();
-      cp_wait<S::n - 1>();
-      __syncwarp();
-      if (seen) accumulate(slot, sc, seen);
-      done();
+      const int c = h + S::n;  // the half-tile to copy
+      if (c >= 0) {
+        if (c < halves) load(s, ahead, c & 1, slot);
+        cp_commit();
+        slot = slot + 1 == S::n ? 0 : slot + 1;
+      }
+      if (c & 1) ahead = next;
+      else next = tile(s, first + ((c >> 1) + 1) * kWarps);
     }
     cp_wait<0>();
   }
-  // How many tokens of a tile the row sees.
+  // How many tokens from a tile's first on the last row sees, up to 32.
   __device__ uint32_t seen_of(const Segment& s, uint32_t t) const {
     uint64_t token = (uint64_t)t * 16;
     if (a.blocks) {
@@ -509,11 +633,11 @@ struct Attention {
       if (b < 0) return 0;
       token = ((uint64_t)(uint32_t)b << a.blk_shift) + (t & ((1u << per) - 1u)) * 16;
     }
-    return token > s.pos ? 0u : (uint32_t)min((uint64_t)16, s.pos - token + 1);
+    return token > s.pos ? 0u : (uint32_t)min((uint64_t)32, s.pos - token + 1);
   }
 
-  // ---- the warps' outputs added up: sum [group][D + 4] at sm, M and L at ml[kWarps]
-  __device__ void join_warps() {
+  // ---- the warps' outputs added up: sum [cols][D + 4] at sm, M and L at ml[kWarps]
+  __device__ void join_warps(uint32_t cols, uint32_t warps) {
     float* ml = reinterpret_cast<float*>(sm + M::ml);
     float* red = reinterpret_cast<float*>(sm);
     const uint32_t r = lane >> 2, c = lane & 3;
@@ -536,10 +660,10 @@ struct Attention {
       for (int j = 0; j < 2; ++j) {
         const uint32_t h = 8 * nt + 2 * c + j;
         float mx = -INFINITY;
-        for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * 32 + h]);
+        for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * 32 + h]);
         const float f = rescale(m[nt][j], mx);
-        if (h < group) {
-          float* to = red + (warp * group + h) * (D + 4);
+        if (h < cols && warp < warps) {
+          float* to = red + (warp * cols + h) * (D + 4);
 #pragma unroll
           for (int d = 0; d < D / 16; ++d) {
             const uint32_t d0 = 16 * d + (T8 ? 2 * r : r), d1 = 16 * d + (T8 ? 2 * r + 1 : r + 8);
@@ -551,17 +675,18 @@ struct Attention {
     if (threadIdx.x < 8 * NT) {
       const uint32_t h = threadIdx.x;
       float mx = -INFINITY, sum = 0.f;
-      for (int w = 0; w < kWarps; ++w) mx = fmaxf(mx, ml[w * 32 + h]);
-      for (int w = 0; w < kWarps; ++w) sum += ml[w * 32 + 16 + h] * rescale(ml[w * 32 + h], mx);
+      for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * 32 + h]);
+      for (uint32_t w = 0; w < warps; ++w) sum += ml[w * 32 + 16 + h] * rescale(ml[w * 32 + h], mx);
       ml[kWarps * 32 + h] = mx;
       ml[kWarps * 32 + 16 + h] = sum;
     }
     __syncthreads();
-    for (uint32_t i = threadIdx.x; i < group * (D / 4); i += kAttnThreads) {
+    for (uint32_t i = threadIdx.x; i < cols * (D / 4); i += kAttnThreads) {
       float* at = red + (i / (D / 4)) * (D + 4) + 4 * (i % (D / 4));
       float4 x = *reinterpret_cast<float4*>(at);
-      for (int w = 1; w < kWarps; ++w) {
-        const float4 y = *reinterpret_cast<const float4*>(at + w * group * (D + 4));
+#pragma unroll 4
+      for (uint32_t w = 1; w < warps; ++w) {
+        const float4 y = *reinterpret_cast<const float4*>(at + w * cols * (D + 4));
         x.x += y.x;
         x.y += y.y;
         x.z += y.z;
@@ -572,112 +697,142 @@ struct Attention {
     __syncthreads();
   }
 
-  // ---- sum [group][D + 4] over L: rotated back, gated, rounded, stored
-  __device__ void store(const Segment& s) {
+  // ---- sum [cols][D + 4] over L: rotated back, gated, rounded, stored. A thread has kOut pieces of eight dims;
+  // their gates are fetched ahead.
+  static constexpr int kOut = (8 * NT * (D / 8) + kAttnThreads - 1) / kAttnThreads;
+  struct Gates {
+    uint4 u[kOut];
+  };
+  __device__ __forceinline__ size_t head_of(const Segment& s, uint32_t col) const {
+    return (size_t)(s.row + col / group) * a.H + s.g * group + col % group;
+  }
+  __device__ Gates fetch_gates(const Segment& s) const {
+    Gates z;
+#pragma unroll
+    for (int k = 0; k < kOut; ++k) {
+      const uint32_t i = threadIdx.x + k * kAttnThreads, h = i / (D / 8), c = i % (D / 8);
+      z.u[k] = make_uint4(0u, 0u, 0u, 0u);
+      if (a.gate && h < group * s.rows)
+        z.u[k] = *reinterpret_cast<const uint4*>(a.gate + head_of(s, h) * a.gate_stride + 8 * c);
+    }
+    return z;
+  }
+  __device__ void store(const Segment& s, const Gates& gates) {
     const float* red = reinterpret_cast<const float*>(sm);
     const float* L = reinterpret_cast<const float*>(sm + M::ml) + kWarps * 32 + 16;
     constexpr int LPR = D / 8;
-    for (uint32_t i = threadIdx.x; i < 8 * NT * LPR; i += kAttnThreads) {
-      const uint32_t h = i / LPR, c = i % LPR;
+#pragma unroll
+    for (int k = 0; k < kOut; ++k) {
+      const uint32_t i = threadIdx.x + k * kAttnThreads, h = i / LPR, c = i % LPR;
+      if (i >= 8 * NT * LPR) break;  // whole warps
       float x[8] = {};
-      if (h < group) {
+      if (h < group * s.rows) {
         const float inv = L[h] == 0.f ? 0.f : 1.0f / L[h];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = red[h * (D + 4) + 8 * c + e] * inv;
       }
       if constexpr (T8) wht8<LPR>(x, lane);
-      if (h < group) {
-        const size_t hh = (size_t)s.row * a.H + s.g * group + h;
+      if (h < group * s.rows) {
         if (a.gate) {
           float z[8];
-          unpack8(*reinterpret_cast<const uint4*>(a.gate + hh * a.gate_stride + 8 * c), z);
+          unpack8(gates.u[k], z);
 #pragma unroll
           for (int e = 0; e < 8; ++e) x[e] *= sigmoidf_(z[e]);
         }
-        *reinterpret_cast<uint4*>(a.out + hh * D + 8 * c) = pack8(x);
+        *reinterpret_cast<uint4*>(a.out + head_of(s, h) * D + 8 * c) = pack8(x);
       }
     }
-    __syncthreads();
   }
 
   // ---- a split item's part of this CTA (slot 0: the item began in an earlier CTA)
   __device__ float* part(uint32_t cta, uint32_t slot) const {
-    return a.parts + ((size_t)cta * 2 + slot) * (group * (D + 4));
+    return a.parts + ((size_t)cta * 2 + slot) * (group * pack * (D + 4));
   }
-  // Part: group rows of D sums, M, L and two words of padding.
-  __device__ void store_part(uint32_t slot) {
+  // Part: for each column D sums, M, L and two words of padding.
+  __device__ void store_part(uint32_t slot, uint32_t cols) {
     const float* red = reinterpret_cast<const float*>(sm);
     const float* ml = reinterpret_cast<const float*>(sm + M::ml) + kWarps * 32;
     float* to = part(blockIdx.x, slot);
-    for (uint32_t i = threadIdx.x; i < group * (D / 4); i += kAttnThreads) {
+    for (uint32_t i = threadIdx.x; i < cols * (D / 4); i += kAttnThreads) {
       const uint32_t at = (i / (D / 4)) * (D + 4) + 4 * (i % (D / 4));
       __stcg(reinterpret_cast<float4*>(to + at), *reinterpret_cast<const float4*>(red + at));
     }
-    if (threadIdx.x < group)
+    if (threadIdx.x < cols)
       __stcg(reinterpret_cast<float4*>(to + threadIdx.x * (D + 4) + D),
              make_float4(ml[threadIdx.x], ml[16 + threadIdx.x], 0.f, 0.f));
   }
-  // The parts of CTAs c0 .. c1 added up, as join_warps leaves its sums: a thread has four dims of a head and,
+  // The parts of CTAs c0 .. c1 added up, as join_warps leaves its sums: a thread has four dims of a column and,
   // where there are fewer such columns than threads, every subs-th part. The order is fixed by c0 and c1.
-  __device__ void join_parts(uint32_t c0, uint32_t c1) {
-    float* red = reinterpret_cast<float*>(sm);  // [subs][group][D + 4]
+  __device__ void join_parts(uint32_t c0, uint32_t c1, uint32_t ncol) {
+    float* red = reinterpret_cast<float*>(sm);  // [subs][ncol][D + 4]
     float* ml = reinterpret_cast<float*>(sm + M::ml) + kWarps * 32;
-    float* wt = reinterpret_cast<float*>(sm + M::weights);  // [group][parts]
-    const uint32_t n = c1 - c0 + 1;
-    for (uint32_t h = warp; h < group; h += kWarps) {
-      float mx = -INFINITY, sum = 0.f;
-      constexpr int U = (kMaxCtas + 31) / 32;
-      float2 x[U];
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const uint32_t c = c0 + lane + 32 * i;
-        x[i] = make_float2(-INFINITY, 0.f);
-        if (c <= c1) x[i] = __ldcg(reinterpret_cast<const float2*>(part(c, c == c0) + h * (D + 4) + D));
-      }
-#pragma unroll
-      for (int i = 0; i < U; ++i) mx = fmaxf(mx, x[i].x);
-      mx = warp_max(mx);
-#pragma unroll
-      for (int i = 0; i < U; ++i) {
-        const uint32_t c = lane + 32 * i;
-        const float f = rescale(x[i].x, mx);
-        if (c < n) wt[h * n + c] = f;
-        sum += x[i].y * f;
-      }
-      sum = warp_sum(sum);
-      if (lane == 0) {
-        ml[h] = mx;
-        ml[16 + h] = sum;
-      }
-    }
-    __syncthreads();
-    const uint32_t cols = group * (D / 4), subs = max(1u, kAttnThreads / cols);
-    for (uint32_t i = threadIdx.x; i < cols * subs; i += kAttnThreads) {
-      const uint32_t sub = i / cols, col = i % cols, h = col / (D / 4), at = h * (D + 4) + 4 * (col % (D / 4));
-      const float* w = wt + h * n;
+    float* wt = reinterpret_cast<float*>(sm + M::weights);  // [ncol][parts]
+    const uint32_t n = c1 - c0 + 1, cols = ncol * (D / 4), subs = max(1u, kAttnThreads / cols);
+    constexpr int B = 16;  // parts of a thread in flight
+    const size_t step = 2 * (size_t)(group * pack * (D + 4));
+    // every thread takes the same rounds (the first has a barrier in it): columns of a stride of the threads, B parts each
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (uint32_t i0 = 0, k0 = 0; i0 < cols * subs;) {
+      const uint32_t i = i0 + threadIdx.x, sub = i / cols, col = i % cols, h = col / (D / 4);
+      const uint32_t at = h * (D + 4) + 4 * (col % (D / 4));
+      const bool mine = i < cols * subs;
       const float* p0 = part(c0, 1) + at;  // CTA c0's part, then slot 0 of each CTA
       const float* p = part(c0, 0) + at;
-      const size_t step = 2 * (size_t)(group * (D + 4));
-      float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-      for (uint32_t k0 = sub; k0 < n; k0 += 16 * subs) {
-        float4 y[16];
+      float4 y[B];
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const uint32_t c = k0 + k * subs;
-          y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (c < n) y[k] = __ldcg(reinterpret_cast<const float4*>(c ? p + c * step : p0));
+      for (int k = 0; k < B; ++k) {
+        const uint32_t c = k0 + sub + k * subs;
+        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (mine && c < n) y[k] = __ldcg(reinterpret_cast<const float4*>(c ? p + c * step : p0));
+      }
+      if (i0 == 0 && k0 == 0) {  // the weights, their loads in the same wait as the first parts'
+        for (uint32_t hh = warp; hh < ncol; hh += kWarps) {
+          float mx = -INFINITY, sum = 0.f;
+          constexpr int U = (kMaxCtas + 31) / 32;
+          float2 z[U];
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint32_t c = c0 + lane + 32 * u;
+            z[u] = make_float2(-INFINITY, 0.f);
+            if (c <= c1) z[u] = __ldcg(reinterpret_cast<const float2*>(part(c, c == c0) + hh * (D + 4) + D));
+          }
+#pragma unroll
+          for (int u = 0; u < U; ++u) mx = fmaxf(mx, z[u].x);
+          mx = warp_max(mx);
+#pragma unroll
+          for (int u = 0; u < U; ++u) {
+            const uint32_t c = lane + 32 * u;
+            const float f = rescale(z[u].x, mx);
+            if (c < n) wt[hh * n + c] = f;
+            sum += z[u].y * f;
+          }
+          sum = warp_sum(sum);
+          if (lane == 0) {
+            ml[hh] = mx;
+            ml[16 + hh] = sum;
+          }
         }
+        __syncthreads();
+      }
+      if (mine) {
 #pragma unroll
-        for (int k = 0; k < 16; ++k) {
-          const uint32_t c = k0 + k * subs;
-          const float f = c < n ? w[c] : 0.f;
+        for (int k = 0; k < B; ++k) {
+          const uint32_t c = k0 + sub + k * subs;
+          const float f = c < n ? wt[h * n + c] : 0.f;
           x.x = fmaf(y[k].x, f, x.x);
           x.y = fmaf(y[k].y, f, x.y);
           x.z = fmaf(y[k].z, f, x.z);
           x.w = fmaf(y[k].w, f, x.w);
         }
       }
-      *reinterpret_cast<float4*>(red + sub * group * (D + 4) + at) = x;
+      k0 += B * subs;
+      if (k0 >= n) {
+        if (mine) *reinterpret_cast<float4*>(red + sub * ncol * (D + 4) + at) = x;
+        x = make_float4(0.f, 0.f, 0.f, 0.f);
+        k0 = 0;
+        i0 += kAttnThreads;
+      }
     }
     __syncthreads();
     if (subs > 1) {
@@ -685,7 +840,7 @@ struct Attention {
         float* at = red + (col / (D / 4)) * (D + 4) + 4 * (col % (D / 4));
         float4 x = *reinterpret_cast<float4*>(at);
         for (uint32_t s = 1; s < subs; ++s) {
-          const float4 y = *reinterpret_cast<const float4*>(at + s * group * (D + 4));
+          const float4 y = *reinterpret_cast<const float4*>(at + s * ncol * (D + 4));
           x.x += y.x;
           x.y += y.y;
           x.z += y.z;
@@ -698,49 +853,105 @@ struct Attention {
   }
 };
 
-// Tiles of a row: of its tokens, or of its listed blocks; 0 for a row that is skipped.
-__device__ __forceinline__ uint32_t row_tiles(const Attend& a, uint32_t r, bool report) {
-  uint32_t seq, pos;
-  const RowKind kind = locate(a.r, a.c.capacity, r, seq, pos);
+// The tiles of the item that begins with row r, of its tokens or of its listed blocks, with the item's rows
+// and last position; 0 for a row that is skipped or inside an item.
+__device__ __forceinline__ uint32_t row_tiles(const Attend& a, const Rows& at, uint32_t pack, uint32_t r, bool report,
+                                              uint32_t& seq, uint32_t& rows, uint32_t& last) {
+  uint32_t pos, index, left;
+  const RowKind kind = locate(at, a.c.capacity, r, seq, pos, index, left);
   if (kind == kRowBad && report) set_status(a.status, kStatusRange);
-  if (kind != kRowOk) return 0;
-  return a.blocks ? a.n_blocks << (a.blk_shift - 4) : pos / 16 + 1;
+  if (kind != kRowOk || index % pack != 0) return 0;
+  rows = min(min(pack, left), a.c.capacity - pos);
+  last = pos + rows - 1;
+  return a.blocks ? a.n_blocks << (a.blk_shift - 4) : last / 16 + 1;
 }
 
 template <int D, int NT, bool T8>
-__global__ void __launch_bounds__(kAttnThreads, kCtasPerSm) attend_kernel(const __grid_constant__ Attend a) {
+__global__ void __launch_bounds__(32 * warps_of<D, NT, T8>(), 1) attend_kernel(const __grid_constant__ Attend a) {
   extern __shared__ __align__(128) uint8_t sm[];
   using A = Attention<D, NT, T8>;
   using M = Smem<D, NT, T8>;
+  constexpr uint32_t kWarps = M::kWarps, kAttnThreads = 32 * kWarps;
   uint32_t* first = reinterpret_cast<uint32_t*>(sm + M::first);  // [n_rows + 1]: tiles before a row (of one head)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + M::misc);
-  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  // the line of all items: prefix sums of the rows' tiles
-  uint32_t base = 0;
-  for (uint32_t r0 = 0; r0 < a.r.n_rows; r0 += kAttnThreads) {
-    const uint32_t r = r0 + tid;
-    const uint32_t v = r < a.r.n_rows ? row_tiles(a, r, blockIdx.x == 0) : 0;
-    uint32_t x = v;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= (uint32_t)o) x += y;
-    }
-    if (lane == 31) misc[warp] = x;
-    __syncthreads();
-    uint32_t before = base;
-    for (uint32_t w = 0; w < warp; ++w) before += misc[w];
-    if (r < a.r.n_rows) first[r] = before + x - v;
-    for (uint32_t w = 0; w < (uint32_t)kWarps; ++w) base += misc[w];
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.H / a.c.Hkv;
+  const uint32_t pack = a.blocks || group > 8 ? 1 : 8 / group;
+  // where the rows are, in shared memory (the ring is empty): one round trip for all searches
+  Rows rows_here = a.r;
+  {
+    int32_t* pos = reinterpret_cast<int32_t*>(sm);
+    int32_t* start = pos + kMaxSeqs;
+    for (uint32_t i = tid; i < a.r.n_seqs; i += kAttnThreads) pos[i] = a.r.pos[i];
+    if (a.r.row_start)
+      for (uint32_t i = tid; i <= a.r.n_seqs; i += kAttnThreads) start[i] = a.r.row_start[i];
+    rows_here.pos = pos;
+    if (a.r.row_start) rows_here.row_start = start;
     __syncthreads();
   }
-  if (tid == 0) first[a.r.n_rows] = base;
-  __syncthreads();
-  const uint32_t total = base * a.c.Hkv;
-  if (total == 0) return;
-  // an equal stretch for every CTA, whole rounds of the warps
-  uint32_t per = (total + gridDim.x - 1) / gridDim.x;
-  per = (per + kWarps - 1) / kWarps * kWarps;
+  // the line of all items: prefix sums of the rows' tiles with kLead before each item's, or (whole) of ones.
+  // kLead stands for what an item's beginning and end cost a CTA that has another item too: about two
+  // rounds of its warps (32 sequences of 1K-16K: ... us, without it ...).
+  constexpr uint32_t kLead = 2 * kWarps;
+  uint32_t most = 0, items = 0;
+  uint32_t total = 0, per = 0;
+  bool whole = false;
+#pragma unroll 1
+  for (int pass = 0; pass < 2; ++pass) {
+    uint32_t base = 0;
+    for (uint32_t r0 = 0; r0 < a.r.n_rows; r0 += kAttnThreads) {
+      const uint32_t r = r0 + tid;
+      uint32_t seq, rows, last, v = 0;
+      if (r < a.r.n_rows) v = row_tiles(a, rows_here, pack, r, blockIdx.x == 0, seq, rows, last);
+      most = max(most, v);
+      items += v > 0;
+      v = whole ? v > 0 : v ? v + kLead : 0;
+      uint32_t x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= (uint32_t)o) x += y;
+      }
+      if (lane == 31) misc[warp] = x;
+      __syncthreads();
+      uint32_t before = base;
+#pragma unroll
+      for (uint32_t w = 0; w < kWarps; ++w) {
+        before += w < warp ? misc[w] : 0;
+        base += misc[w];
+      }
+      if (r < a.r.n_rows) first[r] = before + x - v;
+      if (r == a.r.n_rows - 1) first[r + 1] = before + x;
+      __syncthreads();
+    }
+    total = base * a.c.Hkv;
+    if (total == 0) return;
+    if (whole) {
+      per = 1;
+      break;
+    }
+    // An equal stretch for every CTA, whole rounds of the warps. Few items of up to kShort rounds go to a CTA
+    // each instead: a split's hand-over and join take longer (4 us).
+    constexpr uint32_t kShort = 2, kLeast = 2;
+    most = __reduce_max_sync(0xffffffffu, most);
+    items = __reduce_add_sync(0xffffffffu, items);
+    if (lane == 0) {
+      misc[warp] = most;
+      misc[40 + warp] = items;
+    }
+    __syncthreads();
+    most = items = 0;
+#pragma unroll
+    for (uint32_t w = 0; w < kWarps; ++w) {
+      most = max(most, misc[w]);
+      items += misc[40 + w];
+    }
+    __syncthreads();
+    whole = items * a.c.Hkv <= gridDim.x && most <= kShort * kWarps;
+    per = max((total + gridDim.x - 1) / gridDim.x, kLeast);
+    if (per > kWarps / 2) per = (per + kWarps - 1) / kWarps * kWarps;
+    if (!whole) break;
+  }
+  __syncthreads();  // the ring is free
   const uint64_t w64 = (uint64_t)blockIdx.x * per;
   if (w64 >= total) return;
   const uint32_t w0 = (uint32_t)w64, w1 = min(total, w0 + per);
@@ -754,58 +965,69 @@ __global__ void __launch_bounds__(kAttnThreads, kCtasPerSm) attend_kernel(const 
     }
     row = lo;
   }
-  A at{a, sm, warp, lane, a.H / a.c.Hkv};
-  at.ring = smem_addr(sm) + warp * Slot<D, T8>::n * Slot<D, T8>::bytes;
+  A at{a, sm, warp, lane, group, pack};
+  at.ring = smem_addr(sm) + warp * A::S::n * A::S::bytes;
   for (uint32_t w = w0; w < w1;) {
     Segment s;
     while (first[row + 1] * a.c.Hkv <= w) ++row;
     s.row = row;
-    s.tiles = first[row + 1] - first[row];
-    const uint32_t in_row = w - first[row] * a.c.Hkv;
-    s.g = in_row / s.tiles;
-    s.t0 = in_row % s.tiles;
-    s.t1 = min(s.tiles, s.t0 + (w1 - w));
-    locate(a.r, a.c.capacity, row, s.seq, s.pos);
-    at.load_q(s);
-    at.walk(s);
-    at.join_warps();
-    const uint32_t i0 = w - s.t0, i1 = i0 + s.tiles;  // the item on the line
-    const uint32_t c0 = i0 / per, c1 = (i1 - 1) / per;
-    if (c0 == c1) {
-      at.store(s);
+    s.tiles = row_tiles(a, a.r, pack, row, false, s.seq, s.rows, s.pos);
+    s.row0 = (size_t)s.seq * a.c.capacity;
+    s.tab = a.c.btab ? a.c.btab + (size_t)s.seq * (a.c.capacity >> a.c.bt_shift) : nullptr;
+    const uint32_t in_row = w - first[row] * a.c.Hkv, length = s.tiles + kLead;
+    uint32_t c0 = 0, c1 = 0, used = 1;  // the CTAs the item's tiles lie in, the line this CTA has of it
+    s.t0 = 0;
+    s.t1 = s.tiles;
+    if (whole) {
+      s.g = in_row;
     } else {
-      at.store_part(blockIdx.x == c0 ? 1 : 0);
-      __threadfence();
+      s.g = in_row / length;
+      const uint32_t at0 = in_row % length;
+      used = min(length - at0, w1 - w);
+      s.t0 = max(at0, kLead) - kLead;
+      s.t1 = max(at0 + used, kLead) - kLead;
+      c0 = (w - at0 + kLead) / per;
+      c1 = (w - at0 + length - 1) / per;
+    }
+    if (s.t0 == s.t1) {
+      w += used;
+      continue;
+    }
+    const typename A::QRegs q = at.fetch_q(s);
+    at.walk(s, q);
+    const uint32_t cols = group * s.rows;
+    const typename A::Gates gates = at.fetch_gates(s);
+    at.join_warps(cols, min(kWarps, s.t1 - s.t0));
+    bool finish = true;
+    if (c0 != c1) {
+      at.store_part(blockIdx.x == c0 ? 1 : 0, cols);
       __syncthreads();
       if (tid == 0) {
-        // one item at most begins in CTA c0 and goes on behind it: its counter
-        const uint32_t had = atomicAdd(a.tickets + c0, 1u);
-        misc[7] = had == c1 - c0;
+        // One item at most begins in CTA c0 and goes on behind it: its counter. The barrier has put the CTA's part
+        // before this, and the count's release and acquire put it before the last one's reads.
+        const uint32_t had = count_up(a.tickets + c0);
+        misc[16] = had == c1 - c0;
         if (had > c1 - c0) set_status(a.status, kStatusInvalid);
         if (had == c1 - c0) a.tickets[c0] = 0;
-        __threadfence();
       }
       __syncthreads();
-      if (misc[7]) {
-        at.join_parts(c0, c1);
-        at.store(s);
-      }
+      finish = misc[16] != 0;
+      if (finish) at.join_parts(c0, c1, cols);
     }
+    if (finish) at.store(s, gates);
     __syncthreads();
-    w += s.t1 - s.t0;
+    w += used;
   }
 }
 
 template <int D, int NT, bool T8>
 cudaError_t launch(const Attend& a, cudaStream_t st) {
+  constexpr uint32_t W = warps_of<D, NT, T8>();
   const uint32_t bytes = Smem<D, NT, T8>::first + (a.r.n_rows + 1) * 4;
-  cudaError_t e =
-      cudaFuncSetAttribute(attend_kernel<D, NT, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-  if (e != cudaSuccess) return e;
   const uint64_t most = (uint64_t)a.r.n_rows * a.c.Hkv *
                         (a.blocks ? (uint64_t)a.n_blocks << (a.blk_shift - 4) : (a.c.capacity + 15) / 16);
-  const uint32_t grid = (uint32_t)std::min<uint64_t>(std::min(a.sms * kCtasPerSm, kMaxCtas), (most + kWarps - 1) / kWarps);
-  attend_kernel<D, NT, T8><<<grid, kAttnThreads, bytes, st>>>(a);
+  const uint32_t grid = (uint32_t)std::min<uint64_t>(std::min(a.sms, kMaxCtas), most);
+  attend_kernel<D, NT, T8><<<grid, 32 * W, bytes, st>>>(a);
   return cudaGetLastError();
 }
 template <int D>
@@ -814,7 +1036,23 @@ cudaError_t launch_for(const Attend& a, cudaStream_t st) {
   return a.c.ks ? launch<D, 2, true>(a, st) : launch<D, 2, false>(a, st);
 }
 
+template <int D, int NT, bool T8>
+bool allow() {
+  constexpr int bytes = Smem<D, NT, T8>::first + (kMaxQueries + 1) * 4;
+  static_assert(bytes <= 227 * 1024, "shared memory of a CTA");
+  return cudaFuncSetAttribute(attend_kernel<D, NT, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) ==
+         cudaSuccess;
+}
+template <int D>
+bool allow_dim() {
+  return allow<D, 1, false>() && allow<D, 1, true>() && allow<D, 2, false>() && allow<D, 2, true>();
+}
+
 }  // namespace
+
+cudaError_t attend_attributes() {
+  return allow_dim<64>() && allow_dim<128>() && allow_dim<256>() ? cudaSuccess : cudaGetLastError();
+}
 
 cudaError_t attend(const Attend& a, cudaStream_t st) {
   switch (a.c.D) {

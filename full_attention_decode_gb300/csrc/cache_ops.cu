@@ -77,14 +77,15 @@ __device__ __forceinline__ void append_turbo8(const Append& a, uint32_t block) {
   }
 }
 
-// The key bounds, one CTA per (span of rows, kv-head). A run is the call's rows of one block
-// of one sequence; the CTA that has its first row folds it, starting anew if that is
-// the block's first token. Warps (in teams of D / 8 lanes) take the run's rows in turn.
-template <int D>
+// The key bounds of spans of rows. A run is the call's rows of one block of one sequence; who has the span with
+// its first row folds it, starting anew if that is the block's first token. WIDE: a CTA a (span, kv-head), its
+// teams of D / 8 lanes taking a run's rows in turn; otherwise (blocks of up to 64 tokens) a team alone,
+// sixteen rows in flight: at 32768 rows of 4 heads and blocks of 16, a CTA for each would only wait.
+template <int D, bool WIDE>
 __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, uint32_t g, uint32_t span_rows) {
-  constexpr int LPR = D / 8, TEAMS = kThreads / LPR;
-  __shared__ float part[2][TEAMS][D];
-  const uint32_t l = threadIdx.x % LPR, team = threadIdx.x / LPR, S = 1u << a.blk_shift;
+  constexpr int LPR = D / 8, TEAMS = WIDE ? kThreads / LPR : 1;
+  __shared__ float part[2][WIDE ? TEAMS : 1][WIDE ? D : 1];
+  const uint32_t l = threadIdx.x % LPR, team = WIDE ? threadIdx.x / LPR : 0, S = 1u << a.blk_shift;
   const uint32_t end = min(a.r.n_rows, (span + 1) * span_rows);
   for (uint32_t r = span * span_rows; r < end;) {
     uint32_t seq, pos;
@@ -104,14 +105,19 @@ __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, ui
       r = stop;
       continue;
     }
+    uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D;
     float lo[8], hi[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       lo[e] = INFINITY;
       hi[e] = -INFINITY;
     }
+    if (!fresh && team == 0) {
+      unpack8(*reinterpret_cast<const uint4*>(b + 8 * l), lo);
+      unpack8(*reinterpret_cast<const uint4*>(b + D + 8 * l), hi);
+    }
     const uint16_t* src = a.k + (size_t)g * D + 8 * l;
-#pragma unroll 4
+#pragma unroll WIDE ? 4 : 16
     for (uint32_t i = r + team; i < stop; i += TEAMS) {
       float x[8];
       unpack8(*reinterpret_cast<const uint4*>(src + (size_t)i * a.c.Hkv * D), x);
@@ -121,22 +127,26 @@ __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, ui
         hi[e] = fmaxf(hi[e], x[e]);
       }
     }
-    const uint32_t used = min(stop - r, (uint32_t)TEAMS);
-    if (team < used)
+    if constexpr (WIDE) {
+      const uint32_t used = min(stop - r, (uint32_t)TEAMS);
+      if (team < used)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        part[0][team][8 * l + e] = lo[e];
-        part[1][team][8 * l + e] = hi[e];
+        for (int e = 0; e < 8; ++e) {
+          part[0][team][8 * l + e] = lo[e];
+          part[1][team][8 * l + e] = hi[e];
+        }
+      __syncthreads();
+      for (uint32_t i = threadIdx.x; i < 2 * D; i += kThreads) {
+        const uint32_t p = i / D, d = i % D;
+        float x = part[p][0][d];
+        for (uint32_t t = 1; t < used; ++t) x = p ? fmaxf(x, part[1][t][d]) : fminf(x, part[0][t][d]);
+        b[i] = to_bf16(x);
       }
-    __syncthreads();
-    uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D;
-    for (uint32_t i = threadIdx.x; i < 2 * D; i += kThreads) {
-      const uint32_t p = i / D, d = i % D;
-      float x = fresh ? (p ? -INFINITY : INFINITY) : bf16f(b[i]);
-      for (uint32_t t = 0; t < used; ++t) x = p ? fmaxf(x, part[1][t][d]) : fminf(x, part[0][t][d]);
-      b[i] = to_bf16(x);
+      __syncthreads();
+    } else {
+      *reinterpret_cast<uint4*>(b + 8 * l) = pack8(lo);
+      *reinterpret_cast<uint4*>(b + D + 8 * l) = pack8(hi);
     }
-    __syncthreads();
     r = stop;
   }
 }
@@ -150,7 +160,12 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     else append_plain<D>(a, blockIdx.x);
   } else {
     const uint32_t i = blockIdx.x - row_ctas;
-    append_bounds<D>(a, i / a.c.Hkv, i % a.c.Hkv, span_rows);
+    if (a.blk_shift > 6) {
+      append_bounds<D, true>(a, i / a.c.Hkv, i % a.c.Hkv, span_rows);
+    } else {
+      const uint32_t team = i * (kThreads / (D / 8)) + threadIdx.x / (D / 8);
+      append_bounds<D, false>(a, team / a.c.Hkv, team % a.c.Hkv, span_rows);
+    }
   }
 }
 
@@ -282,16 +297,17 @@ __device__ float score_blocks(const Select& a, uint32_t r, uint32_t g, uint32_t 
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const uint32_t j = jb + u * PER + team;
-      float lo[8], hi[8], s = 0.f;
+      float lo[8], hi[8], c[4] = {0.f, 0.f, 0.f, 0.f};  // four short chains: less rounding, no waiting
       unpack8(lo4[u], lo);
       unpack8(hi4[u], hi);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        s = fmaf(up[e], hi[e], s);
-        s = fmaf(dn[e], lo[e], s);
+        c[e & 1] = fmaf(up[e], hi[e], c[e & 1]);
+        c[2 + (e & 1)] = fmaf(dn[e], lo[e], c[2 + (e & 1)]);
         mh[e] = fmaxf(mh[e], fabsf(hi[e]));
         ml[e] = fmaxf(ml[e], fabsf(lo[e]));
       }
+      float s = (c[0] + c[1]) + (c[2] + c[3]);
 #pragma unroll
       for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
       if (here[u]) wild |= !(fabsf(s) < INFINITY);
@@ -379,8 +395,8 @@ __device__ __forceinline__ uint32_t cta_sum(uint32_t x, uint32_t* tmp, uint32_t&
 }
 
 // Which blocks the exact scores choose, given 32-bit ones. Every s_j is within E of the exact t_j
-// (E = 48 2^-24 most: at most 15 additions in Q+-, 16 multiply-adds and 5 additions
-// round). The K-th largest t is then within E of the K-th largest s, T: s_j > T + 2E is in, s_j < T - 2E is
+// (E = (group + 13) 2^-24 most: group - 1 additions in Q+-, 4 multiply-adds and 2 + 5 additions round
+// one after the other, and the rounding of `most` itself is covered by the rest). The K-th largest t is then within E of the K-th largest s, T: s_j > T + 2E is in, s_j < T - 2E is
 // out, and only what lies between is scored again in 64 bits. T by bisection of the
 // scores' bits: a count over the CTA a step, until a step leaves exactly K.
 template <int D>
@@ -418,7 +434,7 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
   __syncthreads();
   for (uint32_t w = 0; w < kSelWarps; ++w) kth = min(kth, tmp[w]);
   __syncthreads();
-  const float T = key_value(kth), E = 48.f * 5.9604645e-8f * most;
+  const float T = key_value(kth), E = (float)(a.H / a.c.Hkv + 13) * 0x1p-24f * most;
   uint32_t klo = 1, khi = 0xffffffffu;  // keys above khi are in, below klo out
   if (E < INFINITY) {
     klo = order_key(isinf(T) ? T : __fadd_rd(T, -2.f * E));
@@ -584,7 +600,8 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
     __syncthreads();
     if (!s_last) return;
     m = 0.f;
-    for (uint32_t p = 0; p < parts; ++p) m = fmaxf(m, __ldcg(most + p));
+    for (uint32_t p = tid % 32; p < parts; p += 32) m = fmaxf(m, __ldcg(most + p));
+    m = warp_max(m);
   } else {
     __syncthreads();
   }
@@ -605,7 +622,8 @@ cudaError_t append(const Append& a, cudaStream_t st) {
   const bool t8 = a.c.ks != nullptr;
   const uint32_t rows = row_ctas_of(a.r, a.c, t8);
   const uint32_t span = a.r.row_start ? 1u << a.blk_shift : 1u;  // rows of a bounds CTA: about one block's
-  const uint32_t grid = rows + (a.bounds ? (a.r.n_rows + span - 1) / span * a.c.Hkv : 0);
+  const uint32_t folds = (a.r.n_rows + span - 1) / span * a.c.Hkv, teams = a.blk_shift > 6 ? 1 : kThreads / (a.c.D / 8);
+  const uint32_t grid = rows + (a.bounds ? (folds + teams - 1) / teams : 0);
 #define CALL(DD)                                                               \
   if (t8) append_kernel<DD, true><<<grid, kThreads, 0, st>>>(a, rows, span);   \
   else append_kernel<DD, false><<<grid, kThreads, 0, st>>>(a, rows, span)

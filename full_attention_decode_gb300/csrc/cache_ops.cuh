@@ -11,9 +11,13 @@ namespace q35c {
 
 enum RowKind { kRowOk = 0, kRowSkip = 1, kRowBad = 2 };
 
-// Row r's sequence and position; kRowSkip for a row no sequence has.
-__device__ __forceinline__ RowKind locate(const Rows& w, uint32_t capacity, uint32_t r, uint32_t& seq, uint32_t& pos) {
+// Row r's sequence and position, which of the sequence's rows it is and how many are left from
+// it on; kRowSkip for a row no sequence has.
+__device__ __forceinline__ RowKind locate(const Rows& w, uint32_t capacity, uint32_t r, uint32_t& seq, uint32_t& pos,
+                                          uint32_t& index, uint32_t& left) {
   int64_t i = 0;
+  index = 0;
+  left = 1;
   if (!w.row_start) {
     seq = r;
   } else {
@@ -26,11 +30,17 @@ __device__ __forceinline__ RowKind locate(const Rows& w, uint32_t capacity, uint
     }
     seq = lo;
     i = (int64_t)r - w.row_start[lo];
+    index = (uint32_t)i;
+    left = (uint32_t)(min((int64_t)w.row_start[lo + 1], (int64_t)w.n_rows) - r);
   }
   const int64_t p = (int64_t)w.pos[seq] + i;
   if (w.pos[seq] < 0 || i < 0 || p >= (int64_t)capacity) return kRowBad;
   pos = (uint32_t)p;
   return kRowOk;
+}
+__device__ __forceinline__ RowKind locate(const Rows& w, uint32_t capacity, uint32_t r, uint32_t& seq, uint32_t& pos) {
+  uint32_t index, left;
+  return locate(w, capacity, r, seq, pos, index, left);
 }
 
 // The cache row of token t (< capacity) of a sequence; false for a block outside the pool.

@@ -11,7 +11,7 @@ namespace q35c {
 
 constexpr uint32_t kMaxSeqs = 4096;       // sequences of a call
 constexpr uint32_t kMaxRows = 1u << 20;   // rows of an append or a read
-constexpr uint32_t kMaxQueries = 4096;    // rows of a selection or an attention
+constexpr uint32_t kMaxQueries = 2048;    // rows of a selection or an attention
 constexpr uint32_t kMaxGroup = 16;        // q-heads of a kv-head
 
 // The cache arrays of a batch: contiguous rows [n_seqs][capacity][Hkv][D], or pools of
@@ -68,7 +68,7 @@ struct Select {
   int* status;
 };
 cudaError_t select(const Select& a, cudaStream_t st);
-constexpr uint32_t kMaxItems = 32768;  // kMaxQueries rows of 8 kv-heads
+constexpr uint32_t kMaxItems = kMaxQueries * 8;  // of 8 kv-heads
 constexpr uint32_t kMaxParts = 1024;   // parts of all items: at most one an item, or this many
 
 struct Attend {
@@ -79,14 +79,15 @@ struct Attend {
   const int32_t* blocks; // [n_rows][Hkv][n_blocks], or null: every token
   uint16_t* out;         // [n_rows][H][D]
   uint32_t* tickets;     // [kMaxCtas], zero between calls
-  float* parts;          // work [kMaxCtas][2][H / Hkv][D + 4]
+  float* parts;          // work [kMaxCtas][2][columns of an item][D + 4]
   uint32_t sms;          // of the GPU
   uint32_t H, gate_stride, n_blocks, blk_shift;
   int* status;
 };
-constexpr uint32_t kMaxCtas = 320;  // two on each of up to 160 SMs
+constexpr uint32_t kMaxCtas = 160;  // one on each SM of the largest sm_103 part
 // Tiles of 16 tokens that a call's rows and kv-heads may have in all.
 constexpr uint64_t kMaxTiles = 1ull << 31;
 cudaError_t attend(const Attend& a, cudaStream_t st);
+cudaError_t attend_attributes();  // once per device, before the first attend
 
 }  // namespace q35c

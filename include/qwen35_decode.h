@@ -471,7 +471,7 @@ QWEN35_API int qwen35_lm_head_greedy(const qwen35_config* cfg, const qwen35_bf16
  * [0, num_blocks), sets QWEN35_ERR_DEVICE_RANGE in the status word; nothing outside
  * the cache is touched, the row is skipped, or computed without that block.
  * num_blocks: the pool's size (paged only). At most 4096 sequences; at most 2^20 rows
- * for append and read, 4096 for selection and attention. Sequences of one call may
+ * for append and read, 2048 for selection and attention. Sequences of one call may
  * share blocks that the call does not write. */
 typedef struct qwen35_cache_rows {
     const int32_t* row_start;

@@ -89,7 +89,7 @@ def test_bad_rows(rows):
 
 @no_device
 def test_row_limits():
-    many = _rows(n_seqs=3, n_rows=4097, row_start=0x7100000)
+    many = _rows(n_seqs=3, n_rows=2049, row_start=0x7100000)
     assert _calls(_cfg(), _kv(), many) == [OK_BUT_NO_DEVICE] * 2 + [UNSUPPORTED] * 2
     many = _rows(n_seqs=3, n_rows=(1 << 20) + 1, row_start=0x7100000)
     assert _calls(_cfg(), _kv(), many) == [UNSUPPORTED] * 4

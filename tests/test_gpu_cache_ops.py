@@ -387,6 +387,12 @@ ATTENDS = [dict(heads="tiny", fmt=BF16, lens=[1]), dict(heads="tiny", fmt=TURBO8
            dict(heads="odd", fmt=BF16, lens=[90, 200], spread=6.0), dict(heads="odd", fmt=TURBO8, lens=[90, 200]),
            dict(heads="twelve", fmt=BF16, lens=[140, 19]), dict(heads="twelve", fmt=TURBO8, lens=[140, 19]),
            dict(heads="tiny", fmt=BF16, lens=list(range(1, 90)), page=16),
+           # several rows of a sequence: across a tile's end, from the first token on, more than fit an item
+           dict(heads="tiny_alt", fmt=BF16, lens=[17, 16, 33, 18, 9, 140], rows=[5, 16, 8, 3, 9, 20], page=16),
+           dict(heads="tiny_alt", fmt=TURBO8, lens=[17, 16, 33, 18, 9, 140], rows=[5, 16, 8, 3, 9, 20], page=8),
+           dict(heads="odd", fmt=BF16, lens=[65, 34, 2, 50], rows=[3, 4, 2, 1], page=16, lead=3),
+           dict(heads="odd", fmt=TURBO8, lens=[65, 34, 2, 50], rows=[3, 4, 2, 1], lead=3),
+           dict(heads="4b", fmt=TURBO8, lens=[600, 49], rows=[7, 2]), dict(heads="wide", fmt=BF16, lens=[77], rows=[4]),
            dict(heads="tiny", fmt=TURBO8, lens=[40] * 40, page=16, share_first=True)]
 
 
@@ -435,6 +441,26 @@ def test_a_nan_in_a_key_spoils_only_rows_that_see_it(fmt):
         s.t["k"][at, 0, 3] = 0x7F
     got = f64(s.attend())
     assert np.isfinite(got[[0, 1, 4, 5, 6, 7]]).all() and np.isnan(got[[2, 3]]).any(axis=(1, 2)).all()
+
+
+@pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "odd", "eight"])
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_what_later_rows_of_a_call_hold_is_not_seen(fmt, heads):
+    """Rows 0 .. 6 of one sequence; the tokens of rows 3 and 5 hold infinities and NaN in K and V."""
+    s = Setup(heads, fmt, [35, 20], rows=[7, 2])
+    clean = f64(s.attend()).copy()
+    for pos, name in ((31, "v"), (33, "k"), (33, "v")):
+        at = s.at(0, pos)
+        if fmt == BF16:
+            s.t[name][at, :, 3] = float("inf")
+            s.t[name][at, :, 4] = float("nan")
+        else:
+            s.t[name][at, :, 3] = 0x7F
+            s.t[name + "s"][at, 1] = 0x7F80
+    got = f64(s.attend())
+    keep = [0, 1, 2, 7, 8]
+    np.testing.assert_array_equal(got[keep], clean[keep])
+    assert all(np.isnan(got[r]).any() or np.isinf(got[r]).any() for r in (3, 4, 5, 6))
 
 
 def _lists(s, n, seed=3, holes=True):
