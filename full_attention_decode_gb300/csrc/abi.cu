@@ -1271,7 +1271,7 @@ int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_cache* kv, co
   a.exact = reinterpret_cast<double*>(s + need.exact);
   a.most = reinterpret_cast<float*>(s + need.most);
   a.tickets = reinterpret_cast<uint32_t*>(s + kSelTickets);
-  a.ctas = std::min(2u * (uint32_t)num_sms(), q35c::kMaxParts);
+  a.ctas = std::min(4u * (uint32_t)num_sms(), q35c::kMaxParts);
   a.H = cfg->num_heads;
   a.blk_shift = log2_of(bounds->block);
   a.n_select = n_select;

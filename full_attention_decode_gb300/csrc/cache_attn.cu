@@ -142,12 +142,6 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x to 2^-22 relative; 0 bel
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
 __device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.f : ex2(from - to); }
 
-__device__ __forceinline__ uint32_t count_up(uint32_t* p) {
-  uint32_t had;
-  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(had) : "l"(p) : "memory");
-  return had;
-}
-
 // One item's stretch in a CTA: rows row .. row + rows - 1, the last at position pos.
 struct Segment {
   uint32_t row, rows, g, seq, pos;

@@ -54,25 +54,39 @@ __device__ __forceinline__ void append_turbo8(const Append& a, uint32_t block) {
   const bool is_v = team & 8;
   const Item w = find_item(a.r, a.c, item, a.status);
   const uint16_t* src = (is_v ? a.v : a.k) + item * D + 8 * l;
-  float x[D / 4];
+  float2 x[D / 8];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     uint4 u = make_uint4(0u, 0u, 0u, 0u);
     if (w.ok) u = *reinterpret_cast<const uint4*>(src + 32 * i);
-    unpack8(u, x + 8 * i);
+    unpack8(u, reinterpret_cast<float*>(x + 4 * i));
   }
   wht_quad<D>(x, lane);
-#pragma unroll
-  for (int e = 0; e < D / 4; ++e) x[e] = round_bf16(x[e]);
   uint8_t* to = (is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 8 * l;
-  uint16_t* sc = (is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16) + l / 2;
+  uint16_t* sc = (is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16);
+  uint32_t scales[P];  // lane 0: group 2 i's, then 2 i + 1's, which lanes 2 and 3 have
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     uint16_t s;
-    const uint2 codes = quant8(x + 8 * i, s);
-    if (w.ok) {
-      *reinterpret_cast<uint2*>(to + 32 * i) = codes;
-      if (l % 2 == 0) sc[2 * i] = s;
+    uint32_t r[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const __nv_bfloat162 p = __float22bfloat162_rn(x[4 * i + k]);
+      r[k] = *reinterpret_cast<const uint32_t*>(&p);
+    }
+    const uint2 codes = quant8(r, s);
+    if (w.ok) *reinterpret_cast<uint2*>(to + 32 * i) = codes;
+    scales[i] = s;
+  }
+#pragma unroll
+  for (int i = 0; i < P; ++i) scales[i] |= __shfl_xor_sync(0xffffffffu, scales[i], 2) << 16;
+  if (w.ok && l == 0) {
+    if constexpr (P >= 4) {
+#pragma unroll
+      for (int i = 0; i < P; i += 4)
+        reinterpret_cast<uint4*>(sc)[i / 4] = make_uint4(scales[i], scales[i + 1], scales[i + 2], scales[i + 3]);
+    } else {
+      *reinterpret_cast<uint2*>(sc) = make_uint2(scales[0], scales[1]);
     }
   }
 }
@@ -179,23 +193,26 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
     const bool is_v = team & 8;
     const Item w = find_item(a.r, a.c, item, a.status);
     const uint8_t* from = (is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 8 * l;
-    const uint16_t* sc = (is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16) + l / 2;
-    float x[D / 4];
+    const uint16_t* sc = (is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16);
+    float2 x[D / 8];
+    uint2 codes[P];
+    uint32_t s[P];  // the scales of groups 2 i and 2 i + 1
 #pragma unroll
-    for (int i = 0; i < P; ++i) {
-      uint2 codes = make_uint2(0u, 0u);
-      uint16_t s = 0;
-      if (w.ok) {
-        codes = *reinterpret_cast<const uint2*>(from + 32 * i);
-        s = sc[2 * i];
-      }
-      dequant_codes8(codes, bf16f(s), x + 8 * i);
+    for (int i = 0; i < P; ++i) codes[i] = w.ok ? *reinterpret_cast<const uint2*>(from + 32 * i) : make_uint2(0u, 0u);
+#pragma unroll
+    for (int i = 0; i < P; i += 2) {
+      const uint2 u = w.ok ? *reinterpret_cast<const uint2*>(sc + 2 * i) : make_uint2(0u, 0u);
+      s[i] = u.x;
+      s[i + 1] = u.y;
     }
+#pragma unroll
+    for (int i = 0; i < P; ++i) dequant8(codes[i], l < 2 ? bf16lo(s[i]) : bf16hi(s[i]), x + 4 * i);
     wht_quad<D>(x, lane);
     uint16_t* to = (is_v ? a.v : a.k) + item * D + 8 * l;
     if (w.ok)
 #pragma unroll
-      for (int i = 0; i < P; ++i) *reinterpret_cast<uint4*>(to + 32 * i) = pack8(x + 8 * i);
+      for (int i = 0; i < P; ++i)
+        *reinterpret_cast<uint4*>(to + 32 * i) = pack8(reinterpret_cast<const float*>(x + 4 * i));
   } else {
     constexpr int LPR = D / 8;
     const size_t item = (blockIdx.x * (size_t)kThreads + threadIdx.x) / LPR;
@@ -242,6 +259,8 @@ __device__ __forceinline__ bool forced(const Select& a, uint32_t j, uint32_t n) 
 constexpr uint32_t kSelWarps = kThreads / 32;
 constexpr uint32_t kMine = 16;   // scores a thread holds in registers: 4096 blocks a CTA
 constexpr uint32_t kClose = 256;  // blocks scored again side by side
+constexpr int kAhead = 4;         // blocks of a lane in flight
+constexpr uint32_t kInf = 0xff800000u;  // the key of +infinity
 
 // Sums over the group's heads of q's positive and negative parts, eight dims a lane.
 template <int D>
@@ -264,39 +283,48 @@ __device__ __forceinline__ void signed_sums(const Select& a, uint32_t r, uint32_
 
 // Scores of blocks [j0, j1): s_j = sum_d Q+_d hi_jd + Q-_d lo_jd, with Q+ and Q- the sums over the
 // group's heads of q's positive and negative parts: the sum over the heads of the largest q.k that a key
-// inside the bounds could have. LPR lanes a block, four blocks of a lane in flight. Returns (in every
+// inside the bounds could have. LPR lanes a block; the next kAhead blocks of a lane are in flight while
+// the last ones are summed (the bytes of the bounds bound it). Returns (in every
 // thread) sum_d Q+_d max_j|hi_jd| + |Q-_d| max_j|lo_jd|, which bounds every block's sum
 // of absolute terms; infinity where an infinity or NaN leaves no bound.
 template <int D>
-__device__ float score_blocks(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, uint32_t j0,
-                              uint32_t j1, float* out, float* tmp) {
-  constexpr int LPR = D / 8, PER = kThreads / LPR, U = 4;
+__device__ __forceinline__ float score_blocks(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n,
+                                              uint32_t j0, uint32_t j1, float* out, float* tmp) {
+  constexpr int LPR = D / 8, PER = kThreads / LPR;
   const uint32_t l = threadIdx.x % LPR, team = threadIdx.x / LPR;
+  uint4 lo4[kAhead], hi4[kAhead];
+  uint32_t here = 0;  // bit u: block jb + u PER + team has bounds
+  const auto fetch = [&](uint32_t jb) {
+    here = 0;
+#pragma unroll
+    for (int u = 0; u < kAhead; ++u) {
+      const uint32_t j = jb + u * PER + team;
+      size_t row = 0;
+      lo4[u] = hi4[u] = make_uint4(0u, 0u, 0u, 0u);
+      if (j < j1) {
+        if (cache_row(a.c, seq, j << a.blk_shift, row)) {
+          here |= 1u << u;
+          const uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D + 8 * l;
+          lo4[u] = *reinterpret_cast<const uint4*>(b);
+          hi4[u] = *reinterpret_cast<const uint4*>(b + D);
+        } else {
+          set_status(a.status, kStatusRange);
+        }
+      }
+    }
+  };
   float up[8], dn[8], mh[8], ml[8];
+  fetch(j0);
   signed_sums<D>(a, r, g, l, up, dn);
 #pragma unroll
   for (int e = 0; e < 8; ++e) mh[e] = ml[e] = 0.f;
   bool wild = false;
-  for (uint32_t jb = j0; jb < j1; jb += PER * U) {
-    uint4 lo4[U], hi4[U];
-    bool here[U];
+#pragma unroll 1
+  for (uint32_t jb = j0; jb < j1; jb += PER * kAhead) {
+    float s[kAhead];
+    const uint32_t had = here;
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t j = jb + u * PER + team;
-      size_t row = 0;
-      const bool in = j < j1;
-      here[u] = in && cache_row(a.c, seq, j << a.blk_shift, row);
-      if (in && !here[u]) set_status(a.status, kStatusRange);
-      lo4[u] = hi4[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (here[u]) {
-        const uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D + 8 * l;
-        lo4[u] = *reinterpret_cast<const uint4*>(b);
-        hi4[u] = *reinterpret_cast<const uint4*>(b + D);
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const uint32_t j = jb + u * PER + team;
+    for (int u = 0; u < kAhead; ++u) {
       float lo[8], hi[8], c[4] = {0.f, 0.f, 0.f, 0.f};  // four short chains: less rounding, no waiting
       unpack8(lo4[u], lo);
       unpack8(hi4[u], hi);
@@ -307,11 +335,17 @@ __device__ float score_blocks(const Select& a, uint32_t r, uint32_t g, uint32_t 
         mh[e] = fmaxf(mh[e], fabsf(hi[e]));
         ml[e] = fmaxf(ml[e], fabsf(lo[e]));
       }
-      float s = (c[0] + c[1]) + (c[2] + c[3]);
+      s[u] = (c[0] + c[1]) + (c[2] + c[3]);
+    }
+    if (jb + PER * kAhead < j1) fetch(jb + PER * kAhead);
 #pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      if (here[u]) wild |= !(fabsf(s) < INFINITY);
-      if (j < j1 && l == 0) __stcg(out + j, forced(a, j, n) ? INFINITY : here[u] ? s : -INFINITY);
+    for (int u = 0; u < kAhead; ++u) {
+#pragma unroll
+      for (int o = LPR / 2; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
+      const uint32_t j = jb + u * PER + team;
+      const bool in = had >> u & 1;
+      if (in) wild |= !(fabsf(s[u]) < INFINITY);
+      if (j < j1 && l == 0) __stcg(out + j, forced(a, j, n) ? INFINITY : in ? s[u] : -INFINITY);
     }
   }
   float most = 0.f;
@@ -325,29 +359,35 @@ __device__ float score_blocks(const Select& a, uint32_t r, uint32_t g, uint32_t 
   __syncthreads();
   most = tmp[0];
   for (uint32_t w = 1; w < kSelWarps; ++w) most = fmaxf(most, tmp[w]);
-  __syncthreads();
   return most;
 }
 
 // Block j's score in 64 bits, by one warp (the same value in every lane).
 template <int D>
 __device__ double exact_score(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t j) {
-  const uint32_t lane = threadIdx.x & 31, group = a.H / a.c.Hkv;
+  const uint32_t l = (threadIdx.x & 31) % (D / 8), group = a.H / a.c.Hkv;
   size_t row;
   if (!cache_row(a.c, seq, j << a.blk_shift, row)) return -INFINITY;
-  const uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D;
+  const uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D + 8 * l;
+  const uint16_t* q = a.q + ((size_t)r * a.H + g * group) * D + 8 * l;
+  float lo[8], hi[8];
+  unpack8(*reinterpret_cast<const uint4*>(b), lo);
+  unpack8(*reinterpret_cast<const uint4*>(b + D), hi);
   double s = 0.0;
-  for (uint32_t d = lane; d < D; d += 32) {
-    double up = 0.0, dn = 0.0;
-    for (uint32_t h = 0; h < group; ++h) {
-      const double x = bf16f(a.q[((size_t)r * a.H + g * group + h) * D + d]);
-      if (x > 0.0 || x != x) up += x;
-      else dn += x;
+#pragma unroll 4
+  for (uint32_t h = 0; h < group; ++h) {  // sum_h max(q, 0) hi + min(q, 0) lo: the same products, each exact
+    float x[8];
+    unpack8(*reinterpret_cast<const uint4*>(q + (size_t)h * D), x);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      // a product of two bf16 values is exact in 32 bits unless it leaves their range
+      const float p = x[e] * (x[e] < 0.f ? lo[e] : hi[e]);
+      s += fabsf(p) < 1e30f && (fabsf(p) > 1e-30f || x[e] == 0.f) ? (double)p
+                                                               : (double)x[e] * (double)(x[e] < 0.f ? lo[e] : hi[e]);
     }
-    s += up * (double)bf16f(b[D + d]) + dn * (double)bf16f(b[d]);
   }
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+  for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
   return s > 1e300 ? 1e300 : s;  // an infinity stays below the blocks that always come first
 }
 
@@ -394,6 +434,85 @@ __device__ __forceinline__ uint32_t cta_sum(uint32_t x, uint32_t* tmp, uint32_t&
   return x;
 }
 
+// The n_close blocks whose keys lie in [klo, khi], scored in 64 bits: the `need` largest of them (the lower
+// index of equal ones) get the score +infinity, the others -infinity.
+template <int D>
+__device__ __noinline__ void decide(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item,
+                                    uint32_t klo, uint32_t khi, uint32_t n_close, uint32_t need, uint32_t* tmp,
+                                    const uint32_t* close_j) {
+  __shared__ double close_t[kClose];
+  const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  float* s = a.scores + item * a.nblk;
+  const auto close = [&](uint32_t j) {
+    if (j >= n) return false;
+    const uint32_t k = order_key(__ldcg(s + j));
+    return k >= klo && k <= khi;
+  };
+  const auto score = [&](uint32_t j) {
+    const double x = forced(a, j, n) ? (double)INFINITY : exact_score<D>(a, r, g, seq, j);
+    return x != x ? -(double)INFINITY : x;
+  };
+  if (n_close <= kClose) {  // listed in close_j: each ranked among all
+    for (uint32_t i = warp; i < n_close; i += kSelWarps) {
+      const double x = score(close_j[i]);
+      if (lane == 0) close_t[i] = x;
+    }
+    __syncthreads();
+    if (tid < n_close) {
+      uint32_t rank = 0;
+      const double x = close_t[tid];
+      for (uint32_t i = 0; i < n_close; ++i)
+        rank += close_t[i] > x || (close_t[i] == x && close_j[i] < close_j[tid]);
+      __stcg(s + close_j[tid], rank < need ? INFINITY : -INFINITY);
+    }
+    __syncthreads();
+    return;
+  }
+  // many equal or unbounded scores: all of them in 64 bits, then bisection of those bits
+  double* t = a.exact + item * a.nblk;
+  uint32_t turn = 0;
+  __syncthreads();
+  for (uint32_t j0 = warp * 32; j0 < n; j0 += kThreads) {
+    unsigned m = __ballot_sync(0xffffffffu, close(j0 + lane));
+    while (m) {
+      const uint32_t j = j0 + (__ffs(m) - 1);
+      m &= m - 1;
+      const double x = score(j);
+      if (lane == 0) __stcg(t + j, x);
+    }
+  }
+  __syncthreads();
+  const auto count = [&](unsigned long long from, bool above) {
+    uint32_t c = 0;
+    for (uint32_t j = tid; j < n; j += kThreads)
+      if (close(j)) {
+        const unsigned long long x = order_key(__ldcg(t + j));
+        c += above ? x > from : x >= from;
+      }
+    return cta_sum(c, tmp, turn);
+  };
+  unsigned long long bar = 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const unsigned long long c = bar | (1ull << bit);
+    if (count(c, false) >= need) bar = c;
+  }
+  const uint32_t ties = need - count(bar, true);
+  // the first `ties` of those on the bar, in index order: one warp counts
+  if (warp == 0) {
+    uint32_t seen = 0;
+    for (uint32_t j0 = 0; j0 < n; j0 += 32) {
+      const uint32_t j = j0 + lane;
+      const bool c = close(j);
+      const unsigned long long x = c ? order_key(__ldcg(t + j)) : 0ull;
+      const unsigned eq = __ballot_sync(0xffffffffu, c && x == bar);
+      const bool in = x > bar || (x == bar && seen + __popc(eq & ((1u << lane) - 1u)) < ties);
+      if (c) __stcg(s + j, in ? INFINITY : -INFINITY);
+      seen += __popc(eq);
+    }
+  }
+  __syncthreads();
+}
+
 // Which blocks the exact scores choose, given 32-bit ones. Every s_j is within E of the exact t_j
 // (E = (group + 13) 2^-24 most: group - 1 additions in Q+-, 4 multiply-adds and 2 + 5 additions round
 // one after the other, and the rounding of `most` itself is covered by the rest). The K-th largest t is then within E of the K-th largest s, T: s_j > T + 2E is in, s_j < T - 2E is
@@ -401,9 +520,8 @@ __device__ __forceinline__ uint32_t cta_sum(uint32_t x, uint32_t* tmp, uint32_t&
 // scores' bits: a count over the CTA a step, until a step leaves exactly K.
 template <int D>
 __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item, float most) {
-  __shared__ uint32_t tmp[2 * kSelWarps], close_j[kClose], s_close;
-  __shared__ double close_t[kClose];
-  const uint32_t K = a.n_select, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  __shared__ uint32_t tmp[2 * kSelWarps], range[2 * kSelWarps], close_j[kClose];
+  const uint32_t K = a.n_select, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int32_t* out = a.blocks + item * K;
   uint32_t turn = 0;
   Scores sc;
@@ -413,8 +531,32 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     sc.each([&](uint32_t, uint32_t k) { c += k >= from; });
     return cta_sum(c, tmp, turn);
   };
-  // low: the largest tried value with at least K keys from it up
-  uint32_t low = 1, high = 0xffffffffu, at_low = n;
+  // the finite scores' range: most of a bisection of all 32 bits would only find it
+  uint32_t low = 0xffffffffu, high = 0, n_forced = 0;
+  sc.each([&](uint32_t, uint32_t k) {
+    low = k ? min(low, k) : low;
+    high = k < kInf ? max(high, k) : high;
+    n_forced += k >= kInf;
+  });
+  low = __reduce_min_sync(0xffffffffu, low);
+  high = __reduce_max_sync(0xffffffffu, high);
+  if (lane == 0) {
+    range[warp] = low;
+    range[kSelWarps + warp] = high;
+  }
+  uint32_t at_low = n;
+  n_forced = cta_sum(n_forced, tmp, turn);
+  for (uint32_t w = 0; w < kSelWarps; ++w) {
+    low = min(low, range[w]);
+    high = max(high, range[kSelWarps + w]);
+  }
+  ++high;  // below kInf: only what is infinite is from here up
+  if (n_forced >= K) {
+    low = kInf;
+    high = kInf + 1;
+    at_low = n_forced;
+  }
+  // low: the largest tried value with at least K keys from it up; high: the smallest with fewer
   while (at_low != K && high - low > 1) {
     const uint32_t mid = low + (high - low) / 2, c = count(mid);
     if (c >= K) {
@@ -430,10 +572,9 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
   });
   kth = __reduce_min_sync(0xffffffffu, kth);
   __syncthreads();
-  if (lane == 0) tmp[warp] = kth;
+  if (lane == 0) range[warp] = kth;
   __syncthreads();
-  for (uint32_t w = 0; w < kSelWarps; ++w) kth = min(kth, tmp[w]);
-  __syncthreads();
+  for (uint32_t w = 0; w < kSelWarps; ++w) kth = min(kth, range[w]);
   const float T = key_value(kth), E = (float)(a.H / a.c.Hkv + 13) * 0x1p-24f * most;
   uint32_t klo = 1, khi = 0xffffffffu;  // keys above khi are in, below klo out
   if (E < INFINITY) {
@@ -446,123 +587,40 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     c2 += k >= klo && k <= khi;
   });
   const uint32_t n_sure = cta_sum(c1, tmp, turn), n_close = cta_sum(c2, tmp, turn), need = K - n_sure;
-  const bool again = n_close != need, listed = n_close <= kClose;
-  unsigned long long bar = 0;  // (not listed) a close block is in from this key up, `ties` of the equal ones
-  uint32_t ties = 0;
-  double* t = a.exact + item * a.nblk;
-  if (again && listed) {
-    if (tid == 0) s_close = 0;
-    __syncthreads();
-    sc.each([&](uint32_t j, uint32_t k) {
-      if (k >= klo && k <= khi) close_j[atomicAdd(&s_close, 1u)] = j;
-    });
-    __syncthreads();
-    for (uint32_t i = warp; i < n_close; i += kSelWarps) {
-      const uint32_t j = close_j[i];
-      const double x = forced(a, j, n) ? (double)INFINITY : exact_score<D>(a, r, g, seq, j);
-      if (lane == 0) close_t[i] = x != x ? -(double)INFINITY : x;
-    }
-    __syncthreads();
-    // those that are in keep their place in the list, the others leave it
-    uint32_t mine = 0xffffffffu;
-    if (tid < n_close) {
-      uint32_t rank = 0;
-      const double x = close_t[tid];
-      for (uint32_t i = 0; i < n_close; ++i)
-        rank += close_t[i] > x || (close_t[i] == x && close_j[i] < close_j[tid]);
-      if (rank < need) mine = close_j[tid];
-    }
-    __syncthreads();
-    if (tid < n_close) close_j[tid] = mine;
-    __syncthreads();
-  } else if (again) {
-    // many equal or unbounded scores: all of them in 64 bits, then bisection of those bits
-    const uint32_t rounds = (n + kThreads - 1) / kThreads;
-    for (uint32_t i = 0; i < rounds; ++i) {
-      const uint32_t j0 = i * kThreads + warp * 32;
-      const uint32_t k = j0 + lane < n ? order_key(__ldcg(sc.s + j0 + lane)) : 0u;
-      unsigned m = __ballot_sync(0xffffffffu, k >= klo && k <= khi);
-      while (m) {
-        const uint32_t j = j0 + (__ffs(m) - 1);
-        m &= m - 1;
-        const double x = forced(a, j, n) ? (double)INFINITY : exact_score<D>(a, r, g, seq, j);
-        if (lane == 0) __stcg(t + j, x);
-      }
-    }
-    __syncthreads();
-    const auto count64 = [&](unsigned long long from, bool above) {
-      uint32_t c = 0;
+  uint32_t cut = klo;  // in from this key up
+  if (n_close != need) {
+    if (n_close <= kClose) {  // a list of them, in any order
+      if (threadIdx.x == 0) tmp[0] = 0;
+      __syncthreads();
       sc.each([&](uint32_t j, uint32_t k) {
-        if (k >= klo && k <= khi) {
-          const unsigned long long x = order_key(__ldcg(t + j));
-          c += above ? x > from : x >= from;
-        }
+        if (k >= klo && k <= khi) close_j[atomicAdd(tmp, 1u)] = j;
       });
-      return cta_sum(c, tmp, turn);
-    };
-    for (int bit = 63; bit >= 0; --bit) {
-      const unsigned long long c = bar | (1ull << bit);
-      if (count64(c, false) >= need) bar = c;
+      __syncthreads();
     }
-    ties = need - count64(bar, true);
+    decide<D>(a, r, g, seq, n, item, klo, khi, n_close, need, tmp, close_j);
+    sc.take(a.scores + item * a.nblk, n);
+    cut = min(khi, kInf - 1) + 1;
   }
-  // in index order, the lower of equal ones first: a warp's blocks are neighbours, so ranks come from
-  // ballots and the counts of the warps before
-  const auto is_in = [&](uint32_t j, uint32_t k, bool& eq) {
-    eq = false;
-    if (k > khi) return true;
-    if (k < klo) return false;
-    if (!again) return true;
-    if (listed) {
-      for (uint32_t i = 0; i < n_close; ++i)
-        if (close_j[i] == j) return true;
-      return false;
-    }
-    const unsigned long long x = order_key(__ldcg(t + j));
-    eq = x == bar;
-    return x > bar;
-  };
-  uint32_t eq_before = 0, n_in = 0, n_eq = 0;
-  if (again && !listed) {
-    sc.each([&](uint32_t j, uint32_t k) {
-      bool eq;
-      is_in(j, k, eq);
-      n_eq += eq;
-    });
-    n_eq = __reduce_add_sync(0xffffffffu, n_eq);
-    __syncthreads();
-    if (lane == 0) tmp[warp] = n_eq;
-    __syncthreads();
-    for (uint32_t w = 0; w < warp; ++w) eq_before += tmp[w];
-    __syncthreads();
-  }
-  const auto flag = [&](uint32_t j, uint32_t k, uint32_t& rank) {  // rank: equal ones before
-    bool eq, in = is_in(j, k, eq);
-    const unsigned me = __ballot_sync(0xffffffffu, eq);
-    if (eq) in = rank + __popc(me & ((1u << lane) - 1u)) < ties;
-    rank += __popc(me);
-    return in;
-  };
-  uint32_t rank = eq_before;
-  sc.each([&](uint32_t j, uint32_t k) { n_in += __popc(__ballot_sync(0xffffffffu, flag(j, k, rank))); });
+  // in index order: a warp's blocks are neighbours, so places come from ballots and the counts of the warps before
+  uint32_t n_in = 0;
+  sc.each([&](uint32_t, uint32_t k) { n_in += k >= cut; });
+  n_in = __reduce_add_sync(0xffffffffu, n_in);
   __syncthreads();
   if (lane == 0) tmp[warp] = n_in;
   __syncthreads();
   uint32_t at = 0;
   for (uint32_t w = 0; w < warp; ++w) at += tmp[w];
-  rank = eq_before;
   sc.each([&](uint32_t j, uint32_t k) {
-    const bool in = flag(j, k, rank);
-    const unsigned m = __ballot_sync(0xffffffffu, in);
+    const unsigned m = __ballot_sync(0xffffffffu, k >= cut);
     const uint32_t to = at + __popc(m & ((1u << lane) - 1u));
-    if (in && to < K) out[to] = (int32_t)j;
+    if (k >= cut && to < K) out[to] = (int32_t)j;
     at += __popc(m);
   });
 }
 
-// CTA x of a (row, kv-head) scores the x-th part of its blocks; the last of them to finish chooses.
+// CTA x of a (row, kv-head) scores the x-th `part` of its blocks; the last of them to finish chooses.
 template <int D>
-__global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant__ Select a) {
+__global__ void __launch_bounds__(kThreads, 2) select_kernel(const __grid_constant__ Select a, uint32_t part) {
   __shared__ float tmp[kSelWarps];
   __shared__ uint32_t s_last;
   const uint32_t r = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
@@ -579,31 +637,27 @@ __global__ void __launch_bounds__(kThreads) select_kernel(const __grid_constant_
       for (uint32_t i = tid; i < K; i += kThreads) a.blocks[item * K + i] = i < n ? (int32_t)i : -1;
     return;
   }
-  constexpr uint32_t PER = kThreads / (D / 8);
-  const uint32_t part = ((n + gridDim.x - 1) / gridDim.x + PER - 1) / PER * PER, parts = (n + part - 1) / part;
+  const uint32_t parts = (n + part - 1) / part;
   if (blockIdx.x >= parts) return;
   float* most = a.most + item * gridDim.x;
   float m = score_blocks<D>(a, r, g, seq, n, blockIdx.x * part, min(n, (blockIdx.x + 1) * part),
                             a.scores + item * a.nblk, tmp);
+  __syncthreads();
   if (parts > 1) {
-    __threadfence();
-    __syncthreads();
     if (tid == 0) {
+      // the barrier has put the CTA's scores before this; the count's release and acquire put them before the
+      // last one's reads
       __stcg(most + blockIdx.x, m);
-      __threadfence();
-      const uint32_t had = atomicAdd(a.tickets + item, 1u);
+      const uint32_t had = count_up(a.tickets + item);
       s_last = had == parts - 1;
       if (had > parts - 1) set_status(a.status, kStatusInvalid);
       if (had == parts - 1) a.tickets[item] = 0;
-      __threadfence();
     }
     __syncthreads();
     if (!s_last) return;
     m = 0.f;
     for (uint32_t p = tid % 32; p < parts; p += 32) m = fmaxf(m, __ldcg(most + p));
     m = warp_max(m);
-  } else {
-    __syncthreads();
   }
   choose<D>(a, r, g, seq, n, item, m);
 }
@@ -643,15 +697,14 @@ cudaError_t read(const Read& a, cudaStream_t st) {
   return cudaGetLastError();
 }
 
-uint32_t select_parts(uint32_t items, uint32_t nblk, uint32_t D, uint32_t ctas) {
-  // a CTA scores at least one pass of four blocks a team
-  const uint32_t per = kThreads / (D / 8) * 4;
-  return std::max(1u, std::min((nblk + per - 1) / per, ctas / items));
-}
-
 cudaError_t select(const Select& a, cudaStream_t st) {
-  const dim3 grid(select_parts(a.r.n_rows * a.c.Hkv, a.nblk, a.c.D, a.ctas), a.c.Hkv, a.r.n_rows);
-#define CALL(DD) select_kernel<DD><<<grid, kThreads, 0, st>>>(a)
+  // Blocks of a CTA: whole passes of the teams, and no more CTAs than a.ctas if the sequences were all as long as
+  // the capacity (parts of one size, so that a long sequence is not the last to finish)
+  const uint32_t pass = kThreads / (a.c.D / 8) * kAhead, items = a.r.n_rows * a.c.Hkv;
+  const uint32_t parts = std::max(1u, std::min((a.nblk + pass - 1) / pass, a.ctas / items));
+  const uint32_t part = ((a.nblk + parts - 1) / parts + pass - 1) / pass * pass;
+  const dim3 grid((a.nblk + part - 1) / part, a.c.Hkv, a.r.n_rows);
+#define CALL(DD) select_kernel<DD><<<grid, kThreads, 0, st>>>(a, part)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
   return cudaGetLastError();

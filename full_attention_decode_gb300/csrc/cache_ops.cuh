@@ -55,4 +55,12 @@ __device__ __forceinline__ bool cache_row(const Cache& c, uint32_t seq, uint32_t
   return true;
 }
 
+// One more at *p, and how many there were: what this CTA wrote before (a barrier puts its threads' writes
+// before the counting thread's) is seen by who counts after it.
+__device__ __forceinline__ uint32_t count_up(uint32_t* p) {
+  uint32_t had;
+  asm volatile("atom.acq_rel.gpu.global.add.u32 %0, [%1], 1;" : "=r"(had) : "l"(p) : "memory");
+  return had;
+}
+
 }  // namespace q35c

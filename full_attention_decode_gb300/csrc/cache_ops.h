@@ -69,7 +69,7 @@ struct Select {
 };
 cudaError_t select(const Select& a, cudaStream_t st);
 constexpr uint32_t kMaxItems = kMaxQueries * 8;  // of 8 kv-heads
-constexpr uint32_t kMaxParts = 1024;   // parts of all items: at most one an item, or this many
+constexpr uint32_t kMaxParts = 2048;   // parts of all items: at most one an item, or this many
 
 struct Attend {
   Cache c;

@@ -60,78 +60,89 @@ __device__ __forceinline__ void wht8(float (&x)[8], uint32_t lane) {
   for (int e = 0; e < 8; ++e) x[e] *= norm;
 }
 
+// u - w in pairs.
+__device__ __forceinline__ float2 sub2(float2 u, float2 w) { return __ffma2_rn(w, make_float2(-1.f, -1.f), u); }
+
 // The same transform, four lanes a row: lane l of each four holds pieces i < D / 32 of eight
-// elements, [32 i + 8 l, 32 i + 8 l + 8). Index bits 3 and 4 lie on the lanes, all others inside a
-// lane, so a row of 256 costs a warp 16 shuffles (40 with 32 lanes a row).
+// elements, [32 i + 8 l, 32 i + 8 l + 8), in pairs (four a piece). Index bits 3 and 4 lie on the lanes, all
+// others inside a lane, so a row of 256 costs a warp 16 shuffles (40 with 32 lanes a row); sums
+// and differences are taken two at a time.
 template <int D>
-__device__ __forceinline__ void wht_quad(float (&x)[D / 4], uint32_t lane) {
-  constexpr int N = D / 4;
+__device__ __forceinline__ void wht_quad(float2 (&x)[D / 8], uint32_t lane) {
+  constexpr int N = D / 8;
 #pragma unroll
-  for (int hb = 1; hb < 8; hb <<= 1)
+  for (int k = 0; k < N; ++k) x[k] = make_float2(x[k].x + x[k].y, x[k].x - x[k].y);
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (!(e & hb)) {
-        const float u = x[e], w = x[e + hb];
-        x[e] = u + w;
-        x[e + hb] = u - w;
+  for (int hb = 1; hb < 4; hb <<= 1)
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+      if (!(k & hb)) {
+        const float2 u = x[k], w = x[k + hb];
+        x[k] = __fadd2_rn(u, w);
+        x[k + hb] = sub2(u, w);
       }
 #pragma unroll
   for (uint32_t m = 1; m < 4; m <<= 1) {
     const float s = lane & m ? -1.f : 1.f;
 #pragma unroll
-    for (int e = 0; e < N; ++e) x[e] = fmaf(x[e], s, __shfl_xor_sync(0xffffffffu, x[e], m));
+    for (int k = 0; k < N; ++k) {
+      const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, x[k].x, m), __shfl_xor_sync(0xffffffffu, x[k].y, m));
+      x[k] = __ffma2_rn(x[k], make_float2(s, s), o);
+    }
   }
 #pragma unroll
-  for (int hb = 8; hb < N; hb <<= 1)
+  for (int hb = 4; hb < N; hb <<= 1)
 #pragma unroll
-    for (int e = 0; e < N; ++e)
-      if (!(e & hb)) {
-        const float u = x[e], w = x[e + hb];
-        x[e] = u + w;
-        x[e + hb] = u - w;
+    for (int k = 0; k < N; ++k)
+      if (!(k & hb)) {
+        const float2 u = x[k], w = x[k + hb];
+        x[k] = __fadd2_rn(u, w);
+        x[k + hb] = sub2(u, w);
       }
   const float norm = rsqrtf((float)D);
 #pragma unroll
-  for (int e = 0; e < N; ++e) x[e] *= norm;
+  for (int k = 0; k < N; ++k) x[k] = __fmul2_rn(x[k], make_float2(norm, norm));
 }
 
-// Quantise a piece of eight elements, a group of 16 on two lanes: scale = bf16(amax / 448),
-// code = E4M3(x / scale); a zero group keeps scale 0 and codes 0. The quotient is
-// x * (1 / scale) with one residual correction (Markstein 1990: q + (x - q s) / s). x and
-// scale have 8 significant bits and a border between codes 5, so a quotient that is not on a
-// border is at least 2^-13 away from it, and one that is comes out exact: the codes are
-// those of the rounded quotient. Scales near the ends of the range take the division.
-__device__ __forceinline__ uint2 quant8(const float* x, uint16_t& scale) {
-  float amax = 0.f;
+// Quantise a piece of eight bf16 values (in pairs), a group of 16 on two lanes: scale = bf16(amax / 448),
+// code = E4M3(x / scale); a zero group keeps scale 0 and codes 0. Neither quotient needs
+// a division:
+//  - amax has 8 significant bits and 448 = 7 * 64, so amax / 448 is never on a border between two bf16 values (9
+//    bits times 7 has more than 8) and at least 2^-12 away from one: the product with 1 / 448 rounds alike;
+//  - x / scale as q = x r with r near 1 / scale and one residual correction, q + (x - q scale) r (Markstein 1990).
+//    x and scale have 8 bits and a border between codes 5: a quotient that is not on a border is at least
+//    2^-13 away from it, and one that is comes out exact. Scales near the ends of the range take the division.
+__device__ __forceinline__ uint2 quant8(const uint32_t* w, uint16_t& scale) {
+  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(w));
 #pragma unroll
-  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(x[e]));
+  for (int i = 1; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(w + i)));
+  float amax = fmaxf(__low2float(m), __high2float(m));
   amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  scale = to_bf16(amax / 448.f);
+  scale = to_bf16(amax * (1.0f / 448.0f));
   const float sc = bf16f(scale);
   uint32_t c[4] = {0u, 0u, 0u, 0u};
   if (sc > 1e-30f && sc < 1e30f) {
-    const float r = __frcp_rn(sc);
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc));
+    const float2 r2 = make_float2(r, r), s2 = make_float2(-sc, -sc);
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      float q0 = x[2 * i] * r, q1 = x[2 * i + 1] * r;
-      q0 = fmaf(fmaf(-q0, sc, x[2 * i]), r, q0);
-      q1 = fmaf(fmaf(-q1, sc, x[2 * i + 1]), r, q1);
-      c[i] = e4m3_pair(q0, q1);
+      const float2 x = make_float2(bf16lo(w[i]), bf16hi(w[i]));
+      float2 q = __fmul2_rn(x, r2);
+      q = __ffma2_rn(__ffma2_rn(q, s2, x), r2, q);
+      c[i] = e4m3_pair(q.x, q.y);
     }
   } else if (sc != 0.f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3_pair(x[2 * i] / sc, x[2 * i + 1] / sc);
+    for (int i = 0; i < 4; ++i) c[i] = e4m3_pair(bf16lo(w[i]) / sc, bf16hi(w[i]) / sc);
   }
   return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
 }
-// Eight codes times their scale (exact).
-__device__ __forceinline__ void dequant_codes8(uint2 c, float sc, float* x) {
+// Eight codes times their scale (exact), in pairs.
+__device__ __forceinline__ void dequant8(uint2 c, float sc, float2* x) {
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) {
-    const float2 f = e4m3_pair_value((e < 4 ? c.x : c.y) >> (8 * (e % 4)));
-    x[e] = f.x * sc;
-    x[e + 1] = f.y * sc;
-  }
+  for (int i = 0; i < 4; ++i)
+    x[i] = __fmul2_rn(e4m3_pair_value((i < 2 ? c.x : c.y) >> (16 * (i % 2))), make_float2(sc, sc));
 }
 
 }  // namespace q35

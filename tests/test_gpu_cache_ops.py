@@ -532,9 +532,9 @@ def choose(s, row, b, p, n, first, last):
     g, seen = s.H // s.Hkv, p // s.block + 1
     q = f64(s.q[row]).reshape(s.Hkv, g, s.D)
     bounds = f64(s.lo_hi)[s.at(b, np.arange(seen) * s.block) // s.block]
-    up, dn = np.maximum(q, 0).sum(1), np.minimum(q, 0).sum(1)
-    with np.errstate(all="ignore"):
-        score = np.einsum("gd,jgd->gj", up, bounds[:, :, 1]) + np.einsum("gd,jgd->gj", dn, bounds[:, :, 0])
+    with np.errstate(all="ignore"):  # the bound of q.k: hi where q is not negative, lo where it is
+        score = np.where(q[:, :, None] < 0, q[:, :, None] * bounds[:, :, 0].transpose(1, 0, 2)[:, None],
+                         q[:, :, None] * bounds[:, :, 1].transpose(1, 0, 2)[:, None]).sum((1, 3))
     score = np.where(np.isnan(score), -np.inf, score)
     j = np.arange(seen)
     rank = np.where((j < first) | (j >= seen - last), 1, 0)
@@ -567,6 +567,7 @@ def check_choice(s, n, first=1, last=1):
                                   (dict(heads="4b", fmt=TURBO8, lens=[1500, 90], block=32, page=64), 16),
                                   (dict(heads="tiny_alt", fmt=BF16, lens=[700, 650], rows=[6, 2], tail=2, lead=1), 5),
                                   (dict(heads="wide", fmt=BF16, lens=[2100], block=16), 131),
+                                  (dict(heads="tiny", fmt=BF16, lens=[70000], block=16), 33),
                                   (dict(heads="eight", fmt=TURBO8, lens=[9000, 10], block=16, page=32), 33)])
 def test_selection(kw, n, first, last):
     s = Setup(**kw)
