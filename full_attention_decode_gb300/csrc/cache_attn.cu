@@ -32,31 +32,24 @@ namespace q35c {
 using namespace q35;
 namespace {
 
-// Warps of a CTA, one CTA an SM.
-template <int D, int NT, bool T8>
-constexpr int warps_of() {
-#ifndef ATT_T8W
-#define ATT_T8W 8
-#endif
-  return T8 && D * NT <= 256 ? ATT_T8W : 8;
-}
+constexpr int kWarps = 8;  // of a CTA, one CTA an SM (16 warps of 128 registers for Turbo8: 84 us where 8 took 73)
+constexpr int kAttnThreads = 32 * kWarps;
 
 // A ring slot: K or V of 16 tokens. Rows are padded by 16 bytes, which puts eight rows'
 // 16-byte pieces in different banks.
-template <int D, int NT, bool T8>
+template <int D, bool T8>
 struct Slot {
   static constexpr int row = T8 ? D + 16 : 2 * D + 16;
   static constexpr int scales = T8 ? D / 16 * 2 : 0;  // a token's scales
   static constexpr int bytes = 16 * (row + scales);
   // slots of a warp, what shared memory holds up to 4 (K and V of two tiles)
-  static constexpr int n = D == 256 ? (T8 ? (warps_of<D, NT, T8>() == 16 ? 2 : warps_of<D, NT, T8>() == 12 ? 3 : 4) : 3) : 4;
+  static constexpr int n = D == 256 && !T8 ? 3 : 4;
 };
 // Shared memory of a CTA: the rings (reused to join the warps), Q's fragments and (T8)
 // the rotated q, the warps' maxima and sums, T8's transposed V scales, then the rows' first tiles.
 template <int D, int NT, bool T8>
 struct Smem {
-  using S = Slot<D, NT, T8>;
-  static constexpr int kWarps = warps_of<D, NT, T8>();
+  using S = Slot<D, T8>;
   static constexpr int ring = kWarps * S::n * S::bytes;
   static constexpr int join = kWarps * 8 * NT * (D + 4) * 4;
   static constexpr int weights = 24576;  // the parts' weights, behind their sums
@@ -151,19 +144,29 @@ struct Segment {
   const int32_t* tab;  // paged: its table
 };
 
-// The first token of a tile and where its tokens lie: rows of tokens 0-7 and 8-15 (a
-// page holds at least 8 tokens), and how many of the 16 the row sees.
+// The first token of a tile and where its tokens lie: rows of tokens 0-7 and 8-15 (a page holds at least 8
+// tokens), and how many tokens the item's last row sees from the tile's first on, up to 32.
 struct Tile {
   size_t row[2];
   uint32_t token, seen;
   bool in[2];
 };
+__device__ __forceinline__ Tile lane_of(const Tile& t, uint32_t src) {
+  Tile x;
+  x.row[0] = __shfl_sync(0xffffffffu, (unsigned long long)t.row[0], src);
+  x.row[1] = __shfl_sync(0xffffffffu, (unsigned long long)t.row[1], src);
+  x.token = __shfl_sync(0xffffffffu, t.token, src);
+  const uint32_t f = __shfl_sync(0xffffffffu, t.seen | (t.in[0] ? 256u : 0u) | (t.in[1] ? 512u : 0u), src);
+  x.seen = f & 255u;
+  x.in[0] = f & 256u;
+  x.in[1] = f & 512u;
+  return x;
+}
 
 template <int D, int NT, bool T8>
 struct Attention {
-  using S = Slot<D, NT, T8>;
+  using S = Slot<D, T8>;
   using M = Smem<D, NT, T8>;
-  static constexpr int kWarps = M::kWarps, kAttnThreads = 32 * kWarps;
   const Attend& a;
   uint8_t* sm;
   uint32_t warp, lane, group;
@@ -189,7 +192,7 @@ struct Attention {
     }
     if (token > s.pos) return x;
     x.token = (uint32_t)token;
-    x.seen = min(16u, s.pos - x.token + 1);
+    x.seen = min(32u, s.pos - x.token + 1);
     if (s.tab) {
       const uint32_t sh = a.c.bt_shift, mask = (1u << sh) - 1u, t8 = x.token + (x.seen > 8 ? 8 : 0);
       const uint32_t b0 = (uint32_t)s.tab[x.token >> sh], b1 = (uint32_t)s.tab[t8 >> sh];
@@ -211,7 +214,7 @@ struct Attention {
   // and 0 times an infinity would spoil them.
   __device__ void load(const Segment& s, const Tile& x, int p, uint32_t slot) const {
     const uint32_t last = s.pos + 1 - (p ? s.rows - 1 : 0);  // tokens below it
-    const uint32_t seen = x.seen ? min(x.seen, last > x.token ? last - x.token : 0u) : 0u;
+    const uint32_t seen = x.seen ? min(16u, last > x.token ? last - x.token : 0u) : 0u;
     constexpr int C = (T8 ? D : 2 * D) / 16, R = 32 / C > 0 ? 32 / C : 1;  // 16-byte pieces of a row, rows a pass
     const uint8_t* base = p ? a.c.v : a.c.k;
     const uint32_t stride = a.c.Hkv * D * (T8 ? 1 : 2), r0 = lane / C, c = lane % C;
@@ -529,7 +532,7 @@ struct Attention {
   __device__ void add_tail(const Segment& sg, uint32_t t, const float (&p)[NT][4], int ev) {
     const Tile x = tile(sg, t);
     const uint32_t first = sg.pos + 2 - sg.rows, r = lane >> 2;  // the first such token
-    for (uint32_t k = first > x.token ? first - x.token : 0u; k < x.seen; ++k) {
+    for (uint32_t k = first > x.token ? first - x.token : 0u; k < min(x.seen, 16u); ++k) {
       if (!(k & 8 ? x.in[1] : x.in[0])) continue;
       const size_t row = (k & 8 ? x.row[1] : x.row[0]) + (k & 7);
       const size_t at = (row * a.c.Hkv + sg.g) * D;
@@ -588,48 +591,39 @@ struct Attention {
 #pragma unroll
         for (int i = 0; i < 4; ++i) o[d][nt][i] = 0.f;
     float sc[NT][4];
-    uint32_t slot = 0, seen = 0;  // the slot that is read now and refilled then
-    Tile ahead, next;             // the tile that is being copied, and the one after it, looked up half a tile ahead
-    next.seen = ahead.seen = 0;
+    uint32_t slot = 0;                          // the slot that is read now and refilled then
+    uint32_t seen = 0, seen1 = 0, seen2 = 0;    // of the tile that is read, the last one copied, the one before
+    Tile found, ahead;  // each lane: a tile's place, 32 tiles looked up at a time; the tile that is being copied
+    found.seen = ahead.seen = 0;
 #pragma unroll 1
-    for (int h = -S::n - 2; h < max(halves, 1); ++h) {
+    for (int h = -S::n; h < max(halves, 1); ++h) {
       if (h == 0) put_q(q);
       if (h >= 0 && h < halves) {
         cp_wait<S::n - 1>();
         __syncwarp();
-        const uint32_t t = first + (h >> 1) * kWarps;
         if (!(h & 1)) {
-          seen = seen_of(s, t);
+          seen = seen2;  // the copies are one tile ahead
           if (seen) scores(slot, sc);
         } else if (seen) {
           const int ev = accumulate(slot, sc, seen);
-          if (seen < 16 + s.rows - 1 && s.rows > 1) add_tail(s, t, sc, ev);
+          if (seen < 16 + s.rows - 1 && s.rows > 1) add_tail(s, first + (h >> 1) * kWarps, sc, ev);
         }
         __syncwarp();  // this half-tile has been read by every lane
       }
       const int c = h + S::n;  // the half-tile to copy
-      if (c >= 0) {
-        if (c < halves) load(s, ahead, c & 1, slot);
-        cp_commit();
-        slot = slot + 1 == S::n ? 0 : slot + 1;
+      if (!(c & 1)) {
+        const uint32_t i = c >> 1;
+        if (i % 32 == 0) found = tile(s, first + (i + lane) * kWarps);
+        ahead = lane_of(found, i % 32);
+        seen2 = seen1;
+        seen1 = ahead.seen;
       }
-      if (c & 1) ahead = next;
-      else next = tile(s, first + ((c >> 1) + 1) * kWarps);
+      if (c < halves) load(s, ahead, c & 1, slot);
+      cp_commit();
+      slot = slot + 1 == S::n ? 0 : slot + 1;
     }
     cp_wait<0>();
   }
-  // How many tokens from a tile's first on the last row sees, up to 32.
-  __device__ uint32_t seen_of(const Segment& s, uint32_t t) const {
-    uint64_t token = (uint64_t)t * 16;
-    if (a.blocks) {
-      const uint32_t per = a.blk_shift - 4;
-      const int32_t b = a.blocks[((size_t)s.row * a.c.Hkv + s.g) * a.n_blocks + (t >> per)];
-      if (b < 0) return 0;
-      token = ((uint64_t)(uint32_t)b << a.blk_shift) + (t & ((1u << per) - 1u)) * 16;
-    }
-    return token > s.pos ? 0u : (uint32_t)min((uint64_t)32, s.pos - token + 1);
-  }
-
   // ---- the warps' outputs added up: sum [cols][D + 4] at sm, M and L at ml[kWarps]
   __device__ void join_warps(uint32_t cols, uint32_t warps) {
     float* ml = reinterpret_cast<float*>(sm + M::ml);
@@ -861,11 +855,10 @@ __device__ __forceinline__ uint32_t row_tiles(const Attend& a, const Rows& at, u
 }
 
 template <int D, int NT, bool T8>
-__global__ void __launch_bounds__(32 * warps_of<D, NT, T8>(), 1) attend_kernel(const __grid_constant__ Attend a) {
+__global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_constant__ Attend a) {
   extern __shared__ __align__(128) uint8_t sm[];
   using A = Attention<D, NT, T8>;
   using M = Smem<D, NT, T8>;
-  constexpr uint32_t kWarps = M::kWarps, kAttnThreads = 32 * kWarps;
   uint32_t* first = reinterpret_cast<uint32_t*>(sm + M::first);  // [n_rows + 1]: tiles before a row (of one head)
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + M::misc);
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.H / a.c.Hkv;
@@ -1016,12 +1009,11 @@ __global__ void __launch_bounds__(32 * warps_of<D, NT, T8>(), 1) attend_kernel(c
 
 template <int D, int NT, bool T8>
 cudaError_t launch(const Attend& a, cudaStream_t st) {
-  constexpr uint32_t W = warps_of<D, NT, T8>();
   const uint32_t bytes = Smem<D, NT, T8>::first + (a.r.n_rows + 1) * 4;
   const uint64_t most = (uint64_t)a.r.n_rows * a.c.Hkv *
                         (a.blocks ? (uint64_t)a.n_blocks << (a.blk_shift - 4) : (a.c.capacity + 15) / 16);
   const uint32_t grid = (uint32_t)std::min<uint64_t>(std::min(a.sms, kMaxCtas), most);
-  attend_kernel<D, NT, T8><<<grid, 32 * W, bytes, st>>>(a);
+  attend_kernel<D, NT, T8><<<grid, kAttnThreads, bytes, st>>>(a);
   return cudaGetLastError();
 }
 template <int D>
