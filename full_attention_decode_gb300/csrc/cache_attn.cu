@@ -863,6 +863,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   uint32_t* misc = reinterpret_cast<uint32_t*>(sm + M::misc);
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, group = a.H / a.c.Hkv;
   const uint32_t pack = a.blocks || group > 8 ? 1 : 8 / group;
+  pdl_wait();
+  pdl_launch();
   // where the rows are, in shared memory (the ring is empty): one round trip for all searches
   Rows rows_here = a.r;
   {
@@ -1013,8 +1015,7 @@ cudaError_t launch(const Attend& a, cudaStream_t st) {
   const uint64_t most = (uint64_t)a.r.n_rows * a.c.Hkv *
                         (a.blocks ? (uint64_t)a.n_blocks << (a.blk_shift - 4) : (a.c.capacity + 15) / 16);
   const uint32_t grid = (uint32_t)std::min<uint64_t>(std::min(a.sms, kMaxCtas), most);
-  attend_kernel<D, NT, T8><<<grid, kAttnThreads, bytes, st>>>(a);
-  return cudaGetLastError();
+  return launch_early(attend_kernel<D, NT, T8>, dim3(grid), kAttnThreads, bytes, st, a);
 }
 template <int D>
 cudaError_t launch_for(const Attend& a, cudaStream_t st) {

@@ -169,6 +169,8 @@ __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, ui
 template <int D, bool T8>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Append a, uint32_t row_ctas,
                                                           uint32_t span_rows) {
+  pdl_wait();
+  pdl_launch();
   if (blockIdx.x < row_ctas) {
     if constexpr (T8) append_turbo8<D>(a, blockIdx.x);
     else append_plain<D>(a, blockIdx.x);
@@ -185,6 +187,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
 
 template <int D, bool T8>
 __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ Read a) {
+  pdl_wait();
+  pdl_launch();
   if constexpr (T8) {
     constexpr int P = D / 32;
     const size_t team = (blockIdx.x * (size_t)kThreads + threadIdx.x) / 4;
@@ -623,6 +627,8 @@ template <int D>
 __global__ void __launch_bounds__(kThreads, 2) select_kernel(const __grid_constant__ Select a, uint32_t part) {
   __shared__ float tmp[kSelWarps];
   __shared__ uint32_t s_last;
+  pdl_wait();
+  pdl_launch();
   const uint32_t r = blockIdx.z, g = blockIdx.y, tid = threadIdx.x;
   uint32_t seq, pos;
   const RowKind kind = locate(a.r, a.c.capacity, r, seq, pos);
@@ -679,22 +685,20 @@ cudaError_t append(const Append& a, cudaStream_t st) {
   const uint32_t folds = (a.r.n_rows + span - 1) / span * a.c.Hkv, teams = a.blk_shift > 6 ? 1 : kThreads / (a.c.D / 8);
   const uint32_t grid = rows + (a.bounds ? (folds + teams - 1) / teams : 0);
 #define CALL(DD)                                                               \
-  if (t8) append_kernel<DD, true><<<grid, kThreads, 0, st>>>(a, rows, span);   \
-  else append_kernel<DD, false><<<grid, kThreads, 0, st>>>(a, rows, span)
+  return t8 ? launch_early(append_kernel<DD, true>, dim3(grid), kThreads, 0, st, a, rows, span)   \
+            : launch_early(append_kernel<DD, false>, dim3(grid), kThreads, 0, st, a, rows, span)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
-  return cudaGetLastError();
 }
 
 cudaError_t read(const Read& a, cudaStream_t st) {
   const bool t8 = a.c.ks != nullptr;
   const uint32_t grid = row_ctas_of(a.r, a.c, t8);
 #define CALL(DD)                                                   \
-  if (t8) read_kernel<DD, true><<<grid, kThreads, 0, st>>>(a);     \
-  else read_kernel<DD, false><<<grid, kThreads, 0, st>>>(a)
+  return t8 ? launch_early(read_kernel<DD, true>, dim3(grid), kThreads, 0, st, a)     \
+            : launch_early(read_kernel<DD, false>, dim3(grid), kThreads, 0, st, a)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
-  return cudaGetLastError();
 }
 
 cudaError_t select(const Select& a, cudaStream_t st) {
@@ -704,10 +708,9 @@ cudaError_t select(const Select& a, cudaStream_t st) {
   const uint32_t parts = std::max(1u, std::min((a.nblk + pass - 1) / pass, a.ctas / items));
   const uint32_t part = ((a.nblk + parts - 1) / parts + pass - 1) / pass * pass;
   const dim3 grid((a.nblk + part - 1) / part, a.c.Hkv, a.r.n_rows);
-#define CALL(DD) select_kernel<DD><<<grid, kThreads, 0, st>>>(a, part)
+#define CALL(DD) return launch_early(select_kernel<DD>, grid, kThreads, 0, st, a, part)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
-  return cudaGetLastError();
 }
 
 }  // namespace q35c

@@ -55,6 +55,23 @@ __device__ __forceinline__ bool cache_row(const Cache& c, uint32_t seq, uint32_t
   return true;
 }
 
+// Launch with programmatic serialisation: the kernel may be scheduled while the one before it in the stream ends;
+// it begins with pdl_wait(), so it sees everything that one wrote.
+template <typename... P, typename... A>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, uint32_t threads, uint32_t smem, cudaStream_t st, A... args) {
+  cudaLaunchConfig_t c = {};
+  c.gridDim = grid;
+  c.blockDim = dim3(threads);
+  c.dynamicSmemBytes = smem;
+  c.stream = st;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  c.attrs = at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, kernel, static_cast<P>(args)...);
+}
+
 // One more at *p, and how many there were: what this CTA wrote before (a barrier puts its threads' writes
 // before the counting thread's) is seen by who counts after it.
 __device__ __forceinline__ uint32_t count_up(uint32_t* p) {
