@@ -1258,7 +1258,7 @@ int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_cache* kv, co
   if (!bounds) return QWEN35_ERR_INVALID_ARGUMENT;
   if ((r = bounds_ok(kv, bounds))) return r;
   if (!aligned16(q) || !blocks || ((uintptr_t)blocks % 4) || n_select == 0) return QWEN35_ERR_INVALID_ARGUMENT;
-  if (n_select > kv->capacity / bounds->block) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (n_select > q35c::kMaxSelect) return QWEN35_ERR_UNSUPPORTED;
   a.nblk = kv->capacity / bounds->block;
   const CacheNeed need = cache_need(a.c.Hkv, a.nblk, a.r.n_rows);
   if (scratch_bytes < need.total) return QWEN35_ERR_INVALID_ARGUMENT;
@@ -1291,8 +1291,8 @@ int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,
   if (!aligned16(q) || !aligned16(out)) return QWEN35_ERR_INVALID_ARGUMENT;
   if (gate && (!aligned16(gate) || gate_stride < a.c.D || gate_stride % 8)) return QWEN35_ERR_INVALID_ARGUMENT;
   if (blocks) {
-    if (((uintptr_t)blocks % 4) || !sel_block_ok(kv, block) || n_blocks == 0 || n_blocks > kv->capacity / block)
-      return QWEN35_ERR_INVALID_ARGUMENT;
+    if (((uintptr_t)blocks % 4) || !sel_block_ok(kv, block) || n_blocks == 0) return QWEN35_ERR_INVALID_ARGUMENT;
+    if (n_blocks > q35c::kMaxSelect) return QWEN35_ERR_UNSUPPORTED;
     a.blocks = blocks;
     a.n_blocks = n_blocks;
     a.blk_shift = log2_of(block);

@@ -13,6 +13,7 @@ constexpr uint32_t kMaxSeqs = 4096;       // sequences of a call
 constexpr uint32_t kMaxRows = 1u << 20;   // rows of an append or a read
 constexpr uint32_t kMaxQueries = 2048;    // rows of a selection or an attention
 constexpr uint32_t kMaxGroup = 16;        // q-heads of a kv-head
+constexpr uint32_t kMaxSelect = 65536;    // blocks of a list
 
 // The cache arrays of a batch: contiguous rows [n_seqs][capacity][Hkv][D], or pools of
 // num_blocks blocks of 2^bt_shift rows with tables [n_seqs][capacity >> bt_shift].

@@ -527,7 +527,7 @@ QWEN35_API int qwen35_cache_read(const qwen35_config* cfg, const qwen35_kv_cache
  * scores: where 32-bit arithmetic cannot tell two blocks apart, 64 bits decide. A score
  * that is not a number counts as -infinity. q bf16 [n_rows][num_heads][head_dim], in
  * the basis of the rows given to qwen35_cache_append. n_select: 1 to
- * capacity / block. Errors as qwen35_cache_append. */
+ * 65536, more than there are blocks or not. Errors as qwen35_cache_append. */
 QWEN35_API int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
                                     const qwen35_key_bounds* bounds, const qwen35_bf16* q, uint32_t n_select,
                                     uint32_t n_first, uint32_t n_last, int32_t* blocks, void* scratch,

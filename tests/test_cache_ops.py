@@ -134,8 +134,8 @@ def test_selection_and_attention_arguments():
         a = dict(q=x, blocks=_Fake(0xD000000, shape=(3, 1, n)), scratch=scr) | kw
         return B.qwen35_select_blocks(cfg, kv, rows, b, a["q"], a["blocks"], a["scratch"], stream=0)
 
-    assert select(16) == OK_BUT_NO_DEVICE
-    assert select(0) == BAD and select(17) == BAD  # 256 / 16 blocks
+    assert select(16) == OK_BUT_NO_DEVICE and select(17) == OK_BUT_NO_DEVICE  # more than the 256 / 16 blocks there are
+    assert select(0) == BAD and select(65536) == OK_BUT_NO_DEVICE and select(65537) == UNSUPPORTED
     assert select(4, q=_Fake(0xB000002)) == BAD and select(4, blocks=_Fake(0xD000002, shape=(3, 1, 4))) == BAD
     need = B.qwen35_cache_scratch_bytes(cfg, 1 << 20, 16, 3)  # the scores of 65536 blocks
     kv.capacity = 1 << 20
@@ -152,7 +152,8 @@ def test_selection_and_attention_arguments():
     assert attend(gate=x, gate_stride=60) == BAD and attend(gate=x, gate_stride=68) == BAD
     assert attend(gate=_Fake(0xB000008)) == BAD
     assert attend(q=_Fake(0xB000008)) == BAD and attend(out=_Fake(None)) == BAD
-    assert attend(blocks=_Fake(0xD000000, shape=(3, 1, 17)), block=16) == BAD
+    assert attend(blocks=_Fake(0xD000000, shape=(3, 1, 17)), block=16) == OK_BUT_NO_DEVICE
+    assert attend(blocks=_Fake(0xD000000, shape=(3, 1, 65537)), block=16) == UNSUPPORTED
     assert attend(blocks=_Fake(0xD000000, shape=(3, 1, 0)), block=16) == BAD
     assert attend(blocks=_Fake(0xD000002, shape=(3, 1, 4)), block=16) == BAD
     need = B.qwen35_cache_scratch_bytes(cfg, 256, 0, 3)

@@ -575,6 +575,14 @@ def test_selection(kw, n, first, last):
     check_choice(s, n, first, last)
 
 
+def test_lists_longer_than_the_cache_has_blocks():
+    s = Setup("tiny", TURBO8, [40, 1, 17], block=16)
+    s.set_bounds()
+    check_choice(s, 50)
+    lists = select(s, 50)
+    s.check(s.attend(blocks=torch.from_numpy(lists).cuda(), block=16), blocks=lists)
+
+
 @pytest.mark.parametrize("lens", [[400], [40000]])
 def test_selection_of_equal_scores_takes_the_lowest(lens):
     s = Setup("tiny", BF16, lens, block=16)
