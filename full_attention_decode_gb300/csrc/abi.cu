@@ -381,7 +381,8 @@ int qwen35_init(void) {
       cudaDeviceGetAttribute(&coop, cudaDevAttrCooperativeLaunch, dev) != cudaSuccess)
     return QWEN35_ERR_CUDA;
   if (major != 10 || minor != 3 || !coop) return QWEN35_ERR_CUDA;  // built for sm_103a only
-  if (decode_set_attributes() != cudaSuccess || q35c::attend_attributes() != cudaSuccess) return QWEN35_ERR_CUDA;
+  if (decode_set_attributes() != cudaSuccess || q35c::attend_attributes() != cudaSuccess ||
+      q35c::select_attributes() != cudaSuccess) return QWEN35_ERR_CUDA;
   g_num_sms[dev] = sms;
   return QWEN35_OK;
 }

@@ -261,7 +261,8 @@ __device__ __forceinline__ bool forced(const Select& a, uint32_t j, uint32_t n) 
 }
 
 constexpr uint32_t kSelWarps = kThreads / 32;
-constexpr uint32_t kMine = 16;   // scores a thread holds in registers: 4096 blocks a CTA
+constexpr uint32_t kMine = 8;      // scores a thread holds in registers: 2048 blocks a CTA
+constexpr uint32_t kKeys = 16384;  // and all of a CTA in shared memory
 constexpr uint32_t kClose = 256;  // blocks scored again side by side
 constexpr int kAhead = 4;         // blocks of a lane in flight
 constexpr uint32_t kInf = 0xff800000u;  // the key of +infinity
@@ -366,9 +367,20 @@ __device__ __forceinline__ float score_blocks(const Select& a, uint32_t r, uint3
   return most;
 }
 
-// Block j's score in 64 bits, by one warp (the same value in every lane).
-template <int D>
-__device__ double exact_score(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t j) {
+// A sum as two 32-bit numbers: TwoSum (Knuth) of hi and x, its error into lo.
+__device__ __forceinline__ void add_exactly(float& hi, float& lo, float x) {
+  const float t = __fadd_rn(hi, x), z = __fsub_rn(t, hi);
+  lo = __fadd_rn(lo, __fadd_rn(__fsub_rn(hi, __fsub_rn(t, z)), __fsub_rn(x, z)));
+  hi = t;
+}
+
+// Block j's score again, by one warp (the same in every lane): sum over the heads of q hi where q is not negative
+// and q lo where it is. A product of two bf16 values is exact in 32 bits unless it leaves their range.
+// WIDE: in 64 bits. Otherwise as a sum of two 32-bit numbers, within 2^-37 of the sum of absolute terms (at most 40
+// additions one after the other keep lo below 40 2^-24 of it, so each of lo's 40 roundings is below 40 2^-48), NaN
+// where a product leaves the range: this GPU's 64-bit pipe takes 60 cycles an instruction, and a score there 5 us.
+template <int D, bool WIDE>
+__device__ double score_again(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t j) {
   const uint32_t l = (threadIdx.x & 31) % (D / 8), group = a.H / a.c.Hkv;
   size_t row;
   if (!cache_row(a.c, seq, j << a.blk_shift, row)) return -INFINITY;
@@ -377,51 +389,93 @@ __device__ double exact_score(const Select& a, uint32_t r, uint32_t g, uint32_t 
   float lo[8], hi[8];
   unpack8(*reinterpret_cast<const uint4*>(b), lo);
   unpack8(*reinterpret_cast<const uint4*>(b + D), hi);
-  double s = 0.0;
-#pragma unroll 4
-  for (uint32_t h = 0; h < group; ++h) {  // sum_h max(q, 0) hi + min(q, 0) lo: the same products, each exact
-    float x[8];
-    unpack8(*reinterpret_cast<const uint4*>(q + (size_t)h * D), x);
+  if constexpr (WIDE) {
+    double c[8] = {};
+#pragma unroll 2
+    for (uint32_t h = 0; h < group; ++h) {
+      float x[8];
+      unpack8(*reinterpret_cast<const uint4*>(q + (size_t)h * D), x);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      // a product of two bf16 values is exact in 32 bits unless it leaves their range
-      const float p = x[e] * (x[e] < 0.f ? lo[e] : hi[e]);
-      s += fabsf(p) < 1e30f && (fabsf(p) > 1e-30f || x[e] == 0.f) ? (double)p
-                                                               : (double)x[e] * (double)(x[e] < 0.f ? lo[e] : hi[e]);
+      for (int e = 0; e < 8; ++e) c[e] += (double)x[e] * (double)(x[e] < 0.f ? lo[e] : hi[e]);
     }
-  }
+    double s = ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7]));
 #pragma unroll
-  for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-  return s > 1e300 ? 1e300 : s;  // an infinity stays below the blocks that always come first
+    for (int o = D / 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    return s != s ? -(double)INFINITY : s > 1e300 ? 1e300 : s;  // infinity stays below the blocks that always come first
+  } else {
+    float s[4] = {0.f, 0.f, 0.f, 0.f}, t[4] = {0.f, 0.f, 0.f, 0.f};
+    bool out = false;
+#pragma unroll 4
+    for (uint32_t h = 0; h < group; ++h) {
+      float x[8];
+      unpack8(*reinterpret_cast<const uint4*>(q + (size_t)h * D), x);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float y = x[e] < 0.f ? lo[e] : hi[e], p = __fmul_rn(x[e], y);
+        out |= !(fabsf(p) < 1e30f) || (fabsf(p) < 1e-30f && x[e] != 0.f && y != 0.f);
+        add_exactly(s[e & 3], t[e & 3], p);
+      }
+    }
+#pragma unroll
+    for (int e = 1; e < 4; ++e) {
+      add_exactly(s[0], t[0], s[e]);
+      t[0] = __fadd_rn(t[0], t[e]);
+    }
+#pragma unroll
+    for (int o = D / 16; o > 0; o >>= 1) {
+      const float s2 = __shfl_xor_sync(0xffffffffu, s[0], o), t2 = __shfl_xor_sync(0xffffffffu, t[0], o);
+      add_exactly(s[0], t[0], s2);
+      t[0] = __fadd_rn(t[0], t2);
+    }
+    return __any_sync(0xffffffffu, out) ? (double)NAN : (double)s[0] + (double)t[0];
+  }
 }
 
 // The scores of an item, spread over one CTA: warp w has blocks [w span, (w + 1) span), lane l every 32nd
-// of them from l, the first kMine of a thread in registers.
+// of them from l. Their order keys are in registers (the first kMine of a thread) for the counts of the
+// bisection, and in shared memory (the first kKeys of the item) for what runs once, whose code should be short;
+// others are read again.
 struct Scores {
   const float* s;
-  uint32_t n, base, end, mine;  // base: this thread's first block; end: of its warp; mine: how many it has
+  uint32_t* keys;         // a thread reads what it wrote
+  uint32_t n, base, end;  // base: this thread's first block; end: of its warp
   uint32_t key[kMine];
 
-  __device__ void take(const float* scores, uint32_t count) {
+  __device__ __forceinline__ uint32_t load(uint32_t j) const { return j < end ? order_key(__ldcg(s + j)) : 0u; }
+  __device__ void place(const float* scores, uint32_t count, uint32_t* shared) {
     const uint32_t span = (count + kThreads - 1) / kThreads * 32, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     s = scores;
+    keys = shared;
     n = count;
     end = (uint32_t)min((uint64_t)(warp + 1) * span, (uint64_t)count);
     base = warp * span + lane;
-    mine = base < end ? (end - base + 31) / 32 : 0;
-#pragma unroll
-    for (uint32_t i = 0; i < kMine; ++i) key[i] = i < mine ? order_key(__ldcg(s + base + 32 * i)) : 0u;
   }
-  // f(block, key) for this thread's blocks in order; every lane of a warp is called equally often (a key of
-  // 0 stands for no block: a score's key is above it).
-  template <typename F>
-  __device__ __forceinline__ void each(F&& f) const {
-    const uint32_t w0 = base - (threadIdx.x & 31);
-    const uint32_t rounds = w0 < end ? (end - w0 + 31) / 32 : 0;
+  __device__ void take() {
+#pragma unroll
+    for (uint32_t i = 0; i < kMine; ++i) key[i] = load(base + 32 * i);
 #pragma unroll
     for (uint32_t i = 0; i < kMine; ++i)
-      if (i < rounds) f(base + 32 * i, key[i]);
-    for (uint32_t i = kMine; i < rounds; ++i) f(base + 32 * i, i < mine ? order_key(__ldcg(s + base + 32 * i)) : 0u);
+      if (base + 32 * i < min(end, kKeys)) keys[base + 32 * i] = key[i];
+    for (uint32_t j = base + 32 * kMine; j < min(end, kKeys); j += 32) keys[j] = load(j);
+  }
+  // f(key) for this thread's blocks (a key of 0 stands for no block: a score's key is above it)
+  template <typename F>
+  __device__ __forceinline__ void count(F&& f) const {
+    const uint32_t w0 = base - (threadIdx.x & 31);
+#pragma unroll
+    for (uint32_t i = 0; i < kMine; ++i)
+      if (w0 + 32 * i < end) f(key[i]);
+    for (uint32_t j = base + 32 * kMine; j < end; j += 32) f(j < kKeys ? keys[j] : load(j));
+  }
+  // f(block, key) in order; every lane of a warp is called equally often
+  template <typename F>
+  __device__ __forceinline__ void each(F&& f) const {
+    const uint32_t lane = threadIdx.x & 31;
+#pragma unroll 1
+    for (uint32_t j0 = base - lane; j0 < end; j0 += 32) {
+      const uint32_t j = j0 + lane;
+      f(j, j >= end ? 0u : j < kKeys ? keys[j] : load(j));
+    }
   }
 };
 
@@ -438,40 +492,58 @@ __device__ __forceinline__ uint32_t cta_sum(uint32_t x, uint32_t* tmp, uint32_t&
   return x;
 }
 
-// The n_close blocks whose keys lie in [klo, khi], scored in 64 bits: the `need` largest of them (the lower
-// index of equal ones) get the score +infinity, the others -infinity.
+// The n_close blocks whose keys lie in [klo, khi], scored again: the `need` largest of them (the lower
+// index of equal ones) get the score +infinity, the others -infinity. Up to kClose of them are listed in close_j
+// and ranked side by side, by two 32-bit numbers each, and where those leave the last that is in within 2^-36 most
+// of the first that is out, by 64-bit ones.
 template <int D>
-__device__ __noinline__ void decide(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item,
-                                    uint32_t klo, uint32_t khi, uint32_t n_close, uint32_t need, uint32_t* tmp,
-                                    const uint32_t* close_j) {
-  __shared__ double close_t[kClose];
+__device__ __forceinline__ void decide(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item,
+                                       uint32_t klo, uint32_t khi, uint32_t n_close, uint32_t need, float most,
+                                       uint32_t* tmp, const uint32_t* close_j) {
+  __shared__ double close_t[kClose], s_edge[2];
+  __shared__ bool s_nan;
   const uint32_t tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   float* s = a.scores + item * a.nblk;
+  if (n_close <= kClose) {
+    if (tid == 0) s_nan = false;
+    __syncthreads();
+#pragma unroll 1
+    for (int wide = 0; wide < 2; ++wide) {
+      for (uint32_t i = warp; i < n_close; i += kSelWarps) {
+        const uint32_t j = close_j[i];
+        double x = INFINITY;
+        if (!forced(a, j, n)) x = wide ? score_again<D, true>(a, r, g, seq, j) : score_again<D, false>(a, r, g, seq, j);
+        if (lane == 0) close_t[i] = x;
+        if (lane == 0 && x != x) s_nan = true;
+      }
+      __syncthreads();
+      uint32_t rank = 0;
+      if (tid < n_close) {  // as integers: the order of the bits
+        const unsigned long long x = order_key(close_t[tid]);
+        for (uint32_t i = 0; i < n_close; ++i) {
+          const unsigned long long y = order_key(close_t[i]);
+          rank += y > x || (y == x && close_j[i] < close_j[tid]);
+        }
+        if (rank == need - 1) s_edge[0] = close_t[tid];
+        if (rank == need) s_edge[1] = close_t[tid];
+      }
+      __syncthreads();
+      if (wide || (!s_nan && s_edge[0] - s_edge[1] > (double)most * 0x1p-36)) {
+        if (tid < n_close) __stcg(s + close_j[tid], rank < need ? INFINITY : -INFINITY);
+        break;
+      }
+    }
+    __syncthreads();
+    return;
+  }
   const auto close = [&](uint32_t j) {
     if (j >= n) return false;
     const uint32_t k = order_key(__ldcg(s + j));
     return k >= klo && k <= khi;
   };
   const auto score = [&](uint32_t j) {
-    const double x = forced(a, j, n) ? (double)INFINITY : exact_score<D>(a, r, g, seq, j);
-    return x != x ? -(double)INFINITY : x;
+    return forced(a, j, n) ? (double)INFINITY : score_again<D, true>(a, r, g, seq, j);
   };
-  if (n_close <= kClose) {  // listed in close_j: each ranked among all
-    for (uint32_t i = warp; i < n_close; i += kSelWarps) {
-      const double x = score(close_j[i]);
-      if (lane == 0) close_t[i] = x;
-    }
-    __syncthreads();
-    if (tid < n_close) {
-      uint32_t rank = 0;
-      const double x = close_t[tid];
-      for (uint32_t i = 0; i < n_close; ++i)
-        rank += close_t[i] > x || (close_t[i] == x && close_j[i] < close_j[tid]);
-      __stcg(s + close_j[tid], rank < need ? INFINITY : -INFINITY);
-    }
-    __syncthreads();
-    return;
-  }
   // many equal or unbounded scores: all of them in 64 bits, then bisection of those bits
   double* t = a.exact + item * a.nblk;
   uint32_t turn = 0;
@@ -524,20 +596,22 @@ __device__ __noinline__ void decide(const Select& a, uint32_t r, uint32_t g, uin
 // scores' bits: a count over the CTA a step, until a step leaves exactly K.
 template <int D>
 __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item, float most) {
+  extern __shared__ uint32_t keys[];
   __shared__ uint32_t tmp[2 * kSelWarps], range[2 * kSelWarps], close_j[kClose];
   const uint32_t K = a.n_select, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int32_t* out = a.blocks + item * K;
   uint32_t turn = 0;
   Scores sc;
-  sc.take(a.scores + item * a.nblk, n);
+  sc.place(a.scores + item * a.nblk, n, keys);
+  sc.take();
   const auto count = [&](uint32_t from) {  // keys >= from
     uint32_t c = 0;
-    sc.each([&](uint32_t, uint32_t k) { c += k >= from; });
+    sc.count([&](uint32_t k) { c += k >= from; });
     return cta_sum(c, tmp, turn);
   };
   // the finite scores' range: most of a bisection of all 32 bits would only find it
   uint32_t low = 0xffffffffu, high = 0, n_forced = 0;
-  sc.each([&](uint32_t, uint32_t k) {
+  sc.count([&](uint32_t k) {
     low = k ? min(low, k) : low;
     high = k < kInf ? max(high, k) : high;
     n_forced += k >= kInf;
@@ -571,9 +645,7 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     }
   }
   uint32_t kth = 0xffffffffu;  // the smallest key from low up: the K-th largest's
-  sc.each([&](uint32_t, uint32_t k) {
-    if (k >= low) kth = min(kth, k);
-  });
+  sc.count([&](uint32_t k) { kth = k >= low ? min(kth, k) : kth; });
   kth = __reduce_min_sync(0xffffffffu, kth);
   __syncthreads();
   if (lane == 0) range[warp] = kth;
@@ -586,7 +658,7 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     khi = order_key(isinf(T) ? T : __fadd_ru(T, 2.f * E));
   }
   uint32_t c1 = 0, c2 = 0;
-  sc.each([&](uint32_t, uint32_t k) {
+  sc.count([&](uint32_t k) {
     c1 += k > khi;
     c2 += k >= klo && k <= khi;
   });
@@ -601,13 +673,13 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
       });
       __syncthreads();
     }
-    decide<D>(a, r, g, seq, n, item, klo, khi, n_close, need, tmp, close_j);
-    sc.take(a.scores + item * a.nblk, n);
+    decide<D>(a, r, g, seq, n, item, klo, khi, n_close, need, most, tmp, close_j);
+    sc.take();
     cut = min(khi, kInf - 1) + 1;
   }
   // in index order: a warp's blocks are neighbours, so places come from ballots and the counts of the warps before
   uint32_t n_in = 0;
-  sc.each([&](uint32_t, uint32_t k) { n_in += k >= cut; });
+  sc.count([&](uint32_t k) { n_in += k >= cut; });
   n_in = __reduce_add_sync(0xffffffffu, n_in);
   __syncthreads();
   if (lane == 0) tmp[warp] = n_in;
@@ -701,6 +773,14 @@ cudaError_t read(const Read& a, cudaStream_t st) {
 #undef CALL
 }
 
+cudaError_t select_attributes() {
+  const auto allow = [](auto kernel) {
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKeys * 4) == cudaSuccess;
+  };
+  return allow(select_kernel<64>) && allow(select_kernel<128>) && allow(select_kernel<256>) ? cudaSuccess
+                                                                                            : cudaGetLastError();
+}
+
 cudaError_t select(const Select& a, cudaStream_t st) {
   // Blocks of a CTA: whole passes of the teams, and no more CTAs than a.ctas if the sequences were all as long as
   // the capacity (parts of one size, so that a long sequence is not the last to finish)
@@ -708,7 +788,8 @@ cudaError_t select(const Select& a, cudaStream_t st) {
   const uint32_t parts = std::max(1u, std::min((a.nblk + pass - 1) / pass, a.ctas / items));
   const uint32_t part = ((a.nblk + parts - 1) / parts + pass - 1) / pass * pass;
   const dim3 grid((a.nblk + part - 1) / part, a.c.Hkv, a.r.n_rows);
-#define CALL(DD) return launch_early(select_kernel<DD>, grid, kThreads, 0, st, a, part)
+  const uint32_t smem = std::min(a.nblk, kKeys) * 4;
+#define CALL(DD) return launch_early(select_kernel<DD>, grid, kThreads, smem, st, a, part)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
 }

@@ -69,6 +69,7 @@ struct Select {
   int* status;
 };
 cudaError_t select(const Select& a, cudaStream_t st);
+cudaError_t select_attributes();  // once per device, before the first select
 constexpr uint32_t kMaxItems = kMaxQueries * 8;  // of 8 kv-heads
 constexpr uint32_t kMaxParts = 2048;   // parts of all items: at most one an item, or this many
 

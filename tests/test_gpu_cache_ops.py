@@ -567,7 +567,7 @@ def check_choice(s, n, first=1, last=1):
                                   (dict(heads="4b", fmt=TURBO8, lens=[1500, 90], block=32, page=64), 16),
                                   (dict(heads="tiny_alt", fmt=BF16, lens=[700, 650], rows=[6, 2], tail=2, lead=1), 5),
                                   (dict(heads="wide", fmt=BF16, lens=[2100], block=16), 131),
-                                  (dict(heads="tiny", fmt=BF16, lens=[70000], block=16), 33),
+                                  (dict(heads="tiny", fmt=BF16, lens=[70000, 300000], block=16), 33),
                                   (dict(heads="eight", fmt=TURBO8, lens=[9000, 10], block=16, page=32), 33)])
 def test_selection(kw, n, first, last):
     s = Setup(**kw)
@@ -607,6 +607,23 @@ def test_selection_tells_scores_apart_that_32_bits_cannot():
     s.lo_hi.copy_(b.to(torch.bfloat16).cuda())
     check_choice(s, 20)
     check_choice(s, 21, 0, 0)
+
+
+@pytest.mark.parametrize("gap", [2.0 ** -10, 2.0 ** -30, 2.0 ** -60, 0.0])
+def test_selection_tells_close_scores_apart(gap):
+    """Blocks whose scores differ by `gap` of a score of 2^8 or so (0: equal), in falling order of index."""
+    s = Setup("tiny", BF16, [1600], block=16)
+    s.set_bounds()
+    rows = s.lo_hi[:100].clone()
+    rows[20:40] = rows[20]
+    rows[:, :, :, 60:] = 0
+    s.q[0, :, 60:] = 0
+    s.q[0, 1, 61] = 1.0
+    for i in range(20):  # one more product, too small for 32 bits beside the others
+        rows[20 + i, 0, 1, 61] = gap * 2.0 ** 8 * i
+    s.lo_hi[:100] = rows
+    for n in (5, 17, 30, 60):
+        check_choice(s, n, 0, 0)
 
 
 def test_selection_with_infinities_and_nans():
