@@ -879,7 +879,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
   }
   // the line of all items: prefix sums of the rows' tiles with kLead before each item's, or (whole) of ones.
   // kLead stands for what an item's beginning and end cost a CTA that has another item too: about two
-  // rounds of its warps (32 sequences of 1K-16K: ... us, without it ...).
+  // rounds of its warps (32 sequences of 1K-16K: 128 us, without it 134; 128K tokens in Turbo8 66 and 71).
   constexpr uint32_t kLead = 2 * kWarps;
   uint32_t most = 0, items = 0;
   uint32_t total = 0, per = 0;
@@ -918,8 +918,9 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
       per = 1;
       break;
     }
-    // An equal stretch for every CTA, whole rounds of the warps. Few items of up to kShort rounds go to a CTA
-    // each instead: a split's hand-over and join take longer (4 us).
+    // An equal stretch for every CTA, whole rounds of the warps, or at least kLeast tiles where there is less
+    // (512 tokens of 4 heads on 64 CTAs: 9.9 us, on 16 CTAs of a whole round 11.6). Few items of up to kShort rounds go
+    // to a CTA each instead: a split's hand-over and join take 4 us, a round of one CTA 1.5 to 2.5.
     constexpr uint32_t kShort = 2, kLeast = 2;
     most = __reduce_max_sync(0xffffffffu, most);
     items = __reduce_add_sync(0xffffffffu, items);

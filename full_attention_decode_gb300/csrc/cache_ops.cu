@@ -264,7 +264,8 @@ constexpr uint32_t kSelWarps = kThreads / 32;
 constexpr uint32_t kMine = 8;      // scores a thread holds in registers: 2048 blocks a CTA
 constexpr uint32_t kKeys = 16384;  // and all of a CTA in shared memory
 constexpr uint32_t kClose = 256;  // blocks scored again side by side
-constexpr int kAhead = 4;         // blocks of a lane in flight
+constexpr uint32_t kAhead = 8;     // blocks of a lane in flight
+constexpr uint32_t kRing = kAhead * 2 * kThreads * 16;  // their bytes
 constexpr uint32_t kInf = 0xff800000u;  // the key of +infinity
 
 // Sums over the group's heads of q's positive and negative parts, eight dims a lane.
@@ -288,71 +289,71 @@ __device__ __forceinline__ void signed_sums(const Select& a, uint32_t r, uint32_
 
 // Scores of blocks [j0, j1): s_j = sum_d Q+_d hi_jd + Q-_d lo_jd, with Q+ and Q- the sums over the
 // group's heads of q's positive and negative parts: the sum over the heads of the largest q.k that a key
-// inside the bounds could have. LPR lanes a block; the next kAhead blocks of a lane are in flight while
-// the last ones are summed (the bytes of the bounds bound it). Returns (in every
+// inside the bounds could have. The bytes of the bounds bound it: a team of LPR lanes takes a block, each lane
+// copies its own 32 bytes of kAhead blocks ahead (64 KB a CTA in flight, two CTAs an SM: 25.5 us
+// for 16 sequences of 16K-64K tokens; four blocks in registers, 32 KB: 26.5 us; three CTAs of 80 registers: 31.6 us) and waits for nobody else. Returns (in every
 // thread) sum_d Q+_d max_j|hi_jd| + |Q-_d| max_j|lo_jd|, which bounds every block's sum
 // of absolute terms; infinity where an infinity or NaN leaves no bound.
 template <int D>
 __device__ __forceinline__ float score_blocks(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n,
-                                              uint32_t j0, uint32_t j1, float* out, float* tmp) {
+                                              uint32_t j0, uint32_t j1, float* out, uint4* ring, float* tmp) {
   constexpr int LPR = D / 8, PER = kThreads / LPR;
   const uint32_t l = threadIdx.x % LPR, team = threadIdx.x / LPR;
-  uint4 lo4[kAhead], hi4[kAhead];
-  uint32_t here = 0;  // bit u: block jb + u PER + team has bounds
-  const auto fetch = [&](uint32_t jb) {
-    here = 0;
-#pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      const uint32_t j = jb + u * PER + team;
+  const uint32_t mine = j0 + team < j1 ? (j1 - j0 - team + PER - 1) / PER : 0;  // blocks of this team
+  const uint32_t all = (j1 - j0 + PER - 1) / PER;                               // and of the one with the most
+  unsigned long long found = 0;  // where a block's bounds are, plus one: LPR blocks looked up at a time
+  uint32_t have = 0;             // bit k % kAhead: the block there has bounds
+  const auto fetch = [&](uint32_t k) {
+    if (k % LPR == 0) {
       size_t row = 0;
-      lo4[u] = hi4[u] = make_uint4(0u, 0u, 0u, 0u);
-      if (j < j1) {
-        if (cache_row(a.c, seq, j << a.blk_shift, row)) {
-          here |= 1u << u;
-          const uint16_t* b = a.bounds + (((row >> a.blk_shift) * a.c.Hkv + g) * 2) * D + 8 * l;
-          lo4[u] = *reinterpret_cast<const uint4*>(b);
-          hi4[u] = *reinterpret_cast<const uint4*>(b + D);
-        } else {
-          set_status(a.status, kStatusRange);
-        }
+      found = 0;
+      if (k + l < mine) {
+        if (cache_row(a.c, seq, (j0 + (k + l) * PER + team) << a.blk_shift, row)) found = (row >> a.blk_shift) + 1;
+        else set_status(a.status, kStatusRange);
       }
     }
+    const unsigned long long at = __shfl_sync(0xffffffffu, found, k % LPR, LPR);
+    have &= ~(1u << (k % kAhead));
+    if (at) {
+      have |= 1u << (k % kAhead);
+      const uint16_t* b = a.bounds + (((at - 1) * a.c.Hkv + g) * 2) * D + 8 * l;
+      const uint32_t to = smem_addr(ring + (k % kAhead) * 2 * kThreads + threadIdx.x);
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(b) : "memory");
+      asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to + kThreads * 16), "l"(b + D) : "memory");
+    }
+    asm volatile("cp.async.commit_group;" ::: "memory");
   };
   float up[8], dn[8], mh[8], ml[8];
-  fetch(j0);
+#pragma unroll 1
+  for (uint32_t k = 0; k < kAhead; ++k) fetch(k);
   signed_sums<D>(a, r, g, l, up, dn);
 #pragma unroll
   for (int e = 0; e < 8; ++e) mh[e] = ml[e] = 0.f;
   bool wild = false;
 #pragma unroll 1
-  for (uint32_t jb = j0; jb < j1; jb += PER * kAhead) {
-    float s[kAhead];
-    const uint32_t had = here;
+  for (uint32_t k = 0; k < all; ++k) {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kAhead - 1) : "memory");
+    const uint4* from = ring + (k % kAhead) * 2 * kThreads + threadIdx.x;
+    const bool in = have >> (k % kAhead) & 1;
+    float lo[8], hi[8], c[4] = {0.f, 0.f, 0.f, 0.f};  // four short chains: less rounding, no waiting
+    unpack8(in ? from[0] : make_uint4(0u, 0u, 0u, 0u), lo);
+    unpack8(in ? from[kThreads] : make_uint4(0u, 0u, 0u, 0u), hi);
+    fetch(k + kAhead);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-      float lo[8], hi[8], c[4] = {0.f, 0.f, 0.f, 0.f};  // four short chains: less rounding, no waiting
-      unpack8(lo4[u], lo);
-      unpack8(hi4[u], hi);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        c[e & 1] = fmaf(up[e], hi[e], c[e & 1]);
-        c[2 + (e & 1)] = fmaf(dn[e], lo[e], c[2 + (e & 1)]);
-        mh[e] = fmaxf(mh[e], fabsf(hi[e]));
-        ml[e] = fmaxf(ml[e], fabsf(lo[e]));
-      }
-      s[u] = (c[0] + c[1]) + (c[2] + c[3]);
+    for (int e = 0; e < 8; ++e) {
+      c[e & 1] = fmaf(up[e], hi[e], c[e & 1]);
+      c[2 + (e & 1)] = fmaf(dn[e], lo[e], c[2 + (e & 1)]);
+      mh[e] = fmaxf(mh[e], fabsf(hi[e]));
+      ml[e] = fmaxf(ml[e], fabsf(lo[e]));
     }
-    if (jb + PER * kAhead < j1) fetch(jb + PER * kAhead);
+    float s = (c[0] + c[1]) + (c[2] + c[3]);
 #pragma unroll
-    for (int u = 0; u < kAhead; ++u) {
-#pragma unroll
-      for (int o = LPR / 2; o > 0; o >>= 1) s[u] += __shfl_xor_sync(0xffffffffu, s[u], o);
-      const uint32_t j = jb + u * PER + team;
-      const bool in = had >> u & 1;
-      if (in) wild |= !(fabsf(s[u]) < INFINITY);
-      if (j < j1 && l == 0) __stcg(out + j, forced(a, j, n) ? INFINITY : in ? s[u] : -INFINITY);
-    }
+    for (int o = LPR / 2; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const uint32_t j = j0 + k * PER + team;
+    if (in) wild |= !(fabsf(s) < INFINITY);
+    if (k < mine && l == 0) __stcg(out + j, forced(a, j, n) ? INFINITY : in ? s : -INFINITY);
   }
+  asm volatile("cp.async.wait_group 0;" ::: "memory");
   float most = 0.f;
 #pragma unroll
   for (int e = 0; e < 8; ++e) most += up[e] * mh[e] - dn[e] * ml[e];
@@ -596,7 +597,7 @@ __device__ __forceinline__ void decide(const Select& a, uint32_t r, uint32_t g, 
 // scores' bits: a count over the CTA a step, until a step leaves exactly K.
 template <int D>
 __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item, float most) {
-  extern __shared__ uint32_t keys[];
+  extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t tmp[2 * kSelWarps], range[2 * kSelWarps], close_j[kClose];
   const uint32_t K = a.n_select, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int32_t* out = a.blocks + item * K;
@@ -697,6 +698,7 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
 // CTA x of a (row, kv-head) scores the x-th `part` of its blocks; the last of them to finish chooses.
 template <int D>
 __global__ void __launch_bounds__(kThreads, 2) select_kernel(const __grid_constant__ Select a, uint32_t part) {
+  extern __shared__ __align__(16) uint32_t keys[];  // the bounds in flight, then choose()'s keys
   __shared__ float tmp[kSelWarps];
   __shared__ uint32_t s_last;
   pdl_wait();
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const __grid_consta
   if (blockIdx.x >= parts) return;
   float* most = a.most + item * gridDim.x;
   float m = score_blocks<D>(a, r, g, seq, n, blockIdx.x * part, min(n, (blockIdx.x + 1) * part),
-                            a.scores + item * a.nblk, tmp);
+                            a.scores + item * a.nblk, reinterpret_cast<uint4*>(keys), tmp);
   __syncthreads();
   if (parts > 1) {
     if (tid == 0) {
@@ -775,7 +777,8 @@ cudaError_t read(const Read& a, cudaStream_t st) {
 
 cudaError_t select_attributes() {
   const auto allow = [](auto kernel) {
-    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kKeys * 4) == cudaSuccess;
+    return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                (int)std::max(kKeys * 4, kRing)) == cudaSuccess;
   };
   return allow(select_kernel<64>) && allow(select_kernel<128>) && allow(select_kernel<256>) ? cudaSuccess
                                                                                             : cudaGetLastError();
@@ -784,11 +787,11 @@ cudaError_t select_attributes() {
 cudaError_t select(const Select& a, cudaStream_t st) {
   // Blocks of a CTA: whole passes of the teams, and no more CTAs than a.ctas if the sequences were all as long as
   // the capacity (parts of one size, so that a long sequence is not the last to finish)
-  const uint32_t pass = kThreads / (a.c.D / 8) * kAhead, items = a.r.n_rows * a.c.Hkv;
+  const uint32_t pass = kThreads / (a.c.D / 8) * 4, items = a.r.n_rows * a.c.Hkv;
   const uint32_t parts = std::max(1u, std::min((a.nblk + pass - 1) / pass, a.ctas / items));
   const uint32_t part = ((a.nblk + parts - 1) / parts + pass - 1) / pass * pass;
   const dim3 grid((a.nblk + part - 1) / part, a.c.Hkv, a.r.n_rows);
-  const uint32_t smem = std::min(a.nblk, kKeys) * 4;
+  const uint32_t smem = std::max(std::min(a.nblk, kKeys) * 4, kRing);
 #define CALL(DD) return launch_early(select_kernel<DD>, grid, kThreads, smem, st, a, part)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
