@@ -9,6 +9,8 @@
 
 namespace q35c {
 
+constexpr int kStatusInvalid = 1;  // QWEN35_ERR_INVALID_ARGUMENT
+
 enum RowKind { kRowOk = 0, kRowSkip = 1, kRowBad = 2 };
 
 // Row r's sequence and position, which of the sequence's rows it is and how many are left from

@@ -10,7 +10,6 @@
 
 namespace q35 {
 
-constexpr int kStatusInvalid = 1;  // QWEN35_ERR_INVALID_ARGUMENT
 constexpr int kStatusTimeout = 5;  // QWEN35_ERR_DEVICE_TIMEOUT
 constexpr int kStatusRange = 6;    // QWEN35_ERR_DEVICE_RANGE
 constexpr uint64_t kWaitNs = 1000000000ull;  // a bounded wait gives up after 1 s (the default)
