@@ -443,6 +443,59 @@ def test_a_nan_in_a_key_spoils_only_rows_that_see_it(fmt):
     assert np.isfinite(got[[0, 1, 4, 5, 6, 7]]).all() and np.isnan(got[[2, 3]]).any(axis=(1, 2)).all()
 
 
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("rows", [False, True])
+def test_attention_of_many_rows(fmt, rows):
+    """More rows than threads of a CTA, of lengths 1 to 40, sequences without a row among them."""
+    n = 700
+    kw = dict(rows=[(b * 5) % 4 for b in range(n)]) if rows else {}
+    s = Setup("tiny", fmt, [4 + (b * 7) % 37 for b in range(n)], page=8, **kw)
+    s.check(s.attend())
+    assert s.status() == 0
+
+
+def test_attention_of_the_most_rows():
+    s = Setup("tiny", BF16, [2 + b % 3 for b in range(2048)])
+    s.check(s.attend())
+    t = Setup("tiny", BF16, [2 + b % 3 for b in range(4096)], rows=[b % 2 for b in range(4096)])
+    t.check(t.attend())
+    assert s.status() == 0 and t.status() == 0
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_rows_that_run_out_of_the_cache(fmt):
+    """The last two of four rows lie behind the capacity: reported, left as they were, the others right."""
+    s = Setup("tiny_alt", fmt, [48, 20], rows=[4, 3])
+    assert s.cap == 48
+    s.pos[0] = 46
+    out = f64(s.attend())
+    assert s.status() == B.QWEN35_ERR_DEVICE_RANGE
+    assert np.isnan(out[[2, 3]]).all()
+    for row, p in ((0, 46), (1, 47)):
+        ref, vmax = s.reference(row, 0, p)
+        assert np.linalg.norm(out[row] - ref) <= 2.0 ** -7 * np.linalg.norm(ref) + 2.0 ** -10 * vmax.max() * np.sqrt(ref.size)
+    assert np.isfinite(out[[4, 5, 6]]).all()
+
+
+def test_turbo8_values_of_very_different_sizes():
+    """V rows from 2^-40 to 2^40 of one another, each format's step relative to its own group."""
+    s = Setup("tiny", TURBO8, [200, 37], page=16, seed=3)
+    rng = np.random.default_rng(1)
+    scale = np.exp2(rng.integers(-40, 41, size=(s.total, 1)))
+    sc = O.bf16_to_f64(s.t["vs"].cpu().numpy().view(np.uint16)) * scale
+    s.t["vs"].copy_(torch.from_numpy(O.bf16_bits(sc).view(np.int16)))
+    s.stands["v"] = s.stands["v"] * scale[:, :, None]
+    s.check(s.attend())
+    small = Setup("tiny", TURBO8, [100], seed=4)  # all of them tiny, and all of them large
+    base = small.t["vs"].clone()
+    stands = small.stands["v"].copy()
+    for e in (-50, 50):
+        sc = O.bf16_to_f64(base.cpu().numpy().view(np.uint16)) * 2.0 ** e
+        small.t["vs"].copy_(torch.from_numpy(O.bf16_bits(sc).view(np.int16)))
+        small.stands["v"] = stands * 2.0 ** e
+        small.check(small.attend())
+
+
 @pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "odd", "eight"])
 @pytest.mark.parametrize("fmt", [BF16, TURBO8])
 def test_what_later_rows_of_a_call_hold_is_not_seen(fmt, heads):
