@@ -1233,6 +1233,7 @@ int qwen35_cache_append(const qwen35_config* cfg, const qwen35_kv_cache* kv, con
   if (num_sms() <= 0) return QWEN35_ERR_CUDA;
   a.k = k;
   a.v = v;
+  a.wide = (((uintptr_t)k | (uintptr_t)v) % 32) == 0;
   a.status = static_cast<int*>(scratch);
   return cu(q35c::append(a, (cudaStream_t)stream));
 }
@@ -1246,6 +1247,7 @@ int qwen35_cache_read(const qwen35_config* cfg, const qwen35_kv_cache* kv, const
   if (num_sms() <= 0) return QWEN35_ERR_CUDA;
   a.k = k;
   a.v = v;
+  a.wide = (((uintptr_t)k | (uintptr_t)v) % 32) == 0;
   a.status = static_cast<int*>(scratch);
   return cu(q35c::read(a, (cudaStream_t)stream));
 }

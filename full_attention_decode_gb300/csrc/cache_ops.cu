@@ -9,6 +9,7 @@ using namespace q35;
 namespace {
 
 constexpr uint32_t kThreads = 256;
+constexpr uint32_t kWideShift = 4;  // selection blocks of more than 2^this rows: a CTA folds one
 
 // ------------------------------------------------------------------ rows in and out
 
@@ -45,56 +46,56 @@ __device__ __forceinline__ void append_plain(const Append& a, uint32_t block) {
 }
 
 // A Turbo8 row: four lanes an item and K or V, D / 4 elements a lane (wht_quad's layout).
+struct QuadItem {
+  size_t item;
+  uint32_t l;
+  bool is_v;
+};
+__device__ __forceinline__ QuadItem quad_item(uint32_t block) {  // a warp's eight fours: eight items' K or V
+  const size_t team = (block * (size_t)kThreads + threadIdx.x) / 4;
+  return {team / 16 * 8 + team % 8, threadIdx.x & 3, (team & 8) != 0};
+}
+
 template <int D>
 __device__ __forceinline__ void append_turbo8(const Append& a, uint32_t block) {
-  constexpr int P = D / 32;  // pieces of eight elements
-  const size_t team = (block * (size_t)kThreads + threadIdx.x) / 4;
-  const uint32_t lane = threadIdx.x & 31, l = lane & 3;
-  const size_t item = team / 16 * 8 + team % 8;  // a warp's eight teams: eight items' K or V
-  const bool is_v = team & 8;
-  const Item w = find_item(a.r, a.c, item, a.status);
-  const uint16_t* src = (is_v ? a.v : a.k) + item * D + 8 * l;
+  constexpr int P = D / 64;  // pieces of sixteen elements
+  const QuadItem t = quad_item(block);
+  const uint32_t lane = threadIdx.x & 31;
+  const Item w = find_item(a.r, a.c, t.item, a.status);
+  const uint16_t* src = (t.is_v ? a.v : a.k) + t.item * D + 16 * t.l;
   float2 x[D / 8];
 #pragma unroll
   for (int i = 0; i < P; ++i) {
-    uint4 u = make_uint4(0u, 0u, 0u, 0u);
-    if (w.ok) u = *reinterpret_cast<const uint4*>(src + 32 * i);
-    unpack8(u, reinterpret_cast<float*>(x + 4 * i));
+    uint32_t u[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
+    if (w.ok) load32(src + 64 * i, a.wide, u);
+#pragma unroll
+    for (int k = 0; k < 8; ++k) x[8 * i + k] = make_float2(bf16lo(u[k]), bf16hi(u[k]));
   }
   wht_quad<D>(x, lane);
-  uint8_t* to = (is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 8 * l;
-  uint16_t* sc = (is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16);
-  uint32_t scales[P];  // lane 0: group 2 i's, then 2 i + 1's, which lanes 2 and 3 have
+  uint8_t* to = (t.is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 16 * t.l;
+  uint32_t* sc = reinterpret_cast<uint32_t*>((t.is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16));
 #pragma unroll
   for (int i = 0; i < P; ++i) {
     uint16_t s;
-    uint32_t r[4];
+    uint32_t r[8];
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const __nv_bfloat162 p = __float22bfloat162_rn(x[4 * i + k]);
-      r[k] = *reinterpret_cast<const uint32_t*>(&p);
+    for (int k = 0; k < 8; ++k) {
+      const __nv_bfloat162 q = __float22bfloat162_rn(x[8 * i + k]);
+      r[k] = *reinterpret_cast<const uint32_t*>(&q);
     }
-    const uint2 codes = quant8(r, s);
-    if (w.ok) *reinterpret_cast<uint2*>(to + 32 * i) = codes;
-    scales[i] = s;
-  }
-#pragma unroll
-  for (int i = 0; i < P; ++i) scales[i] |= __shfl_xor_sync(0xffffffffu, scales[i], 2) << 16;
-  if (w.ok && l == 0) {
-    if constexpr (P >= 4) {
-#pragma unroll
-      for (int i = 0; i < P; i += 4)
-        reinterpret_cast<uint4*>(sc)[i / 4] = make_uint4(scales[i], scales[i + 1], scales[i + 2], scales[i + 3]);
-    } else {
-      *reinterpret_cast<uint2*>(sc) = make_uint2(scales[0], scales[1]);
-    }
+    const uint4 codes = quant16(r, s);
+    if (w.ok) *reinterpret_cast<uint4*>(to + 64 * i) = codes;
+    // two groups' scales as one word
+    const uint32_t two = s | (uint32_t)__shfl_xor_sync(0xffffffffu, (uint32_t)s, 1) << 16;
+    if (w.ok && t.l % 2 == 0) sc[2 * i + t.l / 2] = two;
   }
 }
 
 // The key bounds of spans of rows. A run is the call's rows of one block of one sequence; who has the span with
 // its first row folds it, starting anew if that is the block's first token. WIDE: a CTA a (span, kv-head), its
-// teams of D / 8 lanes taking a run's rows in turn; otherwise (blocks of up to 64 tokens) a team alone,
-// sixteen rows in flight: at 32768 rows of 4 heads and blocks of 16, a CTA for each would only wait.
+// teams of D / 8 lanes taking a run's rows in turn; otherwise (blocks of 16 tokens) a team alone,
+// sixteen rows in flight (three prompts of 400 to 1500 rows, blocks of 64: 9.5 us wide, 11.0 by teams; 32768 rows,
+// blocks of 16: 168 us wide, 68 by teams).
 template <int D, bool WIDE>
 __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, uint32_t g, uint32_t span_rows) {
   constexpr int LPR = D / 8, TEAMS = WIDE ? kThreads / LPR : 1;
@@ -165,23 +166,21 @@ __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, ui
   }
 }
 
-// CTAs [0, row_ctas) write rows, the others bring the bounds up to date.
+// CTAs [0, bound_ctas) bring the bounds up to date, the others write rows: a bounds' CTA has the longest chain of loads,
+// so it starts first.
 template <int D, bool T8>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Append a, uint32_t row_ctas,
+__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Append a, uint32_t bound_ctas,
                                                           uint32_t span_rows) {
   pdl_wait();
   pdl_launch();
-  if (blockIdx.x < row_ctas) {
-    if constexpr (T8) append_turbo8<D>(a, blockIdx.x);
-    else append_plain<D>(a, blockIdx.x);
+  if (blockIdx.x >= bound_ctas) {
+    if constexpr (T8) append_turbo8<D>(a, blockIdx.x - bound_ctas);
+    else append_plain<D>(a, blockIdx.x - bound_ctas);
+  } else if (a.blk_shift > kWideShift) {
+    append_bounds<D, true>(a, blockIdx.x / a.c.Hkv, blockIdx.x % a.c.Hkv, span_rows);
   } else {
-    const uint32_t i = blockIdx.x - row_ctas;
-    if (a.blk_shift > 6) {
-      append_bounds<D, true>(a, i / a.c.Hkv, i % a.c.Hkv, span_rows);
-    } else {
-      const uint32_t team = i * (kThreads / (D / 8)) + threadIdx.x / (D / 8);
-      append_bounds<D, false>(a, team / a.c.Hkv, team % a.c.Hkv, span_rows);
-    }
+    const uint32_t team = blockIdx.x * (kThreads / (D / 8)) + threadIdx.x / (D / 8);
+    append_bounds<D, false>(a, team / a.c.Hkv, team % a.c.Hkv, span_rows);
   }
 }
 
@@ -190,33 +189,33 @@ __global__ void __launch_bounds__(kThreads) read_kernel(const __grid_constant__ 
   pdl_wait();
   pdl_launch();
   if constexpr (T8) {
-    constexpr int P = D / 32;
-    const size_t team = (blockIdx.x * (size_t)kThreads + threadIdx.x) / 4;
-    const uint32_t lane = threadIdx.x & 31, l = lane & 3;
-    const size_t item = team / 16 * 8 + team % 8;
-    const bool is_v = team & 8;
-    const Item w = find_item(a.r, a.c, item, a.status);
-    const uint8_t* from = (is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 8 * l;
-    const uint16_t* sc = (is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16);
+    constexpr int P = D / 64;
+    const QuadItem t = quad_item(blockIdx.x);
+    const Item w = find_item(a.r, a.c, t.item, a.status);
+    const uint8_t* from = (t.is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 16 * t.l;
+    const uint16_t* sc = (t.is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16) + t.l;
     float2 x[D / 8];
-    uint2 codes[P];
-    uint32_t s[P];  // the scales of groups 2 i and 2 i + 1
+    uint4 codes[P];
+    uint16_t s[P];
 #pragma unroll
-    for (int i = 0; i < P; ++i) codes[i] = w.ok ? *reinterpret_cast<const uint2*>(from + 32 * i) : make_uint2(0u, 0u);
-#pragma unroll
-    for (int i = 0; i < P; i += 2) {
-      const uint2 u = w.ok ? *reinterpret_cast<const uint2*>(sc + 2 * i) : make_uint2(0u, 0u);
-      s[i] = u.x;
-      s[i + 1] = u.y;
+    for (int i = 0; i < P; ++i) {
+      codes[i] = w.ok ? *reinterpret_cast<const uint4*>(from + 64 * i) : make_uint4(0u, 0u, 0u, 0u);
+      s[i] = w.ok ? sc[4 * i] : 0;
     }
 #pragma unroll
-    for (int i = 0; i < P; ++i) dequant8(codes[i], l < 2 ? bf16lo(s[i]) : bf16hi(s[i]), x + 4 * i);
-    wht_quad<D>(x, lane);
-    uint16_t* to = (is_v ? a.v : a.k) + item * D + 8 * l;
-    if (w.ok)
+    for (int i = 0; i < P; ++i) dequant16(codes[i], bf16f(s[i]), x + 8 * i);
+    wht_quad<D>(x, threadIdx.x & 31);
+    uint16_t* to = (t.is_v ? a.v : a.k) + t.item * D + 16 * t.l;
 #pragma unroll
-      for (int i = 0; i < P; ++i)
-        *reinterpret_cast<uint4*>(to + 32 * i) = pack8(reinterpret_cast<const float*>(x + 4 * i));
+    for (int i = 0; i < P; ++i) {
+      uint32_t u[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const __nv_bfloat162 q = __float22bfloat162_rn(x[8 * i + k]);
+        u[k] = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      if (w.ok) store32(to + 64 * i, a.wide, u);
+    }
   } else {
     constexpr int LPR = D / 8;
     const size_t item = (blockIdx.x * (size_t)kThreads + threadIdx.x) / LPR;
@@ -756,11 +755,11 @@ cudaError_t append(const Append& a, cudaStream_t st) {
   const bool t8 = a.c.ks != nullptr;
   const uint32_t rows = row_ctas_of(a.r, a.c, t8);
   const uint32_t span = a.r.row_start ? 1u << a.blk_shift : 1u;  // rows of a bounds CTA: about one block's
-  const uint32_t folds = (a.r.n_rows + span - 1) / span * a.c.Hkv, teams = a.blk_shift > 6 ? 1 : kThreads / (a.c.D / 8);
-  const uint32_t grid = rows + (a.bounds ? (folds + teams - 1) / teams : 0);
+  const uint32_t folds = (a.r.n_rows + span - 1) / span * a.c.Hkv, teams = a.blk_shift > kWideShift ? 1 : kThreads / (a.c.D / 8);
+  const uint32_t bounds = a.bounds ? (folds + teams - 1) / teams : 0, grid = rows + bounds;
 #define CALL(DD)                                                               \
-  return t8 ? launch_early(append_kernel<DD, true>, dim3(grid), kThreads, 0, st, a, rows, span)   \
-            : launch_early(append_kernel<DD, false>, dim3(grid), kThreads, 0, st, a, rows, span)
+  return t8 ? launch_early(append_kernel<DD, true>, dim3(grid), kThreads, 0, st, a, bounds, span)   \
+            : launch_early(append_kernel<DD, false>, dim3(grid), kThreads, 0, st, a, bounds, span)
   Q35C_BY_DIM(a.c.D, CALL)
 #undef CALL
 }

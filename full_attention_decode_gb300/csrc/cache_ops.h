@@ -41,6 +41,7 @@ struct Append {
   const uint16_t* v;
   uint16_t* bounds;  // [rows >> blk_shift][Hkv][2][D], or null
   uint32_t blk_shift;
+  bool wide;  // k and v are 32-byte aligned
   int* status;
 };
 cudaError_t append(const Append& a, cudaStream_t st);
@@ -50,6 +51,7 @@ struct Read {
   Rows r;
   uint16_t* k;  // [n_rows][Hkv][D]
   uint16_t* v;
+  bool wide;  // k and v are 32-byte aligned
   int* status;
 };
 cudaError_t read(const Read& a, cudaStream_t st);

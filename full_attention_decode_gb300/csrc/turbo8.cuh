@@ -63,8 +63,8 @@ __device__ __forceinline__ void wht8(float (&x)[8], uint32_t lane) {
 // u - w in pairs.
 __device__ __forceinline__ float2 sub2(float2 u, float2 w) { return __ffma2_rn(w, make_float2(-1.f, -1.f), u); }
 
-// The same transform, four lanes a row: lane l of each four holds pieces i < D / 32 of eight
-// elements, [32 i + 8 l, 32 i + 8 l + 8), in pairs (four a piece). Index bits 3 and 4 lie on the lanes, all
+// The same transform, four lanes a row: lane l of each four holds pieces i < D / 64 of sixteen
+// elements, [64 i + 16 l, 64 i + 16 l + 16), in pairs (eight a piece). Index bits 4 and 5 lie on the lanes, all
 // others inside a lane, so a row of 256 costs a warp 16 shuffles (40 with 32 lanes a row); sums
 // and differences are taken two at a time.
 template <int D>
@@ -73,7 +73,7 @@ __device__ __forceinline__ void wht_quad(float2 (&x)[D / 8], uint32_t lane) {
 #pragma unroll
   for (int k = 0; k < N; ++k) x[k] = make_float2(x[k].x + x[k].y, x[k].x - x[k].y);
 #pragma unroll
-  for (int hb = 1; hb < 4; hb <<= 1)
+  for (int hb = 1; hb < 8; hb <<= 1)
 #pragma unroll
     for (int k = 0; k < N; ++k)
       if (!(k & hb)) {
@@ -91,7 +91,7 @@ __device__ __forceinline__ void wht_quad(float2 (&x)[D / 8], uint32_t lane) {
     }
   }
 #pragma unroll
-  for (int hb = 4; hb < N; hb <<= 1)
+  for (int hb = 8; hb < N; hb <<= 1)
 #pragma unroll
     for (int k = 0; k < N; ++k)
       if (!(k & hb)) {
@@ -104,29 +104,50 @@ __device__ __forceinline__ void wht_quad(float2 (&x)[D / 8], uint32_t lane) {
   for (int k = 0; k < N; ++k) x[k] = __fmul2_rn(x[k], make_float2(norm, norm));
 }
 
-// Quantise a piece of eight bf16 values (in pairs), a group of 16 on two lanes: scale = bf16(amax / 448),
-// code = E4M3(x / scale); a zero group keeps scale 0 and codes 0. Neither quotient needs
-// a division:
+// 32 bytes of a lane, in one access where the address is a multiple of 32 (wide), else in two.
+__device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("ld.global.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+  } else {
+    const uint4 a = static_cast<const uint4*>(p)[0], b = static_cast<const uint4*>(p)[1];
+    w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
+    w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+  }
+}
+__device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&w)[8]) {
+  if (wide) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                 "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+  } else {
+    static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+    static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+  }
+}
+
+// Quantise a group of sixteen bf16 values (in pairs): scale = bf16(amax / 448), code = E4M3(x / scale); a
+// zero group keeps scale 0 and codes 0. Neither quotient needs a division:
 //  - amax has 8 significant bits and 448 = 7 * 64, so amax / 448 is never on a border between two bf16 values (9
 //    bits times 7 has more than 8) and at least 2^-12 away from one: the product with 1 / 448 rounds alike;
 //  - x / scale as q = x r with r near 1 / scale and one residual correction, q + (x - q scale) r (Markstein 1990).
 //    x and scale have 8 bits and a border between codes 5: a quotient that is not on a border is at least
 //    2^-13 away from it, and one that is comes out exact. Scales near the ends of the range take the division.
-__device__ __forceinline__ uint2 quant8(const uint32_t* w, uint16_t& scale) {
-  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(w));
+__device__ __forceinline__ uint4 quant16(const uint32_t (&w)[8], uint16_t& scale) {
+  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
 #pragma unroll
-  for (int i = 1; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(w + i)));
-  float amax = fmaxf(__low2float(m), __high2float(m));
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+  for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
+  const float amax = fmaxf(__low2float(m), __high2float(m));
   scale = to_bf16(amax * (1.0f / 448.0f));
   const float sc = bf16f(scale);
-  uint32_t c[4] = {0u, 0u, 0u, 0u};
+  uint32_t c[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
   if (sc > 1e-30f && sc < 1e30f) {
     float r;
     asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc));
     const float2 r2 = make_float2(r, r), s2 = make_float2(-sc, -sc);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 8; ++i) {
       const float2 x = make_float2(bf16lo(w[i]), bf16hi(w[i]));
       float2 q = __fmul2_rn(x, r2);
       q = __ffma2_rn(__ffma2_rn(q, s2, x), r2, q);
@@ -134,15 +155,17 @@ __device__ __forceinline__ uint2 quant8(const uint32_t* w, uint16_t& scale) {
     }
   } else if (sc != 0.f) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3_pair(bf16lo(w[i]) / sc, bf16hi(w[i]) / sc);
+    for (int i = 0; i < 8; ++i) c[i] = e4m3_pair(bf16lo(w[i]) / sc, bf16hi(w[i]) / sc);
   }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
+  return make_uint4(c[0] | (c[1] << 16), c[2] | (c[3] << 16), c[4] | (c[5] << 16), c[6] | (c[7] << 16));
 }
-// Eight codes times their scale (exact), in pairs.
-__device__ __forceinline__ void dequant8(uint2 c, float sc, float2* x) {
+// Sixteen codes times their scale (exact), in pairs.
+__device__ __forceinline__ void dequant16(uint4 c, float sc, float2* x) {
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
-    x[i] = __fmul2_rn(e4m3_pair_value((i < 2 ? c.x : c.y) >> (16 * (i % 2))), make_float2(sc, sc));
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t w = i < 2 ? c.x : i < 4 ? c.y : i < 6 ? c.z : c.w;
+    x[i] = __fmul2_rn(e4m3_pair_value(w >> (16 * (i % 2))), make_float2(sc, sc));
+  }
 }
 
 }  // namespace q35

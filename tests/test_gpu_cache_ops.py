@@ -304,6 +304,52 @@ def test_turbo8_append_equals_the_prefill_of_a_layer(cfg_name):
             assert torch.equal(a[:T], b[:T])
 
 
+@pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "4b"])
+def test_rows_aligned_to_16_bytes_only(heads):
+    s = Setup(heads, TURBO8, [40, 33], rows=[40, 5])
+    k, v = [x.cuda() for x in _new_rows(s)]
+    off = []
+    for x in (k, v, torch.zeros_like(k), torch.zeros_like(k)):
+        room = torch.zeros(x.numel() + 8, dtype=torch.bfloat16, device="cuda")
+        assert (room.data_ptr() + 16) % 32 == 16
+        y = room[8:].view_as(x)
+        y.copy_(x)
+        off.append(y)
+    back = [torch.zeros_like(k) for _ in "kv"]
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, None, k, v, s.scratch) == 0
+    assert B.qwen35_cache_read(s.cfg, s.kv, s.r, *back, s.scratch) == 0
+    torch.cuda.synchronize()
+    kept = {n: t.clone() for n, t in s.t.items()}
+    for t in s.t.values():
+        t.zero_()
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, None, off[0], off[1], s.scratch) == 0
+    assert B.qwen35_cache_read(s.cfg, s.kv, s.r, off[2], off[3], s.scratch) == 0
+    torch.cuda.synchronize()
+    at = [int(s.at(b, p)) for _, b, p in s.each_row()]
+    groups = s.Hkv * s.D // 16  # (a row of scales is padded behind them)
+    assert all(torch.equal(kept[n][at, :groups], s.t[n][at, :groups]) for n in ("ks", "vs"))
+    assert all(torch.equal(kept[n][at], s.t[n][at]) for n in "kv")
+    assert torch.equal(back[0], off[2]) and torch.equal(back[1], off[3])
+
+
+@pytest.mark.parametrize("e", [-132, -126, -110, -60, 60, 110, 118])
+def test_turbo8_append_at_the_ends_of_the_range(e):
+    """Rows near the smallest and the largest bf16 values: the oracle's codes and scales."""
+    s = Setup("tiny", TURBO8, [64], rows=[64])
+    rng = np.random.default_rng(abs(e))
+    x = np.zeros((64, 1, s.D))
+    x[np.arange(64), 0, rng.integers(0, s.D, 64)] = np.exp2(e) * rng.integers(128, 256, 64) / 128  # rotated: +-x / 8
+    k = bf16(x)
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, None, k.cuda(), k.cuda(), s.scratch) == 0
+    torch.cuda.synchronize()
+    with np.errstate(all="ignore"):
+        c, sc = O.turbo8_quantize(O.bf16_round(O.wht(f64(k))))
+    at = [int(s.at(0, p)) for p in range(64)]
+    got = O.bf16_to_f64(s.t["ks"].cpu().numpy().view(np.uint16)[at][:, :s.D // 16]).reshape(sc.shape)
+    np.testing.assert_array_equal(got, sc)
+    np.testing.assert_array_equal(s.t["k"].cpu().numpy()[at].reshape(c.shape), c)
+
+
 def test_append_skips_nan_in_bounds_and_keeps_special_rows():
     s = Setup("tiny", BF16, [20, 16], rows=[20, 16], block=16)
     k, v = _new_rows(s)
