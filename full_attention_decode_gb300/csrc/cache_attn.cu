@@ -163,6 +163,8 @@ __device__ __forceinline__ Tile lane_of(const Tile& t, uint32_t src) {
   return x;
 }
 
+constexpr uint32_t kNo0 = 64, kNo1 = 128;  // tokens 0-7, 8-15 lie in no block of the pool
+
 template <int D, int NT, bool T8>
 struct Attention {
   using S = Slot<D, T8>;
@@ -179,7 +181,7 @@ struct Attention {
   // ---- where a tile's tokens are
   __device__ Tile tile(const Segment& s, uint32_t t) const {
     Tile x;
-    x.seen = 0;
+    x.token = x.seen = 0;
     x.in[0] = x.in[1] = false;
     x.row[0] = x.row[1] = 0;
     if (t >= s.t1) return x;
@@ -435,9 +437,9 @@ struct Attention {
   }
 
   // ---- one tile: weights from the scores, then the output from its V slot; the last row sees `seen` tokens
-  // from the tile's first on
+  // from the tile's first on, those in a block outside the pool left out
   __device__ __forceinline__ int accumulate(uint32_t slot, float (&s)[NT][4], uint32_t seen) {
-    const uint32_t r = lane >> 2;
+    const uint32_t r = lane >> 2, seen0 = seen & kNo0 ? 0 : seen & 63u, seen1 = seen & kNo1 ? 0 : seen & 63u;
     int ev = 0;
     if constexpr (T8) ev = v_scales(slot);
     uint32_t ph[NT][2], pl[NT][2];
@@ -452,8 +454,8 @@ struct Attention {
           x0 += (float)ev;
           x1 += (float)ev;
         }
-        if (r + later[nt][j] >= seen) x0 = -INFINITY;
-        if (r + 8 + later[nt][j] >= seen) x1 = -INFINITY;
+        if (r + later[nt][j] >= seen0) x0 = -INFINITY;
+        if (r + 8 + later[nt][j] >= seen1) x1 = -INFINITY;
         float mx = fmaxf(x0, x1);
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
@@ -592,7 +594,8 @@ struct Attention {
         for (int i = 0; i < 4; ++i) o[d][nt][i] = 0.f;
     float sc[NT][4];
     uint32_t slot = 0;                          // the slot that is read now and refilled then
-    uint32_t seen = 0, seen1 = 0, seen2 = 0;    // of the tile that is read, the last one copied, the one before
+    uint32_t seen = 0, seen1 = 0, seen2 = 0;    // of the tile that is read, the last one copied, the one before; with
+                                                // a bit for each half in a block outside the pool
     Tile found, ahead;  // each lane: a tile's place, 32 tiles looked up at a time; the tile that is being copied
     found.seen = ahead.seen = 0;
 #pragma unroll 1
@@ -606,7 +609,7 @@ struct Attention {
           if (seen) scores(slot, sc);
         } else if (seen) {
           const int ev = accumulate(slot, sc, seen);
-          if (seen < 16 + s.rows - 1 && s.rows > 1) add_tail(s, first + (h >> 1) * kWarps, sc, ev);
+          if ((seen & 63u) < 16 + s.rows - 1 && s.rows > 1) add_tail(s, first + (h >> 1) * kWarps, sc, ev);
         }
         __syncwarp();  // this half-tile has been read by every lane
       }
@@ -616,7 +619,7 @@ struct Attention {
         if (i % 32 == 0) found = tile(s, first + (i + lane) * kWarps);
         ahead = lane_of(found, i % 32);
         seen2 = seen1;
-        seen1 = ahead.seen;
+        seen1 = ahead.seen ? ahead.seen | (ahead.in[0] ? 0u : kNo0) | (ahead.in[1] ? 0u : kNo1) : 0u;
       }
       if (c < halves) load(s, ahead, c & 1, slot);
       cp_commit();

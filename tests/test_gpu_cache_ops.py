@@ -405,6 +405,27 @@ def test_rows_out_of_range_are_skipped_and_reported(fmt):
     assert (blocks[1:3] == 7).all() and not (blocks[0] == 7).any()
 
 
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("page", [8, 32])
+def test_attention_leaves_a_block_outside_the_pool_out(fmt, page):
+    s = Setup("tiny", fmt, [100, 60], rows=[3, 2], page=page, block=16)
+    s.table[0, 1] = s.nb + 5
+    s.table[1, 0] = -1
+    out = s.attend()
+    assert s.status() == B.QWEN35_ERR_DEVICE_RANGE
+    got = f64(out)
+    for row, b, p in s.each_row():
+        t = np.arange(p + 1)
+        t = t[t // page != (1 if b == 0 else 0)]
+        rows = s.at(b, t)
+        k, v, q = s.stands["k"][rows, 0], s.stands["v"][rows, 0], f64(s.q[row])
+        x = q @ k.T / np.sqrt(s.D)
+        w = np.exp(x - x.max(-1, keepdims=True))
+        ref = (w / w.sum(-1, keepdims=True)) @ v
+        err, vmax = np.linalg.norm(got[row] - ref, axis=1), np.abs(O.wht(v) if fmt == TURBO8 else v).max()
+        assert np.all(err <= 2.0 ** -8 * np.linalg.norm(ref, axis=1) + 2.0 ** -10 * vmax * np.sqrt(s.D))
+
+
 def test_a_row_start_that_runs_backwards_touches_nothing_outside():
     s = Setup("tiny", BF16, [30, 30, 30], rows=[2, 2, 2], tail=2)
     s.row_start.copy_(torch.tensor([0, 6, 2, 8], dtype=torch.int32))
