@@ -265,6 +265,7 @@ constexpr uint32_t kKeys = 16384;  // and all of a CTA in shared memory
 constexpr uint32_t kClose = 256;  // blocks scored again side by side
 constexpr uint32_t kAhead = 8;     // blocks of a lane in flight
 constexpr uint32_t kRing = kAhead * 2 * kThreads * 16;  // their bytes
+constexpr uint32_t kSteps = 4;     // of eight bits each
 constexpr uint32_t kInf = 0xff800000u;  // the key of +infinity
 
 // Sums over the group's heads of q's positive and negative parts, eight dims a lane.
@@ -289,9 +290,9 @@ __device__ __forceinline__ void signed_sums(const Select& a, uint32_t r, uint32_
 // Scores of blocks [j0, j1): s_j = sum_d Q+_d hi_jd + Q-_d lo_jd, with Q+ and Q- the sums over the
 // group's heads of q's positive and negative parts: the sum over the heads of the largest q.k that a key
 // inside the bounds could have. The bytes of the bounds bound it: a team of LPR lanes takes a block, each lane
-// copies its own 32 bytes of kAhead blocks ahead (64 KB a CTA in flight, two CTAs an SM: 25.5 us
-// for 16 sequences of 16K-64K tokens; four blocks in registers, 32 KB: 26.5 us; three CTAs of 80 registers: 31.6 us) and waits for nobody else. Returns (in every
-// thread) sum_d Q+_d max_j|hi_jd| + |Q-_d| max_j|lo_jd|, which bounds every block's sum
+// copies its own 32 bytes of kAhead blocks ahead (64 KB a CTA in flight, two CTAs an
+// SM: 25.5 us for 16 sequences of 16K-64K tokens; four blocks in registers, 32 KB: 26.5 us; three CTAs of 80
+// registers: 31.6 us) and waits for nobody else. Returns (in every thread) sum_d Q+_d max_j|hi_jd| + |Q-_d| max_j|lo_jd|, which bounds every block's sum
 // of absolute terms; infinity where an infinity or NaN leaves no bound.
 template <int D>
 __device__ __forceinline__ float score_blocks(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n,
@@ -598,18 +599,15 @@ template <int D>
 __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item, float most) {
   extern __shared__ __align__(16) uint32_t keys[];
   __shared__ uint32_t tmp[2 * kSelWarps], range[2 * kSelWarps], close_j[kClose];
+  __shared__ __align__(16) uint32_t s_bins[kSteps][256];
   const uint32_t K = a.n_select, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int32_t* out = a.blocks + item * K;
   uint32_t turn = 0;
   Scores sc;
   sc.place(a.scores + item * a.nblk, n, keys);
   sc.take();
-  const auto count = [&](uint32_t from) {  // keys >= from
-    uint32_t c = 0;
-    sc.count([&](uint32_t k) { c += k >= from; });
-    return cta_sum(c, tmp, turn);
-  };
-  // the finite scores' range: most of a bisection of all 32 bits would only find it
+  for (uint32_t i = threadIdx.x; i < kSteps * 256; i += kThreads) s_bins[0][i] = 0;
+  // the finite scores' range: the first step over all 32 bits would only find it
   uint32_t low = 0xffffffffu, high = 0, n_forced = 0;
   sc.count([&](uint32_t k) {
     low = k ? min(low, k) : low;
@@ -622,8 +620,8 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     range[warp] = low;
     range[kSelWarps + warp] = high;
   }
-  uint32_t at_low = n;
   n_forced = cta_sum(n_forced, tmp, turn);
+  uint32_t at_low = n, at_high = n_forced;
   for (uint32_t w = 0; w < kSelWarps; ++w) {
     low = min(low, range[w]);
     high = max(high, range[kSelWarps + w]);
@@ -634,15 +632,41 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     high = kInf + 1;
     at_low = n_forced;
   }
-  // low: the largest tried value with at least K keys from it up; high: the smallest with fewer
-  while (at_low != K && high - low > 1) {
-    const uint32_t mid = low + (high - low) / 2, c = count(mid);
-    if (c >= K) {
-      low = mid;
-      at_low = c;
-    } else {
-      high = mid;
+  // low: the largest tried value with at least K keys from it up (at_low); high: the smallest with fewer (at_high).
+  // A step cuts what lies between into 256: one count of all bins where a bisection takes eight (kBins)
+  for (uint32_t step = 0; step < kSteps && at_low != K && high - low > 1; ++step) {
+    const uint32_t bits = 32 - __clz(high - low - 1), shift = bits > 8 ? bits - 8 : 0;
+    uint32_t* bins = s_bins[step];
+    sc.count([&](uint32_t k) {
+      if (k >= low && k < high) atomicAdd(bins + ((k - low) >> shift), 1u);
+    });
+    __syncthreads();
+    // every warp for itself: eight bins a lane, the keys above them, and the bin that reaches K
+    const uint4 c0 = reinterpret_cast<const uint4*>(bins)[2 * lane], c1 = reinterpret_cast<const uint4*>(bins)[2 * lane + 1];
+    const uint32_t c[8] = {c0.x, c0.y, c0.z, c0.w, c1.x, c1.y, c1.z, c1.w};
+    uint32_t up = ((c[0] + c[1]) + (c[2] + c[3])) + ((c[4] + c[5]) + (c[6] + c[7])), mine = up;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t x = __shfl_down_sync(0xffffffffu, up, o);
+      up += lane + o < 32 ? x : 0u;
     }
+    uint32_t above = at_high + up - mine, b = 0, to = 0;
+    const unsigned here = __ballot_sync(0xffffffffu, above < K && above + mine >= K);
+    bool found = false;
+#pragma unroll
+    for (int e = 7; e >= 0; --e)
+      if (!found) {
+        to = above + c[e];
+        found = to >= K;
+        if (found) b = 8 * lane + e;
+        else above = to;
+      }
+    const int src = __ffs(here) - 1;
+    at_high = __shfl_sync(0xffffffffu, above, src);
+    at_low = __shfl_sync(0xffffffffu, to, src);
+    b = __shfl_sync(0xffffffffu, b, src);
+    high = (uint32_t)min((uint64_t)high, low + ((uint64_t)(b + 1) << shift));
+    low += b << shift;
   }
   uint32_t kth = 0xffffffffu;  // the smallest key from low up: the K-th largest's
   sc.count([&](uint32_t k) { kth = k >= low ? min(kth, k) : kth; });
@@ -666,10 +690,11 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
   uint32_t cut = klo;  // in from this key up
   if (n_close != need) {
     if (n_close <= kClose) {  // a list of them, in any order
-      if (threadIdx.x == 0) tmp[0] = 0;
+      // counted in `range`, which nobody reads any more (another warp may still read the last sum's part of tmp)
+      if (threadIdx.x == 0) range[0] = 0;
       __syncthreads();
       sc.each([&](uint32_t j, uint32_t k) {
-        if (k >= klo && k <= khi) close_j[atomicAdd(tmp, 1u)] = j;
+        if (k >= klo && k <= khi) close_j[atomicAdd(range, 1u)] = j;
       });
       __syncthreads();
     }
