@@ -433,8 +433,8 @@ __device__ double score_again(const Select& a, uint32_t r, uint32_t g, uint32_t 
 }
 
 // The scores of an item, spread over one CTA: warp w has blocks [w span, (w + 1) span), lane l every 32nd
-// of them from l. Their order keys are in registers (the first kMine of a thread) for the counts of the
-// bisection, and in shared memory (the first kKeys of the item) for what runs once, whose code should be short;
+// of them from l. Their order keys are in registers (the first kMine of a thread) for the counts,
+// and in shared memory (the first kKeys of the item) for what runs once, whose code should be short;
 // others are read again.
 struct Scores {
   const float* s;
@@ -592,13 +592,15 @@ __device__ __forceinline__ void decide(const Select& a, uint32_t r, uint32_t g, 
 
 // Which blocks the exact scores choose, given 32-bit ones. Every s_j is within E of the exact t_j
 // (E = (group + 13) 2^-24 most: group - 1 additions in Q+-, 4 multiply-adds and 2 + 5 additions round
-// one after the other, and the rounding of `most` itself is covered by the rest). The K-th largest t is then within E of the K-th largest s, T: s_j > T + 2E is in, s_j < T - 2E is
-// out, and only what lies between is scored again in 64 bits. T by bisection of the
-// scores' bits: a count over the CTA a step, until a step leaves exactly K.
+// one after the other, and the rounding of `most` itself is covered by the rest). The K-th largest t is then within E
+// of the K-th largest s, T: s_j > T + 2E is in, s_j < T - 2E is out, and only what lies between is scored again. T is
+// found from the scores' bits, eight a step, until a step leaves exactly K. This part is latency (one CTA an item, a
+// few barriers, code that runs once): bisection and a barrier for each count took 0.6 us more of a
+// selection's 8.5 (64K tokens), keys from shared memory alone, with shorter code, 0.4 us more.
 template <int D>
 __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, uint32_t n, size_t item, float most) {
   extern __shared__ __align__(16) uint32_t keys[];
-  __shared__ uint32_t tmp[2 * kSelWarps], range[2 * kSelWarps], close_j[kClose];
+  __shared__ uint32_t tmp[2 * kSelWarps], range[3 * kSelWarps], close_j[kClose];
   __shared__ __align__(16) uint32_t s_bins[kSteps][256];
   const uint32_t K = a.n_select, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   int32_t* out = a.blocks + item * K;
@@ -633,7 +635,7 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     at_low = n_forced;
   }
   // low: the largest tried value with at least K keys from it up (at_low); high: the smallest with fewer (at_high).
-  // A step cuts what lies between into 256: one count of all bins where a bisection takes eight (kBins)
+  // A step cuts what lies between into 256: one count of all bins where a bisection takes eight
   for (uint32_t step = 0; step < kSteps && at_low != K && high - low > 1; ++step) {
     const uint32_t bits = 32 - __clz(high - low - 1), shift = bits > 8 ? bits - 8 : 0;
     uint32_t* bins = s_bins[step];
@@ -671,10 +673,9 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
   uint32_t kth = 0xffffffffu;  // the smallest key from low up: the K-th largest's
   sc.count([&](uint32_t k) { kth = k >= low ? min(kth, k) : kth; });
   kth = __reduce_min_sync(0xffffffffu, kth);
+  if (lane == 0) range[2 * kSelWarps + warp] = kth;
   __syncthreads();
-  if (lane == 0) range[warp] = kth;
-  __syncthreads();
-  for (uint32_t w = 0; w < kSelWarps; ++w) kth = min(kth, range[w]);
+  for (uint32_t w = 0; w < kSelWarps; ++w) kth = min(kth, range[2 * kSelWarps + w]);
   const float T = key_value(kth), E = (float)(a.H / a.c.Hkv + 13) * 0x1p-24f * most;
   uint32_t klo = 1, khi = 0xffffffffu;  // keys above khi are in, below klo out
   if (E < INFINITY) {
@@ -686,11 +687,27 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     c1 += k > khi;
     c2 += k >= klo && k <= khi;
   });
-  const uint32_t n_sure = cta_sum(c1, tmp, turn), n_close = cta_sum(c2, tmp, turn), need = K - n_sure;
+  // over the CTA, and over the warps before this one: where its blocks go in the list
+  c1 = __reduce_add_sync(0xffffffffu, c1);
+  c2 = __reduce_add_sync(0xffffffffu, c2);
+  if (lane == 0) {
+    tmp[warp] = c1;
+    tmp[kSelWarps + warp] = c2;
+  }
+  __syncthreads();
+  uint32_t n_sure = 0, n_close = 0, at = 0;
+#pragma unroll
+  for (uint32_t w = 0; w < kSelWarps; ++w) {
+    const uint32_t x = tmp[w], y = tmp[kSelWarps + w];
+    at += w < warp ? x + y : 0u;
+    n_sure += x;
+    n_close += y;
+  }
+  const uint32_t need = K - n_sure;
   uint32_t cut = klo;  // in from this key up
   if (n_close != need) {
     if (n_close <= kClose) {  // a list of them, in any order
-      // counted in `range`, which nobody reads any more (another warp may still read the last sum's part of tmp)
+      // counted in `range`, which nobody reads any more (another warp may still read the sums in tmp)
       if (threadIdx.x == 0) range[0] = 0;
       __syncthreads();
       sc.each([&](uint32_t j, uint32_t k) {
@@ -701,16 +718,16 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
     decide<D>(a, r, g, seq, n, item, klo, khi, n_close, need, most, tmp, close_j);
     sc.take();
     cut = min(khi, kInf - 1) + 1;
+    uint32_t n_in = 0;
+    sc.count([&](uint32_t k) { n_in += k >= cut; });
+    n_in = __reduce_add_sync(0xffffffffu, n_in);
+    __syncthreads();
+    if (lane == 0) tmp[warp] = n_in;
+    __syncthreads();
+    at = 0;
+    for (uint32_t w = 0; w < warp; ++w) at += tmp[w];
   }
   // in index order: a warp's blocks are neighbours, so places come from ballots and the counts of the warps before
-  uint32_t n_in = 0;
-  sc.count([&](uint32_t k) { n_in += k >= cut; });
-  n_in = __reduce_add_sync(0xffffffffu, n_in);
-  __syncthreads();
-  if (lane == 0) tmp[warp] = n_in;
-  __syncthreads();
-  uint32_t at = 0;
-  for (uint32_t w = 0; w < warp; ++w) at += tmp[w];
   sc.each([&](uint32_t j, uint32_t k) {
     const unsigned m = __ballot_sync(0xffffffffu, k >= cut);
     const uint32_t to = at + __popc(m & ((1u << lane) - 1u));
