@@ -37,10 +37,12 @@ __device__ __forceinline__ void append_plain(const Append& a, uint32_t block) {
   constexpr int LPR = D / 8;
   const size_t item = (block * (size_t)kThreads + threadIdx.x) / LPR;
   const uint32_t l = threadIdx.x % LPR;
+  if (item >= (size_t)a.r.n_rows * a.c.Hkv) return;
+  const size_t src = item * D + 8 * l;  // on its way while the cache row is looked up
+  const uint4 k = load16(a.k + src), v = load16(a.v + src);
   const Item x = find_item(a.r, a.c, item, a.status);
   if (!x.ok) return;
-  const size_t src = item * D + 8 * l, dst = (x.row * a.c.Hkv + x.g) * D + 8 * l;
-  const uint4 k = *reinterpret_cast<const uint4*>(a.k + src), v = *reinterpret_cast<const uint4*>(a.v + src);
+  const size_t dst = (x.row * a.c.Hkv + x.g) * D + 8 * l;
   *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.c.k) + dst) = k;
   *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.c.v) + dst) = v;
 }
@@ -61,16 +63,18 @@ __device__ __forceinline__ void append_turbo8(const Append& a, uint32_t block) {
   constexpr int P = D / 64;  // pieces of sixteen elements
   const QuadItem t = quad_item(block);
   const uint32_t lane = threadIdx.x & 31;
-  const Item w = find_item(a.r, a.c, t.item, a.status);
+  const bool in = t.item < (size_t)a.r.n_rows * a.c.Hkv;
   const uint16_t* src = (t.is_v ? a.v : a.k) + t.item * D + 16 * t.l;
+  uint32_t u[P][8] = {};
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+    if (in) load32(src + 64 * i, a.wide, u[i]);
+  const Item w = find_item(a.r, a.c, t.item, a.status);  // while the rows are on their way
   float2 x[D / 8];
 #pragma unroll
-  for (int i = 0; i < P; ++i) {
-    uint32_t u[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};
-    if (w.ok) load32(src + 64 * i, a.wide, u);
+  for (int i = 0; i < P; ++i)
 #pragma unroll
-    for (int k = 0; k < 8; ++k) x[8 * i + k] = make_float2(bf16lo(u[k]), bf16hi(u[k]));
-  }
+    for (int k = 0; k < 8; ++k) x[8 * i + k] = make_float2(bf16lo(u[i][k]), bf16hi(u[i][k]));
   wht_quad<D>(x, lane);
   uint8_t* to = (t.is_v ? a.c.v : a.c.k) + (w.row * a.c.Hkv + w.g) * D + 16 * t.l;
   uint32_t* sc = reinterpret_cast<uint32_t*>((t.is_v ? a.c.vs : a.c.ks) + w.row * a.c.sstride + w.g * (D / 16));

@@ -104,6 +104,12 @@ __device__ __forceinline__ void wht_quad(float2 (&x)[D / 8], uint32_t lane) {
   for (int k = 0; k < N; ++k) x[k] = __fmul2_rn(x[k], make_float2(norm, norm));
 }
 
+// 16 bytes, loaded where the call stands.
+__device__ __forceinline__ uint4 load16(const void* p) {
+  uint4 r;
+  asm volatile("ld.global.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "l"(p));
+  return r;
+}
 // 32 bytes of a lane, in one access where the address is a multiple of 32 (wide), else in two.
 __device__ __forceinline__ void load32(const void* p, bool wide, uint32_t (&w)[8]) {
   if (wide) {
