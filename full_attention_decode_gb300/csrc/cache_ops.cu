@@ -98,8 +98,8 @@ __device__ __forceinline__ void append_turbo8(const Append& a, uint32_t block) {
 // The key bounds of spans of rows. A run is the call's rows of one block of one sequence; who has the span with
 // its first row folds it, starting anew if that is the block's first token. WIDE: a CTA a (span, kv-head), its
 // teams of D / 8 lanes taking a run's rows in turn; otherwise (blocks of 16 tokens) a team alone,
-// sixteen rows in flight (three prompts of 400 to 1500 rows, blocks of 64: 9.5 us wide, 11.0 by teams; 32768 rows,
-// blocks of 16: 168 us wide, 68 by teams).
+// sixteen rows in flight (three prompts of 400 to 1500 rows, blocks of 64: 9.0 us wide, 10.7 by teams; 32768 rows,
+// blocks of 16: 119 us wide, 57 by teams).
 template <int D, bool WIDE>
 __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, uint32_t g, uint32_t span_rows) {
   constexpr int LPR = D / 8, TEAMS = WIDE ? kThreads / LPR : 1;

@@ -1,6 +1,6 @@
 // Device helpers of the kernels that read and write KV caches: eight bf16 values of a
 // 16-byte word, FP8 E4M3 pairs, and the Walsh-Hadamard transform and quantiser of a
-// Turbo8 row held eight elements a lane.
+// Turbo8 row held eight elements a lane, or by four lanes in pieces of sixteen.
 #pragma once
 
 #include <cuda_fp16.h>
