@@ -759,7 +759,9 @@ struct Attention {
     float* ml = reinterpret_cast<float*>(sm + M::ml) + kWarps * 32;
     float* wt = reinterpret_cast<float*>(sm + M::weights);  // [ncol][parts]
     const uint32_t n = c1 - c0 + 1, cols = ncol * (D / 4), subs = max(1u, kAttnThreads / cols);
-    constexpr int B = 16;  // parts of a thread in flight
+    // Parts of a thread in flight, in its own slots of what the ring leaves.
+    constexpr int B = (M::big - M::parts) / (kAttnThreads * 16);
+    uint4* stage = reinterpret_cast<uint4*>(sm + M::parts) + threadIdx.x;
     const size_t step = 2 * (size_t)(group * pack * (D + 4));
     // every thread takes the same rounds (the first has a barrier in it): columns of a stride of the threads, B parts each
     float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -770,13 +772,13 @@ struct Attention {
       const bool mine = i < cols * subs;
       const float* p0 = part(c0, 1) + at;  // CTA c0's part, then slot 0 of each CTA
       const float* p = part(c0, 0) + at;
-      float4 y[B];
-#pragma unroll
-      for (int k = 0; k < B; ++k) {
+      const uint32_t left = mine && k0 + sub < n ? min((n - k0 - sub + subs - 1) / subs, (uint32_t)B) : 0;
+#pragma unroll 4
+      for (uint32_t k = 0; k < left; ++k) {
         const uint32_t c = k0 + sub + k * subs;
-        y[k] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (mine && c < n) y[k] = __ldcg(reinterpret_cast<const float4*>(c ? p + c * step : p0));
+        cp16(smem_addr(stage + k * kAttnThreads), c ? p + c * step : p0);
       }
+      cp_commit();
       if (i0 == 0 && k0 == 0) {  // the weights, their loads in the same wait as the first parts'
         for (uint32_t hh = warp; hh < ncol; hh += kWarps) {
           float mx = -INFINITY, sum = 0.f;
@@ -806,16 +808,15 @@ struct Attention {
         }
         __syncthreads();
       }
-      if (mine) {
-#pragma unroll
-        for (int k = 0; k < B; ++k) {
-          const uint32_t c = k0 + sub + k * subs;
-          const float f = c < n ? wt[h * n + c] : 0.f;
-          x.x = fmaf(y[k].x, f, x.x);
-          x.y = fmaf(y[k].y, f, x.y);
-          x.z = fmaf(y[k].z, f, x.z);
-          x.w = fmaf(y[k].w, f, x.w);
-        }
+      cp_wait<0>();
+#pragma unroll 4
+      for (uint32_t k = 0; k < left; ++k) {
+        const float4 y = *reinterpret_cast<const float4*>(stage + k * kAttnThreads);
+        const float f = wt[h * n + k0 + sub + k * subs];
+        x.x = fmaf(y.x, f, x.x);
+        x.y = fmaf(y.y, f, x.y);
+        x.z = fmaf(y.z, f, x.z);
+        x.w = fmaf(y.w, f, x.w);
       }
       k0 += B * subs;
       if (k0 >= n) {
