@@ -759,7 +759,8 @@ struct Attention {
     float* ml = reinterpret_cast<float*>(sm + M::ml) + kWarps * 32;
     float* wt = reinterpret_cast<float*>(sm + M::weights);  // [ncol][parts]
     const uint32_t n = c1 - c0 + 1, cols = ncol * (D / 4), subs = max(1u, kAttnThreads / cols);
-    // Parts of a thread in flight, in its own slots of what the ring leaves.
+    // Parts of a thread in flight, in its own slots of what the ring leaves: all of them in one wait where 38 CTAs share an
+    // item, and less code than sixteen in registers (32 sequences 126 us, was 128; 32 chosen blocks 11.5, was 11.8).
     constexpr int B = (M::big - M::parts) / (kAttnThreads * 16);
     uint4* stage = reinterpret_cast<uint4*>(sm + M::parts) + threadIdx.x;
     const size_t step = 2 * (size_t)(group * pack * (D + 4));
