@@ -746,6 +746,32 @@ def test_selection_tells_close_scores_apart(gap):
         check_choice(s, n, 0, 0)
 
 
+@pytest.mark.parametrize("blocks", [700, 2049, 20000])
+@pytest.mark.parametrize("kind", ["octaves", "outliers", "neighbours", "two values"])
+def test_selection_of_scores_of_every_spread(kind, blocks):
+    """Scores whose K-th largest needs one step of its search or all of them: one product each, exact in 32 bits."""
+    s = Setup("tiny", BF16, [16 * blocks], block=16)
+    s.q = torch.zeros_like(s.q)
+    s.q[0, 0, 0] = 1.0
+    g = torch.Generator().manual_seed(blocks)
+    x = torch.randperm(blocks, generator=g).double()
+    if kind == "octaves":
+        x = torch.where(x % 2 == 0, 1.0, -1.0) * 2.0 ** (x % 201 - 100)
+    elif kind == "outliers":
+        x = torch.where(x == 0, 2.0 ** 100, torch.where(x == 1, -2.0 ** 100, 1 + (x % 100) / 128))
+    elif kind == "neighbours":
+        x = (x % 30000 + 0x3000).to(torch.int16).view(torch.bfloat16).double()
+    else:
+        x = torch.where(x < blocks // 3, 1.0, -1.0)
+    n = s.total // 16
+    b = torch.zeros(n, 1, 2, s.D, dtype=torch.float64)
+    b[:blocks, 0, :, 0] = x[:, None]
+    s.lo_hi.copy_(b.to(torch.bfloat16).cuda())
+    for k in (1, 2, 50, blocks // 3, blocks // 3 + 1, blocks - 1):
+        check_choice(s, k, 0, 0)
+    check_choice(s, 50, 3, 2)
+
+
 def test_selection_with_infinities_and_nans():
     s = Setup("tiny", BF16, [1000], block=16)
     s.set_bounds()
