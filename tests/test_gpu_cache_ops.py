@@ -471,6 +471,15 @@ def test_attention_over_every_token(kw):
 
 
 @pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("heads,lens", [("tiny", [6000]), ("tiny", [9001, 3]), ("wide", [7000]), ("odd", [5000, 2500]),
+                                        ("twelve", [4500]), ("eight", [4000])])
+def test_attention_joined_from_many_parts(heads, lens, fmt):
+    """Few long sequences: up to every CTA of the GPU has a part of an item, more than a thread takes at a time."""
+    s = Setup(heads, fmt, lens, page=32)
+    s.check(s.attend())
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
 def test_attention_gate_and_its_stride(fmt):
     s = Setup("4b", fmt, [70, 300])
     gate = bf16(3 * s.rng.standard_normal((2, s.H, s.D)))
