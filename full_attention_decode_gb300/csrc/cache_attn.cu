@@ -19,10 +19,15 @@
 //
 // Roundings: bf16 K, V and q enter the products exactly, the weights P as hi + lo bf16
 // (2^-16 relative). Turbo8 codes enter as f16 (exact); the K scales multiply the fp32
-// products of their 16 dims; the rotated q enters as hi + lo f16 (2^-21). The weights are rounded to f16
-// (2^-12), multiplied by the V scales of each 16 dims and rounded to f16 again (2^-12); the
-// tile's largest scale goes into the exponent of the weights as a power of two, so that neither factor
-// leaves f16's range.
+// products of their 16 dims; the rotated q enters as hi + lo f16 (2^-21). A token's V scales enter as f16
+// over 2^E, E the exponent of the token's largest (exact down to 2^-17 of that one, lost below 2^-25), and E goes into
+// the exponent of the token's weight: the weights that multiply V are 2^(x + E - M), with a running maximum M of x + E of
+// their own, so a token counts by what it adds and not by its neighbours' sizes; the softmax sum keeps the
+// plain 2^x with its own maximum (128K tokens: 67 us; one power of two a tile, which lost tokens beside larger
+// ones, 64). The weights are rounded to f16 (2^-11), up to 2^13 so that f16 holds 2^-27 of the largest in full and what
+// lies 2^-38 below is lost, and rounded again with the scale (2^-11): next to the codes' own 2^-4 and
+// the output's 2^-8 these are small (error against 64 bits 0.00171 at 128K, of fp32 weights 0.00169), and a second
+// f16 for their rest (2^-21) takes 73 us.
 #include "cache_ops.cuh"
 #include "turbo8.cuh"
 
@@ -34,6 +39,9 @@ namespace {
 
 constexpr int kWarps = 8;  // of a CTA, one CTA an SM (16 warps of 128 registers for Turbo8: 84 us where 8 took 73)
 constexpr int kAttnThreads = 32 * kWarps;
+
+constexpr int kMl = 48;  // a warp's maxima, sums and (T8) the sums' maxima, 16 columns each
+constexpr float kUp = 13.f;  // T8: the largest weight of V is 2^kUp
 
 // A ring slot: K or V of 16 tokens. Rows are padded by 16 bytes, which puts eight rows'
 // 16-byte pieces in different banks.
@@ -57,8 +65,8 @@ struct Smem {
   static constexpr int big = ring > join ? (ring > parts ? ring : parts) : join > parts ? join : parts;
   static constexpr int qf = big;                                    // fragments, 8 or (T8) 16 bytes a lane
   static constexpr int qs = qf + (D / 16) * NT * 32 * (T8 ? 16 : 8);  // [8 NT][D] fp32
-  static constexpr int ml = qs + (T8 ? 8 * NT * D * 4 : 0);           // [warps + 1][2][16]
-  static constexpr int vsc = ml + (kWarps + 1) * 2 * 16 * 4;
+  static constexpr int ml = qs + (T8 ? 8 * NT * D * 4 : 0);           // [warps + 1][3][16]
+  static constexpr int vsc = ml + (kWarps + 1) * kMl * 4;
   static constexpr int scale_row = D / 8 + 4;  // words, padded
   static constexpr int misc = vsc + (T8 ? kWarps * scale_row * 16 : 0);
   static constexpr int first = misc + 256;  // [n_rows + 1]
@@ -119,6 +127,11 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
+__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
+  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
+                            *reinterpret_cast<const __half2*>(&c));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -175,6 +188,7 @@ struct Attention {
   uint32_t pack;  // the most rows of an item
   uint32_t ring;  // this warp's slots
   float m[NT][2], l[NT][2], o[D / 16][NT][4];
+  float lm[NT][2];  // T8: the maximum of this lane's scores, which l refers to (m is that of V's weights)
   uint32_t later[NT][2];  // tokens of the item's last row that this column's row does not see
   float qscale[NT][2];  // log2(e) / sqrt(D), with T8's power of two of q
 
@@ -213,7 +227,7 @@ struct Attention {
 
   // ---- K (p = 0) or V of a tile into a slot. Tokens no row sees read as zero; so do the V rows of
   // tokens that only later rows of the item see (add_tail): their weight is 0 in the earlier rows' columns,
-  // and 0 times an infinity would spoil them.
+  // and 0 times an infinity would spoil them. Their V scales are loaded: add_tail's weights need the exponents.
   __device__ void load(const Segment& s, const Tile& x, int p, uint32_t slot) const {
     const uint32_t last = s.pos + 1 - (p ? s.rows - 1 : 0);  // tokens below it
     const uint32_t seen = x.seen ? min(16u, last > x.token ? last - x.token : 0u) : 0u;
@@ -247,7 +261,7 @@ struct Attention {
       const uint8_t* sbase = reinterpret_cast<const uint8_t*>(p ? a.c.vs : a.c.ks);
       const uint32_t r = lane / P, c2 = lane % P;
       if (r < 16) {
-        const bool in = r < seen && (r & 8 ? x.in[1] : x.in[0]);
+        const bool in = r < x.seen && (r & 8 ? x.in[1] : x.in[0]);
         const size_t row = (r & 8 ? x.row[1] : x.row[0]) + (r & 7);
         const uint8_t* src = sbase + (row * a.c.sstride + s.g * (D / 16)) * 2 + c2 * 16;
         const uint32_t sto = dst + 16 * S::row + r * SB + c2 * 16;
@@ -411,9 +425,10 @@ struct Attention {
     }
   }
 
-  // ---- T8: a tile's V scales, divided by 2^e, as f16 pairs of tokens: word (c, g, h) has tokens 2c + 8h and
-  // 2c + 8h + 1 of dims group g; returns e
-  __device__ int v_scales(uint32_t slot) const {
+  // ---- T8: a tile's V scales, each token's over 2^e (e: the exponent of its largest), as f16 pairs of tokens: word
+  // (c, g, h) has tokens 2c + 8h and 2c + 8h + 1 of dims group g; those of tokens from `all` on, which not every
+  // row of the item sees, are 0. e0, e1: of the tokens of this lane's scores.
+  __device__ void v_scales(uint32_t slot, uint32_t all, int& e0, int& e1) const {
     const uint8_t* sc = sm + (ring - smem_addr(sm)) + slot * S::bytes + 16 * S::row;
     uint16_t* t = reinterpret_cast<uint16_t*>(sm + M::vsc + warp * M::scale_row * 16);
     constexpr int PER = D / 32;  // scales a lane: half a token's
@@ -424,24 +439,25 @@ struct Attention {
       const uint32_t u = *reinterpret_cast<const uint32_t*>(sc + tok * S::scales + (g0 + i) * 2);
       f[i] = bf16lo(u);
       f[i + 1] = bf16hi(u);
-      mx = fmaxf(mx, fmaxf(f[i], f[i + 1]));
+      mx = fmaxf(mx, fmaxf(fabsf(f[i]), fabsf(f[i + 1])));
     }
-    mx = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(mx)));  // scales are not negative
-    const int e = mx > 0.f ? min(max((int)(__float_as_uint(mx) >> 23) - 127, -60), 60) : -60;
+    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+    const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
     const float k = pow2(-e);
     uint16_t* to = t + ((tok & 7) >> 1) * M::scale_row * 2 + g0 * 4 + (tok >> 3) * 2 + (tok & 1);
 #pragma unroll
-    for (int i = 0; i < PER; ++i) to[i * 4] = __half_as_ushort(__float2half_rn(f[i] * k));
+    for (int i = 0; i < PER; ++i) to[i * 4] = tok < all ? __half_as_ushort(__float2half_rn(f[i] * k)) : 0;
+    e0 = __shfl_sync(0xffffffffu, e, lane >> 2 << 1);
+    e1 = __shfl_sync(0xffffffffu, e, (lane >> 2 << 1) + 16);
     __syncwarp();
-    return e;
   }
 
   // ---- one tile: weights from the scores, then the output from its V slot; the last row sees `seen` tokens
-  // from the tile's first on, those in a block outside the pool left out
-  __device__ __forceinline__ int accumulate(uint32_t slot, float (&s)[NT][4], uint32_t seen) {
+  // from the tile's first on, those in a block outside the pool left out. e0, e1: v_scales'
+  __device__ __forceinline__ void accumulate(uint32_t slot, float (&s)[NT][4], uint32_t seen, uint32_t rows, int& e0,
+                                             int& e1) {
     const uint32_t r = lane >> 2, seen0 = seen & kNo0 ? 0 : seen & 63u, seen1 = seen & kNo1 ? 0 : seen & 63u;
-    int ev = 0;
-    if constexpr (T8) ev = v_scales(slot);
+    if constexpr (T8) v_scales(slot, max(seen & 63u, rows - 1) - (rows - 1), e0, e1);
     uint32_t ph[NT][2], pl[NT][2];
     bool grew = false;
     float corr[NT][2];
@@ -450,12 +466,15 @@ struct Attention {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float x0 = s[nt][j] * qscale[nt][j], x1 = s[nt][2 + j] * qscale[nt][j];
-        if (T8) {
-          x0 += (float)ev;
-          x1 += (float)ev;
-        }
         if (r + later[nt][j] >= seen0) x0 = -INFINITY;
         if (r + 8 + later[nt][j] >= seen1) x1 = -INFINITY;
+        if constexpr (T8) {
+          const float ln = fmaxf(lm[nt][j], fmaxf(x0, x1)), lu = ln == -INFINITY ? 0.f : ln;
+          l[nt][j] = l[nt][j] * ex2(lm[nt][j] - lu) + (ex2(x0 - lu) + ex2(x1 - lu));
+          lm[nt][j] = ln;
+          x0 += (float)e0;
+          x1 += (float)e1;
+        }
         float mx = fmaxf(x0, x1);
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
@@ -463,10 +482,10 @@ struct Attention {
         corr[nt][j] = m[nt][j] == mn ? 1.f : ex2(m[nt][j] - mu);
         grew |= m[nt][j] != mn;
         m[nt][j] = mn;
-        s[nt][j] = ex2(x0 - mu);
-        s[nt][2 + j] = ex2(x1 - mu);
-        const float sum = s[nt][j] + s[nt][2 + j];
-        l[nt][j] = l[nt][j] * corr[nt][j] + (T8 ? sum * pow2(-ev) : sum);
+        const float ref = T8 ? mu - kUp : mu;
+        s[nt][j] = ex2(x0 - ref);
+        s[nt][2 + j] = ex2(x1 - ref);
+        if constexpr (!T8) l[nt][j] = l[nt][j] * corr[nt][j] + (s[nt][j] + s[nt][2 + j]);
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // tokens 0-7, 8-15: [token][head] to [head][token]
@@ -526,18 +545,18 @@ struct Attention {
         }
       }
     }
-    return ev;
   }
 
   // ---- the tokens of a tile that the item's first row does not see (the call's own later rows: at most
   // seven): their V from the cache, weight times value in the columns that see them
-  __device__ void add_tail(const Segment& sg, uint32_t t, const float (&p)[NT][4], int ev) {
+  __device__ void add_tail(const Segment& sg, uint32_t t, const float (&p)[NT][4], int e0, int e1) {
     const Tile x = tile(sg, t);
     const uint32_t first = sg.pos + 2 - sg.rows, r = lane >> 2;  // the first such token
     for (uint32_t k = first > x.token ? first - x.token : 0u; k < min(x.seen, 16u); ++k) {
       if (!(k & 8 ? x.in[1] : x.in[0])) continue;
       const size_t row = (k & 8 ? x.row[1] : x.row[0]) + (k & 7);
       const size_t at = (row * a.c.Hkv + sg.g) * D;
+      const int ev = T8 ? __shfl_sync(0xffffffffu, k & 8 ? e1 : e0, (k & 7) * 4) : 0;
       float w[NT][2];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
@@ -584,6 +603,7 @@ struct Attention {
       for (int j = 0; j < 2; ++j) {
         m[nt][j] = -INFINITY;
         l[nt][j] = 0.f;
+        lm[nt][j] = -INFINITY;
         later[nt][j] = s.rows - 1 - min((8 * nt + 2 * (lane & 3) + j) / group, s.rows - 1);
       }
 #pragma unroll
@@ -608,8 +628,9 @@ struct Attention {
           seen = seen2;  // the copies are one tile ahead
           if (seen) scores(slot, sc);
         } else if (seen) {
-          const int ev = accumulate(slot, sc, seen);
-          if ((seen & 63u) < 16 + s.rows - 1 && s.rows > 1) add_tail(s, first + (h >> 1) * kWarps, sc, ev);
+          int e0 = 0, e1 = 0;
+          accumulate(slot, sc, seen, s.rows, e0, e1);
+          if ((seen & 63u) < 16 + s.rows - 1 && s.rows > 1) add_tail(s, first + (h >> 1) * kWarps, sc, e0, e1);
         }
         __syncwarp();  // this half-tile has been read by every lane
       }
@@ -627,7 +648,7 @@ struct Attention {
     }
     cp_wait<0>();
   }
-  // ---- the warps' outputs added up: sum [cols][D + 4] at sm, M and L at ml[kWarps]
+  // ---- the warps' outputs added up: sum [cols][D + 4] at sm, M, L and (T8) L's maximum at ml[kWarps]
   __device__ void join_warps(uint32_t cols, uint32_t warps) {
     float* ml = reinterpret_cast<float*>(sm + M::ml);
     float* red = reinterpret_cast<float*>(sm);
@@ -637,11 +658,18 @@ struct Attention {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float x = l[nt][j];
+        if constexpr (T8) {
+          float mx = lm[nt][j];
+#pragma unroll
+          for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+          x *= rescale(lm[nt][j], mx);
+          if (r == 0) ml[warp * kMl + 32 + 8 * nt + 2 * c + j] = mx;
+        }
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
         if (r == 0) {
-          ml[warp * 32 + 8 * nt + 2 * c + j] = m[nt][j];
-          ml[warp * 32 + 16 + 8 * nt + 2 * c + j] = x;
+          ml[warp * kMl + 8 * nt + 2 * c + j] = m[nt][j];
+          ml[warp * kMl + 16 + 8 * nt + 2 * c + j] = x;
         }
       }
     __syncthreads();  // the rings are free too
@@ -651,7 +679,7 @@ struct Attention {
       for (int j = 0; j < 2; ++j) {
         const uint32_t h = 8 * nt + 2 * c + j;
         float mx = -INFINITY;
-        for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * 32 + h]);
+        for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * kMl + h]);
         const float f = rescale(m[nt][j], mx);
         if (h < cols && warp < warps) {
           float* to = red + (warp * cols + h) * (D + 4);
@@ -665,11 +693,14 @@ struct Attention {
       }
     if (threadIdx.x < 8 * NT) {
       const uint32_t h = threadIdx.x;
-      float mx = -INFINITY, sum = 0.f;
-      for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * 32 + h]);
-      for (uint32_t w = 0; w < warps; ++w) sum += ml[w * 32 + 16 + h] * rescale(ml[w * 32 + h], mx);
-      ml[kWarps * 32 + h] = mx;
-      ml[kWarps * 32 + 16 + h] = sum;
+      constexpr int of = T8 ? 32 : 0;  // the maxima that the sums refer to
+      float mx = -INFINITY, sum = 0.f, of_sum = -INFINITY;
+      for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * kMl + h]);
+      for (uint32_t w = 0; w < warps; ++w) of_sum = fmaxf(of_sum, ml[w * kMl + of + h]);
+      for (uint32_t w = 0; w < warps; ++w) sum += ml[w * kMl + 16 + h] * rescale(ml[w * kMl + of + h], of_sum);
+      ml[kWarps * kMl + h] = mx;
+      ml[kWarps * kMl + 16 + h] = sum;
+      if (T8) ml[kWarps * kMl + 32 + h] = of_sum;
     }
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < cols * (D / 4); i += kAttnThreads) {
@@ -710,7 +741,7 @@ struct Attention {
   }
   __device__ void store(const Segment& s, const Gates& gates) {
     const float* red = reinterpret_cast<const float*>(sm);
-    const float* L = reinterpret_cast<const float*>(sm + M::ml) + kWarps * 32 + 16;
+    const float* ml = reinterpret_cast<const float*>(sm + M::ml) + kWarps * kMl;
     constexpr int LPR = D / 8;
 #pragma unroll
     for (int k = 0; k < kOut; ++k) {
@@ -718,9 +749,14 @@ struct Attention {
       if (i >= 8 * NT * LPR) break;  // whole warps
       float x[8] = {};
       if (h < group * s.rows) {
-        const float inv = L[h] == 0.f ? 0.f : 1.0f / L[h];
+        const float L = ml[16 + h], inv = L == 0.f ? 0.f : 1.0f / L;
+        // T8: times 2^(M - kUp - L's maximum), in two steps: it may be 2^-150 where the sums are large
+        const float up = !T8 ? 1.f : L == 0.f ? 0.f : ex2(0.5f * (ml[h] - ml[32 + h] - kUp));
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = red[h * (D + 4) + 8 * c + e] * inv;
+        for (int e = 0; e < 8; ++e) {
+          x[e] = red[h * (D + 4) + 8 * c + e] * inv;
+          if (T8) x[e] = x[e] * up * up;
+        }
       }
       if constexpr (T8) wht8<LPR>(x, lane);
       if (h < group * s.rows) {
@@ -739,10 +775,10 @@ struct Attention {
   __device__ float* part(uint32_t cta, uint32_t slot) const {
     return a.parts + ((size_t)cta * 2 + slot) * (group * pack * (D + 4));
   }
-  // Part: for each column D sums, M, L and two words of padding.
+  // Part: for each column D sums, M, L, (T8) L's maximum and padding.
   __device__ void store_part(uint32_t slot, uint32_t cols) {
     const float* red = reinterpret_cast<const float*>(sm);
-    const float* ml = reinterpret_cast<const float*>(sm + M::ml) + kWarps * 32;
+    const float* ml = reinterpret_cast<const float*>(sm + M::ml) + kWarps * kMl;
     float* to = part(blockIdx.x, slot);
     for (uint32_t i = threadIdx.x; i < cols * (D / 4); i += kAttnThreads) {
       const uint32_t at = (i / (D / 4)) * (D + 4) + 4 * (i % (D / 4));
@@ -750,13 +786,13 @@ struct Attention {
     }
     if (threadIdx.x < cols)
       __stcg(reinterpret_cast<float4*>(to + threadIdx.x * (D + 4) + D),
-             make_float4(ml[threadIdx.x], ml[16 + threadIdx.x], 0.f, 0.f));
+             make_float4(ml[threadIdx.x], ml[16 + threadIdx.x], T8 ? ml[32 + threadIdx.x] : 0.f, 0.f));
   }
   // The parts of CTAs c0 .. c1 added up, as join_warps leaves its sums: a thread has four dims of a column and,
   // where there are fewer such columns than threads, every subs-th part. The order is fixed by c0 and c1.
   __device__ void join_parts(uint32_t c0, uint32_t c1, uint32_t ncol) {
     float* red = reinterpret_cast<float*>(sm);  // [subs][ncol][D + 4]
-    float* ml = reinterpret_cast<float*>(sm + M::ml) + kWarps * 32;
+    float* ml = reinterpret_cast<float*>(sm + M::ml) + kWarps * kMl;
     float* wt = reinterpret_cast<float*>(sm + M::weights);  // [ncol][parts]
     const uint32_t n = c1 - c0 + 1, cols = ncol * (D / 4), subs = max(1u, kAttnThreads / cols);
     // Parts of a thread in flight, in its own slots of what the ring leaves: all of them in one wait where 38 CTAs share an
@@ -782,29 +818,40 @@ struct Attention {
       cp_commit();
       if (i0 == 0 && k0 == 0) {  // the weights, their loads in the same wait as the first parts'
         for (uint32_t hh = warp; hh < ncol; hh += kWarps) {
-          float mx = -INFINITY, sum = 0.f;
+          float mx = -INFINITY, sum = 0.f, of_sum = -INFINITY;
           constexpr int U = (kMaxCtas + 31) / 32;
           float2 z[U];
+          float zm[U];  // what a part's sum refers to
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const uint32_t c = c0 + lane + 32 * u;
             z[u] = make_float2(-INFINITY, 0.f);
-            if (c <= c1) z[u] = __ldcg(reinterpret_cast<const float2*>(part(c, c == c0) + hh * (D + 4) + D));
+            zm[u] = -INFINITY;
+            if (c <= c1) {
+              const float* from = part(c, c == c0) + hh * (D + 4) + D;
+              z[u] = __ldcg(reinterpret_cast<const float2*>(from));
+              zm[u] = T8 ? __ldcg(from + 2) : z[u].x;
+            }
           }
 #pragma unroll
-          for (int u = 0; u < U; ++u) mx = fmaxf(mx, z[u].x);
+          for (int u = 0; u < U; ++u) {
+            mx = fmaxf(mx, z[u].x);
+            of_sum = fmaxf(of_sum, zm[u]);
+          }
           mx = warp_max(mx);
+          of_sum = T8 ? warp_max(of_sum) : mx;
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const uint32_t c = lane + 32 * u;
             const float f = rescale(z[u].x, mx);
             if (c < n) wt[hh * n + c] = f;
-            sum += z[u].y * f;
+            sum += z[u].y * (T8 ? rescale(zm[u], of_sum) : f);
           }
           sum = warp_sum(sum);
           if (lane == 0) {
             ml[hh] = mx;
             ml[16 + hh] = sum;
+            if (T8) ml[32 + hh] = of_sum;
           }
         }
         __syncthreads();

@@ -546,7 +546,11 @@ QWEN35_API int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_ca
  *    `block` tokens (16 to 1024, a power of two that divides capacity and, in a paged
  *    cache, block_tokens). An entry that is negative or behind the row's last
  *    block counts as none, one listed twice counts twice; a row without a token gets zeros.
- * Sums, maxima and weights are held in fp32 and the output rounded to bf16 once. Keys with
+ * Scores, maxima and sums are held in fp32 and the output is rounded to bf16 once. The weights
+ * enter the products with V rounded: as two bf16 parts (2^-16) with a bf16 cache, as f16 (2^-11) before and
+ * after the product with the token's V scale with a Turbo8 cache, relative to what the token adds: how large other
+ * tokens' values are does not matter (a token that adds less than 2^-38 of what another adds may count as
+ * nothing, and so may a group of 16 rotated values below 2^-25 of its own token's largest). Keys with
  * an infinity or NaN spoil only rows that see them. out must not overlap an input. Errors
  * as qwen35_cache_append. */
 QWEN35_API int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,

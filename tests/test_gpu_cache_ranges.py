@@ -1,0 +1,105 @@
+"""The cache operators on values far apart in size, against plain float64 implementations.
+
+Tolerance of the attention over a Turbo8 cache, derived before the first run: the
+output's bf16 rounding, 2^-8 of its norm (the rotation back keeps norms); a weight is off
+by at most 2^-14 (scores of up to 128 octaves in fp32: D / 16 + 4 roundings of 2^-24 each,
+in octaves, times ln 2, in the weight and in the sum), is rounded to f16 before and after
+the product with its V scale (2^-11 each), and a group of 16 values far below its own
+token's largest loses 2^-25 of that one. All of it is relative to what a token adds, so to
+|sum_t w_t |v_t|| (v_t rotated, as the cache holds it), and not to the largest value a
+row sees: 2^-10 + 2^-12 of it in all.
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from full_attention_decode_gb300 import binding as B
+from oracle import qwen35_oracle as O
+
+from test_gpu_cache_ops import BF16, TURBO8, Setup, bf16, f64
+
+pytestmark = pytest.mark.gpu
+
+
+def put(s, name, b, x):
+    """Rows x [tokens][Hkv][D] of sequence b into the cache, and what they stand for."""
+    x = f64(bf16(x))
+    at = torch.from_numpy(np.asarray(s.at(b, np.arange(len(x)))))
+    if s.fmt == BF16:
+        s.t[name][at.cuda()] = bf16(x).cuda()
+        s.stands[name][at] = x
+        return
+    c, sc = O.turbo8_quantize(O.bf16_round(O.wht(x)))
+    s.t[name][at.cuda()] = torch.from_numpy(c).cuda()
+    groups = s.Hkv * s.D // 16
+    s.t[name + "s"][at.cuda(), :groups] = torch.from_numpy(O.bf16_bits(sc).reshape(-1, groups).view(np.int16)).cuda()
+    s.stands[name][at] = O.wht(O.turbo8_dequantize(c, sc))
+
+
+def along(s, scores):
+    """q of every row along one direction a head group, and keys whose scores are `scores` octaves (before
+    the cache's rounding), [tokens]."""
+    rng = np.random.default_rng(17)
+    u = rng.choice([-1.0, 1.0], size=(s.Hkv, s.D))
+    q = np.repeat(u, s.H // s.Hkv, 0)  # q.k / sqrt(D) = sqrt(D) a for k = a u
+    s.q = bf16(np.broadcast_to(q, (s.n_rows, s.H, s.D))).contiguous()
+    return np.asarray(scores)[:, None, None] * np.log(2) / np.sqrt(s.D) * u
+
+
+def weighted(s, row, b, p):
+    """float64 attention of one row and sum_t w_t |v_t| of its rotated values, [H][D] each."""
+    g, rows = s.H // s.Hkv, s.at(b, np.arange(p + 1))
+    out, size = np.zeros((s.H, s.D)), np.zeros((s.H, s.D))
+    for h in range(s.H):
+        k, v = s.stands["k"][rows, h // g], s.stands["v"][rows, h // g]
+        x = k @ f64(s.q[row, h]) / np.sqrt(s.D)
+        w = np.exp(x - x.max())
+        w /= w.sum()
+        out[h], size[h] = w @ v, w @ np.abs(O.wht(v) if s.fmt == TURBO8 else v)
+    return out, size
+
+
+def check_weighted(s):
+    got = f64(s.attend())
+    assert s.status() == 0
+    for row, b, p in s.each_row():
+        ref, size = weighted(s, row, b, p)
+        err = np.linalg.norm(got[row] - ref, axis=1)
+        bound = 2.0 ** -8 * np.linalg.norm(ref, axis=1) + (2.0 ** -10 + 2.0 ** -12) * np.linalg.norm(size, axis=1)
+        assert np.all(err <= bound), (row, b, p, float((err / bound).max()))
+
+
+# octaves: of the small values, how far the large ones lie above them, how far their scores lie below
+SIZES = [(0, 0, 0), (-10, 15, 40), (0, 20, 60), (0, 24, 60), (-10, 30, 60), (0, 40, 30), (0, 100, 0), (-60, 100, 120),
+         (80, 20, 40), (112, 4, 3), (-112, 4, 3), (-100, 180, 3)]
+
+
+@pytest.mark.parametrize("kw", [dict(heads="tiny", lens=[40, 17]), dict(heads="4b", lens=[100], page=16),
+                                dict(heads="wide", lens=[70]), dict(heads="twelve", lens=[50, 33], page=8),
+                                dict(heads="tiny_alt", lens=[37, 60], rows=[5, 3]),
+                                dict(heads="odd", lens=[18, 40], rows=[3, 2], page=32),
+                                dict(heads="tiny", lens=[3000])], ids=str)
+@pytest.mark.parametrize("sizes", SIZES, ids=str)
+def test_turbo8_attention_counts_a_token_by_what_it_adds(kw, sizes):
+    """Tokens of large values and low scores among ones of small values and high scores: in most tiles, in the
+    call's own rows and in other tiles than the small ones."""
+    small, ratio, gap = sizes
+    s = Setup(fmt=TURBO8, **kw)
+    rng = np.random.default_rng(5)
+    for b, m in enumerate(s.lens):
+        large = rng.random(m) < 0.2
+        large[m // 2:m // 2 + 20] = m > 100
+        large[-1] = not large[-2]
+        put(s, "k", b, along(s, np.where(large, -gap / 2, gap / 2) + rng.uniform(-1, 1, m)))
+        put(s, "v", b, rng.standard_normal((m, s.Hkv, s.D)) * np.exp2(small + ratio * large)[:, None, None])
+    check_weighted(s)
+
+
+def test_turbo8_attention_of_a_small_value_beside_a_large_one_of_no_weight():
+    """Two tokens: scales 30 octaves apart, the large one's score 60 octaves below."""
+    s = Setup("tiny", TURBO8, [2])
+    put(s, "k", 0, along(s, [-30, 30]))
+    put(s, "v", 0, np.stack([np.full((1, s.D), 2.0 ** 20), np.full((1, s.D), 2.0 ** -10)]))
+    check_weighted(s)
+    assert np.all(np.abs(f64(s.attend())[0] / 2.0 ** -10 - 1) < 2.0 ** -6)
