@@ -21,9 +21,10 @@
 // (2^-16 relative). Turbo8 codes enter as f16 (exact); the K scales multiply the fp32
 // products of their 16 dims; the rotated q enters as hi + lo f16 (2^-21). A token's V scales enter as f16
 // over 2^E, E the exponent of the token's largest (exact down to 2^-17 of that one, lost below 2^-25), and E goes into
-// the exponent of the token's weight: the weights that multiply V are 2^(x + E - M), with a running maximum M of x + E of
-// their own, so a token counts by what it adds and not by its neighbours' sizes; the softmax sum keeps the
-// plain 2^x with its own maximum (128K tokens: 67 us; one power of two a tile, which lost tokens beside larger
+// the exponent of the token's weight: the weights that multiply V are 2^((x - m) + E - M), M the running
+// maximum of (x - m) + E, so a token counts by what it adds and not by its neighbours' sizes, and E is
+// added where large scores have cancelled. m, which the softmax's sum refers to, follows the scores only when one
+// lies 32 octaves above it: 32 bits have room for that, and the lanes exchange one maximum a tile (128K tokens: 68 us; one power of two a tile, which lost tokens beside larger
 // ones, 64). The weights are rounded to f16 (2^-11), up to 2^13 so that f16 holds 2^-27 of the largest in full and what
 // lies 2^-38 below is lost, and rounded again with the scale (2^-11): next to the codes' own 2^-4 and
 // the output's 2^-8 these are small (error against 64 bits 0.00171 at 128K, of fp32 weights 0.00169), and a second
@@ -40,8 +41,9 @@ namespace {
 constexpr int kWarps = 8;  // of a CTA, one CTA an SM (16 warps of 128 registers for Turbo8: 84 us where 8 took 73)
 constexpr int kAttnThreads = 32 * kWarps;
 
-constexpr int kMl = 48;  // a warp's maxima, sums and (T8) the sums' maxima, 16 columns each
+constexpr int kMl = 48;  // a warp's maxima, sums and (T8) maxima of V's weights, 16 columns each
 constexpr float kUp = 13.f;  // T8: the largest weight of V is 2^kUp
+constexpr float kFar = 32.f;  // T8: how far a score may lie above what the sum refers to
 
 // A ring slot: K or V of 16 tokens. Rows are padded by 16 bytes, which puts eight rows'
 // 16-byte pieces in different banks.
@@ -127,11 +129,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
   const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
   return *reinterpret_cast<const uint32_t*>(&r);
 }
-__device__ __forceinline__ uint32_t hfma2(uint32_t a, uint32_t b, uint32_t c) {
-  const __half2 r = __hfma2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b),
-                            *reinterpret_cast<const __half2*>(&c));
-  return *reinterpret_cast<const uint32_t*>(&r);
-}
 __device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
   const __half2 r = __floats2half2_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&r);
@@ -146,6 +143,14 @@ __device__ __forceinline__ float ex2(float x) {  // 2^x to 2^-22 relative; 0 bel
   return r;
 }
 __device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
+// The maximum over the eight lanes of a column.
+__device__ __forceinline__ float col_max(float x) {
+#pragma unroll
+  for (int w = 4; w < 32; w <<= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, w));
+  return x;
+}
+// What is subtracted for a maximum: 0 where there is nothing yet.
+__device__ __forceinline__ float finite_or_0(float mx) { return mx == -INFINITY ? 0.f : mx; }
 __device__ __forceinline__ float rescale(float from, float to) { return from == -INFINITY ? 0.f : ex2(from - to); }
 
 // One item's stretch in a CTA: rows row .. row + rows - 1, the last at position pos.
@@ -187,8 +192,8 @@ struct Attention {
   uint32_t warp, lane, group;
   uint32_t pack;  // the most rows of an item
   uint32_t ring;  // this warp's slots
-  float m[NT][2], l[NT][2], o[D / 16][NT][4];
-  float lm[NT][2];  // T8: the maximum of this lane's scores, which l refers to (m is that of V's weights)
+  float m[NT][2], l[NT][2], o[D / 16][NT][4];  // m: the scores' maximum (T8: or up to kFar below it), which l refers to
+  float mv[NT][2];  // T8: the maximum of V's weights, relative to m, which o refers to
   uint32_t later[NT][2];  // tokens of the item's last row that this column's row does not see
   float qscale[NT][2];  // log2(e) / sqrt(D), with T8's power of two of q
 
@@ -459,34 +464,55 @@ struct Attention {
     const uint32_t r = lane >> 2, seen0 = seen & kNo0 ? 0 : seen & 63u, seen1 = seen & kNo1 ? 0 : seen & 63u;
     if constexpr (T8) v_scales(slot, max(seen & 63u, rows - 1) - (rows - 1), e0, e1);
     uint32_t ph[NT][2], pl[NT][2];
-    bool grew = false;
+    bool grew = false, far = false;
     float corr[NT][2];
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        float x0 = s[nt][j] * qscale[nt][j], x1 = s[nt][2 + j] * qscale[nt][j];
-        if (r + later[nt][j] >= seen0) x0 = -INFINITY;
-        if (r + 8 + later[nt][j] >= seen1) x1 = -INFINITY;
-        if constexpr (T8) {
-          const float ln = fmaxf(lm[nt][j], fmaxf(x0, x1)), lu = ln == -INFINITY ? 0.f : ln;
-          l[nt][j] = l[nt][j] * ex2(lm[nt][j] - lu) + (ex2(x0 - lu) + ex2(x1 - lu));
-          lm[nt][j] = ln;
-          x0 += (float)e0;
-          x1 += (float)e1;
-        }
-        float mx = fmaxf(x0, x1);
+        s[nt][j] = r + later[nt][j] >= seen0 ? -INFINITY : s[nt][j] * qscale[nt][j];
+        s[nt][2 + j] = r + 8 + later[nt][j] >= seen1 ? -INFINITY : s[nt][2 + j] * qscale[nt][j];
+        far |= fmaxf(s[nt][j], s[nt][2 + j]) > m[nt][j] + kFar;
+      }
+    if constexpr (T8) {
+      if (__any_sync(0xffffffffu, far))  // the first tile, as a rule
 #pragma unroll
-        for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-        const float mn = fmaxf(m[nt][j], mx), mu = mn == -INFINITY ? 0.f : mn;
-        corr[nt][j] = m[nt][j] == mn ? 1.f : ex2(m[nt][j] - mu);
-        grew |= m[nt][j] != mn;
-        m[nt][j] = mn;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const float mx = col_max(fmaxf(s[nt][j], s[nt][2 + j])), down = m[nt][j] - mx;
+            if (mx > m[nt][j] + kFar) {
+              l[nt][j] *= ex2(down);
+              mv[nt][j] += down;
+              m[nt][j] = mx;
+            }
+          }
+    }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        float mn, mu;
+        if constexpr (T8) {
+          mu = finite_or_0(m[nt][j]);
+          const float x0 = s[nt][j] - mu, x1 = s[nt][2 + j] - mu;
+          l[nt][j] += ex2(x0) + ex2(x1);
+          s[nt][j] = x0 + (float)e0;
+          s[nt][2 + j] = x1 + (float)e1;
+        }
+        float& top = T8 ? mv[nt][j] : m[nt][j];
+        mn = fmaxf(top, col_max(fmaxf(s[nt][j], s[nt][2 + j])));
+        mu = finite_or_0(mn);
+        corr[nt][j] = top == mn ? 1.f : ex2(top - mu);
+        grew |= top != mn;
+        top = mn;
         const float ref = T8 ? mu - kUp : mu;
-        s[nt][j] = ex2(x0 - ref);
-        s[nt][2 + j] = ex2(x1 - ref);
+        s[nt][j] = ex2(s[nt][j] - ref);
+        s[nt][2 + j] = ex2(s[nt][2 + j] - ref);
         if constexpr (!T8) l[nt][j] = l[nt][j] * corr[nt][j] + (s[nt][j] + s[nt][2 + j]);
       }
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int h = 0; h < 2; ++h) {  // tokens 0-7, 8-15: [token][head] to [head][token]
         const float u = s[nt][2 * h], v = s[nt][2 * h + 1];
@@ -498,7 +524,6 @@ struct Attention {
           pl[nt][h] = transpose8x8(pack_bf16(u - bf16lo(hi), v - bf16hi(hi)));
         }
       }
-    }
     if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
       for (int d = 0; d < D / 16; ++d)
@@ -603,7 +628,7 @@ struct Attention {
       for (int j = 0; j < 2; ++j) {
         m[nt][j] = -INFINITY;
         l[nt][j] = 0.f;
-        lm[nt][j] = -INFINITY;
+        mv[nt][j] = -INFINITY;
         later[nt][j] = s.rows - 1 - min((8 * nt + 2 * (lane & 3) + j) / group, s.rows - 1);
       }
 #pragma unroll
@@ -648,7 +673,20 @@ struct Attention {
     }
     cp_wait<0>();
   }
-  // ---- the warps' outputs added up: sum [cols][D + 4] at sm, M, L and (T8) L's maximum at ml[kWarps]
+  // T8: the largest of the warps' maxima in column h, and of V's relative to it (warps without a tile have -infinity)
+  __device__ __forceinline__ static float2 tops(const float* ml, uint32_t h) {
+    float m[kWarps], v[kWarps], mx = -INFINITY, vx = -INFINITY;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      m[w] = ml[w * kMl + h];
+      v[w] = ml[w * kMl + 32 + h];
+      mx = fmaxf(mx, m[w]);
+    }
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) vx = fmaxf(vx, v[w] + (m[w] - finite_or_0(mx)));
+    return make_float2(mx, vx);
+  }
+  // ---- the warps' outputs added up: sum [cols][D + 4] at sm, M, L and (T8) V's maximum at ml[kWarps]
   __device__ void join_warps(uint32_t cols, uint32_t warps) {
     float* ml = reinterpret_cast<float*>(sm + M::ml);
     float* red = reinterpret_cast<float*>(sm);
@@ -658,18 +696,12 @@ struct Attention {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         float x = l[nt][j];
-        if constexpr (T8) {
-          float mx = lm[nt][j];
-#pragma unroll
-          for (int w = 4; w < 32; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          x *= rescale(lm[nt][j], mx);
-          if (r == 0) ml[warp * kMl + 32 + 8 * nt + 2 * c + j] = mx;
-        }
 #pragma unroll
         for (int w = 4; w < 32; w <<= 1) x += __shfl_xor_sync(0xffffffffu, x, w);
         if (r == 0) {
           ml[warp * kMl + 8 * nt + 2 * c + j] = m[nt][j];
           ml[warp * kMl + 16 + 8 * nt + 2 * c + j] = x;
+          if (T8) ml[warp * kMl + 32 + 8 * nt + 2 * c + j] = mv[nt][j];
         }
       }
     __syncthreads();  // the rings are free too
@@ -678,9 +710,14 @@ struct Attention {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const uint32_t h = 8 * nt + 2 * c + j;
-        float mx = -INFINITY;
-        for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * kMl + h]);
-        const float f = rescale(m[nt][j], mx);
+        float f, mx = -INFINITY;
+        if constexpr (T8) {
+          const float2 top = tops(ml, h);
+          f = rescale(mv[nt][j] + (m[nt][j] - finite_or_0(top.x)), top.y);
+        } else {
+          for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * kMl + h]);
+          f = rescale(m[nt][j], mx);
+        }
         if (h < cols && warp < warps) {
           float* to = red + (warp * cols + h) * (D + 4);
 #pragma unroll
@@ -693,14 +730,12 @@ struct Attention {
       }
     if (threadIdx.x < 8 * NT) {
       const uint32_t h = threadIdx.x;
-      constexpr int of = T8 ? 32 : 0;  // the maxima that the sums refer to
-      float mx = -INFINITY, sum = 0.f, of_sum = -INFINITY;
+      float mx = -INFINITY, sum = 0.f;
       for (uint32_t w = 0; w < warps; ++w) mx = fmaxf(mx, ml[w * kMl + h]);
-      for (uint32_t w = 0; w < warps; ++w) of_sum = fmaxf(of_sum, ml[w * kMl + of + h]);
-      for (uint32_t w = 0; w < warps; ++w) sum += ml[w * kMl + 16 + h] * rescale(ml[w * kMl + of + h], of_sum);
+      for (uint32_t w = 0; w < warps; ++w) sum += ml[w * kMl + 16 + h] * rescale(ml[w * kMl + h], mx);
       ml[kWarps * kMl + h] = mx;
       ml[kWarps * kMl + 16 + h] = sum;
-      if (T8) ml[kWarps * kMl + 32 + h] = of_sum;
+      if (T8) ml[kWarps * kMl + 32 + h] = tops(ml, h).y;
     }
     __syncthreads();
     for (uint32_t i = threadIdx.x; i < cols * (D / 4); i += kAttnThreads) {
@@ -750,8 +785,8 @@ struct Attention {
       float x[8] = {};
       if (h < group * s.rows) {
         const float L = ml[16 + h], inv = L == 0.f ? 0.f : 1.0f / L;
-        // T8: times 2^(M - kUp - L's maximum), in two steps: it may be 2^-150 where the sums are large
-        const float up = !T8 ? 1.f : L == 0.f ? 0.f : ex2(0.5f * (ml[h] - ml[32 + h] - kUp));
+        // T8: times 2^(V's maximum - kUp), in two steps: it may be 2^-140 where the sums are large
+        const float up = !T8 ? 1.f : L == 0.f ? 0.f : ex2(0.5f * (ml[32 + h] - kUp));
 #pragma unroll
         for (int e = 0; e < 8; ++e) {
           x[e] = red[h * (D + 4) + 8 * c + e] * inv;
@@ -775,7 +810,7 @@ struct Attention {
   __device__ float* part(uint32_t cta, uint32_t slot) const {
     return a.parts + ((size_t)cta * 2 + slot) * (group * pack * (D + 4));
   }
-  // Part: for each column D sums, M, L, (T8) L's maximum and padding.
+  // Part: for each column D sums, M, L, (T8) V's maximum and padding.
   __device__ void store_part(uint32_t slot, uint32_t cols) {
     const float* red = reinterpret_cast<const float*>(sm);
     const float* ml = reinterpret_cast<const float*>(sm + M::ml) + kWarps * kMl;
@@ -818,40 +853,44 @@ struct Attention {
       cp_commit();
       if (i0 == 0 && k0 == 0) {  // the weights, their loads in the same wait as the first parts'
         for (uint32_t hh = warp; hh < ncol; hh += kWarps) {
-          float mx = -INFINITY, sum = 0.f, of_sum = -INFINITY;
+          float mx = -INFINITY, sum = 0.f, vx = -INFINITY;
           constexpr int U = (kMaxCtas + 31) / 32;
           float2 z[U];
-          float zm[U];  // what a part's sum refers to
+          float zv[U];  // T8: V's maximum
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const uint32_t c = c0 + lane + 32 * u;
             z[u] = make_float2(-INFINITY, 0.f);
-            zm[u] = -INFINITY;
+            zv[u] = -INFINITY;
             if (c <= c1) {
               const float* from = part(c, c == c0) + hh * (D + 4) + D;
               z[u] = __ldcg(reinterpret_cast<const float2*>(from));
-              zm[u] = T8 ? __ldcg(from + 2) : z[u].x;
+              if (T8) zv[u] = __ldcg(from + 2);
             }
           }
 #pragma unroll
-          for (int u = 0; u < U; ++u) {
-            mx = fmaxf(mx, z[u].x);
-            of_sum = fmaxf(of_sum, zm[u]);
-          }
+          for (int u = 0; u < U; ++u) mx = fmaxf(mx, z[u].x);
           mx = warp_max(mx);
-          of_sum = T8 ? warp_max(of_sum) : mx;
+          if constexpr (T8) {
+#pragma unroll
+            for (int u = 0; u < U; ++u) {
+              zv[u] += z[u].x - finite_or_0(mx);
+              vx = fmaxf(vx, zv[u]);
+            }
+            vx = warp_max(vx);
+          }
 #pragma unroll
           for (int u = 0; u < U; ++u) {
             const uint32_t c = lane + 32 * u;
             const float f = rescale(z[u].x, mx);
-            if (c < n) wt[hh * n + c] = f;
-            sum += z[u].y * (T8 ? rescale(zm[u], of_sum) : f);
+            if (c < n) wt[hh * n + c] = T8 ? rescale(zv[u], vx) : f;
+            sum += z[u].y * f;
           }
           sum = warp_sum(sum);
           if (lane == 0) {
             ml[hh] = mx;
             ml[16 + hh] = sum;
-            if (T8) ml[32 + hh] = of_sum;
+            if (T8) ml[32 + hh] = vx;
           }
         }
         __syncthreads();

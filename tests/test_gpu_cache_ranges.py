@@ -103,3 +103,17 @@ def test_turbo8_attention_of_a_small_value_beside_a_large_one_of_no_weight():
     put(s, "v", 0, np.stack([np.full((1, s.D), 2.0 ** 20), np.full((1, s.D), 2.0 ** -10)]))
     check_weighted(s)
     assert np.all(np.abs(f64(s.attend())[0] / 2.0 ** -10 - 1) < 2.0 ** -6)
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("q_size,k_size", [(6, 8), (10, 12), (20, 60), (100, -110), (60, -60)])
+@pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "wide"])
+def test_attention_of_very_large_and_very_small_keys(heads, q_size, k_size, fmt):
+    """Scores of 2^14 octaves and more, where the largest takes all the weight and an octave more or less of a token's
+    V is below the score's last bit; and ones near 0, where all tokens weigh the same."""
+    s = Setup(heads, fmt, [60, 17], page=16)
+    for b, m in enumerate(s.lens):
+        put(s, "k", b, along(s, s.rng.permutation(m) + 1.0) / m * np.exp2(k_size))
+        put(s, "v", b, s.rng.standard_normal((m, s.Hkv, s.D)))
+    s.q = bf16(f64(s.q) * np.exp2(q_size))
+    check_weighted(s)
