@@ -19,7 +19,8 @@
 //
 // Roundings: bf16 K, V and q enter the products exactly, the weights P as hi + lo bf16
 // (2^-16 relative). Turbo8 codes enter as f16 (exact); the K scales multiply the fp32
-// products of their 16 dims; the rotated q enters as hi + lo f16 (2^-21). A token's V scales enter as f16
+// products of their 16 dims; the rotated q enters as hi + lo f16 over the power of two of its largest
+// value (2^-22 of a value or 2^-25 of the largest, where the rotation's own sums end too). A token's V scales enter as f16
 // over 2^E, E the exponent of the token's largest (exact down to 2^-17 of that one, lost below 2^-25), and E goes into
 // the exponent of the token's weight: the weights that multiply V are 2^((x - m) + E - M), M the running
 // maximum of (x - m) + E, so a token counts by what it adds and not by its neighbours' sizes, and E is
@@ -326,8 +327,9 @@ struct Attention {
           for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
 #pragma unroll
           for (int w = 1; w < LPR; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
-          // |x| 2^-e below 2^15: e = exponent - 14
-          const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127 - 14, -100), 100);
+          // the largest |x| 2^-e is in [1, 2): no larger than it need be, so that products with keys of up to
+          // 2^118 stay in 32 bits
+          const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127, -126), 126);
           const float f = mx > 0.f ? pow2(-e2) : 1.f;
           if (c == 0) qe[h] = mx > 0.f ? e2 : 0;
 #pragma unroll

@@ -117,3 +117,11 @@ def test_attention_of_very_large_and_very_small_keys(heads, q_size, k_size, fmt)
         put(s, "v", b, s.rng.standard_normal((m, s.Hkv, s.D)))
     s.q = bf16(f64(s.q) * np.exp2(q_size))
     check_weighted(s)
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("q_size,k_size", [(0, 114), (-20, 117), (3, 110), (-100, 110)])
+@pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "wide"])
+def test_attention_of_keys_near_the_largest(heads, q_size, k_size, fmt):
+    """Scores that 32 bits hold, though not 2^15 times as large: the largest takes all the weight."""
+    test_attention_of_very_large_and_very_small_keys(heads, q_size, k_size, fmt)
