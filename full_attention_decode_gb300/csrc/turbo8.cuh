@@ -134,7 +134,8 @@ __device__ __forceinline__ void store32(void* p, bool wide, const uint32_t (&w)[
 }
 
 // Quantise a group of sixteen bf16 values (in pairs): scale = bf16(amax / 448), code = E4M3(x / scale); a
-// zero group keeps scale 0 and codes 0. Neither quotient needs a division:
+// zero group keeps scale 0 and codes 0, and so does one without a number (the layer forwards' maxima skip NaN); one with
+// an infinity gets that as its scale. Neither quotient needs a division:
 //  - amax has 8 significant bits and 448 = 7 * 64, so amax / 448 is never on a border between two bf16 values (9
 //    bits times 7 has more than 8) and at least 2^-12 away from one: the product with 1 / 448 rounds alike;
 //  - x / scale as q = x r with r near 1 / scale and one residual correction, q + (x - q scale) r (Markstein 1990).
@@ -144,7 +145,7 @@ __device__ __forceinline__ uint4 quant16(const uint32_t (&w)[8], uint16_t& scale
   __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
 #pragma unroll
   for (int i = 1; i < 8; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
-  const float amax = fmaxf(__low2float(m), __high2float(m));
+  const float amax = fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f);  // 0 if none is a number
   scale = to_bf16(amax * (1.0f / 448.0f));
   const float sc = bf16f(scale);
   uint32_t c[8] = {0u, 0u, 0u, 0u, 0u, 0u, 0u, 0u};

@@ -502,7 +502,8 @@ QWEN35_API size_t qwen35_cache_scratch_bytes(const qwen35_config* cfg, uint32_t 
 /* Write rows to the cache: k, v bf16 [n_rows][num_kv_heads][head_dim] (keys already
  * normed and rotated by position, as the cache keeps them). A bf16 cache takes them as they
  * are; a Turbo8 cache takes bf16(WHT(x)) as codes and scales, bit for bit what the
- * layer forwards append. bounds may be NULL; otherwise the bounds of every block that
+ * layer forwards append (also of a row with a NaN, which is a NaN in every element once
+ * rotated: its groups have no number, so it is kept as zeros; an infinity gives infinite scales and NaN codes). bounds may be NULL; otherwise the bounds of every block that
  * gets a row are brought up to date: a row at the first position of a block starts
  * the block's bounds anew, other rows widen them (so the bounds are right while a
  * sequence's rows come in order; a NaN never enters them unless a dimension has only

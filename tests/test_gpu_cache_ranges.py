@@ -15,8 +15,10 @@ import pytest
 import torch
 
 from full_attention_decode_gb300 import binding as B
+from full_attention_decode_gb300 import synth
 from oracle import qwen35_oracle as O
 
+from harness import init
 from test_gpu_cache_ops import BF16, TURBO8, Setup, bf16, f64
 
 pytestmark = pytest.mark.gpu
@@ -125,3 +127,69 @@ def test_attention_of_very_large_and_very_small_keys(heads, q_size, k_size, fmt)
 def test_attention_of_keys_near_the_largest(heads, q_size, k_size, fmt):
     """Scores that 32 bits hold, though not 2^15 times as large: the largest takes all the weight."""
     test_attention_of_very_large_and_very_small_keys(heads, q_size, k_size, fmt)
+
+
+# ---------------------------------------------------------------- rows in and out
+
+
+@pytest.mark.parametrize("cfg_name", ["tiny", "tiny_alt", "4b"])
+def test_turbo8_append_of_nan_rows_equals_the_prefill_of_a_layer(cfg_name):
+    """Tokens whose input holds a NaN, through the prefill of a layer and through the operator: codes and scales bit
+    for bit, all of them 0 for the rows that are NaN."""
+    init()
+    cfg = synth.config(cfg_name)
+    c = B.make_config(cfg)
+    T, cap = 19, 32
+    Hkv, D = cfg["num_kv_heads"], cfg["head_dim"]
+    layer = B.DeviceFaLayer(synth.fa_layer(1, 1, cfg))
+    scratch = B.new_scratch(B.qwen35_prefill_scratch_bytes(c, T))
+    rows = np.stack([synth.x_in(1, t, cfg) for t in range(T)])
+    rows[[3, 11, 12], 5] = 0x7FC0
+    x = B.to_device(rows)
+    y = torch.empty_like(x)
+    zero = np.zeros((cap, Hkv, D), dtype=np.uint16)
+    flat = B.DeviceKv(zero, zero)
+    t8, mine = (B.DeviceKvTurbo8(zero.astype(np.uint8), np.zeros((cap, Hkv, D // 16), np.uint16), zero.astype(np.uint8),
+                                 np.zeros((cap, Hkv, D // 16), np.uint16), cfg) for _ in "ab")
+    for kv in (flat, t8):
+        assert B.qwen35_prefill_full_attention(c, layer.struct, scratch, kv.struct, x, y, 0, T) == 0
+    r = B.DeviceRows(torch.zeros(1, dtype=torch.int32, device="cuda"),
+                     torch.tensor([0, T], dtype=torch.int32, device="cuda"), T)
+    s2 = B.new_scratch(B.qwen35_cache_scratch_bytes(c, cap, 0, T))
+    k, v = (a.view(torch.bfloat16)[:T].contiguous() for a in (flat.k, flat.v))
+    assert torch.isnan(v.float()).flatten(1).all(1).cpu().nonzero().flatten().tolist() == [3, 11, 12]
+    assert B.qwen35_cache_append(c, mine.struct, r, None, k, v, s2) == 0
+    torch.cuda.synchronize()
+    for a, b in ((mine.k, t8.k), (mine.v, t8.v), (mine.ks, t8.ks), (mine.vs, t8.vs)):
+        assert torch.equal(a[:T], b[:T])
+    assert not mine.vs[[3, 11, 12]].any() and not mine.v[[3, 11, 12]].any() and mine.v[[2, 4, 10, 13]].any()
+
+
+@pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "4b"])
+def test_turbo8_append_of_rows_without_finite_values(heads):
+    """Rotated, a row with a NaN is NaN throughout (zeros), one with an infinity infinite throughout (infinite scales,
+    NaN codes), one with two of them infinite or NaN by element: by the definition whose maximum skips NaN."""
+    s = Setup(heads, TURBO8, [40], rows=[40])
+    rng = np.random.default_rng(3)
+    x = rng.standard_normal((40, s.Hkv, s.D))
+    x[3, :, 7], x[5, :, 0], x[6, :, s.D - 1] = np.nan, np.inf, -np.inf
+    x[9, :, 2], x[9, :, 3] = np.inf, np.inf
+    x[10, :, 1], x[10, :, s.D // 2 + 1] = np.inf, -np.inf
+    x[11, :, 4], x[11, :, 20] = np.inf, np.nan
+    x = f64(bf16(x))
+    k = bf16(x).cuda()
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, None, k, k, s.scratch) == 0
+    torch.cuda.synchronize()
+    with np.errstate(all="ignore"):
+        h = np.ones((1, 1))
+        while len(h) < s.D:
+            h = np.block([[h, h], [h, -h]])
+        rot = np.stack([(r[:, None, :] * h).sum(-1) for r in x[[3, 5, 6, 9, 10, 11]]])
+        amax = np.fmax.reduce(np.abs(rot.reshape(6, s.Hkv, -1, 16)), axis=-1, initial=0.0)
+    assert set(amax[0].flat) == {0.0} and set(amax[1].flat) == {np.inf} and set(amax[5].flat) == {0.0}
+    at = [int(s.at(0, p)) for p in (3, 5, 6, 9, 10, 11)]
+    for name in "kv":
+        sc = O.bf16_to_f64(s.t[name + "s"].cpu().numpy().view(np.uint16)[at][:, :s.Hkv * s.D // 16])
+        np.testing.assert_array_equal(sc.reshape(amax.shape), amax)
+        codes = s.t[name].cpu().numpy()[at].reshape(amax.shape + (16,))
+        np.testing.assert_array_equal(codes & 0x7F, np.where(amax[..., None] > 0, 0x7F, np.zeros(16, np.uint8)))
