@@ -762,7 +762,11 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const __grid_consta
   const size_t item = (size_t)r * a.c.Hkv + g;
   if (n <= K) {  // every block is taken
     if (blockIdx.x == 0)
-      for (uint32_t i = tid; i < K; i += kThreads) a.blocks[item * K + i] = i < n ? (int32_t)i : -1;
+      for (uint32_t i = tid; i < K; i += kThreads) {
+        size_t row;
+        if (i < n && !cache_row(a.c, seq, i << a.blk_shift, row)) set_status(a.status, kStatusRange);
+        a.blocks[item * K + i] = i < n ? (int32_t)i : -1;
+      }
     return;
   }
   const uint32_t parts = (n + part - 1) / part;

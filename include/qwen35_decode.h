@@ -466,8 +466,8 @@ QWEN35_API int qwen35_lm_head_greedy(const qwen35_config* cfg, const qwen35_bf16
  * (n_rows == n_seqs). A sequence may have no row (row_start[b + 1] ==
  * row_start[b]); rows before row_start[0] or from row_start[n_seqs] on are left as they were.
  * row_start [n_seqs + 1] and pos [n_seqs] lie in device memory and are read when the
- * kernels run. A row whose position is outside [0, capacity), or whose token (any of
- * its tokens, for the attention and the selection) lies in a block outside
+ * kernels run. A row whose position is outside [0, capacity), or whose token (for the
+ * selection any token up to the row's position, for the attention any that it reads) lies in a block outside
  * [0, num_blocks), sets QWEN35_ERR_DEVICE_RANGE in the status word; nothing outside
  * the cache is touched, the row is skipped, or computed without that block.
  * num_blocks: the pool's size (paged only). At most 4096 sequences; at most 2^20 rows

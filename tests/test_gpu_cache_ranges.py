@@ -193,3 +193,28 @@ def test_turbo8_append_of_rows_without_finite_values(heads):
         np.testing.assert_array_equal(sc.reshape(amax.shape), amax)
         codes = s.t[name].cpu().numpy()[at].reshape(amax.shape + (16,))
         np.testing.assert_array_equal(codes & 0x7F, np.where(amax[..., None] > 0, 0x7F, np.zeros(16, np.uint8)))
+
+
+# ---------------------------------------------------------------- selection
+
+
+@pytest.mark.parametrize("n_select", [1, 3, 5, 6, 7, 40])
+@pytest.mark.parametrize("entry", [0, 2, 5])
+def test_selection_reports_a_block_outside_the_pool(n_select, entry):
+    """The only fault of the call: one entry of the table, of a block that the row sees. Lists shorter than the blocks
+    seen (6) and not."""
+    s = Setup("tiny_alt", BF16, [20, 90, 30], page=16, block=16)
+    s.set_bounds()
+    out = torch.zeros(3, s.Hkv, n_select, dtype=torch.int32, device="cuda")
+    q = s.q.cuda()
+    assert B.qwen35_select_blocks(s.cfg, s.kv, s.r, s.bounds, q, out, s.scratch) == 0
+    torch.cuda.synchronize()
+    assert s.status() == 0
+    clean = out.clone()
+    s.table[1, entry] = s.nb
+    assert B.qwen35_select_blocks(s.cfg, s.kv, s.r, s.bounds, q, out, s.scratch) == 0
+    torch.cuda.synchronize()
+    assert s.status() == B.QWEN35_ERR_DEVICE_RANGE
+    assert torch.equal(out[[0, 2]], clean[[0, 2]])
+    if n_select >= 6:
+        assert torch.equal(out, clean)
