@@ -598,8 +598,9 @@ __device__ __forceinline__ void decide(const Select& a, uint32_t r, uint32_t g, 
 }
 
 // Which blocks the exact scores choose, given 32-bit ones. Every s_j is within E of the exact t_j
-// (E = (group + 13) 2^-24 most: group - 1 additions in Q+-, 4 multiply-adds and 2 + 5 additions round
-// one after the other, and the rounding of `most` itself is covered by the rest). The K-th largest t is then within E
+// (E = (group + 13) 2^-24 most + (D + 1) 2^-149: group - 1 additions in Q+-, 4 multiply-adds and 2 + 5 additions round
+// one after the other, and the rounding of `most` itself is covered by the rest; where products leave 32 bits at the
+// lower end, each of the 2 D multiply-adds loses up to 2^-150 besides, and so may E). The K-th largest t is then within E
 // of the K-th largest s, T: s_j > T + 2E is in, s_j < T - 2E is out, and only what lies between is scored again. T is
 // found from the scores' bits, eight a step, until a step leaves exactly K. This part is latency (one CTA an item, a
 // few barriers, code that runs once): bisection and a barrier for each count took 0.6 us more of a
@@ -683,7 +684,7 @@ __device__ void choose(const Select& a, uint32_t r, uint32_t g, uint32_t seq, ui
   if (lane == 0) range[2 * kSelWarps + warp] = kth;
   __syncthreads();
   for (uint32_t w = 0; w < kSelWarps; ++w) kth = min(kth, range[2 * kSelWarps + w]);
-  const float T = key_value(kth), E = (float)(a.H / a.c.Hkv + 13) * 0x1p-24f * most;
+  const float T = key_value(kth), E = fmaf((float)(a.H / a.c.Hkv + 13) * 0x1p-24f, most, (D + 1) * 0x1p-149f);
   uint32_t klo = 1, khi = 0xffffffffu;  // keys above khi are in, below klo out
   if (E < INFINITY) {
     klo = order_key(isinf(T) ? T : __fadd_rd(T, -2.f * E));

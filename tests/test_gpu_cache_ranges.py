@@ -19,7 +19,7 @@ from full_attention_decode_gb300 import synth
 from oracle import qwen35_oracle as O
 
 from harness import init
-from test_gpu_cache_ops import BF16, TURBO8, Setup, bf16, f64
+from test_gpu_cache_ops import BF16, TURBO8, Setup, bf16, check_choice, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -218,3 +218,32 @@ def test_selection_reports_a_block_outside_the_pool(n_select, entry):
     assert torch.equal(out[[0, 2]], clean[[0, 2]])
     if n_select >= 6:
         assert torch.equal(out, clean)
+
+
+@pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "4b"])
+@pytest.mark.parametrize("e", [-152, -149, -140, -126, -100])
+def test_selection_of_scores_at_the_lower_end_of_32_bits(heads, e):
+    """Products of about 2^e: 32-bit sums lose them, or half a unit of 2^-149 of each."""
+    s = Setup(heads, BF16, [1600], block=16)
+    rng = np.random.default_rng(-e)
+    s.q = bf16(np.exp2(-76) * rng.uniform(0.5, 1.0, size=s.q.shape) * np.where(rng.random(s.q.shape) < 0.7, 1, -1))
+    b = rng.uniform(0.2, 0.8, size=(s.total // 16, s.Hkv, 2, s.D))
+    b *= np.where(rng.random(b.shape) < 0.1, 10, 1) * (rng.random((len(b), 1, 1, 1)) < 0.8)
+    b[::3, :, :, 1:] = 0  # blocks of one product
+    b[:, :, 0] *= -1
+    s.lo_hi.copy_(bf16(b * np.exp2(e + 76)).cuda())
+    for n in (1, 7, 30, 66):
+        check_choice(s, n, 0, 0)
+
+
+def test_selection_where_many_small_products_weigh_more_than_one():
+    """A score of 64 products of 0.45 units of 2^-149, which 32 bits lose one by one, and one of a product of 5."""
+    s = Setup("tiny", BF16, [32], block=16)
+    s.q = torch.zeros_like(s.q)
+    s.q[0, 0] = 2.0 ** -75
+    b = torch.zeros(2, 1, 2, s.D, dtype=torch.float64)
+    b[1, 0, 1], b[0, 0, 1, 0] = 0.45 * 2.0 ** -74, 5 * 2.0 ** -74
+    s.lo_hi[:2] = b.to(torch.bfloat16).cuda()
+    check_choice(s, 1, 0, 0)
+    s.lo_hi[:2] = b.flip(0).to(torch.bfloat16).cuda()
+    check_choice(s, 1, 0, 0)
