@@ -96,7 +96,8 @@ __device__ __forceinline__ void append_turbo8(const Append& a, uint32_t block) {
 }
 
 // The key bounds of spans of rows. A run is the call's rows of one block of one sequence; who has the span with
-// its first row folds it, starting anew if that is the block's first token. WIDE: a CTA a (span, kv-head), its
+// its first row folds it, starting anew if that is the block's first token. A dimension in which every value was NaN (lo
+// is still above hi) gets NaN for its bounds, which later rows' values replace. WIDE: a CTA a (span, kv-head), its
 // teams of D / 8 lanes taking a run's rows in turn; otherwise (blocks of 16 tokens) a team alone,
 // sixteen rows in flight (three prompts of 400 to 1500 rows, blocks of 64: 9.0 us wide, 10.7 by teams; 32768 rows,
 // blocks of 16: 119 us wide, 57 by teams).
@@ -155,14 +156,20 @@ __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, ui
           part[1][team][8 * l + e] = hi[e];
         }
       __syncthreads();
-      for (uint32_t i = threadIdx.x; i < 2 * D; i += kThreads) {
-        const uint32_t p = i / D, d = i % D;
-        float x = part[p][0][d];
-        for (uint32_t t = 1; t < used; ++t) x = p ? fmaxf(x, part[1][t][d]) : fminf(x, part[0][t][d]);
-        b[i] = to_bf16(x);
+      for (uint32_t d = threadIdx.x; d < D; d += kThreads) {
+        float x = part[0][0][d], y = part[1][0][d];
+        for (uint32_t t = 1; t < used; ++t) {
+          x = fminf(x, part[0][t][d]);
+          y = fmaxf(y, part[1][t][d]);
+        }
+        b[d] = to_bf16(x > y ? NAN : x);
+        b[D + d] = to_bf16(x > y ? NAN : y);
       }
       __syncthreads();
     } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (lo[e] > hi[e]) lo[e] = hi[e] = NAN;
       *reinterpret_cast<uint4*>(b + 8 * l) = pack8(lo);
       *reinterpret_cast<uint4*>(b + D + 8 * l) = pack8(hi);
     }

@@ -506,8 +506,8 @@ QWEN35_API size_t qwen35_cache_scratch_bytes(const qwen35_config* cfg, uint32_t 
  * rotated: its groups have no number, so it is kept as zeros; an infinity gives infinite scales and NaN codes). bounds may be NULL; otherwise the bounds of every block that
  * gets a row are brought up to date: a row at the first position of a block starts
  * the block's bounds anew, other rows widen them (so the bounds are right while a
- * sequence's rows come in order; a NaN never enters them unless a dimension has only
- * NaN). Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
+ * sequence's rows come in order). They skip NaN: a dimension that has held nothing else has
+ * NaN for both of its bounds until a number comes. Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
 QWEN35_API int qwen35_cache_append(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
                                    const qwen35_key_bounds* bounds, const qwen35_bf16* k, const qwen35_bf16* v,
                                    void* scratch, size_t scratch_bytes, void* stream);

@@ -247,3 +247,38 @@ def test_selection_where_many_small_products_weigh_more_than_one():
     check_choice(s, 1, 0, 0)
     s.lo_hi[:2] = b.flip(0).to(torch.bfloat16).cuda()
     check_choice(s, 1, 0, 0)
+
+
+@pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "4b"])
+@pytest.mark.parametrize("block", [16, 64, 512])
+def test_bounds_of_a_dimension_that_has_only_nan(heads, block):
+    """NaN for both bounds until a row brings a number, then that number's; a block with such a dimension has no
+    score, so it comes last."""
+    s = Setup(heads, BF16, [2 * block, 2 * block - 1], rows=[2 * block - 2, block + 5], block=block)
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((s.n_rows, s.Hkv, s.D))
+    one = s.start[1]
+    x[:block, :, 3] = np.nan  # sequence 0, tokens 2 .. block + 1
+    x[one:, 0, 9] = np.nan    # sequence 1, tokens block - 6 .. 2 block - 2
+    s.lo_hi.zero_()           # of the blocks' earlier tokens
+    k = bf16(x).cuda()
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, s.bounds, k, k, s.scratch) == 0
+    torch.cuda.synchronize()
+    got, y = f64(s.lo_hi), f64(k)
+    e = [int(s.at(b, j * block)) // block for b in (0, 1) for j in (0, 1)]
+
+    def fold(rows, **kw):
+        return np.stack([np.fmin.reduce(rows, 0, **kw), np.fmax.reduce(rows, 0, **kw)], 1)
+
+    np.testing.assert_array_equal(got[e[0]], fold(y[:block - 2], initial=0.0))
+    np.testing.assert_array_equal(got[e[1]], fold(y[block - 2:one]))  # two rows of NaN, then numbers
+    np.testing.assert_array_equal(got[e[2]], fold(y[one:one + 6], initial=0.0))
+    np.testing.assert_array_equal(got[e[3]], fold(y[one + 6:]))
+    assert np.isnan(got[e[3], 0, :, 9]).all() and not np.isnan(got[e[:3]]).any()
+    check_choice(s, 1, 0, 0)
+    # one more row of sequence 1's last block brings numbers
+    r = B.DeviceRows(torch.tensor([0, 2 * block - 1], dtype=torch.int32, device="cuda"))
+    new = bf16(rng.standard_normal((2, s.Hkv, s.D))).cuda()
+    assert B.qwen35_cache_append(s.cfg, s.kv, r, s.bounds, new, new, s.scratch) == 0
+    torch.cuda.synchronize()
+    np.testing.assert_array_equal(f64(s.lo_hi)[e[3], 0, :, 9], np.repeat(f64(new)[1, 0, 9], 2))
