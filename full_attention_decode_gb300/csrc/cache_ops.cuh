@@ -1,7 +1,8 @@
 // Where a call's rows and a cache's tokens are (device side of cache_ops.h). Whatever
 // the arrays in device memory hold, no address outside the cache is formed: a position
-// outside [0, capacity), a row count that runs backwards or a table entry outside the
-// pool makes the caller skip the access and set the range status.
+// outside [0, capacity) or a table entry outside the pool makes the caller skip the access
+// and set the range status. Row starts that fall or lie below 0 leave a row with a position of one of the
+// sequences from its pos on, or with none; which one is not said, and nothing reports it.
 #pragma once
 
 #include "cache_ops.h"

@@ -464,7 +464,8 @@ QWEN35_API int qwen35_lm_head_greedy(const qwen35_config* cfg, const qwen35_bf16
  * of every [n_rows][...] argument, at positions pos[b], pos[b] + 1, ... (pos[b]: how
  * many tokens the cache held before them). row_start NULL: one row a sequence
  * (n_rows == n_seqs). A sequence may have no row (row_start[b + 1] ==
- * row_start[b]); rows before row_start[0] or from row_start[n_seqs] on are left as they were.
+ * row_start[b]); row_start must not fall and has to begin at 0 or more (otherwise rows may take
+ * other rows' places behind pos, or none, which is not reported); rows before row_start[0] or from row_start[n_seqs] on are left as they were.
  * row_start [n_seqs + 1] and pos [n_seqs] lie in device memory and are read when the
  * kernels run. A row whose position is outside [0, capacity), or whose token (for the
  * selection any token up to the row's position, for the attention any that it reads) lies in a block outside

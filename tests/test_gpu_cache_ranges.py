@@ -282,3 +282,74 @@ def test_bounds_of_a_dimension_that_has_only_nan(heads, block):
     assert B.qwen35_cache_append(s.cfg, s.kv, r, s.bounds, new, new, s.scratch) == 0
     torch.cuda.synchronize()
     np.testing.assert_array_equal(f64(s.lo_hi)[e[3], 0, :, 9], np.repeat(f64(new)[1, 0, 9], 2))
+
+
+# ---------------------------------------------------------------- malformed row starts
+
+
+def _guarded(t, room=4096):
+    """A copy of t between two filled bands of its allocation, and what says whether the bands are as they were."""
+    n = t.numel() * t.element_size()
+    band = (room + 255) // 256 * 256
+    raw = torch.full((band + (n + 255) // 256 * 256 + band,), 0xA5, dtype=torch.uint8, device="cuda")
+    inner = raw[band:band + n].view(t.dtype).view(t.shape)
+    inner.copy_(t)
+    return inner, lambda: bool((raw[:band] == 0xA5).all()) and bool((raw[band + n:] == 0xA5).all())
+
+
+STARTS = [[0, 6, 2, 8], [-5, 1 << 30, -(1 << 30), 1 << 30], [8, 0, 8, 0], [0, 0, 0, (1 << 31) - 1],
+          [-(1 << 31), -1, 3, (1 << 31) - 1], [5, 4, 3, 2], [-3, 2, 2, 8], [7, 7, 7, 7]]
+
+
+@pytest.mark.parametrize("page", [0, 16])
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("starts", STARTS, ids=str)
+def test_row_starts_that_fall_touch_nothing_outside(starts, fmt, page):
+    """Every operator with row starts that fall, lie below 0 or behind the rows: all that is written lies in the call's
+    arrays, and in the cache at or behind some sequence's position."""
+    s = Setup("tiny_alt", fmt, [30, 30, 44], rows=[2, 2, 2], tail=2, page=page)
+    lo, hi = s.set_bounds()
+    k, v = (bf16(s.rng.standard_normal((s.n_rows, s.Hkv, s.D))) for _ in "kv")
+    bands = {}
+    for name in list(s.t):
+        s.t[name], bands[name] = _guarded(s.t[name])
+    s.lo_hi, bands["bounds"] = _guarded(s.lo_hi)
+    s.bounds = B.DeviceKeyBounds(s.lo_hi, s.block)
+    ptr = [s.t[n].data_ptr() if n in s.t else None for n in ("k", "v", "ks", "vs")]
+    s.kv = B.qwen35_kv_cache(ptr[0], ptr[1], s.cap, B.QWEN35_KV_TURBO8 if fmt == TURBO8 else B.QWEN35_KV_BF16, ptr[2],
+                             ptr[3], s.table.data_ptr() if page else None, page, 0)
+    outs = {}
+    for name, shape, kind in (("k_back", k.shape, torch.bfloat16), ("v_back", v.shape, torch.bfloat16),
+                              ("out", s.q.shape, torch.bfloat16), ("sparse", s.q.shape, torch.bfloat16),
+                              ("blocks", (s.n_rows, s.Hkv, 2), torch.int32)):
+        outs[name], bands[name] = _guarded(torch.full(shape, -9, dtype=kind, device="cuda"))
+    s.row_start.copy_(torch.tensor(starts, dtype=torch.int64).to(torch.int32))
+    before = {n: t.clone() for n, t in s.t.items()}
+    bounds_before = s.lo_hi.clone()
+    q = s.q.cuda()
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, s.bounds, k.cuda(), v.cuda(), s.scratch) == 0
+    assert B.qwen35_cache_read(s.cfg, s.kv, s.r, outs["k_back"], outs["v_back"], s.scratch) == 0
+    assert B.qwen35_select_blocks(s.cfg, s.kv, s.r, s.bounds, q, outs["blocks"], s.scratch) == 0
+    assert B.qwen35_decode_attention(s.cfg, s.kv, s.r, q, outs["out"], s.scratch) == 0
+    assert B.qwen35_decode_attention(s.cfg, s.kv, s.r, q, outs["sparse"], s.scratch, blocks=outs["blocks"],
+                                     block=s.block) == 0
+    torch.cuda.synchronize()
+    assert s.status() in (0, B.QWEN35_ERR_DEVICE_RANGE)
+    assert [n for n, ok in bands.items() if not ok()] == []
+    may = np.zeros(s.total, dtype=bool)
+    for b, p in enumerate(s.pos.tolist()):
+        may[s.at(b, np.arange(p, s.cap))] = True
+    for name, t in s.t.items():
+        assert torch.equal(before[name].cpu().view(torch.uint8)[~may], t.cpu().view(torch.uint8)[~may])
+    kept = ~may.reshape(-1, s.block).any(1)
+    assert torch.equal(bounds_before.cpu().view(torch.int16)[kept], s.lo_hi.cpu().view(torch.int16)[kept])
+    # the operators work on as before with row starts as they should be
+    s.row_start.copy_(torch.tensor(s.start, dtype=torch.int32))
+    B.qwen35_scratch_init(s.scratch)
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, s.bounds, k.cuda(), v.cuda(), s.scratch) == 0
+    back = [torch.zeros_like(x).cuda() for x in (k, v)]
+    assert B.qwen35_cache_read(s.cfg, s.kv, s.r, *back, s.scratch) == 0
+    torch.cuda.synchronize()
+    assert s.status() == 0
+    if fmt == BF16:
+        assert torch.equal(back[0][:6].cpu(), k[:6]) and torch.equal(back[1][:6].cpu(), v[:6])
