@@ -208,8 +208,8 @@ def _ptr(t):
 
 
 def _stream(stream):
-    if stream is None:  # the raw handle: no Stream object is made for every call
-        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+    if stream is None:
+        return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
