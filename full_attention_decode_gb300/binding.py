@@ -207,8 +207,15 @@ def _ptr(t):
     return t.data_ptr()
 
 
+# torch's handle of the current stream without a Stream object for each call: 8 rows appended take 4.8 us a call with
+# it, 7.9 with torch.cuda.current_stream(), which a torch without it falls back to.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(stream):
     if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(torch.cuda.current_device())
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
