@@ -353,3 +353,73 @@ def test_row_starts_that_fall_touch_nothing_outside(starts, fmt, page):
     assert s.status() == 0
     if fmt == BF16:
         assert torch.equal(back[0][:6].cpu(), k[:6]) and torch.equal(back[1][:6].cpu(), v[:6])
+
+
+# ---------------------------------------------------------------- rows in and out, further
+
+
+@pytest.mark.parametrize("heads", ["tiny", "4b"])
+def test_turbo8_codes_of_rows_whose_rotation_is_exact(heads):
+    """Whole numbers below 16: the rotation's sums and its power of two are exact in 32 bits, so the codes and scales
+    are the oracle's, every one."""
+    s = Setup(heads, TURBO8, [700, 45], rows=[650, 45], page=32)
+    x = np.random.default_rng(2).integers(-15, 16, size=(s.n_rows, s.Hkv, s.D)).astype(np.float64)
+    x *= np.exp2(np.random.default_rng(3).integers(-20, 21, size=(s.n_rows, 1, 1)))
+    k = bf16(x)
+    np.testing.assert_array_equal(f64(k), x)
+    c, sc = O.turbo8_quantize(O.bf16_round(O.wht(x)))
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, None, k.cuda(), k.flip(0).cuda(), s.scratch) == 0
+    torch.cuda.synchronize()
+    at = [int(s.at(b, p)) for _, b, p in s.each_row()]
+    for name, codes, scales in (("k", c, sc), ("v", c[::-1], sc[::-1])):
+        np.testing.assert_array_equal(s.t[name].cpu().numpy()[at], codes)
+        got = O.bf16_to_f64(s.t[name + "s"].cpu().numpy().view(np.uint16)[at][:, :s.Hkv * s.D // 16])
+        np.testing.assert_array_equal(got.reshape(scales.shape), scales)
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("n,per,block", [(24, 2, 64), (60, 1, 256), (40, 1, 1024), (200, 3, 16), (90, 5, 32),
+                                         (64, 0, 128)])
+def test_bounds_of_many_short_runs(n, per, block, fmt):
+    """A few rows of each of many sequences, 0 to 2 per of them, many runs to a block's span of rows: some start a
+    block, some cross into the next, some widen one."""
+    rows = [(b * 7) % (2 * per + 1) if per else int(b == 40) for b in range(n)]
+    lens = [block - 2 + (b * 5) % 7 + rows[b] for b in range(n)]
+    s = Setup("tiny", fmt, lens, rows=rows, block=block, lead=1, tail=2)
+    s.set_bounds()
+    before = f64(s.lo_hi).copy()
+    k, v = (bf16(5 * s.rng.standard_normal((s.n_rows, s.Hkv, s.D))) for _ in "kv")
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, s.bounds, k.cuda(), v.cuda(), s.scratch) == 0
+    torch.cuda.synchronize()
+    assert s.status() == 0
+    want, x = before.copy(), f64(k)
+    for row, b, p in s.each_row():
+        e = int(s.at(b, p)) // block
+        new = np.stack([x[row], x[row]], 1)
+        want[e] = new if p % block == 0 else np.stack([np.fmin(want[e, :, 0], x[row]), np.fmax(want[e, :, 1], x[row])], 1)
+    np.testing.assert_array_equal(f64(s.lo_hi), want)
+
+
+def test_selections_at_once_with_their_own_scratch():
+    """Two streams, each with selections whose items several CTAs score, and a third with attention."""
+    a = Setup("tiny", BF16, [30000, 9000], page=64, block=16, seed=1)
+    b = Setup("odd", BF16, [20000, 8000, 700], block=32, seed=2)
+    c = Setup("4b", TURBO8, [2800, 100], page=16, seed=3)
+    jobs = []
+    for s, n in ((a, 40), (b, 64)):
+        s.set_bounds()
+        check_choice(s, n)
+        out = torch.full((s.n_rows, s.Hkv, n), -9, dtype=torch.int32, device="cuda")
+        q = s.q.cuda()
+        assert B.qwen35_select_blocks(s.cfg, s.kv, s.r, s.bounds, q, out, s.scratch) == 0
+        jobs.append((s, q, out, torch.zeros_like(out), torch.cuda.Stream()))
+    ref, qc, oc, sc = c.attend().clone(), c.q.cuda(), torch.zeros_like(c.q).cuda(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for s, q, _, out, st in jobs:
+            assert B.qwen35_select_blocks(s.cfg, s.kv, s.r, s.bounds, q, out, s.scratch, stream=st) == 0
+        assert B.qwen35_decode_attention(c.cfg, c.kv, c.r, qc, oc, c.scratch, stream=sc) == 0
+    torch.cuda.synchronize()
+    for s, _, want, got, _ in jobs:
+        assert torch.equal(want, got) and s.status() == 0
+    assert torch.equal(ref, oc)
