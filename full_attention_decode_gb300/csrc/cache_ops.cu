@@ -9,7 +9,6 @@ using namespace q35;
 namespace {
 
 constexpr uint32_t kThreads = 256;
-constexpr uint32_t kWideShift = 4;  // selection blocks of more than 2^this rows: a CTA folds one
 
 // ------------------------------------------------------------------ rows in and out
 
@@ -98,9 +97,7 @@ __device__ __forceinline__ void append_turbo8(const Append& a, uint32_t block) {
 // The key bounds of spans of rows. A run is the call's rows of one block of one sequence; who has the span with
 // its first row folds it, starting anew if that is the block's first token. A dimension in which every value was NaN (lo
 // is still above hi) gets NaN for its bounds, which later rows' values replace. WIDE: a CTA a (span, kv-head), its
-// teams of D / 8 lanes taking a run's rows in turn; otherwise (blocks of 16 tokens) a team alone,
-// sixteen rows in flight (three prompts of 400 to 1500 rows, blocks of 64: 9.0 us wide, 10.7 by teams; 32768 rows,
-// blocks of 16: 119 us wide, 57 by teams).
+// teams of D / 8 lanes taking a run's rows in turn; otherwise a team alone, sixteen rows in flight (fold_wide).
 template <int D, bool WIDE>
 __device__ __forceinline__ void append_bounds(const Append& a, uint32_t span, uint32_t g, uint32_t span_rows) {
   constexpr int LPR = D / 8, TEAMS = WIDE ? kThreads / LPR : 1;
@@ -190,7 +187,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const uint32_t block = blockIdx.x - min(turn + 1, bound_ctas);
     if constexpr (T8) append_turbo8<D>(a, block);
     else append_plain<D>(a, block);
-  } else if (a.blk_shift > kWideShift) {
+  } else if (a.wide_bounds) {
     append_bounds<D, true>(a, turn / a.c.Hkv, turn % a.c.Hkv, span_rows);
   } else {
     const uint32_t team = turn * (kThreads / (D / 8)) + threadIdx.x / (D / 8);
@@ -812,11 +809,24 @@ __global__ void __launch_bounds__(kThreads, 2) select_kernel(const __grid_consta
     default: return cudaErrorInvalidValue;   \
   }
 
-cudaError_t append(const Append& a, cudaStream_t st) {
+// Whether a CTA folds a block's bounds, or a team of D / 8 lanes. A CTA ends a block sooner, teams keep more blocks in
+// flight. us of an append of 4 heads of 256 (Turbo8 | bf16), by a CTA and by teams:
+//             300 rows                2 688 rows in 3 prompts   32 768 rows
+//   block 16  3.6, 4.0 | 3.4, 4.1     12.0, 6.9 | 9.0, 7.4      106, 55 | 75, 45
+//         32  3.6, 4.2 | 3.7, 5.2     9.5, 8.0 | 7.9, 10.1      73, 54 | 56, 46
+//         64  3.6, 5.4 | 4.0, 8.5     8.5, 10.0 | 8.3, 13.0     64, 54 | 49, 50
+//        128  3.8, 8.4 | 5.3, 15.0    7.5, 13.8 | 9.1, 19.2     59, 58 | 47, 63
+// so by a CTA from 128 tokens on, and from 32 on while such CTAs are few (folds: 40, 336 and 4 096 at blocks of 32).
+bool fold_wide(uint32_t blk_shift, uint32_t folds) { return blk_shift >= 7 || (blk_shift >= 5 && folds <= 512); }
+
+cudaError_t append(const Append& args, cudaStream_t st) {
+  Append a = args;
   const bool t8 = a.c.ks != nullptr;
   const uint32_t rows = row_ctas_of(a.r, a.c, t8);
   const uint32_t span = a.r.row_start ? 1u << a.blk_shift : 1u;  // rows of a bounds CTA: about one block's
-  const uint32_t folds = (a.r.n_rows + span - 1) / span * a.c.Hkv, teams = a.blk_shift > kWideShift ? 1 : kThreads / (a.c.D / 8);
+  const uint32_t folds = (a.r.n_rows + span - 1) / span * a.c.Hkv;
+  a.wide_bounds = fold_wide(a.blk_shift, folds);
+  const uint32_t teams = a.wide_bounds ? 1 : kThreads / (a.c.D / 8);
   const uint32_t bounds = a.bounds ? (folds + teams - 1) / teams : 0, grid = rows + bounds;
   uint32_t shift = 0;
   while (bounds && (grid / bounds) >> (shift + 1)) ++shift;

@@ -41,7 +41,8 @@ struct Append {
   const uint16_t* v;
   uint16_t* bounds;  // [rows >> blk_shift][Hkv][2][D], or null
   uint32_t blk_shift;
-  bool wide;  // k and v are 32-byte aligned
+  bool wide;         // k and v are 32-byte aligned
+  bool wide_bounds;  // set by append(): a CTA folds a block's bounds, not a team
   int* status;
 };
 cudaError_t append(const Append& a, cudaStream_t st);

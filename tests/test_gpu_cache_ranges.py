@@ -423,3 +423,26 @@ def test_selections_at_once_with_their_own_scratch():
     for s, _, want, got, _ in jobs:
         assert torch.equal(want, got) and s.status() == 0
     assert torch.equal(ref, oc)
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("block", [16, 32, 64, 128])
+def test_bounds_of_many_blocks(block, fmt):
+    """Long prompts, more blocks and heads than are folded by a CTA each (16 to 64 tokens); one begins inside a block."""
+    s = Setup("eight", fmt, [9000, 3011], rows=[9000, 2990], page=128, block=block)
+    s.set_bounds()
+    want = f64(s.lo_hi).copy()
+    k, v = (bf16(s.rng.standard_normal((s.n_rows, s.Hkv, s.D))) for _ in "kv")
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, s.bounds, k.cuda(), v.cuda(), s.scratch) == 0
+    torch.cuda.synchronize()
+    assert s.status() == 0
+    x = f64(k)
+    for b, (m, r) in enumerate(zip(s.lens, s.rows)):
+        for j in range((m - r) // block, (m - 1) // block + 1):
+            e, p0 = int(s.at(b, j * block)) // block, max(j * block, m - r)
+            rows = x[s.start[b] + p0 - (m - r):s.start[b] + min(m, (j + 1) * block) - (m - r)]
+            lo, hi = rows.min(0), rows.max(0)
+            if p0 > j * block:
+                lo, hi = np.minimum(lo, want[e, :, 0]), np.maximum(hi, want[e, :, 1])
+            want[e] = np.stack([lo, hi], 1)
+    np.testing.assert_array_equal(f64(s.lo_hi), want)
