@@ -1210,7 +1210,7 @@ int bounds_ok(const qwen35_kv_cache* kv, const qwen35_key_bounds* b) {
 extern "C" {
 
 size_t qwen35_cache_scratch_bytes(const qwen35_config* cfg, uint32_t capacity, uint32_t block, uint32_t max_rows) {
-  if (cache_dims(cfg) || capacity == 0 || max_rows == 0 || max_rows > q35c::kMaxRows) return 0;
+  if (cache_dims(cfg) || capacity == 0 || capacity > (1u << 31) || max_rows == 0 || max_rows > q35c::kMaxRows) return 0;
   if (block && (block < 16 || block > 1024 || !power_of_two(block))) return 0;
   const uint32_t rows = max_rows < q35c::kMaxQueries ? max_rows : q35c::kMaxQueries;
   const size_t sel = cache_need(cfg->num_kv_heads, block ? capacity / block : 0, rows).total;
