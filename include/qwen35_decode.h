@@ -191,8 +191,9 @@ QWEN35_API const char* qwen35_status_string(int status);
 QWEN35_API size_t qwen35_scratch_bytes(const qwen35_config* cfg, int layer_kind);
 QWEN35_API size_t qwen35_stack_scratch_bytes(const qwen35_config* cfg);
 
-/* Zero the device status word and the internal counters of a scratch buffer
- * (enqueued on `stream`). Call once after allocating scratch. */
+/* Zero the device status word and the internal counters of a scratch buffer, its first
+ * 65 KiB (enqueued on `stream`). Call once after allocating scratch; called again, it
+ * takes what a forward left there (qwen35_debug_scratch_offset) with it. */
 QWEN35_API int qwen35_scratch_init(void* scratch, size_t scratch_bytes, void* stream);
 
 /* Synchronise `stream`, then copy the device status word of `scratch` into
@@ -443,9 +444,10 @@ QWEN35_API int qwen35_lm_head_greedy(const qwen35_config* cfg, const qwen35_bf16
  * qwen35_cache_append, (qwen35_select_blocks,) qwen35_decode_attention; a captured
  * graph of them decodes on as the caller advances the positions in device memory.
  * The pages keep the append and the attention inside forward_full_attention
- * ("full_attention.rs") and leave sparse attention out; rounding, rotation and
- * formats here are that forward's, so a cache may pass between these calls, the
- * layer forwards and the prefill.
+ * ("full_attention.rs") and leave sparse attention out; the cached rows' formats,
+ * rotation and rounding are that forward's, so a cache may pass between these calls,
+ * the layer forwards and the prefill. Key bounds do not: only qwen35_cache_append keeps
+ * them (see qwen35_key_bounds).
  *
  * Of the config only num_heads, num_kv_heads and head_dim are read: head_dim 64, 128
  * or 256, at most 8 kv-heads of at most 16 q-heads each (UNSUPPORTED otherwise).
@@ -457,23 +459,28 @@ QWEN35_API int qwen35_lm_head_greedy(const qwen35_config* cfg, const qwen35_bf16
  * may pass 2^32 bytes.
  *
  * Scratch: qwen35_cache_scratch_bytes, made with qwen35_scratch_init and not shared
- * with the layer forwards. It belongs to one call at a time: calls (or replays of
+ * with the layer forwards. The append and the read use its first 256 bytes alone, the
+ * attention what block 0 gives, the selection 12 bytes for each row, kv-head and block
+ * of the capacity besides. It belongs to one call at a time: calls (or replays of
  * graphs that hold them) that overlap on the GPU need one each.
  *
  * The rows of a call: sequence b's tokens are rows [row_start[b], row_start[b + 1])
  * of every [n_rows][...] argument, at positions pos[b], pos[b] + 1, ... (pos[b]: how
  * many tokens the cache held before them). row_start NULL: one row a sequence
  * (n_rows == n_seqs). A sequence may have no row (row_start[b + 1] ==
- * row_start[b]); row_start must not fall and has to begin at 0 or more (otherwise rows may take
- * other rows' places behind pos, or none, which is not reported); rows before row_start[0] or from row_start[n_seqs] on are left as they were.
+ * row_start[b]); row_start must not fall and has to begin at 0 or more (otherwise rows
+ * may take other rows' places behind pos, or none, which is not reported); rows before
+ * row_start[0] or from row_start[n_seqs] on are left as they were.
  * row_start [n_seqs + 1] and pos [n_seqs] lie in device memory and are read when the
  * kernels run. A row whose position is outside [0, capacity), or whose token (for the
- * selection any token up to the row's position, for the attention any that it reads) lies in a block outside
- * [0, num_blocks), sets QWEN35_ERR_DEVICE_RANGE in the status word; nothing outside
- * the cache is touched, the row is skipped, or computed without that block.
- * num_blocks: the pool's size (paged only). At most 4096 sequences; at most 2^20 rows
- * for append and read, 2048 for selection and attention. Sequences of one call may
- * share blocks that the call does not write. */
+ * selection any token up to the row's position, for the attention any that it reads)
+ * lies in a block outside [0, num_blocks), sets QWEN35_ERR_DEVICE_RANGE in the status
+ * word; nothing outside the cache is touched, the row is skipped, or computed without
+ * that block. num_blocks: the pool's size (paged only). n_seqs and n_rows: 1 or more; at
+ * most 4096 sequences; at most 2^20 rows for append and read, 2048 for selection and
+ * attention, and for the attention n_rows * num_kv_heads * (capacity, or listed tokens)
+ * below 2^35 (UNSUPPORTED above). Sequences of one call may share blocks that the call
+ * does not write. */
 typedef struct qwen35_cache_rows {
     const int32_t* row_start;
     const int32_t* pos;
@@ -487,7 +494,13 @@ typedef struct qwen35_cache_rows {
  * [head_dim] (lo, then hi), indexed by where the block lies in the cache arrays, so a
  * block shared by sequences has one entry. block: tokens, a power of two of 16 to
  * 1024 that divides capacity and, in a paged cache, block_tokens. The keys are the
- * rows given to qwen35_cache_append (not rotated, before Turbo8 rounds them). */
+ * rows given to qwen35_cache_append (not rotated, before Turbo8 rounds them). Rows that
+ * a layer forward or the prefill wrote have no bounds; qwen35_cache_read and an append of
+ * what it gives make them: in a bf16 cache in place (the rows stay as they are bit for
+ * bit), for a Turbo8 cache into a bf16 one of the same capacity or table, since a second
+ * quantisation would change its rows (the bounds are then those of the rows as they are
+ * cached). Bounds only widen within a block: tokens that are taken back (rejected drafts)
+ * leave theirs wider than need be until the block begins anew. */
 typedef struct qwen35_key_bounds {
     qwen35_bf16* lo_hi;
     uint32_t block;
@@ -504,11 +517,13 @@ QWEN35_API size_t qwen35_cache_scratch_bytes(const qwen35_config* cfg, uint32_t 
  * normed and rotated by position, as the cache keeps them). A bf16 cache takes them as they
  * are; a Turbo8 cache takes bf16(WHT(x)) as codes and scales, bit for bit what the
  * layer forwards append (also of a row with a NaN, which is a NaN in every element once
- * rotated: its groups have no number, so it is kept as zeros; an infinity gives infinite scales and NaN codes). bounds may be NULL; otherwise the bounds of every block that
+ * rotated: its groups have no number, so it is kept as zeros; an infinity gives infinite
+ * scales and NaN codes). bounds may be NULL; otherwise the bounds of every block that
  * gets a row are brought up to date: a row at the first position of a block starts
  * the block's bounds anew, other rows widen them (so the bounds are right while a
- * sequence's rows come in order). They skip NaN: a dimension that has held nothing else has
- * NaN for both of its bounds until a number comes. Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
+ * sequence's rows come in order). They skip NaN: a dimension that has held nothing else
+ * has NaN for both of its bounds until a number comes. Errors: INVALID_ARGUMENT,
+ * UNSUPPORTED, CUDA. */
 QWEN35_API int qwen35_cache_append(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
                                    const qwen35_key_bounds* bounds, const qwen35_bf16* k, const qwen35_bf16* v,
                                    void* scratch, size_t scratch_bytes, void* stream);
@@ -522,7 +537,7 @@ QWEN35_API int qwen35_cache_read(const qwen35_config* cfg, const qwen35_kv_cache
 /* Choose blocks of the cache for every row and kv-head by the bounds: a row at
  * position p sees blocks 0 .. p / block, and a block's score is the sum over the
  * kv-head's q-heads of the largest q . k that a key inside the block's bounds could
- * have, sum_h sum_d max(q_hd lo_d, q_hd hi_d). blocks int32 [n_rows][num_kv_heads]
+ * have, sum_h sum_d (q_hd < 0 ? q_hd lo_d : q_hd hi_d). blocks int32 [n_rows][num_kv_heads]
  * [n_select]: the n_select highest-scoring blocks in rising order, the lower index of
  * equal scores, then -1 where fewer blocks are seen. The first n_first and the last
  * n_last seen blocks come before all others. The choice is that of the exact
@@ -548,11 +563,13 @@ QWEN35_API int qwen35_select_blocks(const qwen35_config* cfg, const qwen35_kv_ca
  *    `block` tokens (16 to 1024, a power of two that divides capacity and, in a paged
  *    cache, block_tokens). An entry that is negative or behind the row's last
  *    block counts as none, one listed twice counts twice; a row without a token gets zeros.
- * Scores, maxima and sums are held in fp32 and the output is rounded to bf16 once. The weights
- * enter the products with V rounded: as two bf16 parts (2^-16) with a bf16 cache, as f16 (2^-11) before and
- * after the product with the token's V scale with a Turbo8 cache, relative to what the token adds: how large other
- * tokens' values are does not matter (a token that adds less than 2^-38 of what another adds may count as
- * nothing, and so may a group of 16 rotated values below 2^-25 of its own token's largest). Keys with
+ * Scores, maxima and sums are held in fp32 and the output is rounded to bf16 once. The
+ * weights enter the products with V rounded: as two bf16 parts (2^-16) with a bf16 cache,
+ * as f16 (2^-11) before and after the product with the token's V scale with a Turbo8
+ * cache, relative to what the token adds, however large other tokens' values are (a token
+ * that adds less than 2^-38 of what another adds may count as nothing, and so may a group
+ * of 16 rotated values below 2^-25 of its own token's largest). A Turbo8 cache's keys may
+ * be up to 2^118 in size, a bf16 cache's as large as their scores stay finite. Keys with
  * an infinity or NaN spoil only rows that see them. out must not overlap an input. Errors
  * as qwen35_cache_append. */
 QWEN35_API int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,

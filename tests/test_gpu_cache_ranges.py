@@ -446,3 +446,33 @@ def test_bounds_of_many_blocks(block, fmt):
                 lo, hi = np.minimum(lo, want[e, :, 0]), np.maximum(hi, want[e, :, 1])
             want[e] = np.stack([lo, hi], 1)
     np.testing.assert_array_equal(f64(s.lo_hi), want)
+
+
+# ---------------------------------------------------------------- bounds of rows that are in the cache already
+
+
+@pytest.mark.parametrize("fmt,page", [(BF16, 0), (BF16, 32), (TURBO8, 0), (TURBO8, 32)])
+def test_bounds_of_a_cache_that_holds_rows(fmt, page):
+    """Rows that came without bounds are read and appended with them: in place for bf16, into a bf16 cache of the same
+    layout for Turbo8. The cache stays as it is, the bounds are those of the rows as cached, and selection takes them."""
+    s = Setup("tiny_alt", fmt, [300, 77, 200], rows=[300, 77, 200], page=page, block=32)
+    s.lo_hi.zero_()
+    rows = [torch.zeros(s.n_rows, s.Hkv, s.D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    kept = {n: t.clone() for n, t in s.t.items()}
+    assert B.qwen35_cache_read(s.cfg, s.kv, s.r, *rows, s.scratch) == 0
+    kv = s.kv
+    if fmt == TURBO8:
+        other = [torch.zeros(s.total, s.Hkv, s.D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+        kv = B.qwen35_kv_cache(other[0].data_ptr(), other[1].data_ptr(), s.cap, B.QWEN35_KV_BF16, None, None,
+                               s.table.data_ptr() if page else None, page, 0)
+    assert B.qwen35_cache_append(s.cfg, kv, s.r, s.bounds, *rows, s.scratch) == 0
+    torch.cuda.synchronize()
+    for name, t in s.t.items():
+        assert torch.equal(t.view(torch.uint8), kept[name].view(torch.uint8))
+    x, got = f64(rows[0]), f64(s.lo_hi)
+    for b, m in enumerate(s.lens):
+        for j in range((m - 1) // 32 + 1):
+            y = x[s.start[b] + 32 * j:s.start[b] + min(m, 32 * j + 32)]
+            np.testing.assert_array_equal(got[int(s.at(b, 32 * j)) // 32], np.stack([y.min(0), y.max(0)], 1))
+    check_choice(s, 3)
+    assert s.status() == 0
