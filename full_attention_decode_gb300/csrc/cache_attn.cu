@@ -25,8 +25,8 @@
 // the exponent of the token's weight: the weights that multiply V are 2^((x - m) + E - M), M the running
 // maximum of (x - m) + E, so a token counts by what it adds and not by its neighbours' sizes, and E is
 // added where large scores have cancelled. m, which the softmax's sum refers to, follows the scores only when one
-// lies 32 octaves above it: 32 bits have room for that, and the lanes exchange one maximum a tile (128K tokens: 68 us; one power of two a tile, which lost tokens beside larger
-// ones, 64). The weights are rounded to f16 (2^-11), up to 2^13 so that f16 holds 2^-27 of the largest in full and what
+// lies 32 octaves above it: 32 bits have room for that, and the lanes exchange one maximum a tile (128K tokens: 68 us;
+// one power of two a tile, which lost tokens beside larger ones, 64). The weights are rounded to f16 (2^-11), up to 2^13 so that f16 holds 2^-27 of the largest in full and what
 // lies 2^-38 below is lost, and rounded again with the scale (2^-11): next to the codes' own 2^-4 and
 // the output's 2^-8 these are small (error against 64 bits 0.00171 at 128K, of fp32 weights 0.00169), and a second
 // f16 for their rest (2^-21) takes 73 us.
@@ -1013,7 +1013,7 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attend_kernel(const __grid_co
     }
     // An equal stretch for every CTA, whole rounds of the warps, or at least kLeast tiles where there is less
     // (512 tokens of 4 heads on 64 CTAs: 9.9 us, on 16 CTAs of a whole round 11.6). Few items of up to kShort rounds go
-    // to a CTA each instead: a split's hand-over and join take 4 us, a round of one CTA 1.5 to 2.5.
+    // to a CTA each instead: a split's hand-over and join take 4 us or more (6.4 for 32 parts), a round of one CTA 1.5 to 2.5.
     constexpr uint32_t kShort = 2, kLeast = 2;
     most = __reduce_max_sync(0xffffffffu, most);
     items = __reduce_add_sync(0xffffffffu, items);
