@@ -19,7 +19,7 @@ from full_attention_decode_gb300 import synth
 from oracle import qwen35_oracle as O
 
 from harness import init
-from test_gpu_cache_ops import BF16, TURBO8, Setup, bf16, check_choice, f64
+from test_gpu_cache_ops import BF16, TURBO8, Setup, bf16, check_choice, choose, f64
 
 pytestmark = pytest.mark.gpu
 
@@ -476,3 +476,111 @@ def test_bounds_of_a_cache_that_holds_rows(fmt, page):
             np.testing.assert_array_equal(got[int(s.at(b, 32 * j)) // 32], np.stack([y.min(0), y.max(0)], 1))
     check_choice(s, 3)
     assert s.status() == 0
+
+
+# ---------------------------------------------------------------- sizes and replays
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("cap", [1, 7, 17, 37])
+def test_a_contiguous_cache_of_any_capacity(cap, fmt):
+    """Capacities that end inside a tile of 16 tokens; the last sequence's last row is the cache's last."""
+    s = Setup("odd", fmt, [cap, max(1, cap - 3), cap], rows=[min(cap, 3), 1, min(cap, 2)])
+    groups, n = s.Hkv * s.D // 16, 3 * cap
+    t, stands = {}, {}
+    for name, x in s.t.items():
+        x = x.view(3, s.cap, *x.shape[1:])[:, :cap]
+        t[name], _ = _guarded(x.reshape(n, *x.shape[2:]))
+    for name in "kv":
+        stands[name] = s.stands[name].reshape(3, s.cap, s.Hkv, s.D)[:, :cap].reshape(n, s.Hkv, s.D)
+    s.t, s.stands, s.cap, s.total = t, stands, cap, n
+    scales = [t[a].data_ptr() if fmt == TURBO8 else None for a in ("ks", "vs")]
+    s.kv = B.qwen35_kv_cache(t["k"].data_ptr(), t["v"].data_ptr(), cap,
+                             B.QWEN35_KV_TURBO8 if fmt == TURBO8 else B.QWEN35_KV_BF16, *scales, None, 0, 0)
+    check_weighted(s)
+    rows = [torch.zeros(s.n_rows, s.Hkv, s.D, dtype=torch.bfloat16, device="cuda") for _ in "kv"]
+    assert B.qwen35_cache_read(s.cfg, s.kv, s.r, *rows, s.scratch) == 0
+    torch.cuda.synchronize()
+    at = [int(s.at(b, p)) for _, b, p in s.each_row()]
+    for name, got in zip("kv", rows):
+        err = np.abs(f64(got) - s.stands[name][at])
+        norm = np.linalg.norm(s.stands[name][at], axis=-1, keepdims=True)
+        assert np.all(err <= 2.0 ** -8 * np.abs(s.stands[name][at]) + 2.0 ** -20 * norm)
+    before = {a: x.clone() for a, x in t.items()}
+    if fmt == BF16:
+        assert B.qwen35_cache_append(s.cfg, s.kv, s.r, None, *rows, s.scratch) == 0
+        torch.cuda.synchronize()
+        assert all(torch.equal(before[a].view(torch.int16), t[a].view(torch.int16)) for a in t)
+    assert s.status() == 0
+
+
+@pytest.mark.parametrize("fmt,page", [(BF16, 64), (TURBO8, 0)])
+def test_a_graph_replayed_at_positions_far_apart(fmt, page):
+    """Selection and attention captured once and replayed with positions from the first token to the last, in any
+    order (one CTA, few parts, all of them): each replay gives the eager call's bits, whatever ran before it."""
+    s = Setup("tiny", fmt, [12000, 12000, 12000], page=page, block=16, seed=5)
+    s.set_bounds()
+    q = s.q.cuda()
+    blocks = torch.zeros(3, 1, 20, dtype=torch.int32, device="cuda")
+    out, part = torch.zeros_like(q), torch.zeros_like(q)
+
+    def step(scratch):
+        assert B.qwen35_select_blocks(s.cfg, s.kv, s.r, s.bounds, q, blocks, scratch) == 0
+        assert B.qwen35_decode_attention(s.cfg, s.kv, s.r, q, out, scratch) == 0
+        assert B.qwen35_decode_attention(s.cfg, s.kv, s.r, q, part, scratch, blocks=blocks, block=16) == 0
+
+    step(s.scratch)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        step(s.scratch)
+    for pos in ([0, 15, 16], [11999, 0, 300], [5, 11999, 7000], [319, 320, 321], [11999] * 3, [1, 2, 3], [0, 15, 16]):
+        s.pos.copy_(torch.tensor(pos, dtype=torch.int32))
+        for t in (blocks, out, part):
+            t.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [t.clone() for t in (blocks, out, part)]
+        for t in (blocks, out, part):
+            t.zero_()
+        fresh = B.new_scratch(s.scratch.numel())
+        step(fresh)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, (blocks, out, part)))
+        for r, p in enumerate(pos):
+            np.testing.assert_array_equal(got[0][r].cpu().numpy(), choose(s, r, r, p, 20, 1, 1))
+            ref, size = weighted(s, r, r, p)
+            err = np.linalg.norm(f64(got[1][r]) - ref, axis=1)
+            assert np.all(err <= 2.0 ** -8 * np.linalg.norm(ref, axis=1) +
+                          (2.0 ** -10 + 2.0 ** -12) * np.linalg.norm(size, axis=1))
+    assert s.status() == 0
+
+
+def test_the_most_rows_of_an_append_and_a_read():
+    """2^20 rows of one sequence, in both formats; the last row lies at the last position."""
+    init()
+    cfg = B.make_config(synth.config("tiny"))
+    n, D = 1 << 20, 64
+    x = torch.randn(n, 1, D, device="cuda", generator=torch.Generator("cuda").manual_seed(1)).to(torch.bfloat16)
+    rows = B.DeviceRows(torch.zeros(1, dtype=torch.int32, device="cuda"),
+                        torch.tensor([0, n], dtype=torch.int32, device="cuda"), n)
+    scratch = B.new_scratch(B.qwen35_cache_scratch_bytes(cfg, n, 0, n))
+    for fmt in (BF16, TURBO8):
+        kind = torch.bfloat16 if fmt == BF16 else torch.uint8
+        t = [torch.zeros(n, 1, D, dtype=kind, device="cuda") for _ in "kv"]
+        sc = [torch.zeros(n, 8, dtype=torch.int16, device="cuda") for _ in "kv"]
+        lo_hi = torch.zeros(n // 16, 1, 2, D, dtype=torch.bfloat16, device="cuda")
+        kv = B.qwen35_kv_cache(t[0].data_ptr(), t[1].data_ptr(), n, B.QWEN35_KV_BF16 if fmt == BF16 else B.QWEN35_KV_TURBO8,
+                               sc[0].data_ptr(), sc[1].data_ptr(), None, 0, 0)
+        assert B.qwen35_cache_append(cfg, kv, rows, B.DeviceKeyBounds(lo_hi, 16), x, x.flip(0), scratch) == 0
+        back = [torch.zeros_like(x) for _ in "kv"]
+        assert B.qwen35_cache_read(cfg, kv, rows, *back, scratch) == 0
+        torch.cuda.synchronize()
+        y = x.view(n // 16, 16, 1, D)
+        assert torch.equal(lo_hi[:, :, 0], y.amin(1)) and torch.equal(lo_hi[:, :, 1], y.amax(1))
+        for got, want in zip(back, (x, x.flip(0))):
+            if fmt == BF16:
+                assert torch.equal(got, want)
+            else:  # a rotated value is off by 2^-4 of itself or 2^-10 of its group's largest, and rounded to 8 bits twice
+                norm = want.float().norm(dim=-1)
+                assert bool(((got.float() - want.float()).norm(dim=-1) <= (2.0 ** -4 + 2.0 ** -6) * norm).all())
+    assert B.qwen35_read_device_status(scratch) == 0
