@@ -17,19 +17,23 @@
 // stretch of it, whatever the sequences' lengths. An item that lies in several CTAs is joined by
 // the last of them to finish, in the order of the CTAs, so equal calls give equal bits.
 //
-// Roundings: bf16 K, V and q enter the products exactly, the weights P as hi + lo bf16
+// Roundings. bf16 K, V and q enter the products exactly, the weights P as hi + lo bf16
 // (2^-16 relative). Turbo8 codes enter as f16 (exact); the K scales multiply the fp32
-// products of their 16 dims; the rotated q enters as hi + lo f16 over the power of two of its largest
-// value (2^-22 of a value or 2^-25 of the largest, where the rotation's own sums end too). A token's V scales enter as f16
-// over 2^E, E the exponent of the token's largest (exact down to 2^-17 of that one, lost below 2^-25), and E goes into
-// the exponent of the token's weight: the weights that multiply V are 2^((x - m) + E - M), M the running
-// maximum of (x - m) + E, so a token counts by what it adds and not by its neighbours' sizes, and E is
-// added where large scores have cancelled. m, which the softmax's sum refers to, follows the scores only when one
-// lies 32 octaves above it: 32 bits have room for that, and the lanes exchange one maximum a tile (128K tokens: 68 us;
-// one power of two a tile, which lost tokens beside larger ones, 64). The weights are rounded to f16 (2^-11), up to 2^13 so that f16 holds 2^-27 of the largest in full and what
-// lies 2^-38 below is lost, and rounded again with the scale (2^-11): next to the codes' own 2^-4 and
-// the output's 2^-8 these are small (error against 64 bits 0.00171 at 128K, of fp32 weights 0.00169), and a second
-// f16 for their rest (2^-21) takes 73 us.
+// products of their 16 dims; the rotated q enters as hi + lo f16 over the power of two of
+// its largest value (2^-22 of a value or 2^-25 of the largest, where the rotation's own
+// sums end too).
+// A token's V scales enter as f16 over 2^E, E the exponent of the token's largest (exact
+// down to 2^-17 of that one, lost below 2^-25), and E goes into the exponent of the token's
+// weight: the weights that multiply V are 2^((x - m) + E - M), M the running maximum of
+// (x - m) + E, so a token counts by what it adds and not by its neighbours' sizes, and E is
+// added where large scores have cancelled. m, which the softmax's sum refers to, follows the
+// scores only when one lies 32 octaves above it: 32 bits have room for that, and the lanes
+// exchange one maximum a tile (128K tokens: 68 us; one power of two a tile, which lost
+// tokens beside larger ones: 64).
+// Those weights are rounded to f16 (2^-11), up to 2^13 so that f16 holds 2^-27 of the largest
+// in full and what lies 2^-38 below is lost, and rounded again with the scale (2^-11): next
+// to the codes' own 2^-4 and the output's 2^-8 these are small (error against 64 bits 0.00171
+// at 128K, of fp32 weights 0.00169), and a second f16 for their rest (2^-21) takes 73 us.
 #include "cache_ops.cuh"
 #include "turbo8.cuh"
 
@@ -193,7 +197,7 @@ struct Attention {
   uint32_t warp, lane, group;
   uint32_t pack;  // the most rows of an item
   uint32_t ring;  // this warp's slots
-  float m[NT][2], l[NT][2], o[D / 16][NT][4];  // m: the scores' maximum (T8: or up to kFar below it), which l refers to
+  float m[NT][2], l[NT][2], o[D / 16][NT][4];  // l refers to m, the scores' maximum (T8: or up to kFar below it)
   float mv[NT][2];  // T8: the maximum of V's weights, relative to m, which o refers to
   uint32_t later[NT][2];  // tokens of the item's last row that this column's row does not see
   float qscale[NT][2];  // log2(e) / sqrt(D), with T8's power of two of q
