@@ -155,6 +155,18 @@ _SIGS = {
     "qwen35_decode_attention": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
                                           C.POINTER(qwen35_cache_rows), _P, _P, _U, _P, _U, _U, _P, _P, C.c_size_t,
                                           _P]),
+    "qwen35_rows_scratch_bytes": (C.c_size_t, [C.POINTER(qwen35_config), _U]),
+    "qwen35_cache_append_rope": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
+                                           C.POINTER(qwen35_cache_rows), _P, C.POINTER(qwen35_key_bounds), _P, _U, _P,
+                                           _P, _P, _P, _P, _P, _P, C.c_size_t, _P]),
+    "qwen35_cache_keep": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
+                                    C.POINTER(qwen35_cache_rows), C.POINTER(qwen35_key_bounds), _P, _P, C.c_size_t,
+                                    _P]),
+    "qwen35_tree_attention": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
+                                        C.POINTER(qwen35_cache_rows), _P, _P, _P, _U, _P, _P, C.c_size_t, _P]),
+    "qwen35_window_attention": (C.c_int, [C.POINTER(qwen35_config), C.POINTER(qwen35_kv_cache),
+                                          C.POINTER(qwen35_cache_rows), _U, _U, _P, _P, _U, _P, _P, C.c_size_t, _P]),
+    "qwen35_sample": (C.c_int, [_P, _U, _U, C.c_uint64, _P, _P, _P, _P, _P, _P, _P, _P]),
     "qwen35_debug_scratch_offset": (C.c_size_t, [C.POINTER(qwen35_config), C.c_int, C.c_char_p]),
     "qwen35_debug_stack_scratch_offset": (C.c_size_t, [C.POINTER(qwen35_config), C.c_char_p]),
     "qwen35_debug_stage_dump": (C.c_int, [C.c_int]),
@@ -413,6 +425,48 @@ def qwen35_decode_attention(cfg, kv, rows, q, out, scratch, gate=None, gate_stri
                                          gate_stride or cfg.head_dim, _ptr(blocks),
                                          blocks.shape[-1] if blocks is not None else 0, block, _ptr(out),
                                          _ptr(scratch), scratch.numel(), _stream(stream))
+
+
+def qwen35_rows_scratch_bytes(cfg, max_rows: int) -> int:
+    return lib().qwen35_rows_scratch_bytes(C.byref(cfg), max_rows)
+
+
+def qwen35_cache_append_rope(cfg, kv, rows, q, k, v, q_out, scratch, q_norm=None, k_norm=None, q_stride: int = 0,
+                             rope_pos=None, bounds=None, k_out=None, stream=None):
+    """q, q_out may be None (keys and values alone). q_stride 0: the queries' rows lie head_dim apart."""
+    return lib().qwen35_cache_append_rope(C.byref(cfg), C.byref(kv), C.byref(rows.struct), _ptr(rope_pos),
+                                          C.byref(bounds.struct) if bounds is not None else None, _ptr(q),
+                                          q_stride or cfg.head_dim, _ptr(q_norm), _ptr(k), _ptr(k_norm), _ptr(v),
+                                          _ptr(q_out), _ptr(k_out), _ptr(scratch), scratch.numel(), _stream(stream))
+
+
+def qwen35_cache_keep(cfg, kv, rows, path, scratch, bounds=None, stream=None):
+    return lib().qwen35_cache_keep(C.byref(cfg), C.byref(kv), C.byref(rows.struct),
+                                   C.byref(bounds.struct) if bounds is not None else None, _ptr(path), _ptr(scratch),
+                                   scratch.numel(), _stream(stream))
+
+
+def qwen35_tree_attention(cfg, kv, rows, parent, q, out, scratch, gate=None, gate_stride: int = 0, stream=None):
+    """gate_stride 0: the gate's rows lie head_dim apart."""
+    return lib().qwen35_tree_attention(C.byref(cfg), C.byref(kv), C.byref(rows.struct), _ptr(parent), _ptr(q),
+                                       _ptr(gate), gate_stride or cfg.head_dim, _ptr(out), _ptr(scratch),
+                                       scratch.numel(), _stream(stream))
+
+
+def qwen35_window_attention(cfg, kv, rows, window: int, n_first: int, q, out, scratch, gate=None,
+                            gate_stride: int = 0, stream=None):
+    """gate_stride 0: the gate's rows lie head_dim apart."""
+    return lib().qwen35_window_attention(C.byref(cfg), C.byref(kv), C.byref(rows.struct), window, n_first, _ptr(q),
+                                         _ptr(gate), gate_stride or cfg.head_dim, _ptr(out), _ptr(scratch),
+                                         scratch.numel(), _stream(stream))
+
+
+def qwen35_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, prob=None, stream=None):
+    """logits: bf16 [n_rows][vocab], values of a row side by side, or [vocab]."""
+    n_rows, stride = (logits.shape[0], logits.stride(0)) if len(logits.shape) == 2 else (1, logits.shape[-1])
+    return lib().qwen35_sample(_ptr(logits), n_rows, logits.shape[-1], max(stride, logits.shape[-1]), _ptr(u),
+                               _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(prob),
+                               _stream(stream))
 
 
 def qwen35_debug_scratch_offset(cfg, kind, name: str) -> int:

@@ -15,6 +15,7 @@
 
 #include "qwen35_decode.h"  // include/ (on the include path)
 #include "cache_ops.h"
+#include "rows_ops.h"
 #include "common.cuh"
 #include "decode.h"
 #include "prefill.h"
@@ -382,7 +383,8 @@ int qwen35_init(void) {
     return QWEN35_ERR_CUDA;
   if (major != 10 || minor != 3 || !coop) return QWEN35_ERR_CUDA;  // built for sm_103a only
   if (decode_set_attributes() != cudaSuccess || q35c::attend_attributes() != cudaSuccess ||
-      q35c::select_attributes() != cudaSuccess) return QWEN35_ERR_CUDA;
+      q35c::select_attributes() != cudaSuccess || q35c::rows_attend_attributes() != cudaSuccess ||
+      q35c::sample_attributes() != cudaSuccess) return QWEN35_ERR_CUDA;
   g_num_sms[dev] = sms;
   return QWEN35_OK;
 }
@@ -1317,6 +1319,145 @@ int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,
   a.H = cfg->num_heads;
   a.status = static_cast<int*>(scratch);
   return cu(q35c::attend(a, (cudaStream_t)stream));
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------- operators of a drafting loop
+
+namespace {
+
+// Scratch of these operators: the status word's 256 bytes, then the attention's work space.
+size_t rows_need(const qwen35_config* c, uint32_t n_rows) {
+  return kCacheTickets + q35c::rows_work_bytes(n_rows, c->num_heads, c->num_kv_heads, c->head_dim);
+}
+bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
+
+// The tree's and the window's attention.
+int rows_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                   const qwen35_bf16* q, const qwen35_bf16* gate, uint32_t gate_stride, qwen35_bf16* out, void* scratch,
+                   size_t scratch_bytes, void* stream, q35c::RowsAttend& a, uint64_t tokens) {
+  const int r = cache_begin(cfg, kv, rows, q35c::kMaxQueries, scratch, scratch_bytes, a.c, a.r);
+  if (r) return r;
+  if (!aligned16(q) || !aligned16(out)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (gate && (!aligned16(gate) || gate_stride < a.c.D || gate_stride % 8)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (a.parent == nullptr && a.window == 0) return QWEN35_ERR_INVALID_ARGUMENT;
+  tokens = std::min(tokens, (uint64_t)a.c.capacity);
+  if (tokens * a.r.n_rows * a.c.Hkv >= 16 * q35c::kMaxTiles) return QWEN35_ERR_UNSUPPORTED;
+  if (scratch_bytes < rows_need(cfg, a.r.n_rows)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  a.q = q;
+  a.gate = gate;
+  a.gate_stride = gate_stride;
+  a.out = out;
+  a.work = static_cast<uint8_t*>(scratch) + kCacheTickets;
+  a.sms = (uint32_t)num_sms();
+  a.H = cfg->num_heads;
+  a.wait_ns = g_wait_ns;
+  a.status = static_cast<int*>(scratch);
+  return cu(q35c::rows_attend(a, (cudaStream_t)stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t qwen35_rows_scratch_bytes(const qwen35_config* cfg, uint32_t max_rows) {
+  if (cache_dims(cfg) || max_rows == 0 || max_rows > q35c::kMaxRows) return 0;
+  return rows_need(cfg, std::min(max_rows, q35c::kMaxQueries));
+}
+
+int qwen35_cache_append_rope(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                             const int32_t* rope_pos, const qwen35_key_bounds* bounds, const qwen35_bf16* q,
+                             uint32_t q_stride, const qwen35_bf16* q_norm, const qwen35_bf16* k,
+                             const qwen35_bf16* k_norm, const qwen35_bf16* v, qwen35_bf16* q_out, qwen35_bf16* k_out,
+                             void* scratch, size_t scratch_bytes, void* stream) {
+  q35c::RopeAppend a = {};
+  int r = cache_begin(cfg, kv, rows, q35c::kMaxRows, scratch, scratch_bytes, a.c, a.r);
+  if (r) return r;
+  if (!aligned16(k) || !aligned16(v) || !aligned4(rope_pos)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if ((q_norm && !aligned16(q_norm)) || (k_norm && !aligned16(k_norm)) || (k_out && !aligned16(k_out)))
+    return QWEN35_ERR_INVALID_ARGUMENT;
+  if (q && (!aligned16(q) || !aligned16(q_out) || q_stride < a.c.D || q_stride % 8 || (q == q_out && q_stride != a.c.D)))
+    return QWEN35_ERR_INVALID_ARGUMENT;
+  if (cfg->rotary_dim > a.c.D || cfg->rotary_dim % 2) return QWEN35_ERR_UNSUPPORTED;
+  if (!(cfg->rope_theta > 0.f) || !(cfg->rms_eps >= 0.f)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (bounds) {
+    if ((r = bounds_ok(kv, bounds))) return r;
+    if (!k_out) return QWEN35_ERR_INVALID_ARGUMENT;
+  }
+  if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  a.rope_pos = rope_pos;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.q_norm = q_norm;
+  a.k_norm = k_norm;
+  a.q_out = q_out;
+  a.k_out = k_out;
+  a.H = cfg->num_heads;
+  a.q_stride = q_stride;
+  a.R = cfg->rotary_dim;
+  a.to_cache = !bounds;
+  a.eps = cfg->rms_eps;
+  a.status = static_cast<int*>(scratch);
+  for (uint32_t i = 0; i < a.R / 2; ++i)  // theta^(-2i/R) in double, kept fp32, as in the layer forwards
+    a.inv_freq[i] = (float)std::pow((double)cfg->rope_theta, -2.0 * (double)i / (double)a.R);
+  r = cu(q35c::rope_append(a, (cudaStream_t)stream));
+  if (r || !bounds) return r;
+  // with bounds the rotated keys go on through the append that keeps them
+  return qwen35_cache_append(cfg, kv, rows, bounds, k_out, v, scratch, scratch_bytes, stream);
+}
+
+int qwen35_cache_keep(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                      const qwen35_key_bounds* bounds, const int32_t* path, void* scratch, size_t scratch_bytes,
+                      void* stream) {
+  q35c::Keep a = {};
+  int r = cache_begin(cfg, kv, rows, q35c::kMaxRows, scratch, scratch_bytes, a.c, a.r);
+  if (r) return r;
+  if (!path || !aligned4(path)) return QWEN35_ERR_INVALID_ARGUMENT;
+  if (bounds) {
+    if ((r = bounds_ok(kv, bounds))) return r;
+    a.bounds = bounds->lo_hi;
+    a.blk_shift = log2_of(bounds->block);
+  }
+  if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  a.path = path;
+  a.status = static_cast<int*>(scratch);
+  return cu(q35c::keep(a, (cudaStream_t)stream));
+}
+
+int qwen35_tree_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                          const int32_t* parent, const qwen35_bf16* q, const qwen35_bf16* gate, uint32_t gate_stride,
+                          qwen35_bf16* out, void* scratch, size_t scratch_bytes, void* stream) {
+  if (!parent || !aligned4(parent)) return QWEN35_ERR_INVALID_ARGUMENT;
+  q35c::RowsAttend a = {};
+  a.parent = parent;
+  return rows_attention(cfg, kv, rows, q, gate, gate_stride, out, scratch, scratch_bytes, stream, a, UINT64_MAX);
+}
+
+int qwen35_window_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                            uint32_t window, uint32_t n_first, const qwen35_bf16* q, const qwen35_bf16* gate,
+                            uint32_t gate_stride, qwen35_bf16* out, void* scratch, size_t scratch_bytes, void* stream) {
+  q35c::RowsAttend a = {};
+  a.window = window;
+  a.n_first = n_first;
+  return rows_attention(cfg, kv, rows, q, gate, gate_stride, out, scratch, scratch_bytes, stream, a,
+                        (uint64_t)window + n_first + 256);
+}
+
+int qwen35_sample(const qwen35_bf16* logits, uint32_t n_rows, uint32_t vocab, uint64_t row_stride, const float* u,
+                  const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                  int32_t* token, float* prob, void* stream) {
+  if (!aligned16(logits) || n_rows == 0 || vocab == 0 || row_stride < vocab || !u || !token)
+    return QWEN35_ERR_INVALID_ARGUMENT;
+  if (!aligned4(u) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) ||
+      !aligned4(token) || !aligned4(prob))
+    return QWEN35_ERR_INVALID_ARGUMENT;
+  if (vocab > q35c::kMaxVocab || n_rows > q35c::kMaxSampleRows) return QWEN35_ERR_UNSUPPORTED;
+  if (num_sms() <= 0) return QWEN35_ERR_CUDA;
+  return cu(q35c::sample({logits, u, temperature, top_k, top_p, min_p, token, prob, n_rows, vocab, row_stride},
+                         (cudaStream_t)stream));
 }
 
 }  // extern "C"

@@ -577,6 +577,109 @@ QWEN35_API int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv
                                        uint32_t gate_stride, const int32_t* blocks, uint32_t n_blocks, uint32_t block,
                                        qwen35_bf16* out, void* scratch, size_t scratch_bytes, void* stream);
 
+/* ---------------------------------------------------------------- a drafting loop
+ *
+ * What a serving loop needs beside the cache operators when it drafts several tokens a
+ * step, or lets rows see only the last tokens: rows normed and rotated on their way into
+ * the cache (the layer forwards do it inside), the attention of a tree of drafted tokens,
+ * the accepted path's rows moved together, attention through a sliding window, and the
+ * next tokens sampled from logits. One step: qwen35_cache_append_rope (the tree's rows, rope_pos =
+ * position of each node's level), qwen35_tree_attention, the head, qwen35_sample for every node, the
+ * caller's choice of a path, qwen35_cache_keep. The pages leave all of it to the caller. Dims,
+ * caches and rows are as for the cache operators above, with the same limits and errors.
+ *
+ * Scratch: qwen35_rows_scratch_bytes(cfg, rows of the largest call), made with
+ * qwen35_scratch_init; a scratch of the cache operators does for qwen35_cache_append_rope and
+ * qwen35_cache_keep, which use its first 256 bytes alone. It belongs to one call at a time. About
+ * (rows * num_heads + 160 * 128) * (head_dim + 8) * 4 bytes. 0 for dims the calls reject. */
+QWEN35_API size_t qwen35_rows_scratch_bytes(const qwen35_config* cfg, uint32_t max_rows);
+
+/* Norm and rotate rows and write them to the cache, as forward_full_attention does between
+ * its projections and its attention ("full_attention.rs": q/k norm, RoPE, append):
+ *   q_out = rope(bf16(RMSNorm(q) q_norm)), cached key = rope(bf16(RMSNorm(k) k_norm)),
+ * eps = cfg->rms_eps, RoPE on the first cfg->rotary_dim dims in halves (dim i with
+ * i + rotary_dim / 2) by the angle float(position) * float(rope_theta^(-2i / rotary_dim)), a product
+ * of 32 bits, rounded to bf16 after the norm and after the rotation, all as in the layer forwards, up
+ * to which of two neighbouring bf16 values a sum of squares in another order rounds to. v is
+ * written as it is. A Turbo8 cache takes the rotated rows as qwen35_cache_append does.
+ *  - k, v bf16 [n_rows][num_kv_heads][head_dim]; q NULL, or bf16, head h of row r at
+ *    q + (r * num_heads + h) * q_stride (q_stride >= head_dim, a multiple of 8: q_proj's [Q_h | gate_h]
+ *    rows give 2 * head_dim); q_norm, k_norm bf16 [head_dim], or NULL: not normed.
+ *  - q_out bf16 [n_rows][num_heads][head_dim] (with q); k_out NULL, or bf16 [n_rows][num_kv_heads]
+ *    [head_dim]: the rotated keys as given to the cache. q_out may be q (q_stride = head_dim) and
+ *    k_out may be k; nothing else may overlap.
+ *  - rope_pos NULL: a row turns by its position in the cache; or int32 [n_rows] in device memory: by that
+ *    (a tree's nodes lie one after another and turn by their levels).
+ *  - bounds NULL, or brought up to date as by qwen35_cache_append (k_out is needed then).
+ * Rows that the cache operators skip are skipped, in q_out and k_out too. Errors: INVALID_ARGUMENT,
+ * UNSUPPORTED (as the cache operators; rotary_dim odd or > head_dim), CUDA. */
+QWEN35_API int qwen35_cache_append_rope(const qwen35_config* cfg, const qwen35_kv_cache* kv,
+                                        const qwen35_cache_rows* rows, const int32_t* rope_pos,
+                                        const qwen35_key_bounds* bounds, const qwen35_bf16* q, uint32_t q_stride,
+                                        const qwen35_bf16* q_norm, const qwen35_bf16* k, const qwen35_bf16* k_norm,
+                                        const qwen35_bf16* v, qwen35_bf16* q_out, qwen35_bf16* k_out, void* scratch,
+                                        size_t scratch_bytes, void* stream);
+
+/* Attention of a tree of drafted tokens in each sequence: the sequence's rows are the nodes, node i
+ * at cache position pos[b] + i (its key and value there, so after their append), parent int32
+ * [n_rows]: the node's parent as an index among the sequence's nodes, below its own, or -1 for a child of
+ * the token before the tree. A node sees the tokens [0, pos[b]), its ancestors and itself:
+ * softmax(q . k / sqrt(head_dim)) v over those, times sigmoid(gate), arguments and layout as in
+ * qwen35_decode_attention (which a chain, parent[i] = i - 1, equals). At most 128 nodes a sequence. A node
+ * behind those, or with a parent that is none on the way to -1, sets QWEN35_ERR_DEVICE_RANGE and is
+ * skipped. Keys and values that a row does not see leave no trace in it, infinities and NaN among them.
+ * Scores, maxima and sums are held in fp32 and the output is rounded to bf16 once. The weights enter the
+ * products with V as two bf16 parts (2^-16) with a bf16 cache. With a Turbo8 cache the rotated q, the codes times
+ * their scales and the weights are rounded to f16 (2^-11 each, the keys' and values' over a power of two of
+ * the token's largest, 2^-25 of that at the least), so a score is off by up to 2^-10 of the sum of its
+ * terms' sizes: for scores of usual size (below 100) far less than the codes' own 2^-4. */
+QWEN35_API int qwen35_tree_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                                     const int32_t* parent, const qwen35_bf16* q, const qwen35_bf16* gate,
+                                     uint32_t gate_stride, qwen35_bf16* out, void* scratch, size_t scratch_bytes,
+                                     void* stream);
+
+/* Attention of each row (position p) over the last `window` tokens up to its own, (p - window, p], and the
+ * first n_first tokens [0, n_first) (those of them up to p): attention sinks. window >= 1; one of
+ * the capacity or more gives every token. Only pages that hold such a token are looked up and read, so
+ * others may have been given away. Otherwise as qwen35_tree_attention, for any number of rows a sequence
+ * (2048 a call). */
+QWEN35_API int qwen35_window_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,
+                                       const qwen35_cache_rows* rows, uint32_t window, uint32_t n_first,
+                                       const qwen35_bf16* q, const qwen35_bf16* gate, uint32_t gate_stride,
+                                       qwen35_bf16* out, void* scratch, size_t scratch_bytes, void* stream);
+
+/* Move the rows of an accepted path together: the sequence's rows are the path's entries, path int32
+ * [n_rows], and the cache row at position pos[b] + path[i] goes to pos[b] + i, bit for bit (a Turbo8 cache's
+ * codes and scales), i the entry's place in its sequence. The entries of a sequence rise, begin at 0 or more
+ * and are at most 128; otherwise, or where a position is outside the capacity or a block outside the
+ * pool, QWEN35_ERR_DEVICE_RANGE is set and that sequence's rows stay as they are. Rows behind the path
+ * keep what they hold. bounds: NULL, or widened so that they hold the moved keys. Errors as
+ * qwen35_cache_append. */
+QWEN35_API int qwen35_cache_keep(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
+                                 const qwen35_key_bounds* bounds, const int32_t* path, void* scratch,
+                                 size_t scratch_bytes, void* stream);
+
+/* A token for each row of logits, by the row's own settings and random number:
+ *  1. the tokens in falling order of their logits, the lower index of equal ones first; their weights
+ *     w = exp((logit - largest) / temperature);
+ *  2. top-k: the first top_k of them (0 or less: all);
+ *  3. top-p: of those, each with less than top_p of their sum before it, the first always (1 or more, NaN: all);
+ *  4. min-p: of those, each with w >= min_p (of the largest, which is 1 and always stays);
+ *  5. token = the first whose running sum passes u times the sum of what is left.
+ * temperature not above 0: the first of all, whatever u. Everything is decided on whole multiples of 2^-44 of the
+ * largest weight, so the choice is that of the exact sums but for borders nearer than that; a token of less
+ * has no weight. NaN logits are never chosen (-1, with probability 0, if every logit is one); where the largest is infinite, tokens
+ * equal to it have weight 1 and all others none.
+ *  - logits bf16, row r at logits + r * row_stride (row_stride >= vocab, in elements), as
+ *    qwen35_lm_head_greedy writes them; vocab at most 524160, n_rows at most 65536 (UNSUPPORTED above).
+ *  - u fp32 [n_rows], from [0, 1) (outside: as its nearest end; NaN: 0); temperature, top_p, min_p fp32 [n_rows], top_k
+ *    int32 [n_rows], each or NULL: 1, 1, 0 and 0. All in device memory, read when the kernel runs.
+ *  - token int32 [n_rows], written; prob NULL, or fp32 [n_rows]: the token's probability among what was left.
+ * logits 16-byte aligned, the others 4-byte aligned. No scratch. Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
+QWEN35_API int qwen35_sample(const qwen35_bf16* logits, uint32_t n_rows, uint32_t vocab, uint64_t row_stride,
+                             const float* u, const float* temperature, const int32_t* top_k, const float* top_p,
+                             const float* min_p, int32_t* token, float* prob, void* stream);
+
 /* Byte offset inside a layer's scratch of a named intermediate the last forward of
  * that kind left there, or (size_t)-1 for an unknown name: the counterpart of the
  * intra_dump hook of "linear_attention.rs" (named buffers readable after a stream

@@ -1,0 +1,790 @@
+"""The operators of a drafting loop on the GPU against plain float64 implementations.
+
+Tolerances, derived before the first run (a rounding to bf16 is off by at most 2^-8 of the value, to f16 by
+2^-11, to fp32 by 2^-24):
+ - rows moved, codes and scales of rotated rows against qwen35_cache_append of the same rows, tokens sampled: equal;
+ - a rotated value y = a cos - b sin: its rounding, 2^-8 |y|; the rounding of the normed a and b, 2^-8 (|a| + |b|),
+   where there is a norm; and the fp32 arithmetic, far below 2^-18 (|a| + |b|);
+ - attention over a bf16 cache: the output's rounding, 2^-8 |y|, and 2^-14 of the largest value: the weights
+   are good to 2^-16, scores and sums are fp32;
+ - over a Turbo8 cache the rotated q, the keys and so the scores are off by 2^-11 each: 2^-10 sum |q_d k_d| / sqrt D <=
+   2^-10 |q| |k| / sqrt D = d; weights and values lose 2^-11 each: an error of the rotated output of
+   norm at most (2 d + 2^-10) max |v|, which the rotation back keeps. Roundings are of either sign, so the whole output's
+   2-norm is also held to 2^-8 + 2^-9 of the reference's (one bf16 rounding, and half of that for all others).
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from full_attention_decode_gb300 import binding as B
+from full_attention_decode_gb300 import synth
+from oracle import qwen35_oracle as O
+
+from test_gpu_cache_ops import BF16, HEADS, TURBO8, Setup, bf16, f64
+
+pytestmark = pytest.mark.gpu
+
+NAN = float("nan")
+
+
+def status(s):
+    torch.cuda.synchronize()
+    return B.qwen35_read_device_status(s.scratch)
+
+
+def setup(heads, fmt, lens, rows, **kw):
+    s = Setup(heads, fmt, lens, rows, **kw)
+    s.scratch = B.new_scratch(B.qwen35_rows_scratch_bytes(s.cfg, s.n_rows))
+    return s
+
+
+# ---------------------------------------------------------------- attention
+
+
+def visible_tree(parent, pos, i):
+    see = list(range(pos))
+    while i >= 0:
+        see.append(pos + i)
+        i = parent[i]
+    return see
+
+
+def visible_window(p, window, first):
+    low = max(0, p - window + 1)
+    return list(range(min(first, low))) + list(range(low, p + 1))
+
+
+def expect(s, see, gate=None):
+    """{row: (float64 output [H][D], tolerance)} with see(b, i, p) -> tokens."""
+    out = {}
+    for b, (m, r) in enumerate(zip(s.lens, s.rows)):
+        for i in range(r):
+            row, p = s.start[b] + i, m - r + i
+            t = see(b, i, p)
+            if t is None:
+                continue
+            at = s.at(b, np.asarray(t))
+            k, v = (s.stands[n][at] for n in "kv")
+            q = f64(s.q[row]).reshape(s.Hkv, -1, s.D)
+            x = np.einsum("ghd,tgd->ght", q, k) / np.sqrt(s.D)
+            w = np.exp(x - x.max(-1, keepdims=True))
+            w /= w.sum(-1, keepdims=True)
+            o = np.einsum("ght,tgd->ghd", w, v).reshape(s.H, s.D)
+            if s.fmt == TURBO8:
+                d = 2.0 ** -10 * np.linalg.norm(q, axis=-1).max() * np.linalg.norm(k, axis=-1).max() / np.sqrt(s.D)
+                tol = (2 * d + 2.0 ** -10) * np.linalg.norm(v, axis=-1).max()
+            else:
+                tol = 2.0 ** -14 * np.abs(v).max()
+            z = 1.0
+            if gate is not None:
+                z = 1 / (1 + np.exp(-f64(gate[row]).reshape(s.H, -1)[:, :s.D]))
+            out[row] = (o * z, tol)
+    return out
+
+
+def check(s, out, want):
+    got = f64(out)
+    for r in range(s.n_rows):
+        if r not in want:
+            assert np.isnan(got[r]).all(), f"row {r} is not left as it was"
+            continue
+        ref, tol = want[r]
+        err = np.abs(got[r] - ref)
+        assert (err <= 2.0 ** -8 * np.abs(ref) + tol).all(), (r, float(np.nanmax(err)), tol, np.isnan(got[r]).sum())
+    if want:
+        a, b = (np.stack([x[r] for r in sorted(want)]) for x in (got, {r: w[0] for r, w in want.items()}))
+        assert np.linalg.norm(a - b) <= (2.0 ** -8 + 2.0 ** -9) * np.linalg.norm(b)
+
+
+def blank(s):
+    return torch.full((s.n_rows, s.H, s.D), NAN, dtype=torch.bfloat16, device="cuda")
+
+
+def tree_of(kind, n, rng):
+    if kind == "chain":
+        return [i - 1 for i in range(n)]
+    if kind == "star":
+        return [-1] + [0] * (n - 1)
+    if kind == "forest":
+        return [-1 if i % 5 == 0 else int(rng.integers(0, i)) for i in range(n)]
+    return [-1] + [int(rng.integers(max(0, (i - 1) // 4), i)) for i in range(1, n)]
+
+
+def run_tree(s, parents, gate=None, **kw):
+    flat = np.full(s.n_rows, 7777, dtype=np.int32)
+    for b, p in enumerate(parents):
+        flat[s.start[b]:s.start[b] + len(p)] = p
+    out = blank(s)
+    rc = B.qwen35_tree_attention(s.cfg, s.kv, s.r, torch.from_numpy(flat).cuda(), s.q.cuda(), out, s.scratch, gate=gate,
+                                 **kw)
+    assert rc == 0
+    return out
+
+
+@pytest.mark.parametrize("heads", list(HEADS))
+@pytest.mark.parametrize("fmt,page", [(BF16, 0), (BF16, 16), (TURBO8, 0), (TURBO8, 64)])
+def test_trees(heads, fmt, page):
+    rng = np.random.default_rng(1)
+    nodes = [1, 7, 0, 33, 16, 64, 5]
+    before = [0, 1, 40, 63, 200, 130, 517]
+    s = setup(heads, fmt, [n + b for n, b in zip(nodes, before)], nodes, page=page, lead=2, tail=3)
+    kinds = ["chain", "star", "chain", "random", "forest", "random", "chain"]
+    parents = [tree_of(k, n, rng) if n else [] for k, n in zip(kinds, nodes)]
+    out = run_tree(s, parents)
+    check(s, out, expect(s, lambda b, i, p: visible_tree(parents[b], before[b], i)))
+    assert status(s) == 0
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("n", [31, 32, 33, 65, 127, 128])
+@pytest.mark.parametrize("kind", ["chain", "random"])
+def test_large_trees_with_gates(fmt, n, kind):
+    rng = np.random.default_rng(n)
+    s = setup("4b", fmt, [300 + n, n], [n, n], page=16)
+    parents = [tree_of(kind, n, rng) for _ in range(2)]
+    gate = bf16(rng.standard_normal((s.n_rows, s.H, 2 * s.D))).cuda()
+    out = run_tree(s, parents, gate=gate, gate_stride=2 * s.D)
+    check(s, out, expect(s, lambda b, i, p: visible_tree(parents[b], [300, 0][b], i), gate))
+    assert status(s) == 0
+
+
+@pytest.mark.parametrize("heads,fmt", [("4b", BF16), ("4b", TURBO8), ("tiny_alt", TURBO8), ("tiny", BF16)])
+def test_a_long_context_is_split_and_joined(heads, fmt):
+    rng = np.random.default_rng(5)
+    s = setup(heads, fmt, [9001 + 40, 700 + 3], [40, 3], page=32)
+    parents = [tree_of("random", 40, rng), tree_of("star", 3, rng)]
+    want = expect(s, lambda b, i, p: visible_tree(parents[b], [9001, 700][b], i))
+    first = run_tree(s, parents)
+    check(s, first, want)
+    for _ in range(3):
+        assert torch.equal(run_tree(s, parents).view(torch.int16), first.view(torch.int16))
+    assert status(s) == 0
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("bad", [NAN, float("inf"), -float("inf")])
+def test_nodes_that_a_row_does_not_see_leave_no_trace(fmt, bad):
+    """Key and value of a node that holds no number: only the nodes below it are spoiled."""
+    s = setup("4b", fmt, [100 + 20], [20], page=16)
+    parent = [-1, 0, 0, 1, 1, 2, 3, 3, 4, 5, 5, 6, 8, 9, -1, 14, 14, 15, 17, 18]
+    at = s.at(0, np.asarray([100 + 3, 100 + 15]))
+    under = [i for i in range(20) if any(t - 100 in (3, 15) for t in visible_tree(parent, 100, i))]
+    if fmt == TURBO8:
+        for n in "kv":
+            s.t[n + "s"][torch.from_numpy(at).cuda()] = bf16([bad]).view(torch.int16).item()
+            s.stands[n][at] = np.nan
+    else:
+        for n in "kv":
+            s.t[n][torch.from_numpy(at).cuda()] = bad
+            s.stands[n][at] = bad
+    out = run_tree(s, [parent])
+    want = expect(s, lambda b, i, p: None if i in under else visible_tree(parent, 100, i))
+    got = f64(out)
+    for i in under:
+        assert not np.isfinite(got[i]).all()
+        out[i] = NAN
+    check(s, out, want)
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_values_that_are_infinite_reach_the_rows_that_see_them(fmt):
+    """One element of one node's value is infinite: the node's descendants get that dimension (Turbo8: its
+    group's scale is infinite, so they get no number), the others nothing."""
+    s = setup("tiny_alt", fmt, [64 + 6], [6])
+    parent, at = [-1, 0, 0, 1, 2, 3], int(s.at(0, 65))
+    if fmt == BF16:
+        s.t["v"][at, 1, 77] = float("inf")
+        s.stands["v"][at, 1, 77] = np.inf
+    else:
+        s.t["vs"][at, (128 + 77) // 16] = bf16([float("inf")]).view(torch.int16).item()
+    got = f64(run_tree(s, [parent]))
+    for i in range(6):
+        below = 1 in [t - 64 for t in visible_tree(parent, 64, i)]
+        assert np.isfinite(got[i][[0, 2]]).all()
+        if fmt == BF16:
+            assert np.isfinite(np.delete(got[i][1], 77)).all()
+            assert not np.isfinite(got[i][1, 77]) if below else np.isfinite(got[i][1, 77])
+        else:
+            assert not np.isfinite(got[i][1]).all() if below else np.isfinite(got[i][1]).all()
+
+
+def test_bad_nodes_are_skipped_and_reported():
+    s = setup("tiny", BF16, [50 + 9, 30 + 4, 20 + 3], [9, 4, 3])
+    parents = [[-1, 0, 5, 2, 1, -2, 5, 7, 0], [-1, 0, 1, 2], [0, 0, 99]]
+    out = run_tree(s, parents)
+    ok = {0: [0, 1, 4, 8], 1: [0, 1, 2, 3], 2: []}
+    check(s, out, expect(s, lambda b, i, p: visible_tree(parents[b], [50, 30, 20][b], i) if i in ok[b] else None))
+    assert status(s) == B.QWEN35_ERR_DEVICE_RANGE
+
+
+def test_nodes_behind_the_most_are_skipped_and_reported():
+    s = setup("tiny", BF16, [10 + 131], [131])
+    parent = [-1] + [0] * 130
+    out = run_tree(s, [parent])
+    check(s, out, expect(s, lambda b, i, p: visible_tree(parent, 10, i) if i < 128 else None))
+    assert status(s) == B.QWEN35_ERR_DEVICE_RANGE
+
+
+@pytest.mark.parametrize("pos", [-1, 2 ** 31 - 1, 190])
+def test_trees_at_positions_outside_the_cache(pos):
+    s = setup("tiny", BF16, [40 + 5, 60 + 2], [5, 2], page=16)
+    assert s.cap == 64
+    s.pos[0] = pos
+    parents = [tree_of("star", 5, None), [-1, 0]]
+    out = run_tree(s, parents)
+    check(s, out, expect(s, lambda b, i, p: visible_tree(parents[b], 60, i) if b else None))
+    assert status(s) == B.QWEN35_ERR_DEVICE_RANGE
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_blocks_outside_the_pool_are_left_out_and_reported(fmt):
+    s = setup("4b", fmt, [80 + 4], [4], page=16)
+    s.table[0, 2] = s.nb
+    s.table[0, 4] = -5
+    parent = [-1, 0, 0, 1]
+    gone = set(range(32, 48)) | set(range(64, 80))
+    out = run_tree(s, [parent])
+    check(s, out, expect(s, lambda b, i, p: [t for t in visible_tree(parent, 80, i) if t not in gone]))
+    assert status(s) == B.QWEN35_ERR_DEVICE_RANGE
+
+
+def test_a_row_without_a_token_gets_zeros():
+    s = setup("4b", BF16, [3, 70], [1, 2], page=16)
+    s.table[0, 0] = s.nb
+    out = run_tree(s, [[-1], [-1, 0]])
+    assert (out[0] == 0).all()
+    assert torch.isfinite(out[1:].float()).all()
+    assert status(s) == B.QWEN35_ERR_DEVICE_RANGE
+
+
+def run_window(s, window, first, gate=None, **kw):
+    out = blank(s)
+    rc = B.qwen35_window_attention(s.cfg, s.kv, s.r, window, first, s.q.cuda(), out, s.scratch, gate=gate, **kw)
+    assert rc == 0
+    return out
+
+
+@pytest.mark.parametrize("heads", list(HEADS))
+@pytest.mark.parametrize("fmt,page", [(BF16, 0), (BF16, 64), (TURBO8, 0), (TURBO8, 16)])
+@pytest.mark.parametrize("window,first", [(1, 0), (64, 4), (200, 70)])
+def test_windows(heads, fmt, page, window, first):
+    lens = [1, 2, 65, 64, 700, 331, 9]
+    s = setup(heads, fmt, lens, None, page=page)
+    out = run_window(s, window, first)
+    check(s, out, expect(s, lambda b, i, p: visible_window(p, window, first)))
+    assert status(s) == 0
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("window,first", [(1, 0), (1, 1), (7, 0), (63, 5), (65, 64), (128, 0), (10 ** 6, 3), (2 ** 32 - 1, 0),
+                                          (100, 2 ** 32 - 1), (8, 300)])
+def test_windows_of_several_rows(fmt, window, first):
+    s = setup("4b", fmt, [300, 130, 40, 77], [130, 130, 3, 0], page=16, lead=1, tail=2)
+    gate = bf16(s.rng.standard_normal((s.n_rows, s.H, s.D))).cuda()
+    out = run_window(s, window, first, gate=gate)
+    check(s, out, expect(s, lambda b, i, p: visible_window(p, window, first), gate))
+    assert status(s) == 0
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_pages_outside_the_window_are_not_read(fmt):
+    """Their entries name no block, or blocks without a number."""
+    s = setup("4b", fmt, [640, 641], None, page=16)
+    window, first = 100, 20
+    for b, p in enumerate((639, 640)):
+        seen = {t // 16 for t in visible_window(p, window, first)}
+        for j in range(640 // 16 + 1):
+            if j not in seen:
+                s.table[b, j] = -1
+    want = expect(s, lambda b, i, p: visible_window(p, window, first))
+    out = run_window(s, window, first)
+    check(s, out, want)
+    assert status(s) == 0
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("bad", [NAN, float("inf")])
+def test_tokens_that_left_the_window_leave_no_trace(fmt, bad):
+    """Rows of one call: the first ones see a token without a number, the later ones no longer."""
+    s = setup("4b", fmt, [300], [60])
+    at = int(s.at(0, 180))  # seen up to position 180 + 79
+    for n in "kv":
+        if fmt == TURBO8:
+            s.t[n + "s"][at] = bf16([bad]).view(torch.int16).item()
+        else:
+            s.t[n][at] = bad
+        s.stands[n][at] = np.nan
+    out = run_window(s, 80, 2)
+    got = f64(out)
+    assert all(not np.isfinite(got[i]).all() for i in range(20))
+    out[:20] = NAN
+    check(s, out, expect(s, lambda b, i, p: visible_window(p, 80, 2) if i >= 20 else None))
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_a_long_window_of_a_long_context(fmt):
+    s = setup("4b", fmt, [20000, 12345, 4000, 700, 6000], None, page=64)
+    out = run_window(s, 5000, 4)
+    check(s, out, expect(s, lambda b, i, p: visible_window(p, 5000, 4)))
+    assert status(s) == 0
+
+
+@pytest.mark.parametrize("scale", [2.0 ** -40, 2.0 ** 40])
+def test_values_and_scores_of_any_size(scale):
+    """V scaled by a power of two scales the output; q down scales the scores to nothing."""
+    s = setup("4b", TURBO8, [200 + 3], [3])
+    plain = f64(run_tree(s, [[-1, 0, 0]]))
+    s.t["vs"] = (s.t["vs"].view(torch.bfloat16).float() * scale).to(torch.bfloat16).view(torch.int16)
+    s.kv.v_scales = s.t["vs"].data_ptr()
+    assert np.array_equal(f64(run_tree(s, [[-1, 0, 0]])), plain * scale)
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_large_scores(fmt):
+    """One key far ahead of the others, at several places; equal outputs to its value."""
+    s = setup("4b", fmt, [500], None, spread=4.0)
+    s.q = s.q * 16
+    out = run_window(s, 400, 1)
+    want = expect(s, lambda b, i, p: visible_window(p, 400, 1))
+    if fmt == BF16:
+        check(s, out, want)
+    assert torch.isfinite(out.float()).all()
+
+
+def test_chains_are_decode_attention():
+    s = setup("4b", BF16, [900, 77], [6, 2], page=16)
+    out = run_tree(s, [[-1, 0, 1, 2, 3, 4], [-1, 0]])
+    other = blank(s)
+    scratch = B.new_scratch(B.qwen35_cache_scratch_bytes(s.cfg, s.cap, 0, s.n_rows))
+    assert B.qwen35_decode_attention(s.cfg, s.kv, s.r, s.q.cuda(), other, scratch) == 0
+    a, b = f64(out), f64(other)
+    assert (np.abs(a - b) <= 2.0 ** -7 * np.abs(b) + 2.0 ** -13 * 5).all()
+
+
+# ---------------------------------------------------------------- rotated rows
+
+
+def rotated(cfg, x, w, pos):
+    """float64: the normed (not rounded) pairs' parts a, b and the rotated value, dim by dim."""
+    y = f64(x)
+    if w is not None:
+        y = y / np.sqrt((y * y).mean(-1, keepdims=True) + cfg.rms_eps) * f64(w)
+    R = cfg.rotary_dim
+    out, size = y.copy(), np.abs(y)
+    if R:
+        i = np.arange(R // 2)
+        freq = (float(cfg.rope_theta) ** (-2.0 * i / R)).astype(np.float32)
+        a = (np.asarray(pos, dtype=np.float32)[:, None, None] * freq).astype(np.float32).astype(np.float64)
+        lo, hi = y[..., :R // 2], y[..., R // 2:R]
+        out[..., :R // 2] = lo * np.cos(a) - hi * np.sin(a)
+        out[..., R // 2:R] = hi * np.cos(a) + lo * np.sin(a)
+        size[..., :R // 2] = size[..., R // 2:R] = np.abs(lo) + np.abs(hi)
+    return out, size
+
+
+def rope_setup(heads, fmt, lens, rows, R, page=0, **kw):
+    s = setup(heads, fmt, lens, rows, page=page, **kw)
+    s.cfg.rotary_dim, s.cfg.rope_theta, s.cfg.rms_eps = R, 1e7, 1e-6
+    rng = s.rng
+    s.qg = bf16(2 * rng.standard_normal((s.n_rows, s.H, 2 * s.D))).cuda()
+    s.k_new = bf16(3 * rng.standard_normal((s.n_rows, s.Hkv, s.D))).cuda()
+    s.v_new = bf16(rng.standard_normal((s.n_rows, s.Hkv, s.D))).cuda()
+    s.wq, s.wk = (bf16(1 + 0.1 * rng.standard_normal(s.D)).cuda() for _ in range(2))
+    s.q_out = blank(s)
+    s.k_out = torch.full_like(s.k_new, NAN)
+    return s
+
+
+def cache_state(s):
+    return {n: t.clone() for n, t in s.t.items()}
+
+
+@pytest.mark.parametrize("heads,R", [("4b", 64), ("tiny", 16), ("tiny_alt", 32), ("wide", 128), ("eight", 2), ("odd", 6),
+                                     ("twelve", 250), ("4b", 0), ("4b", 256)])
+@pytest.mark.parametrize("fmt,page", [(BF16, 0), (BF16, 16), (TURBO8, 0), (TURBO8, 64)])
+@pytest.mark.parametrize("norm", [True, False])
+def test_rotated_rows(heads, R, fmt, page, norm):
+    lens, rows = [1, 90, 64, 700, 30], [1, 17, 0, 40, 3]
+    s = rope_setup(heads, fmt, lens, rows, R, page=page, lead=2, tail=1)
+    before = cache_state(s)
+    kw = dict(q_norm=s.wq, k_norm=s.wk) if norm else {}
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, s.qg, s.k_new, s.v_new, s.q_out, s.scratch, q_stride=2 * s.D,
+                                      k_out=s.k_out, **kw) == 0
+    assert status(s) == 0
+    rows_pos = list(s.each_row())
+    idx, pos = [r for r, _, _ in rows_pos], [p for _, _, p in rows_pos]
+    for got, x, w in ((s.q_out, s.qg[..., :s.D], s.wq), (s.k_out, s.k_new, s.wk)):
+        ref, size = rotated(s.cfg, x[idx], w if norm else None, pos)
+        tol = 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 if norm else 0) * size + 2.0 ** -18 * size
+        assert (np.abs(f64(got[idx]) - ref) <= tol).all()
+        rest = [r for r in range(s.n_rows) if r not in idx]
+        assert torch.isnan(got[rest].float()).all()
+    # the cache: what qwen35_cache_append makes of the rotated keys, and nothing else
+    after = cache_state(s)
+    for n in s.t:
+        s.t[n].copy_(before[n])
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, None, s.k_out, s.v_new, s.scratch) == 0
+    for n in s.t:
+        assert torch.equal(s.t[n].view(torch.uint8), after[n].view(torch.uint8)), n
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_positions_of_a_tree_and_far_ones(fmt):
+    s = rope_setup("4b", fmt, [100, 50], [10, 4], 64, page=16)
+    where = [0, 5, 131071, 7, 1 << 20, 105615, 105616, 99999999, 3, 2 ** 31 - 1, 0, 1, 1, 2]
+    rp = torch.tensor(where, dtype=torch.int32, device="cuda")
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, s.qg, s.k_new, s.v_new, s.q_out, s.scratch, q_norm=s.wq,
+                                      k_norm=s.wk, q_stride=2 * s.D, rope_pos=rp, k_out=s.k_out) == 0
+    for got, x, w in ((s.q_out, s.qg[..., :s.D], s.wq), (s.k_out, s.k_new, s.wk)):
+        ref, size = rotated(s.cfg, x, w, where)
+        assert (np.abs(f64(got) - ref) <= 2.0 ** -8 * np.abs(ref) + (2.0 ** -8 + 2.0 ** -18) * size).all()
+
+
+@pytest.mark.parametrize("heads,fmt,page", [("4b", BF16, 64), ("4b", TURBO8, 0), ("tiny", TURBO8, 32)])
+def test_in_place_and_with_bounds(heads, fmt, page):
+    lens, rows = [90, 33], [50, 33]
+    s = rope_setup(heads, fmt, lens, rows, 16, page=page, block=16)
+    q = s.qg[..., :s.D].contiguous()
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, q, s.k_new, s.v_new, s.q_out, s.scratch, q_norm=s.wq,
+                                      k_norm=s.wk, k_out=s.k_out) == 0
+    one, k1, q1 = cache_state(s), s.k_out.clone(), s.q_out.clone()
+    s.lo_hi.zero_()
+    k_in = s.k_new.clone()
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, q, k_in, s.v_new, q, s.scratch, q_norm=s.wq, k_norm=s.wk,
+                                      k_out=k_in, bounds=s.bounds) == 0
+    assert torch.equal(q, q1) and torch.equal(k_in, k1)
+    for n in s.t:
+        assert torch.equal(s.t[n].view(torch.uint8), one[n].view(torch.uint8)), n
+    got = s.lo_hi.clone()
+    s.lo_hi.zero_()
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, s.bounds, k1, s.v_new, s.scratch) == 0
+    assert torch.equal(got, s.lo_hi)
+
+
+def test_keys_alone_and_rows_outside():
+    s = rope_setup("tiny", BF16, [20, 30, 10], [2, 3, 1], 16, page=16)
+    s.pos[1] = s.cap - 1  # its second row is outside
+    s.table[2, 0] = s.nb
+    before = cache_state(s)
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, None, s.k_new, s.v_new, None, s.scratch, k_norm=s.wk,
+                                      k_out=s.k_out) == 0
+    assert status(s) == B.QWEN35_ERR_DEVICE_RANGE
+    assert torch.isfinite(s.k_out[[0, 1, 2]].float()).all() and torch.isnan(s.k_out[[3, 4, 5]].float()).all()
+    changed = (s.t["k"].view(torch.int16) != before["k"].view(torch.int16)).any(-1).any(-1).sum()
+    assert changed == 3
+
+
+def test_rotated_rows_are_those_of_the_prefill():
+    """A layer's own keys and values, cached by its prefill: within one bf16 step of the operator's from
+    the projections that the layer left in its scratch would be, here from its cached, turned-back rows: a row
+    turned by p, then by -p, is itself within two roundings."""
+    s = rope_setup("4b", BF16, [40], [40], 64)
+    rp = torch.arange(40, dtype=torch.int32, device="cuda")
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, None, s.k_new, s.v_new, None, s.scratch, k_out=s.k_out,
+                                      rope_pos=rp) == 0
+    back = torch.empty_like(s.k_out)
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, None, s.k_out, s.v_new, None, s.scratch, k_out=back,
+                                      rope_pos=-rp) == 0
+    a, b = f64(back), f64(s.k_new)
+    size = np.abs(b).copy()
+    size[..., :32] = size[..., 32:64] = np.abs(b[..., :32]) + np.abs(b[..., 32:64])
+    assert (np.abs(a - b) <= 2.0 ** -8 * np.abs(b) + 2 * 2.0 ** -8 * size).all()
+
+
+# ---------------------------------------------------------------- kept rows
+
+
+def run_keep(s, paths, bounds=None):
+    flat = [x for p in paths for x in p]
+    start = np.concatenate([[0], np.cumsum([len(p) for p in paths])]).astype(np.int32)
+    rows = B.DeviceRows(s.pos, torch.from_numpy(start).cuda(), max(1, len(flat)), s.nb)
+    path = torch.tensor(flat or [0], dtype=torch.int32, device="cuda")
+    return B.qwen35_cache_keep(s.cfg, s.kv, rows, path, s.scratch, bounds=bounds)
+
+
+@pytest.mark.parametrize("heads", ["4b", "tiny", "tiny_alt", "wide"])
+@pytest.mark.parametrize("fmt,page", [(BF16, 0), (BF16, 16), (TURBO8, 0), (TURBO8, 8)])
+def test_kept_rows(heads, fmt, page):
+    n = [20, 128, 64, 1, 9, 128]
+    s = setup(heads, fmt, [b + x for b, x in zip([5, 70, 0, 33, 16, 8], n)], n, page=page, block=16 if page != 8 else 16)
+    rng = np.random.default_rng(3)
+    paths = [[0, 2, 9, 19], sorted(rng.choice(128, 40, replace=False).tolist()), [], [0], [8], list(range(128))]
+    want = cache_state(s)
+    for b, path in enumerate(paths):
+        p0 = int(s.pos[b])
+        src = torch.from_numpy(s.at(b, p0 + np.asarray(path, dtype=np.int64))).cuda()
+        dst = torch.from_numpy(s.at(b, p0 + np.arange(len(path)))).cuda()
+        for t in want:
+            want[t][dst] = want[t][src].clone()
+    assert run_keep(s, paths) == 0
+    assert status(s) == 0
+    for t in want:
+        assert torch.equal(s.t[t].view(torch.uint8), want[t].view(torch.uint8)), t
+
+
+@pytest.mark.parametrize("path", [[3, 2], [1, 1], [-1, 2], [0, 5, 4000], list(range(129))])
+def test_bad_paths_move_nothing(path):
+    s = setup("tiny", BF16, [40 + 130, 40 + 130], [130, 130], page=16)
+    before = cache_state(s)
+    assert run_keep(s, [path, [0, 4]]) == 0
+    assert status(s) == B.QWEN35_ERR_DEVICE_RANGE
+    dst, src = int(s.at(1, 41)), int(s.at(1, 44))
+    before["k"][dst], before["v"][dst] = before["k"][src].clone(), before["v"][src].clone()
+    for t in before:
+        assert torch.equal(s.t[t].view(torch.uint8), before[t].view(torch.uint8))
+
+
+def test_paths_in_blocks_outside_the_pool():
+    s = setup("tiny", BF16, [16 + 20], [20], page=16)
+    s.table[0, 2] = s.nb + 4
+    before = cache_state(s)
+    assert run_keep(s, [[0, 17]]) == 0
+    assert status(s) == B.QWEN35_ERR_DEVICE_RANGE
+    assert torch.equal(s.t["k"].view(torch.uint8), before["k"].view(torch.uint8))
+
+
+def test_bounds_hold_the_kept_keys():
+    s = setup("4b", BF16, [25 + 60], [60], page=32, block=16)
+    s.set_bounds()
+    path = [0, 8, 20, 21, 39, 59]
+    assert run_keep(s, [path], bounds=s.bounds) == 0
+    lo_hi = f64(s.lo_hi)
+    for i in range(len(path)):
+        at = int(s.at(0, 25 + i))
+        key = f64(s.t["k"][at])
+        lo, hi = lo_hi[at // 16, :, 0], lo_hi[at // 16, :, 1]
+        assert (lo <= key).all() and (key <= hi).all()
+
+
+# ---------------------------------------------------------------- sampling
+
+
+def plain_sample(x, u, t=1.0, k=0, p=1.0, m=0.0):
+    """float64, one row [vocab] of logits: (token, probability)."""
+    ids = np.nonzero(~np.isnan(x))[0]
+    if len(ids) == 0:
+        return -1, 0.0
+    x = x[ids]
+    order = np.lexsort((ids, -x))
+    x, ids = x[order], ids[order]
+    if not t > 0:
+        return int(ids[0]), 1.0
+    with np.errstate(invalid="ignore"):
+        w = np.where(x == x[0], 1.0, np.exp((x - x[0]) / t))
+    if k > 0:
+        w = w[:k]
+    if p < 1:
+        c = np.cumsum(w)
+        w = w[:1 + int((c[:-1] < max(p, 0.0) * c[-1]).sum())]
+    w = w[w >= min(m, 1.0)] if m > 0 else w
+    c = np.cumsum(w)
+    u = 0.0 if not u > 0 else u
+    j = min(int((c <= u * c[-1]).sum()), int((w > 0).sum()) - 1)
+    return int(ids[j]), w[j] / c[-1]
+
+
+def dev(x, dtype=torch.float32):
+    return None if x is None else torch.tensor(np.asarray(x), dtype=dtype, device="cuda")
+
+
+def run_sample(x, u, t=None, k=None, p=None, m=None):
+    n = x.shape[0]
+    token = torch.full((n,), -7, dtype=torch.int32, device="cuda")
+    prob = torch.full((n,), NAN, device="cuda")
+    u = dev(u)
+    rc = B.qwen35_sample(x, u, token, temperature=dev(t), top_k=dev(k, torch.int32), top_p=dev(p), min_p=dev(m), prob=prob)
+    assert rc == 0
+    return token.cpu().numpy(), prob.cpu().numpy()
+
+
+def check_sample(x, u, t=None, k=None, p=None, m=None):
+    token, prob = run_sample(x, u, t, k, p, m)
+    f32 = lambda v, r, d: d if v is None else float(np.float32(v[r]))  # noqa: E731
+    host = f64(x)
+    for r in range(x.shape[0]):
+        want, q = plain_sample(host[r], float(np.float32(u[r])), f32(t, r, 1.0), 0 if k is None else int(k[r]),
+                               f32(p, r, 1.0), f32(m, r, 0.0))
+        assert token[r] == want, (r, token[r], want)
+        # fp32 roundings of weight, sum and quotient, and the weight's own 2^-44 of the largest
+        assert abs(prob[r] - q) <= 2.0 ** -21 * q + 2.0 ** -43, (r, prob[r], q)
+
+
+def logits(n, vocab, seed=0, spread=2.5):
+    rng = np.random.default_rng(seed)
+    x = spread * rng.standard_normal((n, vocab))
+    for r in range(n):
+        x[r, rng.integers(0, vocab, 12)] += 8
+    return bf16(x).cuda()
+
+
+@pytest.fixture(autouse=True)
+def _init():
+    from harness import init
+    init()
+
+
+@pytest.mark.parametrize("vocab", [1, 2, 7, 8, 9, 63, 64, 65, 500, 4097, 65537, 248320])
+@pytest.mark.parametrize("mode", ["none", "all", "mixed"])
+def test_samples(vocab, mode):
+    n = 24 if vocab < 60000 else 9
+    rng = np.random.default_rng(vocab)
+    x = logits(n, vocab, vocab)
+    u, t = rng.random(n), 0.3 + 1.5 * rng.random(n)
+    if mode == "none":
+        return check_sample(x, u, t)
+    k = rng.integers(1, 100, n) * (1 if mode == "all" else rng.integers(0, 2, n))
+    p = 0.3 + 0.69 * rng.random(n) if mode == "all" else np.where(rng.random(n) < 0.5, rng.random(n), 1.0)
+    m = 0.2 * rng.random(n) * (1 if mode == "all" else rng.integers(0, 2, n))
+    check_sample(x, u, t, k, p, m)
+
+
+def test_settings_at_their_ends():
+    inf = float("inf")
+    rows = [dict(u=0.0), dict(u=1.0), dict(u=-3.0), dict(u=NAN), dict(u=7.0), dict(u=1 - 2.0 ** -24), dict(t=0.0), dict(t=-1.0),
+            dict(t=NAN), dict(t=1e-30), dict(t=1e30), dict(t=inf), dict(k=1), dict(k=-4), dict(k=2 ** 31 - 1), dict(k=1000),
+            dict(p=0.0), dict(p=-1.0), dict(p=1e-9), dict(p=NAN), dict(p=2.0), dict(m=1.0), dict(m=5.0), dict(m=NAN),
+            dict(m=-1.0), dict(k=3, p=0.0, m=1.0), dict(t=0.0, k=5, u=0.9), dict(k=5, t=100.0, u=0.999)]
+    d = dict(u=0.6, t=0.9, k=0, p=1.0, m=0.0)
+    rows = [d | r for r in rows]
+    x = logits(1, 1000, 3).expand(len(rows), -1).contiguous()
+    check_sample(x, *([r[n] for r in rows] for n in "utkpm"))
+
+
+@pytest.mark.parametrize("values", [[0.0], [1.0, -0.0, 0.0], [2.0, 2.0, -3.0], [-1e38, -1e38, -3e38], [5.0, -float("inf")],
+                                    [-float("inf")], [float("inf"), 3.0], [NAN, 1.0, 0.5], [NAN], [3.4e38, -3.4e38]])
+def test_few_values(values):
+    """Ties in the thousands: the lower indexes first, whatever the cuts."""
+    rng = np.random.default_rng(0)
+    n, vocab = 16, 3001
+    x = bf16(rng.choice(values, (n, vocab))).cuda()
+    u = np.arange(n) / n
+    with np.errstate(over="ignore"):
+        check_sample(x, u)
+        check_sample(x, u, k=1 + np.arange(n) * 150)
+        check_sample(x, u, p=np.float32((1 + np.arange(n)) / 16.0))
+        check_sample(x, u, t=np.full(n, 2.0), k=np.full(n, 700), p=np.full(n, 0.5), m=np.full(n, 0.3))
+
+
+def test_the_largest_vocabulary_of_one_value():
+    """Counts at their most: every token of a CTA's part equal."""
+    vocab = 8 * 65520
+    x = torch.ones(3, vocab, dtype=torch.bfloat16, device="cuda")
+    token, prob = run_sample(x, [0.0, 0.5, 1.0])
+    assert token.tolist() == [0, vocab // 2, vocab - 1]
+    assert np.allclose(prob, 1 / vocab, rtol=2.0 ** -22)
+
+
+@pytest.mark.parametrize("vocab,stride", [(500, 500), (501, 501), (777, 1003), (64, 71), (5, 5)])
+def test_rows_at_any_stride(vocab, stride):
+    n = 11
+    base = torch.full((n, stride), 60000.0, dtype=torch.bfloat16, device="cuda")  # the gaps hold larger values
+    x = base[:, :vocab]
+    x.copy_(logits(n, vocab, 5))
+    rng = np.random.default_rng(1)
+    check_sample(x, rng.random(n), k=rng.integers(0, 40, n))
+
+
+def test_many_rows_and_shares():
+    """Tokens come as often as their probabilities say (and every row of 4096 is its own)."""
+    n = 4096
+    x = bf16([[0.0, 1.0, 2.0, -1.0, 0.5]]).cuda().expand(n, -1).contiguous()
+    u = (np.arange(n) + 0.5) / n
+    token, _ = run_sample(x, u)
+    w = np.exp(f64(x[0]))
+    share = np.bincount(token, minlength=5) / n
+    assert np.abs(share - w / w.sum()).max() <= 1.5 / n
+
+
+# ---------------------------------------------------------------- together
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("captured", [False, True])
+def test_a_drafting_step(fmt, captured):
+    """Trees appended, attended, a token sampled for every node, the accepted path kept, the next step on top:
+    the cache then holds what appending the accepted tokens alone would have left, and a captured step does the same."""
+    H, Hkv, D = HEADS["4b"]
+    rows, lens = [7, 7], [100 + 7, 33 + 7]
+    s = rope_setup("4b", fmt, lens, rows, 64, page=16)
+    parent = [-1, 0, 0, 1, 1, 2, 4]
+    depth = torch.tensor([0, 1, 1, 2, 2, 2, 3] * 2, dtype=torch.int32, device="cuda")
+    paths = [[0, 1, 4, 6], [0, 2, 5]]
+    par = torch.tensor(parent * 2, dtype=torch.int32, device="cuda")
+    rope_pos = torch.repeat_interleave(s.pos, 7).int() + depth
+    start = torch.tensor([0, 4, 7], dtype=torch.int32, device="cuda")
+    keep_rows = B.DeviceRows(s.pos, start, 7, s.nb)
+    path = torch.tensor(sum(paths, []), dtype=torch.int32, device="cuda")
+    out, head = blank(s), bf16(s.rng.standard_normal((H * D, 300)) / 64).cuda()
+    lg = torch.empty(s.n_rows, 300, dtype=torch.bfloat16, device="cuda")
+    u = torch.rand(s.n_rows, device="cuda")
+    token = torch.empty(s.n_rows, dtype=torch.int32, device="cuda")
+
+    def step():
+        assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, s.qg, s.k_new, s.v_new, s.q_out, s.scratch, q_norm=s.wq,
+                                          k_norm=s.wk, q_stride=2 * D, rope_pos=rope_pos, k_out=s.k_out) == 0
+        assert B.qwen35_tree_attention(s.cfg, s.kv, s.r, par, s.q_out, out, s.scratch, gate=s.qg[..., D:].contiguous()) == 0
+        torch.matmul(out.flatten(1), head, out=lg)
+        assert B.qwen35_sample(lg, u, token) == 0
+        assert B.qwen35_cache_keep(s.cfg, s.kv, keep_rows, path, s.scratch) == 0
+
+    before = cache_state(s)
+    step()
+    assert status(s) == 0
+    results = [t.clone() for t in (s.q_out, out, token)] + list(cache_state(s).values())
+    if captured:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            step()
+        for n in s.t:
+            s.t[n].copy_(before[n])
+        for t in (s.q_out, out):
+            t.fill_(NAN)
+        g.replay()
+        for a, b in zip([s.q_out, out, token] + list(s.t.values()), results):
+            assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+        assert status(s) == 0
+    # appending the accepted nodes' rows alone leaves the same rows
+    held = cache_state(s)
+    for n in s.t:
+        s.t[n].copy_(before[n])
+    pick = torch.tensor([0, 1, 4, 6, 7, 9, 12], device="cuda")
+    r2 = B.DeviceRows(s.pos, start, 7, s.nb)
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, r2, None, s.k_new[pick], s.v_new[pick], None, s.scratch,
+                                      k_norm=s.wk) == 0
+    for b, p in enumerate(paths):
+        at = torch.from_numpy(s.at(b, int(s.pos[b]) + np.arange(len(p)))).cuda()
+        for n in s.t:
+            assert torch.equal(s.t[n][at].view(torch.uint8), held[n][at].view(torch.uint8))
+
+
+def test_calls_on_other_streams():
+    s = setup("4b", BF16, [500, 90], None, page=16)
+    want = run_window(s, 100, 4)
+    side = torch.cuda.Stream()
+    out = blank(s)
+    q = s.q.cuda()
+    torch.cuda.synchronize()
+    assert B.qwen35_window_attention(s.cfg, s.kv, s.r, 100, 4, q, out, s.scratch, stream=side) == 0
+    side.synchronize()
+    assert torch.equal(out.view(torch.int16), want.view(torch.int16))
+
+
+def test_offsets_past_32_bits():
+    """A contiguous cache of more than 2^32 bytes a tensor: the last sequence's rows lie behind them."""
+    s = setup("4b", BF16, [40], None)
+    cap, n = 1 << 18, 9  # 9 sequences of 2^18 rows of 2 KB
+    k = torch.empty(n * cap, s.Hkv, s.D, dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    lo = cap * (n - 1) + cap - 40
+    k[lo:lo + 40], v[lo:lo + 40] = s.t["k"][:40], s.t["v"][:40]
+    kv = B.qwen35_kv_cache(k.data_ptr(), v.data_ptr(), cap, B.QWEN35_KV_BF16)
+    pos = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    pos[-1] = cap - 1
+    q = s.q.cuda().expand(n, -1, -1).contiguous()
+    out = torch.full_like(q, NAN)
+    scratch = B.new_scratch(B.qwen35_rows_scratch_bytes(s.cfg, n))
+    assert B.qwen35_window_attention(s.cfg, kv, B.DeviceRows(pos), 40, 0, q, out, scratch) == 0
+    ref, tol = expect(s, lambda b, i, p: list(range(40)))[0]
+    assert (np.abs(f64(out[-1]) - ref) <= 2.0 ** -8 * np.abs(ref) + tol).all()
+    assert torch.isnan(out[:-1].float()).all()
