@@ -1351,6 +1351,7 @@ int rows_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qw
   a.gate_stride = gate_stride;
   a.out = out;
   a.work = static_cast<uint8_t*>(scratch) + kCacheTickets;
+  a.wide = (uintptr_t)a.work % 32 == 0;
   a.sms = (uint32_t)num_sms();
   a.H = cfg->num_heads;
   a.wait_ns = g_wait_ns;

@@ -1,130 +1,1097 @@
-// Attention of drafted trees and of rows that see a sliding window (rows_ops.h).
+// Attention of drafted trees and of rows that see a sliding window (rows_ops.h): any number
+// of rows a sequence, one pass over K and V for up to 128 (row, q-head) pairs.
+//
+// An item is a kv-head of a block of a sequence's rows: 128 / group rows, whose (row, q-head) pairs are the
+// M = 128 rows of the products (TMEM's lanes); the tokens come in tiles of 64:
+//   S [128 x 64] = Q [128 x D] K^T,  P = 2^(S - m),  O [128 x D] += P [128 x 64] V,
+// on the fifth-generation tensor cores: Q, K and V in shared memory (V as it lies, rows along the inner
+// dimension), S and O in tensor memory, P written back there as the second product's first factor. A decode row of 4
+// q-heads leaves most of M empty; what bounds the call is the bytes of K and V all the same: a tile of D = 256
+// is 64 KB, 1.5 us of an SM's share of the memory, its products 1 us.
+//
+// Roles of a CTA's 13 warps: 0-3 own a lane of S, P and O each thread (the softmax: no exchange between threads); one
+// thread of warp 4 issues the products; 5-12 fill a ring of K and V tiles, 16-byte pieces by asynchronous
+// copies (pages as small as 8 tokens, rows outside as zeros), Turbo8 through registers as f16. The softmax of a tile
+// runs under the product of the tile before and the scores of the next (two S, two P).
+//
+// The line of all items' tiles is cut into equal stretches, one CTA an SM. A stretch leaves its sums and maxima
+// in the scratch, and a second launch adds an item's parts up in the order of the CTAs, so equal calls give equal
+// bits; its columns are spread over the GPU: one CTA that joined a block of 128 columns would read 2.5 MB.
+//
+// Roundings. bf16: Q, K, V exactly, P as hi + lo bf16 (2^-16). Turbo8: the rotated q as f16 over the power of two of its largest
+// value; K's and V's codes times scale / 2^E, E the exponent of the token's largest scale, as f16 (a product of 4
+// and 8 bits, rounded to 11); 2^E of K multiplies the score in fp32, E of V goes into the weight's exponent: weights of V are
+// 2^((x - m) + E - R) in f16, R following the largest within 2^4, so a token counts by what it adds. l refers to m alone.
+//
+// A tile that not every row of the item sees to its end may hold anything where it is not seen, and 0 times infinity would
+// spoil the rows that do not: V's infinities and NaN are taken out of such tiles (Turbo8: of all) on their way in, and
+// added by plain arithmetic for the rows that see them (`mend`).
 #include "rows_ops.h"
 
 #include "cache_ops.cuh"
+#include "tcgen05.cuh"
 #include "turbo8.cuh"
+
+#include <algorithm>
 
 namespace q35c {
 using namespace q35;
 namespace {
 
-// A warp a (row, q-head), token after token.
-template <int D, bool T8>
-__global__ void __launch_bounds__(128) rows_kernel(const __grid_constant__ RowsAttend a) {
-  constexpr int E = D / 32;
-  pdl_wait();
-  pdl_launch();
-  const uint32_t item = blockIdx.x * 4 + threadIdx.x / 32, lane = threadIdx.x & 31;
-  if (item >= a.r.n_rows * a.H) return;
-  const uint32_t r = item / a.H, h = item % a.H, g = h / (a.H / a.c.Hkv);
-  uint32_t seq, pos, index, left;
-  const RowKind kind = locate(a.r, a.c.capacity, r, seq, pos, index, left);
-  if (kind != kRowOk) {
-    if (kind == kRowBad && lane == 0) set_status(a.status, kStatusRange);
-    return;
+constexpr uint32_t kM = 128, kTile = 64, kOctets = kTile / 8;
+constexpr uint32_t kLoaders = 8, kLoadThreads = 32 * kLoaders, kRowsThreads = 128 + 32 + kLoadThreads;
+constexpr uint32_t kLead = 2;   // what an item's beginning and end cost a CTA, in tiles
+constexpr uint32_t kLeast = 2;  // tiles of a stretch at least
+constexpr float kSlack = 8.f;   // how far a score may lie above what P and l refer to before they are moved
+constexpr float kSlack8 = 4.f, kUp8 = 11.f;  // Turbo8's weights of V: at most 2^(kUp8 + kSlack8) in f16
+constexpr uint32_t kInfo = 8;   // tiles whose notes are kept (a ring of 4 tiles and two of the softmax's)
+
+template <int D>
+struct Ring {
+  static constexpr uint32_t bytes = kTile * D * 2;                // K or V of a tile
+  static constexpr uint32_t slots = D == 256 ? 4 : 8;             // even ones K, odd ones V
+  static constexpr uint32_t slab = kTile * 128, q_slab = kM * 128;  // 64 dims of all rows
+  static constexpr uint32_t q = kM * D * 2;
+  static_assert(slots / 2 + 2 <= kInfo, "notes");
+};
+
+// Shared memory behind Q and the ring.
+struct Notes {
+  uint64_t full[8], empty[8], s_full[2], s_free[2], p_full[2], q_full;
+  uint32_t tmem;
+  uint32_t sums[kRowsThreads / 32];
+  uint32_t valid[kInfo];             // octets of the tile that hold tokens
+  uint8_t dirty[kInfo][kLoaders];    // V held something that is no number (a loader warp each)
+  float k_scale[kInfo][kTile], v_exp[kInfo][kTile];  // Turbo8: 2^E of K's tokens, E of V's
+  float q_scale[kM];
+  int32_t parent[kMaxNodes];
+};
+
+// A row of the call as every CTA keeps it.
+struct RowNote {
+  uint32_t pos;
+  uint16_t seq, index;  // index: which of its sequence's rows (clipped)
+};
+
+struct Work {  // the scratch
+  float* nat;      // [n_rows][H][D]: an item's first stretch
+  float* cont;     // [CTAs][128][D]: the stretch of an item that a CTA goes on with
+  float4* nat_ml;  // m, l, R of a column; l < 0: a row that is skipped
+  float4* cont_ml;
+  uint32_t* rec;   // [n_rows][Hkv]: the CTAs of the row's item, its place in the block
+};
+__host__ __device__ inline Work work_of(uint8_t* p, uint32_t n_rows, uint32_t H, uint32_t D) {
+  Work w;
+  w.nat = reinterpret_cast<float*>(p);
+  w.cont = w.nat + (size_t)n_rows * H * D;
+  w.nat_ml = reinterpret_cast<float4*>(w.cont + (size_t)kMaxCtas * kM * D);
+  w.cont_ml = w.nat_ml + (size_t)n_rows * H;
+  w.rec = reinterpret_cast<uint32_t*>(w.cont_ml + kMaxCtas * kM);
+  return w;
+}
+constexpr uint32_t kRecOk = 1u << 24;
+
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
+}
+// Arrive on bar when this thread's copies so far have landed.
+__device__ __forceinline__ void cp_arrive(uint64_t* bar) {
+  asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+__device__ __forceinline__ float ex2(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+__device__ __forceinline__ float pow2(int e) { return __int_as_float((e + 127) << 23); }  // e in [-126, 127]
+__device__ __forceinline__ float finite_or_0(float m) { return m == -INFINITY ? 0.f : m; }
+__device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t pack_f16(float lo, float hi) {
+  const __half2 r = __floats2half2_rn(lo, hi);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t e4m3_to_f16x2(uint32_t two) {
+  uint32_t h2;
+  asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"((uint16_t)two));
+  return h2;
+}
+__device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
+  const __half2 r = __hmul2(*reinterpret_cast<const __half2*>(&a), *reinterpret_cast<const __half2*>(&b));
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+// 16-byte piece j of row r in a slab.
+__device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
+__device__ __forceinline__ uint32_t bits_below(int64_t n) { return n <= 0 ? 0u : n >= 8 ? 0xffu : (1u << n) - 1u; }
+
+// A block of rows and the tokens it sees: octets of eight tokens, nA first ones, then from b8 on.
+struct Block {
+  uint32_t row, rows, seq, index, pos, last;  // pos, last: positions of the first and the last row
+  uint32_t nA, b8, octets;
+  uint32_t from;  // the first token behind nA's that a row sees
+  __device__ __forceinline__ uint32_t token(uint32_t o) const { return o < nA ? 8 * o : b8 + 8 * (o - nA); }
+  __device__ __forceinline__ uint32_t tiles() const { return (octets + kOctets - 1) / kOctets; }
+};
+__device__ __forceinline__ Block block_of(const RowsAttend& a, uint32_t row, uint32_t rows, const RowNote& n) {
+  Block b;
+  b.row = row;
+  b.rows = rows;
+  b.seq = n.seq;
+  b.index = n.index;
+  b.pos = n.pos;
+  b.last = n.pos + rows - 1;
+  b.nA = b.b8 = b.from = 0;
+  if (!a.parent) {
+    b.from = b.pos + 1 > a.window ? b.pos + 1 - a.window : 0;
+    b.b8 = b.from & ~7u;
+    b.nA = a.n_first / 8 + (a.n_first % 8 != 0);
+    if (b.nA > b.b8 / 8) b.nA = b.b8 = b.from = 0;  // the first tokens reach the window
   }
-  uint32_t line[kMaxNodes / 32] = {};
-  if (a.parent) {
-    bool bad = index >= kMaxNodes || index > r;  // the latter: row starts that fall below 0
-    for (int32_t i = (int32_t)index; !bad;) {
-#pragma unroll
-      for (uint32_t w = 0; w < kMaxNodes / 32; ++w)
-        if (i / 32 == (int32_t)w) line[w] |= 1u << (i % 32);
-      const int32_t p = a.parent[r - index + i];
-      if (p == -1) break;
-      bad = p < 0 || p >= i;
-      i = p;
+  b.octets = b.nA + (b.last - b.b8) / 8 + 1;
+  return b;
+}
+// Whether every row of the block sees all of octet o.
+__device__ __forceinline__ bool octet_full(const RowsAttend& a, const Block& b, uint32_t o) {
+  if (o >= b.octets) return false;
+  const uint32_t t = b.token(o);
+  if (a.parent) return t + 7 < b.pos - b.index;
+  return t + 7 <= b.pos && (b.last - t < a.window || (t < a.n_first && a.n_first - t >= 8));
+}
+
+// A CTA's stretch of an item.
+struct Stretch {
+  Block b;
+  uint32_t g, t0, t1, c0;
+};
+// The line: prefix sums over the rows, the CTA's part [w, w1), cut into stretches.
+struct Line {
+  const RowsAttend& a;
+  const uint32_t* first;
+  const RowNote* note;
+  const uint8_t* rows;
+  uint32_t per, w, w1, row;
+  __device__ __forceinline__ bool next(Stretch& s) {
+    while (w < w1) {
+      const uint32_t Hkv = a.c.Hkv;
+      while (first[row + 1] * Hkv <= w) ++row;
+      s.b = block_of(a, row, rows[row], note[row]);
+      const uint32_t length = s.b.tiles() + kLead, in = w - first[row] * Hkv;
+      s.g = in / length;
+      const uint32_t at = in % length, used = min(length - at, w1 - w);
+      s.t0 = max(at, kLead) - kLead;
+      s.t1 = max(at + used, kLead) - kLead;
+      s.c0 = (w - at + kLead) / per;
+      w += used;
+      if (s.t0 != s.t1) return true;
     }
-    if (bad) {
-      if (lane == 0) set_status(a.status, kStatusRange);
-      return;
+    return false;
+  }
+};
+
+// Bounded waits of one thread: after one has run out no other waits.
+struct Waiter {
+  uint64_t limit;
+  int* status;
+  bool dead;
+  __device__ __forceinline__ void operator()(uint64_t* bar, uint32_t parity) {
+    if (!dead && !mbar_wait(bar, parity, limit)) {
+      set_status(status, kStatusTimeout);
+      dead = true;
     }
   }
-  float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-  float buf[E];
-  const uint16_t* qs = a.q + ((size_t)r * a.H + h) * D + lane * E;
+};
+
+// Where a half-tile h (2 n for tile n's K, 2 n + 1 for its V; n counts the CTA's tiles) lies in the ring.
+template <int D>
+struct Place {
+  uint32_t slot, turn;
+  __device__ __forceinline__ explicit Place(uint32_t h) : slot(h % Ring<D>::slots), turn(h / Ring<D>::slots) {}
+};
+
+// ------------------------------------------------------------------ loaders
+
+// Where the octets of four tiles lie, an octet a lane.
+struct Found {
+  size_t row;
+  bool in;
+};
+__device__ __forceinline__ Found find(const RowsAttend& a, const Block& b, uint32_t t, uint32_t lane) {
+  Found f = {0, false};
+  const uint32_t o = t * kOctets + lane;
+  if (o < b.octets) {
+    f.in = cache_row(a.c, b.seq, b.token(o), f.row);
+    if (!f.in) set_status(a.status, kStatusRange);
+  }
+  return f;
+}
+// Rows of the octet at token t that are loaded: [lo, hi).
+__device__ __forceinline__ void octet_rows(const RowsAttend& a, const Block& b, uint32_t o, uint32_t& lo, uint32_t& hi) {
+  const uint32_t t = b.token(o);
+  lo = 0;
+  hi = min(8u, b.last - t + 1);
+  if (o < b.nA) hi = min(8u, a.n_first - t);
+  else if (b.from > t) lo = b.from - t;
+}
+__device__ __forceinline__ bool not_a_number_bf16(uint32_t w) {  // in either half, infinities too
+  return (w & 0x7f80u) == 0x7f80u || (w & 0x7f800000u) == 0x7f800000u;
+}
+
+template <int D>
+__device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line0, uint8_t* ring, Notes& sh, uint32_t tid,
+                                           Waiter& wait) {
+  constexpr uint32_t C = D / 8, STEP = kLoadThreads / C, J = kTile / STEP;  // pieces of a row, rows of a pass, passes
+  const uint32_t warp = tid / 32, lane = tid % 32, r0 = tid / C, c = tid % C;
+  const uint32_t to = (c / 8) * Ring<D>::slab, stride = a.c.Hkv * D;
+  Line line = line0;
+  Stretch s;
+  uint32_t n = 0;
+  while (line.next(s)) {
+    Found now = find(a, s.b, s.t0, lane), then = find(a, s.b, s.t0 + 4, lane);
+    for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
+      const uint32_t i = (t - s.t0) % 4;
+      if (i == 0 && t != s.t0) {
+        now = then;
+        then = find(a, s.b, t + 4, lane);
+      }
+      const bool full = __all_sync(0xffffffffu, octet_full(a, s.b, t * kOctets + lane % 8));
+      const uint32_t valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
+#pragma unroll 1
+      for (uint32_t p = 0; p < 2; ++p) {
+        const Place<D> at(2 * n + p);
+        if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
+        uint8_t* slot = ring + at.slot * Ring<D>::bytes;
+        const uint16_t* base = reinterpret_cast<const uint16_t*>(p ? a.c.v : a.c.k);
+        const uint16_t* src[J];
+        bool in[J];
 #pragma unroll
-  for (int e = 0; e < E; ++e) q[e] = bf16f(qs[e]);
-  auto rotate = [&](float (&x)[E]) {
-#pragma unroll
-    for (int hb = 1; hb < E; hb <<= 1)
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if (!(e & hb)) {
-          const float u = x[e], w = x[e + hb];
-          x[e] = u + w;
-          x[e + hb] = u - w;
+        for (uint32_t j = 0; j < J; ++j) {
+          const uint32_t r = r0 + j * STEP, q = (warp * 32 / C + j * STEP) / 8;  // a warp's rows lie in one octet
+          const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)now.row, 8 * i + q);
+          uint32_t lo, hi;
+          octet_rows(a, s.b, t * kOctets + q, lo, hi);
+          in[j] = (valid >> q & 1) && r % 8 >= lo && r % 8 < hi;
+          src[j] = in[j] ? base + (row + r % 8) * stride + s.g * D + 8 * c : base;
         }
-    for (uint32_t b = 1; b < 32; b <<= 1)
+        if (!p || full) {
+          const uint32_t dst = smem_addr(slot) + to;
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        const float y = __shfl_xor_sync(0xffffffffu, x[e], b);
-        x[e] = lane & b ? y - x[e] : x[e] + y;
+          for (uint32_t j = 0; j < J; ++j) cp16(dst + sw(r0 + j * STEP, c % 8), src[j], in[j]);
+          cp_arrive(&sh.full[at.slot]);
+        } else {
+          uint4 x[J];
+#pragma unroll
+          for (uint32_t j = 0; j < J; ++j) x[j] = in[j] ? load16(src[j]) : make_uint4(0u, 0u, 0u, 0u);
+          bool bad = false;
+#pragma unroll
+          for (uint32_t j = 0; j < J; ++j) {
+            uint32_t* w = &x[j].x;
+#pragma unroll
+            for (uint32_t e = 0; e < 4; ++e)
+              if (not_a_number_bf16(w[e])) {
+                bad = true;
+                if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
+              }
+            *reinterpret_cast<uint4*>(slot + to + sw(r0 + j * STEP, c % 8)) = x[j];
+          }
+          bad = __any_sync(0xffffffffu, bad);
+          if (lane == 0) sh.dirty[n % kInfo][warp] = bad;
+          tm_fence_shared();
+          mbar_arrive(&sh.full[at.slot]);
+        }
+        if (p && tid == 0) {  // an arrival that the notes are released by
+          sh.valid[n % kInfo] = valid;
+          mbar_arrive(&sh.full[at.slot]);
+        }
+      }
+    }
+  }
+  asm volatile("cp.async.wait_all;" ::: "memory");
+}
+
+// Turbo8: sixteen codes and their scale a piece, kHeld half-tiles of them in registers on their way.
+constexpr uint32_t kHeld = 4;
+template <int J>
+struct Codes {
+  uint4 c[J];
+  uint16_t s[J];
+};
+template <int D>
+struct LoadTurbo8 {
+  static constexpr uint32_t C = D / 16, STEP = kLoadThreads / C, J = kTile / STEP;
+  const RowsAttend& a;
+  uint8_t* ring;
+  Notes& sh;
+  uint32_t tid, warp, lane, r0, c;
+  Waiter& wait;
+  // what is fetched: its own walk along the line, kHeld half-tiles ahead
+  Line line;
+  Stretch s;
+  Found now, then;
+  uint32_t t, p;
+  bool more;
+
+  __device__ __forceinline__ void begin() {
+    more = line.next(s);
+    p = 0;
+    if (more) {
+      t = s.t0;
+      now = find(a, s.b, t, lane);
+      then = find(a, s.b, t + 4, lane);
+    }
+  }
+  // The next half-tile; `valid`: its tile's octets.
+  __device__ __forceinline__ void fetch(Codes<J>& x, uint32_t& valid) {
+    valid = 0;
+    if (!more) return;
+    const uint32_t i = (t - s.t0) % 4;
+    valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
+    const uint8_t* base = p ? a.c.v : a.c.k;
+    const uint16_t* sc = p ? a.c.vs : a.c.ks;
+#pragma unroll
+    for (uint32_t j = 0; j < J; ++j) {
+      const uint32_t r = r0 + j * STEP, q = (warp * 32 / C + j * STEP) / 8;
+      const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)now.row, 8 * i + q) + r % 8;
+      uint32_t lo, hi;
+      octet_rows(a, s.b, t * kOctets + q, lo, hi);
+      const bool in = (valid >> q & 1) && r % 8 >= lo && r % 8 < hi;
+      x.c[j] = make_uint4(0u, 0u, 0u, 0u);
+      x.s[j] = 0;
+      if (in) {
+        x.c[j] = load16(base + (row * a.c.Hkv + s.g) * D + 16 * c);
+        x.s[j] = sc[row * a.c.sstride + s.g * C + c];
+      }
+    }
+    if (++p == 2) {
+      p = 0;
+      if (++t == s.t1) {
+        begin();
+      } else if ((t - s.t0) % 4 == 0) {
+        now = then;
+        then = find(a, s.b, t + 4, lane);
+      }
+    }
+  }
+  // Half-tile h into the ring, as f16 over 2^E.
+  __device__ __forceinline__ void put(const Codes<J>& x, uint32_t h, uint32_t valid) {
+    const Place<D> at(h);
+    const uint32_t n = h / 2, v = h % 2;
+    if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
+    uint8_t* slot = ring + at.slot * Ring<D>::bytes + (c / 4) * Ring<D>::slab;
+    bool bad = false;
+#pragma unroll
+    for (uint32_t j = 0; j < J; ++j) {
+      const uint32_t r = r0 + j * STEP;
+      const float scale = bf16f(x.s[j]);
+      const bool number = (x.s[j] & 0x7f80u) != 0x7f80u;
+      float mx = number ? fabsf(scale) : 0.f;
+#pragma unroll
+      for (uint32_t m = 1; m < C; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
+      if (c == 0) (v ? sh.v_exp : sh.k_scale)[n % kInfo][r] = v ? (float)e : pow2(e);
+      float f = scale * pow2(-e);
+      uint32_t w[4] = {x.c[j].x, x.c[j].y, x.c[j].z, x.c[j].w};
+      if (v) {
+        if (!number) {
+          bad = true;
+          f = 0.f;
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // codes 0x7f and 0xff are NaN
+          const uint32_t nan = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          bad |= nan != 0;
+          w[i] &= ~nan;
+        }
+      }
+      const uint32_t f2 = pack_f16(f, f);
+      uint32_t y[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) y[i] = hmul2(e4m3_to_f16x2(w[i / 2] >> (16 * (i % 2))), f2);
+      const uint32_t j8 = (c % 4) * 2;
+      *reinterpret_cast<uint4*>(slot + sw(r, j8)) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(slot + sw(r, j8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+    }
+    if (v) {
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) sh.dirty[n % kInfo][warp] = bad;
+    }
+    tm_fence_shared();
+    mbar_arrive(&sh.full[at.slot]);
+    if (v && tid == 0) {
+      sh.valid[n % kInfo] = valid;
+      mbar_arrive(&sh.full[at.slot]);
+    }
+  }
+  __device__ __forceinline__ void run(uint32_t halves) {
+    Codes<J> x[kHeld];
+    uint32_t valid[kHeld];
+    begin();
+#pragma unroll
+    for (uint32_t k = 0; k < kHeld; ++k) fetch(x[k], valid[k]);
+    for (uint32_t h = 0; h < halves; h += kHeld) {
+#pragma unroll
+      for (uint32_t k = 0; k < kHeld; ++k)
+        if (h + k < halves) {
+          put(x[k], h + k, valid[k]);
+          fetch(x[k], valid[k]);
+        }
+    }
+  }
+};
+
+// ------------------------------------------------------------------ softmax
+
+// V's elements of a tile that are no numbers, which the loaders took out: weight w[j] times each for the rows that see
+// it. Runs after the tile's product; rare, so plain and slow.
+template <int D, bool T8>
+__device__ __noinline__ void mend(const RowsAttend& a, const Block& b, uint32_t g, uint32_t t, uint32_t valid, uint64_t vis,
+                                  const float* w, uint32_t o_col) {
+#pragma unroll 1
+  for (uint32_t j = 0; j < kTile; ++j) {
+    if (!(valid >> (j / 8) & 1)) continue;
+    const uint32_t tok = b.token(t * kOctets + j / 8) + j % 8;
+    const bool see = vis >> j & 1;
+    size_t row;
+    if (!__any_sync(0xffffffffu, see) || tok > b.last || !cache_row(a.c, b.seq, tok, row)) continue;
+    const size_t at = (row * a.c.Hkv + g) * D;
+#pragma unroll 1
+    for (uint32_t d = 0; d < D; ++d) {
+      float x;
+      if constexpr (T8) x = e4m3_pair_value(a.c.v[at + d]).x * bf16f(a.c.vs[row * a.c.sstride + g * (D / 16) + d / 16]);
+      else x = bf16f(reinterpret_cast<const uint16_t*>(a.c.v)[at + d]);
+      if (fabsf(x) < INFINITY) continue;
+      const float o = __uint_as_float(tm_ld1(o_col + d));
+      tm_st1(o_col + d, __float_as_uint(see ? fmaf(w[j], x, o) : o));
+      tm_stored();
+    }
+  }
+}
+
+template <int D, bool T8>
+struct Softmax {
+  const RowsAttend& a;
+  uint8_t* q_sm;
+  Notes& sh;
+  uint32_t tid, warp, lane, tmem, group;
+  Waiter& wait;
+  Work work;
+  float scale;
+  // the thread's column
+  uint32_t p;       // its row's position
+  bool live, skip;  // has a row; the row is skipped
+  uint64_t line0, line1;  // tree: the nodes that the row sees
+  float m, l, R;
+
+  __device__ __forceinline__ uint32_t s_col(uint32_t n) const { return tmem + ((32 * warp) << 16) + (n & 1) * kTile; }
+  __device__ __forceinline__ uint32_t p_col(uint32_t n) const { return tmem + ((32 * warp) << 16) + 128 + (n & 1) * 64; }
+  __device__ __forceinline__ uint32_t o_col() const { return tmem + ((32 * warp) << 16) + 256; }
+
+  __device__ void put_q(const Block& b, uint32_t g) {
+    constexpr uint32_t LPR = D / 8;
+    const uint32_t cols = b.rows * group;
+    const auto from = [&](uint32_t col) { return a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D; };
+#pragma unroll 4
+    for (uint32_t c0 = 0; c0 < cols; c0 += 128 / LPR) {
+      const uint32_t col = c0 + tid / LPR, j = tid % LPR;
+      uint4 u = make_uint4(0u, 0u, 0u, 0u);
+      if (col < cols) u = load16(from(col) + 8 * j);
+      if constexpr (T8) {
+        float x[8], mx = 0.f;
+        unpack8(u, x);
+        wht8<LPR>(x, lane);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+#pragma unroll
+        for (uint32_t w = 1; w < LPR; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127, -126), 126);
+        const float f = pow2(-e2);
+        if (j == 0 && col < cols) sh.q_scale[col] = pow2(e2);
+        u = make_uint4(pack_f16(x[0] * f, x[1] * f), pack_f16(x[2] * f, x[3] * f), pack_f16(x[4] * f, x[5] * f),
+                       pack_f16(x[6] * f, x[7] * f));
+      }
+      if (col < cols) *reinterpret_cast<uint4*>(q_sm + (j / 8) * Ring<D>::q_slab + sw(col, j % 8)) = u;
+    }
+    tm_fence_shared();
+    mbar_arrive(&sh.q_full);
+  }
+
+  __device__ void begin(const Block& b) {
+    const uint32_t r = tid / group;
+    live = tid < b.rows * group;
+    p = b.pos + r;
+    skip = false;
+    line0 = line1 = 0;
+    if (a.parent) {
+      const uint32_t nodes = b.index + b.rows;  // at most kMaxNodes
+      if (tid < nodes) sh.parent[tid] = a.parent[b.row - b.index + tid];
+      named_barrier(1, 128);
+      if (live) {
+        for (int32_t i = (int32_t)(b.index + r);;) {
+          if (i < 64) line0 |= 1ull << i;
+          else line1 |= 1ull << (i & 63);
+          const int32_t up = sh.parent[i];
+          if (up == -1) break;
+          if (up < 0 || up >= i) {
+            skip = true;
+            set_status(a.status, kStatusRange);
+            break;
+          }
+          i = up;
+        }
+      }
+      named_barrier(1, 128);  // the next block's parents come here
+    }
+    m = R = -INFINITY;
+    l = 0.f;
+  }
+
+  // Tokens of tile t that the thread's row sees, of those that are there.
+  __device__ __forceinline__ uint64_t seen(const Block& b, uint32_t t, uint32_t valid) const {
+    uint64_t bits = 0;
+#pragma unroll 1
+    for (uint32_t q = 0; q < kOctets; ++q) {
+      if (!(valid >> q & 1)) continue;
+      const int64_t t0 = b.token(t * kOctets + q);
+      uint32_t x;
+      if (a.parent) {
+        const int64_t off = t0 - (int64_t)(b.pos - b.index);
+        x = bits_below(-off);
+        if (off > -8 && off < 128) {
+          const uint64_t w = off < 0 ? line0 << -off : off < 64 ? line0 >> off | (off ? line1 << (64 - off) : 0) : line1 >> (off - 64);
+          x |= (uint32_t)w & 0xffu;
+        }
+      } else {
+        x = bits_below((int64_t)p + 1 - t0) & (~bits_below((int64_t)p + 1 - (int64_t)a.window - t0) | bits_below((int64_t)a.n_first - t0));
+      }
+      bits |= (uint64_t)(x & 0xffu) << (8 * q);
+    }
+    return bits;
+  }
+
+  __device__ __forceinline__ void rescale_o(float f) {
+#pragma unroll 1
+    for (uint32_t c = 0; c < D; c += 32) {
+      uint32_t r[32];
+      tm_ld32(o_col() + c, r);
+      tm_loaded(r);
+#pragma unroll
+      for (int i = 0; i < 32; ++i) r[i] = __float_as_uint(__uint_as_float(r[i]) * f);
+      tm_st32(o_col() + c, r);
+    }
+    tm_stored();
+  }
+
+  __device__ __forceinline__ void tile(const Stretch& st, uint32_t t, uint32_t n) {
+    const Place<D> pv(2 * n + 1);
+    wait(&sh.full[pv.slot], pv.turn & 1);  // the tile's notes
+    const uint32_t valid = sh.valid[n % kInfo];
+    const bool full = __all_sync(0xffffffffu, octet_full(a, st.b, t * kOctets + lane % 8)) && valid == 0xffu;
+    uint32_t dirty = 0;
+    if (T8 || !full) {
+      const uint2 u = *reinterpret_cast<const uint2*>(sh.dirty[n % kInfo]);
+      dirty = u.x | u.y;
+    }
+    // bf16: only tiles that are not wholly seen have been looked through
+    if (!T8 && __all_sync(0xffffffffu, octet_full(a, st.b, t * kOctets + lane % 8))) dirty = 0;
+    wait(&sh.s_full[n & 1], (n >> 1) & 1);
+    tm_after_sync();
+    const bool busy = 32 * warp < st.b.rows * group;
+    float s[kTile];
+    uint64_t vis = 0;
+    if (busy) {
+      {
+        uint32_t r[32], r2[32];
+        tm_ld32(s_col(n), r);
+        tm_ld32(s_col(n) + 32, r2);
+        tm_loaded(r);
+        tm_loaded(r2);
+#pragma unroll
+        for (int i = 0; i < 32; ++i) {
+          s[i] = __uint_as_float(r[i]);
+          s[32 + i] = __uint_as_float(r2[i]);
+        }
+      }
+      tm_before_sync();
+    }
+    mbar_arrive(&sh.s_free[n & 1]);
+    if (busy) {
+      float mx = -INFINITY;
+      if constexpr (T8) {
+        const float sc = scale * (live ? sh.q_scale[tid] : 0.f);
+#pragma unroll
+        for (uint32_t j = 0; j < kTile; j += 4) {
+          const float4 k = *reinterpret_cast<const float4*>(&sh.k_scale[n % kInfo][j]);
+          s[j] = s[j] * sc * k.x;
+          s[j + 1] = s[j + 1] * sc * k.y;
+          s[j + 2] = s[j + 2] * sc * k.z;
+          s[j + 3] = s[j + 3] * sc * k.w;
+        }
+      }
+      if (!full) {
+        vis = live && !skip ? seen(st.b, t, valid) : 0;
+#pragma unroll
+        for (uint32_t j = 0; j < kTile; ++j) s[j] = vis >> j & 1 ? s[j] : -INFINITY;
+      } else {
+        vis = ~0ull;
       }
 #pragma unroll
-    for (int e = 0; e < E; ++e) x[e] *= rsqrtf((float)D);
-  };
-  if (T8) rotate(q);
-  const float scale = 1.4426950408889634f / sqrtf((float)D);
-  const uint32_t base = pos - (a.parent ? index : 0), low = a.parent || pos < a.window ? 0 : pos - a.window + 1;
-  for (uint32_t t = 0; t <= pos; ++t) {
-    if (a.parent) {
-      const uint32_t i = t - base;
-      if (t >= base && !(line[i / 32] >> (i % 32) & 1)) continue;
-    } else if (t < low && t >= a.n_first) {
-      t = low - 1;
-      continue;
-    }
-    size_t row;
-    if (!cache_row(a.c, seq, t, row)) {
-      if (lane == 0) set_status(a.status, kStatusRange);
-      continue;
-    }
-    const size_t at = (row * a.c.Hkv + g) * D + lane * E;
-    const auto load = [&](const uint8_t* x, const uint16_t* sc) {
-#pragma unroll
-      for (int e = 0; e < E; ++e)
-        if constexpr (T8) {
-          const float2 v = e4m3_pair_value(x[at + e]);
-          buf[e] = v.x * bf16f(sc[row * a.c.sstride + g * (D / 16) + (lane * E + e) / 16]);
-        } else {
-          buf[e] = bf16f(reinterpret_cast<const uint16_t*>(x)[at + e]);
+      for (uint32_t j = 0; j < kTile; ++j) mx = fmaxf(mx, s[j]);
+      float f = 1.f;  // what O is multiplied by
+      if constexpr (T8) {
+        const float mn = fmaxf(m, mx), down = m - finite_or_0(mn);
+        if (mn != m) {
+          l *= m == -INFINITY ? 0.f : ex2(down);
+          R += m == -INFINITY ? 0.f : down;  // R is relative to m, the sums O are not
+          m = mn;
         }
-    };
-    load(a.c.k, a.c.ks);
-    float s = 0.f;
+        const float mu = finite_or_0(m);
+        float top = -INFINITY;
 #pragma unroll
-    for (int e = 0; e < E; ++e) s = fmaf(q[e], buf[e], s);
-    s = warp_sum(s) * scale;
-    const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : exp2f(m - mn), p = s == -INFINITY ? 0.f : exp2f(s - mn);
-    load(a.c.v, a.c.vs);
-    l = l * f + p;
+        for (uint32_t j = 0; j < kTile; j += 4) {
+          const float4 e = *reinterpret_cast<const float4*>(&sh.v_exp[n % kInfo][j]);
+          const float ee[4] = {e.x, e.y, e.z, e.w};
 #pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = fmaf(p, buf[e], o[e] * f);
-    m = mn;
+          for (int i = 0; i < 4; ++i) {
+            const float d = s[j + i] - mu;
+            l += ex2(d);
+            s[j + i] = d + ee[i];
+            top = fmaxf(top, s[j + i]);
+          }
+        }
+        const float want = top - kUp8;
+        if (want > R + kSlack8 || R == -INFINITY) {
+          if (want > R) {
+            f = R == -INFINITY ? 0.f : ex2(R - want);
+            R = want;
+          }
+        }
+        const float ref = finite_or_0(R);
+#pragma unroll
+        for (uint32_t j = 0; j < kTile; ++j) s[j] = ex2(s[j] - ref);
+      } else {
+        mx *= scale;
+        if (mx > m + kSlack || m == -INFINITY) {
+          if (mx > m) {
+            f = m == -INFINITY ? 0.f : ex2(m - mx);
+            l *= f;
+            m = mx;
+          }
+        }
+        const float ref = finite_or_0(m);
+#pragma unroll
+        for (uint32_t j = 0; j < kTile; ++j) {
+          s[j] = ex2(fmaf(s[j], scale, -ref));
+          l += s[j];
+        }
+      }
+      if (t != st.t0 && __any_sync(0xffffffffu, f != 1.f)) {
+        const Place<D> before(2 * n - 1);
+        wait(&sh.empty[before.slot], before.turn & 1);
+        tm_after_sync();
+        rescale_o(f);
+      }
+      if (n >= 2) {  // the product that read this P
+        const Place<D> old(2 * n - 3);
+        wait(&sh.empty[old.slot], old.turn & 1);
+        tm_after_sync();
+      }
+#pragma unroll
+      for (uint32_t c = 0; c < 2; ++c) {  // 32 tokens
+        uint32_t h[16];
+        if constexpr (T8) {
+#pragma unroll
+          for (int i = 0; i < 16; ++i) h[i] = pack_f16(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]);
+          tm_st16(p_col(n) + 16 * c, h);
+        } else {
+          uint32_t lo[16];
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const float u = s[32 * c + 2 * i], v = s[32 * c + 2 * i + 1];
+            h[i] = pack_bf16(u, v);
+            lo[i] = pack_bf16(u - bf16lo(h[i]), v - bf16hi(h[i]));
+          }
+          tm_st16(p_col(n) + 16 * c, h);
+          tm_st16(p_col(n) + 32 + 16 * c, lo);
+        }
+      }
+      tm_stored();
+      tm_before_sync();
+    }
+    mbar_arrive(&sh.p_full[n & 1]);
+    if (dirty && busy) {
+      wait(&sh.empty[pv.slot], pv.turn & 1);
+      tm_after_sync();
+      float w[kTile];
+#pragma unroll
+      for (uint32_t j = 0; j < kTile; ++j) w[j] = s[j];
+      mend<D, T8>(a, st.b, st.g, t, valid, live ? vis : 0, w, o_col());
+      tm_before_sync();
+    }
+  }
+
+  // The sums of a stretch, the last of whose tiles is tile n of the CTA.
+  __device__ void store(const Stretch& st, uint32_t n) {
+    const Place<D> pv(2 * n + 1);
+    wait(&sh.empty[pv.slot], pv.turn & 1);
+    tm_after_sync();
+    if (32 * warp >= st.b.rows * group) return;
+    const bool nat = st.c0 == blockIdx.x;
+    const size_t col = nat ? (size_t)(st.b.row + tid / group) * a.H + st.g * group + tid % group : (size_t)blockIdx.x * kM + tid;
+    float* to = (nat ? work.nat : work.cont) + col * D;
+#pragma unroll 1
+    for (uint32_t c = 0; c < D; c += 32) {
+      uint32_t r[32];
+      tm_ld32(o_col() + c, r);
+      tm_loaded(r);
+      if (live) {
+#pragma unroll
+        for (uint32_t i = 0; i < 32; i += 8) {
+          const uint32_t w[8] = {r[i], r[i + 1], r[i + 2], r[i + 3], r[i + 4], r[i + 5], r[i + 6], r[i + 7]};
+          store32(to + c + i, a.wide, w);
+        }
+      }
+    }
+    if (live) (nat ? work.nat_ml : work.cont_ml)[col] = make_float4(m, skip ? -1.f : l, R, 0.f);
+    tm_before_sync();
+  }
+};
+
+// ------------------------------------------------------------------ products
+
+template <int D, bool T8>
+__device__ __forceinline__ void issue(Line line, uint32_t q, uint32_t ring, Notes& sh, uint32_t tmem, Waiter& wait) {
+  constexpr uint32_t kQK = tm_idesc(!T8, false, kM, kTile), kPV = tm_idesc(!T8, true, kM, D);
+  Stretch s;
+  uint32_t n = 0, items = 0;
+  const auto values = [&](uint32_t i, bool add) {  // O += P V of tile i
+    const Place<D> v(2 * i + 1);
+    wait(&sh.full[v.slot], v.turn & 1);
+    wait(&sh.p_full[i & 1], (i >> 1) & 1);
+    tm_after_sync();
+    tm_fence_shared();
+    const uint32_t p = tmem + 128 + (i & 1) * 64, sv = ring + v.slot * Ring<D>::bytes;
+#pragma unroll
+    for (uint32_t k = 0; k < kTile / 16; ++k) {
+      const uint64_t b = tm_desc(sv + k * 2048, Ring<D>::slab, 1024);
+      tm_mma_ta(tmem + 256, p + 8 * k, b, kPV, add || k);
+      if (!T8) tm_mma_ta(tmem + 256, p + 32 + 8 * k, b, kPV, true);
+    }
+    tm_commit(&sh.empty[v.slot]);
+  };
+  while (line.next(s)) {
+    wait(&sh.q_full, items++ & 1);
+    for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
+      const Place<D> k(2 * n);
+      wait(&sh.full[k.slot], k.turn & 1);
+      if (n >= 2) wait(&sh.s_free[n & 1], ((n - 2) >> 1) & 1);
+      tm_after_sync();
+      tm_fence_shared();
+      const uint32_t sk = ring + k.slot * Ring<D>::bytes;
+#pragma unroll
+      for (uint32_t i = 0; i < D / 16; ++i)
+        tm_mma(tmem + (n & 1) * kTile, tm_desc(q + (i / 4) * Ring<D>::q_slab + (i % 4) * 32, 16, 1024),
+               tm_desc(sk + (i / 4) * Ring<D>::slab + (i % 4) * 32, 16, 1024), kQK, i != 0);
+      tm_commit(&sh.s_full[n & 1]);
+      tm_commit(&sh.empty[k.slot]);
+      if (t != s.t0) values(n - 1, t - 1 != s.t0);
+    }
+    values(n - 1, s.t1 - 1 != s.t0);
+  }
+  if (n) {  // every product is complete before the tensor memory goes
+    const Place<D> last(2 * n - 1);
+    wait(&sh.empty[last.slot], last.turn & 1);
+  }
+}
+
+// ------------------------------------------------------------------ the kernel
+
+template <int D, bool T8>
+__global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ RowsAttend a) {
+  extern __shared__ uint8_t raw[];
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  uint8_t* q_sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
+  uint8_t* ring = q_sm + Ring<D>::q;
+  Notes& sh = *reinterpret_cast<Notes*>(ring + Ring<D>::slots * Ring<D>::bytes);
+  uint32_t* first = reinterpret_cast<uint32_t*>(&sh + 1);  // [n_rows + 1]
+  RowNote* note = reinterpret_cast<RowNote*>(first + (a.r.n_rows + 2) / 2 * 2);
+  uint8_t* block_rows = reinterpret_cast<uint8_t*>(note + a.r.n_rows);
+  if (tid == 0) {
+    for (uint32_t i = 0; i < Ring<D>::slots; ++i) {
+      mbar_init(&sh.full[i], kLoadThreads + i % 2);
+      mbar_init(&sh.empty[i], 1);
+    }
+    for (uint32_t i = 0; i < 2; ++i) {
+      mbar_init(&sh.s_full[i], 1);
+      mbar_init(&sh.s_free[i], 128);
+      mbar_init(&sh.p_full[i], 128);
+    }
+    mbar_init(&sh.q_full, 128);
+    mbar_fence_init();
+  }
+  if (warp == 4) tm_alloc(&sh.tmem, 512);
+  pdl_wait();
+  pdl_launch();
+
+  // ---- the rows' places, looked up in shared memory (the ring is empty), and the line of tiles
+  const uint32_t group = a.H / a.c.Hkv, RB = kM / group;
+  Rows here = a.r;
+  {
+    int32_t* pos = reinterpret_cast<int32_t*>(ring);
+    int32_t* start = pos + kMaxSeqs;
+    for (uint32_t i = tid; i < a.r.n_seqs; i += kRowsThreads) pos[i] = a.r.pos[i];
+    if (a.r.row_start)
+      for (uint32_t i = tid; i <= a.r.n_seqs; i += kRowsThreads) start[i] = a.r.row_start[i];
+    here.pos = pos;
+    if (a.r.row_start) here.row_start = start;
+    __syncthreads();
+  }
+  uint32_t base = 0;
+  for (uint32_t r0 = 0; r0 < a.r.n_rows; r0 += kRowsThreads) {
+    const uint32_t r = r0 + tid;
+    uint32_t v = 0;
+    if (r < a.r.n_rows) {
+      uint32_t seq = 0, pos = 0, index = 0, left = 1, rows = 0;
+      RowKind kind = locate(here, a.c.capacity, r, seq, pos, index, left);
+      if (kind == kRowOk && (index > r || (a.parent && index >= kMaxNodes))) kind = kRowBad;
+      if (kind == kRowBad && blockIdx.x == 0) set_status(a.status, kStatusRange);
+      note[r] = {pos, (uint16_t)(kind == kRowOk ? seq : 0xffffu), (uint16_t)min(index, 0xffffu)};
+      if (kind == kRowOk && index % RB == 0) {
+        rows = min(min(min(RB, left), a.r.n_rows - r), a.c.capacity - pos);
+        if (a.parent) rows = min(rows, kMaxNodes - index);
+        v = block_of(a, r, rows, note[r]).tiles() + kLead;
+      }
+      block_rows[r] = (uint8_t)rows;
+    }
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= (uint32_t)o) x += y;
+    }
+    if (lane == 31) sh.sums[warp] = x;
+    __syncthreads();
+    uint32_t before = base;
+#pragma unroll
+    for (uint32_t w = 0; w < kRowsThreads / 32; ++w) {
+      before += w < warp ? sh.sums[w] : 0;
+      base += sh.sums[w];
+    }
+    if (r < a.r.n_rows) first[r] = before + x - v;
+    if (r == a.r.n_rows - 1) first[r + 1] = before + x;
+    __syncthreads();
+  }
+  const uint32_t total = base * a.c.Hkv, per = max((total + gridDim.x - 1) / gridDim.x, kLeast);
+  const Work work = work_of(a.work, a.r.n_rows, a.H, D);
+  // every row's record for the join
+  for (uint32_t i = blockIdx.x * kRowsThreads + tid; i < a.r.n_rows * a.c.Hkv; i += gridDim.x * kRowsThreads) {
+    const uint32_t r = i / a.c.Hkv, g = i % a.c.Hkv, off = note[r].index % RB;
+    uint32_t rec = 0;
+    if (note[r].seq != 0xffffu && off <= r && note[r - off].seq == note[r].seq && off < block_rows[r - off]) {
+      const uint32_t b = r - off, length = first[b + 1] - first[b], w = first[b] * a.c.Hkv + g * length;
+      rec = (w + kLead) / per | ((w + length - 1) / per) << 8 | off << 16 | kRecOk;
+    }
+    work.rec[i] = rec;
+  }
+  tm_before_sync();
+  __syncthreads();
+  tm_after_sync();
+  const uint32_t tmem = sh.tmem;
+  const uint64_t w64 = (uint64_t)blockIdx.x * per;
+  Line line{a, first, note, block_rows, per, (uint32_t)min(w64, (uint64_t)total), (uint32_t)min(w64 + per, (uint64_t)total), 0};
+  if (line.w < line.w1) {
+    uint32_t lo = 0, hi = a.r.n_rows;  // first[lo] Hkv <= w < first[hi] Hkv
+    while (hi - lo > 1) {
+      const uint32_t mid = (lo + hi) / 2;
+      if (first[mid] * a.c.Hkv <= line.w) lo = mid;
+      else hi = mid;
+    }
+    line.row = lo;
+  }
+  Waiter wait{a.wait_ns, a.status, false};
+  if (warp < 4) {
+    Softmax<D, T8> x{a, q_sm, sh, tid, warp, lane, tmem, group, wait, work, 1.4426950408889634f / sqrtf((float)D)};
+    Stretch s;
+    uint32_t n = 0;
+    while (line.next(s)) {
+      x.put_q(s.b, s.g);
+      x.begin(s.b);
+      if (T8) named_barrier(1, 128);  // q's scales
+      for (uint32_t t = s.t0; t < s.t1; ++t, ++n) x.tile(s, t, n);
+      x.store(s, n - 1);
+    }
+  } else if (warp == 4) {
+    if (lane == 0) issue<D, T8>(line, smem_addr(q_sm), smem_addr(ring), sh, tmem, wait);
+    __syncwarp();
+  } else if constexpr (T8) {
+    uint32_t halves = 0;
+    Line count = line;
+    Stretch s;
+    while (count.next(s)) halves += 2 * (s.t1 - s.t0);
+    const uint32_t i = tid - 160;
+    LoadTurbo8<D> x{a, ring, sh, i, i / 32, lane, i / (D / 16), i % (D / 16), wait, line};
+    x.run(halves);
+  } else {
+    load_plain<D>(a, line, ring, sh, tid - 160, wait);
+  }
+  tm_before_sync();
+  __syncthreads();
+  if (warp == 4) {
+    tm_after_sync();
+    tm_free(tmem, 512);
+  }
+}
+
+// ------------------------------------------------------------------ the join
+
+// A column's parts added up: TEAMS teams of D / 8 lanes take its parts in turn, eight dims a lane.
+template <int D, bool T8, int TEAMS>
+__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ RowsAttend a) {
+  constexpr uint32_t LPR = D / 8, COLS = 256 / LPR / TEAMS;
+  __shared__ float sums[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? COLS : 1][TEAMS > 1 ? D : 1];
+  const uint32_t l = threadIdx.x % LPR, slot = threadIdx.x / LPR, sub = slot % TEAMS, at = slot / TEAMS, lane = threadIdx.x & 31;
+  const uint32_t group = a.H / a.c.Hkv, col = blockIdx.x * COLS + at;
+  const uint32_t r = col / a.H, h = col % a.H;
+  const bool in = r < a.r.n_rows;
+  const Work work = work_of(a.work, a.r.n_rows, a.H, D);
+  uint4 z = make_uint4(0u, 0u, 0u, 0u);
+  pdl_wait();
+  pdl_launch();
+  if (in && a.gate) z = load16(a.gate + (size_t)col * a.gate_stride + 8 * l);
+  const uint32_t rec = in ? work.rec[r * a.c.Hkv + h / group] : 0;
+  const uint32_t c0 = rec & 255u, n = rec & kRecOk ? (rec >> 8 & 255u) - c0 + 1 : 0, cont = (rec >> 16 & 255u) * group + h % group;
+  const auto ml = [&](uint32_t k) { return k ? work.cont_ml[(size_t)(c0 + k) * kM + cont] : work.nat_ml[col]; };
+  const auto part = [&](uint32_t k) { return (k ? work.cont + ((size_t)(c0 + k) * kM + cont) * D : work.nat + (size_t)col * D) + 8 * l; };
+  // the largest maximum and (T8) V's relative to it, the sum: a part a lane, in rounds
+  bool ok = n > 0;
+  float M = -INFINITY, V = -INFINITY, L = 0.f;
+  for (uint32_t k = l; k < n; k += LPR) {
+    const float4 x = ml(k);
+    if (x.y < 0.f) ok = false;
+    M = fmaxf(M, x.x);
+  }
+  const uint32_t lanes = LPR == 32 ? 0xffffffffu : ((1u << (LPR % 32)) - 1u) << (lane / LPR * LPR);
+#pragma unroll
+  for (uint32_t w = 1; w < LPR; w <<= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, w));
+  ok = __all_sync(lanes, ok);
+  const float mu = finite_or_0(M);
+  const auto exponent = [&](const float4& x) { return T8 ? x.z + (finite_or_0(x.x) - mu) : x.x - mu; };  // of its sums O
+  for (uint32_t k = l; k < n; k += LPR) {
+    const float4 x = ml(k);
+    if (T8) V = fmaxf(V, exponent(x));
+    L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - mu);
   }
 #pragma unroll
-  for (int e = 0; e < E; ++e) o[e] = l == 0.f ? 0.f : o[e] / l;
-  if (T8) rotate(o);
-  uint16_t* out = a.out + ((size_t)r * a.H + h) * D + lane * E;
-  const uint16_t* gate = a.gate ? a.gate + ((size_t)r * a.H + h) * a.gate_stride + lane * E : nullptr;
+  for (uint32_t w = 1; w < LPR; w <<= 1) {
+    V = fmaxf(V, __shfl_xor_sync(lanes, V, w));
+    L += __shfl_xor_sync(lanes, L, w);
+  }
+  const float down = T8 ? finite_or_0(V) : 0.f;
+  float x[8] = {};
+#pragma unroll 4
+  for (uint32_t k = sub; k < n; k += TEAMS) {
+    const float4 y = ml(k);
+    const float f = y.x == -INFINITY || (T8 && y.z == -INFINITY) ? 0.f : ex2(exponent(y) - down);
+    const float4* from = reinterpret_cast<const float4*>(part(k));
+    const float4 u = from[0], v = from[1];
+    if (f != 0.f) {
+      x[0] = fmaf(u.x, f, x[0]);
+      x[1] = fmaf(u.y, f, x[1]);
+      x[2] = fmaf(u.z, f, x[2]);
+      x[3] = fmaf(u.w, f, x[3]);
+      x[4] = fmaf(v.x, f, x[4]);
+      x[5] = fmaf(v.y, f, x[5]);
+      x[6] = fmaf(v.z, f, x[6]);
+      x[7] = fmaf(v.w, f, x[7]);
+    }
+  }
+  if constexpr (TEAMS > 1) {
 #pragma unroll
-  for (int e = 0; e < E; ++e) out[e] = to_bf16(gate ? o[e] * sigmoidf_(bf16f(gate[e])) : o[e]);
+    for (int e = 0; e < 8; ++e) sums[sub][at][8 * l + e] = x[e];
+    __syncthreads();
+    if (sub) return;
+#pragma unroll 1
+    for (uint32_t k = 1; k < TEAMS; ++k)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] += sums[k][at][8 * l + e];
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L, up = T8 ? ex2(0.5f * down) : 1.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) x[e] = L == 0.f ? 0.f : T8 ? x[e] * inv * up * up : x[e] * inv;
+  if constexpr (T8) {
+    if constexpr (TEAMS > 1 && LPR < 32) {  // the column's own lanes alone are here
+      static_assert(COLS == 1, "one column a CTA");
+    }
+    float y[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) y[e] = x[e];
+#pragma unroll
+    for (int hb = 1; hb < 8; hb <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!(e & hb)) {
+          const float u = y[e], w = y[e + hb];
+          y[e] = u + w;
+          y[e + hb] = u - w;
+        }
+#pragma unroll
+    for (uint32_t w = 1; w < LPR; w <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const float o = __shfl_xor_sync(lanes, y[e], w);
+        y[e] = lane & w ? o - y[e] : y[e] + o;
+      }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = y[e] * rsqrtf((float)D);
+  }
+  if (!ok) return;
+  if (a.gate) {
+    float g[8];
+    unpack8(z, g);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] *= sigmoidf_(g[e]);
+  }
+  *reinterpret_cast<uint4*>(a.out + (size_t)col * D + 8 * l) = pack8(x);
+}
+
+template <int D>
+uint32_t smem_of(uint32_t n_rows) {
+  return 1024 + Ring<D>::q + Ring<D>::slots * Ring<D>::bytes + sizeof(Notes) + (n_rows + 2) / 2 * 8 + n_rows * (sizeof(RowNote) + 1);
+}
+template <int D, bool T8>
+bool allow() {
+  return smem_of<D>(kMaxQueries) <= 227 * 1024 &&
+         cudaFuncSetAttribute(rows_kernel<D, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<D>(kMaxQueries)) == cudaSuccess;
+}
+
+template <int D, bool T8>
+cudaError_t launch(const RowsAttend& a, cudaStream_t st) {
+  static_assert(2 * kMaxSeqs * 4 + 4 <= Ring<64>::slots * Ring<64>::bytes, "the rows' places");
+  cudaError_t e = launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D>(a.r.n_rows), st, a);
+  if (e != cudaSuccess) return e;
+  // few columns: each a CTA, whose teams share its parts; many: a team a column
+  constexpr uint32_t all = 256 / (D / 8);
+  const uint32_t cols = a.r.n_rows * a.H;
+  if (cols <= 2048) return launch_early(join_kernel<D, T8, all>, dim3(cols), 256, 0, st, a);
+  return launch_early(join_kernel<D, T8, 1>, dim3((cols + all - 1) / all), 256, 0, st, a);
 }
 
 }  // namespace
 
 size_t rows_work_bytes(uint32_t n_rows, uint32_t H, uint32_t Hkv, uint32_t D) {
-  return ((size_t)n_rows * H + kMaxCtas * 128) * (D + 8) * 4 + (size_t)n_rows * Hkv * 16;
+  return ((size_t)n_rows * H + kMaxCtas * kM) * (D * 4 + 16) + (size_t)n_rows * Hkv * 4;
 }
-cudaError_t rows_attend_attributes() { return cudaSuccess; }
+cudaError_t rows_attend_attributes() {
+  return allow<64, false>() && allow<64, true>() && allow<128, false>() && allow<128, true>() && allow<256, false>() &&
+                 allow<256, true>()
+             ? cudaSuccess
+             : cudaErrorInvalidValue;
+}
 
 cudaError_t rows_attend(const RowsAttend& a, cudaStream_t st) {
-  const dim3 grid((a.r.n_rows * a.H + 3) / 4);
   const bool t8 = a.c.ks != nullptr;
-#define CALL(DD)                                                        \
-  return t8 ? launch_early(rows_kernel<DD, true>, grid, 128, 0, st, a)  \
-            : launch_early(rows_kernel<DD, false>, grid, 128, 0, st, a)
+#define CALL(DD) return t8 ? launch<DD, true>(a, st) : launch<DD, false>(a, st)
   switch (a.c.D) {
     case 64: CALL(64);
     case 128: CALL(128);

@@ -49,6 +49,7 @@ struct RowsAttend {
   const uint16_t* gate;  // as Attend's
   uint16_t* out;         // [n_rows][H][D]
   uint8_t* work;         // rows_work_bytes
+  bool wide;             // it is 32-byte aligned
   uint32_t sms;          // of the GPU
   uint32_t H, gate_stride;
   uint64_t wait_ns;
