@@ -9,10 +9,10 @@
 // q-heads leaves most of M empty; what bounds the call is the bytes of K and V all the same: a tile of D = 256
 // is 64 KB, 1.5 us of an SM's share of the memory, its products 1 us.
 //
-// Roles of a CTA's 13 warps: 0-3 own a lane of S, P and O each thread (the softmax: no exchange between threads); one
-// thread of warp 4 issues the products; 5-12 fill a ring of K and V tiles, 16-byte pieces by asynchronous
-// copies (pages as small as 8 tokens, rows outside as zeros), Turbo8 through registers as f16. The softmax of a tile
-// runs under the product of the tile before and the scores of the next (two S, two P).
+// Roles of a CTA's 17 warps: 0-7 are the softmax, two threads a row with 32 of a tile's 64 tokens each, which
+// exchange their maxima; one thread of warp 8 issues the products; 9-16 fill a ring of K and V tiles, 16-byte pieces by
+// asynchronous copies (pages as small as 8 tokens, rows outside as zeros), Turbo8 through registers as f16. The softmax of a
+// tile runs under the product of the tile before and the scores of the next (two S, two P).
 //
 // The line of all items' tiles is cut into equal stretches, one CTA an SM. A stretch leaves its sums and maxima
 // in the scratch, and a second launch adds an item's parts up in the order of the CTAs, so equal calls give equal
@@ -39,12 +39,13 @@ using namespace q35;
 namespace {
 
 constexpr uint32_t kM = 128, kTile = 64, kOctets = kTile / 8;
-constexpr uint32_t kLoaders = 8, kLoadThreads = 32 * kLoaders, kRowsThreads = 128 + 32 + kLoadThreads;
+constexpr uint32_t kSoft = 256;  // threads of the softmax
+constexpr uint32_t kLoaders = 8, kLoadThreads = 32 * kLoaders, kRowsThreads = kSoft + 32 + kLoadThreads;
+constexpr uint32_t kHalf = kTile / 2;  // tokens of a thread
 constexpr uint32_t kLead = 2;   // what an item's beginning and end cost a CTA, in tiles
 constexpr uint32_t kLeast = 2;  // tiles of a stretch at least
 constexpr float kSlack = 8.f;   // how far a score may lie above what P and l refer to before they are moved
 constexpr float kSlack8 = 4.f, kUp8 = 11.f;  // Turbo8's weights of V: at most 2^(kUp8 + kSlack8) in f16
-constexpr uint32_t kInfo = 8;   // tiles whose notes are kept (a ring of 4 tiles and two of the softmax's)
 
 template <int D>
 struct Ring {
@@ -52,11 +53,13 @@ struct Ring {
   static constexpr uint32_t slots = D == 256 ? 4 : 8;             // even ones K, odd ones V
   static constexpr uint32_t slab = kTile * 128, q_slab = kM * 128;  // 64 dims of all rows
   static constexpr uint32_t q = kM * D * 2;
-  static_assert(slots / 2 + 2 <= kInfo, "notes");
+  static constexpr uint32_t info = D == 256 ? 4 : 8;               // tiles whose notes are kept: the ring's and two of the softmax's
+  static_assert(slots / 2 + 2 <= info, "notes");
 };
 
 // Shared memory behind Q and the ring.
-struct Notes {
+template <uint32_t kInfo>
+struct NotesOf {
   uint64_t full[8], empty[8], s_full[2], s_free[2], p_full[2], q_full;
   uint32_t tmem;
   uint32_t sums[kRowsThreads / 32];
@@ -64,8 +67,13 @@ struct Notes {
   uint8_t dirty[kInfo][kLoaders];    // V held something that is no number (a loader warp each)
   float k_scale[kInfo][kTile], v_exp[kInfo][kTile];  // Turbo8: 2^E of K's tokens, E of V's
   float q_scale[kM];
+  float2 top[2][2][kM];  // a row's two threads' maxima
+  float sum[kM];         // the second thread's sum
   int32_t parent[kMaxNodes];
 };
+
+template <int D>
+using Notes = NotesOf<Ring<D>::info>;
 
 // A row of the call as every CTA keeps it.
 struct RowNote {
@@ -74,11 +82,13 @@ struct RowNote {
 };
 
 struct Work {  // the scratch
-  float* nat;      // [n_rows][H][D]: an item's first stretch
-  float* cont;     // [CTAs][128][D]: the stretch of an item that a CTA goes on with
+  // Sums of an item's first stretch and of the one that a CTA goes on with: [D / 8][columns][8], so that a
+  // thread's 32 bytes lie beside its neighbours'. Items lie one behind another: block's rows x H columns.
+  float* nat;
+  float* cont;     // [CTAs][D / 8][128][8]
   float4* nat_ml;  // m, l, R of a column; l < 0: a row that is skipped
   float4* cont_ml;
-  uint32_t* rec;   // [n_rows][Hkv]: the CTAs of the row's item, its place in the block
+  uint32_t* rec;   // [n_rows][Hkv]: the CTAs of the row's item, the block's rows, the row's place in it
 };
 __host__ __device__ inline Work work_of(uint8_t* p, uint32_t n_rows, uint32_t H, uint32_t D) {
   Work w;
@@ -89,7 +99,7 @@ __host__ __device__ inline Work work_of(uint8_t* p, uint32_t n_rows, uint32_t H,
   w.rec = reinterpret_cast<uint32_t*>(w.cont_ml + kMaxCtas * kM);
   return w;
 }
-constexpr uint32_t kRecOk = 1u << 24;
+constexpr uint32_t kRecOk = 1u << 30;
 
 __device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool in) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(in ? 16 : 0) : "memory");
@@ -239,11 +249,13 @@ __device__ __forceinline__ bool not_a_number_bf16(uint32_t w) {  // in either ha
 }
 
 template <int D>
-__device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line0, uint8_t* ring, Notes& sh, uint32_t tid,
+__device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line0, uint8_t* ring, Notes<D>& sh, uint32_t tid,
                                            Waiter& wait) {
   constexpr uint32_t C = D / 8, STEP = kLoadThreads / C, J = kTile / STEP;  // pieces of a row, rows of a pass, passes
-  const uint32_t warp = tid / 32, lane = tid % 32, r0 = tid / C, c = tid % C;
-  const uint32_t to = (c / 8) * Ring<D>::slab, stride = a.c.Hkv * D;
+  const uint32_t warp = tid / 32, lane = tid % 32, r0 = tid / C, c = tid % C, q0 = warp * 32 / C / 8;
+  const uint32_t to = (c / 8) * Ring<D>::slab + sw(r0, c % 8);  // STEP is a multiple of 8: piece j lies STEP * 128 behind
+  static_assert(STEP % 8 == 0, "the swizzle of a thread's rows");
+  const uint32_t stride = a.c.Hkv * D;
   Line line = line0;
   Stretch s;
   uint32_t n = 0;
@@ -257,32 +269,37 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line
       }
       const bool full = __all_sync(0xffffffffu, octet_full(a, s.b, t * kOctets + lane % 8));
       const uint32_t valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
+      uint32_t rows = 0xffu;  // lane % 8's octet: rows of it that are loaded
+      if (!full) {
+        uint32_t lo, hi;
+        octet_rows(a, s.b, t * kOctets + lane % 8, lo, hi);
+        rows = bits_below(hi) & ~bits_below(lo);
+      }
+      if (!(valid >> (lane % 8) & 1)) rows = 0;
+      size_t off[J];
+      uint32_t in = 0;
+#pragma unroll
+      for (uint32_t j = 0; j < J; ++j) {
+        const uint32_t q = q0 + j * STEP / 8;  // a warp's rows lie in one octet
+        const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)now.row, 8 * i + q) + r0 % 8;
+        in |= (__shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u) << j;
+        off[j] = row * stride + s.g * D + 8 * c;
+      }
 #pragma unroll 1
       for (uint32_t p = 0; p < 2; ++p) {
         const Place<D> at(2 * n + p);
         if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
         uint8_t* slot = ring + at.slot * Ring<D>::bytes;
         const uint16_t* base = reinterpret_cast<const uint16_t*>(p ? a.c.v : a.c.k);
-        const uint16_t* src[J];
-        bool in[J];
-#pragma unroll
-        for (uint32_t j = 0; j < J; ++j) {
-          const uint32_t r = r0 + j * STEP, q = (warp * 32 / C + j * STEP) / 8;  // a warp's rows lie in one octet
-          const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)now.row, 8 * i + q);
-          uint32_t lo, hi;
-          octet_rows(a, s.b, t * kOctets + q, lo, hi);
-          in[j] = (valid >> q & 1) && r % 8 >= lo && r % 8 < hi;
-          src[j] = in[j] ? base + (row + r % 8) * stride + s.g * D + 8 * c : base;
-        }
         if (!p || full) {
           const uint32_t dst = smem_addr(slot) + to;
 #pragma unroll
-          for (uint32_t j = 0; j < J; ++j) cp16(dst + sw(r0 + j * STEP, c % 8), src[j], in[j]);
+          for (uint32_t j = 0; j < J; ++j) cp16(dst + j * STEP * 128, in >> j & 1 ? base + off[j] : base, in >> j & 1);
           cp_arrive(&sh.full[at.slot]);
         } else {
           uint4 x[J];
 #pragma unroll
-          for (uint32_t j = 0; j < J; ++j) x[j] = in[j] ? load16(src[j]) : make_uint4(0u, 0u, 0u, 0u);
+          for (uint32_t j = 0; j < J; ++j) x[j] = in >> j & 1 ? load16(base + off[j]) : make_uint4(0u, 0u, 0u, 0u);
           bool bad = false;
 #pragma unroll
           for (uint32_t j = 0; j < J; ++j) {
@@ -294,15 +311,15 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line
                 if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
                 if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
               }
-            *reinterpret_cast<uint4*>(slot + to + sw(r0 + j * STEP, c % 8)) = x[j];
+            *reinterpret_cast<uint4*>(slot + to + j * STEP * 128) = x[j];
           }
           bad = __any_sync(0xffffffffu, bad);
-          if (lane == 0) sh.dirty[n % kInfo][warp] = bad;
+          if (lane == 0) sh.dirty[n % Ring<D>::info][warp] = bad;
           tm_fence_shared();
           mbar_arrive(&sh.full[at.slot]);
         }
-        if (p && tid == 0) {  // an arrival that the notes are released by
-          sh.valid[n % kInfo] = valid;
+        if (!p && tid == 0) {  // an arrival that the notes are released by
+          sh.valid[n % Ring<D>::info] = valid;
           mbar_arrive(&sh.full[at.slot]);
         }
       }
@@ -311,40 +328,36 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Turbo8: sixteen codes and their scale a piece, kHeld half-tiles of them in registers on their way.
-constexpr uint32_t kHeld = 4;
-template <int J>
-struct Codes {
-  uint4 c[J];
-  uint16_t s[J];
-};
+// Turbo8: sixteen codes and their scale a piece, in registers on their way: K of the next tile is fetched as soon as
+// this one's is put, and so is V.
 template <int D>
 struct LoadTurbo8 {
   static constexpr uint32_t C = D / 16, STEP = kLoadThreads / C, J = kTile / STEP;
+  struct Codes {
+    uint4 c[J];
+    uint16_t s[J];
+  };
   const RowsAttend& a;
   uint8_t* ring;
-  Notes& sh;
+  Notes<D>& sh;
   uint32_t tid, warp, lane, r0, c;
   Waiter& wait;
-  // what is fetched: its own walk along the line, kHeld half-tiles ahead
+  // the tile that is fetched, ahead of the one that is put
   Line line;
   Stretch s;
   Found now, then;
-  uint32_t t, p;
+  uint32_t t, valid;
   bool more;
 
   __device__ __forceinline__ void begin() {
     more = line.next(s);
-    p = 0;
     if (more) {
       t = s.t0;
       now = find(a, s.b, t, lane);
       then = find(a, s.b, t + 4, lane);
     }
   }
-  // The next half-tile; `valid`: its tile's octets.
-  __device__ __forceinline__ void fetch(Codes<J>& x, uint32_t& valid) {
-    valid = 0;
+  __device__ __forceinline__ void fetch(Codes& x, uint32_t p) {
     if (!more) return;
     const uint32_t i = (t - s.t0) % 4;
     valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
@@ -364,37 +377,46 @@ struct LoadTurbo8 {
         x.s[j] = sc[row * a.c.sstride + s.g * C + c];
       }
     }
-    if (++p == 2) {
-      p = 0;
-      if (++t == s.t1) {
-        begin();
-      } else if ((t - s.t0) % 4 == 0) {
-        now = then;
-        then = find(a, s.b, t + 4, lane);
-      }
+  }
+  __device__ __forceinline__ void advance() {
+    if (!more) return;
+    if (++t == s.t1) {
+      begin();
+    } else if ((t - s.t0) % 4 == 0) {
+      now = then;
+      then = find(a, s.b, t + 4, lane);
     }
   }
-  // Half-tile h into the ring, as f16 over 2^E.
-  __device__ __forceinline__ void put(const Codes<J>& x, uint32_t h, uint32_t valid) {
-    const Place<D> at(h);
-    const uint32_t n = h / 2, v = h % 2;
+  static __device__ __forceinline__ bool number(uint16_t scale) { return (scale & 0x7f80u) != 0x7f80u; }
+  // The exponent of a token's largest scale, from the lanes that have it.
+  static __device__ __forceinline__ int exponent(uint16_t scale) {
+    float mx = number(scale) ? fabsf(bf16f(scale)) : 0.f;
+#pragma unroll
+    for (uint32_t m = 1; m < C; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
+    return min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
+  }
+  // A half-tile of tile n into the ring, as f16 over 2^E. K's arrival releases the notes: K's scales, V's exponents and what octets are there.
+  template <uint32_t V>
+  __device__ __forceinline__ void put(const Codes& x, const Codes& v, uint32_t n, uint32_t valid) {
+    const Place<D> at(2 * n + V);
     if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
     uint8_t* slot = ring + at.slot * Ring<D>::bytes + (c / 4) * Ring<D>::slab;
     bool bad = false;
 #pragma unroll
     for (uint32_t j = 0; j < J; ++j) {
       const uint32_t r = r0 + j * STEP;
-      const float scale = bf16f(x.s[j]);
-      const bool number = (x.s[j] & 0x7f80u) != 0x7f80u;
-      float mx = number ? fabsf(scale) : 0.f;
-#pragma unroll
-      for (uint32_t m = 1; m < C; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-      const int e = min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
-      if (c == 0) (v ? sh.v_exp : sh.k_scale)[n % kInfo][r] = v ? (float)e : pow2(e);
-      float f = scale * pow2(-e);
+      const int e = exponent(x.s[j]);
+      if (!V) {
+        const int ev = exponent(v.s[j]);
+        if (c == 0) {
+          sh.k_scale[n % Ring<D>::info][r] = pow2(e);
+          sh.v_exp[n % Ring<D>::info][r] = (float)ev;
+        }
+      }
+      float f = bf16f(x.s[j]) * pow2(-e);
       uint32_t w[4] = {x.c[j].x, x.c[j].y, x.c[j].z, x.c[j].w};
-      if (v) {
-        if (!number) {
+      if (V) {
+        if (!number(x.s[j])) {
           bad = true;
           f = 0.f;
         }
@@ -413,45 +435,48 @@ struct LoadTurbo8 {
       *reinterpret_cast<uint4*>(slot + sw(r, j8)) = make_uint4(y[0], y[1], y[2], y[3]);
       *reinterpret_cast<uint4*>(slot + sw(r, j8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
     }
-    if (v) {
+    if (V) {
       bad = __any_sync(0xffffffffu, bad);
-      if (lane == 0) sh.dirty[n % kInfo][warp] = bad;
+      if (lane == 0) sh.dirty[n % Ring<D>::info][warp] = bad;
     }
     tm_fence_shared();
     mbar_arrive(&sh.full[at.slot]);
-    if (v && tid == 0) {
-      sh.valid[n % kInfo] = valid;
+    if (!V && tid == 0) {
+      sh.valid[n % Ring<D>::info] = valid;
       mbar_arrive(&sh.full[at.slot]);
     }
   }
-  __device__ __forceinline__ void run(uint32_t halves) {
-    Codes<J> x[kHeld];
-    uint32_t valid[kHeld];
+  __device__ __forceinline__ void run(uint32_t tiles) {
+    Codes k, v;
     begin();
-#pragma unroll
-    for (uint32_t k = 0; k < kHeld; ++k) fetch(x[k], valid[k]);
-    for (uint32_t h = 0; h < halves; h += kHeld) {
-#pragma unroll
-      for (uint32_t k = 0; k < kHeld; ++k)
-        if (h + k < halves) {
-          put(x[k], h + k, valid[k]);
-          fetch(x[k], valid[k]);
-        }
+    fetch(k, 0);
+    fetch(v, 1);
+    uint32_t here = valid;
+    advance();
+#pragma unroll 1
+    for (uint32_t n = 0; n < tiles; ++n) {
+      put<0>(k, v, n, here);
+      fetch(k, 0);
+      put<1>(v, v, n, here);
+      fetch(v, 1);
+      here = valid;
+      advance();
     }
   }
 };
 
 // ------------------------------------------------------------------ softmax
 
-// V's elements of a tile that are no numbers, which the loaders took out: weight w[j] times each for the rows that see
-// it. Runs after the tile's product; rare, so plain and slow.
+// V's elements of a half of a tile (tokens j0 ..) that are no numbers, which the loaders took out: weight w[j] times each
+// for the rows that see it (bit j of vis). Runs after the tile's product; rare, so plain and slow.
 template <int D, bool T8>
-__device__ __noinline__ void mend(const RowsAttend& a, const Block& b, uint32_t g, uint32_t t, uint32_t valid, uint64_t vis,
-                                  const float* w, uint32_t o_col) {
+__device__ __noinline__ void mend(const RowsAttend& a, const Block& b, uint32_t g, uint32_t t, uint32_t j0, uint32_t valid,
+                                  uint32_t vis, const float* w, uint32_t o_col) {
 #pragma unroll 1
-  for (uint32_t j = 0; j < kTile; ++j) {
-    if (!(valid >> (j / 8) & 1)) continue;
-    const uint32_t tok = b.token(t * kOctets + j / 8) + j % 8;
+  for (uint32_t j = 0; j < kHalf; ++j) {
+    const uint32_t q = (j0 + j) / 8;
+    if (!(valid >> q & 1)) continue;
+    const uint32_t tok = b.token(t * kOctets + q) + j % 8;
     const bool see = vis >> j & 1;
     size_t row;
     if (!__any_sync(0xffffffffu, see) || tok > b.last || !cache_row(a.c, b.seq, tok, row)) continue;
@@ -469,35 +494,38 @@ __device__ __noinline__ void mend(const RowsAttend& a, const Block& b, uint32_t 
   }
 }
 
+// Thread tid of 256: row (TMEM lane) tid % 128, half tid / 128 of each tile's tokens and of O's columns.
 template <int D, bool T8>
 struct Softmax {
   const RowsAttend& a;
   uint8_t* q_sm;
-  Notes& sh;
-  uint32_t tid, warp, lane, tmem, group;
+  Notes<D>& sh;
+  uint32_t tid, lane, tmem, group;  // tmem: the warp's lanes of it
   Waiter& wait;
   Work work;
   float scale;
-  // the thread's column
-  uint32_t p;       // its row's position
-  bool live, skip;  // has a row; the row is skipped
-  uint64_t line0, line1;  // tree: the nodes that the row sees
+  uint32_t row, half, pair;  // pair: the barrier of the warp and its other half
+  // the thread's row
+  uint32_t p;             // its position
+  bool live, skip;        // it is one of the block's; it is skipped
+  uint64_t line0, line1;  // tree: the nodes that it sees
   float m, l, R;
 
-  __device__ __forceinline__ uint32_t s_col(uint32_t n) const { return tmem + ((32 * warp) << 16) + (n & 1) * kTile; }
-  __device__ __forceinline__ uint32_t p_col(uint32_t n) const { return tmem + ((32 * warp) << 16) + 128 + (n & 1) * 64; }
-  __device__ __forceinline__ uint32_t o_col() const { return tmem + ((32 * warp) << 16) + 256; }
+  __device__ __forceinline__ uint32_t s_col(uint32_t n) const { return tmem + (n & 1) * kTile + half * kHalf; }
+  __device__ __forceinline__ uint32_t p_col(uint32_t n) const { return tmem + 128 + (n & 1) * 64 + half * (kHalf / 2); }
+  __device__ __forceinline__ uint32_t o_col() const { return tmem + 256; }
 
-  __device__ void put_q(const Block& b, uint32_t g) {
-    constexpr uint32_t LPR = D / 8;
-    const uint32_t cols = b.rows * group;
-    const auto from = [&](uint32_t col) { return a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D; };
+  __device__ __forceinline__ void put_q(const Block& b, uint32_t g) {
+    constexpr uint32_t LPR = D / 8, PER = kSoft / LPR;
+    const uint32_t cols = b.rows * group, j = tid % LPR;
+    const auto from = [&](uint32_t col) { return a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D + 8 * j; };
+    uint8_t* to = q_sm + (j / 8) * Ring<D>::q_slab;
+    if constexpr (T8) {
 #pragma unroll 4
-    for (uint32_t c0 = 0; c0 < cols; c0 += 128 / LPR) {
-      const uint32_t col = c0 + tid / LPR, j = tid % LPR;
-      uint4 u = make_uint4(0u, 0u, 0u, 0u);
-      if (col < cols) u = load16(from(col) + 8 * j);
-      if constexpr (T8) {
+      for (uint32_t c0 = 0; c0 < cols; c0 += PER) {
+        const uint32_t col = c0 + tid / LPR;
+        uint4 u = make_uint4(0u, 0u, 0u, 0u);
+        if (col < cols) u = load16(from(col));
         float x[8], mx = 0.f;
         unpack8(u, x);
         wht8<LPR>(x, lane);
@@ -510,23 +538,26 @@ struct Softmax {
         if (j == 0 && col < cols) sh.q_scale[col] = pow2(e2);
         u = make_uint4(pack_f16(x[0] * f, x[1] * f), pack_f16(x[2] * f, x[3] * f), pack_f16(x[4] * f, x[5] * f),
                        pack_f16(x[6] * f, x[7] * f));
+        if (col < cols) *reinterpret_cast<uint4*>(to + sw(col, j % 8)) = u;
       }
-      if (col < cols) *reinterpret_cast<uint4*>(q_sm + (j / 8) * Ring<D>::q_slab + sw(col, j % 8)) = u;
+    } else {
+      for (uint32_t col = tid / LPR; col < cols; col += PER) cp16(smem_addr(to + sw(col, j % 8)), from(col), true);
+      asm volatile("cp.async.wait_all;" ::: "memory");
     }
     tm_fence_shared();
     mbar_arrive(&sh.q_full);
   }
 
-  __device__ void begin(const Block& b) {
-    const uint32_t r = tid / group;
-    live = tid < b.rows * group;
+  __device__ __forceinline__ void begin(const Block& b) {
+    const uint32_t r = row / group;
+    live = row < b.rows * group;
     p = b.pos + r;
     skip = false;
     line0 = line1 = 0;
     if (a.parent) {
       const uint32_t nodes = b.index + b.rows;  // at most kMaxNodes
       if (tid < nodes) sh.parent[tid] = a.parent[b.row - b.index + tid];
-      named_barrier(1, 128);
+      named_barrier(1, kSoft);
       if (live) {
         for (int32_t i = (int32_t)(b.index + r);;) {
           if (i < 64) line0 |= 1ull << i;
@@ -541,17 +572,18 @@ struct Softmax {
           i = up;
         }
       }
-      named_barrier(1, 128);  // the next block's parents come here
     }
+    if (T8 || a.parent) named_barrier(1, kSoft);  // q's scales are there; the next block's parents may come
     m = R = -INFINITY;
     l = 0.f;
   }
 
-  // Tokens of tile t that the thread's row sees, of those that are there.
-  __device__ __forceinline__ uint64_t seen(const Block& b, uint32_t t, uint32_t valid) const {
-    uint64_t bits = 0;
+  // Tokens of the thread's half of tile t that its row sees, of those that are there.
+  __device__ __forceinline__ uint32_t seen(const Block& b, uint32_t t, uint32_t valid) const {
+    uint32_t bits = 0;
 #pragma unroll 1
-    for (uint32_t q = 0; q < kOctets; ++q) {
+    for (uint32_t i = 0; i < kHalf / 8; ++i) {
+      const uint32_t q = half * (kHalf / 8) + i;
       if (!(valid >> q & 1)) continue;
       const int64_t t0 = b.token(t * kOctets + q);
       uint32_t x;
@@ -565,14 +597,14 @@ struct Softmax {
       } else {
         x = bits_below((int64_t)p + 1 - t0) & (~bits_below((int64_t)p + 1 - (int64_t)a.window - t0) | bits_below((int64_t)a.n_first - t0));
       }
-      bits |= (uint64_t)(x & 0xffu) << (8 * q);
+      bits |= (x & 0xffu) << (8 * i);
     }
     return bits;
   }
 
   __device__ __forceinline__ void rescale_o(float f) {
 #pragma unroll 1
-    for (uint32_t c = 0; c < D; c += 32) {
+    for (uint32_t c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
       uint32_t r[32];
       tm_ld32(o_col() + c, r);
       tm_loaded(r);
@@ -584,108 +616,101 @@ struct Softmax {
   }
 
   __device__ __forceinline__ void tile(const Stretch& st, uint32_t t, uint32_t n) {
+    const bool busy = row - lane % 32 < st.b.rows * group;
+    const bool all = __all_sync(0xffffffffu, octet_full(a, st.b, t * kOctets + lane % 8));
     const Place<D> pv(2 * n + 1);
-    wait(&sh.full[pv.slot], pv.turn & 1);  // the tile's notes
-    const uint32_t valid = sh.valid[n % kInfo];
-    const bool full = __all_sync(0xffffffffu, octet_full(a, st.b, t * kOctets + lane % 8)) && valid == 0xffu;
-    uint32_t dirty = 0;
-    if (T8 || !full) {
-      const uint2 u = *reinterpret_cast<const uint2*>(sh.dirty[n % kInfo]);
-      dirty = u.x | u.y;
-    }
-    // bf16: only tiles that are not wholly seen have been looked through
-    if (!T8 && __all_sync(0xffffffffu, octet_full(a, st.b, t * kOctets + lane % 8))) dirty = 0;
     wait(&sh.s_full[n & 1], (n >> 1) & 1);
     tm_after_sync();
-    const bool busy = 32 * warp < st.b.rows * group;
-    float s[kTile];
-    uint64_t vis = 0;
+    const uint32_t valid = sh.valid[n % Ring<D>::info];
+    float s[kHalf];
+    uint32_t vis = ~0u;
     if (busy) {
-      {
-        uint32_t r[32], r2[32];
-        tm_ld32(s_col(n), r);
-        tm_ld32(s_col(n) + 32, r2);
-        tm_loaded(r);
-        tm_loaded(r2);
+      uint32_t r[32];
+      tm_ld32(s_col(n), r);
+      tm_loaded(r);
 #pragma unroll
-        for (int i = 0; i < 32; ++i) {
-          s[i] = __uint_as_float(r[i]);
-          s[32 + i] = __uint_as_float(r2[i]);
-        }
-      }
+      for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
       tm_before_sync();
     }
     mbar_arrive(&sh.s_free[n & 1]);
     if (busy) {
-      float mx = -INFINITY;
       if constexpr (T8) {
-        const float sc = scale * (live ? sh.q_scale[tid] : 0.f);
+        const float sc = scale * (live ? sh.q_scale[row] : 0.f);
 #pragma unroll
-        for (uint32_t j = 0; j < kTile; j += 4) {
-          const float4 k = *reinterpret_cast<const float4*>(&sh.k_scale[n % kInfo][j]);
+        for (uint32_t j = 0; j < kHalf; j += 4) {
+          const float4 k = *reinterpret_cast<const float4*>(&sh.k_scale[n % Ring<D>::info][half * kHalf + j]);
           s[j] = s[j] * sc * k.x;
           s[j + 1] = s[j + 1] * sc * k.y;
           s[j + 2] = s[j + 2] * sc * k.z;
           s[j + 3] = s[j + 3] * sc * k.w;
         }
       }
-      if (!full) {
+      if (!all || valid != 0xffu) {
         vis = live && !skip ? seen(st.b, t, valid) : 0;
 #pragma unroll
-        for (uint32_t j = 0; j < kTile; ++j) s[j] = vis >> j & 1 ? s[j] : -INFINITY;
-      } else {
-        vis = ~0ull;
+        for (uint32_t j = 0; j < kHalf; ++j) s[j] = vis >> j & 1 ? s[j] : -INFINITY;
       }
+      // the largest score, and (T8) with V's exponent, of both threads of the row
+      float2 top = make_float2(-INFINITY, -INFINITY);
+      {
+        float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY}, y[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-      for (uint32_t j = 0; j < kTile; ++j) mx = fmaxf(mx, s[j]);
-      float f = 1.f;  // what O is multiplied by
+        for (uint32_t j = 0; j < kHalf; j += 4) {
+          float4 e;
+          if (T8) e = *reinterpret_cast<const float4*>(&sh.v_exp[n % Ring<D>::info][half * kHalf + j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            x[i] = fmaxf(x[i], s[j + i]);
+            if (T8) y[i] = fmaxf(y[i], s[j + i] + (i == 0 ? e.x : i == 1 ? e.y : i == 2 ? e.z : e.w));
+          }
+        }
+        top.x = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3]));
+        if (T8) top.y = fmaxf(fmaxf(y[0], y[1]), fmaxf(y[2], y[3]));
+      }
+      sh.top[n & 1][half][row] = top;
+      named_barrier(pair, 64);
+      const float2 other = sh.top[n & 1][half ^ 1][row];
+      top.x = fmaxf(top.x, other.x);
+      top.y = fmaxf(top.y, other.y);
+      float f = 1.f, sums[4] = {0.f, 0.f, 0.f, 0.f};  // f: what O is multiplied by
       if constexpr (T8) {
-        const float mn = fmaxf(m, mx), down = m - finite_or_0(mn);
+        const float mn = fmaxf(m, top.x), down = m - finite_or_0(mn);
         if (mn != m) {
           l *= m == -INFINITY ? 0.f : ex2(down);
           R += m == -INFINITY ? 0.f : down;  // R is relative to m, the sums O are not
           m = mn;
         }
-        const float mu = finite_or_0(m);
-        float top = -INFINITY;
-#pragma unroll
-        for (uint32_t j = 0; j < kTile; j += 4) {
-          const float4 e = *reinterpret_cast<const float4*>(&sh.v_exp[n % kInfo][j]);
-          const float ee[4] = {e.x, e.y, e.z, e.w};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float d = s[j + i] - mu;
-            l += ex2(d);
-            s[j + i] = d + ee[i];
-            top = fmaxf(top, s[j + i]);
-          }
-        }
-        const float want = top - kUp8;
-        if (want > R + kSlack8 || R == -INFINITY) {
-          if (want > R) {
-            f = R == -INFINITY ? 0.f : ex2(R - want);
-            R = want;
-          }
+        const float mu = finite_or_0(m), want = top.y - mu - kUp8;
+        if (want > R && (want > R + kSlack8 || R == -INFINITY)) {
+          f = R == -INFINITY ? 0.f : ex2(R - want);
+          R = want;
         }
         const float ref = finite_or_0(R);
 #pragma unroll
-        for (uint32_t j = 0; j < kTile; ++j) s[j] = ex2(s[j] - ref);
-      } else {
-        mx *= scale;
-        if (mx > m + kSlack || m == -INFINITY) {
-          if (mx > m) {
-            f = m == -INFINITY ? 0.f : ex2(m - mx);
-            l *= f;
-            m = mx;
+        for (uint32_t j = 0; j < kHalf; j += 4) {
+          const float4 e = *reinterpret_cast<const float4*>(&sh.v_exp[n % Ring<D>::info][half * kHalf + j]);
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float d = s[j + i] - mu;
+            sums[i] += ex2(d);
+            s[j + i] = ex2(d + (i == 0 ? e.x : i == 1 ? e.y : i == 2 ? e.z : e.w) - ref);
           }
+        }
+      } else {
+        const float mx = top.x * scale;
+        if (mx > m && (mx > m + kSlack || m == -INFINITY)) {
+          f = m == -INFINITY ? 0.f : ex2(m - mx);
+          l *= f;
+          m = mx;
         }
         const float ref = finite_or_0(m);
 #pragma unroll
-        for (uint32_t j = 0; j < kTile; ++j) {
+        for (uint32_t j = 0; j < kHalf; ++j) {
           s[j] = ex2(fmaf(s[j], scale, -ref));
-          l += s[j];
+          sums[j % 4] += s[j];
         }
       }
+      l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
       if (t != st.t0 && __any_sync(0xffffffffu, f != 1.f)) {
         const Place<D> before(2 * n - 1);
         wait(&sh.empty[before.slot], before.turn & 1);
@@ -697,51 +722,63 @@ struct Softmax {
         wait(&sh.empty[old.slot], old.turn & 1);
         tm_after_sync();
       }
+      uint32_t h[16];
+      if constexpr (T8) {
 #pragma unroll
-      for (uint32_t c = 0; c < 2; ++c) {  // 32 tokens
-        uint32_t h[16];
-        if constexpr (T8) {
+        for (int i = 0; i < 16; ++i) h[i] = pack_f16(s[2 * i], s[2 * i + 1]);
+        tm_st16(p_col(n), h);
+      } else {
+        uint32_t lo[16];
 #pragma unroll
-          for (int i = 0; i < 16; ++i) h[i] = pack_f16(s[32 * c + 2 * i], s[32 * c + 2 * i + 1]);
-          tm_st16(p_col(n) + 16 * c, h);
-        } else {
-          uint32_t lo[16];
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const float u = s[32 * c + 2 * i], v = s[32 * c + 2 * i + 1];
-            h[i] = pack_bf16(u, v);
-            lo[i] = pack_bf16(u - bf16lo(h[i]), v - bf16hi(h[i]));
-          }
-          tm_st16(p_col(n) + 16 * c, h);
-          tm_st16(p_col(n) + 32 + 16 * c, lo);
+        for (int i = 0; i < 16; ++i) {
+          const float u = s[2 * i], v = s[2 * i + 1];
+          h[i] = pack_bf16(u, v);
+          lo[i] = pack_bf16(u - bf16lo(h[i]), v - bf16hi(h[i]));
         }
+        tm_st16(p_col(n), h);
+        tm_st16(p_col(n) + 32, lo);
       }
       tm_stored();
       tm_before_sync();
     }
+    bool dirty = false;
+    if (busy && (T8 || !all)) {  // bf16: the other tiles have not been looked through
+      wait(&sh.full[pv.slot], pv.turn & 1);  // before the arrival: behind it the slot may be filled again
+      const uint2 u = *reinterpret_cast<const uint2*>(sh.dirty[n % Ring<D>::info]);
+      dirty = (u.x | u.y) != 0;
+    }
     mbar_arrive(&sh.p_full[n & 1]);
-    if (dirty && busy) {
+    if (dirty) {
       wait(&sh.empty[pv.slot], pv.turn & 1);
-      tm_after_sync();
-      float w[kTile];
+      float w[kHalf];
 #pragma unroll
-      for (uint32_t j = 0; j < kTile; ++j) w[j] = s[j];
-      mend<D, T8>(a, st.b, st.g, t, valid, live ? vis : 0, w, o_col());
-      tm_before_sync();
+      for (uint32_t j = 0; j < kHalf; ++j) w[j] = s[j];
+#pragma unroll 1
+      for (uint32_t h = 0; h < 2; ++h) {  // one thread of a row after the other
+        tm_after_sync();
+        if (half == h) mend<D, T8>(a, st.b, st.g, t, half * kHalf, valid, live ? vis : 0, w, o_col());
+        tm_before_sync();
+        named_barrier(pair, 64);
+      }
+      tm_after_sync();
     }
   }
 
   // The sums of a stretch, the last of whose tiles is tile n of the CTA.
-  __device__ void store(const Stretch& st, uint32_t n) {
+  __device__ __forceinline__ void store(const Stretch& st, uint32_t n) {
     const Place<D> pv(2 * n + 1);
     wait(&sh.empty[pv.slot], pv.turn & 1);
     tm_after_sync();
-    if (32 * warp >= st.b.rows * group) return;
+    const uint32_t cols = st.b.rows * group;
+    if (row - lane % 32 >= cols) return;
+    if (half) sh.sum[row] = l;
+    named_barrier(pair, 64);
     const bool nat = st.c0 == blockIdx.x;
-    const size_t col = nat ? (size_t)(st.b.row + tid / group) * a.H + st.g * group + tid % group : (size_t)blockIdx.x * kM + tid;
-    float* to = (nat ? work.nat : work.cont) + col * D;
+    const size_t first = nat ? (size_t)st.b.row * a.H + st.g * cols : (size_t)blockIdx.x * kM;
+    const uint32_t wide = nat ? cols : kM;
+    float* to = (nat ? work.nat : work.cont) + first * D + row * 8;
 #pragma unroll 1
-    for (uint32_t c = 0; c < D; c += 32) {
+    for (uint32_t c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
       uint32_t r[32];
       tm_ld32(o_col() + c, r);
       tm_loaded(r);
@@ -749,11 +786,11 @@ struct Softmax {
 #pragma unroll
         for (uint32_t i = 0; i < 32; i += 8) {
           const uint32_t w[8] = {r[i], r[i + 1], r[i + 2], r[i + 3], r[i + 4], r[i + 5], r[i + 6], r[i + 7]};
-          store32(to + c + i, a.wide, w);
+          store32(to + (c + i) * (size_t)wide, a.wide, w);
         }
       }
     }
-    if (live) (nat ? work.nat_ml : work.cont_ml)[col] = make_float4(m, skip ? -1.f : l, R, 0.f);
+    if (live && !half) (nat ? work.nat_ml : work.cont_ml)[first + row] = make_float4(m, skip ? -1.f : l + sh.sum[row], R, 0.f);
     tm_before_sync();
   }
 };
@@ -761,8 +798,9 @@ struct Softmax {
 // ------------------------------------------------------------------ products
 
 template <int D, bool T8>
-__device__ __forceinline__ void issue(Line line, uint32_t q, uint32_t ring, Notes& sh, uint32_t tmem, Waiter& wait) {
+__device__ __forceinline__ void issue(Line line, uint32_t q, uint32_t ring, Notes<D>& sh, uint32_t tmem, Waiter& wait) {
   constexpr uint32_t kQK = tm_idesc(!T8, false, kM, kTile), kPV = tm_idesc(!T8, true, kM, D);
+  const uint64_t dq = tm_desc(q, 16, 1024);
   Stretch s;
   uint32_t n = 0, items = 0;
   const auto values = [&](uint32_t i, bool add) {  // O += P V of tile i
@@ -771,10 +809,11 @@ __device__ __forceinline__ void issue(Line line, uint32_t q, uint32_t ring, Note
     wait(&sh.p_full[i & 1], (i >> 1) & 1);
     tm_after_sync();
     tm_fence_shared();
-    const uint32_t p = tmem + 128 + (i & 1) * 64, sv = ring + v.slot * Ring<D>::bytes;
+    const uint32_t p = tmem + 128 + (i & 1) * 64;
+    const uint64_t dv = tm_desc(ring + v.slot * Ring<D>::bytes, Ring<D>::slab, 1024);
 #pragma unroll
     for (uint32_t k = 0; k < kTile / 16; ++k) {
-      const uint64_t b = tm_desc(sv + k * 2048, Ring<D>::slab, 1024);
+      const uint64_t b = dv + k * 2048 / 16;
       tm_mma_ta(tmem + 256, p + 8 * k, b, kPV, add || k);
       if (!T8) tm_mma_ta(tmem + 256, p + 32 + 8 * k, b, kPV, true);
     }
@@ -788,12 +827,13 @@ __device__ __forceinline__ void issue(Line line, uint32_t q, uint32_t ring, Note
       if (n >= 2) wait(&sh.s_free[n & 1], ((n - 2) >> 1) & 1);
       tm_after_sync();
       tm_fence_shared();
-      const uint32_t sk = ring + k.slot * Ring<D>::bytes;
+      const uint64_t dk = tm_desc(ring + k.slot * Ring<D>::bytes, 16, 1024);
 #pragma unroll
-      for (uint32_t i = 0; i < D / 16; ++i)
-        tm_mma(tmem + (n & 1) * kTile, tm_desc(q + (i / 4) * Ring<D>::q_slab + (i % 4) * 32, 16, 1024),
-               tm_desc(sk + (i / 4) * Ring<D>::slab + (i % 4) * 32, 16, 1024), kQK, i != 0);
+      for (uint32_t i = 0; i < D / 16; ++i)  // descriptors count in 16 bytes
+        tm_mma(tmem + (n & 1) * kTile, dq + ((i / 4) * Ring<D>::q_slab + (i % 4) * 32) / 16,
+               dk + ((i / 4) * Ring<D>::slab + (i % 4) * 32) / 16, kQK, i != 0);
       tm_commit(&sh.s_full[n & 1]);
+      mbar_arrive(&sh.s_full[n & 1]);  // passes the loaders' notes on
       tm_commit(&sh.empty[k.slot]);
       if (t != s.t0) values(n - 1, t - 1 != s.t0);
     }
@@ -813,24 +853,24 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* q_sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
   uint8_t* ring = q_sm + Ring<D>::q;
-  Notes& sh = *reinterpret_cast<Notes*>(ring + Ring<D>::slots * Ring<D>::bytes);
+  Notes<D>& sh = *reinterpret_cast<Notes<D>*>(ring + Ring<D>::slots * Ring<D>::bytes);
   uint32_t* first = reinterpret_cast<uint32_t*>(&sh + 1);  // [n_rows + 1]
   RowNote* note = reinterpret_cast<RowNote*>(first + (a.r.n_rows + 2) / 2 * 2);
   uint8_t* block_rows = reinterpret_cast<uint8_t*>(note + a.r.n_rows);
   if (tid == 0) {
     for (uint32_t i = 0; i < Ring<D>::slots; ++i) {
-      mbar_init(&sh.full[i], kLoadThreads + i % 2);
+      mbar_init(&sh.full[i], kLoadThreads + (i % 2 == 0));
       mbar_init(&sh.empty[i], 1);
     }
     for (uint32_t i = 0; i < 2; ++i) {
-      mbar_init(&sh.s_full[i], 1);
-      mbar_init(&sh.s_free[i], 128);
-      mbar_init(&sh.p_full[i], 128);
+      mbar_init(&sh.s_full[i], 2);
+      mbar_init(&sh.s_free[i], kSoft);
+      mbar_init(&sh.p_full[i], kSoft);
     }
-    mbar_init(&sh.q_full, 128);
+    mbar_init(&sh.q_full, kSoft);
     mbar_fence_init();
   }
-  if (warp == 4) tm_alloc(&sh.tmem, 512);
+  if (warp == kSoft / 32) tm_alloc(&sh.tmem, 512);
   pdl_wait();
   pdl_launch();
 
@@ -890,7 +930,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     uint32_t rec = 0;
     if (note[r].seq != 0xffffu && off <= r && note[r - off].seq == note[r].seq && off < block_rows[r - off]) {
       const uint32_t b = r - off, length = first[b + 1] - first[b], w = first[b] * a.c.Hkv + g * length;
-      rec = (w + kLead) / per | ((w + length - 1) / per) << 8 | off << 16 | kRecOk;
+      rec = (w + kLead) / per | ((w + length - 1) / per) << 8 | off << 16 | (block_rows[b] - 1u) << 23 | kRecOk;
     }
     work.rec[i] = rec;
   }
@@ -910,34 +950,34 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     line.row = lo;
   }
   Waiter wait{a.wait_ns, a.status, false};
-  if (warp < 4) {
-    Softmax<D, T8> x{a, q_sm, sh, tid, warp, lane, tmem, group, wait, work, 1.4426950408889634f / sqrtf((float)D)};
+  if (tid < kSoft) {
+    Softmax<D, T8> x{a, q_sm, sh, tid, lane, tmem + ((32 * (warp % 4)) << 16), group, wait, work,
+                     1.4426950408889634f / sqrtf((float)D), tid % kM, tid / kM, 2 + warp % 4};
     Stretch s;
     uint32_t n = 0;
     while (line.next(s)) {
       x.put_q(s.b, s.g);
       x.begin(s.b);
-      if (T8) named_barrier(1, 128);  // q's scales
       for (uint32_t t = s.t0; t < s.t1; ++t, ++n) x.tile(s, t, n);
       x.store(s, n - 1);
     }
-  } else if (warp == 4) {
+  } else if (warp == kSoft / 32) {
     if (lane == 0) issue<D, T8>(line, smem_addr(q_sm), smem_addr(ring), sh, tmem, wait);
     __syncwarp();
   } else if constexpr (T8) {
-    uint32_t halves = 0;
+    uint32_t tiles = 0;
     Line count = line;
     Stretch s;
-    while (count.next(s)) halves += 2 * (s.t1 - s.t0);
-    const uint32_t i = tid - 160;
+    while (count.next(s)) tiles += s.t1 - s.t0;
+    const uint32_t i = tid - kSoft - 32;
     LoadTurbo8<D> x{a, ring, sh, i, i / 32, lane, i / (D / 16), i % (D / 16), wait, line};
-    x.run(halves);
+    x.run(tiles);
   } else {
-    load_plain<D>(a, line, ring, sh, tid - 160, wait);
+    load_plain<D>(a, line, ring, sh, tid - kSoft - 32, wait);
   }
   tm_before_sync();
   __syncthreads();
-  if (warp == 4) {
+  if (warp == kSoft / 32) {
     tm_after_sync();
     tm_free(tmem, 512);
   }
@@ -945,124 +985,151 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
 
 // ------------------------------------------------------------------ the join
 
-// A column's parts added up: TEAMS teams of D / 8 lanes take its parts in turn, eight dims a lane.
+// Columns' parts added up. A warp takes four neighbouring columns of a row's heads (four lanes read 128 bytes side by
+// side), a lane D / 8 / 8 pieces of eight dims of one; TEAMS warps of a CTA take a column's parts in turn.
 template <int D, bool T8, int TEAMS>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ RowsAttend a) {
-  constexpr uint32_t LPR = D / 8, COLS = 256 / LPR / TEAMS;
-  __shared__ float sums[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? COLS : 1][TEAMS > 1 ? D : 1];
-  const uint32_t l = threadIdx.x % LPR, slot = threadIdx.x / LPR, sub = slot % TEAMS, at = slot / TEAMS, lane = threadIdx.x & 31;
-  const uint32_t group = a.H / a.c.Hkv, col = blockIdx.x * COLS + at;
-  const uint32_t r = col / a.H, h = col % a.H;
+  constexpr uint32_t P = D / 64, FOURS = 8 / TEAMS;  // pieces of a lane, fours of columns of a CTA
+  __shared__ float sums[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? 8 * P : 1][32];
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % TEAMS;
+  const uint32_t group = a.H / a.c.Hkv, c = blockIdx.x * FOURS * 4 + warp / TEAMS * 4 + lane % 4, l8 = lane / 4;
+  const uint32_t r = c / a.H, h = c % a.H;
   const bool in = r < a.r.n_rows;
   const Work work = work_of(a.work, a.r.n_rows, a.H, D);
-  uint4 z = make_uint4(0u, 0u, 0u, 0u);
   pdl_wait();
   pdl_launch();
-  if (in && a.gate) z = load16(a.gate + (size_t)col * a.gate_stride + 8 * l);
   const uint32_t rec = in ? work.rec[r * a.c.Hkv + h / group] : 0;
-  const uint32_t c0 = rec & 255u, n = rec & kRecOk ? (rec >> 8 & 255u) - c0 + 1 : 0, cont = (rec >> 16 & 255u) * group + h % group;
-  const auto ml = [&](uint32_t k) { return k ? work.cont_ml[(size_t)(c0 + k) * kM + cont] : work.nat_ml[col]; };
-  const auto part = [&](uint32_t k) { return (k ? work.cont + ((size_t)(c0 + k) * kM + cont) * D : work.nat + (size_t)col * D) + 8 * l; };
-  // the largest maximum and (T8) V's relative to it, the sum: a part a lane, in rounds
+  const uint32_t c0 = rec & 255u, n = rec & kRecOk ? (rec >> 8 & 255u) - c0 + 1 : 0, off = rec >> 16 & 127u;
+  const uint32_t cols = ((rec >> 23 & 127u) + 1) * group, col = off * group + h % group;  // the item's, and this one among them
+  const size_t first = in ? (size_t)(r - off) * a.H + h / group * cols : 0;
+  const auto ml = [&](uint32_t k) { return k ? work.cont_ml[(size_t)(c0 + k) * kM + col] : work.nat_ml[first + col]; };
+  // the largest maximum and (T8) V's relative to it, the sum: a part each of the column's eight lanes, in rounds
   bool ok = n > 0;
   float M = -INFINITY, V = -INFINITY, L = 0.f;
-  for (uint32_t k = l; k < n; k += LPR) {
+  for (uint32_t k = l8; k < n; k += 8) {
     const float4 x = ml(k);
     if (x.y < 0.f) ok = false;
     M = fmaxf(M, x.x);
   }
-  const uint32_t lanes = LPR == 32 ? 0xffffffffu : ((1u << (LPR % 32)) - 1u) << (lane / LPR * LPR);
 #pragma unroll
-  for (uint32_t w = 1; w < LPR; w <<= 1) M = fmaxf(M, __shfl_xor_sync(lanes, M, w));
-  ok = __all_sync(lanes, ok);
+  for (uint32_t w = 4; w < 32; w <<= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    ok &= __shfl_xor_sync(0xffffffffu, ok, w);
+  }
   const float mu = finite_or_0(M);
   const auto exponent = [&](const float4& x) { return T8 ? x.z + (finite_or_0(x.x) - mu) : x.x - mu; };  // of its sums O
-  for (uint32_t k = l; k < n; k += LPR) {
+  for (uint32_t k = l8; k < n; k += 8) {
     const float4 x = ml(k);
     if (T8) V = fmaxf(V, exponent(x));
     L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - mu);
   }
 #pragma unroll
-  for (uint32_t w = 1; w < LPR; w <<= 1) {
-    V = fmaxf(V, __shfl_xor_sync(lanes, V, w));
-    L += __shfl_xor_sync(lanes, L, w);
+  for (uint32_t w = 4; w < 32; w <<= 1) {
+    V = fmaxf(V, __shfl_xor_sync(0xffffffffu, V, w));
+    L += __shfl_xor_sync(0xffffffffu, L, w);
   }
   const float down = T8 ? finite_or_0(V) : 0.f;
-  float x[8] = {};
-#pragma unroll 4
+  float x[P][8] = {};
+#pragma unroll 2
   for (uint32_t k = sub; k < n; k += TEAMS) {
     const float4 y = ml(k);
     const float f = y.x == -INFINITY || (T8 && y.z == -INFINITY) ? 0.f : ex2(exponent(y) - down);
-    const float4* from = reinterpret_cast<const float4*>(part(k));
-    const float4 u = from[0], v = from[1];
-    if (f != 0.f) {
-      x[0] = fmaf(u.x, f, x[0]);
-      x[1] = fmaf(u.y, f, x[1]);
-      x[2] = fmaf(u.z, f, x[2]);
-      x[3] = fmaf(u.w, f, x[3]);
-      x[4] = fmaf(v.x, f, x[4]);
-      x[5] = fmaf(v.y, f, x[5]);
-      x[6] = fmaf(v.z, f, x[6]);
-      x[7] = fmaf(v.w, f, x[7]);
-    }
+    const float* from = k ? work.cont + (size_t)(c0 + k) * kM * D + col * 8 : work.nat + first * D + col * 8;
+    const uint32_t wide = k ? kM : cols;
+    float4 u[P][2];
+#pragma unroll
+    for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) u[i][j] = __ldcg(reinterpret_cast<const float4*>(from + (size_t)(l8 + 8 * i) * 8 * wide) + j);
+    if (f != 0.f)
+#pragma unroll
+      for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x[i][4 * j] = fmaf(u[i][j].x, f, x[i][4 * j]);
+          x[i][4 * j + 1] = fmaf(u[i][j].y, f, x[i][4 * j + 1]);
+          x[i][4 * j + 2] = fmaf(u[i][j].z, f, x[i][4 * j + 2]);
+          x[i][4 * j + 3] = fmaf(u[i][j].w, f, x[i][4 * j + 3]);
+        }
   }
   if constexpr (TEAMS > 1) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) sums[sub][at][8 * l + e] = x[e];
+    for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sums[sub][8 * i + e][lane] = x[i][e];
     __syncthreads();
     if (sub) return;
 #pragma unroll 1
     for (uint32_t k = 1; k < TEAMS; ++k)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) x[e] += sums[k][at][8 * l + e];
+      for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] += sums[k][8 * i + e][lane];
   }
   const float inv = L == 0.f ? 0.f : 1.f / L, up = T8 ? ex2(0.5f * down) : 1.f;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) x[e] = L == 0.f ? 0.f : T8 ? x[e] * inv * up * up : x[e] * inv;
-  if constexpr (T8) {
-    if constexpr (TEAMS > 1 && LPR < 32) {  // the column's own lanes alone are here
-      static_assert(COLS == 1, "one column a CTA");
-    }
-    float y[8];
+  for (uint32_t i = 0; i < P; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) y[e] = x[e];
+    for (int e = 0; e < 8; ++e) x[i][e] = L == 0.f ? 0.f : T8 ? x[i][e] * inv * up * up : x[i][e] * inv;
+  if constexpr (T8) {  // rotated back: dim 8 (l8 + 8 i) + e
 #pragma unroll
-    for (int hb = 1; hb < 8; hb <<= 1)
+    for (uint32_t i = 0; i < P; ++i) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (!(e & hb)) {
-          const float u = y[e], w = y[e + hb];
-          y[e] = u + w;
-          y[e + hb] = u - w;
+      for (int hb = 1; hb < 8; hb <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!(e & hb)) {
+            const float u = x[i][e], w = x[i][e + hb];
+            x[i][e] = u + w;
+            x[i][e + hb] = u - w;
+          }
+#pragma unroll
+      for (uint32_t w = 4; w < 32; w <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float o = __shfl_xor_sync(0xffffffffu, x[i][e], w);
+          x[i][e] = lane & w ? o - x[i][e] : x[i][e] + o;
         }
+    }
 #pragma unroll
-    for (uint32_t w = 1; w < LPR; w <<= 1)
+    for (uint32_t hb = 1; hb < P; hb <<= 1)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float o = __shfl_xor_sync(lanes, y[e], w);
-        y[e] = lane & w ? o - y[e] : y[e] + o;
-      }
+      for (uint32_t i = 0; i < P; ++i)
+        if (!(i & hb))
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = y[e] * rsqrtf((float)D);
+          for (int e = 0; e < 8; ++e) {
+            const float u = x[i][e], w = x[i + hb][e];
+            x[i][e] = u + w;
+            x[i + hb][e] = u - w;
+          }
+    const float norm = rsqrtf((float)D);
+#pragma unroll
+    for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] *= norm;
   }
   if (!ok) return;
-  if (a.gate) {
-    float g[8];
-    unpack8(z, g);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] *= sigmoidf_(g[e]);
+  for (uint32_t i = 0; i < P; ++i) {
+    const uint32_t d = 8 * (l8 + 8 * i);
+    if (a.gate) {
+      float g[8];
+      unpack8(*reinterpret_cast<const uint4*>(a.gate + (size_t)c * a.gate_stride + d), g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] *= sigmoidf_(g[e]);
+    }
+    *reinterpret_cast<uint4*>(a.out + (size_t)c * D + d) = pack8(x[i]);
   }
-  *reinterpret_cast<uint4*>(a.out + (size_t)col * D + 8 * l) = pack8(x);
 }
 
 template <int D>
-uint32_t smem_of(uint32_t n_rows) {
-  return 1024 + Ring<D>::q + Ring<D>::slots * Ring<D>::bytes + sizeof(Notes) + (n_rows + 2) / 2 * 8 + n_rows * (sizeof(RowNote) + 1);
+constexpr uint32_t smem_of(uint32_t n_rows) {
+  return 1024 + Ring<D>::q + Ring<D>::slots * Ring<D>::bytes + sizeof(Notes<D>) + (n_rows + 2) / 2 * 8 + n_rows * (sizeof(RowNote) + 1);
 }
 template <int D, bool T8>
 bool allow() {
-  return smem_of<D>(kMaxQueries) <= 227 * 1024 &&
-         cudaFuncSetAttribute(rows_kernel<D, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<D>(kMaxQueries)) == cudaSuccess;
+  static_assert(smem_of<D>(kMaxQueries) <= 227 * 1024, "shared memory of a CTA");
+  return cudaFuncSetAttribute(rows_kernel<D, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<D>(kMaxQueries)) == cudaSuccess;
 }
 
 template <int D, bool T8>
@@ -1070,11 +1137,10 @@ cudaError_t launch(const RowsAttend& a, cudaStream_t st) {
   static_assert(2 * kMaxSeqs * 4 + 4 <= Ring<64>::slots * Ring<64>::bytes, "the rows' places");
   cudaError_t e = launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D>(a.r.n_rows), st, a);
   if (e != cudaSuccess) return e;
-  // few columns: each a CTA, whose teams share its parts; many: a team a column
-  constexpr uint32_t all = 256 / (D / 8);
+  // few columns: a CTA for four of them, whose warps share their parts; many: a warp for four
   const uint32_t cols = a.r.n_rows * a.H;
-  if (cols <= 2048) return launch_early(join_kernel<D, T8, all>, dim3(cols), 256, 0, st, a);
-  return launch_early(join_kernel<D, T8, 1>, dim3((cols + all - 1) / all), 256, 0, st, a);
+  if (cols <= 2048) return launch_early(join_kernel<D, T8, 8>, dim3((cols + 3) / 4), 256, 0, st, a);
+  return launch_early(join_kernel<D, T8, 1>, dim3((cols + 31) / 32), 256, 0, st, a);
 }
 
 }  // namespace
