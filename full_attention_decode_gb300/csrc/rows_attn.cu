@@ -57,6 +57,85 @@ struct Ring {
   static_assert(slots / 2 + 2 <= info, "notes");
 };
 
+// A row of the call as every CTA keeps it: position, sequence, which of its sequence's rows it is, and how many rows the
+// block has that begins with it.
+struct RowNote {
+  uint32_t pos, bits;
+  __device__ __forceinline__ uint32_t seq() const { return bits & 4095u; }
+  __device__ __forceinline__ uint32_t index() const { return bits >> 12 & 2047u; }
+  __device__ __forceinline__ uint32_t rows() const { return bits >> 23 & 255u; }
+  __device__ __forceinline__ bool ok() const { return bits >> 31; }
+};
+static_assert(kMaxSeqs <= 4096 && kMaxQueries <= 2048, "bits of a row's note");
+// Behind the prefix sums [n_rows + 1].
+__device__ __forceinline__ RowNote* notes_of(const uint32_t* first, uint32_t n_rows) {
+  return reinterpret_cast<RowNote*>(const_cast<uint32_t*>(first) + (n_rows + 2) / 2 * 2);
+}
+
+// A block of rows and the tokens it sees: octets of eight tokens, nA first ones, then from b8 on.
+struct Block {
+  uint32_t row, rows, seq, index, pos, last;  // pos, last: positions of the first and the last row
+  uint32_t nA, b8, octets;
+  uint32_t from;  // the first token behind nA's that a row sees
+  __device__ __forceinline__ uint32_t token(uint32_t o) const { return o < nA ? 8 * o : b8 + 8 * (o - nA); }
+  __device__ __forceinline__ uint32_t tiles() const { return (octets + kOctets - 1) / kOctets; }
+};
+__device__ __forceinline__ Block block_of(const RowsAttend& a, uint32_t row, uint32_t rows, const RowNote& n) {
+  Block b;
+  b.row = row;
+  b.rows = rows;
+  b.seq = n.seq();
+  b.index = n.index();
+  b.pos = n.pos;
+  b.last = n.pos + rows - 1;
+  b.nA = b.b8 = b.from = 0;
+  if (!a.parent) {
+    b.from = b.pos + 1 > a.window ? b.pos + 1 - a.window : 0;
+    b.b8 = b.from & ~7u;
+    b.nA = a.n_first / 8 + (a.n_first % 8 != 0);
+    if (b.nA > b.b8 / 8) b.nA = b.b8 = b.from = 0;  // the first tokens reach the window
+  }
+  b.octets = b.nA + (b.last - b.b8) / 8 + 1;
+  return b;
+}
+// A CTA's stretch of an item.
+struct Stretch {
+  Block b;
+  uint32_t g, t0, t1, c0;
+};
+// A warp's way along the line: its CTA's part is [w, w1), cut into stretches. In shared memory, one for each warp: the
+// registers are the loops'.
+struct Walk {
+  uint32_t w, w1, row, more;
+  Stretch s;
+};
+__device__ __forceinline__ bool next(const RowsAttend& a, const uint32_t* first, uint32_t per, Walk& k, uint32_t lane) {
+  __syncwarp();
+  if (lane == 0) {
+    const RowNote* note = notes_of(first, a.r.n_rows);
+    const uint32_t Hkv = a.c.Hkv, w1 = k.w1;
+    uint32_t w = k.w, row = k.row, more = 0;
+    while (w < w1 && !more) {
+      while (first[row + 1] * Hkv <= w) ++row;
+      const Block b = block_of(a, row, note[row].rows(), note[row]);
+      const uint32_t length = b.tiles() + kLead, in = w - first[row] * Hkv;
+      const uint32_t at = in % length, used = min(length - at, w1 - w);
+      k.s.b = b;
+      k.s.g = in / length;
+      k.s.t0 = max(at, kLead) - kLead;
+      k.s.t1 = max(at + used, kLead) - kLead;
+      k.s.c0 = (w - at + kLead) / per;
+      w += used;
+      more = k.s.t0 != k.s.t1;
+    }
+    k.w = w;
+    k.row = row;
+    k.more = more;
+  }
+  __syncwarp();
+  return k.more;
+}
+
 // Shared memory behind Q and the ring.
 template <uint32_t kInfo>
 struct NotesOf {
@@ -70,16 +149,14 @@ struct NotesOf {
   float2 top[2][2][kM];  // a row's two threads' maxima
   float sum[kM];         // the second thread's sum
   int32_t parent[kMaxNodes];
+  Walk walk[kRowsThreads / 32];
 };
 
 template <int D>
 using Notes = NotesOf<Ring<D>::info>;
 
-// A row of the call as every CTA keeps it.
-struct RowNote {
-  uint32_t pos;
-  uint16_t seq, index;  // index: which of its sequence's rows (clipped)
-};
+template <int D>
+using Notes = NotesOf<Ring<D>::info>;
 
 struct Work {  // the scratch
   // Sums of an item's first stretch and of the one that a CTA goes on with: [D / 8][columns][8], so that a
@@ -136,32 +213,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 __device__ __forceinline__ uint32_t bits_below(int64_t n) { return n <= 0 ? 0u : n >= 8 ? 0xffu : (1u << n) - 1u; }
 
-// A block of rows and the tokens it sees: octets of eight tokens, nA first ones, then from b8 on.
-struct Block {
-  uint32_t row, rows, seq, index, pos, last;  // pos, last: positions of the first and the last row
-  uint32_t nA, b8, octets;
-  uint32_t from;  // the first token behind nA's that a row sees
-  __device__ __forceinline__ uint32_t token(uint32_t o) const { return o < nA ? 8 * o : b8 + 8 * (o - nA); }
-  __device__ __forceinline__ uint32_t tiles() const { return (octets + kOctets - 1) / kOctets; }
-};
-__device__ __forceinline__ Block block_of(const RowsAttend& a, uint32_t row, uint32_t rows, const RowNote& n) {
-  Block b;
-  b.row = row;
-  b.rows = rows;
-  b.seq = n.seq;
-  b.index = n.index;
-  b.pos = n.pos;
-  b.last = n.pos + rows - 1;
-  b.nA = b.b8 = b.from = 0;
-  if (!a.parent) {
-    b.from = b.pos + 1 > a.window ? b.pos + 1 - a.window : 0;
-    b.b8 = b.from & ~7u;
-    b.nA = a.n_first / 8 + (a.n_first % 8 != 0);
-    if (b.nA > b.b8 / 8) b.nA = b.b8 = b.from = 0;  // the first tokens reach the window
-  }
-  b.octets = b.nA + (b.last - b.b8) / 8 + 1;
-  return b;
-}
 // Whether every row of the block sees all of octet o.
 __device__ __forceinline__ bool octet_full(const RowsAttend& a, const Block& b, uint32_t o) {
   if (o >= b.octets) return false;
@@ -169,36 +220,6 @@ __device__ __forceinline__ bool octet_full(const RowsAttend& a, const Block& b, 
   if (a.parent) return t + 7 < b.pos - b.index;
   return t + 7 <= b.pos && (b.last - t < a.window || (t < a.n_first && a.n_first - t >= 8));
 }
-
-// A CTA's stretch of an item.
-struct Stretch {
-  Block b;
-  uint32_t g, t0, t1, c0;
-};
-// The line: prefix sums over the rows, the CTA's part [w, w1), cut into stretches.
-struct Line {
-  const RowsAttend& a;
-  const uint32_t* first;
-  const RowNote* note;
-  const uint8_t* rows;
-  uint32_t per, w, w1, row;
-  __device__ __forceinline__ bool next(Stretch& s) {
-    while (w < w1) {
-      const uint32_t Hkv = a.c.Hkv;
-      while (first[row + 1] * Hkv <= w) ++row;
-      s.b = block_of(a, row, rows[row], note[row]);
-      const uint32_t length = s.b.tiles() + kLead, in = w - first[row] * Hkv;
-      s.g = in / length;
-      const uint32_t at = in % length, used = min(length - at, w1 - w);
-      s.t0 = max(at, kLead) - kLead;
-      s.t1 = max(at + used, kLead) - kLead;
-      s.c0 = (w - at + kLead) / per;
-      w += used;
-      if (s.t0 != s.t1) return true;
-    }
-    return false;
-  }
-};
 
 // Bounded waits of one thread: after one has run out no other waits.
 struct Waiter {
@@ -224,14 +245,16 @@ struct Place {
 
 // Where the octets of four tiles lie, an octet a lane.
 struct Found {
-  size_t row;
+  uint32_t row;  // a row is 128 bytes of K and V at least: no memory holds 2^32
   bool in;
 };
 __device__ __forceinline__ Found find(const RowsAttend& a, const Block& b, uint32_t t, uint32_t lane) {
   Found f = {0, false};
   const uint32_t o = t * kOctets + lane;
   if (o < b.octets) {
-    f.in = cache_row(a.c, b.seq, b.token(o), f.row);
+    size_t row = 0;
+    f.in = cache_row(a.c, b.seq, b.token(o), row);
+    f.row = (uint32_t)row;
     if (!f.in) set_status(a.status, kStatusRange);
   }
   return f;
@@ -249,17 +272,16 @@ __device__ __forceinline__ bool not_a_number_bf16(uint32_t w) {  // in either ha
 }
 
 template <int D>
-__device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line0, uint8_t* ring, Notes<D>& sh, uint32_t tid,
-                                           Waiter& wait) {
+__device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* first, uint32_t per, Walk& walk, uint8_t* ring,
+                                           Notes<D>& sh, uint32_t tid, Waiter& wait) {
   constexpr uint32_t C = D / 8, STEP = kLoadThreads / C, J = kTile / STEP;  // pieces of a row, rows of a pass, passes
   const uint32_t warp = tid / 32, lane = tid % 32, r0 = tid / C, c = tid % C, q0 = warp * 32 / C / 8;
   const uint32_t to = (c / 8) * Ring<D>::slab + sw(r0, c % 8);  // STEP is a multiple of 8: piece j lies STEP * 128 behind
   static_assert(STEP % 8 == 0, "the swizzle of a thread's rows");
   const uint32_t stride = a.c.Hkv * D;
-  Line line = line0;
-  Stretch s;
+  const Stretch& s = walk.s;
   uint32_t n = 0;
-  while (line.next(s)) {
+  while (next(a, first, per, walk, lane)) {
     Found now = find(a, s.b, s.t0, lane), then = find(a, s.b, s.t0 + 4, lane);
     for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
       const uint32_t i = (t - s.t0) % 4;
@@ -276,30 +298,28 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line
         rows = bits_below(hi) & ~bits_below(lo);
       }
       if (!(valid >> (lane % 8) & 1)) rows = 0;
-      size_t off[J];
-      uint32_t in = 0;
+      uint32_t row[J], in = 0;
 #pragma unroll
       for (uint32_t j = 0; j < J; ++j) {
         const uint32_t q = q0 + j * STEP / 8;  // a warp's rows lie in one octet
-        const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)now.row, 8 * i + q) + r0 % 8;
+        row[j] = __shfl_sync(0xffffffffu, now.row, 8 * i + q) + r0 % 8;
         in |= (__shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u) << j;
-        off[j] = row * stride + s.g * D + 8 * c;
       }
 #pragma unroll 1
       for (uint32_t p = 0; p < 2; ++p) {
         const Place<D> at(2 * n + p);
         if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
         uint8_t* slot = ring + at.slot * Ring<D>::bytes;
-        const uint16_t* base = reinterpret_cast<const uint16_t*>(p ? a.c.v : a.c.k);
+        const uint16_t* base = reinterpret_cast<const uint16_t*>(p ? a.c.v : a.c.k) + s.g * D + 8 * c;
         if (!p || full) {
           const uint32_t dst = smem_addr(slot) + to;
 #pragma unroll
-          for (uint32_t j = 0; j < J; ++j) cp16(dst + j * STEP * 128, in >> j & 1 ? base + off[j] : base, in >> j & 1);
+          for (uint32_t j = 0; j < J; ++j) cp16(dst + j * STEP * 128, in >> j & 1 ? base + (size_t)row[j] * stride : base, in >> j & 1);
           cp_arrive(&sh.full[at.slot]);
         } else {
           uint4 x[J];
 #pragma unroll
-          for (uint32_t j = 0; j < J; ++j) x[j] = in >> j & 1 ? load16(base + off[j]) : make_uint4(0u, 0u, 0u, 0u);
+          for (uint32_t j = 0; j < J; ++j) x[j] = in >> j & 1 ? load16(base + (size_t)row[j] * stride) : make_uint4(0u, 0u, 0u, 0u);
           bool bad = false;
 #pragma unroll
           for (uint32_t j = 0; j < J; ++j) {
@@ -333,52 +353,69 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const Line& line
 template <int D>
 struct LoadTurbo8 {
   static constexpr uint32_t C = D / 16, STEP = kLoadThreads / C, J = kTile / STEP;
-  struct Codes {
-    uint4 c[J];
-    uint16_t s[J];
-  };
   const RowsAttend& a;
   uint8_t* ring;
   Notes<D>& sh;
   uint32_t tid, warp, lane, r0, c;
   Waiter& wait;
   // the tile that is fetched, ahead of the one that is put
-  Line line;
-  Stretch s;
+  const uint32_t* first;
+  uint32_t per;
+  Walk& walk;
+  const Stretch& s;
   Found now, then;
-  uint32_t t, valid;
+  uint32_t t, valid, in;
   bool more;
+  uint32_t row[J];  // of a piece
 
   __device__ __forceinline__ void begin() {
-    more = line.next(s);
+    more = next(a, first, per, walk, lane);
     if (more) {
       t = s.t0;
       now = find(a, s.b, t, lane);
       then = find(a, s.b, t + 4, lane);
     }
   }
-  __device__ __forceinline__ void fetch(Codes& x, uint32_t p) {
+  static __device__ __forceinline__ uint16_t load2(const uint16_t* p) {  // nothing waits for it here
+    uint16_t r;
+    asm volatile("ld.global.b16 %0, [%1];" : "=h"(r) : "l"(p));
+    return r;
+  }
+  // Where the next tile's pieces lie, then its scales and K's codes.
+  __device__ __forceinline__ void fetch_k(uint4 (&k)[J], uint16_t (&ks)[J], uint16_t (&vs)[J]) {
+    in = 0;
     if (!more) return;
     const uint32_t i = (t - s.t0) % 4;
     valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
-    const uint8_t* base = p ? a.c.v : a.c.k;
-    const uint16_t* sc = p ? a.c.vs : a.c.ks;
+    uint32_t rows = 0xffu;  // lane % 8's octet: rows of it that are loaded
+    if (!__all_sync(0xffffffffu, octet_full(a, s.b, t * kOctets + lane % 8))) {
+      uint32_t lo, hi;
+      octet_rows(a, s.b, t * kOctets + lane % 8, lo, hi);
+      rows = bits_below(hi) & ~bits_below(lo);
+    }
+    if (!(valid >> (lane % 8) & 1)) rows = 0;
 #pragma unroll
     for (uint32_t j = 0; j < J; ++j) {
-      const uint32_t r = r0 + j * STEP, q = (warp * 32 / C + j * STEP) / 8;
-      const size_t row = __shfl_sync(0xffffffffu, (unsigned long long)now.row, 8 * i + q) + r % 8;
-      uint32_t lo, hi;
-      octet_rows(a, s.b, t * kOctets + q, lo, hi);
-      const bool in = (valid >> q & 1) && r % 8 >= lo && r % 8 < hi;
-      x.c[j] = make_uint4(0u, 0u, 0u, 0u);
-      x.s[j] = 0;
-      if (in) {
-        x.c[j] = load16(base + (row * a.c.Hkv + s.g) * D + 16 * c);
-        x.s[j] = sc[row * a.c.sstride + s.g * C + c];
+      const uint32_t q = warp * 32 / C / 8 + j * STEP / 8;  // a warp's rows lie in one octet
+      row[j] = __shfl_sync(0xffffffffu, now.row, 8 * i + q) + r0 % 8;
+      const bool here = __shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u;
+      in |= (uint32_t)here << j;
+      const size_t so = (size_t)row[j] * a.c.sstride + s.g * C + c;
+      ks[j] = vs[j] = 0;
+      k[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (here) {
+        ks[j] = load2(a.c.ks + so);
+        vs[j] = load2(a.c.vs + so);
+        k[j] = load16(a.c.k + s.g * D + 16 * c + (size_t)row[j] * (a.c.Hkv * D));
       }
     }
   }
-  __device__ __forceinline__ void advance() {
+  __device__ __forceinline__ void fetch_v(uint4 (&v)[J]) {
+#pragma unroll
+    for (uint32_t j = 0; j < J; ++j) {
+      v[j] = make_uint4(0u, 0u, 0u, 0u);
+      if (in >> j & 1) v[j] = load16(a.c.v + s.g * D + 16 * c + (size_t)row[j] * (a.c.Hkv * D));
+    }
     if (!more) return;
     if (++t == s.t1) {
       begin();
@@ -387,80 +424,100 @@ struct LoadTurbo8 {
       then = find(a, s.b, t + 4, lane);
     }
   }
-  static __device__ __forceinline__ bool number(uint16_t scale) { return (scale & 0x7f80u) != 0x7f80u; }
-  // The exponent of a token's largest scale, from the lanes that have it.
-  static __device__ __forceinline__ int exponent(uint16_t scale) {
-    float mx = number(scale) ? fabsf(bf16f(scale)) : 0.f;
+  // Sixteen codes times f (twice, in f16) into a piece's place.
+  __device__ __forceinline__ void put(uint8_t* slab, uint32_t r, const uint32_t (&w)[4], uint32_t f2) const {
+    uint32_t y[8];
 #pragma unroll
-    for (uint32_t m = 1; m < C; m <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, m));
-    return min(max((int)(__float_as_uint(mx) >> 23) - 127, -126), 126);
+    for (int i = 0; i < 8; ++i) y[i] = hmul2(e4m3_to_f16x2(w[i / 2] >> (16 * (i % 2))), f2);
+    const uint32_t j8 = (c % 4) * 2;
+    *reinterpret_cast<uint4*>(slab + sw(r, j8)) = make_uint4(y[0], y[1], y[2], y[3]);
+    *reinterpret_cast<uint4*>(slab + sw(r, j8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
   }
-  // A half-tile of tile n into the ring, as f16 over 2^E. K's arrival releases the notes: K's scales, V's exponents and what octets are there.
-  template <uint32_t V>
-  __device__ __forceinline__ void put(const Codes& x, const Codes& v, uint32_t n, uint32_t valid) {
-    const Place<D> at(2 * n + V);
+  __device__ __forceinline__ uint8_t* slot_of(const Place<D>& at) {
     if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
-    uint8_t* slot = ring + at.slot * Ring<D>::bytes + (c / 4) * Ring<D>::slab;
-    bool bad = false;
-#pragma unroll
-    for (uint32_t j = 0; j < J; ++j) {
-      const uint32_t r = r0 + j * STEP;
-      const int e = exponent(x.s[j]);
-      if (!V) {
-        const int ev = exponent(v.s[j]);
-        if (c == 0) {
-          sh.k_scale[n % Ring<D>::info][r] = pow2(e);
-          sh.v_exp[n % Ring<D>::info][r] = (float)ev;
-        }
-      }
-      float f = bf16f(x.s[j]) * pow2(-e);
-      uint32_t w[4] = {x.c[j].x, x.c[j].y, x.c[j].z, x.c[j].w};
-      if (V) {
-        if (!number(x.s[j])) {
-          bad = true;
-          f = 0.f;
-        }
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {  // codes 0x7f and 0xff are NaN
-          const uint32_t nan = __vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          bad |= nan != 0;
-          w[i] &= ~nan;
-        }
-      }
-      const uint32_t f2 = pack_f16(f, f);
-      uint32_t y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = hmul2(e4m3_to_f16x2(w[i / 2] >> (16 * (i % 2))), f2);
-      const uint32_t j8 = (c % 4) * 2;
-      *reinterpret_cast<uint4*>(slot + sw(r, j8)) = make_uint4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint4*>(slot + sw(r, j8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-    }
-    if (V) {
-      bad = __any_sync(0xffffffffu, bad);
-      if (lane == 0) sh.dirty[n % Ring<D>::info][warp] = bad;
-    }
-    tm_fence_shared();
-    mbar_arrive(&sh.full[at.slot]);
-    if (!V && tid == 0) {
-      sh.valid[n % Ring<D>::info] = valid;
-      mbar_arrive(&sh.full[at.slot]);
-    }
+    return ring + at.slot * Ring<D>::bytes + (c / 4) * Ring<D>::slab;
   }
-  __device__ __forceinline__ void run(uint32_t tiles) {
-    Codes k, v;
+  // Tiles into the ring, as f16 over 2^E. K's arrival releases the notes: K's scales, V's exponents, what octets are there.
+  __device__ __forceinline__ void run() {
+    uint4 k[J], v[J];
+    uint16_t ks[J], vs[J];
     begin();
-    fetch(k, 0);
-    fetch(v, 1);
+    bool go = more;
+    fetch_k(k, ks, vs);
     uint32_t here = valid;
-    advance();
+    fetch_v(v);
 #pragma unroll 1
-    for (uint32_t n = 0; n < tiles; ++n) {
-      put<0>(k, v, n, here);
-      fetch(k, 0);
-      put<1>(v, v, n, here);
-      fetch(v, 1);
+    for (uint32_t n = 0; go; ++n) {
+      // a token's largest scales, K's and V's at once, from the lanes that have them; those that are no numbers do not count
+      uint32_t fk[J], fv[J], bad = 0;
+      {
+        uint32_t mx[J], scale[J];  // K's in the low half
+#pragma unroll
+        for (uint32_t j = 0; j < J; ++j) {
+          scale[j] = ks[j] | (uint32_t)vs[j] << 16;
+          mx[j] = scale[j] & 0x7fff7fffu;
+          if ((mx[j] & 0x7f80u) == 0x7f80u) mx[j] &= 0xffff0000u;
+          if ((mx[j] & 0x7f800000u) == 0x7f800000u) {
+            mx[j] &= 0xffffu;
+            bad = 1;
+            scale[j] &= 0xffffu;
+          }
+        }
+#pragma unroll
+        for (uint32_t m = 1; m < C; m <<= 1)
+#pragma unroll
+          for (uint32_t j = 0; j < J; ++j) mx[j] = __vmaxu2(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], m));
+#pragma unroll
+        for (uint32_t j = 0; j < J; ++j) {
+          const int ek = min(max((int)(mx[j] >> 7 & 255u) - 127, -126), 126), ev = min(max((int)(mx[j] >> 23) - 127, -126), 126);
+          if (c == 0) {
+            sh.k_scale[n % Ring<D>::info][r0 + j * STEP] = pow2(ek);
+            sh.v_exp[n % Ring<D>::info][r0 + j * STEP] = (float)ev;
+          }
+          const float x = bf16lo(scale[j]) * pow2(-ek), y = bf16hi(scale[j]) * pow2(-ev);
+          fk[j] = pack_f16(x, x);
+          fv[j] = pack_f16(y, y);
+        }
+      }
+      {
+        const Place<D> at(2 * n);
+        uint8_t* slab = slot_of(at);
+#pragma unroll
+        for (uint32_t j = 0; j < J; ++j) {
+          const uint32_t w[4] = {k[j].x, k[j].y, k[j].z, k[j].w};
+          put(slab, r0 + j * STEP, w, fk[j]);
+        }
+        tm_fence_shared();
+        mbar_arrive(&sh.full[at.slot]);
+        if (tid == 0) {
+          sh.valid[n % Ring<D>::info] = here;
+          mbar_arrive(&sh.full[at.slot]);
+        }
+      }
+      go = more;
+      fetch_k(k, ks, vs);
+      {
+        const Place<D> at(2 * n + 1);
+        uint8_t* slab = slot_of(at);
+#pragma unroll
+        for (uint32_t j = 0; j < J; ++j) {
+          uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w}, nan = 0;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) nan |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // codes 0x7f and 0xff
+          if (nan) {
+            bad = 1;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+          }
+          put(slab, r0 + j * STEP, w, fv[j]);
+        }
+        const bool any = __any_sync(0xffffffffu, bad);
+        if (lane == 0) sh.dirty[n % Ring<D>::info][warp] = any;
+        tm_fence_shared();
+        mbar_arrive(&sh.full[at.slot]);
+      }
       here = valid;
-      advance();
+      fetch_v(v);
     }
   }
 };
@@ -520,12 +577,15 @@ struct Softmax {
     const uint32_t cols = b.rows * group, j = tid % LPR;
     const auto from = [&](uint32_t col) { return a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D + 8 * j; };
     uint8_t* to = q_sm + (j / 8) * Ring<D>::q_slab;
-    if constexpr (T8) {
+    for (uint32_t col = tid / LPR; col < cols; col += PER) cp16(smem_addr(to + sw(col, j % 8)), from(col), true);
+    asm volatile("cp.async.wait_all;" ::: "memory");
+    if constexpr (T8) {  // each lane its own pieces, where they lie
 #pragma unroll 4
       for (uint32_t c0 = 0; c0 < cols; c0 += PER) {
         const uint32_t col = c0 + tid / LPR;
+        uint4* at = reinterpret_cast<uint4*>(to + sw(col, j % 8));
         uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (col < cols) u = load16(from(col));
+        if (col < cols) u = *at;
         float x[8], mx = 0.f;
         unpack8(u, x);
         wht8<LPR>(x, lane);
@@ -536,13 +596,10 @@ struct Softmax {
         const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127, -126), 126);
         const float f = pow2(-e2);
         if (j == 0 && col < cols) sh.q_scale[col] = pow2(e2);
-        u = make_uint4(pack_f16(x[0] * f, x[1] * f), pack_f16(x[2] * f, x[3] * f), pack_f16(x[4] * f, x[5] * f),
-                       pack_f16(x[6] * f, x[7] * f));
-        if (col < cols) *reinterpret_cast<uint4*>(to + sw(col, j % 8)) = u;
+        if (col < cols)
+          *at = make_uint4(pack_f16(x[0] * f, x[1] * f), pack_f16(x[2] * f, x[3] * f), pack_f16(x[4] * f, x[5] * f),
+                           pack_f16(x[6] * f, x[7] * f));
       }
-    } else {
-      for (uint32_t col = tid / LPR; col < cols; col += PER) cp16(smem_addr(to + sw(col, j % 8)), from(col), true);
-      asm volatile("cp.async.wait_all;" ::: "memory");
     }
     tm_fence_shared();
     mbar_arrive(&sh.q_full);
@@ -797,11 +854,12 @@ struct Softmax {
 
 // ------------------------------------------------------------------ products
 
+// A warp forms and waits, one lane issues.
 template <int D, bool T8>
-__device__ __forceinline__ void issue(Line line, uint32_t q, uint32_t ring, Notes<D>& sh, uint32_t tmem, Waiter& wait) {
+__device__ __forceinline__ void issue(const RowsAttend& a, const uint32_t* first, uint32_t per, Walk& walk, uint32_t lane, uint32_t q, uint32_t ring, Notes<D>& sh, uint32_t tmem, Waiter& wait) {
   constexpr uint32_t kQK = tm_idesc(!T8, false, kM, kTile), kPV = tm_idesc(!T8, true, kM, D);
   const uint64_t dq = tm_desc(q, 16, 1024);
-  Stretch s;
+  const Stretch& s = walk.s;
   uint32_t n = 0, items = 0;
   const auto values = [&](uint32_t i, bool add) {  // O += P V of tile i
     const Place<D> v(2 * i + 1);
@@ -811,15 +869,18 @@ __device__ __forceinline__ void issue(Line line, uint32_t q, uint32_t ring, Note
     tm_fence_shared();
     const uint32_t p = tmem + 128 + (i & 1) * 64;
     const uint64_t dv = tm_desc(ring + v.slot * Ring<D>::bytes, Ring<D>::slab, 1024);
+    if (elect_one()) {
 #pragma unroll
-    for (uint32_t k = 0; k < kTile / 16; ++k) {
-      const uint64_t b = dv + k * 2048 / 16;
-      tm_mma_ta(tmem + 256, p + 8 * k, b, kPV, add || k);
-      if (!T8) tm_mma_ta(tmem + 256, p + 32 + 8 * k, b, kPV, true);
+      for (uint32_t k = 0; k < kTile / 16; ++k) {
+        const uint64_t b = dv + k * 2048 / 16;
+        tm_mma_ta(tmem + 256, p + 8 * k, b, kPV, add || k);
+        if (!T8) tm_mma_ta(tmem + 256, p + 32 + 8 * k, b, kPV, true);
+      }
+      tm_commit(&sh.empty[v.slot]);
     }
-    tm_commit(&sh.empty[v.slot]);
+    __syncwarp();
   };
-  while (line.next(s)) {
+  while (next(a, first, per, walk, lane)) {
     wait(&sh.q_full, items++ & 1);
     for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
       const Place<D> k(2 * n);
@@ -828,13 +889,16 @@ __device__ __forceinline__ void issue(Line line, uint32_t q, uint32_t ring, Note
       tm_after_sync();
       tm_fence_shared();
       const uint64_t dk = tm_desc(ring + k.slot * Ring<D>::bytes, 16, 1024);
+      if (elect_one()) {
 #pragma unroll
-      for (uint32_t i = 0; i < D / 16; ++i)  // descriptors count in 16 bytes
-        tm_mma(tmem + (n & 1) * kTile, dq + ((i / 4) * Ring<D>::q_slab + (i % 4) * 32) / 16,
-               dk + ((i / 4) * Ring<D>::slab + (i % 4) * 32) / 16, kQK, i != 0);
-      tm_commit(&sh.s_full[n & 1]);
-      mbar_arrive(&sh.s_full[n & 1]);  // passes the loaders' notes on
-      tm_commit(&sh.empty[k.slot]);
+        for (uint32_t i = 0; i < D / 16; ++i)  // descriptors count in 16 bytes
+          tm_mma(tmem + (n & 1) * kTile, dq + ((i / 4) * Ring<D>::q_slab + (i % 4) * 32) / 16,
+                 dk + ((i / 4) * Ring<D>::slab + (i % 4) * 32) / 16, kQK, i != 0);
+        tm_commit(&sh.s_full[n & 1]);
+        mbar_arrive(&sh.s_full[n & 1]);  // passes the loaders' notes on
+        tm_commit(&sh.empty[k.slot]);
+      }
+      __syncwarp();
       if (t != s.t0) values(n - 1, t - 1 != s.t0);
     }
     values(n - 1, s.t1 - 1 != s.t0);
@@ -855,8 +919,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   uint8_t* ring = q_sm + Ring<D>::q;
   Notes<D>& sh = *reinterpret_cast<Notes<D>*>(ring + Ring<D>::slots * Ring<D>::bytes);
   uint32_t* first = reinterpret_cast<uint32_t*>(&sh + 1);  // [n_rows + 1]
-  RowNote* note = reinterpret_cast<RowNote*>(first + (a.r.n_rows + 2) / 2 * 2);
-  uint8_t* block_rows = reinterpret_cast<uint8_t*>(note + a.r.n_rows);
+  RowNote* note = notes_of(first, a.r.n_rows);
   if (tid == 0) {
     for (uint32_t i = 0; i < Ring<D>::slots; ++i) {
       mbar_init(&sh.full[i], kLoadThreads + (i % 2 == 0));
@@ -896,13 +959,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
       RowKind kind = locate(here, a.c.capacity, r, seq, pos, index, left);
       if (kind == kRowOk && (index > r || (a.parent && index >= kMaxNodes))) kind = kRowBad;
       if (kind == kRowBad && blockIdx.x == 0) set_status(a.status, kStatusRange);
-      note[r] = {pos, (uint16_t)(kind == kRowOk ? seq : 0xffffu), (uint16_t)min(index, 0xffffu)};
+      RowNote x = {pos, seq | min(index, 2047u) << 12 | (uint32_t)(kind == kRowOk) << 31};
       if (kind == kRowOk && index % RB == 0) {
         rows = min(min(min(RB, left), a.r.n_rows - r), a.c.capacity - pos);
         if (a.parent) rows = min(rows, kMaxNodes - index);
-        v = block_of(a, r, rows, note[r]).tiles() + kLead;
+        v = block_of(a, r, rows, x).tiles() + kLead;
+        x.bits |= rows << 23;
       }
-      block_rows[r] = (uint8_t)rows;
+      note[r] = x;
     }
     uint32_t x = v;
 #pragma unroll
@@ -926,11 +990,11 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   const Work work = work_of(a.work, a.r.n_rows, a.H, D);
   // every row's record for the join
   for (uint32_t i = blockIdx.x * kRowsThreads + tid; i < a.r.n_rows * a.c.Hkv; i += gridDim.x * kRowsThreads) {
-    const uint32_t r = i / a.c.Hkv, g = i % a.c.Hkv, off = note[r].index % RB;
+    const uint32_t r = i / a.c.Hkv, g = i % a.c.Hkv, off = note[r].index() % RB;
     uint32_t rec = 0;
-    if (note[r].seq != 0xffffu && off <= r && note[r - off].seq == note[r].seq && off < block_rows[r - off]) {
+    if (note[r].ok() && off <= r && note[r - off].seq() == note[r].seq() && off < note[r - off].rows()) {
       const uint32_t b = r - off, length = first[b + 1] - first[b], w = first[b] * a.c.Hkv + g * length;
-      rec = (w + kLead) / per | ((w + length - 1) / per) << 8 | off << 16 | (block_rows[b] - 1u) << 23 | kRecOk;
+      rec = (w + kLead) / per | ((w + length - 1) / per) << 8 | off << 16 | (note[b].rows() - 1u) << 23 | kRecOk;
     }
     work.rec[i] = rec;
   }
@@ -939,41 +1003,38 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   tm_after_sync();
   const uint32_t tmem = sh.tmem;
   const uint64_t w64 = (uint64_t)blockIdx.x * per;
-  Line line{a, first, note, block_rows, per, (uint32_t)min(w64, (uint64_t)total), (uint32_t)min(w64 + per, (uint64_t)total), 0};
-  if (line.w < line.w1) {
-    uint32_t lo = 0, hi = a.r.n_rows;  // first[lo] Hkv <= w < first[hi] Hkv
-    while (hi - lo > 1) {
+  Walk& walk = sh.walk[warp];
+  if (lane == 0) {
+    walk.w = (uint32_t)min(w64, (uint64_t)total);
+    walk.w1 = (uint32_t)min(w64 + per, (uint64_t)total);
+    uint32_t lo = 0, hi = a.r.n_rows;  // first[lo] Hkv <= w < first[hi] Hkv, if there is anything
+    while (walk.w < walk.w1 && hi - lo > 1) {
       const uint32_t mid = (lo + hi) / 2;
-      if (first[mid] * a.c.Hkv <= line.w) lo = mid;
+      if (first[mid] * a.c.Hkv <= walk.w) lo = mid;
       else hi = mid;
     }
-    line.row = lo;
+    walk.row = lo;
   }
   Waiter wait{a.wait_ns, a.status, false};
   if (tid < kSoft) {
     Softmax<D, T8> x{a, q_sm, sh, tid, lane, tmem + ((32 * (warp % 4)) << 16), group, wait, work,
                      1.4426950408889634f / sqrtf((float)D), tid % kM, tid / kM, 2 + warp % 4};
-    Stretch s;
+    const Stretch& s = walk.s;
     uint32_t n = 0;
-    while (line.next(s)) {
+    while (next(a, first, per, walk, lane)) {
       x.put_q(s.b, s.g);
       x.begin(s.b);
       for (uint32_t t = s.t0; t < s.t1; ++t, ++n) x.tile(s, t, n);
       x.store(s, n - 1);
     }
   } else if (warp == kSoft / 32) {
-    if (lane == 0) issue<D, T8>(line, smem_addr(q_sm), smem_addr(ring), sh, tmem, wait);
-    __syncwarp();
+    issue<D, T8>(a, first, per, walk, lane, smem_addr(q_sm), smem_addr(ring), sh, tmem, wait);
   } else if constexpr (T8) {
-    uint32_t tiles = 0;
-    Line count = line;
-    Stretch s;
-    while (count.next(s)) tiles += s.t1 - s.t0;
     const uint32_t i = tid - kSoft - 32;
-    LoadTurbo8<D> x{a, ring, sh, i, i / 32, lane, i / (D / 16), i % (D / 16), wait, line};
-    x.run(tiles);
+    LoadTurbo8<D> x{a, ring, sh, i, i / 32, lane, i / (D / 16), i % (D / 16), wait, first, per, walk, walk.s};
+    x.run();
   } else {
-    load_plain<D>(a, line, ring, sh, tid - kSoft - 32, wait);
+    load_plain<D>(a, first, per, walk, ring, sh, tid - kSoft - 32, wait);
   }
   tm_before_sync();
   __syncthreads();
@@ -1124,7 +1185,7 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ RowsA
 
 template <int D>
 constexpr uint32_t smem_of(uint32_t n_rows) {
-  return 1024 + Ring<D>::q + Ring<D>::slots * Ring<D>::bytes + sizeof(Notes<D>) + (n_rows + 2) / 2 * 8 + n_rows * (sizeof(RowNote) + 1);
+  return 1024 + Ring<D>::q + Ring<D>::slots * Ring<D>::bytes + sizeof(Notes<D>) + (n_rows + 2) / 2 * 8 + n_rows * sizeof(RowNote);
 }
 template <int D, bool T8>
 bool allow() {

@@ -18,6 +18,13 @@ __device__ __forceinline__ void tm_before_sync() { asm volatile("tcgen05.fence::
 __device__ __forceinline__ void tm_after_sync() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 // Shared memory written by ordinary stores and copies, made visible to the tensor cores.
 __device__ __forceinline__ void tm_fence_shared() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+// One lane of a converged warp, always the same one. What it issues is formed by the whole warp: registers that the
+// compiler knows to be uniform go into the instructions as they are (a product then takes a few cycles to issue, not 80).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t one;
+  asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(one));
+  return one != 0;
+}
 // Arrive once on bar when every product this thread issued before is complete.
 __device__ __forceinline__ void tm_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
