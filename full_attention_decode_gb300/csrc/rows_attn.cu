@@ -398,25 +398,19 @@ struct LoadTurbo8 {
     for (uint32_t j = 0; j < J; ++j) {
       const uint32_t q = warp * 32 / C / 8 + j * STEP / 8;  // a warp's rows lie in one octet
       row[j] = __shfl_sync(0xffffffffu, now.row, 8 * i + q) + r0 % 8;
-      const bool here = __shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u;
-      in |= (uint32_t)here << j;
+      const uint32_t here = __shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u;
+      in |= here << j;
+      if (!here) row[j] = 0;  // rows that nobody sees: whatever lies there, V's taken out later
       const size_t so = (size_t)row[j] * a.c.sstride + s.g * C + c;
-      ks[j] = vs[j] = 0;
-      k[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (here) {
-        ks[j] = load2(a.c.ks + so);
-        vs[j] = load2(a.c.vs + so);
-        k[j] = load16(a.c.k + s.g * D + 16 * c + (size_t)row[j] * (a.c.Hkv * D));
-      }
+      ks[j] = load2(a.c.ks + so);
+      vs[j] = load2(a.c.vs + so);
+      k[j] = load16(a.c.k + s.g * D + 16 * c + (size_t)row[j] * (a.c.Hkv * D));
     }
   }
   __device__ __forceinline__ void fetch_v(uint4 (&v)[J]) {
-#pragma unroll
-    for (uint32_t j = 0; j < J; ++j) {
-      v[j] = make_uint4(0u, 0u, 0u, 0u);
-      if (in >> j & 1) v[j] = load16(a.c.v + s.g * D + 16 * c + (size_t)row[j] * (a.c.Hkv * D));
-    }
     if (!more) return;
+#pragma unroll
+    for (uint32_t j = 0; j < J; ++j) v[j] = load16(a.c.v + s.g * D + 16 * c + (size_t)row[j] * (a.c.Hkv * D));
     if (++t == s.t1) {
       begin();
     } else if ((t - s.t0) % 4 == 0) {
@@ -444,7 +438,7 @@ struct LoadTurbo8 {
     begin();
     bool go = more;
     fetch_k(k, ks, vs);
-    uint32_t here = valid;
+    uint32_t here = valid, rows = in;
     fetch_v(v);
 #pragma unroll 1
     for (uint32_t n = 0; go; ++n) {
@@ -459,7 +453,7 @@ struct LoadTurbo8 {
           if ((mx[j] & 0x7f80u) == 0x7f80u) mx[j] &= 0xffff0000u;
           if ((mx[j] & 0x7f800000u) == 0x7f800000u) {
             mx[j] &= 0xffffu;
-            bad = 1;
+            bad |= rows >> j & 1;
             scale[j] &= 0xffffu;
           }
         }
@@ -505,7 +499,7 @@ struct LoadTurbo8 {
 #pragma unroll
           for (int i = 0; i < 4; ++i) nan |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // codes 0x7f and 0xff
           if (nan) {
-            bad = 1;
+            bad |= rows >> j & 1;
 #pragma unroll
             for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
           }
@@ -517,6 +511,7 @@ struct LoadTurbo8 {
         mbar_arrive(&sh.full[at.slot]);
       }
       here = valid;
+      rows = in;
       fetch_v(v);
     }
   }
@@ -768,6 +763,7 @@ struct Softmax {
         }
       }
       l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
+      if (!live) f = 1.f;  // whatever its scores are
       if (t != st.t0 && __any_sync(0xffffffffu, f != 1.f)) {
         const Place<D> before(2 * n - 1);
         wait(&sh.empty[before.slot], before.turn & 1);
