@@ -1400,10 +1400,25 @@ int qwen35_cache_append_rope(const qwen35_config* cfg, const qwen35_kv_cache* kv
   a.q_stride = q_stride;
   a.R = cfg->rotary_dim;
   a.to_cache = !bounds;
+  const auto wide = [](const void* p) { return (uintptr_t)p % 32 == 0; };
+  a.wide_q = wide(q) && q_stride % 16 == 0;
+  a.wide_kv = wide(k) && wide(v);
+  a.wide_out = wide(q_out) && wide(k_out);
+  a.wide_cache = wide(kv->k) && wide(kv->v);
   a.eps = cfg->rms_eps;
   a.status = static_cast<int*>(scratch);
-  for (uint32_t i = 0; i < a.R / 2; ++i)  // theta^(-2i/R) in double, kept fp32, as in the layer forwards
-    a.inv_freq[i] = (float)std::pow((double)cfg->rope_theta, -2.0 * (double)i / (double)a.R);
+  // theta^(-2i/R) in double, kept fp32, as in the layer forwards; a thread keeps its last configuration's (64 powers: 2 us)
+  static thread_local struct {
+    float theta = 0.f, inv_freq[128];
+    uint32_t R = 0;
+  } table;
+  if (table.theta != cfg->rope_theta || table.R != a.R) {
+    for (uint32_t i = 0; i < a.R / 2; ++i)
+      table.inv_freq[i] = (float)std::pow((double)cfg->rope_theta, -2.0 * (double)i / (double)a.R);
+    table.theta = cfg->rope_theta;
+    table.R = a.R;
+  }
+  std::copy(table.inv_freq, table.inv_freq + a.R / 2, a.inv_freq);
   r = cu(q35c::rope_append(a, (cudaStream_t)stream));
   if (r || !bounds) return r;
   // with bounds the rotated keys go on through the append that keeps them

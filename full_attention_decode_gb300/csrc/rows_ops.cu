@@ -15,119 +15,182 @@ constexpr uint32_t kThreads = 256;
 
 // ------------------------------------------------------------------ rotated append
 
-// Eight of the sixteen values of a group, the others in the neighbouring lane, as quant16 does it.
-__device__ __forceinline__ uint2 quant8(const uint32_t (&w)[4], uint16_t& scale) {
-  __nv_bfloat162 m = __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[0]));
-#pragma unroll
-  for (int i = 1; i < 4; ++i) m = __hmax2(m, __habs2(*reinterpret_cast<const __nv_bfloat162*>(&w[i])));
-  float amax = fmaxf(fmaxf(__low2float(m), __high2float(m)), 0.f);
-  amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-  scale = to_bf16(amax * (1.0f / 448.0f));
-  const float sc = bf16f(scale);
-  uint32_t c[4] = {0u, 0u, 0u, 0u};
-  if (sc > 1e-30f && sc < 1e30f) {
-    float r;
-    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(sc));
-    const float2 r2 = make_float2(r, r), s2 = make_float2(-sc, -sc);
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const float2 x = make_float2(bf16lo(w[i]), bf16hi(w[i]));
-      float2 q = __fmul2_rn(x, r2);
-      q = __ffma2_rn(__ffma2_rn(q, s2, x), r2, q);
-      c[i] = e4m3_pair(q.x, q.y);
-    }
-  } else if (sc != 0.f) {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) c[i] = e4m3_pair(bf16lo(w[i]) / sc, bf16hi(w[i]) / sc);
-  }
-  return make_uint2(c[0] | (c[1] << 16), c[2] | (c[3] << 16));
-}
-
-// bf16(RMSNorm(x) w) of a head's row, eight dims a lane, then RoPE on its first R dims in halves: dim i < R / 2
-// turns with dim i + R / 2 by the angle whose (cos, sin) is cs[i]. swap: a row in shared memory, for the other half's
-// values. The roundings are the layer forwards'.
-template <int LPR>
-__device__ __forceinline__ void norm_rotate(float (&x)[8], const uint16_t* w, const float2* cs, float* swap, uint32_t l,
+// bf16(RMSNorm(x) w) of a head's row (wht_quad's layout: four lanes, pieces of sixteen dims in pairs), then RoPE on its first R
+// dims in halves: dim i < R / 2 turns with dim i + R / 2 by the angle whose (cos, sin) is cs[i]. The other half's
+// values are bf16 by then and come through the team's row of shared memory. The roundings are the layer forwards'.
+template <int D>
+__device__ __forceinline__ void norm_rotate(float2 (&x)[D / 8], const uint16_t* w, const float2* cs, uint16_t* swap, uint32_t l,
                                             uint32_t R, float eps) {
-  float s = 0.f;
+  constexpr int P = D / 64;
+  float2 s2 = make_float2(0.f, 0.f);
 #pragma unroll
-  for (int e = 0; e < 8; ++e) s = fmaf(x[e], x[e], s);
+  for (int k = 0; k < D / 8; ++k) s2 = __ffma2_rn(x[k], x[k], s2);
+  float s = s2.x + s2.y;
+  s += __shfl_xor_sync(0xffffffffu, s, 1);
+  s += __shfl_xor_sync(0xffffffffu, s, 2);
+  if (w) {  // null for a row that is not normed: teams of a warp differ
+    const float inv = rsqrtf(s / (float)D + eps);
 #pragma unroll
-  for (uint32_t m = 1; m < LPR; m <<= 1) s += __shfl_xor_sync(0xffffffffu, s, m);
-  if (w) {  // null for a row that is not normed: teams of one warp differ
-    float g[8];
-    unpack8(*reinterpret_cast<const uint4*>(w + 8 * l), g);
-    const float inv = rsqrtf(s / (float)(8 * LPR) + eps);
+    for (int i = 0; i < P; ++i) {
+      const uint4* g4 = reinterpret_cast<const uint4*>(w + 64 * i + 16 * l);
+      const uint4 ga = g4[0], gb = g4[1];
+      const uint32_t g[8] = {ga.x, ga.y, ga.z, ga.w, gb.x, gb.y, gb.z, gb.w};
 #pragma unroll
-    for (int e = 0; e < 8; ++e) x[e] = round_bf16(x[e] * inv * g[e]);
+      for (int k = 0; k < 8; ++k) {
+        float2& v = x[8 * i + k];
+        v = make_float2(round_bf16(v.x * inv * bf16lo(g[k])), round_bf16(v.y * inv * bf16hi(g[k])));
+      }
+    }
   }
   const uint32_t half = R / 2;
-  if (8 * l < R)
 #pragma unroll
-    for (int e = 0; e < 8; ++e) swap[8 * l + e] = x[e];
-  __syncwarp();
+  for (int i = 0; i < P; ++i) {
+    const uint32_t d0 = 64 * i + 16 * l;
+    if (d0 < R) {
+      uint32_t u[8];
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const uint32_t d = 8 * l + e;
-    if (d < R) {
-      const float2 c = cs[d < half ? d : d - half];
-      x[e] = round_bf16(d < half ? x[e] * c.x - swap[d + half] * c.y : x[e] * c.x + swap[d - half] * c.y);
+      for (int k = 0; k < 8; ++k) {
+        const __nv_bfloat162 q = __float22bfloat162_rn(x[8 * i + k]);
+        u[k] = *reinterpret_cast<const uint32_t*>(&q);
+      }
+      reinterpret_cast<uint4*>(swap + d0)[0] = make_uint4(u[0], u[1], u[2], u[3]);
+      reinterpret_cast<uint4*>(swap + d0)[1] = make_uint4(u[4], u[5], u[6], u[7]);
     }
   }
   __syncwarp();
+#pragma unroll
+  for (int i = 0; i < P; ++i)
+#pragma unroll
+    for (int h = 0; h < 2; ++h) {
+      const uint32_t d = 64 * i + 16 * l + 8 * h;
+      float2* v = x + 8 * i + 4 * h;
+      if (d < R && half % 8 == 0) {  // eight dims on one side, their partners side by side
+        const bool low = d < half;
+        const uint32_t first = low ? d : d - half;
+        const float4* c4 = reinterpret_cast<const float4*>(cs + first);
+        const uint4 o = *reinterpret_cast<const uint4*>(swap + (low ? d + half : first));
+        const uint32_t other[4] = {o.x, o.y, o.z, o.w};
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          const float4 c = c4[k];  // cos, sin of two dims
+          const float a = low ? -c.y : c.y, b = low ? -c.w : c.w;
+          v[k] = make_float2(round_bf16(v[k].x * c.x + bf16lo(other[k]) * a), round_bf16(v[k].y * c.z + bf16hi(other[k]) * b));
+        }
+      } else if (d < R) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          float& y = e & 1 ? v[e / 2].y : v[e / 2].x;
+          if (d + e < half) y = round_bf16(y * cs[d + e].x - bf16f(swap[d + e + half]) * cs[d + e].y);
+          else if (d + e < R) y = round_bf16(y * cs[d + e - half].x + bf16f(swap[d + e - half]) * cs[d + e - half].y);
+        }
+      }
+    }
+  __syncwarp();
 }
 
-// A CTA takes a row: the angles once for all heads, then a team of D / 8 lanes a head's row, q-heads, then k, then v.
+constexpr uint32_t kTeams = kThreads / 4;
+constexpr uint32_t kRopeRows = 8;  // rows of a CTA at most
+
+// A CTA takes a few rows: their places and angles once for all heads, then four lanes a head's row, q-heads, then k, then v.
+// Bound by the instructions of norm, rotation and quantiser where there are many rows, by the chain of loads of the place where
+// there are few.
 template <int D, bool T8>
-__global__ void __launch_bounds__(kThreads) rope_kernel(const __grid_constant__ RopeAppend a) {
-  constexpr uint32_t LPR = D / 8, TEAMS = kThreads / LPR;
-  __shared__ float2 cs[D / 2];
-  __shared__ float swap[TEAMS][D];
-  const uint32_t r = blockIdx.x, l = threadIdx.x % LPR, team = threadIdx.x / LPR, lane = threadIdx.x & 31;
+__global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ RopeAppend a, uint32_t rows) {
+  constexpr int P = D / 64;
+  __shared__ __align__(16) float2 cs[kRopeRows][D / 2];
+  __shared__ __align__(16) uint16_t swap[kTeams][D + 8];
+  __shared__ size_t place[kRopeRows];
+  __shared__ int32_t turn[kRopeRows];
+  __shared__ bool ok[kRopeRows];
+  const uint32_t r0 = blockIdx.x * rows, tid = threadIdx.x, l = tid & 3, team = tid / 4, lane = tid & 31;
   pdl_wait();
   pdl_launch();
-  uint32_t seq, pos;
-  size_t row = 0;
-  const RowKind kind = locate(a.r, a.c.capacity, r, seq, pos);
-  const bool ok = kind == kRowOk && cache_row(a.c, seq, pos, row);
-  if (!ok) {
-    if (kind != kRowSkip && threadIdx.x == 0) set_status(a.status, kStatusRange);
-    return;
-  }
-  const int32_t p = a.rope_pos ? a.rope_pos[r] : (int32_t)pos;
-  for (uint32_t i = threadIdx.x; i < a.R / 2; i += kThreads) {
-    float sn, c;
-    sincosf((float)p * a.inv_freq[i], &sn, &c);
-    cs[i] = make_float2(c, sn);
+  const uint32_t nq = a.q ? a.H : 0, slots = nq + 2 * a.c.Hkv, items = min(rows, a.r.n_rows - r0) * slots;
+  uint32_t u[P][8];
+  const uint16_t* w = nullptr;
+  uint32_t r = 0, slot = 0, g = 0;
+  bool is_q = false, is_v = false, in = false;
+  const auto fetch = [&](uint32_t item) {
+    in = item < items;
+    r = in ? item / slots : 0;
+    slot = in ? item % slots : 0;
+    is_q = slot < nq;
+    is_v = slot >= nq + a.c.Hkv;
+    g = is_q ? slot : is_v ? slot - nq - a.c.Hkv : slot - nq;
+    w = is_q ? a.q_norm : is_v ? nullptr : a.k_norm;
+    const size_t row = r0 + r;
+    const uint16_t* src = is_q ? a.q + (row * a.H + g) * a.q_stride : (is_v ? a.v : a.k) + (row * a.c.Hkv + g) * D;
+    const bool wide = is_q ? a.wide_q : a.wide_kv;
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+      if (in) load32(src + 64 * i + 16 * l, wide, u[i]);
+  };
+  fetch(team);  // on their way while the places are looked up
+  if (tid < min(rows, a.r.n_rows - r0)) {
+    uint32_t seq, pos;
+    size_t row = 0;
+    const RowKind kind = locate(a.r, a.c.capacity, r0 + tid, seq, pos);
+    ok[tid] = kind == kRowOk && cache_row(a.c, seq, pos, row);
+    if (!ok[tid] && kind != kRowSkip) set_status(a.status, kStatusRange);
+    place[tid] = row;
+    turn[tid] = !ok[tid] ? 0 : a.rope_pos ? a.rope_pos[r0 + tid] : (int32_t)pos;
   }
   __syncthreads();
-  const uint32_t nq = a.q ? a.H : 0, slots = nq + 2 * a.c.Hkv;
-  for (uint32_t s0 = 0; s0 < slots; s0 += TEAMS) {
-    const uint32_t s = s0 + team;
-    const bool in = s < slots, is_q = s < nq, is_v = s >= nq + a.c.Hkv;
-    const uint32_t g = is_q ? s : is_v ? s - nq - a.c.Hkv : s - nq;
-    const uint16_t* src = is_q ? a.q + ((size_t)r * a.H + g) * a.q_stride : (is_v ? a.v : a.k) + ((size_t)r * a.c.Hkv + g) * D;
-    float x[8] = {};
-    if (in) unpack8(*reinterpret_cast<const uint4*>(src + 8 * l), x);
-    const bool turns = in && !is_v;
-    norm_rotate<LPR>(x, !turns ? nullptr : is_q ? a.q_norm : a.k_norm, cs, swap[team], l, turns ? a.R : 0, a.eps);
-    if (in && is_q) *reinterpret_cast<uint4*>(a.q_out + ((size_t)r * a.H + g) * D + 8 * l) = pack8(x);
-    if (in && !is_q && !is_v && a.k_out)
-      *reinterpret_cast<uint4*>(a.k_out + ((size_t)r * a.c.Hkv + g) * D + 8 * l) = pack8(x);
-    if (!a.to_cache) continue;
-    const size_t at = (row * a.c.Hkv + g) * D + 8 * l;
-    if constexpr (T8) {
-      wht8<LPR>(x, lane);
-      const uint4 u = pack8(x);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-      uint16_t sc;
-      const uint2 codes = quant8(w, sc);
-      if (in && !is_q) {
-        *reinterpret_cast<uint2*>((is_v ? a.c.v : a.c.k) + at) = codes;
-        if (l % 2 == 0) (is_v ? a.c.vs : a.c.ks)[row * a.c.sstride + g * (D / 16) + l / 2] = sc;
+  const uint32_t half = a.R / 2;
+  for (uint32_t i = tid; i < min(rows, a.r.n_rows - r0) * half; i += kThreads) {
+    float sn, c;
+    sincosf((float)turn[i / half] * a.inv_freq[i % half], &sn, &c);
+    cs[i / half][i % half] = make_float2(c, sn);
+  }
+  __syncthreads();
+  for (uint32_t item = team; item - team < items; item += kTeams) {  // whole CTAs
+    if (item != team) fetch(item);
+    float2 x[D / 8];
+#pragma unroll
+    for (int i = 0; i < P; ++i)
+#pragma unroll
+      for (int k = 0; k < 8; ++k) x[8 * i + k] = in ? make_float2(bf16lo(u[i][k]), bf16hi(u[i][k])) : make_float2(0.f, 0.f);
+    const bool go = in && ok[r];
+    norm_rotate<D>(x, in ? w : nullptr, cs[r], swap[team], l, in && !is_v ? a.R : 0, a.eps);
+    const size_t row = r0 + r;
+    const auto store = [&](uint16_t* to, bool wide) {
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        uint32_t y[8];
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const __nv_bfloat162 q = __float22bfloat162_rn(x[8 * i + k]);
+          y[k] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        store32(to + 64 * i + 16 * l, wide, y);
       }
-    } else if (in && !is_q) {
-      *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + at) = pack8(x);
+    };
+    if (go && is_q) store(a.q_out + (row * a.H + g) * D, a.wide_out);
+    if (go && !is_q && !is_v && a.k_out) store(a.k_out + (row * a.c.Hkv + g) * D, a.wide_out);
+    if (!a.to_cache) continue;
+    const size_t at = go ? (place[r] * a.c.Hkv + g) * D : 0;
+    if constexpr (T8) {
+      if (__all_sync(0xffffffffu, !go || is_q)) continue;
+      wht_quad<D>(x, lane);
+      uint32_t* sc = reinterpret_cast<uint32_t*>((is_v ? a.c.vs : a.c.ks) + (go ? place[r] : 0) * a.c.sstride + (go && !is_q ? g : 0) * (D / 16));
+#pragma unroll
+      for (int i = 0; i < P; ++i) {
+        uint32_t y[8];
+        uint16_t s;
+#pragma unroll
+        for (int k = 0; k < 8; ++k) {
+          const __nv_bfloat162 q = __float22bfloat162_rn(x[8 * i + k]);
+          y[k] = *reinterpret_cast<const uint32_t*>(&q);
+        }
+        const uint4 codes = quant16(y, s);
+        const uint32_t two = s | (uint32_t)__shfl_xor_sync(0xffffffffu, (uint32_t)s, 1) << 16;  // two groups' scales as one word
+        if (go && !is_q) {
+          *reinterpret_cast<uint4*>((is_v ? a.c.v : a.c.k) + at + 64 * i + 16 * l) = codes;
+          if (l % 2 == 0) sc[2 * i + l / 2] = two;
+        }
+      }
+    } else if (go && !is_q) {
+      store(reinterpret_cast<uint16_t*>(is_v ? a.c.v : a.c.k) + at, a.wide_cache);
     }
   }
 }
@@ -210,9 +273,12 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const __grid_constant__ 
 
 cudaError_t rope_append(const RopeAppend& a, cudaStream_t st) {
   const bool t8 = a.c.ks != nullptr;
-#define CALL(DD)                                                                                       \
-  return t8 ? launch_early(rope_kernel<DD, true>, dim3(a.r.n_rows), kThreads, 0, st, a)                \
-            : launch_early(rope_kernel<DD, false>, dim3(a.r.n_rows), kThreads, 0, st, a)
+  // a row a CTA until the GPU is full, then more, which share the places' latency
+  const uint32_t rows = std::min(std::max(a.r.n_rows / 304, 1u), kRopeRows);
+  const dim3 grid((a.r.n_rows + rows - 1) / rows);
+#define CALL(DD)                                                                         \
+  return t8 ? launch_early(rope_kernel<DD, true>, grid, kThreads, 0, st, a, rows)        \
+            : launch_early(rope_kernel<DD, false>, grid, kThreads, 0, st, a, rows)
   switch (a.c.D) {
     case 64: CALL(64);
     case 128: CALL(128);

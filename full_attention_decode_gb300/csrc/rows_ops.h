@@ -24,6 +24,7 @@ struct RopeAppend {
   uint16_t* k_out;  // [n_rows][Hkv][D], or null
   uint32_t H, q_stride, R;
   bool to_cache;  // else q_out and k_out alone
+  bool wide_q, wide_kv, wide_out, wide_cache;  // rows are 32-byte aligned
   float eps;
   int* status;
   float inv_freq[128];
@@ -71,8 +72,7 @@ struct Sample {
   uint32_t n_rows, vocab;
   uint64_t row_stride;
 };
-constexpr uint32_t kSampleCtas = 8;                       // of a row
-constexpr uint32_t kMaxVocab = kSampleCtas * 65520;       // counts of a CTA's part fit 16 bits
+constexpr uint32_t kMaxVocab = 8 * 65520;  // eight CTAs a row at most; counts of a CTA's part fit 16 bits
 constexpr uint32_t kMaxSampleRows = 65536;
 cudaError_t sample(const Sample& a, cudaStream_t st);
 cudaError_t sample_attributes();  // once per device, before the first sample

@@ -3,11 +3,13 @@
 // bf16 logits take at most 2^16 values, so a row is a histogram: counts are whole numbers, a token's weight
 // 2^-y, y = (largest - logit) log2(e) / temperature, is that of its value, and the cuts of top-k, top-p and
 // min-p are places in the line of values from the largest down, with the lower indexes of equal ones first. Weights
-// are whole multiples of 2^-44 (2^-48 accurate before that rounding), so every sum of them is exact and the same in any
-// order: what is chosen is what 64-bit arithmetic chooses.
+// are whole multiples of 2^-44 (2^-40 of themselves accurate before that rounding), so every sum of them is exact and the
+// same in any order. No sort: the 64-bit pipe and the order of sums stay out of it.
 //
-// A row is taken by a cluster of kSampleCtas CTAs, each with a part of the tokens: its own histogram in shared memory
-// (16-bit counts), read by all through distributed shared memory: a CTA adds up an equal part of the values.
+// A row is taken by a cluster of CTAs, each with a part of the tokens and a histogram of it in shared memory (16-bit counts).
+// The values come in runs of 128 (a sign and an exponent). Each CTA weighs its own part run by run; all read all runs'
+// sums through distributed shared memory, so all know where the cuts lie without asking; the run that a cut lies in is
+// then added up value by value. Bound by the shared-memory additions of the counting and a chain of reads and barriers.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -20,13 +22,14 @@ using namespace q35;
 namespace cg = cooperative_groups;
 namespace {
 
-constexpr uint32_t kThreads = 512;
-constexpr uint32_t kKeyCount = 65536, kBins = kKeyCount / kSampleCtas;  // values of a CTA at most
-constexpr uint32_t kSmem = kKeyCount * 2 + kBins * (4 + 8);
+constexpr uint32_t kThreads = 1024;
+constexpr uint32_t kKeyCount = 65536, kRun = 128, kRuns = kKeyCount / kRun;
+constexpr uint32_t kSmem = kKeyCount * 2;
 constexpr int kOne = 44;  // the largest weight is 2^kOne: kMaxVocab < 2^19 of them fit 64 bits
+typedef unsigned long long u64;
 
 struct Table {
-  unsigned long long t[64];  // 2^63 2^(-i / 64)
+  u64 t[64];  // 2^63 2^(-i / 64)
 };
 struct Args {
   Sample s;
@@ -43,73 +46,128 @@ __device__ __forceinline__ float key_value(uint32_t k) {
 }
 __device__ __forceinline__ bool is_nan(uint32_t u) { return (u & 0x7fffu) > 0x7f80u; }
 
-// 2^-y as m 2^-(63 + n), m to 2^-48: n whole, 2^(-i / 64) from the table, e^-z for the rest z < 2^-6 ln 2 by its
+// How a row weighs its values. y = (largest - value) rate in two 32-bit numbers each (TwoSum, Knuth, and products with
+// their errors by fma): 2^-46 of it; values and rate over and times two, so that no difference overflows.
+struct Scale {
+  float half_largest, rate, rate_low;  // rate: 2 log2(e) / temperature
+  uint32_t most;                       // the largest value's key
+};
+__device__ __forceinline__ Scale scale_of(uint32_t most, float temperature) {
+  Scale c;
+  c.most = most;
+  c.half_largest = 0.5f * key_value(most);
+  constexpr float kHi = 2.88539004f, kLo = 3.8519259822532e-08f;  // 2 log2(e)
+  c.rate = c.rate_low = 0.f;
+  if (temperature > 0.f && temperature < INFINITY) {
+    c.rate = kHi / temperature;
+    c.rate_low = (fmaf(-c.rate, temperature, kHi) + kLo) / temperature;
+    if (!(fabsf(c.rate_low) < INFINITY)) c.rate_low = 0.f;
+  }
+  return c;
+}
+// 2^-y of key k's value as m 2^-(63 + n): n whole, 2^(-i / 64) from the table, e^-z for the rest z < 2^-6 ln 2 by its
 // series to z^5 / 120 (the next term is below 2^-48 of it).
-__device__ __forceinline__ unsigned long long weight(const Table& tab, double y, uint32_t& n) {
+__device__ __forceinline__ u64 weight(const Table& tab, const Scale& c, uint32_t k, uint32_t& n) {
+  const float a = c.half_largest, b = -0.5f * key_value(k), s = a + b, t = s - a;
+  const float low = (a - (s - t)) + (b - t);
+  const float y = s * c.rate;
   n = 64;
-  if (!(y < 63.0)) return 0;
-  n = (uint32_t)y;
-  const unsigned long long f = __double2ull_rd((y - (double)n) * 18446744073709551616.0);  // in 2^-64
-  constexpr unsigned long long kLn2 = 12786308645202655660ull, kAll = ~0ull;                // ln 2 in 2^-64
-  const unsigned long long z = __umul64hi(f << 6, kLn2) >> 6;
-  unsigned long long e = kAll - z / 5;
+  if (k == c.most) {
+    n = 0;
+    return 1ull << 63;
+  }
+  if (!(y < 63.f)) return 0;
+  const float err = fmaf(s, c.rate, -y) + fmaf(s, c.rate_low, low * c.rate);
+  const float whole = floorf(y);
+  long long f = (long long)__float2ull_rn((y - whole) * 9223372036854775808.f) + __float2ll_rn(err * 9223372036854775808.f);
+  int w = (int)whole;
+  if (f < 0) {  // in 2^-63, to [0, 2^63): below 0, or past it as an unsigned number
+    const bool past = y - whole > 0.5f;
+    w += past ? 1 : -1;
+    f = past ? (long long)((u64)f - (1ull << 63)) : (long long)((u64)f + (1ull << 63));
+    if (w < 0) w = 0, f = 0;
+  }
+  n = (uint32_t)w;
+  const u64 g = (u64)f << 1;                                     // in 2^-64
+  constexpr u64 kLn2 = 12786308645202655660ull, kAll = ~0ull;  // ln 2 in 2^-64
+  const u64 z = __umul64hi(g << 6, kLn2) >> 6;
+  u64 e = kAll - z / 5;
   e = kAll - __umul64hi(z / 4, e);
   e = kAll - __umul64hi(z / 3, e);
   e = kAll - __umul64hi(z / 2, e);
   e = kAll - __umul64hi(z, e);
-  return __umul64hi(tab.t[f >> 58], e);
+  return __umul64hi(tab.t[g >> 58], e);
 }
-__device__ __forceinline__ unsigned long long fixed(unsigned long long m, uint32_t n) {  // in 2^-kOne, rounded
+__device__ __forceinline__ u64 fixed(u64 m, uint32_t n) {  // in 2^-kOne, rounded
   const uint32_t s = 63 - kOne + n;
   return s > 63 ? 0 : (m + (1ull << (s - 1))) >> s;
 }
-
-// A place in the line of tokens: how many lie before it and what they weigh.
-struct Place {
-  unsigned long long weight;
-  uint32_t count;
-};
+// floor(p x), or ceil, for p in [0, 1]: exact.
+__device__ __forceinline__ u64 share(float p, u64 x, bool up) {
+  const uint32_t b = __float_as_uint(p), e = b >> 23;
+  if (!(p > 0.f)) return 0;
+  if (p >= 1.f) return x;
+  const u64 m = (b & 0x7fffffu) | (e ? 0x800000u : 0u), hi = __umul64hi(m, x), lo = m * x;
+  const uint32_t s = 150 - (e ? e : 1);  // p = m 2^-s, s >= 24
+  u64 q, rest;
+  if (s < 64) {
+    q = lo >> s | hi << (64 - s);
+    rest = lo << (64 - s);
+  } else {
+    q = s < 128 ? hi >> (s - 64) : 0;
+    rest = lo | (s < 128 ? (s > 64 ? hi << (128 - s) : 0) : hi);
+  }
+  return q + (up && rest != 0);
+}
 
 struct Shared {
-  unsigned long long warp_w[kThreads / 32];
-  uint32_t warp_c[kThreads / 32];
-  uint32_t least, most;           // this CTA's keys
-  Place total;                    // of this CTA's values
-  unsigned long long cut;         // what the kept tokens weigh (written by the CTA that finds it)
-  unsigned long long floor_w;     // this CTA's weight of values that min-p keeps
-  uint32_t key;                   // the chosen value, from the CTA that finds it
-  uint32_t nth;                   // which of its tokens
-  uint32_t token;
+  u64 run_weight[kRuns];  // of this CTA's part
+  uint32_t run_count[kRuns];
+  u64 floor_weight;       // of its values that min-p keeps
+  uint32_t least, most;
+  // from here on the same in all CTAs
+  u64 before_weight;  // of the run that is searched
+  uint32_t before_count;
+  u64 warp_w[32];
+  uint32_t warp_c[32];
+  uint32_t fine[kRun];  // the row's counts of a run's values, from its largest down
+  uint32_t run;
+  u64 place;    // what a search found
+  uint32_t key, nth;
 };
 
+template <uint32_t C>
 __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_constant__ Args g) {
   extern __shared__ __align__(16) uint8_t sm[];
   __shared__ Shared sh;
   uint32_t* hist = reinterpret_cast<uint32_t*>(sm);  // two 16-bit counts a word
-  unsigned long long* wt = reinterpret_cast<unsigned long long*>(sm + kKeyCount * 2);  // [kBins], from the largest value down
-  uint32_t* cnt = reinterpret_cast<uint32_t*>(sm + kKeyCount * 2 + kBins * 8);
   const Sample& a = g.s;
   const cg::cluster_group cl = cg::this_cluster();
-  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = cl.block_rank(), r = blockIdx.x / kSampleCtas;
+  const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = cl.block_rank(), r = blockIdx.x / C;
   for (uint32_t i = tid; i < kKeyCount * 2 / 16; i += kThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0u, 0u, 0u, 0u);
   if (tid == 0) {
     sh.least = kKeyCount;
     sh.most = 0;
+    sh.floor_weight = 0;
   }
   pdl_wait();
   pdl_launch();
+  const float temperature = a.temperature ? a.temperature[r] : 1.f;
+  const float u = a.u[r], top_p = a.top_p ? a.top_p[r] : 1.f, min_p = a.min_p ? a.min_p[r] : 0.f;
+  const bool greedy = !(temperature > 0.f);
+  const int32_t top_k = greedy ? 1 : a.top_k ? a.top_k[r] : 0;
   __syncthreads();
 
   // ---- this CTA's tokens: eights of 16 aligned bytes, `lead` of the first eight before the row's first token
   const uint16_t* x = a.logits + (size_t)r * a.row_stride;
   const uint32_t lead = (uint32_t)((uintptr_t)x / 2 % 8), eights = (lead + a.vocab + 7) / 8;
-  const uint32_t part = (eights + kSampleCtas - 1) / kSampleCtas, t0 = min(eights, me * part), t1 = min(eights, t0 + part);
+  const uint32_t part = (eights + C - 1) / C, t0 = min(eights, me * part), t1 = min(eights, t0 + part);
   // the tokens of an eight, in order
   const auto tokens = [&](uint32_t t, auto&& use) {
     const int32_t i0 = (int32_t)(8 * t) - (int32_t)lead;
     if (i0 >= 0 && (uint32_t)i0 + 8 <= a.vocab) {
-      const uint4 u = *reinterpret_cast<const uint4*>(x + i0);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      const uint4 v = *reinterpret_cast<const uint4*>(x + i0);
+      const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         use(w[i] & 0xffffu, i0 + 2 * i);
@@ -122,9 +180,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
   uint32_t least = kKeyCount, most = 0;
 #pragma unroll 4
   for (uint32_t t = t0 + tid; t < t1; t += kThreads)
-    tokens(t, [&](uint32_t u, int32_t) {
-      if (is_nan(u)) return;
-      const uint32_t k = key_of(u);
+    tokens(t, [&](uint32_t v, int32_t) {
+      if (is_nan(v)) return;
+      const uint32_t k = key_of(v);
       least = min(least, k);
       most = max(most, k);
       atomicAdd(hist + (k >> 1), k & 1 ? 65536u : 1u);
@@ -136,9 +194,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     atomicMax(&sh.most, most);
   }
   cl.sync();
-
-  // ---- the values between the row's least and largest, an equal part a CTA, from the largest down
-  for (uint32_t c = 0; c < kSampleCtas; ++c) {
+  for (uint32_t c = 0; c < C; ++c) {
     const Shared* o = cl.map_shared_rank(&sh, c);
     least = min(least, o->least);
     most = max(most, o->most);
@@ -151,204 +207,239 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     cl.sync();
     return;
   }
-  const float temperature = a.temperature ? a.temperature[r] : 1.f;
-  const bool greedy = !(temperature > 0.f);
-  const double rate = greedy ? 0.0 : 1.4426950408889634 / (double)temperature;
-  const double largest = (double)key_value(most);
-  const auto octaves = [&](uint32_t k) { return k == most ? 0.0 : (largest - (double)key_value(k)) * rate; };
-  const uint32_t n = most - least + 1, each = (n + kSampleCtas - 1) / kSampleCtas;
-  const uint32_t b0 = min(n, me * each), bins = min(n, b0 + each) - b0;  // value b of this CTA: key most - b0 - b
-  for (uint32_t b = tid; b < bins; b += kThreads) {
-    const uint32_t k = most - b0 - b;
-    uint32_t c = 0;
-#pragma unroll
-    for (uint32_t o = 0; o < kSampleCtas; ++o) c += cl.map_shared_rank(hist, o)[k >> 1] >> (k & 1 ? 16 : 0) & 0xffffu;
-    cnt[b] = c;
-    uint32_t e = 64;
-    unsigned long long m = 0;
-    if (c) m = weight(g.table, octaves(k), e);
-    wt[b] = fixed(m, e);
-  }
-  __syncthreads();
 
-  // ---- each thread a run of values: what lies before it in the row's line
-  const uint32_t run = (bins + kThreads - 1) / kThreads, v0 = min(bins, tid * run), v1 = min(bins, v0 + run);
-  const int64_t k64 = greedy ? 1 : a.top_k ? a.top_k[r] : 0;
-  const float min_p = a.min_p && a.min_p[r] > 0.f ? fminf(a.min_p[r], 1.f) : 0.f;
-  const unsigned long long floor_w = min_p > 0.f ? __double2ull_ru((double)min_p * (double)(1ull << kOne)) : 0;
-  Place mine = {0, 0};
-  unsigned long long over = 0;
-  for (uint32_t b = v0; b < v1; ++b) {
-    const unsigned long long w = wt[b] * cnt[b];
-    mine.count += cnt[b];
-    mine.weight += w;
-    if (wt[b] >= floor_w) over += w;
-  }
-  Place at = mine;  // inclusive sums of the warp
+  // ---- this CTA's part weighed: a run a warp in turn, so that full ones lie in different warps
+  const Scale scale = scale_of(most, greedy ? 0.f : temperature);
+  const u64 floor_w = min_p > 0.f ? share(fminf(min_p, 1.f), 1ull << kOne, true) : 0;
+  u64 over = 0;
+  const uint32_t run0 = least / kRun, run1 = most / kRun + 1;
+  for (uint32_t q = warp; q < kRuns; q += kThreads / 32) {
+    u64 w = 0;
+    uint32_t n = 0;
+    if (q >= run0 && q < run1) {
+      const uint32_t h[2] = {hist[q * 64 + lane], hist[q * 64 + 32 + lane]};
+      if (__any_sync(0xffffffffu, h[0] | h[1])) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const unsigned long long w = __shfl_up_sync(0xffffffffu, at.weight, o);
-    const uint32_t c = __shfl_up_sync(0xffffffffu, at.count, o);
-    if (lane >= (uint32_t)o) {
-      at.weight += w;
-      at.count += c;
+        for (int i = 0; i < 4; ++i) {
+          const uint32_t c = i & 1 ? h[i / 2] >> 16 : h[i / 2] & 0xffffu, k = q * kRun + (i / 2) * 64 + 2 * lane + (i & 1);
+          if (c) {
+            uint32_t e;
+            const u64 m = weight(g.table, scale, k, e), v = fixed(m, e);
+            w += v * c;
+            n += c;
+            if (v >= floor_w) over += v * c;
+          }
+        }
+        n = __reduce_add_sync(0xffffffffu, n);
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
+      }
+    }
+    if (lane == 0) {
+      sh.run_weight[q] = w;
+      sh.run_count[q] = n;
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) over += __shfl_xor_sync(0xffffffffu, over, o);
-  if (lane == 31) {
-    sh.warp_w[warp] = at.weight;
-    sh.warp_c[warp] = at.count;
-  }
-  if (tid == 0) sh.floor_w = 0;
-  __syncthreads();
-  if (lane == 0) atomicAdd(&sh.floor_w, over);
-  at.weight -= mine.weight;
-  at.count -= mine.count;
-  Place all = {0, 0};
-  for (uint32_t w = 0; w < kThreads / 32; ++w) {
-    if (w < warp) {
-      at.weight += sh.warp_w[w];
-      at.count += sh.warp_c[w];
-    }
-    all.weight += sh.warp_w[w];
-    all.count += sh.warp_c[w];
-  }
-  if (tid == 0) sh.total = all;
+  if (lane == 0 && over) atomicAdd(&sh.floor_weight, over);
   cl.sync();
-  Place row = {0, 0};
-  unsigned long long row_floor = 0;
-  for (uint32_t c = 0; c < kSampleCtas; ++c) {
-    const Shared* o = cl.map_shared_rank(&sh, c);
-    const Place p = o->total;
-    if (c < me) {
-      at.weight += p.weight;
-      at.count += p.count;
-    }
-    row.weight += p.weight;
-    row.count += p.count;
-    row_floor += o->floor_w;
-  }
 
-  // ---- the cuts: what the kept tokens weigh. The thread whose run holds a cut tells all CTAs.
-  const auto tell = [&](unsigned long long w) {
-    for (uint32_t c = 0; c < kSampleCtas; ++c) cl.map_shared_rank(&sh, c)->cut = w;
-  };
-  unsigned long long kept = row.weight;
-  if (k64 > 0 && k64 < (int64_t)row.count) {
-    const uint32_t k = (uint32_t)k64;
-    if (at.count < k && k <= at.count + mine.count) {
-      Place p = at;
-      for (uint32_t b = v0; b < v1; ++b) {
-        const uint32_t take = min(cnt[b], k - p.count);
-        p.weight += wt[b] * take;
-        p.count += take;
+  // ---- the row's runs, from the largest values down: thread i has run kRuns - 1 - i; what lies before each
+  u64 mine_w = 0, floor_sum = 0;
+  uint32_t mine_c = 0;
+  if (tid < kRuns) {
+    const uint32_t q = kRuns - 1 - tid;
+#pragma unroll
+    for (uint32_t c = 0; c < C; ++c) {
+      const Shared* o = cl.map_shared_rank(&sh, c);
+      mine_w += o->run_weight[q];
+      mine_c += o->run_count[q];
+    }
+  }
+#pragma unroll
+  for (uint32_t c = 0; c < C; ++c) floor_sum += cl.map_shared_rank(&sh, c)->floor_weight;
+  u64 at_w = mine_w;
+  uint32_t at_c = mine_c;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const u64 w = __shfl_up_sync(0xffffffffu, at_w, o);
+    const uint32_t c = __shfl_up_sync(0xffffffffu, at_c, o);
+    if (lane >= (uint32_t)o) {
+      at_w += w;
+      at_c += c;
+    }
+  }
+  if (lane == 31) {
+    sh.warp_w[warp] = at_w;
+    sh.warp_c[warp] = at_c;
+  }
+  __syncthreads();
+  u64 row_w = 0;
+  uint32_t row_c = 0;
+  for (uint32_t w = 0; w < kRuns / 32; ++w) {
+    if (w < warp) {
+      at_w += sh.warp_w[w];
+      at_c += sh.warp_c[w];
+    }
+    row_w += sh.warp_w[w];
+    row_c += sh.warp_c[w];
+  }
+  at_w -= mine_w;  // before this run
+  at_c -= mine_c;
+
+  // A search: the thread whose run holds the place says so, the run's counts are added up over the CTAs, and warp 0 walks its values,
+  // four a lane from the largest down: find(weight and count before the value, its weight and count, its key).
+  const auto search = [&](bool here, auto&& find) {
+    if (here) {
+      sh.run = kRuns - 1 - tid;
+      sh.before_weight = at_w;
+      sh.before_count = at_c;
+    }
+    if (tid < kRun) sh.fine[tid] = 0;
+    __syncthreads();
+    const uint32_t q = sh.run;
+    if (tid < 64 * C) {
+      const uint32_t h = cl.map_shared_rank(hist, tid / 64)[q * 64 + tid % 64], k = 2 * (tid % 64);
+      if (h & 0xffffu) atomicAdd(&sh.fine[kRun - 1 - k], h & 0xffffu);
+      if (h >> 16) atomicAdd(&sh.fine[kRun - 2 - k], h >> 16);
+    }
+    __syncthreads();
+    if (warp == 0) {
+      u64 w[4], sum = 0;
+      uint32_t c[4], n = 0;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        c[i] = sh.fine[4 * lane + i];
+        w[i] = 0;
+        if (c[i]) {
+          uint32_t e;
+          const u64 m = weight(g.table, scale, q * kRun + kRun - 1 - (4 * lane + i), e);
+          w[i] = fixed(m, e);
+        }
+        sum += w[i] * c[i];
+        n += c[i];
       }
-      tell(p.weight);
+      u64 bw = sum;
+      uint32_t bc = n;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const u64 y = __shfl_up_sync(0xffffffffu, bw, o);
+        const uint32_t z = __shfl_up_sync(0xffffffffu, bc, o);
+        if (lane >= (uint32_t)o) {
+          bw += y;
+          bc += z;
+        }
+      }
+      bw += sh.before_weight - sum;
+      bc += sh.before_count - n;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        find(bw, bc, w[i], c[i], q * kRun + kRun - 1 - (4 * lane + i));
+        bw += w[i] * c[i];
+        bc += c[i];
+      }
     }
-    cl.sync();
-    kept = sh.cut;
-    cl.sync();
+    __syncthreads();
+  };
+
+  // ---- the cuts: what the kept tokens weigh
+  u64 kept = row_w;
+  if (top_k > 0 && (uint32_t)top_k < row_c) {
+    const uint32_t k = (uint32_t)top_k;
+    search(at_c < k && k <= at_c + mine_c, [&](u64 bw, uint32_t bc, u64 w, uint32_t c, uint32_t) {
+      if (bc < k && k <= bc + c) sh.place = bw + w * (k - bc);
+    });
+    kept = sh.place;
   }
-  const float top_p = a.top_p ? a.top_p[r] : 1.f;
   if (top_p < 1.f) {
-    // tokens with less than `limit` before them, the first always
-    const double limit = fmax((double)top_p, 0.0) * (double)kept;
-    const unsigned long long need = max(1ull, __double2ull_ru(limit));  // the least sum that is not below the limit
-    if (at.weight < need && need <= at.weight + mine.weight) {
-      unsigned long long p = at.weight;
-      for (uint32_t b = v0; b < v1 && p < need; ++b)
-        if (cnt[b] && wt[b]) p += wt[b] * min((unsigned long long)cnt[b], (need - p + wt[b] - 1) / wt[b]);
-      tell(p);
-    }
-    cl.sync();
-    kept = min(kept, sh.cut);
-    cl.sync();
+    // tokens with less than top_p of the sum before them, the first always: the least sum that is not below it
+    const u64 need = max(1ull, share(top_p, kept, true));
+    search(at_w < need && need <= at_w + mine_w, [&](u64 bw, uint32_t, u64 w, uint32_t c, uint32_t) {
+      if (bw < need && need <= bw + w * c) sh.place = bw + w * ((need - bw + w - 1) / w);
+    });
+    kept = min(kept, sh.place);
   }
-  kept = min(kept, row_floor);
+  kept = min(kept, floor_sum);
 
   // ---- the token with u of that before it
-  const float u = a.u[r];
-  unsigned long long goal = u > 0.f ? __double2ull_rd((double)u * (double)kept) : 0;
-  goal = min(goal, kept - 1);
-  if (at.weight <= goal && goal < at.weight + mine.weight) {
-    unsigned long long p = at.weight;
-    uint32_t b = v0;
-    while (goal - p >= wt[b] * cnt[b]) p += wt[b] * cnt[b], ++b;
-    const uint32_t key = most - b0 - b, nth = (uint32_t)((goal - p) / wt[b]);
-    for (uint32_t c = 0; c < kSampleCtas; ++c) {
-      Shared* o = cl.map_shared_rank(&sh, c);
-      o->key = key;
-      o->nth = nth;
+  const u64 goal = min(share(u, kept, false), kept - 1);
+  search(at_w <= goal && goal < at_w + mine_w, [&](u64 bw, uint32_t, u64 w, uint32_t c, uint32_t key) {
+    if (bw <= goal && goal < bw + w * c) {
+      sh.key = key;
+      sh.nth = (uint32_t)((goal - bw) / w);
+      if (a.prob && me == 0) {
+        uint32_t e;
+        const u64 m = weight(g.table, scale, key, e);
+        a.prob[r] = ldexpf((float)m, kOne - 63 - (int)e) / (float)kept;
+      }
     }
-    if (a.prob) {
-      uint32_t e;
-      const unsigned long long m = weight(g.table, octaves(key), e);
-      a.prob[r] = ldexpf((float)m, kOne - 63 - (int)e) / (float)kept;
-    }
-  }
-  cl.sync();
+  });
   // ---- its index: the nth token of that value, in the CTA that holds it
   const uint32_t key = sh.key;
-  uint32_t nth = sh.nth, here = 0;
+  uint32_t nth = sh.nth, before = 0, here = 0;
   for (uint32_t c = 0; c <= me; ++c) {
+    before += here;
     here = cl.map_shared_rank(hist, c)[key >> 1] >> (key & 1 ? 16 : 0) & 0xffffu;
-    if (c < me) {
-      if (nth < here) here = kKeyCount;  // an earlier CTA's
-      if (here == kKeyCount) break;
-      nth -= here;
-    }
   }
-  if (here != kKeyCount && nth < here) {
+  if (before <= nth && nth < before + here) {
+    nth -= before;
     const uint32_t per = (part + kThreads - 1) / kThreads;  // eights of a thread, in order
     const uint32_t e0 = min(t1, t0 + tid * per), e1 = min(t1, e0 + per);
     uint32_t found = 0;
-    for (uint32_t t = e0; t < e1; ++t) tokens(t, [&](uint32_t u, int32_t) { found += !is_nan(u) && key_of(u) == key; });
-    uint32_t before = found;
+    for (uint32_t t = e0; t < e1; ++t) tokens(t, [&](uint32_t v, int32_t) { found += !is_nan(v) && key_of(v) == key; });
+    uint32_t ahead = found;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, before, o);
-      if (lane >= (uint32_t)o) before += y;
+      const uint32_t y = __shfl_up_sync(0xffffffffu, ahead, o);
+      if (lane >= (uint32_t)o) ahead += y;
     }
-    if (lane == 31) sh.warp_c[warp] = before;
+    if (lane == 31) sh.warp_c[warp] = ahead;
     __syncthreads();
-    before -= found;
-    for (uint32_t w = 0; w < warp; ++w) before += sh.warp_c[w];
-    if (before <= nth && nth < before + found)
+    ahead -= found;
+    for (uint32_t w = 0; w < warp; ++w) ahead += sh.warp_c[w];
+    if (ahead <= nth && nth < ahead + found)
       for (uint32_t t = e0; t < e1; ++t)
-        tokens(t, [&](uint32_t u, int32_t i) {
-          if (!is_nan(u) && key_of(u) == key && before++ == nth) a.token[r] = i;
+        tokens(t, [&](uint32_t v, int32_t i) {
+          if (!is_nan(v) && key_of(v) == key && ahead++ == nth) a.token[r] = i;
         });
   }
   cl.sync();  // no CTA leaves while another reads its counts
 }
 
-}  // namespace
-
-cudaError_t sample_attributes() {
-  return cudaFuncSetAttribute(sample_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
-}
-
-cudaError_t sample(const Sample& s, cudaStream_t st) {
-  static const Table table = [] {
-    Table t;
-    for (int i = 0; i < 64; ++i) t.t[i] = (unsigned long long)std::ldexp(std::exp2(-i / 64.0), 63);
-    return t;
-  }();
+template <uint32_t C>
+cudaError_t launch(const Args& g, cudaStream_t st) {
   cudaLaunchConfig_t c = {};
-  c.gridDim = dim3(s.n_rows * kSampleCtas);
+  c.gridDim = dim3(g.s.n_rows * C);
   c.blockDim = dim3(kThreads);
   c.dynamicSmemBytes = kSmem;
   c.stream = st;
   cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = kSampleCtas;
+  at[0].val.clusterDim.x = C;
   at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
   at[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[1].val.programmaticStreamSerializationAllowed = 1;
   c.attrs = at;
   c.numAttrs = 2;
-  return cudaLaunchKernelEx(&c, sample_kernel, Args{s, table});
+  return cudaLaunchKernelEx(&c, sample_kernel<C>, g);
+}
+
+}  // namespace
+
+cudaError_t sample_attributes() {
+  const cudaError_t e = cudaFuncSetAttribute(sample_kernel<8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+  return e != cudaSuccess ? e : cudaFuncSetAttribute(sample_kernel<4>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmem);
+}
+
+cudaError_t sample(const Sample& s, cudaStream_t st) {
+  static const Table table = [] {
+    Table t;
+    for (int i = 0; i < 64; ++i) t.t[i] = (u64)std::ldexp(std::exp2(-i / 64.0), 63);
+    return t;
+  }();
+  // Eight CTAs a row while all rows run at once, or where four could not count the tokens in 16 bits; otherwise four.
+  return s.n_rows <= 16 || s.vocab > 4 * (kMaxVocab / 8) ? launch<8>({s, table}, st) : launch<4>({s, table}, st);
 }
 
 }  // namespace q35c
