@@ -7,12 +7,14 @@
 // same in any order. No sort: the 64-bit pipe and the order of sums stay out of it.
 //
 // A row is taken by a cluster of CTAs, each with a part of the tokens and a histogram of it in shared memory (16-bit counts).
-// The values come in runs of 128 (a sign and an exponent). Each CTA weighs its own part run by run; all read all runs'
-// sums through distributed shared memory, so all know where the cuts lie without asking; the run that a cut lies in is
-// then added up value by value. Bound by the shared-memory additions of the counting and a chain of reads and barriers.
+// The values come in runs of 128 (a sign and an exponent). Each run that holds a token is added up over the CTAs, through
+// distributed shared memory, and weighed by one of them; all read all runs' sums, so all know where the cuts lie without
+// asking; the run that a cut lies in is then added up again value by value. Bound by the shared-memory additions of the counting
+// and a chain of reads and barriers.
 #include <cooperative_groups.h>
 
 #include <cmath>
+#include <utility>
 
 #include "common.cuh"
 #include "rows_ops.h"
@@ -120,17 +122,26 @@ __device__ __forceinline__ u64 share(float p, u64 x, bool up) {
   return q + (up && rest != 0);
 }
 
+// What other CTAs need is pushed to them: a store into another CTA's shared memory waits for nothing, a load takes a microsecond.
 struct Shared {
-  u64 run_weight[kRuns];  // of this CTA's part
+  u64 mine_weight[kRuns];  // of the runs that are this CTA's (run % CTAs)
+  uint32_t mine_count[kRuns];
+  uint32_t used[kRuns];  // runs of this CTA that hold a token in any
+  uint32_t list[kRuns], listed;  // those, in no order
+  u64 mine_floor;        // of those runs' values that min-p keeps
+  uint32_t found[kRuns]; // runs that hold a token of this CTA
+  uint32_t word[8 * kRun / 2];  // each CTA's counts of the run that was searched last
+  // the row's, written by all CTAs
+  u64 run_weight[kRuns];
   uint32_t run_count[kRuns];
-  u64 floor_weight;       // of its values that min-p keeps
+  u64 floor_weight;
   uint32_t least, most;
-  // from here on the same in all CTAs
   u64 before_weight;  // of the run that is searched
   uint32_t before_count;
   u64 warp_w[32];
   uint32_t warp_c[32];
   uint32_t fine[kRun];  // the row's counts of a run's values, from its largest down
+  u64 fine_w[kRun];     // and their weights
   uint32_t run;
   u64 place;    // what a search found
   uint32_t key, nth;
@@ -145,11 +156,18 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
   const cg::cluster_group cl = cg::this_cluster();
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, me = cl.block_rank(), r = blockIdx.x / C;
   for (uint32_t i = tid; i < kKeyCount * 2 / 16; i += kThreads) reinterpret_cast<uint4*>(sm)[i] = make_uint4(0u, 0u, 0u, 0u);
+  if (tid < kRuns) {
+    sh.mine_weight[tid] = sh.run_weight[tid] = 0;
+    sh.mine_count[tid] = sh.run_count[tid] = 0;
+    sh.used[tid] = sh.found[tid] = 0;
+  }
   if (tid == 0) {
     sh.least = kKeyCount;
     sh.most = 0;
-    sh.floor_weight = 0;
+    sh.mine_floor = sh.floor_weight = 0;
+    sh.listed = 0;
   }
+  auto begun = cl.barrier_arrive();  // the other CTAs may write here
   pdl_wait();
   pdl_launch();
   const float temperature = a.temperature ? a.temperature[r] : 1.f;
@@ -178,87 +196,129 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     }
   };
   uint32_t least = kKeyCount, most = 0;
-#pragma unroll 4
-  for (uint32_t t = t0 + tid; t < t1; t += kThreads)
-    tokens(t, [&](uint32_t v, int32_t) {
-      if (is_nan(v)) return;
-      const uint32_t k = key_of(v);
-      least = min(least, k);
-      most = max(most, k);
-      atomicAdd(hist + (k >> 1), k & 1 ? 65536u : 1u);
-    });
+  const auto add = [&](uint32_t k) { atomicAdd(hist + (k >> 1), k & 1 ? 65536u : 1u); };
+  constexpr uint32_t kAhead = 4;  // eights of a thread in flight
+  for (uint32_t b = t0 + tid; b < t1; b += kAhead * kThreads) {
+    uint4 v[kAhead];
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i) {
+      const uint32_t t = b + i * kThreads;
+      const int32_t i0 = (int32_t)(8 * t) - (int32_t)lead;
+      // an eight that is not wholly the row's, or none: zeros, which are counted one by one
+      v[i] = t < t1 && i0 >= 0 && (uint32_t)i0 + 8 <= a.vocab ? *reinterpret_cast<const uint4*>(x + i0) : make_uint4(0u, 0u, 0u, 0u);
+    }
+#pragma unroll
+    for (uint32_t i = 0; i < kAhead; ++i) {
+      const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+      uint32_t low = 0xffffffffu, high = 0;  // sizes, two a word
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        low = __vminu2(low, w[j] & 0x7fff7fffu);
+        high = __vmaxu2(high, w[j] & 0x7fff7fffu);
+      }
+      if ((low & 0xffffu) && low >> 16 && (high & 0xffffu) <= 0x7f80u && high >> 16 <= 0x7f80u) {  // no zero, no NaN: two keys at once
+        uint32_t kmin = 0xffffffffu, kmax = 0;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint32_t k2 = w[j] ^ ((w[j] >> 15 & 0x00010001u) * 0x7fffu | 0x80008000u);
+          kmin = __vminu2(kmin, k2);
+          kmax = __vmaxu2(kmax, k2);
+          add(k2 & 0xffffu);
+          add(k2 >> 16);
+        }
+        least = min(least, min(kmin & 0xffffu, kmin >> 16));
+        most = max(most, max(kmax & 0xffffu, kmax >> 16));
+      } else if (b + i * kThreads < t1) {
+        tokens(b + i * kThreads, [&](uint32_t y, int32_t) {
+          if (is_nan(y)) return;
+          const uint32_t k = key_of(y);
+          least = min(least, k);
+          most = max(most, k);
+          add(k);
+        });
+      }
+    }
+  }
   least = __reduce_min_sync(0xffffffffu, least);
   most = __reduce_max_sync(0xffffffffu, most);
-  if (lane == 0) {
-    atomicMin(&sh.least, least);
-    atomicMax(&sh.most, most);
+  cl.barrier_wait(std::move(begun));
+  if (lane < C) {  // a warp tells CTA `lane`
+    Shared* o = cl.map_shared_rank(&sh, lane);
+    atomicMin(&o->least, least);
+    atomicMax(&o->most, most);
   }
+  __syncthreads();
+  for (uint32_t i = tid; i < kKeyCount * 2 / 16; i += kThreads) {
+    const uint4 v = reinterpret_cast<const uint4*>(sm)[i];
+    if (v.x | v.y | v.z | v.w) sh.found[i * 8 / kRun] = 1;
+  }
+  __syncthreads();
+  if (tid < kRuns && sh.found[tid]) cl.map_shared_rank(&sh, tid % C)->used[tid] = 1;
   cl.sync();
-  for (uint32_t c = 0; c < C; ++c) {
-    const Shared* o = cl.map_shared_rank(&sh, c);
-    least = min(least, o->least);
-    most = max(most, o->most);
-  }
+  least = sh.least;
+  most = sh.most;
   if (least == kKeyCount) {  // no number among them
     if (me == 0 && tid == 0) {
       a.token[r] = -1;
       if (a.prob) a.prob[r] = 0.f;
     }
-    cl.sync();
-    return;
+    return;  // no CTA reads another's memory any more
   }
 
-  // ---- this CTA's part weighed: a run a warp in turn, so that full ones lie in different warps
+  // ---- this CTA's runs: half a run a warp, two values a lane
   const Scale scale = scale_of(most, greedy ? 0.f : temperature);
   const u64 floor_w = min_p > 0.f ? share(fminf(min_p, 1.f), 1ull << kOne, true) : 0;
   u64 over = 0;
-  const uint32_t run0 = least / kRun, run1 = most / kRun + 1;
-  for (uint32_t q = warp; q < kRuns; q += kThreads / 32) {
-    u64 w = 0;
-    uint32_t n = 0;
-    if (q >= run0 && q < run1) {
-      const uint32_t h[2] = {hist[q * 64 + lane], hist[q * 64 + 32 + lane]};
-      if (__any_sync(0xffffffffu, h[0] | h[1])) {
+  if (tid < kRuns && sh.used[tid]) sh.list[atomicAdd(&sh.listed, 1u)] = tid;
+  __syncthreads();
+  for (uint32_t unit = warp; unit < 2 * sh.listed; unit += kThreads / 32) {
+    const uint32_t q = sh.list[unit / 2], word = q * (kRun / 2) + unit % 2 * 32 + lane;
+    uint32_t c0 = 0, c1 = 0;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const uint32_t c = i & 1 ? h[i / 2] >> 16 : h[i / 2] & 0xffffu, k = q * kRun + (i / 2) * 64 + 2 * lane + (i & 1);
-          if (c) {
-            uint32_t e;
-            const u64 m = weight(g.table, scale, k, e), v = fixed(m, e);
-            w += v * c;
-            n += c;
-            if (v >= floor_w) over += v * c;
-          }
-        }
-        n = __reduce_add_sync(0xffffffffu, n);
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
-      }
+    for (uint32_t c = 0; c < C; ++c) {
+      const uint32_t y = cl.map_shared_rank(hist, c)[word];
+      c0 += y & 0xffffu;
+      c1 += y >> 16;
     }
+    u64 w = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < 2; ++i) {
+      const uint32_t n = i ? c1 : c0;
+      uint32_t e;
+      const u64 m = n ? weight(g.table, scale, 2 * word + i, e) : 0, y = n ? fixed(m, e) : 0;
+      w += y * n;
+      if (y >= floor_w) over += y * n;
+    }
+    const uint32_t n = __reduce_add_sync(0xffffffffu, c0 + c1);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) w += __shfl_xor_sync(0xffffffffu, w, o);
     if (lane == 0) {
-      sh.run_weight[q] = w;
-      sh.run_count[q] = n;
+      atomicAdd(&sh.mine_weight[q], w);
+      atomicAdd(&sh.mine_count[q], n);
     }
   }
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) over += __shfl_xor_sync(0xffffffffu, over, o);
-  if (lane == 0 && over) atomicAdd(&sh.floor_weight, over);
+  if (lane == 0 && over) atomicAdd(&sh.mine_floor, over);
+  __syncthreads();
+  if (tid < kRuns) {  // thread i: run i / C of this CTA's, to CTA i % C
+    const uint32_t q = tid / C * C + me;
+    if (sh.mine_count[q]) {
+      Shared* o = cl.map_shared_rank(&sh, tid % C);
+      o->run_weight[q] = sh.mine_weight[q];
+      o->run_count[q] = sh.mine_count[q];
+    }
+    if (tid < C) atomicAdd(&cl.map_shared_rank(&sh, tid)->floor_weight, sh.mine_floor);
+  }
   cl.sync();
 
   // ---- the row's runs, from the largest values down: thread i has run kRuns - 1 - i; what lies before each
-  u64 mine_w = 0, floor_sum = 0;
+  u64 mine_w = 0;
   uint32_t mine_c = 0;
   if (tid < kRuns) {
-    const uint32_t q = kRuns - 1 - tid;
-#pragma unroll
-    for (uint32_t c = 0; c < C; ++c) {
-      const Shared* o = cl.map_shared_rank(&sh, c);
-      mine_w += o->run_weight[q];
-      mine_c += o->run_count[q];
-    }
+    mine_w = sh.run_weight[kRuns - 1 - tid];
+    mine_c = sh.run_count[kRuns - 1 - tid];
   }
-#pragma unroll
-  for (uint32_t c = 0; c < C; ++c) floor_sum += cl.map_shared_rank(&sh, c)->floor_weight;
   u64 at_w = mine_w;
   uint32_t at_c = mine_c;
 #pragma unroll
@@ -288,8 +348,9 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
   at_w -= mine_w;  // before this run
   at_c -= mine_c;
 
-  // A search: the thread whose run holds the place says so, the run's counts are added up over the CTAs, and warp 0 walks its values,
-  // four a lane from the largest down: find(weight and count before the value, its weight and count, its key).
+  // A search: the thread whose run holds the place says so, the run's counts are added up over the CTAs and weighed, and
+  // warp 0 walks its values, four a lane from the largest down: find(weight and count before the value, its weight and count,
+  // its key).
   const auto search = [&](bool here, auto&& find) {
     if (here) {
       sh.run = kRuns - 1 - tid;
@@ -301,22 +362,24 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     const uint32_t q = sh.run;
     if (tid < 64 * C) {
       const uint32_t h = cl.map_shared_rank(hist, tid / 64)[q * 64 + tid % 64], k = 2 * (tid % 64);
+      sh.word[tid] = h;
       if (h & 0xffffu) atomicAdd(&sh.fine[kRun - 1 - k], h & 0xffffu);
       if (h >> 16) atomicAdd(&sh.fine[kRun - 2 - k], h >> 16);
     }
     __syncthreads();
+    if (tid < kRun) {
+      uint32_t e;
+      const u64 m = sh.fine[tid] ? weight(g.table, scale, q * kRun + kRun - 1 - tid, e) : 0;
+      sh.fine_w[tid] = m ? fixed(m, e) : 0;
+    }
+    if (tid < kRun) named_barrier(1, kRun);  // the warps that weighed; warp 0 goes on alone
     if (warp == 0) {
       u64 w[4], sum = 0;
       uint32_t c[4], n = 0;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
         c[i] = sh.fine[4 * lane + i];
-        w[i] = 0;
-        if (c[i]) {
-          uint32_t e;
-          const u64 m = weight(g.table, scale, q * kRun + kRun - 1 - (4 * lane + i), e);
-          w[i] = fixed(m, e);
-        }
+        w[i] = sh.fine_w[4 * lane + i];
         sum += w[i] * c[i];
         n += c[i];
       }
@@ -360,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     });
     kept = min(kept, sh.place);
   }
-  kept = min(kept, floor_sum);
+  kept = min(kept, sh.floor_weight);
 
   // ---- the token with u of that before it
   const u64 goal = min(share(u, kept, false), kept - 1);
@@ -376,35 +439,57 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     }
   });
   // ---- its index: the nth token of that value, in the CTA that holds it
+  auto read = cl.barrier_arrive();  // this CTA reads no other's counts any more
   const uint32_t key = sh.key;
   uint32_t nth = sh.nth, before = 0, here = 0;
   for (uint32_t c = 0; c <= me; ++c) {
     before += here;
-    here = cl.map_shared_rank(hist, c)[key >> 1] >> (key & 1 ? 16 : 0) & 0xffffu;
+    here = sh.word[c * (kRun / 2) + (key % kRun) / 2] >> (key & 1 ? 16 : 0) & 0xffffu;
   }
   if (before <= nth && nth < before + here) {
     nth -= before;
-    const uint32_t per = (part + kThreads - 1) / kThreads;  // eights of a thread, in order
-    const uint32_t e0 = min(t1, t0 + tid * per), e1 = min(t1, e0 + per);
-    uint32_t found = 0;
-    for (uint32_t t = e0; t < e1; ++t) tokens(t, [&](uint32_t v, int32_t) { found += !is_nan(v) && key_of(v) == key; });
-    uint32_t ahead = found;
+    // each warp a stretch of eights, its lanes side by side: counted, then looked through by the warp that has the token
+    const uint32_t per = (part + kThreads / 32 - 1) / (kThreads / 32), e0 = min(t1, t0 + warp * per), e1 = min(t1, e0 + per);
+    const uint32_t bits = key & 0x8000u ? key & 0x7fffu : 0xffffu & ~key, two = bits | bits << 16;
+    // which tokens of an eight are of that value
+    const auto which = [&](uint32_t t) {
+      const int32_t i0 = (int32_t)(8 * t) - (int32_t)lead;
+      uint32_t is = 0;
+      if (t < e1 && bits && i0 >= 0 && (uint32_t)i0 + 8 <= a.vocab) {
+        const uint4 v = *reinterpret_cast<const uint4*>(x + i0);
+        const uint32_t w[4] = {v.x ^ two, v.y ^ two, v.z ^ two, v.w ^ two};
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, ahead, o);
-      if (lane >= (uint32_t)o) ahead += y;
-    }
-    if (lane == 31) sh.warp_c[warp] = ahead;
+        for (int i = 0; i < 4; ++i) is |= (uint32_t)((w[i] & 0xffffu) == 0) << 2 * i | (uint32_t)(w[i] >> 16 == 0) << (2 * i + 1);
+      } else if (t < e1) {  // an end, or either zero
+        tokens(t, [&](uint32_t v, int32_t i) { is |= (uint32_t)(!is_nan(v) && key_of(v) == key) << (i - i0); });
+      }
+      return is;
+    };
+    uint32_t found = 0;
+#pragma unroll 4
+    for (uint32_t t = e0 + lane; t - lane < e1; t += 32) found += __popc(which(t));
+    found = __reduce_add_sync(0xffffffffu, found);
+    if (lane == 0) sh.warp_c[warp] = found;
     __syncthreads();
-    ahead -= found;
-    for (uint32_t w = 0; w < warp; ++w) ahead += sh.warp_c[w];
+    uint32_t ahead = __reduce_add_sync(0xffffffffu, lane < warp ? sh.warp_c[lane] : 0u);
     if (ahead <= nth && nth < ahead + found)
-      for (uint32_t t = e0; t < e1; ++t)
-        tokens(t, [&](uint32_t v, int32_t i) {
-          if (!is_nan(v) && key_of(v) == key && ahead++ == nth) a.token[r] = i;
-        });
+      for (uint32_t t = e0 + lane; t - lane < e1; t += 32) {
+        uint32_t is = which(t), n = __popc(is), upto = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, upto, o);
+          if (lane >= (uint32_t)o) upto += y;
+        }
+        const uint32_t rank = ahead + upto - n;
+        if (rank <= nth && nth < rank + n) {
+          for (uint32_t k = rank; k < nth; ++k) is &= is - 1;
+          a.token[r] = (int32_t)(8 * t) - (int32_t)lead + __ffs(is) - 1;
+        }
+        ahead += __shfl_sync(0xffffffffu, upto, 31);
+        if (nth < ahead) break;
+      }
   }
-  cl.sync();  // no CTA leaves while another reads its counts
+  cl.barrier_wait(std::move(read));  // and none leaves while another reads its own
 }
 
 template <uint32_t C>
