@@ -40,7 +40,16 @@ namespace {
 
 constexpr uint32_t kM = 128, kTile = 64, kOctets = kTile / 8;
 constexpr uint32_t kSoft = 256;  // threads of the softmax
-constexpr uint32_t kLoaders = 8, kLoadThreads = 32 * kLoaders, kRowsThreads = kSoft + 32 + kLoadThreads;
+constexpr uint32_t kLoaders = 8, kLoadThreads = 32 * kLoaders, kRowsThreads = kSoft + kLoadThreads + 32;
+// Registers of a thread: as launched (what 17 warps leave, five of them on one scheduler), then shared out anew where
+// one role needs more. (A loader that spilled words on their way would wait for each: Turbo8's with 64 registers took 3 000
+// cycles a tile to issue its loads.)
+constexpr int kRegsLaunch = 96;
+template <bool T8>
+struct Regs {
+  static constexpr int soft = T8 ? 96 : 112, load = T8 ? 96 : 80;
+  static_assert(8 * (soft + load) <= 16 * kRegsLaunch, "no more than the block was launched with");
+};
 constexpr uint32_t kHalf = kTile / 2;  // tokens of a thread
 constexpr uint32_t kLead = 2;   // what an item's beginning and end cost a CTA, in tiles
 constexpr uint32_t kLeast = 2;  // tiles of a stretch at least
@@ -102,7 +111,25 @@ __device__ __forceinline__ Block block_of(const RowsAttend& a, uint32_t row, uin
 struct Stretch {
   Block b;
   uint32_t g, t0, t1, c0;
+  // tiles of which every row of the block sees every token: [0, whole0) and [whole1, whole2)
+  uint32_t whole0, whole1, whole2;
+  __device__ __forceinline__ bool whole(uint32_t t) const { return t < whole0 || (t >= whole1 && t < whole2); }
 };
+__device__ __forceinline__ void set_whole(const RowsAttend& a, Stretch& s) {
+  const Block& b = s.b;
+  s.whole0 = 0;
+  if (a.parent) {
+    s.whole1 = 0;
+    s.whole2 = (b.pos - b.index) / kTile;
+  } else {
+    if (b.nA) s.whole0 = a.n_first / kTile;
+    // octets behind the first tokens' that lie in the last row's window and not behind the first row's position
+    const uint32_t low = b.last + 1 > a.window ? b.last + 1 - a.window : 0, from = max(low, b.b8);
+    const uint32_t o1 = b.nA + (from - b.b8 + 7) / 8, o2 = b.pos + 1 > b.b8 ? b.nA + (b.pos + 1 - b.b8) / 8 : 0;
+    s.whole1 = (o1 + kOctets - 1) / kOctets;
+    s.whole2 = o2 / kOctets;
+  }
+}
 // A warp's way along the line: its CTA's part is [w, w1), cut into stretches. In shared memory, one for each warp: the
 // registers are the loops'.
 struct Walk {
@@ -125,6 +152,7 @@ __device__ __forceinline__ bool next(const RowsAttend& a, const uint32_t* first,
       k.s.t0 = max(at, kLead) - kLead;
       k.s.t1 = max(at + used, kLead) - kLead;
       k.s.c0 = (w - at + kLead) / per;
+      set_whole(a, k.s);
       w += used;
       more = k.s.t0 != k.s.t1;
     }
@@ -213,14 +241,6 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 __device__ __forceinline__ uint32_t bits_below(int64_t n) { return n <= 0 ? 0u : n >= 8 ? 0xffu : (1u << n) - 1u; }
 
-// Whether every row of the block sees all of octet o.
-__device__ __forceinline__ bool octet_full(const RowsAttend& a, const Block& b, uint32_t o) {
-  if (o >= b.octets) return false;
-  const uint32_t t = b.token(o);
-  if (a.parent) return t + 7 < b.pos - b.index;
-  return t + 7 <= b.pos && (b.last - t < a.window || (t < a.n_first && a.n_first - t >= 8));
-}
-
 // Bounded waits of one thread: after one has run out no other waits.
 struct Waiter {
   uint64_t limit;
@@ -289,7 +309,7 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* 
         now = then;
         then = find(a, s.b, t + 4, lane);
       }
-      const bool full = __all_sync(0xffffffffu, octet_full(a, s.b, t * kOctets + lane % 8));
+      const bool full = s.whole(t);
       const uint32_t valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
       uint32_t rows = 0xffu;  // lane % 8's octet: rows of it that are loaded
       if (!full) {
@@ -376,19 +396,20 @@ struct LoadTurbo8 {
       then = find(a, s.b, t + 4, lane);
     }
   }
-  static __device__ __forceinline__ uint16_t load2(const uint16_t* p) {  // nothing waits for it here
-    uint16_t r;
-    asm volatile("ld.global.b16 %0, [%1];" : "=h"(r) : "l"(p));
+  // A scale in a whole register: 16-bit ones are packed two by two as they arrive, and the packing waits for the loads.
+  static __device__ __forceinline__ uint32_t load2(const uint16_t* p) {
+    uint32_t r;
+    asm volatile("ld.global.u16 %0, [%1];" : "=r"(r) : "l"(p));
     return r;
   }
   // Where the next tile's pieces lie, then its scales and K's codes.
-  __device__ __forceinline__ void fetch_k(uint4 (&k)[J], uint16_t (&ks)[J], uint16_t (&vs)[J]) {
+  __device__ __forceinline__ void fetch_k(uint4 (&k)[J], uint32_t (&ks)[J], uint32_t (&vs)[J]) {
     in = 0;
     if (!more) return;
     const uint32_t i = (t - s.t0) % 4;
     valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
     uint32_t rows = 0xffu;  // lane % 8's octet: rows of it that are loaded
-    if (!__all_sync(0xffffffffu, octet_full(a, s.b, t * kOctets + lane % 8))) {
+    if (!s.whole(t)) {
       uint32_t lo, hi;
       octet_rows(a, s.b, t * kOctets + lane % 8, lo, hi);
       rows = bits_below(hi) & ~bits_below(lo);
@@ -434,7 +455,7 @@ struct LoadTurbo8 {
   // Tiles into the ring, as f16 over 2^E. K's arrival releases the notes: K's scales, V's exponents, what octets are there.
   __device__ __forceinline__ void run() {
     uint4 k[J], v[J];
-    uint16_t ks[J], vs[J];
+    uint32_t ks[J], vs[J];
     begin();
     bool go = more;
     fetch_k(k, ks, vs);
@@ -448,7 +469,7 @@ struct LoadTurbo8 {
         uint32_t mx[J], scale[J];  // K's in the low half
 #pragma unroll
         for (uint32_t j = 0; j < J; ++j) {
-          scale[j] = ks[j] | (uint32_t)vs[j] << 16;
+          scale[j] = ks[j] | vs[j] << 16;
           mx[j] = scale[j] & 0x7fff7fffu;
           if ((mx[j] & 0x7f80u) == 0x7f80u) mx[j] &= 0xffff0000u;
           if ((mx[j] & 0x7f800000u) == 0x7f800000u) {
@@ -554,7 +575,6 @@ struct Softmax {
   Notes<D>& sh;
   uint32_t tid, lane, tmem, group;  // tmem: the warp's lanes of it
   Waiter& wait;
-  Work work;
   float scale;
   uint32_t row, half, pair;  // pair: the barrier of the warp and its other half
   // the thread's row
@@ -669,7 +689,7 @@ struct Softmax {
 
   __device__ __forceinline__ void tile(const Stretch& st, uint32_t t, uint32_t n) {
     const bool busy = row - lane % 32 < st.b.rows * group;
-    const bool all = __all_sync(0xffffffffu, octet_full(a, st.b, t * kOctets + lane % 8));
+    const bool all = st.whole(t);
     const Place<D> pv(2 * n + 1);
     wait(&sh.s_full[n & 1], (n >> 1) & 1);
     tm_after_sync();
@@ -826,6 +846,7 @@ struct Softmax {
     if (row - lane % 32 >= cols) return;
     if (half) sh.sum[row] = l;
     named_barrier(pair, 64);
+    const Work work = work_of(a.work, a.r.n_rows, a.H, D);
     const bool nat = st.c0 == blockIdx.x;
     const size_t first = nat ? (size_t)st.b.row * a.H + st.g * cols : (size_t)blockIdx.x * kM;
     const uint32_t wide = nat ? cols : kM;
@@ -907,6 +928,13 @@ __device__ __forceinline__ void issue(const RowsAttend& a, const uint32_t* first
 
 // ------------------------------------------------------------------ the kernel
 
+template <int N>
+__device__ __forceinline__ void set_registers() {
+  if constexpr (N == kRegsLaunch) return;
+  else if constexpr (N > kRegsLaunch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 template <int D, bool T8>
 __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_constant__ RowsAttend a) {
   extern __shared__ uint8_t raw[];
@@ -929,7 +957,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     mbar_init(&sh.q_full, kSoft);
     mbar_fence_init();
   }
-  if (warp == kSoft / 32) tm_alloc(&sh.tmem, 512);
+  constexpr uint32_t kIssuer = kRowsThreads / 32 - 1;
+  if (warp == kIssuer) tm_alloc(&sh.tmem, 512);
   pdl_wait();
   pdl_launch();
 
@@ -1013,7 +1042,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   }
   Waiter wait{a.wait_ns, a.status, false};
   if (tid < kSoft) {
-    Softmax<D, T8> x{a, q_sm, sh, tid, lane, tmem + ((32 * (warp % 4)) << 16), group, wait, work,
+    set_registers<Regs<T8>::soft>();
+    Softmax<D, T8> x{a, q_sm, sh, tid, lane, tmem + ((32 * (warp % 4)) << 16), group, wait,
                      1.4426950408889634f / sqrtf((float)D), tid % kM, tid / kM, 2 + warp % 4};
     const Stretch& s = walk.s;
     uint32_t n = 0;
@@ -1023,18 +1053,21 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
       for (uint32_t t = s.t0; t < s.t1; ++t, ++n) x.tile(s, t, n);
       x.store(s, n - 1);
     }
-  } else if (warp == kSoft / 32) {
+  } else if (warp == kIssuer) {
     issue<D, T8>(a, first, per, walk, lane, smem_addr(q_sm), smem_addr(ring), sh, tmem, wait);
-  } else if constexpr (T8) {
-    const uint32_t i = tid - kSoft - 32;
-    LoadTurbo8<D> x{a, ring, sh, i, i / 32, lane, i / (D / 16), i % (D / 16), wait, first, per, walk, walk.s};
-    x.run();
   } else {
-    load_plain<D>(a, first, per, walk, ring, sh, tid - kSoft - 32, wait);
+    set_registers<Regs<T8>::load>();
+    const uint32_t i = tid - kSoft;
+    if constexpr (T8) {
+      LoadTurbo8<D> x{a, ring, sh, i, i / 32, lane, i / (D / 16), i % (D / 16), wait, first, per, walk, walk.s};
+      x.run();
+    } else {
+      load_plain<D>(a, first, per, walk, ring, sh, i, wait);
+    }
   }
   tm_before_sync();
   __syncthreads();
-  if (warp == kSoft / 32) {
+  if (warp == kIssuer) {
     tm_after_sync();
     tm_free(tmem, 512);
   }
