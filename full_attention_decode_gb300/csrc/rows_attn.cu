@@ -33,6 +33,7 @@
 #include "turbo8.cuh"
 
 #include <algorithm>
+#include <type_traits>
 
 namespace q35c {
 using namespace q35;
@@ -42,27 +43,27 @@ constexpr uint32_t kM = 128, kTile = 64, kOctets = kTile / 8;
 constexpr uint32_t kSoft = 256;  // threads of the softmax
 constexpr uint32_t kLoaders = 8, kLoadThreads = 32 * kLoaders, kRowsThreads = kSoft + kLoadThreads + 32;
 // Registers of a thread: as launched (what 17 warps leave, five of them on one scheduler), then shared out anew where
-// one role needs more. (A loader that spilled words on their way would wait for each: Turbo8's with 64 registers took 3 000
-// cycles a tile to issue its loads.)
+// one role needs more.
 constexpr int kRegsLaunch = 96;
-template <bool T8>
-struct Regs {
-  static constexpr int soft = T8 ? 96 : 112, load = T8 ? 96 : 80;
-  static_assert(8 * (soft + load) <= 16 * kRegsLaunch, "no more than the block was launched with");
-};
+constexpr int kRegsSoft = 112, kRegsLoad = 80;
+static_assert(8 * (kRegsSoft + kRegsLoad) <= 16 * kRegsLaunch, "no more than the block was launched with");
 constexpr uint32_t kHalf = kTile / 2;  // tokens of a thread
 constexpr uint32_t kLead = 2;   // what an item's beginning and end cost a CTA, in tiles
 constexpr uint32_t kLeast = 2;  // tiles of a stretch at least
 constexpr float kSlack = 8.f;   // how far a score may lie above what P and l refer to before they are moved
 constexpr float kSlack8 = 4.f, kUp8 = 11.f;  // Turbo8's weights of V: at most 2^(kUp8 + kSlack8) in f16
 
-template <int D>
+// Q, then the ring of K (even slots) and V tiles as the products take them; Turbo8: then `raw` halves of tiles as they lie in
+// the cache, on their way. (Loads into registers instead hang on the L1, which has a few KB beside this: 16 trees 174 us.)
+template <int D, bool T8>
 struct Ring {
-  static constexpr uint32_t bytes = kTile * D * 2;                // K or V of a tile
-  static constexpr uint32_t slots = D == 256 ? 4 : 8;             // even ones K, odd ones V
+  static constexpr uint32_t bytes = kTile * D * 2;  // K or V of a tile
+  static constexpr uint32_t slots = T8 ? (D == 256 ? 2 : 4) : D == 256 ? 4 : 8;
   static constexpr uint32_t slab = kTile * 128, q_slab = kM * 128;  // 64 dims of all rows
   static constexpr uint32_t q = kM * D * 2;
-  static constexpr uint32_t info = D == 256 ? 4 : 8;               // tiles whose notes are kept: the ring's and two of the softmax's
+  static constexpr uint32_t raw = T8 ? (D == 256 ? 3 : 6) : 0, raw_bytes = kTile * (D + D / 8);  // codes, then scales
+  static constexpr uint32_t all = q + slots * bytes + raw * raw_bytes;
+  static constexpr uint32_t info = D == 256 ? 4 : 8;  // tiles whose notes are kept: the ring's and two of the softmax's
   static_assert(slots / 2 + 2 <= info, "notes");
 };
 
@@ -167,24 +168,22 @@ __device__ __forceinline__ bool next(const RowsAttend& a, const uint32_t* first,
 // Shared memory behind Q and the ring.
 template <uint32_t kInfo>
 struct NotesOf {
-  uint64_t full[8], empty[8], s_full[2], s_free[2], p_full[2], q_full;
+  uint64_t full[8], empty[8], s_full[2], s_free[2], p_full[2], v_notes[kInfo], q_full;
   uint32_t tmem;
   uint32_t sums[kRowsThreads / 32];
   uint32_t valid[kInfo];             // octets of the tile that hold tokens
-  uint8_t dirty[kInfo][kLoaders];    // V held something that is no number (a loader warp each)
-  float k_scale[kInfo][kTile], v_exp[kInfo][kTile];  // Turbo8: 2^E of K's tokens, E of V's
+  uint32_t ahead[8];                 // Turbo8: of the tiles that are on their way
+  alignas(16) uint8_t dirty[kInfo][kLoaders];  // V held something that is no number (a loader warp each)
+  alignas(16) float k_scale[kInfo][kTile], v_exp[kInfo][kTile];  // Turbo8: 2^E of K's tokens, E of V's
   float q_scale[kM];
-  float2 top[2][2][kM];  // a row's two threads' maxima
+  alignas(16) float2 top[2][2][kM];  // a row's two threads' maxima
   float sum[kM];         // the second thread's sum
   int32_t parent[kMaxNodes];
   Walk walk[kRowsThreads / 32];
 };
 
 template <int D>
-using Notes = NotesOf<Ring<D>::info>;
-
-template <int D>
-using Notes = NotesOf<Ring<D>::info>;
+using Notes = NotesOf<Ring<D, false>::info>;
 
 struct Work {  // the scratch
   // Sums of an item's first stretch and of the one that a CTA goes on with: [D / 8][columns][8], so that a
@@ -255,27 +254,33 @@ struct Waiter {
 };
 
 // Where a half-tile h (2 n for tile n's K, 2 n + 1 for its V; n counts the CTA's tiles) lies in the ring.
-template <int D>
+template <int D, bool T8>
 struct Place {
   uint32_t slot, turn;
-  __device__ __forceinline__ explicit Place(uint32_t h) : slot(h % Ring<D>::slots), turn(h / Ring<D>::slots) {}
+  __device__ __forceinline__ explicit Place(uint32_t h) : slot(h % Ring<D, T8>::slots), turn(h / Ring<D, T8>::slots) {}
 };
 
 // ------------------------------------------------------------------ loaders
 
-// Where the octets of four tiles lie, an octet a lane.
+// Where the octets of four tiles lie, an octet a lane. A lookup is made four tiles ahead; nothing looks at it before.
 struct Found {
   uint32_t row;  // a row is 128 bytes of K and V at least: no memory holds 2^32
   bool in;
 };
-__device__ __forceinline__ Found find(const RowsAttend& a, const Block& b, uint32_t t, uint32_t lane) {
-  Found f = {0, false};
+__device__ __forceinline__ uint32_t look_up(const RowsAttend& a, const Block& b, uint32_t t, uint32_t lane) {
   const uint32_t o = t * kOctets + lane;
-  if (o < b.octets) {
-    size_t row = 0;
-    f.in = cache_row(a.c, b.seq, b.token(o), row);
-    f.row = (uint32_t)row;
-    if (!f.in) set_status(a.status, kStatusRange);
+  if (!a.c.btab || o >= b.octets) return 0;
+  return (uint32_t)a.c.btab[(size_t)b.seq * (a.c.capacity >> a.c.bt_shift) + (b.token(o) >> a.c.bt_shift)];
+}
+__device__ __forceinline__ Found found(const RowsAttend& a, const Block& b, uint32_t t, uint32_t lane, uint32_t block) {
+  const uint32_t o = t * kOctets + lane, token = b.token(o);
+  Found f = {b.seq * a.c.capacity + token, o < b.octets};
+  if (a.c.btab) {
+    if (f.in && block >= a.c.num_blocks) {
+      set_status(a.status, kStatusRange);
+      f.in = false;
+    }
+    f.row = block << a.c.bt_shift | (token & ((1u << a.c.bt_shift) - 1u));
   }
   return f;
 }
@@ -296,18 +301,19 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* 
                                            Notes<D>& sh, uint32_t tid, Waiter& wait) {
   constexpr uint32_t C = D / 8, STEP = kLoadThreads / C, J = kTile / STEP;  // pieces of a row, rows of a pass, passes
   const uint32_t warp = tid / 32, lane = tid % 32, r0 = tid / C, c = tid % C, q0 = warp * 32 / C / 8;
-  const uint32_t to = (c / 8) * Ring<D>::slab + sw(r0, c % 8);  // STEP is a multiple of 8: piece j lies STEP * 128 behind
+  const uint32_t to = (c / 8) * Ring<D, false>::slab + sw(r0, c % 8);  // STEP is a multiple of 8: piece j lies STEP * 128 behind
   static_assert(STEP % 8 == 0, "the swizzle of a thread's rows");
   const uint32_t stride = a.c.Hkv * D;
   const Stretch& s = walk.s;
   uint32_t n = 0;
   while (next(a, first, per, walk, lane)) {
-    Found now = find(a, s.b, s.t0, lane), then = find(a, s.b, s.t0 + 4, lane);
+    Found now = {0, false};
+    uint32_t then = look_up(a, s.b, s.t0, lane);
     for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
       const uint32_t i = (t - s.t0) % 4;
-      if (i == 0 && t != s.t0) {
-        now = then;
-        then = find(a, s.b, t + 4, lane);
+      if (i == 0) {
+        now = found(a, s.b, t, lane, then);
+        then = look_up(a, s.b, t + 4, lane);
       }
       const bool full = s.whole(t);
       const uint32_t valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
@@ -327,9 +333,9 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* 
       }
 #pragma unroll 1
       for (uint32_t p = 0; p < 2; ++p) {
-        const Place<D> at(2 * n + p);
+        const Place<D, false> at(2 * n + p);
         if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
-        uint8_t* slot = ring + at.slot * Ring<D>::bytes;
+        uint8_t* slot = ring + at.slot * Ring<D, false>::bytes;
         const uint16_t* base = reinterpret_cast<const uint16_t*>(p ? a.c.v : a.c.k) + s.g * D + 8 * c;
         if (!p || full) {
           const uint32_t dst = smem_addr(slot) + to;
@@ -354,12 +360,12 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* 
             *reinterpret_cast<uint4*>(slot + to + j * STEP * 128) = x[j];
           }
           bad = __any_sync(0xffffffffu, bad);
-          if (lane == 0) sh.dirty[n % Ring<D>::info][warp] = bad;
+          if (lane == 0) sh.dirty[n % Ring<D, false>::info][warp] = bad;
           tm_fence_shared();
           mbar_arrive(&sh.full[at.slot]);
         }
         if (!p && tid == 0) {  // an arrival that the notes are released by
-          sh.valid[n % Ring<D>::info] = valid;
+          sh.valid[n % Ring<D, false>::info] = valid;
           mbar_arrive(&sh.full[at.slot]);
         }
       }
@@ -368,46 +374,46 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* 
   asm volatile("cp.async.wait_all;" ::: "memory");
 }
 
-// Turbo8: sixteen codes and their scale a piece, in registers on their way: K of the next tile is fetched as soon as
-// this one's is put, and so is V.
+// Turbo8: sixteen codes and their scale a piece. A thread copies the pieces that it will turn into f16 itself, Ring::raw halves
+// of tiles ahead; its warp's rows' scales come with them. So only the warp waits. The order is K of tile 0, then K of tile n + 1
+// and V of tile n in turn: K's place is free as soon as tile n's scores are there, V's only after its softmax.
 template <int D>
 struct LoadTurbo8 {
+  using R = Ring<D, true>;
   static constexpr uint32_t C = D / 16, STEP = kLoadThreads / C, J = kTile / STEP;
+  static constexpr uint32_t RW = 32 / C, S = D == 256 ? 2 : 1;  // a warp's rows of a pass; lanes that copy a row's scales
   const RowsAttend& a;
   uint8_t* ring;
   Notes<D>& sh;
   uint32_t tid, warp, lane, r0, c;
   Waiter& wait;
-  // the tile that is fetched, ahead of the one that is put
   const uint32_t* first;
   uint32_t per;
   Walk& walk;
   const Stretch& s;
-  Found now, then;
-  uint32_t t, valid, in;
+  Found now;
+  // the tile that is copied next, into a stage; how many there were
+  uint32_t then, t, stage, tiles;
   bool more;
-  uint32_t row[J];  // of a piece
+  struct Pieces {  // the thread's, of a tile: which are there (bit 31: the scales), their rows, the kv-head
+    uint32_t in, row[J], scale_row, g;
+  } kp, vp;
 
+  __device__ __forceinline__ uint8_t* raw(uint32_t st) const { return ring + R::slots * R::bytes + st * R::raw_bytes; }
   __device__ __forceinline__ void begin() {
     more = next(a, first, per, walk, lane);
-    if (more) {
-      t = s.t0;
-      now = find(a, s.b, t, lane);
-      then = find(a, s.b, t + 4, lane);
-    }
-  }
-  // A scale in a whole register: 16-bit ones are packed two by two as they arrive, and the packing waits for the loads.
-  static __device__ __forceinline__ uint32_t load2(const uint16_t* p) {
-    uint32_t r;
-    asm volatile("ld.global.u16 %0, [%1];" : "=r"(r) : "l"(p));
-    return r;
-  }
-  // Where the next tile's pieces lie, then its scales and K's codes.
-  __device__ __forceinline__ void fetch_k(uint4 (&k)[J], uint32_t (&ks)[J], uint32_t (&vs)[J]) {
-    in = 0;
     if (!more) return;
+    t = s.t0;
+    then = look_up(a, s.b, t, lane);
+  }
+  __device__ __forceinline__ void places() {
     const uint32_t i = (t - s.t0) % 4;
-    valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
+    if (i == 0) {
+      now = found(a, s.b, t, lane, then);
+      then = look_up(a, s.b, t + 4, lane);
+    }
+    const uint32_t valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
+    if (tid == 0) sh.ahead[tiles % 8] = valid;
     uint32_t rows = 0xffu;  // lane % 8's octet: rows of it that are loaded
     if (!s.whole(t)) {
       uint32_t lo, hi;
@@ -415,126 +421,161 @@ struct LoadTurbo8 {
       rows = bits_below(hi) & ~bits_below(lo);
     }
     if (!(valid >> (lane % 8) & 1)) rows = 0;
+    kp.in = 0;
+    kp.g = s.g;
 #pragma unroll
     for (uint32_t j = 0; j < J; ++j) {
-      const uint32_t q = warp * 32 / C / 8 + j * STEP / 8;  // a warp's rows lie in one octet
-      row[j] = __shfl_sync(0xffffffffu, now.row, 8 * i + q) + r0 % 8;
-      const uint32_t here = __shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u;
-      in |= here << j;
-      if (!here) row[j] = 0;  // rows that nobody sees: whatever lies there, V's taken out later
-      const size_t so = (size_t)row[j] * a.c.sstride + s.g * C + c;
-      ks[j] = load2(a.c.ks + so);
-      vs[j] = load2(a.c.vs + so);
-      k[j] = load16(a.c.k + s.g * D + 16 * c + (size_t)row[j] * (a.c.Hkv * D));
+      const uint32_t q = warp * RW / 8 + j * STEP / 8;  // a warp's rows lie in one octet
+      kp.row[j] = __shfl_sync(0xffffffffu, now.row, 8 * i + q) + r0 % 8;
+      kp.in |= (__shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u) << j;
+    }
+    const uint32_t r = scale_of();
+    kp.scale_row = __shfl_sync(0xffffffffu, now.row, 8 * i + r / 8) + r % 8;
+    kp.in |= (__shfl_sync(0xffffffffu, rows, r / 8) >> (r % 8) & (lane < 8 * S ? 1u : 0u)) << 31;
+  }
+  // The row of the tile whose scales the lane copies, 16 bytes of them or (D = 64) 8: one of its warp's eight.
+  __device__ __forceinline__ uint32_t scale_of() const {
+    const uint32_t k = lane / S % 8;
+    return warp * RW + k % RW + k / RW * STEP;
+  }
+  __device__ __forceinline__ void copy(const Pieces& x, const uint8_t* codes, const uint16_t* scales) {
+    codes += x.g * D + 16 * c;
+    scales += x.g * C + lane % S * 8;
+    const uint32_t to = smem_addr(raw(stage));
+#pragma unroll
+    for (uint32_t j = 0; j < J; ++j)
+      cp16(to + (j * kLoadThreads + tid) * 16, x.in >> j & 1 ? codes + (size_t)x.row[j] * (a.c.Hkv * D) : codes, x.in >> j & 1);
+    if (lane < 8 * S) {
+      const bool here = x.in >> 31;
+      const uint16_t* from = here ? scales + (size_t)x.scale_row * a.c.sstride : scales;
+      const uint32_t dst = to + kTile * D + scale_of() * (D / 8) + lane % S * 16;
+      if constexpr (D != 64) cp16(dst, from, here);
+      else asm volatile("cp.async.ca.shared.global [%0], [%1], 8, %2;" ::"r"(dst), "l"(from), "r"(here ? 8 : 0) : "memory");
     }
   }
-  __device__ __forceinline__ void fetch_v(uint4 (&v)[J]) {
-    if (!more) return;
-#pragma unroll
-    for (uint32_t j = 0; j < J; ++j) v[j] = load16(a.c.v + s.g * D + 16 * c + (size_t)row[j] * (a.c.Hkv * D));
-    if (++t == s.t1) {
-      begin();
-    } else if ((t - s.t0) % 4 == 0) {
-      now = then;
-      then = find(a, s.b, t + 4, lane);
+  __device__ __forceinline__ void copied() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    stage = stage + 1 == R::raw ? 0 : stage + 1;
+  }
+  __device__ __forceinline__ void copy_k() {  // of the next tile, if there is one
+    vp = kp;
+    if (more) {
+      places();
+      copy(kp, a.c.k, a.c.ks);
+      ++tiles;
+      if (++t == s.t1) begin();
     }
+    copied();
   }
-  // Sixteen codes times f (twice, in f16) into a piece's place.
-  __device__ __forceinline__ void put(uint8_t* slab, uint32_t r, const uint32_t (&w)[4], uint32_t f2) const {
-    uint32_t y[8];
+  __device__ __forceinline__ void copy_v(bool any) {  // of the tile before that
+    if (any) copy(vp, a.c.v, a.c.vs);
+    copied();
+  }
+  // A half of tile n into the ring, as f16 over 2^E. K's arrival releases its scales and what octets are there, V's exponents have a
+  // barrier of their own: they are known before their place in the ring is free.
+  template <uint32_t V>
+  __device__ __forceinline__ void put(uint32_t n, uint32_t st) {
+    const uint8_t* from = raw(st);
+    uint32_t sc[J], mx[(J + 1) / 2], f[J], bad = 0;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) y[i] = hmul2(e4m3_to_f16x2(w[i / 2] >> (16 * (i % 2))), f2);
-    const uint32_t j8 = (c % 4) * 2;
-    *reinterpret_cast<uint4*>(slab + sw(r, j8)) = make_uint4(y[0], y[1], y[2], y[3]);
-    *reinterpret_cast<uint4*>(slab + sw(r, j8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
-  }
-  __device__ __forceinline__ uint8_t* slot_of(const Place<D>& at) {
+    for (uint32_t j = 0; j < J; ++j) sc[j] = *reinterpret_cast<const uint16_t*>(from + kTile * D + (r0 + j * STEP) * (D / 8) + 2 * c);
+    // a token's largest scale, two pieces at once, from the lanes that have them; those that are no numbers do not count
+#pragma unroll
+    for (uint32_t j = 0; j < J; ++j) {
+      uint32_t m = sc[j] & 0x7fffu;
+      if (m >= 0x7f80u) {
+        m = 0;
+        bad = 1;
+      }
+      mx[j / 2] = j % 2 ? mx[j / 2] | m << 16 : m;
+    }
+#pragma unroll
+    for (uint32_t m = 1; m < C; m <<= 1)
+#pragma unroll
+      for (uint32_t j = 0; j < (J + 1) / 2; ++j) mx[j] = __vmaxu2(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], m));
+#pragma unroll
+    for (uint32_t j = 0; j < J; ++j) {
+      const int e = min(max((int)(mx[j / 2] >> (j % 2 ? 23 : 7) & 255u) - 127, -126), 126);
+      if (c == 0) {
+        if (V) sh.v_exp[n % R::info][r0 + j * STEP] = (float)e;
+        else sh.k_scale[n % R::info][r0 + j * STEP] = pow2(e);
+      }
+      float y = __uint_as_float(sc[j] << 16) * pow2(-e);
+      if (V && (sc[j] & 0x7f80u) == 0x7f80u) y = 0.f;
+      f[j] = pack_f16(y, y);
+    }
+    if (V) mbar_arrive(&sh.v_notes[n % R::info]);
+    const Place<D, true> at(2 * n + V);
     if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
-    return ring + at.slot * Ring<D>::bytes + (c / 4) * Ring<D>::slab;
-  }
-  // Tiles into the ring, as f16 over 2^E. K's arrival releases the notes: K's scales, V's exponents, what octets are there.
-  __device__ __forceinline__ void run() {
-    uint4 k[J], v[J];
-    uint32_t ks[J], vs[J];
-    begin();
-    bool go = more;
-    fetch_k(k, ks, vs);
-    uint32_t here = valid, rows = in;
-    fetch_v(v);
-#pragma unroll 1
-    for (uint32_t n = 0; go; ++n) {
-      // a token's largest scales, K's and V's at once, from the lanes that have them; those that are no numbers do not count
-      uint32_t fk[J], fv[J], bad = 0;
-      {
-        uint32_t mx[J], scale[J];  // K's in the low half
+    uint8_t* slab = ring + at.slot * R::bytes + (c / 4) * R::slab;
+    const uint32_t j8 = (c % 4) * 2;
 #pragma unroll
-        for (uint32_t j = 0; j < J; ++j) {
-          scale[j] = ks[j] | vs[j] << 16;
-          mx[j] = scale[j] & 0x7fff7fffu;
-          if ((mx[j] & 0x7f80u) == 0x7f80u) mx[j] &= 0xffff0000u;
-          if ((mx[j] & 0x7f800000u) == 0x7f800000u) {
-            mx[j] &= 0xffffu;
-            bad |= rows >> j & 1;
-            scale[j] &= 0xffffu;
-          }
-        }
+    for (uint32_t j = 0; j < J; ++j) {
+      const uint4 u = *reinterpret_cast<const uint4*>(from + (j * kLoadThreads + tid) * 16);
+      uint32_t w[4] = {u.x, u.y, u.z, u.w};
+      if (V) {
+        uint32_t nan = 0;
 #pragma unroll
-        for (uint32_t m = 1; m < C; m <<= 1)
+        for (int i = 0; i < 4; ++i) nan |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // codes 0x7f and 0xff
+        if (nan) {
+          bad = 1;
 #pragma unroll
-          for (uint32_t j = 0; j < J; ++j) mx[j] = __vmaxu2(mx[j], __shfl_xor_sync(0xffffffffu, mx[j], m));
-#pragma unroll
-        for (uint32_t j = 0; j < J; ++j) {
-          const int ek = min(max((int)(mx[j] >> 7 & 255u) - 127, -126), 126), ev = min(max((int)(mx[j] >> 23) - 127, -126), 126);
-          if (c == 0) {
-            sh.k_scale[n % Ring<D>::info][r0 + j * STEP] = pow2(ek);
-            sh.v_exp[n % Ring<D>::info][r0 + j * STEP] = (float)ev;
-          }
-          const float x = bf16lo(scale[j]) * pow2(-ek), y = bf16hi(scale[j]) * pow2(-ev);
-          fk[j] = pack_f16(x, x);
-          fv[j] = pack_f16(y, y);
+          for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
         }
       }
-      {
-        const Place<D> at(2 * n);
-        uint8_t* slab = slot_of(at);
+      uint32_t y[8];
 #pragma unroll
-        for (uint32_t j = 0; j < J; ++j) {
-          const uint32_t w[4] = {k[j].x, k[j].y, k[j].z, k[j].w};
-          put(slab, r0 + j * STEP, w, fk[j]);
-        }
-        tm_fence_shared();
-        mbar_arrive(&sh.full[at.slot]);
-        if (tid == 0) {
-          sh.valid[n % Ring<D>::info] = here;
-          mbar_arrive(&sh.full[at.slot]);
-        }
-      }
-      go = more;
-      fetch_k(k, ks, vs);
-      {
-        const Place<D> at(2 * n + 1);
-        uint8_t* slab = slot_of(at);
-#pragma unroll
-        for (uint32_t j = 0; j < J; ++j) {
-          uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w}, nan = 0;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) nan |= ((w[i] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;  // codes 0x7f and 0xff
-          if (nan) {
-            bad |= rows >> j & 1;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
-          }
-          put(slab, r0 + j * STEP, w, fv[j]);
-        }
-        const bool any = __any_sync(0xffffffffu, bad);
-        if (lane == 0) sh.dirty[n % Ring<D>::info][warp] = any;
-        tm_fence_shared();
-        mbar_arrive(&sh.full[at.slot]);
-      }
-      here = valid;
-      rows = in;
-      fetch_v(v);
+      for (int i = 0; i < 8; ++i) y[i] = hmul2(e4m3_to_f16x2(w[i / 2] >> (16 * (i % 2))), f[j]);
+      const uint32_t r = r0 + j * STEP;
+      *reinterpret_cast<uint4*>(slab + sw(r, j8)) = make_uint4(y[0], y[1], y[2], y[3]);
+      *reinterpret_cast<uint4*>(slab + sw(r, j8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
     }
+    if (V) {
+      const bool any = __any_sync(0xffffffffu, bad);
+      if (lane == 0) sh.dirty[n % R::info][warp] = any;
+    }
+    tm_fence_shared();
+    mbar_arrive(&sh.full[at.slot]);
+    if (!V && tid == 0) {
+      sh.valid[n % R::info] = sh.ahead[n % 8];
+      mbar_arrive(&sh.full[at.slot]);
+    }
+  }
+  __device__ __forceinline__ void run() {
+    constexpr uint32_t N = R::raw;  // halves on their way: K0, K1, V0, K2, V1, ...
+    stage = tiles = 0;
+    begin();
+    copy_k();
+#pragma unroll 1
+    for (uint32_t i = 1; i < N; ++i) {
+      if (i % 2) copy_k();
+      else copy_v(i / 2 - 1 < tiles);
+    }
+    uint32_t st = 0, q = 0;  // the half that is put: its stage, its number
+    const auto landed = [&] {
+      asm volatile("cp.async.wait_group %0;" ::"n"(N - 1) : "memory");
+      __syncwarp();
+    };
+    const auto done = [&] {  // a half, and half q + N after it
+      __syncwarp();          // its scales have been read
+      st = st + 1 == N ? 0 : st + 1;
+      if ((q + N) % 2) copy_k();
+      else copy_v((q + N) / 2 - 1 < tiles);
+      ++q;
+    };
+    landed();
+    if (tiles) put<0>(0, st);
+    done();
+#pragma unroll 1
+    for (uint32_t n = 0; n < tiles; ++n) {
+      landed();
+      if (n + 1 < tiles) put<0>(n + 1, st);
+      done();
+      landed();
+      put<1>(n, st);
+      done();
+    }
+    asm volatile("cp.async.wait_all;" ::: "memory");
   }
 };
 
@@ -591,7 +632,7 @@ struct Softmax {
     constexpr uint32_t LPR = D / 8, PER = kSoft / LPR;
     const uint32_t cols = b.rows * group, j = tid % LPR;
     const auto from = [&](uint32_t col) { return a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D + 8 * j; };
-    uint8_t* to = q_sm + (j / 8) * Ring<D>::q_slab;
+    uint8_t* to = q_sm + (j / 8) * Ring<D, T8>::q_slab;
     for (uint32_t col = tid / LPR; col < cols; col += PER) cp16(smem_addr(to + sw(col, j % 8)), from(col), true);
     asm volatile("cp.async.wait_all;" ::: "memory");
     if constexpr (T8) {  // each lane its own pieces, where they lie
@@ -690,10 +731,11 @@ struct Softmax {
   __device__ __forceinline__ void tile(const Stretch& st, uint32_t t, uint32_t n) {
     const bool busy = row - lane % 32 < st.b.rows * group;
     const bool all = st.whole(t);
-    const Place<D> pv(2 * n + 1);
+    const Place<D, T8> pv(2 * n + 1);
     wait(&sh.s_full[n & 1], (n >> 1) & 1);
     tm_after_sync();
-    const uint32_t valid = sh.valid[n % Ring<D>::info];
+    const uint32_t valid = sh.valid[n % Ring<D, T8>::info];
+    if (T8) wait(&sh.v_notes[n % Ring<D, T8>::info], n / Ring<D, T8>::info & 1);
     float s[kHalf];
     uint32_t vis = ~0u;
     if (busy) {
@@ -710,7 +752,7 @@ struct Softmax {
         const float sc = scale * (live ? sh.q_scale[row] : 0.f);
 #pragma unroll
         for (uint32_t j = 0; j < kHalf; j += 4) {
-          const float4 k = *reinterpret_cast<const float4*>(&sh.k_scale[n % Ring<D>::info][half * kHalf + j]);
+          const float4 k = *reinterpret_cast<const float4*>(&sh.k_scale[n % Ring<D, T8>::info][half * kHalf + j]);
           s[j] = s[j] * sc * k.x;
           s[j + 1] = s[j + 1] * sc * k.y;
           s[j + 2] = s[j + 2] * sc * k.z;
@@ -729,7 +771,7 @@ struct Softmax {
 #pragma unroll
         for (uint32_t j = 0; j < kHalf; j += 4) {
           float4 e;
-          if (T8) e = *reinterpret_cast<const float4*>(&sh.v_exp[n % Ring<D>::info][half * kHalf + j]);
+          if (T8) e = *reinterpret_cast<const float4*>(&sh.v_exp[n % Ring<D, T8>::info][half * kHalf + j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             x[i] = fmaxf(x[i], s[j + i]);
@@ -760,7 +802,7 @@ struct Softmax {
         const float ref = finite_or_0(R);
 #pragma unroll
         for (uint32_t j = 0; j < kHalf; j += 4) {
-          const float4 e = *reinterpret_cast<const float4*>(&sh.v_exp[n % Ring<D>::info][half * kHalf + j]);
+          const float4 e = *reinterpret_cast<const float4*>(&sh.v_exp[n % Ring<D, T8>::info][half * kHalf + j]);
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             const float d = s[j + i] - mu;
@@ -785,16 +827,12 @@ struct Softmax {
       l += (sums[0] + sums[1]) + (sums[2] + sums[3]);
       if (!live) f = 1.f;  // whatever its scores are
       if (t != st.t0 && __any_sync(0xffffffffu, f != 1.f)) {
-        const Place<D> before(2 * n - 1);
+        const Place<D, T8> before(2 * n - 1);
         wait(&sh.empty[before.slot], before.turn & 1);
         tm_after_sync();
         rescale_o(f);
       }
-      if (n >= 2) {  // the product that read this P
-        const Place<D> old(2 * n - 3);
-        wait(&sh.empty[old.slot], old.turn & 1);
-        tm_after_sync();
-      }
+      // the product that read this P two tiles ago was issued before these scores', whose arrival covers it
       uint32_t h[16];
       if constexpr (T8) {
 #pragma unroll
@@ -817,7 +855,7 @@ struct Softmax {
     bool dirty = false;
     if (busy && (T8 || !all)) {  // bf16: the other tiles have not been looked through
       wait(&sh.full[pv.slot], pv.turn & 1);  // before the arrival: behind it the slot may be filled again
-      const uint2 u = *reinterpret_cast<const uint2*>(sh.dirty[n % Ring<D>::info]);
+      const uint2 u = *reinterpret_cast<const uint2*>(sh.dirty[n % Ring<D, T8>::info]);
       dirty = (u.x | u.y) != 0;
     }
     mbar_arrive(&sh.p_full[n & 1]);
@@ -839,7 +877,7 @@ struct Softmax {
 
   // The sums of a stretch, the last of whose tiles is tile n of the CTA.
   __device__ __forceinline__ void store(const Stretch& st, uint32_t n) {
-    const Place<D> pv(2 * n + 1);
+    const Place<D, T8> pv(2 * n + 1);
     wait(&sh.empty[pv.slot], pv.turn & 1);
     tm_after_sync();
     const uint32_t cols = st.b.rows * group;
@@ -879,13 +917,13 @@ __device__ __forceinline__ void issue(const RowsAttend& a, const uint32_t* first
   const Stretch& s = walk.s;
   uint32_t n = 0, items = 0;
   const auto values = [&](uint32_t i, bool add) {  // O += P V of tile i
-    const Place<D> v(2 * i + 1);
+    const Place<D, T8> v(2 * i + 1);
     wait(&sh.full[v.slot], v.turn & 1);
     wait(&sh.p_full[i & 1], (i >> 1) & 1);
     tm_after_sync();
     tm_fence_shared();
     const uint32_t p = tmem + 128 + (i & 1) * 64;
-    const uint64_t dv = tm_desc(ring + v.slot * Ring<D>::bytes, Ring<D>::slab, 1024);
+    const uint64_t dv = tm_desc(ring + v.slot * Ring<D, T8>::bytes, Ring<D, T8>::slab, 1024);
     if (elect_one()) {
 #pragma unroll
       for (uint32_t k = 0; k < kTile / 16; ++k) {
@@ -900,17 +938,17 @@ __device__ __forceinline__ void issue(const RowsAttend& a, const uint32_t* first
   while (next(a, first, per, walk, lane)) {
     wait(&sh.q_full, items++ & 1);
     for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
-      const Place<D> k(2 * n);
+      const Place<D, T8> k(2 * n);
       wait(&sh.full[k.slot], k.turn & 1);
       if (n >= 2) wait(&sh.s_free[n & 1], ((n - 2) >> 1) & 1);
       tm_after_sync();
       tm_fence_shared();
-      const uint64_t dk = tm_desc(ring + k.slot * Ring<D>::bytes, 16, 1024);
+      const uint64_t dk = tm_desc(ring + k.slot * Ring<D, T8>::bytes, 16, 1024);
       if (elect_one()) {
 #pragma unroll
         for (uint32_t i = 0; i < D / 16; ++i)  // descriptors count in 16 bytes
-          tm_mma(tmem + (n & 1) * kTile, dq + ((i / 4) * Ring<D>::q_slab + (i % 4) * 32) / 16,
-                 dk + ((i / 4) * Ring<D>::slab + (i % 4) * 32) / 16, kQK, i != 0);
+          tm_mma(tmem + (n & 1) * kTile, dq + ((i / 4) * Ring<D, T8>::q_slab + (i % 4) * 32) / 16,
+                 dk + ((i / 4) * Ring<D, T8>::slab + (i % 4) * 32) / 16, kQK, i != 0);
         tm_commit(&sh.s_full[n & 1]);
         mbar_arrive(&sh.s_full[n & 1]);  // passes the loaders' notes on
         tm_commit(&sh.empty[k.slot]);
@@ -921,7 +959,7 @@ __device__ __forceinline__ void issue(const RowsAttend& a, const uint32_t* first
     values(n - 1, s.t1 - 1 != s.t0);
   }
   if (n) {  // every product is complete before the tensor memory goes
-    const Place<D> last(2 * n - 1);
+    const Place<D, T8> last(2 * n - 1);
     wait(&sh.empty[last.slot], last.turn & 1);
   }
 }
@@ -930,8 +968,7 @@ __device__ __forceinline__ void issue(const RowsAttend& a, const uint32_t* first
 
 template <int N>
 __device__ __forceinline__ void set_registers() {
-  if constexpr (N == kRegsLaunch) return;
-  else if constexpr (N > kRegsLaunch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+  if constexpr (N > kRegsLaunch) asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
   else asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
@@ -940,12 +977,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   extern __shared__ uint8_t raw[];
   const uint32_t tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   uint8_t* q_sm = raw + ((1024u - (smem_addr(raw) & 1023u)) & 1023u);
-  uint8_t* ring = q_sm + Ring<D>::q;
-  Notes<D>& sh = *reinterpret_cast<Notes<D>*>(ring + Ring<D>::slots * Ring<D>::bytes);
+  uint8_t* ring = q_sm + Ring<D, T8>::q;
+  Notes<D>& sh = *reinterpret_cast<Notes<D>*>(q_sm + Ring<D, T8>::all);
   uint32_t* first = reinterpret_cast<uint32_t*>(&sh + 1);  // [n_rows + 1]
   RowNote* note = notes_of(first, a.r.n_rows);
   if (tid == 0) {
-    for (uint32_t i = 0; i < Ring<D>::slots; ++i) {
+    for (uint32_t i = 0; i < Ring<D, T8>::slots; ++i) {
       mbar_init(&sh.full[i], kLoadThreads + (i % 2 == 0));
       mbar_init(&sh.empty[i], 1);
     }
@@ -954,6 +991,8 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
       mbar_init(&sh.s_free[i], kSoft);
       mbar_init(&sh.p_full[i], kSoft);
     }
+    if (T8)
+      for (uint32_t i = 0; i < Ring<D, T8>::info; ++i) mbar_init(&sh.v_notes[i], kLoadThreads);
     mbar_init(&sh.q_full, kSoft);
     mbar_fence_init();
   }
@@ -1042,7 +1081,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   }
   Waiter wait{a.wait_ns, a.status, false};
   if (tid < kSoft) {
-    set_registers<Regs<T8>::soft>();
+    set_registers<kRegsSoft>();
     Softmax<D, T8> x{a, q_sm, sh, tid, lane, tmem + ((32 * (warp % 4)) << 16), group, wait,
                      1.4426950408889634f / sqrtf((float)D), tid % kM, tid / kM, 2 + warp % 4};
     const Stretch& s = walk.s;
@@ -1056,10 +1095,10 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   } else if (warp == kIssuer) {
     issue<D, T8>(a, first, per, walk, lane, smem_addr(q_sm), smem_addr(ring), sh, tmem, wait);
   } else {
-    set_registers<Regs<T8>::load>();
+    set_registers<kRegsLoad>();
     const uint32_t i = tid - kSoft;
     if constexpr (T8) {
-      LoadTurbo8<D> x{a, ring, sh, i, i / 32, lane, i / (D / 16), i % (D / 16), wait, first, per, walk, walk.s};
+      LoadTurbo8<D> x{a, ring, sh, i, i / 32, lane, i / (D / 16), i % (D / 16), wait, first, per, walk, walk.s, {0, false}};
       x.run();
     } else {
       load_plain<D>(a, first, per, walk, ring, sh, i, wait);
@@ -1212,20 +1251,20 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ RowsA
   }
 }
 
-template <int D>
+template <int D, bool T8>
 constexpr uint32_t smem_of(uint32_t n_rows) {
-  return 1024 + Ring<D>::q + Ring<D>::slots * Ring<D>::bytes + sizeof(Notes<D>) + (n_rows + 2) / 2 * 8 + n_rows * sizeof(RowNote);
+  return 1024 + Ring<D, T8>::all + sizeof(Notes<D>) + (n_rows + 2) / 2 * 8 + n_rows * sizeof(RowNote);
 }
 template <int D, bool T8>
 bool allow() {
-  static_assert(smem_of<D>(kMaxQueries) <= 227 * 1024, "shared memory of a CTA");
-  return cudaFuncSetAttribute(rows_kernel<D, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<D>(kMaxQueries)) == cudaSuccess;
+  static_assert(smem_of<D, T8>(kMaxQueries) <= 227 * 1024, "shared memory of a CTA");
+  return cudaFuncSetAttribute(rows_kernel<D, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<D, T8>(kMaxQueries)) == cudaSuccess;
 }
 
 template <int D, bool T8>
 cudaError_t launch(const RowsAttend& a, cudaStream_t st) {
-  static_assert(2 * kMaxSeqs * 4 + 4 <= Ring<64>::slots * Ring<64>::bytes, "the rows' places");
-  cudaError_t e = launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D>(a.r.n_rows), st, a);
+  static_assert(2 * kMaxSeqs * 4 + 4 <= Ring<64, true>::all - Ring<64, true>::q, "the rows' places");
+  cudaError_t e = launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D, T8>(a.r.n_rows), st, a);
   if (e != cudaSuccess) return e;
   // few columns: a CTA for four of them, whose warps share their parts; many: a warp for four
   const uint32_t cols = a.r.n_rows * a.H;
