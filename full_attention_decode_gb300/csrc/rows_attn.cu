@@ -240,6 +240,12 @@ __device__ __forceinline__ uint32_t hmul2(uint32_t a, uint32_t b) {
 __device__ __forceinline__ uint32_t sw(uint32_t r, uint32_t j) { return r * 128 + ((j ^ (r & 7)) << 4); }
 __device__ __forceinline__ uint32_t bits_below(int64_t n) { return n <= 0 ? 0u : n >= 8 ? 0xffu : (1u << n) - 1u; }
 
+// One arrival for a warp, behind everything its lanes have done. (Each lane's own arrival is a turn at the barrier's word.)
+__device__ __forceinline__ void arrive_warp(uint64_t* bar, uint32_t lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
+}
+
 // Bounded waits of one thread: after one has run out no other waits.
 struct Waiter {
   uint64_t limit;
@@ -504,7 +510,7 @@ struct LoadTurbo8 {
       if (V && (sc[j] & 0x7f80u) == 0x7f80u) y = 0.f;
       f[j] = pack_f16(y, y);
     }
-    if (V) mbar_arrive(&sh.v_notes[n % R::info]);
+    if (V) arrive_warp(&sh.v_notes[n % R::info], lane);
     const Place<D, true> at(2 * n + V);
     if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
     uint8_t* slab = ring + at.slot * R::bytes + (c / 4) * R::slab;
@@ -534,12 +540,9 @@ struct LoadTurbo8 {
       const bool any = __any_sync(0xffffffffu, bad);
       if (lane == 0) sh.dirty[n % R::info][warp] = any;
     }
+    if (!V && tid == 0) sh.valid[n % R::info] = sh.ahead[n % 8];
     tm_fence_shared();
-    mbar_arrive(&sh.full[at.slot]);
-    if (!V && tid == 0) {
-      sh.valid[n % R::info] = sh.ahead[n % 8];
-      mbar_arrive(&sh.full[at.slot]);
-    }
+    arrive_warp(&sh.full[at.slot], lane);
   }
   __device__ __forceinline__ void run() {
     constexpr uint32_t N = R::raw;  // halves on their way: K0, K1, V0, K2, V1, ...
@@ -658,7 +661,7 @@ struct Softmax {
       }
     }
     tm_fence_shared();
-    mbar_arrive(&sh.q_full);
+    arrive_warp(&sh.q_full, lane);
   }
 
   __device__ __forceinline__ void begin(const Block& b) {
@@ -746,7 +749,7 @@ struct Softmax {
       for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
       tm_before_sync();
     }
-    mbar_arrive(&sh.s_free[n & 1]);
+    arrive_warp(&sh.s_free[n & 1], lane);
     if (busy) {
       if constexpr (T8) {
         const float sc = scale * (live ? sh.q_scale[row] : 0.f);
@@ -858,7 +861,7 @@ struct Softmax {
       const uint2 u = *reinterpret_cast<const uint2*>(sh.dirty[n % Ring<D, T8>::info]);
       dirty = (u.x | u.y) != 0;
     }
-    mbar_arrive(&sh.p_full[n & 1]);
+    arrive_warp(&sh.p_full[n & 1], lane);
     if (dirty) {
       wait(&sh.empty[pv.slot], pv.turn & 1);
       float w[kHalf];
@@ -983,17 +986,17 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   RowNote* note = notes_of(first, a.r.n_rows);
   if (tid == 0) {
     for (uint32_t i = 0; i < Ring<D, T8>::slots; ++i) {
-      mbar_init(&sh.full[i], kLoadThreads + (i % 2 == 0));
+      mbar_init(&sh.full[i], T8 ? kLoaders : kLoadThreads + (i % 2 == 0));
       mbar_init(&sh.empty[i], 1);
     }
     for (uint32_t i = 0; i < 2; ++i) {
       mbar_init(&sh.s_full[i], 2);
-      mbar_init(&sh.s_free[i], kSoft);
-      mbar_init(&sh.p_full[i], kSoft);
+      mbar_init(&sh.s_free[i], kSoft / 32);
+      mbar_init(&sh.p_full[i], kSoft / 32);
     }
     if (T8)
-      for (uint32_t i = 0; i < Ring<D, T8>::info; ++i) mbar_init(&sh.v_notes[i], kLoadThreads);
-    mbar_init(&sh.q_full, kSoft);
+      for (uint32_t i = 0; i < Ring<D, T8>::info; ++i) mbar_init(&sh.v_notes[i], kLoaders);
+    mbar_init(&sh.q_full, kSoft / 32);
     mbar_fence_init();
   }
   constexpr uint32_t kIssuer = kRowsThreads / 32 - 1;
