@@ -1327,9 +1327,9 @@ int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,
 
 namespace {
 
-// Scratch of these operators: the status word's 256 bytes, then the attention's work space.
+// Scratch of these operators: the status word, the cache operators' counters, then the attention's work space.
 size_t rows_need(const qwen35_config* c, uint32_t n_rows) {
-  return kCacheTickets + q35c::rows_work_bytes(n_rows, c->num_heads, c->num_kv_heads, c->head_dim);
+  return kCacheWork + q35c::rows_work_bytes(n_rows, c->num_heads, c->num_kv_heads, c->head_dim);
 }
 bool aligned4(const void* p) { return (uintptr_t)p % 4 == 0; }
 
@@ -1350,7 +1350,8 @@ int rows_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qw
   a.gate = gate;
   a.gate_stride = gate_stride;
   a.out = out;
-  a.work = static_cast<uint8_t*>(scratch) + kCacheTickets;
+  a.tickets = reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(scratch) + kCacheTickets);
+  a.work = static_cast<uint8_t*>(scratch) + kCacheWork;
   a.wide = (uintptr_t)a.work % 32 == 0;
   a.sms = (uint32_t)num_sms();
   a.H = cfg->num_heads;

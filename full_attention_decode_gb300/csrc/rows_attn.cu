@@ -111,7 +111,7 @@ __device__ __forceinline__ Block block_of(const RowsAttend& a, uint32_t row, uin
 // A CTA's stretch of an item.
 struct Stretch {
   Block b;
-  uint32_t g, t0, t1, c0;
+  uint32_t g, t0, t1, c0, c1;
   // tiles of which every row of the block sees every token: [0, whole0) and [whole1, whole2)
   uint32_t whole0, whole1, whole2;
   __device__ __forceinline__ bool whole(uint32_t t) const { return t < whole0 || (t >= whole1 && t < whole2); }
@@ -153,6 +153,7 @@ __device__ __forceinline__ bool next(const RowsAttend& a, const uint32_t* first,
       k.s.t0 = max(at, kLead) - kLead;
       k.s.t1 = max(at + used, kLead) - kLead;
       k.s.c0 = (w - at + kLead) / per;
+      k.s.c1 = (w - at + length - 1) / per;
       set_whole(a, k.s);
       w += used;
       more = k.s.t0 != k.s.t1;
@@ -169,7 +170,7 @@ __device__ __forceinline__ bool next(const RowsAttend& a, const uint32_t* first,
 template <uint32_t kInfo>
 struct NotesOf {
   uint64_t full[8], empty[8], s_full[2], s_free[2], p_full[2], v_notes[kInfo], q_full;
-  uint32_t tmem;
+  uint32_t tmem, last;
   uint32_t sums[kRowsThreads / 32];
   uint32_t valid[kInfo];             // octets of the tile that hold tokens
   uint32_t ahead[8];                 // Turbo8: of the tiles that are on their way
@@ -582,6 +583,138 @@ struct LoadTurbo8 {
   }
 };
 
+// ------------------------------------------------------------------ the join
+
+// Columns' parts added up. A warp takes four neighbouring columns of a row's heads (four lanes read 128 bytes side by
+// side), a lane D / 8 / 8 pieces of eight dims of one; TEAMS warps of a CTA take a column's parts in turn.
+// Column c = row H + head of the output, whose item lies in CTAs c0 .. c0 + n - 1 (0: none) and has `cols` columns from
+// `first` on, this one the col-th. sync: of the teams' threads, sums theirs.
+template <int D, bool T8, int TEAMS, typename Sync>
+__device__ __forceinline__ void join_columns(const RowsAttend& a, const Work& work, uint32_t sub, uint32_t lane, uint32_t c,
+                                             uint32_t c0, uint32_t n, uint32_t cols, uint32_t col, size_t first,
+                                             float (*sums)[D / 8][32], Sync&& sync) {
+  constexpr uint32_t P = D / 64;  // pieces of a lane
+  const uint32_t l8 = lane / 4;
+  const auto ml = [&](uint32_t k) { return __ldcg(k ? work.cont_ml + (size_t)(c0 + k) * kM + col : work.nat_ml + first + col); };
+  // the largest maximum and (T8) V's relative to it, the sum: a part each of the column's eight lanes, in rounds
+  bool ok = n > 0;
+  float M = -INFINITY, V = -INFINITY, L = 0.f;
+  for (uint32_t k = l8; k < n; k += 8) {
+    const float4 x = ml(k);
+    if (x.y < 0.f) ok = false;
+    M = fmaxf(M, x.x);
+  }
+#pragma unroll
+  for (uint32_t w = 4; w < 32; w <<= 1) {
+    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
+    ok &= __shfl_xor_sync(0xffffffffu, ok, w);
+  }
+  const float mu = finite_or_0(M);
+  const auto exponent = [&](const float4& x) { return T8 ? x.z + (finite_or_0(x.x) - mu) : x.x - mu; };  // of its sums O
+  for (uint32_t k = l8; k < n; k += 8) {
+    const float4 x = ml(k);
+    if (T8) V = fmaxf(V, exponent(x));
+    L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - mu);
+  }
+#pragma unroll
+  for (uint32_t w = 4; w < 32; w <<= 1) {
+    V = fmaxf(V, __shfl_xor_sync(0xffffffffu, V, w));
+    L += __shfl_xor_sync(0xffffffffu, L, w);
+  }
+  const float down = T8 ? finite_or_0(V) : 0.f;
+  float x[P][8] = {};
+#pragma unroll 2
+  for (uint32_t k = sub; k < n; k += TEAMS) {
+    const float4 y = ml(k);
+    const float f = y.x == -INFINITY || (T8 && y.z == -INFINITY) ? 0.f : ex2(exponent(y) - down);
+    const float* from = k ? work.cont + (size_t)(c0 + k) * kM * D + col * 8 : work.nat + first * D + col * 8;
+    const uint32_t wide = k ? kM : cols;
+    float4 u[P][2];
+#pragma unroll
+    for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) u[i][j] = __ldcg(reinterpret_cast<const float4*>(from + (size_t)(l8 + 8 * i) * 8 * wide) + j);
+    if (f != 0.f)
+#pragma unroll
+      for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          x[i][4 * j] = fmaf(u[i][j].x, f, x[i][4 * j]);
+          x[i][4 * j + 1] = fmaf(u[i][j].y, f, x[i][4 * j + 1]);
+          x[i][4 * j + 2] = fmaf(u[i][j].z, f, x[i][4 * j + 2]);
+          x[i][4 * j + 3] = fmaf(u[i][j].w, f, x[i][4 * j + 3]);
+        }
+  }
+  if constexpr (TEAMS > 1) {
+#pragma unroll
+    for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sums[sub][8 * i + e][lane] = x[i][e];
+    sync();
+    if (sub) return;
+#pragma unroll 1
+    for (uint32_t k = 1; k < TEAMS; ++k)
+#pragma unroll
+      for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) x[i][e] += sums[k][8 * i + e][lane];
+  }
+  const float inv = L == 0.f ? 0.f : 1.f / L, up = T8 ? ex2(0.5f * down) : 1.f;
+#pragma unroll
+  for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[i][e] = L == 0.f ? 0.f : T8 ? x[i][e] * inv * up * up : x[i][e] * inv;
+  if constexpr (T8) {  // rotated back: dim 8 (l8 + 8 i) + e
+#pragma unroll
+    for (uint32_t i = 0; i < P; ++i) {
+#pragma unroll
+      for (int hb = 1; hb < 8; hb <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+          if (!(e & hb)) {
+            const float u = x[i][e], w = x[i][e + hb];
+            x[i][e] = u + w;
+            x[i][e + hb] = u - w;
+          }
+#pragma unroll
+      for (uint32_t w = 4; w < 32; w <<= 1)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const float o = __shfl_xor_sync(0xffffffffu, x[i][e], w);
+          x[i][e] = lane & w ? o - x[i][e] : x[i][e] + o;
+        }
+    }
+#pragma unroll
+    for (uint32_t hb = 1; hb < P; hb <<= 1)
+#pragma unroll
+      for (uint32_t i = 0; i < P; ++i)
+        if (!(i & hb))
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const float u = x[i][e], w = x[i + hb][e];
+            x[i][e] = u + w;
+            x[i + hb][e] = u - w;
+          }
+    const float norm = rsqrtf((float)D);
+#pragma unroll
+    for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] *= norm;
+  }
+  if (!ok) return;
+#pragma unroll
+  for (uint32_t i = 0; i < P; ++i) {
+    const uint32_t d = 8 * (l8 + 8 * i);
+    if (a.gate) {
+      float g[8];
+      unpack8(*reinterpret_cast<const uint4*>(a.gate + (size_t)c * a.gate_stride + d), g);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[i][e] *= sigmoidf_(g[e]);
+    }
+    *reinterpret_cast<uint4*>(a.out + (size_t)c * D + d) = pack8(x[i]);
+  }
+}
+
 // ------------------------------------------------------------------ softmax
 
 // V's elements of a half of a tile (tokens j0 ..) that are no numbers, which the loaders took out: weight w[j] times each
@@ -631,33 +764,47 @@ struct Softmax {
   __device__ __forceinline__ uint32_t p_col(uint32_t n) const { return tmem + 128 + (n & 1) * 64 + half * (kHalf / 2); }
   __device__ __forceinline__ uint32_t o_col() const { return tmem + 256; }
 
+  // Each thread copies the pieces that it goes on with: four lanes a column, sixteen dims of each 64 a lane.
   __device__ __forceinline__ void put_q(const Block& b, uint32_t g) {
-    constexpr uint32_t LPR = D / 8, PER = kSoft / LPR;
-    const uint32_t cols = b.rows * group, j = tid % LPR;
-    const auto from = [&](uint32_t col) { return a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D + 8 * j; };
-    uint8_t* to = q_sm + (j / 8) * Ring<D, T8>::q_slab;
-    for (uint32_t col = tid / LPR; col < cols; col += PER) cp16(smem_addr(to + sw(col, j % 8)), from(col), true);
+    constexpr uint32_t P = D / 64, PER = kSoft / 4;
+    const uint32_t cols = b.rows * group, l4 = tid & 3;
+    for (uint32_t col = tid / 4; col < cols; col += PER) {
+      const uint16_t* from = a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D + 16 * l4;
+#pragma unroll
+      for (uint32_t i = 0; i < P; ++i)
+#pragma unroll
+        for (uint32_t h = 0; h < 2; ++h) cp16(smem_addr(q_sm + i * Ring<D, T8>::q_slab + sw(col, 2 * l4 + h)), from + 64 * i + 8 * h, true);
+    }
     asm volatile("cp.async.wait_all;" ::: "memory");
-    if constexpr (T8) {  // each lane its own pieces, where they lie
-#pragma unroll 4
+    if constexpr (T8) {
+#pragma unroll 1
       for (uint32_t c0 = 0; c0 < cols; c0 += PER) {
-        const uint32_t col = c0 + tid / LPR;
-        uint4* at = reinterpret_cast<uint4*>(to + sw(col, j % 8));
-        uint4 u = make_uint4(0u, 0u, 0u, 0u);
-        if (col < cols) u = *at;
-        float x[8], mx = 0.f;
-        unpack8(u, x);
-        wht8<LPR>(x, lane);
+        const uint32_t col = c0 + tid / 4;
+        float2 x[D / 8];
+        float mx = 0.f;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) mx = fmaxf(mx, fabsf(x[e]));
+        for (uint32_t i = 0; i < 2 * P; ++i) {
+          const uint4 u = col < cols ? *reinterpret_cast<const uint4*>(q_sm + i / 2 * Ring<D, T8>::q_slab + sw(col, 2 * l4 + i % 2))
+                                     : make_uint4(0u, 0u, 0u, 0u);
+          x[4 * i] = make_float2(bf16lo(u.x), bf16hi(u.x));
+          x[4 * i + 1] = make_float2(bf16lo(u.y), bf16hi(u.y));
+          x[4 * i + 2] = make_float2(bf16lo(u.z), bf16hi(u.z));
+          x[4 * i + 3] = make_float2(bf16lo(u.w), bf16hi(u.w));
+        }
+        wht_quad<D>(x, lane);
 #pragma unroll
-        for (uint32_t w = 1; w < LPR; w <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, w));
+        for (uint32_t i = 0; i < D / 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
         const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127, -126), 126);
         const float f = pow2(-e2);
-        if (j == 0 && col < cols) sh.q_scale[col] = pow2(e2);
-        if (col < cols)
-          *at = make_uint4(pack_f16(x[0] * f, x[1] * f), pack_f16(x[2] * f, x[3] * f), pack_f16(x[4] * f, x[5] * f),
-                           pack_f16(x[6] * f, x[7] * f));
+        if (l4 == 0 && col < cols) sh.q_scale[col] = pow2(e2);
+#pragma unroll
+        for (uint32_t i = 0; i < 2 * P; ++i)
+          if (col < cols)
+            *reinterpret_cast<uint4*>(q_sm + i / 2 * Ring<D, T8>::q_slab + sw(col, 2 * l4 + i % 2)) =
+                make_uint4(pack_f16(x[4 * i].x * f, x[4 * i].y * f), pack_f16(x[4 * i + 1].x * f, x[4 * i + 1].y * f),
+                           pack_f16(x[4 * i + 2].x * f, x[4 * i + 2].y * f), pack_f16(x[4 * i + 3].x * f, x[4 * i + 3].y * f));
       }
     }
     tm_fence_shared();
@@ -878,6 +1025,31 @@ struct Softmax {
     }
   }
 
+  // a.here: the last of an item's CTAs adds its parts up. One item at most begins in CTA c0 and goes on behind it: its ticket.
+  __device__ void finish(const Stretch& st) {
+    const Work work = work_of(a.work, a.r.n_rows, a.H, D);
+    const uint32_t cols = st.b.rows * group, n = st.c1 - st.c0 + 1;
+    if (n > 1) {
+      named_barrier(1, kSoft);  // the CTA's part lies before this, and the count's release and acquire put it before the last one's reads
+      if (tid == 0) {
+        const uint32_t had = count_up(a.tickets + st.c0);
+        sh.last = had + 1 == n;
+        if (had >= n) set_status(a.status, kStatusInvalid);
+        if (had + 1 >= n) a.tickets[st.c0] = 0;
+      }
+    }
+    named_barrier(1, kSoft);
+    if (n > 1 && !sh.last) return;
+    float(*sums)[D / 8][32] = reinterpret_cast<float(*)[D / 8][32]>(q_sm);  // the products are done with Q
+    for (uint32_t c4 = 0; c4 < cols; c4 += 4) {
+      const uint32_t col = c4 + lane % 4, r = st.b.row + col / group;
+      const bool in = col < cols;
+      join_columns<D, T8, 8>(a, work, tid / 32, lane, in ? r * a.H + st.g * group + col % group : 0, st.c0, in ? n : 0, cols,
+                             in ? col : 0, (size_t)st.b.row * a.H + st.g * cols, sums, [] { named_barrier(1, kSoft); });
+      named_barrier(1, kSoft);  // the sums are free
+    }
+  }
+
   // The sums of a stretch, the last of whose tiles is tile n of the CTA.
   __device__ __forceinline__ void store(const Stretch& st, uint32_t n) {
     const Place<D, T8> pv(2 * n + 1);
@@ -1094,6 +1266,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
       x.begin(s.b);
       for (uint32_t t = s.t0; t < s.t1; ++t, ++n) x.tile(s, t, n);
       x.store(s, n - 1);
+      if (a.here) x.finish(s);
     }
   } else if (warp == kIssuer) {
     issue<D, T8>(a, first, per, walk, lane, smem_addr(q_sm), smem_addr(ring), sh, tmem, wait);
@@ -1115,16 +1288,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   }
 }
 
-// ------------------------------------------------------------------ the join
-
-// Columns' parts added up. A warp takes four neighbouring columns of a row's heads (four lanes read 128 bytes side by
-// side), a lane D / 8 / 8 pieces of eight dims of one; TEAMS warps of a CTA take a column's parts in turn.
 template <int D, bool T8, int TEAMS>
 __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ RowsAttend a) {
-  constexpr uint32_t P = D / 64, FOURS = 8 / TEAMS;  // pieces of a lane, fours of columns of a CTA
-  __shared__ float sums[TEAMS > 1 ? TEAMS : 1][TEAMS > 1 ? 8 * P : 1][32];
-  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = warp % TEAMS;
-  const uint32_t group = a.H / a.c.Hkv, c = blockIdx.x * FOURS * 4 + warp / TEAMS * 4 + lane % 4, l8 = lane / 4;
+  constexpr uint32_t FOURS = 8 / TEAMS;  // fours of columns of a CTA
+  __shared__ float sums[TEAMS > 1 ? TEAMS : 1][D / 8][32];
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t group = a.H / a.c.Hkv, c = blockIdx.x * FOURS * 4 + warp / TEAMS * 4 + lane % 4;
   const uint32_t r = c / a.H, h = c % a.H;
   const bool in = r < a.r.n_rows;
   const Work work = work_of(a.work, a.r.n_rows, a.H, D);
@@ -1132,126 +1301,9 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ RowsA
   pdl_launch();
   const uint32_t rec = in ? work.rec[r * a.c.Hkv + h / group] : 0;
   const uint32_t c0 = rec & 255u, n = rec & kRecOk ? (rec >> 8 & 255u) - c0 + 1 : 0, off = rec >> 16 & 127u;
-  const uint32_t cols = ((rec >> 23 & 127u) + 1) * group, col = off * group + h % group;  // the item's, and this one among them
-  const size_t first = in ? (size_t)(r - off) * a.H + h / group * cols : 0;
-  const auto ml = [&](uint32_t k) { return k ? work.cont_ml[(size_t)(c0 + k) * kM + col] : work.nat_ml[first + col]; };
-  // the largest maximum and (T8) V's relative to it, the sum: a part each of the column's eight lanes, in rounds
-  bool ok = n > 0;
-  float M = -INFINITY, V = -INFINITY, L = 0.f;
-  for (uint32_t k = l8; k < n; k += 8) {
-    const float4 x = ml(k);
-    if (x.y < 0.f) ok = false;
-    M = fmaxf(M, x.x);
-  }
-#pragma unroll
-  for (uint32_t w = 4; w < 32; w <<= 1) {
-    M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
-    ok &= __shfl_xor_sync(0xffffffffu, ok, w);
-  }
-  const float mu = finite_or_0(M);
-  const auto exponent = [&](const float4& x) { return T8 ? x.z + (finite_or_0(x.x) - mu) : x.x - mu; };  // of its sums O
-  for (uint32_t k = l8; k < n; k += 8) {
-    const float4 x = ml(k);
-    if (T8) V = fmaxf(V, exponent(x));
-    L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - mu);
-  }
-#pragma unroll
-  for (uint32_t w = 4; w < 32; w <<= 1) {
-    V = fmaxf(V, __shfl_xor_sync(0xffffffffu, V, w));
-    L += __shfl_xor_sync(0xffffffffu, L, w);
-  }
-  const float down = T8 ? finite_or_0(V) : 0.f;
-  float x[P][8] = {};
-#pragma unroll 2
-  for (uint32_t k = sub; k < n; k += TEAMS) {
-    const float4 y = ml(k);
-    const float f = y.x == -INFINITY || (T8 && y.z == -INFINITY) ? 0.f : ex2(exponent(y) - down);
-    const float* from = k ? work.cont + (size_t)(c0 + k) * kM * D + col * 8 : work.nat + first * D + col * 8;
-    const uint32_t wide = k ? kM : cols;
-    float4 u[P][2];
-#pragma unroll
-    for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) u[i][j] = __ldcg(reinterpret_cast<const float4*>(from + (size_t)(l8 + 8 * i) * 8 * wide) + j);
-    if (f != 0.f)
-#pragma unroll
-      for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          x[i][4 * j] = fmaf(u[i][j].x, f, x[i][4 * j]);
-          x[i][4 * j + 1] = fmaf(u[i][j].y, f, x[i][4 * j + 1]);
-          x[i][4 * j + 2] = fmaf(u[i][j].z, f, x[i][4 * j + 2]);
-          x[i][4 * j + 3] = fmaf(u[i][j].w, f, x[i][4 * j + 3]);
-        }
-  }
-  if constexpr (TEAMS > 1) {
-#pragma unroll
-    for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sums[sub][8 * i + e][lane] = x[i][e];
-    __syncthreads();
-    if (sub) return;
-#pragma unroll 1
-    for (uint32_t k = 1; k < TEAMS; ++k)
-#pragma unroll
-      for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] += sums[k][8 * i + e][lane];
-  }
-  const float inv = L == 0.f ? 0.f : 1.f / L, up = T8 ? ex2(0.5f * down) : 1.f;
-#pragma unroll
-  for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[i][e] = L == 0.f ? 0.f : T8 ? x[i][e] * inv * up * up : x[i][e] * inv;
-  if constexpr (T8) {  // rotated back: dim 8 (l8 + 8 i) + e
-#pragma unroll
-    for (uint32_t i = 0; i < P; ++i) {
-#pragma unroll
-      for (int hb = 1; hb < 8; hb <<= 1)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!(e & hb)) {
-            const float u = x[i][e], w = x[i][e + hb];
-            x[i][e] = u + w;
-            x[i][e + hb] = u - w;
-          }
-#pragma unroll
-      for (uint32_t w = 4; w < 32; w <<= 1)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl_xor_sync(0xffffffffu, x[i][e], w);
-          x[i][e] = lane & w ? o - x[i][e] : x[i][e] + o;
-        }
-    }
-#pragma unroll
-    for (uint32_t hb = 1; hb < P; hb <<= 1)
-#pragma unroll
-      for (uint32_t i = 0; i < P; ++i)
-        if (!(i & hb))
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float u = x[i][e], w = x[i + hb][e];
-            x[i][e] = u + w;
-            x[i + hb][e] = u - w;
-          }
-    const float norm = rsqrtf((float)D);
-#pragma unroll
-    for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] *= norm;
-  }
-  if (!ok) return;
-#pragma unroll
-  for (uint32_t i = 0; i < P; ++i) {
-    const uint32_t d = 8 * (l8 + 8 * i);
-    if (a.gate) {
-      float g[8];
-      unpack8(*reinterpret_cast<const uint4*>(a.gate + (size_t)c * a.gate_stride + d), g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] *= sigmoidf_(g[e]);
-    }
-    *reinterpret_cast<uint4*>(a.out + (size_t)c * D + d) = pack8(x[i]);
-  }
+  const uint32_t cols = ((rec >> 23 & 127u) + 1) * group;
+  join_columns<D, T8, TEAMS>(a, work, warp % TEAMS, lane, c, c0, n, cols, off * group + h % group,
+                             in ? (size_t)(r - off) * a.H + h / group * cols : 0, sums, [] { __syncthreads(); });
 }
 
 template <int D, bool T8>
@@ -1269,6 +1321,7 @@ cudaError_t launch(const RowsAttend& a, cudaStream_t st) {
   static_assert(2 * kMaxSeqs * 4 + 4 <= Ring<64, true>::all - Ring<64, true>::q, "the rows' places");
   cudaError_t e = launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D, T8>(a.r.n_rows), st, a);
   if (e != cudaSuccess) return e;
+  if (a.here) return cudaSuccess;
   // few columns: a CTA for four of them, whose warps share their parts; many: a warp for four
   const uint32_t cols = a.r.n_rows * a.H;
   if (cols <= 2048) return launch_early(join_kernel<D, T8, 8>, dim3((cols + 3) / 4), 256, 0, st, a);
@@ -1287,7 +1340,11 @@ cudaError_t rows_attend_attributes() {
              : cudaErrorInvalidValue;
 }
 
-cudaError_t rows_attend(const RowsAttend& a, cudaStream_t st) {
+cudaError_t rows_attend(const RowsAttend& args, cudaStream_t st) {
+  RowsAttend a = args;
+  // An item of few columns is joined where its last part is made (one row through a window of 512: us by a second launch 17.2,
+  // here ....); one of many by many CTAs.
+  a.here = a.H / a.c.Hkv * (a.r.row_start ? a.r.n_rows : 1) <= 8;
   const bool t8 = a.c.ks != nullptr;
 #define CALL(DD) return t8 ? launch<DD, true>(a, st) : launch<DD, false>(a, st)
   switch (a.c.D) {

@@ -49,6 +49,8 @@ struct RowsAttend {
   const uint16_t* q;     // [n_rows][H][D]
   const uint16_t* gate;  // as Attend's
   uint16_t* out;         // [n_rows][H][D]
+  uint32_t* tickets;     // [kMaxCtas], zero between calls
+  bool here;             // set by rows_attend(): the parts are added up by the last CTA of an item, not by a second launch
   uint8_t* work;         // rows_work_bytes
   bool wide;             // it is 32-byte aligned
   uint32_t sms;          // of the GPU
