@@ -181,6 +181,7 @@ struct NotesOf {
   float sum[kM];         // the second thread's sum
   int32_t parent[kMaxNodes];
   Walk walk[kRowsThreads / 32];
+  int32_t pos[32], start[33];  // few rows: where they are
 };
 
 template <int D>
@@ -1173,14 +1174,56 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   }
   constexpr uint32_t kIssuer = kRowsThreads / 32 - 1;
   if (warp == kIssuer) tm_alloc(&sh.tmem, 512);
+  tm_before_sync();
+  __syncthreads();
+  tm_after_sync();
+  const uint32_t tmem = sh.tmem;
   pdl_wait();
   pdl_launch();
 
-  // ---- the rows' places, looked up in shared memory (the ring is empty), and the line of tiles
+  // ---- the rows' places, looked up in shared memory, and the line of tiles
   const uint32_t group = a.H / a.c.Hkv, RB = kM / group;
+  // Row r's note, and its tiles if a block begins with it.
+  const auto row_tiles = [&](const Rows& here, uint32_t r) {
+    uint32_t seq = 0, pos = 0, index = 0, left = 1, v = 0;
+    RowKind kind = locate(here, a.c.capacity, r, seq, pos, index, left);
+    if (kind == kRowOk && (index > r || (a.parent && index >= kMaxNodes))) kind = kRowBad;
+    if (kind == kRowBad && blockIdx.x == 0) set_status(a.status, kStatusRange);
+    RowNote x = {pos, seq | min(index, 2047u) << 12 | (uint32_t)(kind == kRowOk) << 31};
+    if (kind == kRowOk && index % RB == 0) {
+      uint32_t rows = min(min(min(RB, left), a.r.n_rows - r), a.c.capacity - pos);
+      if (a.parent) rows = min(rows, kMaxNodes - index);
+      v = block_of(a, r, rows, x).tiles() + kLead;
+      x.bits |= rows << 23;
+    }
+    note[r] = x;
+    return v;
+  };
   Rows here = a.r;
-  {
-    int32_t* pos = reinterpret_cast<int32_t*>(ring);
+  uint32_t base = 0;
+  if (a.r.n_rows <= 32 && a.r.n_seqs <= 32) {
+    // Few rows: every warp looks them up for itself, the same values into the same places, and goes on without the others
+    if (lane < a.r.n_seqs) sh.pos[lane] = a.r.pos[lane];
+    if (a.r.row_start) {
+      if (lane < a.r.n_seqs) sh.start[lane] = a.r.row_start[lane];
+      if (lane == 0) sh.start[a.r.n_seqs] = a.r.row_start[a.r.n_seqs];
+      here.row_start = sh.start;
+    }
+    here.pos = sh.pos;
+    __syncwarp();
+    const uint32_t v = lane < a.r.n_rows ? row_tiles(here, lane) : 0;
+    uint32_t x = v;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+      if (lane >= (uint32_t)o) x += y;
+    }
+    if (lane < a.r.n_rows) first[lane] = x - v;
+    base = __shfl_sync(0xffffffffu, x, 31);
+    if (lane == 0) first[a.r.n_rows] = base;
+    __syncwarp();
+  } else {
+    int32_t* pos = reinterpret_cast<int32_t*>(ring);  // which is empty
     int32_t* start = pos + kMaxSeqs;
     for (uint32_t i = tid; i < a.r.n_seqs; i += kRowsThreads) pos[i] = a.r.pos[i];
     if (a.r.row_start)
@@ -1188,42 +1231,26 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     here.pos = pos;
     if (a.r.row_start) here.row_start = start;
     __syncthreads();
-  }
-  uint32_t base = 0;
-  for (uint32_t r0 = 0; r0 < a.r.n_rows; r0 += kRowsThreads) {
-    const uint32_t r = r0 + tid;
-    uint32_t v = 0;
-    if (r < a.r.n_rows) {
-      uint32_t seq = 0, pos = 0, index = 0, left = 1, rows = 0;
-      RowKind kind = locate(here, a.c.capacity, r, seq, pos, index, left);
-      if (kind == kRowOk && (index > r || (a.parent && index >= kMaxNodes))) kind = kRowBad;
-      if (kind == kRowBad && blockIdx.x == 0) set_status(a.status, kStatusRange);
-      RowNote x = {pos, seq | min(index, 2047u) << 12 | (uint32_t)(kind == kRowOk) << 31};
-      if (kind == kRowOk && index % RB == 0) {
-        rows = min(min(min(RB, left), a.r.n_rows - r), a.c.capacity - pos);
-        if (a.parent) rows = min(rows, kMaxNodes - index);
-        v = block_of(a, r, rows, x).tiles() + kLead;
-        x.bits |= rows << 23;
+    for (uint32_t r0 = 0; r0 < a.r.n_rows; r0 += kRowsThreads) {
+      const uint32_t r = r0 + tid, v = r < a.r.n_rows ? row_tiles(here, r) : 0;
+      uint32_t x = v;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+        if (lane >= (uint32_t)o) x += y;
       }
-      note[r] = x;
-    }
-    uint32_t x = v;
+      if (lane == 31) sh.sums[warp] = x;
+      __syncthreads();
+      uint32_t before = base;
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
-      if (lane >= (uint32_t)o) x += y;
+      for (uint32_t w = 0; w < kRowsThreads / 32; ++w) {
+        before += w < warp ? sh.sums[w] : 0;
+        base += sh.sums[w];
+      }
+      if (r < a.r.n_rows) first[r] = before + x - v;
+      if (r == a.r.n_rows - 1) first[r + 1] = before + x;
+      __syncthreads();
     }
-    if (lane == 31) sh.sums[warp] = x;
-    __syncthreads();
-    uint32_t before = base;
-#pragma unroll
-    for (uint32_t w = 0; w < kRowsThreads / 32; ++w) {
-      before += w < warp ? sh.sums[w] : 0;
-      base += sh.sums[w];
-    }
-    if (r < a.r.n_rows) first[r] = before + x - v;
-    if (r == a.r.n_rows - 1) first[r + 1] = before + x;
-    __syncthreads();
   }
   const uint32_t total = base * a.c.Hkv, per = max((total + gridDim.x - 1) / gridDim.x, kLeast);
   const Work work = work_of(a.work, a.r.n_rows, a.H, D);
@@ -1237,10 +1264,6 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
     }
     work.rec[i] = rec;
   }
-  tm_before_sync();
-  __syncthreads();
-  tm_after_sync();
-  const uint32_t tmem = sh.tmem;
   const uint64_t w64 = (uint64_t)blockIdx.x * per;
   Walk& walk = sh.walk[warp];
   if (lane == 0) {
@@ -1344,7 +1367,7 @@ cudaError_t rows_attend(const RowsAttend& args, cudaStream_t st) {
   RowsAttend a = args;
   // An item of few columns is joined where its last part is made (one row through a window of 512: us by a second launch 17.2,
   // here ....); one of many by many CTAs.
-  a.here = a.H / a.c.Hkv * (a.r.row_start ? a.r.n_rows : 1) <= 8;
+  a.here = a.H / a.c.Hkv * (a.r.row_start ? a.r.n_rows : 1) <= 8 && a.r.n_rows * a.H <= 128;
   const bool t8 = a.c.ks != nullptr;
 #define CALL(DD) return t8 ? launch<DD, true>(a, st) : launch<DD, false>(a, st)
   switch (a.c.D) {
