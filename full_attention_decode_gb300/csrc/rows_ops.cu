@@ -92,8 +92,9 @@ constexpr uint32_t kTeams = kThreads / 4;
 constexpr uint32_t kRopeRows = 8;  // rows of a CTA at most
 
 // A CTA takes a few rows: their places and angles once for all heads, then four lanes a head's row, q-heads, then k, then v.
-// Bound by the instructions of norm, rotation and quantiser where there are many rows, by the chain of loads of the place where
-// there are few.
+// Bound by the instructions of norm, rotation and quantiser where there are many rows (five prompts of 700 to 4097 tokens into
+// Turbo8, 24 heads of 256: 99 us; a warp a head's row with its own angles 159), by the launch and the chain of loads of the place
+// where there are few (8 rows: 6.7 us).
 template <int D, bool T8>
 __global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ RopeAppend a, uint32_t rows) {
   constexpr int P = D / 64;
@@ -273,8 +274,9 @@ __global__ void __launch_bounds__(kThreads) keep_kernel(const __grid_constant__ 
 
 cudaError_t rope_append(const RopeAppend& a, cudaStream_t st) {
   const bool t8 = a.c.ks != nullptr;
-  // a row a CTA until the GPU is full, then more, which share the places' latency
-  const uint32_t rows = std::min(std::max(a.r.n_rows / 304, 1u), kRopeRows);
+  // A row a CTA while one wave of two CTAs an SM takes all, then as many as keep it one wave, which share the places' latency:
+  // 64 rows (bf16, 24 heads of 256) by 1, 2 and 8 a CTA take 5.8, 6.2 and 10.6 us, 608 rows 9.3, 6.6 and 11.0, 8192 rows 105, 67 and 55.
+  const uint32_t rows = std::min((a.r.n_rows + 303) / 304, kRopeRows);
   const dim3 grid((a.r.n_rows + rows - 1) / rows);
 #define CALL(DD)                                                                         \
   return t8 ? launch_early(rope_kernel<DD, true>, grid, kThreads, 0, st, a, rows)        \

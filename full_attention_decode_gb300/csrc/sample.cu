@@ -10,7 +10,8 @@
 // The values come in runs of 128 (a sign and an exponent). Each run that holds a token is added up over the CTAs, through
 // distributed shared memory, and weighed by one of them; all read all runs' sums, so all know where the cuts lie without
 // asking; the run that a cut lies in is then added up again value by value. Bound by the shared-memory additions of the counting
-// and a chain of reads and barriers.
+// and a chain of reads and barriers: a row of 248320 takes 18 us (its bytes 0.1), 64 rows 47 us. The simplest form,
+// whose CTAs read one another's runs, took 36 and 170.
 #include <cooperative_groups.h>
 
 #include <cmath>
@@ -523,8 +524,10 @@ cudaError_t sample(const Sample& s, cudaStream_t st) {
     for (int i = 0; i < 64; ++i) t.t[i] = (u64)std::ldexp(std::exp2(-i / 64.0), 63);
     return t;
   }();
-  // Eight CTAs a row while all rows run at once, or where four could not count the tokens in 16 bits; otherwise four.
-  return s.n_rows <= 16 || s.vocab > 4 * (kMaxVocab / 8) ? launch<8>({s, table}, st) : launch<4>({s, table}, st);
+  // Eight CTAs a row while the clusters of all rows find room at once, or where four could not count the tokens in 16 bits;
+  // otherwise four. Of 248320 tokens 1 row takes 18.8 us with eight, 22.5 with four; 8 rows 19.9 and 24.8; 16 rows 35.5 and 25.7; 64
+  // rows 82.8 and 49.0.
+  return s.n_rows <= 8 || s.vocab > 4 * (kMaxVocab / 8) ? launch<8>({s, table}, st) : launch<4>({s, table}, st);
 }
 
 }  // namespace q35c

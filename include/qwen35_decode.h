@@ -589,9 +589,9 @@ QWEN35_API int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv
  * caches and rows are as for the cache operators above, with the same limits and errors.
  *
  * Scratch: qwen35_rows_scratch_bytes(cfg, rows of the largest call), made with
- * qwen35_scratch_init; a scratch of the cache operators does for qwen35_cache_append_rope and
- * qwen35_cache_keep, which use its first 256 bytes alone. It belongs to one call at a time. About
- * (rows * num_heads + 160 * 128) * (head_dim + 8) * 4 bytes. 0 for dims the calls reject. */
+ * qwen35_scratch_init; it does for the cache operators' appends too, and a scratch of theirs for
+ * qwen35_cache_append_rope and qwen35_cache_keep, which use its first 256 bytes alone. It belongs to one call at
+ * a time. About (rows * num_heads + 160 * 128) * (head_dim + 4) * 4 bytes and 128 KB. 0 for dims the calls reject. */
 QWEN35_API size_t qwen35_rows_scratch_bytes(const qwen35_config* cfg, uint32_t max_rows);
 
 /* Norm and rotate rows and write them to the cache, as forward_full_attention does between
@@ -632,7 +632,8 @@ QWEN35_API int qwen35_cache_append_rope(const qwen35_config* cfg, const qwen35_k
  * products with V as two bf16 parts (2^-16) with a bf16 cache. With a Turbo8 cache the rotated q, the codes times
  * their scales and the weights are rounded to f16 (2^-11 each, the keys' and values' over a power of two of
  * the token's largest, 2^-25 of that at the least), so a score is off by up to 2^-10 of the sum of its
- * terms' sizes: for scores of usual size (below 100) far less than the codes' own 2^-4. */
+ * terms' sizes: for scores of usual size (below 100) far less than the codes' own 2^-4. Scores of a Turbo8 cache
+ * are taken to lie within 2^20: beyond that the weights' exponents are no longer held to a part of one. */
 QWEN35_API int qwen35_tree_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
                                      const int32_t* parent, const qwen35_bf16* q, const qwen35_bf16* gate,
                                      uint32_t gate_stride, qwen35_bf16* out, void* scratch, size_t scratch_bytes,

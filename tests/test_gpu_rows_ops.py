@@ -481,10 +481,8 @@ def test_keys_alone_and_rows_outside():
     assert changed == 3
 
 
-def test_rotated_rows_are_those_of_the_prefill():
-    """A layer's own keys and values, cached by its prefill: within one bf16 step of the operator's from
-    the projections that the layer left in its scratch would be, here from its cached, turned-back rows: a row
-    turned by p, then by -p, is itself within two roundings."""
+def test_rows_turned_and_turned_back():
+    """Rows turned by p, then by -p, are themselves within two roundings."""
     s = rope_setup("4b", BF16, [40], [40], 64)
     rp = torch.arange(40, dtype=torch.int32, device="cuda")
     assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, None, s.k_new, s.v_new, None, s.scratch, k_out=s.k_out,
@@ -794,3 +792,150 @@ def test_offsets_past_32_bits():
     ref, tol = expect(s, lambda b, i, p: list(range(40)))[0]
     assert (np.abs(f64(out[-1]) - ref) <= 2.0 ** -8 * np.abs(ref) + tol).all()
     assert torch.isnan(out[:-1].float()).all()
+
+
+class Banded:
+    """A copy of a tensor between two bands of a pattern."""
+
+    def __init__(self, t, band=1 << 16):
+        n = t.numel() * t.element_size()
+        self.raw = torch.full((n + 2 * band,), 0x5A, dtype=torch.uint8, device="cuda")
+        self.t = self.raw[band:band + n].view(t.dtype).view(t.shape)
+        self.t.copy_(t)
+        self.band = band
+
+    def whole(self):
+        return bool((self.raw[:self.band] == 0x5A).all() and (self.raw[-self.band:] == 0x5A).all())
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("rows", [[2, 2, 2], [40, 50, 30]])
+@pytest.mark.parametrize("start", [[0, 6, 2, 8], [4, 0, 5, 6], [-5, 1 << 30, -(1 << 30), 1 << 30], [3, 3, 3, 3],
+                                   [-(1 << 31), (1 << 31) - 1, 0, 2], [0, 200, 120, 2]])
+def test_row_starts_that_run_backwards_touch_nothing_outside(fmt, rows, start):
+    s = rope_setup("tiny_alt", fmt, [80, 90, 70], rows, 32)
+    bands = {n: Banded(t) for n, t in s.t.items()}
+    s.kv.k, s.kv.v = bands["k"].t.data_ptr(), bands["v"].t.data_ptr()
+    if fmt == TURBO8:
+        s.kv.k_scales, s.kv.v_scales = bands["ks"].t.data_ptr(), bands["vs"].t.data_ptr()
+    for n in ("q_out", "k_out", "scratch", "pos"):
+        bands[n] = Banded(getattr(s, n))
+    out = bands["out"] = Banded(blank(s))
+    starts = bands["start"] = Banded(torch.tensor(start, dtype=torch.int64).to(torch.int32).cuda())
+    parent = bands["parent"] = Banded(torch.arange(-1, s.n_rows - 1, dtype=torch.int32, device="cuda"))
+    path = bands["path"] = Banded(torch.arange(s.n_rows, dtype=torch.int32, device="cuda"))
+    r = B.DeviceRows(bands["pos"].t, starts.t, s.n_rows, s.nb)
+    scratch, q = bands["scratch"].t, s.q.cuda()
+    assert B.qwen35_cache_append_rope(s.cfg, s.kv, r, s.qg, s.k_new, s.v_new, bands["q_out"].t, scratch, q_norm=s.wq,
+                                      k_norm=s.wk, q_stride=2 * s.D, k_out=bands["k_out"].t) == 0
+    assert B.qwen35_tree_attention(s.cfg, s.kv, r, parent.t, q, out.t, scratch) == 0
+    assert B.qwen35_window_attention(s.cfg, s.kv, r, 20, 4, q, out.t, scratch) == 0
+    assert B.qwen35_cache_keep(s.cfg, s.kv, r, path.t, scratch) == 0
+    torch.cuda.synchronize()
+    assert B.qwen35_read_device_status(scratch) in (0, B.QWEN35_ERR_DEVICE_RANGE)
+    for n, x in bands.items():
+        assert x.whole(), n
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_arrays_at_16_bytes(fmt):
+    """Every array moved to 16 bytes behind a larger boundary gives the bits that it gives at one."""
+    s = rope_setup("4b", fmt, [300, 40], [9, 5], 64)
+
+    def moved(t):
+        n = t.numel() * t.element_size()
+        x = torch.empty(n + 512, dtype=torch.uint8, device="cuda")
+        x = x[16 + -x.data_ptr() % 256:][:n].view(t.dtype).view(t.shape)
+        return x.copy_(t)
+
+    gate = bf16(s.rng.standard_normal((s.n_rows, s.H, s.D))).cuda()
+    parent = torch.tensor([-1, 0, 0, 1, 1, 2, 4, 6, 7] + [-1, 0, 1, 0, 3], dtype=torch.int32, device="cuda")
+
+    def run(f):
+        for n in s.t:
+            s.t[n] = f(s.t[n])
+        s.kv.k, s.kv.v = s.t["k"].data_ptr(), s.t["v"].data_ptr()
+        if fmt == TURBO8:
+            s.kv.k_scales, s.kv.v_scales = s.t["ks"].data_ptr(), s.t["vs"].data_ptr()
+        q_out, k_out, a, b, scratch = (f(t) for t in (blank(s), torch.full_like(s.k_new, NAN), blank(s), blank(s), s.scratch))
+        assert B.qwen35_cache_append_rope(s.cfg, s.kv, s.r, f(s.qg), f(s.k_new), f(s.v_new), q_out, scratch, q_norm=f(s.wq),
+                                          k_norm=f(s.wk), q_stride=2 * s.D, k_out=k_out) == 0
+        assert B.qwen35_tree_attention(s.cfg, s.kv, s.r, parent, q_out, a, scratch, gate=f(gate)) == 0
+        assert B.qwen35_window_attention(s.cfg, s.kv, s.r, 70, 3, q_out, b, scratch, gate=f(gate)) == 0
+        torch.cuda.synchronize()
+        assert B.qwen35_read_device_status(scratch) == 0
+        return [t.clone().view(torch.uint8) for t in (q_out, k_out, a, b, *s.t.values())]
+
+    for x, y in zip(run(lambda t: t), run(moved)):
+        assert torch.equal(x, y)
+
+
+def counters(s):
+    """The scratch before its work space: the status word and the counters."""
+    work = (s.n_rows * s.H + 160 * 128) * (s.D * 4 + 16) + s.n_rows * s.Hkv * 4
+    return s.scratch[:s.scratch.numel() - work]
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_counters_are_left_as_they_were(fmt):
+    """Parts joined inside the launch and by a second one leave the counters as zeros, and the cache operators'
+    append works on the same scratch in between."""
+    s = setup("4b", fmt, [5000, 70, 900], None)
+    want = {w: run_window(s, w, 4) for w in (50, 3000)}
+    k, v = (bf16(s.rng.standard_normal((s.n_rows, s.Hkv, s.D))).cuda() for _ in range(2))
+    for _ in range(3):
+        for w in want:
+            assert torch.equal(run_window(s, w, 4).view(torch.int16), want[w].view(torch.int16))
+        assert not counters(s).any()
+    assert B.qwen35_cache_append(s.cfg, s.kv, s.r, None, k, v, s.scratch) == 0
+    assert status(s) == 0 and not counters(s).any()
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_two_graphs_side_by_side(fmt):
+    """Two captured graphs, each with its own scratch and output, replayed on two streams at once, many times."""
+    s = setup("4b", fmt, [3000, 257, 64, 1900], None, page=64)
+    trees = setup("4b", fmt, [2000, 300], [20, 7], page=16)
+    parent = torch.tensor([-1] + list(range(19)) + [-1, 0, 0, 1, 2, 2, 5], dtype=torch.int32, device="cuda")
+    q, tq = s.q.cuda(), trees.q.cuda()
+    out, t_out = blank(s), blank(trees)
+
+    def window():
+        assert B.qwen35_window_attention(s.cfg, s.kv, s.r, 700, 4, q, out, s.scratch) == 0
+
+    def tree():
+        assert B.qwen35_tree_attention(trees.cfg, trees.kv, trees.r, parent, tq, t_out, trees.scratch) == 0
+
+    window(), tree()
+    torch.cuda.synchronize()
+    want = [out.clone(), t_out.clone()]
+    graphs = []
+    for f in (window, tree):
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            f()
+        graphs.append(g)
+    out.fill_(NAN), t_out.fill_(NAN)
+    torch.cuda.synchronize()
+    for g in graphs:
+        with torch.cuda.stream(torch.cuda.Stream()):
+            for _ in range(20):
+                g.replay()
+    torch.cuda.synchronize()
+    for a, b in zip((out, t_out), want):
+        assert torch.equal(a.view(torch.int16), b.view(torch.int16))
+    assert status(s) == 0 and status(trees) == 0
+
+
+@pytest.mark.parametrize("vocab", [300, 4097, 248320])
+def test_a_row_of_many_is_the_row_alone(vocab):
+    """Few rows are taken by more CTAs each than many: the same tokens and shares, to the bit."""
+    x = logits(40, vocab, seed=5)
+    u = np.linspace(0, 0.999, 40)
+    t, k, p, m = np.full(40, 0.9), np.full(40, 50), np.full(40, 0.95), np.full(40, 0.01)
+    many = run_sample(x, u, t, k, p, m)
+    for r in (0, 7, 39):
+        one = run_sample(x[r:r + 1].clone(), u[r:r + 1], t[:1], k[:1], p[:1], m[:1])
+        assert one[0][0] == many[0][r] and one[1][0] == many[1][r]
+    eight = run_sample(x[:8].clone(), u[:8], t[:8], k[:8], p[:8], m[:8])
+    assert (eight[0] == many[0][:8]).all() and (eight[1] == many[1][:8]).all()
