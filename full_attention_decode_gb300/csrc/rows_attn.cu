@@ -596,134 +596,121 @@ struct LoadTurbo8 {
 
 // ------------------------------------------------------------------ the join
 
-// Columns' parts added up. A warp takes four neighbouring columns of a row's heads (four lanes read 128 bytes side by
-// side), a lane D / 8 / 8 pieces of eight dims of one; TEAMS warps of a CTA take a column's parts in turn.
+// Columns' parts added up. A lane has eight dims, so D / 8 lanes a column and 256 / D columns a warp; `teams` warps of a
+// CTA, one of them `team`, take a column's parts in turn. Little code on purpose: it runs once, as fast as its instructions come
+// (32 dims a lane, four columns a warp, unrolled: 16 Turbo8 trees 168 us, with this 144).
 // Column c = row H + head of the output, whose item lies in CTAs c0 .. c0 + n - 1 (0: none) and has `cols` columns from
-// `first` on, this one the col-th. sync: of the teams' threads, sums theirs.
-template <int D, bool T8, int TEAMS, typename Sync>
-__device__ __forceinline__ void join_columns(const RowsAttend& a, const Work& work, uint32_t sub, uint32_t lane, uint32_t c,
-                                             uint32_t c0, uint32_t n, uint32_t cols, uint32_t col, size_t first,
-                                             float (*sums)[D / 8][32], Sync&& sync) {
-  constexpr uint32_t P = D / 64;  // pieces of a lane
-  const uint32_t l8 = lane / 4;
+// `first` on, this one the col-th. sync: of the CTA's eight warps, which come here together; sums theirs.
+template <int D>
+constexpr uint32_t kJoinColumns = 256 / D;
+__device__ __forceinline__ void load_part(const float* p, bool wide, float (&x)[8]) {  // written by other SMs: from the L2
+  if (wide) {
+    asm volatile("ld.relaxed.gpu.global.v8.f32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=f"(x[0]), "=f"(x[1]), "=f"(x[2]), "=f"(x[3]), "=f"(x[4]), "=f"(x[5]), "=f"(x[6]), "=f"(x[7])
+                 : "l"(p)
+                 : "memory");
+  } else {
+    const float4 u = __ldcg(reinterpret_cast<const float4*>(p)), v = __ldcg(reinterpret_cast<const float4*>(p) + 1);
+    x[0] = u.x, x[1] = u.y, x[2] = u.z, x[3] = u.w;
+    x[4] = v.x, x[5] = v.y, x[6] = v.z, x[7] = v.w;
+  }
+}
+template <int D, bool T8, typename Sync>
+__device__ __forceinline__ void join_columns(const RowsAttend& a, const Work& work, uint32_t warp, uint32_t teams, uint32_t lane,
+                                             uint32_t c, uint32_t c0, uint32_t n, uint32_t cols, uint32_t col, size_t first,
+                                             float (*sums)[8][32], Sync&& sync) {
+  constexpr uint32_t L = D / 8;
+  const uint32_t piece = lane % L, team = warp % teams, most = __reduce_max_sync(0xffffffffu, n);
+  uint4 gate = make_uint4(0, 0, 0, 0);
+  if (a.gate && n && team == 0) gate = *reinterpret_cast<const uint4*>(a.gate + (size_t)c * a.gate_stride + 8 * piece);
   const auto ml = [&](uint32_t k) { return __ldcg(k ? work.cont_ml + (size_t)(c0 + k) * kM + col : work.nat_ml + first + col); };
-  // the largest maximum and (T8) V's relative to it, the sum: a part each of the column's eight lanes, in rounds
+  // the largest maximum and (T8) V's relative to it, the sum: a part each of the column's lanes, in rounds
+  const float4 mine = piece < n ? ml(piece) : make_float4(-INFINITY, 0.f, -INFINITY, 0.f);
   bool ok = n > 0;
-  float M = -INFINITY, V = -INFINITY, L = 0.f;
-  for (uint32_t k = l8; k < n; k += 8) {
-    const float4 x = ml(k);
+  float M = -INFINITY, V = -INFINITY, l = 0.f;
+#pragma unroll 1
+  for (uint32_t k = piece; k < n; k += L) {
+    const float4 x = k < L ? mine : ml(k);
     if (x.y < 0.f) ok = false;
     M = fmaxf(M, x.x);
   }
 #pragma unroll
-  for (uint32_t w = 4; w < 32; w <<= 1) {
+  for (uint32_t w = 1; w < L; w <<= 1) {
     M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, w));
     ok &= __shfl_xor_sync(0xffffffffu, ok, w);
   }
   const float mu = finite_or_0(M);
   const auto exponent = [&](const float4& x) { return T8 ? x.z + (finite_or_0(x.x) - mu) : x.x - mu; };  // of its sums O
-  for (uint32_t k = l8; k < n; k += 8) {
-    const float4 x = ml(k);
+#pragma unroll 1
+  for (uint32_t k = piece; k < n; k += L) {
+    const float4 x = k < L ? mine : ml(k);
     if (T8) V = fmaxf(V, exponent(x));
-    L += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - mu);
+    l += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - mu);
   }
 #pragma unroll
-  for (uint32_t w = 4; w < 32; w <<= 1) {
-    V = fmaxf(V, __shfl_xor_sync(0xffffffffu, V, w));
-    L += __shfl_xor_sync(0xffffffffu, L, w);
+  for (uint32_t w = 1; w < L; w <<= 1) {
+    if (T8) V = fmaxf(V, __shfl_xor_sync(0xffffffffu, V, w));
+    l += __shfl_xor_sync(0xffffffffu, l, w);
   }
   const float down = T8 ? finite_or_0(V) : 0.f;
-  float x[P][8] = {};
-#pragma unroll 2
-  for (uint32_t k = sub; k < n; k += TEAMS) {
-    const float4 y = ml(k);
-    const float f = y.x == -INFINITY || (T8 && y.z == -INFINITY) ? 0.f : ex2(exponent(y) - down);
-    const float* from = k ? work.cont + (size_t)(c0 + k) * kM * D + col * 8 : work.nat + first * D + col * 8;
-    const uint32_t wide = k ? kM : cols;
-    float4 u[P][2];
+  const auto factor = [&](const float4& y) {
+    return y.x == -INFINITY || (T8 && y.z == -INFINITY) ? 0.f : ex2(exponent(y) - down);
+  };
+  const float own = factor(mine);
+  float x[8] = {};
+#pragma unroll 4
+  for (uint32_t k = team; k < most; k += teams) {
+    float f = __shfl_sync(0xffffffffu, own, min(k, L - 1), L), u[8] = {};
+    if (k < n) {
+      load_part((k ? work.cont + (size_t)(c0 + k) * kM * D + (piece * kM + col) * 8 : work.nat + first * D + (piece * cols + col) * 8),
+                a.wide, u);
+      if (k >= L) f = factor(ml(k));
+      if (f != 0.f)
 #pragma unroll
-    for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-      for (int j = 0; j < 2; ++j) u[i][j] = __ldcg(reinterpret_cast<const float4*>(from + (size_t)(l8 + 8 * i) * 8 * wide) + j);
-    if (f != 0.f)
-#pragma unroll
-      for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          x[i][4 * j] = fmaf(u[i][j].x, f, x[i][4 * j]);
-          x[i][4 * j + 1] = fmaf(u[i][j].y, f, x[i][4 * j + 1]);
-          x[i][4 * j + 2] = fmaf(u[i][j].z, f, x[i][4 * j + 2]);
-          x[i][4 * j + 3] = fmaf(u[i][j].w, f, x[i][4 * j + 3]);
-        }
-  }
-  if constexpr (TEAMS > 1) {
-#pragma unroll
-    for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sums[sub][8 * i + e][lane] = x[i][e];
-    sync();
-    if (sub) return;
-#pragma unroll 1
-    for (uint32_t k = 1; k < TEAMS; ++k)
-#pragma unroll
-      for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] += sums[k][8 * i + e][lane];
-  }
-  const float inv = L == 0.f ? 0.f : 1.f / L, up = T8 ? ex2(0.5f * down) : 1.f;
-#pragma unroll
-  for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[i][e] = L == 0.f ? 0.f : T8 ? x[i][e] * inv * up * up : x[i][e] * inv;
-  if constexpr (T8) {  // rotated back: dim 8 (l8 + 8 i) + e
-#pragma unroll
-    for (uint32_t i = 0; i < P; ++i) {
-#pragma unroll
-      for (int hb = 1; hb < 8; hb <<= 1)
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-          if (!(e & hb)) {
-            const float u = x[i][e], w = x[i][e + hb];
-            x[i][e] = u + w;
-            x[i][e + hb] = u - w;
-          }
-#pragma unroll
-      for (uint32_t w = 4; w < 32; w <<= 1)
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float o = __shfl_xor_sync(0xffffffffu, x[i][e], w);
-          x[i][e] = lane & w ? o - x[i][e] : x[i][e] + o;
-        }
+        for (int e = 0; e < 8; ++e) x[e] = fmaf(u[e], f, x[e]);
     }
+  }
+  if (teams > 1) {
 #pragma unroll
-    for (uint32_t hb = 1; hb < P; hb <<= 1)
+    for (int e = 0; e < 8; ++e) sums[warp][e][lane] = x[e];
+    sync();
+    if (team) return;
+#pragma unroll 1
+    for (uint32_t k = 1; k < teams; ++k)
 #pragma unroll
-      for (uint32_t i = 0; i < P; ++i)
-        if (!(i & hb))
+      for (int e = 0; e < 8; ++e) x[e] += sums[warp + k][e][lane];
+  }
+  const float inv = l == 0.f ? 0.f : 1.f / l, up = T8 ? ex2(0.5f * down) : 1.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const float u = x[i][e], w = x[i + hb][e];
-            x[i][e] = u + w;
-            x[i + hb][e] = u - w;
-          }
+  for (int e = 0; e < 8; ++e) x[e] = l == 0.f ? 0.f : T8 ? x[e] * inv * up * up : x[e] * inv;
+  if constexpr (T8) {  // rotated back: dim 8 piece + e
+#pragma unroll
+    for (int hb = 1; hb < 8; hb <<= 1)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (!(e & hb)) {
+          const float u = x[e], w = x[e + hb];
+          x[e] = u + w;
+          x[e + hb] = u - w;
+        }
+#pragma unroll 1
+    for (uint32_t w = 1; w < L; w <<= 1) {
+      const float sign = lane & w ? -1.f : 1.f;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = fmaf(x[e], sign, __shfl_xor_sync(0xffffffffu, x[e], w));
+    }
     const float norm = rsqrtf((float)D);
 #pragma unroll
-    for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] *= norm;
+    for (int e = 0; e < 8; ++e) x[e] *= norm;
   }
   if (!ok) return;
+  if (a.gate) {
+    float g[8];
+    unpack8(gate, g);
 #pragma unroll
-  for (uint32_t i = 0; i < P; ++i) {
-    const uint32_t d = 8 * (l8 + 8 * i);
-    if (a.gate) {
-      float g[8];
-      unpack8(*reinterpret_cast<const uint4*>(a.gate + (size_t)c * a.gate_stride + d), g);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] *= sigmoidf_(g[e]);
-    }
-    *reinterpret_cast<uint4*>(a.out + (size_t)c * D + d) = pack8(x[i]);
+    for (int e = 0; e < 8; ++e) x[e] *= sigmoidf_(g[e]);
   }
+  *reinterpret_cast<uint4*>(a.out + (size_t)c * D + 8 * piece) = pack8(x);
 }
 
 // ------------------------------------------------------------------ softmax
@@ -1051,14 +1038,14 @@ struct Softmax {
     }
     named_barrier(1, kSoft);
     if (n > 1 && !sh.last) return;
-    float(*sums)[D / 8][32] = reinterpret_cast<float(*)[D / 8][32]>(q_sm);  // the products are done with Q
-    for (uint32_t c4 = 0; c4 < cols; c4 += 4) {
-      const uint32_t col = c4 + lane % 4, r = st.b.row + col / group;
-      const bool in = col < cols;
-      join_columns<D, T8, 8>(a, work, tid / 32, lane, in ? r * a.H + st.g * group + col % group : 0, st.c0, in ? n : 0, cols,
-                             in ? col : 0, (size_t)st.b.row * a.H + st.g * cols, sums, [] { named_barrier(1, kSoft); });
-      named_barrier(1, kSoft);  // the sums are free
-    }
+    float(*sums)[8][32] = reinterpret_cast<float(*)[8][32]>(q_sm);  // the products are done with Q
+    // as many warps a column as there are: at most eight columns, 256 / D of them a warp
+    const uint32_t fours = (cols + kJoinColumns<D> - 1) / kJoinColumns<D>, teams = fours > 4 ? 1 : fours > 2 ? 2 : fours > 1 ? 4 : 8;
+    const uint32_t col = tid / 32 / teams * kJoinColumns<D> + lane / (D / 8), r = st.b.row + col / group;
+    const bool in = col < cols;
+    join_columns<D, T8>(a, work, tid / 32, teams, lane, in ? r * a.H + st.g * group + col % group : 0, st.c0, in ? n : 0, cols,
+                        in ? col : 0, (size_t)st.b.row * a.H + st.g * cols, sums, [] { named_barrier(1, kSoft); });
+    named_barrier(1, kSoft);  // the sums are free
   }
 
   // The sums of a stretch, the last of whose tiles is tile n of the CTA.
@@ -1321,12 +1308,12 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   }
 }
 
-template <int D, bool T8, int TEAMS>
-__global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ RowsAttend a) {
-  constexpr uint32_t FOURS = 8 / TEAMS;  // fours of columns of a CTA
-  __shared__ float sums[TEAMS > 1 ? TEAMS : 1][D / 8][32];
+// Registers that leave it room beside a CTA of rows_kernel, so it waits for that on the SM.
+template <int D, bool T8>
+__global__ void __launch_bounds__(256, 5) join_kernel(const __grid_constant__ RowsAttend a, uint32_t teams) {
+  __shared__ float sums[8][8][32];
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint32_t group = a.H / a.c.Hkv, c = blockIdx.x * FOURS * 4 + warp / TEAMS * 4 + lane % 4;
+  const uint32_t group = a.H / a.c.Hkv, c = (blockIdx.x * (8 / teams) + warp / teams) * kJoinColumns<D> + lane / (D / 8);
   const uint32_t r = c / a.H, h = c % a.H;
   const bool in = r < a.r.n_rows;
   const Work work = work_of(a.work, a.r.n_rows, a.H, D);
@@ -1335,8 +1322,8 @@ __global__ void __launch_bounds__(256) join_kernel(const __grid_constant__ RowsA
   const uint32_t rec = in ? work.rec[r * a.c.Hkv + h / group] : 0;
   const uint32_t c0 = rec & 255u, n = rec & kRecOk ? (rec >> 8 & 255u) - c0 + 1 : 0, off = rec >> 16 & 127u;
   const uint32_t cols = ((rec >> 23 & 127u) + 1) * group;
-  join_columns<D, T8, TEAMS>(a, work, warp % TEAMS, lane, c, c0, n, cols, off * group + h % group,
-                             in ? (size_t)(r - off) * a.H + h / group * cols : 0, sums, [] { __syncthreads(); });
+  join_columns<D, T8>(a, work, warp, teams, lane, c, c0, n, cols, off * group + h % group,
+                      in ? (size_t)(r - off) * a.H + h / group * cols : 0, sums, [] { __syncthreads(); });
 }
 
 template <int D, bool T8>
@@ -1355,10 +1342,11 @@ cudaError_t launch(const RowsAttend& a, cudaStream_t st) {
   cudaError_t e = launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D, T8>(a.r.n_rows), st, a);
   if (e != cudaSuccess) return e;
   if (a.here) return cudaSuccess;
-  // few columns: a CTA for four of them, whose warps share their parts; many: a warp for four
-  const uint32_t cols = a.r.n_rows * a.H;
-  if (cols <= 2048) return launch_early(join_kernel<D, T8, 8>, dim3((cols + 3) / 4), 256, 0, st, a);
-  return launch_early(join_kernel<D, T8, 1>, dim3((cols + 31) / 32), 256, 0, st, a);
+  // up to eight warps a column, as long as the SMs hold all CTAs at once (four each)
+  const uint32_t warps = (a.r.n_rows * a.H + kJoinColumns<D> - 1) / kJoinColumns<D>;
+  uint32_t teams = 8;
+  while (teams > 1 && warps * teams > 32 * a.sms) teams /= 2;
+  return launch_early(join_kernel<D, T8>, dim3((warps * teams + 7) / 8), 256, 0, st, a, teams);
 }
 
 }  // namespace
