@@ -19,10 +19,10 @@
 // joined by the last of the item's CTAs; those of a block of many rows by a second launch, spread over the GPU: one CTA that
 // joined a block of 128 columns would read 2.5 MB.
 //
-// What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 94 us,
-// 4.4 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8192 tokens: 43 us, 200 TFLOP/s, where an
-// item's 32 tiles a CTA share with the way in and the join. Turbo8, 16 trees: 169 us, the chain of loader, product and
-// softmax a tile: without the loader's arithmetic 129 us, without the softmax 143, without the products 157.
+// What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 90 us,
+// 4.6 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8192 tokens: 38 us, 228 TFLOP/s, where
+// seven tiles a CTA share with the way in and the join. Turbo8, 16 trees: 144 us, the chain of loader, product and softmax a
+// tile (of 166 us that it took before the join was made short, 37 were the loader's arithmetic, 23 the softmax, 9 the products).
 //
 // Roundings. bf16: Q, K, V exactly, P as hi + lo bf16 (2^-16). Turbo8: the rotated q as f16 over the power of two of its largest
 // value; K's and V's codes times scale / 2^E, E the exponent of the token's largest scale, as f16 (a product of 4
@@ -1342,7 +1342,8 @@ cudaError_t launch(const RowsAttend& a, cudaStream_t st) {
   cudaError_t e = launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D, T8>(a.r.n_rows), st, a);
   if (e != cudaSuccess) return e;
   if (a.here) return cudaSuccess;
-  // up to eight warps a column, as long as the SMs hold all CTAs at once (four each)
+  // Up to eight warps a column, as long as the SMs hold all CTAs at once, four each (64 nodes over 8191 tokens, one after another:
+  // 31.9 us, half as many warps 35.0, twice as many 34.1).
   const uint32_t warps = (a.r.n_rows * a.H + kJoinColumns<D> - 1) / kJoinColumns<D>;
   uint32_t teams = 8;
   while (teams > 1 && warps * teams > 32 * a.sms) teams /= 2;
@@ -1363,9 +1364,10 @@ cudaError_t rows_attend_attributes() {
 
 cudaError_t rows_attend(const RowsAttend& args, cudaStream_t st) {
   RowsAttend a = args;
-  // An item of few columns is joined where its last part is made (one row through a window of 512: 17.7 us here, 18.6 by
-  // a second launch); those of many rows by many CTAs (32 rows through windows of 4096: 98.9 us by a second launch, 102.6 here).
-  a.here = a.H / a.c.Hkv * (a.r.row_start ? a.r.n_rows : 1) <= 8 && a.r.n_rows * a.H <= 128;
+  // Eight columns, one for each warp of the softmax, are joined where their last part is made (one row through a window of 512:
+  // 13.7 us, by a second launch 15.1; 32 rows through windows of 128 15.2 and 18.1, of 4096 89.4 and 89.8; 1024 rows through windows
+  // of 64 273 and 263); more columns by CTAs of their own.
+  a.here = a.H / a.c.Hkv * (a.r.row_start ? a.r.n_rows : 1) <= 8;
   const bool t8 = a.c.ks != nullptr;
 #define CALL(DD) return t8 ? launch<DD, true>(a, st) : launch<DD, false>(a, st)
   switch (a.c.D) {
