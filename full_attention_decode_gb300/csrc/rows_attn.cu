@@ -323,70 +323,88 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* 
   static_assert(STEP % 8 == 0, "the swizzle of a thread's rows");
   const uint32_t stride = a.c.Hkv * D;
   const Stretch& s = walk.s;
-  uint32_t n = 0;
-  while (next(a, first, per, walk, lane)) {
-    Found now = {0, false};
-    uint32_t then = look_up(a, s.b, s.t0, lane);
-    for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
-      const uint32_t i = (t - s.t0) % 4;
-      if (i == 0) {
-        now = found(a, s.b, t, lane, then);
-        then = look_up(a, s.b, t + 4, lane);
-      }
-      const bool full = s.whole(t);
-      const uint32_t valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
-      uint32_t rows = 0xffu;  // lane % 8's octet: rows of it that are loaded
-      if (!full) {
-        uint32_t lo, hi;
-        octet_rows(a, s.b, t * kOctets + lane % 8, lo, hi);
-        rows = bits_below(hi) & ~bits_below(lo);
-      }
-      if (!(valid >> (lane % 8) & 1)) rows = 0;
-      uint32_t row[J], in = 0;
+  uint32_t n = 0, then = 0;
+  Found now = {0, false};
+  struct Pieces {  // the thread's, of a tile: their rows, which are there; the tile's octets, and whether it is seen to its end
+    uint32_t row[J], in, valid;
+    bool full;
+  };
+  const auto places = [&](uint32_t t) {
+    Pieces x;
+    const uint32_t i = (t - s.t0) % 4;
+    if (i == 0) {
+      now = found(a, s.b, t, lane, then);
+      then = look_up(a, s.b, t + 4, lane);
+    }
+    x.full = s.whole(t);
+    x.valid = __ballot_sync(0xffffffffu, now.in) >> (8 * i) & 0xffu;
+    uint32_t rows = 0xffu;  // lane % 8's octet: rows of it that are loaded
+    if (!x.full) {
+      uint32_t lo, hi;
+      octet_rows(a, s.b, t * kOctets + lane % 8, lo, hi);
+      rows = bits_below(hi) & ~bits_below(lo);
+    }
+    if (!(x.valid >> (lane % 8) & 1)) rows = 0;
+    x.in = 0;
+#pragma unroll
+    for (uint32_t j = 0; j < J; ++j) {
+      const uint32_t q = q0 + j * STEP / 8;  // a warp's rows lie in one octet
+      x.row[j] = __shfl_sync(0xffffffffu, now.row, 8 * i + q) + r0 % 8;
+      x.in |= (__shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u) << j;
+    }
+    return x;
+  };
+  const auto put = [&](const Pieces& x, uint32_t n, bool v) {
+    const Place<D, false> at(2 * n + v);
+    if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
+    uint8_t* slot = ring + at.slot * Ring<D, false>::bytes;
+    const uint16_t* base = reinterpret_cast<const uint16_t*>(v ? a.c.v : a.c.k) + s.g * D + 8 * c;
+    if (!v || x.full) {
+      const uint32_t dst = smem_addr(slot) + to;
+#pragma unroll
+      for (uint32_t j = 0; j < J; ++j) cp16(dst + j * STEP * 128, x.in >> j & 1 ? base + (size_t)x.row[j] * stride : base, x.in >> j & 1);
+      cp_arrive(&sh.full[at.slot]);
+    } else {
+      uint4 u[J];
+#pragma unroll
+      for (uint32_t j = 0; j < J; ++j) u[j] = x.in >> j & 1 ? load16(base + (size_t)x.row[j] * stride) : make_uint4(0u, 0u, 0u, 0u);
+      bool bad = false;
 #pragma unroll
       for (uint32_t j = 0; j < J; ++j) {
-        const uint32_t q = q0 + j * STEP / 8;  // a warp's rows lie in one octet
-        row[j] = __shfl_sync(0xffffffffu, now.row, 8 * i + q) + r0 % 8;
-        in |= (__shfl_sync(0xffffffffu, rows, q) >> (r0 % 8) & 1u) << j;
-      }
-#pragma unroll 1
-      for (uint32_t p = 0; p < 2; ++p) {
-        const Place<D, false> at(2 * n + p);
-        if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
-        uint8_t* slot = ring + at.slot * Ring<D, false>::bytes;
-        const uint16_t* base = reinterpret_cast<const uint16_t*>(p ? a.c.v : a.c.k) + s.g * D + 8 * c;
-        if (!p || full) {
-          const uint32_t dst = smem_addr(slot) + to;
+        uint32_t* w = &u[j].x;
 #pragma unroll
-          for (uint32_t j = 0; j < J; ++j) cp16(dst + j * STEP * 128, in >> j & 1 ? base + (size_t)row[j] * stride : base, in >> j & 1);
-          cp_arrive(&sh.full[at.slot]);
-        } else {
-          uint4 x[J];
-#pragma unroll
-          for (uint32_t j = 0; j < J; ++j) x[j] = in >> j & 1 ? load16(base + (size_t)row[j] * stride) : make_uint4(0u, 0u, 0u, 0u);
-          bool bad = false;
-#pragma unroll
-          for (uint32_t j = 0; j < J; ++j) {
-            uint32_t* w = &x[j].x;
-#pragma unroll
-            for (uint32_t e = 0; e < 4; ++e)
-              if (not_a_number_bf16(w[e])) {
-                bad = true;
-                if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
-                if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
-              }
-            *reinterpret_cast<uint4*>(slot + to + j * STEP * 128) = x[j];
+        for (uint32_t e = 0; e < 4; ++e)
+          if (not_a_number_bf16(w[e])) {
+            bad = true;
+            if ((w[e] & 0x7f80u) == 0x7f80u) w[e] &= 0xffff0000u;
+            if ((w[e] & 0x7f800000u) == 0x7f800000u) w[e] &= 0xffffu;
           }
-          bad = __any_sync(0xffffffffu, bad);
-          if (lane == 0) sh.dirty[n % Ring<D, false>::info][warp] = bad;
-          tm_fence_shared();
-          mbar_arrive(&sh.full[at.slot]);
-        }
-        if (!p && tid == 0) {  // an arrival that the notes are released by
-          sh.valid[n % Ring<D, false>::info] = valid;
-          mbar_arrive(&sh.full[at.slot]);
-        }
+        *reinterpret_cast<uint4*>(slot + to + j * STEP * 128) = u[j];
       }
+      bad = __any_sync(0xffffffffu, bad);
+      if (lane == 0) sh.dirty[n % Ring<D, false>::info][warp] = bad;
+      tm_fence_shared();
+      mbar_arrive(&sh.full[at.slot]);
+    }
+    if (!v && tid == 0) {  // an arrival that the notes are released by
+      sh.valid[n % Ring<D, false>::info] = x.valid;
+      mbar_arrive(&sh.full[at.slot]);
+    }
+  };
+  // K of tile n + 1 before V of tile n: K's place is free as soon as its scores are there, V's only after its softmax
+  while (next(a, first, per, walk, lane)) {
+    then = look_up(a, s.b, s.t0, lane);
+    Pieces x = places(s.t0);
+    put(x, n, false);
+#pragma unroll 1
+    for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
+      Pieces y = x;
+      if (t + 1 < s.t1) {
+        y = places(t + 1);
+        put(y, n + 1, false);
+      }
+      put(x, n, true);
+      x = y;
     }
   }
   asm volatile("cp.async.wait_all;" ::: "memory");
