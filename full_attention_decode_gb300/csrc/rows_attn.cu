@@ -19,8 +19,8 @@
 // joined by the last of the item's CTAs; those of a block of many rows by a second launch, spread over the GPU: one CTA that
 // joined a block of 128 columns would read 2.5 MB.
 //
-// What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 90 us,
-// 4.6 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8192 tokens: 38 us, 228 TFLOP/s, where
+// What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 78 us,
+// 5.3 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8192 tokens: 34 us, 251 TFLOP/s, where
 // seven tiles a CTA share with the way in and the join. Turbo8, 16 trees: 144 us, the chain of loader, product and softmax a
 // tile (of 166 us that it took before the join was made short, 37 were the loader's arithmetic, 23 the softmax, 9 the products).
 //
@@ -391,7 +391,8 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* 
       mbar_arrive(&sh.full[at.slot]);
     }
   };
-  // K of tile n + 1 before V of tile n: K's place is free as soon as its scores are there, V's only after its softmax
+  // K of tile n + 1 before V of tile n: K's place is free as soon as its scores are there, V's only after its softmax (32 rows through
+  // windows of 4096: 78 us, V of a tile straight after its K 89)
   while (next(a, first, per, walk, lane)) {
     then = look_up(a, s.b, s.t0, lane);
     Pieces x = places(s.t0);
@@ -1383,8 +1384,7 @@ cudaError_t rows_attend_attributes() {
 cudaError_t rows_attend(const RowsAttend& args, cudaStream_t st) {
   RowsAttend a = args;
   // Eight columns, one for each warp of the softmax, are joined where their last part is made (one row through a window of 512:
-  // 13.7 us, by a second launch 15.1; 32 rows through windows of 128 15.2 and 18.1, of 4096 89.4 and 89.8; 1024 rows through windows
-  // of 64 273 and 263); more columns by CTAs of their own.
+  // 13.7 us, by a second launch 15.1; 32 rows through windows of 128 15.2 and 18.1; 1024 rows through windows of 64 273 and 263); more columns by CTAs of their own.
   a.here = a.H / a.c.Hkv * (a.r.row_start ? a.r.n_rows : 1) <= 8;
   const bool t8 = a.c.ks != nullptr;
 #define CALL(DD) return t8 ? launch<DD, true>(a, st) : launch<DD, false>(a, st)
