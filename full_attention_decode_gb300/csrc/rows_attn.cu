@@ -19,9 +19,9 @@
 // joined by the last of the item's CTAs; those of a block of many rows by a second launch, spread over the GPU: one CTA that
 // joined a block of 128 columns would read 2.5 MB.
 //
-// What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 78 us,
-// 5.3 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8192 tokens: 34 us, 251 TFLOP/s, where
-// seven tiles a CTA share with the way in and the join. Turbo8, 16 trees: 144 us, the chain of loader, product and softmax a
+// What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 76 us,
+// 5.4 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8191 tokens: 31 us, 273 TFLOP/s, where
+// seven tiles a CTA share with the way in and the join. Turbo8, 16 trees: 139 us, the chain of loader, product and softmax a
 // tile (of 166 us that it took before the join was made short, 37 were the loader's arithmetic, 23 the softmax, 9 the products).
 //
 // Roundings. bf16: Q, K, V exactly, P as hi + lo bf16 (2^-16). Turbo8: the rotated q as f16 over the power of two of its largest
@@ -54,10 +54,10 @@ constexpr int kRegsLaunch = 96;
 constexpr int kRegsSoft = 112, kRegsLoad = 80;
 static_assert(8 * (kRegsSoft + kRegsLoad) <= 16 * kRegsLaunch, "no more than the block was launched with");
 constexpr uint32_t kHalf = kTile / 2;  // tokens of a thread
-// What an item's beginning and end cost a CTA, in tiles (64 nodes over 8192 tokens: 1 40.4 us, 2 38.7, 4 37.5; 32 rows through
-// windows: 99.1, 98.9, 100.6), and the tiles of a stretch at least (a row through a window of 512: 1 17.7 us, 2 17.7, 3 19.4, 4 21.0;
-// eight nodes over 1000 tokens: 20.9, 19.6, 20.6, 21.4).
-constexpr uint32_t kLead = 2, kLeast = 2;
+// What an item's beginning and end cost a CTA, in tiles (1, 2, 4, 6: 64 nodes over 8191 tokens 33.3, 32.0, 29.3, 29.7 us, 16
+// Turbo8 trees 149, 143, 139, 141, 32 rows through windows of 4096 80.2, 78.6, 76.3, 77.0, of 128 -, 15.2, 18.7, 18.5), and the tiles of
+// a stretch at least (1, 2, 3: a row through a window of 512 13.0, 13.5, 14.2, eight nodes over 1000 tokens 14.0, 14.7, 15.9).
+constexpr uint32_t kLead = 4, kLeast = 1;
 // How far a score may lie above what P and l refer to before O, in tensor memory, is read, scaled and written back: weights up to
 // 2^8 cost bf16's hi + lo and fp32 sums no digit, and after an item's first tiles nearly none moves them.
 constexpr float kSlack = 8.f;
