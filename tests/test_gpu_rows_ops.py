@@ -939,3 +939,15 @@ def test_a_row_of_many_is_the_row_alone(vocab):
         assert one[0][0] == many[0][r] and one[1][0] == many[1][r]
     eight = run_sample(x[:8].clone(), u[:8], t[:8], k[:8], p[:8], m[:8])
     assert (eight[0] == many[0][:8]).all() and (eight[1] == many[1][:8]).all()
+
+
+@pytest.mark.parametrize("heads", ["tiny", "tiny_alt", "4b", "twelve"])
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("rows", [None, [20]])
+def test_more_parts_than_a_column_has_lanes(heads, fmt, rows):
+    """A long item lies in many CTAs, whose parts a column's 8 to 32 lanes take in rounds: inside the launch (one
+    row) and by a second one, with a gate."""
+    s = setup(heads, fmt, [7000], rows, page=16)
+    gate = bf16(s.rng.standard_normal((s.n_rows, s.H, s.D))).cuda()
+    check(s, run_window(s, 6900, 4, gate=gate), expect(s, lambda b, i, p: visible_window(p, 6900, 4), gate))
+    assert status(s) == 0
