@@ -462,11 +462,19 @@ def qwen35_window_attention(cfg, kv, rows, window: int, n_first: int, q, out, sc
 
 
 def qwen35_sample(logits, u, token, temperature=None, top_k=None, top_p=None, min_p=None, prob=None, stream=None):
-    """logits: bf16 [n_rows][vocab], values of a row side by side, or [vocab]."""
-    n_rows, stride = (logits.shape[0], logits.stride(0)) if len(logits.shape) == 2 else (1, logits.shape[-1])
-    return lib().qwen35_sample(_ptr(logits), n_rows, logits.shape[-1], max(stride, logits.shape[-1]), _ptr(u),
-                               _ptr(temperature), _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(token), _ptr(prob),
-                               _stream(stream))
+    """logits: bf16 [n_rows][vocab], values of a row side by side (rows at any stride, 0 of expand() among them), or [vocab]."""
+    shape = logits.shape
+    if not 1 <= len(shape) <= 2:
+        raise ValueError("logits are [n_rows][vocab] or [vocab]")
+    n_rows, vocab = (shape[0] if len(shape) == 2 else 1), shape[-1]
+    if isinstance(logits, torch.Tensor):
+        if vocab > 1 and logits.stride(-1) != 1:
+            raise ValueError("the values of a row of logits lie side by side")
+        stride = logits.stride(0) if n_rows > 1 else vocab
+    else:  # a stand-in without a tensor's strides
+        stride = max(logits.stride(0), vocab)
+    return lib().qwen35_sample(_ptr(logits), n_rows, vocab, stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p),
+                               _ptr(min_p), _ptr(token), _ptr(prob), _stream(stream))
 
 
 def qwen35_debug_scratch_offset(cfg, kind, name: str) -> int:

@@ -1466,7 +1466,7 @@ int qwen35_window_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv,
 int qwen35_sample(const qwen35_bf16* logits, uint32_t n_rows, uint32_t vocab, uint64_t row_stride, const float* u,
                   const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
                   int32_t* token, float* prob, void* stream) {
-  if (!aligned16(logits) || n_rows == 0 || vocab == 0 || row_stride < vocab || !u || !token)
+  if (!aligned16(logits) || n_rows == 0 || vocab == 0 || (row_stride < vocab && row_stride != 0) || !u || !token)
     return QWEN35_ERR_INVALID_ARGUMENT;
   if (!aligned4(u) || !aligned4(temperature) || !aligned4(top_k) || !aligned4(top_p) || !aligned4(min_p) ||
       !aligned4(token) || !aligned4(prob))

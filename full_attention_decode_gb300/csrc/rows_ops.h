@@ -63,7 +63,7 @@ cudaError_t rows_attend_attributes();  // once per device, before the first rows
 cudaError_t rows_attend(const RowsAttend& a, cudaStream_t st);
 
 struct Sample {
-  const uint16_t* logits;  // [n_rows] values of vocab, row_stride apart
+  const uint16_t* logits;  // [n_rows] values of vocab, row_stride apart (0: all rows are one)
   const float* u;
   const float* temperature;
   const int32_t* top_k;

@@ -671,8 +671,8 @@ QWEN35_API int qwen35_cache_keep(const qwen35_config* cfg, const qwen35_kv_cache
  * largest weight, so the choice is that of the exact sums but for borders nearer than that; a token of less
  * has no weight. NaN logits are never chosen (-1, with probability 0, if every logit is one); where the largest is infinite, tokens
  * equal to it have weight 1 and all others none.
- *  - logits bf16, row r at logits + r * row_stride (row_stride >= vocab, in elements), as
- *    qwen35_lm_head_greedy writes them; vocab at most 524160, n_rows at most 65536 (UNSUPPORTED above).
+ *  - logits bf16, row r at logits + r * row_stride (row_stride >= vocab, in elements, or 0: one row of logits for
+ *    all n_rows draws), as qwen35_lm_head_greedy writes them; vocab at most 524160, n_rows at most 65536 (UNSUPPORTED above).
  *  - u fp32 [n_rows], from [0, 1) (outside: as its nearest end; NaN: 0); temperature, top_p, min_p fp32 [n_rows], top_k
  *    int32 [n_rows], each or NULL: 1, 1, 0 and 0. All in device memory, read when the kernel runs.
  *  - token int32 [n_rows], written; prob NULL, or fp32 [n_rows]: the token's probability among what was left.

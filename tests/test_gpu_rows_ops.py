@@ -951,3 +951,17 @@ def test_more_parts_than_a_column_has_lanes(heads, fmt, rows):
     gate = bf16(s.rng.standard_normal((s.n_rows, s.H, s.D))).cuda()
     check(s, run_window(s, 6900, 4, gate=gate), expect(s, lambda b, i, p: visible_window(p, 6900, 4), gate))
     assert status(s) == 0
+
+
+@pytest.mark.parametrize("vocab", [5, 777, 4097, 248320])
+def test_tokens_drawn_from_one_row(vocab):
+    """Logits of row stride 0, of one row, in a column of a wider tensor: as their contiguous copies."""
+    rng = np.random.default_rng(vocab)
+    u = rng.random(12)
+    x = logits(1, vocab, 7)[0].expand(12, -1)
+    assert x.stride(0) == 0
+    check_sample(x, u, k=rng.integers(0, 40, 12))
+    a, b = run_sample(x, u), run_sample(x.contiguous(), u)
+    assert (a[0] == b[0]).all() and (a[1] == b[1]).all()
+    one = torch.zeros(1, dtype=torch.bfloat16, device="cuda").expand(3, 1)
+    assert run_sample(one, [0.0, 0.5, 1.0])[0].tolist() == [0, 0, 0]

@@ -3,6 +3,7 @@ enqueued (fake, never dereferenced addresses, so only where no CUDA device is pr
 scratch sizes."""
 
 import pytest
+import torch
 
 from full_attention_decode_gb300 import binding as B
 from full_attention_decode_gb300 import synth
@@ -137,3 +138,51 @@ def test_sample_arguments():
     assert B.lib().qwen35_sample(0xB000000, 3, 500, 499, 0xC000000, None, None, None, None, 0xD000000, None, 0) == BAD
     assert call(vocab=524161) == UNSUPPORTED
     assert call(n=65537) == UNSUPPORTED
+
+
+def _called_with(monkeypatch, logits):
+    """(n_rows, vocab, row_stride) that the binding hands to the C entry, which is not called."""
+    got = []
+
+    class _Lib:
+        @staticmethod
+        def qwen35_sample(ptr, n_rows, vocab, row_stride, *_):
+            got.append((n_rows, vocab, row_stride))
+            return 0
+
+    monkeypatch.setattr(B, "lib", lambda: _Lib)
+    assert B.qwen35_sample(logits, Y, Z, stream=0) == 0
+    return got[0]
+
+
+def test_sample_takes_logits_as_they_lie(monkeypatch):
+    """Every element that the C entry reads, row r's at r * row_stride + [0, vocab), is one of the tensor's rows."""
+    base = torch.arange(6000, dtype=torch.float32)
+    for x in (base[:1000], base[:1000].expand(4, -1), base[:1].expand(3, 1), base[:6000].view(6, 1000), base.view(6, 1000)[::2],
+              base.view(6, 1000)[:, 8:900], base.view(6, 1000)[2:3], base.view(1000, 6)[:, :1], base[:1000].view(1, 1000).expand(5, -1),
+              base[16:].as_strided((5, 1000), (1008, 1)), base.view(1000, 6)[:4, :1], base[:6].view(6, 1).expand(6, 1)):
+        n, vocab, stride = _called_with(monkeypatch, x)
+        rows = x.view(1, -1) if x.dim() == 1 else x
+        assert (n, vocab) == tuple(rows.shape)
+        for r in range(n):
+            i = x.storage_offset() + r * stride
+            assert torch.equal(base[i:i + vocab], rows[r])
+
+
+@pytest.mark.parametrize("x", [torch.zeros(1000, 4).t(), torch.zeros(2000)[::2], torch.zeros(4, 2000)[:, ::2],
+                               torch.zeros(1).expand(4, 1000), torch.zeros(2, 3, 1000), torch.zeros(())])
+def test_sample_refuses_logits_that_no_stride_describes(x):
+    with pytest.raises(ValueError):
+        B.qwen35_sample(x, Y, Z, stream=0)
+
+
+@no_device
+def test_sample_strides():
+    """0: one row for all; rows that overlap otherwise are refused."""
+    def call(n, stride):
+        return B.lib().qwen35_sample(0xB000000, n, 500, stride, 0xC000000, None, None, None, None, 0xD000000, None, 0)
+
+    assert call(3, 0) == call(1, 0) == call(3, 500) == call(3, 501) == OK_BUT_NO_DEVICE
+    assert call(3, 1) == call(3, 499) == call(1, 499) == BAD
+    x = torch.zeros(1000).as_strided((3, 500), (250, 1))
+    assert B.qwen35_sample(x, Y, Z, stream=0) == BAD
