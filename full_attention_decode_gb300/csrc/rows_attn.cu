@@ -664,7 +664,7 @@ __device__ __forceinline__ void join_columns(const RowsAttend& a, const Work& wo
   for (uint32_t k = piece; k < n; k += L) {
     const float4 x = k < L ? mine : ml(k);
     if (T8) V = fmaxf(V, exponent(x));
-    l += x.x == -INFINITY ? 0.f : x.y * ex2(x.x - mu);
+    l += x.x == -INFINITY ? x.y : x.y * ex2(x.x - mu);  // no score that is a number: 0 of no token, or NaN
   }
 #pragma unroll
   for (uint32_t w = 1; w < L; w <<= 1) {

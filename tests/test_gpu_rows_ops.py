@@ -965,3 +965,74 @@ def test_tokens_drawn_from_one_row(vocab):
     assert (a[0] == b[0]).all() and (a[1] == b[1]).all()
     one = torch.zeros(1, dtype=torch.bfloat16, device="cuda").expand(3, 1)
     assert run_sample(one, [0.0, 0.5, 1.0])[0].tolist() == [0, 0, 0]
+
+
+# ---------------------------------------------------------------- what is no number
+
+
+def under(s, kind, first=4):
+    """(call, see): trees of the rows (stars), or windows of 10^6 or 64 tokens."""
+    if kind == "tree":
+        parents = [[-1] + [0] * (r - 1) for r in s.rows]
+        return lambda: run_tree(s, parents), lambda b, i, p: visible_tree(parents[b], p - i, i)
+    window = 10 ** 6 if kind == "all" else 64
+    return lambda: run_window(s, window, first), lambda b, i, p: visible_window(p, window, first)
+
+
+@pytest.mark.parametrize("heads", ["4b", "tiny_alt", "wide"])
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("kind", ["tree", "all", "near"])
+@pytest.mark.parametrize("bad", [NAN, float("inf")])
+def test_a_query_without_a_number_gives_none(heads, fmt, kind, bad):
+    """One element of a head's query is no number: its scores are NaN (or, of an infinity, of both signs), in every part
+    of its tokens, and so are its outputs; the others' are as they were."""
+    s = setup(heads, fmt, [4000 + 3, 1, 70 + 2], [3, 1, 2], page=16)
+    call, see = under(s, kind)
+    want = expect(s, see)
+    s.q[1, 1, 5] = s.q[3, 0, 0] = bad
+    got = f64(call())
+    if not np.isnan(bad) and fmt == BF16:  # an infinite score of one sign among tokens: NaN too, but for a row of one token
+        bad_rows = [(1, 1)]                # or of scores that are all -inf, which weigh nothing
+    else:
+        bad_rows = [(1, 1), (3, 0)]
+    for r, h in bad_rows:
+        assert np.isnan(got[r, h]).all(), (r, h)
+    for r, (ref, tol) in want.items():
+        for h in range(s.H):
+            if (r, h) not in [(1, 1), (3, 0)]:
+                assert (np.abs(got[r, h] - ref[h]) <= 2.0 ** -8 * np.abs(ref[h]) + tol).all(), (r, h)
+
+
+@pytest.mark.parametrize("heads", ["4b", "tiny"])
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("kind", ["tree", "all", "near"])
+@pytest.mark.parametrize("token", [0, 3999, 4000, 4001])
+def test_a_key_without_a_number_spoils_the_rows_that_see_it(heads, fmt, kind, token):
+    """Every element of one key is NaN. In a part of its own or not, its rows are NaN."""
+    s = setup(heads, fmt, [4000 + 3, 1], [3, 1], page=16)
+    call, see = under(s, kind, first=0)
+    want = expect(s, see)
+    at = s.at(0, token)
+    if fmt == BF16:
+        s.t["k"][at, 0] = NAN
+    else:
+        s.t["ks"][at, :s.D // 16] = bf16([NAN]).view(torch.int16).item()
+    got, g = f64(call()), s.H // s.Hkv
+    for r, (ref, tol) in want.items():
+        b, i, p = (0, r, 4000 + r) if r < 3 else (1, 0, 0)
+        spoiled = b == 0 and token in see(b, i, p)
+        if spoiled:
+            assert np.isnan(got[r, :g]).all()
+        keep = slice(g if spoiled else 0, None)
+        assert (np.abs(got[r, keep] - ref[keep]) <= 2.0 ** -8 * np.abs(ref[keep]) + tol).all()
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_a_row_of_one_token_whose_key_is_no_number(fmt):
+    s = setup("4b", fmt, [300, 64, 1], None, page=16)
+    for b, p in enumerate((299, 63, 0)):
+        if fmt == BF16:
+            s.t["k"][s.at(b, p)] = NAN
+        else:
+            s.t["ks"][s.at(b, p)] = bf16([NAN]).view(torch.int16).item()
+    assert torch.isnan(run_window(s, 1, 0)).all()
