@@ -31,7 +31,8 @@
 //
 // A tile that not every row of the item sees to its end may hold anything where it is not seen, and 0 times infinity would
 // spoil the rows that do not: V's infinities and NaN are taken out of such tiles (Turbo8: of all) on their way in, and
-// added by plain arithmetic for the rows that see them (`mend`).
+// added by plain arithmetic for the rows that see them (`mend`). Other bf16 tiles go in as they lie; where a stretch's sums
+// are no numbers then, they are put right at its end (`put_infinities`), so it does not matter where in a tile a token lies.
 #include "rows_ops.h"
 
 #include "cache_ops.cuh"
@@ -673,7 +674,8 @@ __device__ __forceinline__ void join_columns(const RowsAttend& a, const Work& wo
   }
   const float down = T8 ? finite_or_0(V) : 0.f;
   const auto factor = [&](const float4& y) {
-    return y.x == -INFINITY || (T8 && y.z == -INFINITY) ? 0.f : ex2(exponent(y) - down);
+    if (y.x == -INFINITY || (T8 && y.z == -INFINITY)) return 0.f;
+    return fmaxf(ex2(exponent(y) - down), T8 ? 0.f : 1.4e-45f);  // bf16: an infinity counts, however small its weight
   };
   const float own = factor(mine);
   float x[8] = {};
@@ -757,6 +759,56 @@ __device__ __noinline__ void mend(const RowsAttend& a, const Block& b, uint32_t 
       const float o = __uint_as_float(tm_ld1(o_col + d));
       tm_st1(o_col + d, __float_as_uint(see ? fmaf(w[j], x, o) : o));
       tm_stored();
+    }
+  }
+}
+
+// O of a stretch over a bf16 cache where infinities among V that its tiles hold as they lie have left NaN (hi and lo of a
+// weight times one, and 0 or less times one): every infinity and NaN among the values that a row sees is added to it, whatever its
+// weight, the first in the NaN's place. A warp's 32 rows and its half of O's columns, D / 64 a lane as V is looked through, a token
+// at a time; a column that every row holds for good is passed over. Rare, so plain and slow.
+template <int D>
+__device__ __noinline__ void put_infinities(const RowsAttend& a, const Stretch& st, uint32_t half, bool live, uint32_t p,
+                                            uint64_t line0, uint64_t line1, uint32_t o_col) {
+  constexpr uint32_t K = D / 64;
+  const Block& b = st.b;
+  const uint32_t lane = threadIdx.x % 32, c0 = half * (D / 2);
+  constexpr uint32_t kNone = 0x7fc00001u;  // a NaN that is the sum's own; the matrix unit's is 0x7fffffff
+  uint32_t held = 0;  // two bits a column of the lane: what all rows have there, 1 and 2 an infinity of a sign, 3 NaN
+#pragma unroll 1
+  for (uint32_t i = st.t0 * kTile; i < min(st.t1 * kOctets, b.octets) * 8; ++i) {
+    const uint32_t tok = b.token(i / 8) + i % 8;
+    bool see;
+    if (a.parent) {
+      const uint32_t start = b.pos - b.index, off = tok - start;
+      see = tok < start || (off < 64 ? line0 >> off & 1 : off < 128 && (line1 >> (off - 64) & 1));
+    } else {
+      see = tok <= p && ((uint64_t)tok + a.window > p || tok < a.n_first);
+    }
+    see &= live;
+    size_t row;
+    if (!__any_sync(0xffffffffu, see) || !cache_row(a.c, b.seq, tok, row)) continue;
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v) + (row * a.c.Hkv + st.g) * D + c0 + lane * K;
+#pragma unroll 1
+    for (uint32_t e = 0; e < K; ++e) {
+      const float x = bf16f(v[e]);
+      const uint32_t has = held >> (2 * e) & 3u, want = x != x ? 3u : x > 0.f ? 1u : 2u;
+      uint32_t who = __ballot_sync(0xffffffffu, !(fabsf(x) < INFINITY) && has != 3u && has != want);
+      while (who) {
+        const uint32_t from = __ffs(who) - 1, col = o_col + c0 + from * K + e;
+        who &= who - 1;
+        const float y = __shfl_sync(0xffffffffu, x, from);
+        uint32_t u = tm_ld1(col);
+        if (see && u != kNone) {
+          const float o = __uint_as_float(u), sum = o == o ? o + y : y;
+          u = sum == sum ? __float_as_uint(sum) : kNone;
+        }
+        tm_st1(col, u);
+        tm_stored();
+        const bool nan = __all_sync(0xffffffffu, !live || u == kNone);
+        const bool same = __all_sync(0xffffffffu, !live || __uint_as_float(u) == y);
+        if (lane == from) held = (held & ~(3u << (2 * e))) | (nan ? 3u : !same ? 0u : y > 0.f ? 1u : 2u) << (2 * e);
+      }
     }
   }
 }
@@ -1081,17 +1133,31 @@ struct Softmax {
     const size_t first = nat ? (size_t)st.b.row * a.H + st.g * cols : (size_t)blockIdx.x * kM;
     const uint32_t wide = nat ? cols : kM;
     float* to = (nat ? work.nat : work.cont) + first * D + row * 8;
+    float odd = 0.f;  // NaN of an infinity or a NaN
+    const auto write = [&] {
 #pragma unroll 1
-    for (uint32_t c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
-      uint32_t r[32];
-      tm_ld32(o_col() + c, r);
-      tm_loaded(r);
-      if (live) {
+      for (uint32_t c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
+        uint32_t r[32];
+        tm_ld32(o_col() + c, r);
+        tm_loaded(r);
+        if (live) {
 #pragma unroll
-        for (uint32_t i = 0; i < 32; i += 8) {
-          const uint32_t w[8] = {r[i], r[i + 1], r[i + 2], r[i + 3], r[i + 4], r[i + 5], r[i + 6], r[i + 7]};
-          store32(to + (c + i) * (size_t)wide, a.wide, w);
+          for (uint32_t i = 0; i < 32; i += 8) {
+            const uint32_t w[8] = {r[i], r[i + 1], r[i + 2], r[i + 3], r[i + 4], r[i + 5], r[i + 6], r[i + 7]};
+            store32(to + (c + i) * (size_t)wide, a.wide, w);
+          }
+          if (!T8)
+#pragma unroll
+            for (uint32_t i = 0; i < 32; ++i) odd = fmaf(__uint_as_float(r[i]), 0.f, odd);
         }
+      }
+    };
+    write();
+    if constexpr (!T8) {
+      const bool number = live && !skip && l == l;  // else the row is NaN by its scores, or not written
+      if (__any_sync(0xffffffffu, number && odd != odd)) {
+        put_infinities<D>(a, st, half, number, p, line0, line1, o_col());
+        write();
       }
     }
     if (live && !half) (nat ? work.nat_ml : work.cont_ml)[first + row] = make_float4(m, skip ? -1.f : l + sh.sum[row], R, 0.f);

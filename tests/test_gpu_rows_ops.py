@@ -1036,3 +1036,47 @@ def test_a_row_of_one_token_whose_key_is_no_number(fmt):
         else:
             s.t["ks"][s.at(b, p)] = bf16([NAN]).view(torch.int16).item()
     assert torch.isnan(run_window(s, 1, 0)).all()
+
+
+@pytest.mark.parametrize("heads,quiet", [("4b", False), ("tiny", False), ("tiny_alt", False), ("tiny", True)])
+@pytest.mark.parametrize("kind", ["tree", "all", "near"])
+@pytest.mark.parametrize("tokens", [{0: 1}, {700: -1}, {3998: 1}, {4001: 1}, {5: 1, 70: 1, 3999: 1}, {64: 1, 2000: -1},
+                                    {2000: 1, 3996: 1, 4000: -1}, {3000: "nan"}, {10: 1, 4000: "nan"}], ids=str)
+def test_infinite_values_are_the_outputs_of_the_rows_that_see_them(heads, kind, tokens, quiet):
+    """bf16, wherever the token lies: one infinity, or several of one sign, give it, both signs or a NaN give NaN; the
+    other elements are as without. quiet: the tokens' scores lie 400 below the others."""
+    s = setup(heads, BF16, [4000 + 3, 50], [3, 1], page=16)
+    call, see = under(s, kind)
+    dim = s.D // 2 + 5
+    if quiet:
+        s.q = bf16(np.full(s.q.shape, 2.0))
+        for t in tokens:
+            s.t["k"][s.at(0, t)] = -400.0 / 2 / np.sqrt(s.D)
+            s.stands["k"][s.at(0, t)] = f64(bf16(-400.0 / 2 / np.sqrt(s.D)))
+    want = expect(s, see)
+    for t, sign in tokens.items():
+        s.t["v"][s.at(0, t), 0, dim] = NAN if sign == "nan" else sign * float("inf")
+    got, g = f64(call()), s.H // s.Hkv
+    for r, (ref, tol) in want.items():
+        b, i, p = (0, r, 4000 + r) if r < 3 else (1, 0, 49)
+        seen = {sign for t, sign in tokens.items() if b == 0 and t in see(b, i, p)}
+        expected = None if not seen else np.nan if len(seen) > 1 or "nan" in seen else seen.pop() * np.inf
+        for h in range(s.H):
+            ok = np.abs(got[r, h] - ref[h]) <= 2.0 ** -8 * np.abs(ref[h]) + tol
+            if h < g and expected is not None:
+                assert np.array_equal(got[r, h, dim], expected, equal_nan=True), (r, h, got[r, h, dim], expected)
+                ok[dim] = True
+            assert ok.all(), (r, h)
+
+
+@pytest.mark.parametrize("kind", ["tree", "all"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_every_value_infinite(kind, sign):
+    """Whole caches of one infinity, then with one of the other sign."""
+    s = setup("4b", BF16, [1500 + 40], [40], page=16)
+    call, _ = under(s, kind)
+    s.t["v"][:] = sign * float("inf")
+    assert (call() == sign * float("inf")).all()
+    s.t["v"][s.at(0, 777)] = -sign * float("inf")
+    assert torch.isnan(call()).all()
+    assert status(s) == 0
