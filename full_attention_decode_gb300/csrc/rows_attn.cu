@@ -5,14 +5,15 @@
 // M = 128 rows of the products (TMEM's lanes); the tokens come in tiles of 64:
 //   S [128 x 64] = Q [128 x D] K^T,  P = 2^(S - m),  O [128 x D] += P [128 x 64] V,
 // on the fifth-generation tensor cores: Q, K and V in shared memory (V as it lies, rows along the inner
-// dimension), S and O in tensor memory, P written back there as the second product's first factor. A decode row of 4
+// dimension), S and O in tensor memory, P written back there as the second product's first factor (Turbo8: over its S, as q's
+// upper part lies there too). A decode row of 4
 // q-heads leaves most of M empty; what bounds the call is the bytes of K and V all the same: a tile of D = 256
 // is 64 KB, 1.5 us of an SM's share of the memory, its products 1 us.
 //
 // Roles of a CTA's 17 warps: 0-7 are the softmax, two threads a row with 32 of a tile's 64 tokens each, which
 // exchange their maxima; 8-15 fill a ring of K and V tiles, 16-byte pieces by asynchronous copies (pages as small as 8
 // tokens, rows outside as zeros), Turbo8's as they lie and then as f16; one thread of warp 16 issues the products. The softmax
-// of a tile runs under the product of the tile before and the scores of the next (two S, two P).
+// of a tile runs under the product of the tile before and the scores of the next (two S, two P; Turbo8 with one S and two P beside it: 16 trees 168 us where 157).
 //
 // The line of all items' tiles is cut into equal stretches, one CTA an SM. A stretch leaves its sums and maxima in the
 // scratch, and an item's parts are added up in the order of the CTAs, so equal calls give equal bits. Few columns are
@@ -21,12 +22,15 @@
 //
 // What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 76 us,
 // 5.4 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8191 tokens: 31 us, 273 TFLOP/s, where
-// seven tiles a CTA share with the way in and the join. Turbo8, 16 trees: 139 us, the chain of loader, product and softmax a
-// tile (of 166 us that it took before the join was made short, 37 were the loader's arithmetic, 23 the softmax, 9 the products).
+// seven tiles a CTA share with the way in and the join. Turbo8, 16 trees: 157 us, the chain of loader, products and softmax a
+// tile, 3.3 us: conversions and exponentials share a pipe (1 us), shared memory's bandwidth takes 1.4, the products 1.3. Scores of
+// one f16 q and one f16 K took 139: q's lower part costs 6 us, K's second part 4, the wait for P's product under the next S and
+// the way of q about 8.
 //
-// Roundings. bf16: Q, K, V exactly, P as hi + lo bf16 (2^-16). Turbo8: the rotated q as f16 over the power of two of its largest
-// value; K's and V's codes times scale / 2^E, E the exponent of the token's largest scale, as f16 (a product of 4
-// and 8 bits, rounded to 11); 2^E of K multiplies the score in fp32, E of V goes into the weight's exponent: weights of V are
+// Roundings. bf16: Q, K, V exactly, P as hi + lo bf16 (2^-16). Turbo8: the rotated q as hi + lo f16 over the power of two of its
+// largest value (2^-22 of a value or 2^-25 of the largest); K's codes times scale / 2^E, E the exponent of the token's largest
+// scale, exactly, as two f16 (a product of 4 and 8 bits has 12, f16 11), lo times the second left out (at most 2^-11 2^-7 of a term); V's as
+// one f16 (2^-11); 2^E of K multiplies the score in fp32, E of V goes into the weight's exponent: weights of V are
 // 2^((x - m) + E - R) in f16, R following the largest within 2^4, so a token counts by what it adds. l refers to m alone.
 //
 // A tile that not every row of the item sees to its end may hold anything where it is not seen, and 0 times infinity would
@@ -64,22 +68,25 @@ constexpr uint32_t kLead = 4, kLeast = 1;
 constexpr float kSlack = 8.f;
 constexpr float kSlack8 = 4.f, kUp8 = 11.f;  // Turbo8's weights of V: at most 2^(kUp8 + kSlack8) in f16
 
-// Q, then the ring of K (even slots) and V tiles as the products take them; Turbo8: then `raw` halves of tiles as they lie in
-// the cache, on their way. (Loads into registers instead hang on the L1, which has a few KB beside this: 16 trees 174 us.)
+// Q (Turbo8: its lower part), then the ring of K (even slots; Turbo8: two parts) and V tiles as the products take them; Turbo8:
+// then `raw` halves of tiles as they lie in the cache, on their way. (Loads into registers instead hang on the L1, which has a
+// few KB beside this: 16 trees 174 us.)
 template <int D, bool T8>
 struct Ring {
   static constexpr uint32_t bytes = kTile * D * 2;  // K or V of a tile
+  static constexpr uint32_t k_bytes = (T8 ? 2 : 1) * bytes;
   static constexpr uint32_t slots = T8 ? (D == 256 ? 2 : 4) : D == 256 ? 4 : 8;
   static constexpr uint32_t slab = kTile * 128, q_slab = kM * 128;  // 64 dims of all rows
   static constexpr uint32_t q = kM * D * 2;
-  static constexpr uint32_t raw = T8 ? (D == 256 ? 3 : 6) : 0, raw_bytes = kTile * (D + D / 8);  // codes, then scales
-  static constexpr uint32_t all = q + slots * bytes + raw * raw_bytes;
+  static constexpr uint32_t raw = T8 ? (D == 256 ? 2 : 6) : 0, raw_bytes = kTile * (D + D / 8);  // codes, then scales
+  static constexpr uint32_t places = slots / 2 * (k_bytes + bytes), all = q + places + raw * raw_bytes;
+  static __device__ __forceinline__ uint32_t at(uint32_t slot) { return slot / 2 * (k_bytes + bytes) + slot % 2 * k_bytes; }
   static constexpr uint32_t info = D == 256 ? 4 : 8;  // tiles whose notes are kept: the ring's and two of the softmax's
   static_assert(slots / 2 + 2 <= info, "notes");
 };
 
 // A row of the call as every CTA keeps it: position, sequence, which of its sequence's rows it is, and how many rows the
-// block has that begins with it.
+// block has that begins with it. Positions of more rows than shared memory has room for (a.near) are looked up again.
 struct RowNote {
   uint32_t pos, bits;
   __device__ __forceinline__ uint32_t seq() const { return bits & 4095u; }
@@ -88,10 +95,23 @@ struct RowNote {
   __device__ __forceinline__ bool ok() const { return bits >> 31; }
 };
 static_assert(kMaxSeqs <= 4096 && kMaxQueries <= 2048, "bits of a row's note");
-// Behind the prefix sums [n_rows + 1].
-__device__ __forceinline__ RowNote* notes_of(const uint32_t* first, uint32_t n_rows) {
-  return reinterpret_cast<RowNote*>(const_cast<uint32_t*>(first) + (n_rows + 2) / 2 * 2);
-}
+// Behind the prefix sums [n_rows + 1]: bits [n_rows], positions [n_rows].
+struct RowNotes {
+  uint32_t *bits, *pos;
+  __device__ __forceinline__ RowNotes(const RowsAttend& a, const uint32_t* first)
+      : bits(const_cast<uint32_t*>(first) + a.r.n_rows + 1), pos(a.near ? bits + a.r.n_rows : nullptr) {}
+  __device__ __forceinline__ void put(uint32_t r, const RowNote& x) {
+    bits[r] = x.bits;
+    if (pos) pos[r] = x.pos;
+  }
+  __device__ __forceinline__ RowNote without_pos(uint32_t r) const { return {0, bits[r]}; }
+  __device__ __forceinline__ RowNote get(const RowsAttend& a, uint32_t r) const {
+    RowNote x = without_pos(r);
+    x.pos = pos ? pos[r] : (uint32_t)a.r.pos[x.seq()] + x.index();
+    return x;
+  }
+};
+constexpr uint32_t rows_bytes(uint32_t n_rows, bool near) { return ((near ? 3 : 2) * n_rows + 1) * 4; }
 
 // A block of rows and the tokens it sees: octets of eight tokens, nA first ones, then from b8 on.
 struct Block {
@@ -151,12 +171,13 @@ struct Walk {
 __device__ __forceinline__ bool next(const RowsAttend& a, const uint32_t* first, uint32_t per, Walk& k, uint32_t lane) {
   __syncwarp();
   if (lane == 0) {
-    const RowNote* note = notes_of(first, a.r.n_rows);
+    const RowNotes notes(a, first);
     const uint32_t Hkv = a.c.Hkv, w1 = k.w1;
     uint32_t w = k.w, row = k.row, more = 0;
     while (w < w1 && !more) {
       while (first[row + 1] * Hkv <= w) ++row;
-      const Block b = block_of(a, row, note[row].rows(), note[row]);
+      const RowNote note = notes.get(a, row);
+      const Block b = block_of(a, row, note.rows(), note);
       const uint32_t length = b.tiles() + kLead, in = w - first[row] * Hkv;
       const uint32_t at = in % length, used = min(length - at, w1 - w);
       k.s.b = b;
@@ -358,7 +379,7 @@ __device__ __forceinline__ void load_plain(const RowsAttend& a, const uint32_t* 
   const auto put = [&](const Pieces& x, uint32_t n, bool v) {
     const Place<D, false> at(2 * n + v);
     if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
-    uint8_t* slot = ring + at.slot * Ring<D, false>::bytes;
+    uint8_t* slot = ring + Ring<D, false>::at(at.slot);
     const uint16_t* base = reinterpret_cast<const uint16_t*>(v ? a.c.v : a.c.k) + s.g * D + 8 * c;
     if (!v || x.full) {
       const uint32_t dst = smem_addr(slot) + to;
@@ -437,7 +458,7 @@ struct LoadTurbo8 {
     uint32_t in, row[J], scale_row, g;
   } kp, vp;
 
-  __device__ __forceinline__ uint8_t* raw(uint32_t st) const { return ring + R::slots * R::bytes + st * R::raw_bytes; }
+  __device__ __forceinline__ uint8_t* raw(uint32_t st) const { return ring + R::places + st * R::raw_bytes; }
   __device__ __forceinline__ void begin() {
     more = next(a, first, per, walk, lane);
     if (!more) return;
@@ -509,12 +530,13 @@ struct LoadTurbo8 {
     if (any) copy(vp, a.c.v, a.c.vs);
     copied();
   }
-  // A half of tile n into the ring, as f16 over 2^E. K's arrival releases its scales and what octets are there, V's exponents have a
+  // A half of tile n into the ring, as f16 over 2^E. A code has 4 bits and a scale 8, their product 12, one more than f16: K goes in as
+  // two, with the scale's upper seven bits and with its last. K's arrival releases its scales and what octets are there, V's exponents have a
   // barrier of their own: they are known before their place in the ring is free.
   template <uint32_t V>
   __device__ __forceinline__ void put(uint32_t n, uint32_t st) {
     const uint8_t* from = raw(st);
-    uint32_t sc[J], mx[(J + 1) / 2], f[J], bad = 0;
+    uint32_t sc[J], mx[(J + 1) / 2], f[J], last[J], bad = 0;
 #pragma unroll
     for (uint32_t j = 0; j < J; ++j) sc[j] = *reinterpret_cast<const uint16_t*>(from + kTile * D + (r0 + j * STEP) * (D / 8) + 2 * c);
     // a token's largest scale, two pieces at once, from the lanes that have them; those that are no numbers do not count
@@ -538,14 +560,21 @@ struct LoadTurbo8 {
         if (V) sh.v_exp[n % R::info][r0 + j * STEP] = (float)e;
         else sh.k_scale[n % R::info][r0 + j * STEP] = pow2(e);
       }
-      float y = __uint_as_float(sc[j] << 16) * pow2(-e);
-      if (V && (sc[j] & 0x7f80u) == 0x7f80u) y = 0.f;
-      f[j] = pack_f16(y, y);
+      const bool number = (sc[j] & 0x7f80u) != 0x7f80u;
+      const float full = bf16f(sc[j]);
+      if (V) {
+        const float y = number ? full * pow2(-e) : 0.f;
+        f[j] = pack_f16(y, y);
+      } else {
+        const float seven = number ? bf16f(sc[j] & 0xfffeu) : full, rest = number ? full - seven : 0.f;
+        f[j] = pack_f16(seven * pow2(-e), seven * pow2(-e));
+        last[j] = pack_f16(rest * pow2(-e), rest * pow2(-e));
+      }
     }
     if (V) arrive_warp(&sh.v_notes[n % R::info], lane);
     const Place<D, true> at(2 * n + V);
     if (at.turn) wait(&sh.empty[at.slot], (at.turn - 1) & 1);
-    uint8_t* slab = ring + at.slot * R::bytes + (c / 4) * R::slab;
+    uint8_t* slab = ring + R::at(at.slot) + (c / 4) * R::slab;
     const uint32_t j8 = (c % 4) * 2;
 #pragma unroll
     for (uint32_t j = 0; j < J; ++j) {
@@ -561,12 +590,22 @@ struct LoadTurbo8 {
           for (int i = 0; i < 4; ++i) w[i] &= ~__vcmpeq4(w[i] & 0x7f7f7f7fu, 0x7f7f7f7fu);
         }
       }
-      uint32_t y[8];
-#pragma unroll
-      for (int i = 0; i < 8; ++i) y[i] = hmul2(e4m3_to_f16x2(w[i / 2] >> (16 * (i % 2))), f[j]);
       const uint32_t r = r0 + j * STEP;
-      *reinterpret_cast<uint4*>(slab + sw(r, j8)) = make_uint4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<uint4*>(slab + sw(r, j8 + 1)) = make_uint4(y[4], y[5], y[6], y[7]);
+#pragma unroll
+      for (uint32_t h = 0; h < 2; ++h) {
+        uint32_t x[4], y[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          x[i] = e4m3_to_f16x2(w[2 * h + i / 2] >> (16 * (i % 2)));
+          y[i] = hmul2(x[i], f[j]);
+        }
+        *reinterpret_cast<uint4*>(slab + sw(r, j8 + h)) = make_uint4(y[0], y[1], y[2], y[3]);
+        if (!V) {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) y[i] = hmul2(x[i], last[j]);
+          *reinterpret_cast<uint4*>(slab + R::bytes + sw(r, j8 + h)) = make_uint4(y[0], y[1], y[2], y[3]);
+        }
+      }
     }
     if (V) {
       const bool any = __any_sync(0xffffffffu, bad);
@@ -830,51 +869,101 @@ struct Softmax {
   float m, l, R;
 
   __device__ __forceinline__ uint32_t s_col(uint32_t n) const { return tmem + (n & 1) * kTile + half * kHalf; }
-  __device__ __forceinline__ uint32_t p_col(uint32_t n) const { return tmem + 128 + (n & 1) * 64 + half * (kHalf / 2); }
+  // Turbo8: over the S that it is made of, beside q's upper part
+  __device__ __forceinline__ uint32_t p_col(uint32_t n) const { return tmem + (T8 ? 0 : 128) + (n & 1) * 64 + half * (kHalf / 2); }
   __device__ __forceinline__ uint32_t o_col() const { return tmem + 256; }
 
   // Each thread copies the pieces that it goes on with: four lanes a column, sixteen dims of each 64 a lane.
   __device__ __forceinline__ void put_q(const Block& b, uint32_t g) {
-    constexpr uint32_t P = D / 64, PER = kSoft / 4;
-    const uint32_t cols = b.rows * group, l4 = tid & 3;
-    for (uint32_t col = tid / 4; col < cols; col += PER) {
-      const uint16_t* from = a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D + 16 * l4;
+    constexpr uint32_t P = D / 64;
+    // Turbo8: a warp and its other half take the columns of their lanes of tensor memory
+    constexpr uint32_t STEP = T8 ? 8 : kSoft / 4, TIMES = kM * 4 / kSoft;
+    const uint32_t cols = b.rows * group, l4 = tid & 3, from = T8 ? row / 32 * 32 + 16 * half + lane / 4 : tid / 4;
+    const auto piece = [&](uint32_t col, uint32_t i) {
+      return reinterpret_cast<uint4*>(q_sm + i / 2 * Ring<D, T8>::q_slab + sw(col, 2 * l4 + i % 2));
+    };
+    for (uint32_t k = 0, col = from; k < TIMES && col < cols; ++k, col += STEP) {
+      const uint16_t* q = a.q + ((size_t)(b.row + col / group) * a.H + g * group + col % group) * D + 16 * l4;
 #pragma unroll
-      for (uint32_t i = 0; i < P; ++i)
-#pragma unroll
-        for (uint32_t h = 0; h < 2; ++h) cp16(smem_addr(q_sm + i * Ring<D, T8>::q_slab + sw(col, 2 * l4 + h)), from + 64 * i + 8 * h, true);
+      for (uint32_t i = 0; i < 2 * P; ++i) cp16(smem_addr(piece(col, i)), q + 64 * (i / 2) + 8 * (i % 2), true);
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
     if constexpr (T8) {
+      // The rotated q over the power of two of its largest value, as hi + lo f16: hi through this memory into tensor memory, a thread
+      // half of its row, then lo in its place. Meanwhile lo lies where O will (registers that went to local memory, and barriers
+      // of all 256 threads: chunks of 100 to 257 rows 70 us, with this 68).
+      constexpr uint32_t W = 16, N = D == 256 ? 2 : 1;  // words at once, times (D = 64: half of them are lo)
+      const uint32_t aside = o_col() + half * (D / 2);
+      if (row / 32 * 32 < cols) {
 #pragma unroll 1
-      for (uint32_t c0 = 0; c0 < cols; c0 += PER) {
-        const uint32_t col = c0 + tid / 4;
-        float2 x[D / 8];
-        float mx = 0.f;
+        for (uint32_t k = 0; k < TIMES && from - lane / 4 + STEP * k < cols; ++k) {
+          const uint32_t col = from + STEP * k;
+          float2 x[D / 8];
+          float mx = 0.f;
 #pragma unroll
-        for (uint32_t i = 0; i < 2 * P; ++i) {
-          const uint4 u = col < cols ? *reinterpret_cast<const uint4*>(q_sm + i / 2 * Ring<D, T8>::q_slab + sw(col, 2 * l4 + i % 2))
-                                     : make_uint4(0u, 0u, 0u, 0u);
-          x[4 * i] = make_float2(bf16lo(u.x), bf16hi(u.x));
-          x[4 * i + 1] = make_float2(bf16lo(u.y), bf16hi(u.y));
-          x[4 * i + 2] = make_float2(bf16lo(u.z), bf16hi(u.z));
-          x[4 * i + 3] = make_float2(bf16lo(u.w), bf16hi(u.w));
+          for (uint32_t i = 0; i < 2 * P; ++i) {
+            const uint4 u = col < cols ? *piece(col, i) : make_uint4(0u, 0u, 0u, 0u);
+            x[4 * i] = make_float2(bf16lo(u.x), bf16hi(u.x));
+            x[4 * i + 1] = make_float2(bf16lo(u.y), bf16hi(u.y));
+            x[4 * i + 2] = make_float2(bf16lo(u.z), bf16hi(u.z));
+            x[4 * i + 3] = make_float2(bf16lo(u.w), bf16hi(u.w));
+          }
+          wht_quad<D>(x, lane);
+#pragma unroll
+          for (uint32_t i = 0; i < D / 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+          mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+          const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127, -126), 126);
+          const float f = pow2(-e2);
+          if (l4 == 0 && col < cols) sh.q_scale[col] = pow2(e2);
+#pragma unroll
+          for (uint32_t n = 0; n < N; ++n) {
+            uint32_t lo[W] = {};
+#pragma unroll
+            for (uint32_t i = 0; i < 2 * P / N; ++i) {
+              uint32_t hi[4];
+#pragma unroll
+              for (uint32_t j = 0; j < 4; ++j) {
+                const float2 y = x[4 * (i + n * (2 * P / N)) + j];
+                const float u = y.x * f, v = y.y * f;
+                hi[j] = pack_f16(u, v);
+                const float2 back = __half22float2(*reinterpret_cast<const __half2*>(&hi[j]));
+                lo[4 * i + j] = pack_f16(u - back.x, v - back.y);
+              }
+              if (col < cols) *piece(col, i + n * (2 * P / N)) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+            }
+            tm_st16(aside + W * (N * k + n), lo);
+          }
         }
-        wht_quad<D>(x, lane);
+        named_barrier(pair, 64);
+#pragma unroll 1
+        for (uint32_t w = half * (D / 4); w < (half + 1) * (D / 4); w += W) {
+          uint32_t r[W];
 #pragma unroll
-        for (uint32_t i = 0; i < D / 8; ++i) mx = fmaxf(mx, fmaxf(fabsf(x[i].x), fabsf(x[i].y)));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        const int e2 = min(max((int)((__float_as_uint(mx) >> 23) & 255) - 127, -126), 126);
-        const float f = pow2(-e2);
-        if (l4 == 0 && col < cols) sh.q_scale[col] = pow2(e2);
+          for (uint32_t k = 0; k < W / 4; ++k) {
+            const uint32_t j = w / 4 + k;
+            const uint4 u = *reinterpret_cast<const uint4*>(q_sm + j / 8 * Ring<D, T8>::q_slab + sw(row, j % 8));
+            r[4 * k] = u.x, r[4 * k + 1] = u.y, r[4 * k + 2] = u.z, r[4 * k + 3] = u.w;
+          }
+          tm_st16(tmem + 128 + w, r);
+        }
+        tm_stored();
+        named_barrier(pair, 64);
+#pragma unroll 1
+        for (uint32_t k = 0; k < TIMES && from - lane / 4 + STEP * k < cols; ++k) {
+          const uint32_t col = from + STEP * k;
 #pragma unroll
-        for (uint32_t i = 0; i < 2 * P; ++i)
-          if (col < cols)
-            *reinterpret_cast<uint4*>(q_sm + i / 2 * Ring<D, T8>::q_slab + sw(col, 2 * l4 + i % 2)) =
-                make_uint4(pack_f16(x[4 * i].x * f, x[4 * i].y * f), pack_f16(x[4 * i + 1].x * f, x[4 * i + 1].y * f),
-                           pack_f16(x[4 * i + 2].x * f, x[4 * i + 2].y * f), pack_f16(x[4 * i + 3].x * f, x[4 * i + 3].y * f));
+          for (uint32_t n = 0; n < N; ++n) {
+            uint32_t lo[W];
+            tm_ld16(aside + W * (N * k + n), lo);
+            tm_loaded(lo);
+#pragma unroll
+            for (uint32_t i = 0; i < 2 * P / N; ++i)
+              if (col < cols) *piece(col, i + n * (2 * P / N)) = make_uint4(lo[4 * i], lo[4 * i + 1], lo[4 * i + 2], lo[4 * i + 3]);
+          }
+        }
       }
+      tm_before_sync();
     }
     tm_fence_shared();
     arrive_warp(&sh.q_full, lane);
@@ -965,7 +1054,7 @@ struct Softmax {
       for (int i = 0; i < 32; ++i) s[i] = __uint_as_float(r[i]);
       tm_before_sync();
     }
-    arrive_warp(&sh.s_free[n & 1], lane);
+    if (!T8) arrive_warp(&sh.s_free[n & 1], lane);
     if (busy) {
       if constexpr (T8) {
         const float sc = scale * (live ? sh.q_scale[row] : 0.f);
@@ -1002,6 +1091,7 @@ struct Softmax {
       }
       sh.top[n & 1][half][row] = top;
       named_barrier(pair, 64);
+      if (T8) tm_after_sync();  // both halves of S have been loaded: P may come
       const float2 other = sh.top[n & 1][half ^ 1][row];
       top.x = fmaxf(top.x, other.x);
       top.y = fmaxf(top.y, other.y);
@@ -1051,7 +1141,7 @@ struct Softmax {
         tm_after_sync();
         rescale_o(f);
       }
-      // the product that read this P two tiles ago was issued before these scores', whose arrival covers it
+      // bf16: the product that read this P two tiles ago was issued before these scores', whose arrival covers it
       uint32_t h[16];
       if constexpr (T8) {
 #pragma unroll
@@ -1180,8 +1270,8 @@ __device__ __forceinline__ void issue(const RowsAttend& a, const uint32_t* first
     wait(&sh.p_full[i & 1], (i >> 1) & 1);
     tm_after_sync();
     tm_fence_shared();
-    const uint32_t p = tmem + 128 + (i & 1) * 64;
-    const uint64_t dv = tm_desc(ring + v.slot * Ring<D, T8>::bytes, Ring<D, T8>::slab, 1024);
+    const uint32_t p = tmem + (T8 ? 0 : 128) + (i & 1) * 64;
+    const uint64_t dv = tm_desc(ring + Ring<D, T8>::at(v.slot), Ring<D, T8>::slab, 1024);
     if (elect_one()) {
 #pragma unroll
       for (uint32_t k = 0; k < kTile / 16; ++k) {
@@ -1198,15 +1288,30 @@ __device__ __forceinline__ void issue(const RowsAttend& a, const uint32_t* first
     for (uint32_t t = s.t0; t < s.t1; ++t, ++n) {
       const Place<D, T8> k(2 * n);
       wait(&sh.full[k.slot], k.turn & 1);
-      if (n >= 2) wait(&sh.s_free[n & 1], ((n - 2) >> 1) & 1);
+      if (!T8) {
+        if (n >= 2) wait(&sh.s_free[n & 1], ((n - 2) >> 1) & 1);
+      } else if (t - s.t0 >= 2) {  // P of the tile before the last lay there; an item's first two tiles come after q, and that after all
+        const Place<D, T8> v(2 * n - 3);
+        wait(&sh.empty[v.slot], v.turn & 1);
+      }
       tm_after_sync();
       tm_fence_shared();
-      const uint64_t dk = tm_desc(ring + k.slot * Ring<D, T8>::bytes, 16, 1024);
+      const uint64_t dk = tm_desc(ring + Ring<D, T8>::at(k.slot), 16, 1024);
+      const uint32_t to = tmem + (n & 1) * kTile;
+      const auto q_at = [](uint32_t i) { return ((i / 4) * Ring<D, T8>::q_slab + (i % 4) * 32) / 16; };  // descriptors count in 16 bytes
+      const auto k_at = [](uint32_t i) { return ((i / 4) * Ring<D, T8>::slab + (i % 4) * 32) / 16; };
       if (elect_one()) {
+        if constexpr (T8) {  // the small terms first: q's lower part and the scales' last bits
 #pragma unroll
-        for (uint32_t i = 0; i < D / 16; ++i)  // descriptors count in 16 bytes
-          tm_mma(tmem + (n & 1) * kTile, dq + ((i / 4) * Ring<D, T8>::q_slab + (i % 4) * 32) / 16,
-                 dk + ((i / 4) * Ring<D, T8>::slab + (i % 4) * 32) / 16, kQK, i != 0);
+          for (uint32_t i = 0; i < D / 16; ++i) tm_mma(to, dq + q_at(i), dk + k_at(i), kQK, i != 0);
+#pragma unroll
+          for (uint32_t i = 0; i < D / 16; ++i) tm_mma_ta(to, tmem + 128 + 8 * i, dk + Ring<D, T8>::bytes / 16 + k_at(i), kQK, true);
+#pragma unroll
+          for (uint32_t i = 0; i < D / 16; ++i) tm_mma_ta(to, tmem + 128 + 8 * i, dk + k_at(i), kQK, true);
+        } else {
+#pragma unroll
+          for (uint32_t i = 0; i < D / 16; ++i) tm_mma(to, dq + q_at(i), dk + k_at(i), kQK, i != 0);
+        }
         tm_commit(&sh.s_full[n & 1]);
         mbar_arrive(&sh.s_full[n & 1]);  // passes the loaders' notes on
         tm_commit(&sh.empty[k.slot]);
@@ -1238,7 +1343,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   uint8_t* ring = q_sm + Ring<D, T8>::q;
   Notes<D>& sh = *reinterpret_cast<Notes<D>*>(q_sm + Ring<D, T8>::all);
   uint32_t* first = reinterpret_cast<uint32_t*>(&sh + 1);  // [n_rows + 1]
-  RowNote* note = notes_of(first, a.r.n_rows);
+  RowNotes notes(a, first);
   if (tid == 0) {
     for (uint32_t i = 0; i < Ring<D, T8>::slots; ++i) {
       mbar_init(&sh.full[i], T8 ? kLoaders : kLoadThreads + (i % 2 == 0));
@@ -1278,7 +1383,7 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
       v = block_of(a, r, rows, x).tiles() + kLead;
       x.bits |= rows << 23;
     }
-    note[r] = x;
+    notes.put(r, x);
     return v;
   };
   Rows here = a.r;
@@ -1338,11 +1443,14 @@ __global__ void __launch_bounds__(kRowsThreads, 1) rows_kernel(const __grid_cons
   const Work work = work_of(a.work, a.r.n_rows, a.H, D);
   // every row's record for the join
   for (uint32_t i = blockIdx.x * kRowsThreads + tid; i < a.r.n_rows * a.c.Hkv; i += gridDim.x * kRowsThreads) {
-    const uint32_t r = i / a.c.Hkv, g = i % a.c.Hkv, off = note[r].index() % RB;
+    const uint32_t r = i / a.c.Hkv, g = i % a.c.Hkv;
+    const RowNote x = notes.without_pos(r);
+    const uint32_t off = x.index() % RB;
+    const RowNote start = notes.without_pos(off <= r ? r - off : r);
     uint32_t rec = 0;
-    if (note[r].ok() && off <= r && note[r - off].seq() == note[r].seq() && off < note[r - off].rows()) {
+    if (x.ok() && off <= r && start.seq() == x.seq() && off < start.rows()) {
       const uint32_t b = r - off, length = first[b + 1] - first[b], w = first[b] * a.c.Hkv + g * length;
-      rec = (w + kLead) / per | ((w + length - 1) / per) << 8 | off << 16 | (note[b].rows() - 1u) << 23 | kRecOk;
+      rec = (w + kLead) / per | ((w + length - 1) / per) << 8 | off << 16 | (start.rows() - 1u) << 23 | kRecOk;
     }
     work.rec[i] = rec;
   }
@@ -1411,20 +1519,23 @@ __global__ void __launch_bounds__(256, 5) join_kernel(const __grid_constant__ Ro
                       in ? (size_t)(r - off) * a.H + h / group * cols : 0, sums, [] { __syncthreads(); });
 }
 
+constexpr uint32_t kSmemMost = 227 * 1024;
 template <int D, bool T8>
-constexpr uint32_t smem_of(uint32_t n_rows) {
-  return 1024 + Ring<D, T8>::all + sizeof(Notes<D>) + (n_rows + 2) / 2 * 8 + n_rows * sizeof(RowNote);
+constexpr uint32_t smem_of(uint32_t n_rows, bool near) {
+  return 1024 + Ring<D, T8>::all + sizeof(Notes<D>) + rows_bytes(n_rows, near);
 }
 template <int D, bool T8>
 bool allow() {
-  static_assert(smem_of<D, T8>(kMaxQueries) <= 227 * 1024, "shared memory of a CTA");
-  return cudaFuncSetAttribute(rows_kernel<D, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem_of<D, T8>(kMaxQueries)) == cudaSuccess;
+  static_assert(smem_of<D, T8>(kMaxQueries, T8 && D == 256 ? false : true) <= kSmemMost, "shared memory of a CTA");
+  return cudaFuncSetAttribute(rows_kernel<D, T8>, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemMost) == cudaSuccess;
 }
 
 template <int D, bool T8>
-cudaError_t launch(const RowsAttend& a, cudaStream_t st) {
+cudaError_t launch(RowsAttend& a, cudaStream_t st) {
   static_assert(2 * kMaxSeqs * 4 + 4 <= Ring<64, true>::all - Ring<64, true>::q, "the rows' places");
-  cudaError_t e = launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D, T8>(a.r.n_rows), st, a);
+  a.near = smem_of<D, T8>(a.r.n_rows, true) <= kSmemMost;
+  cudaError_t e =
+      launch_early(rows_kernel<D, T8>, dim3(std::min(a.sms, kMaxCtas)), kRowsThreads, smem_of<D, T8>(a.r.n_rows, a.near), st, a);
   if (e != cudaSuccess) return e;
   if (a.here) return cudaSuccess;
   // Up to eight warps a column, as long as the SMs hold all CTAs at once, four each (64 nodes over 8191 tokens, one after another:

@@ -51,6 +51,7 @@ struct RowsAttend {
   uint16_t* out;         // [n_rows][H][D]
   uint32_t* tickets;     // [kMaxCtas], zero between calls
   bool here;             // set by rows_attend(): the parts are added up by the last CTA of an item, not by a second launch
+  bool near;             // set by rows_attend(): the rows' positions lie in shared memory
   uint8_t* work;         // rows_work_bytes
   bool wide;             // it is 32-byte aligned
   uint32_t sms;          // of the GPU

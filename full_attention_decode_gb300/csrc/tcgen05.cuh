@@ -74,6 +74,15 @@ __device__ __forceinline__ void tm_ld32(uint32_t a, uint32_t (&r)[32]) {
 __device__ __forceinline__ void tm_loaded(uint32_t (&r)[32]) {
   asm volatile("tcgen05.wait::ld.sync.aligned;" : Q35_M8(r, 0), Q35_M8(r, 8), Q35_M8(r, 16), Q35_M8(r, 24)::"memory");
 }
+__device__ __forceinline__ void tm_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : Q35_W8(r, 0), Q35_W8(r, 8)
+      : "r"(a));
+}
+__device__ __forceinline__ void tm_loaded(uint32_t (&r)[16]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;" : Q35_M8(r, 0), Q35_M8(r, 8)::"memory");
+}
 __device__ __forceinline__ uint32_t tm_ld1(uint32_t a) {
   uint32_t r;
   asm volatile("tcgen05.ld.sync.aligned.32x32b.x1.b32 {%0}, [%1];" : "=r"(r) : "r"(a));

@@ -632,10 +632,10 @@ QWEN35_API int qwen35_cache_append_rope(const qwen35_config* cfg, const qwen35_k
  * small its weight (NaN beside one of the other sign or a NaN; in qwen35_decode_attention it may be NaN alone); with a Turbo8
  * cache the head then holds what is no number.
  * Scores, maxima and sums are held in fp32 and the output is rounded to bf16 once. The weights enter the
- * products with V as two bf16 parts (2^-16) with a bf16 cache. With a Turbo8 cache the rotated q, the codes times
- * their scales and the weights are rounded to f16 (2^-11 each, the keys' and values' over a power of two of
- * the token's largest, 2^-25 of that at the least), so a score is off by up to 2^-10 of the sum of its
- * terms' sizes: for scores of usual size (below 100) far less than the codes' own 2^-4. Scores of a Turbo8 cache
+ * products with V as two bf16 parts (2^-16) with a bf16 cache. With a Turbo8 cache the rotated q is held
+ * to 2^-22 of a value or 2^-25 of its largest, codes times scales exactly (to 2^-25 of the power of two of the token's largest
+ * scale), each term of a score to 2^-18, the sums in fp32; V's codes times their scales and the weights are rounded to
+ * f16 (2^-11 each, V's over a power of two of the token's largest, 2^-25 of that at the least). Scores of a Turbo8 cache
  * are taken to lie within 2^20: beyond that the weights' exponents are no longer held to a part of one. */
 QWEN35_API int qwen35_tree_attention(const qwen35_config* cfg, const qwen35_kv_cache* kv, const qwen35_cache_rows* rows,
                                      const int32_t* parent, const qwen35_bf16* q, const qwen35_bf16* gate,

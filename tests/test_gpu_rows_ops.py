@@ -22,6 +22,7 @@ from full_attention_decode_gb300 import synth
 from oracle import qwen35_oracle as O
 
 from test_gpu_cache_ops import BF16, HEADS, TURBO8, Setup, bf16, f64
+from test_gpu_cache_ranges import put
 
 pytestmark = pytest.mark.gpu
 
@@ -1079,4 +1080,126 @@ def test_every_value_infinite(kind, sign):
     assert (call() == sign * float("inf")).all()
     s.t["v"][s.at(0, 777)] = -sign * float("inf")
     assert torch.isnan(call()).all()
+    assert status(s) == 0
+
+
+# ---------------------------------------------------------------- Turbo8: large scores
+#
+# Tolerances, derived before the first run. The rotated q is held to 2^-22 of a value or 2^-25 of its largest, a key's code times
+# its scale exactly (down to 2^-25 of 2^E, the power of two of the token's largest scale), as a product with the scale's upper seven
+# bits and one with its last, whose product with q's lower part (2^-7 2^-11 of a term) is left out. The small terms are added first, so
+# a score is a sum of D / 16 + 4 fp32 steps of 2^-23 each of at most sum |q_d k_d|, and 2 D / 16 more of 2^-6 of that: for D = 256
+# 20 2^-23 + 2^-24 + 2^-18 + 2^-22 + 2^-21 < 2^-17, so 2^-17 sum |q_d k_d| / sqrt D = d in all.
+# A weight and a value lose 2^-11 each, so a row is off by 2^-8 |y| (its rounding) and (2 d + 2^-10) max |v|; roundings are of either
+# sign, so the whole output's 2-norm is held to 2^-8 + 2^-9 of the reference's, as everywhere in this file.
+
+
+def along_one(s, scores, noise=0.05):
+    """Keys and queries along one direction a kv-head, with noise; scores of about `scores` (natural units)."""
+    rng = np.random.default_rng(23)
+    u = rng.standard_normal((s.Hkv, s.D))
+    a = scores / np.sqrt(s.D)  # |u|^2 is about D
+    q = np.repeat(u, s.H // s.Hkv, 0)
+    s.q = bf16(a * (q + noise * rng.standard_normal((s.n_rows, s.H, s.D))))
+    for b, m in enumerate(s.lens):
+        put(s, "k", b, u + noise * rng.standard_normal((m, s.Hkv, s.D)))
+
+
+def check_scores(s, out, see):
+    got, refs = f64(out), {}
+    for row, b, p in s.each_row():
+        at, i = s.at(b, np.asarray(see(b, row - s.start[b], p))), row - s.start[b]
+        ref, tol = np.zeros((s.H, s.D)), np.zeros((s.H, 1))
+        for h in range(s.H):
+            k, v = (s.stands[n][at, h // (s.H // s.Hkv)] for n in "kv")
+            q = f64(s.q[row, h])
+            x = k @ q / np.sqrt(s.D)
+            w = np.exp(x - x.max())
+            ref[h] = w / w.sum() @ v
+            d = 2.0 ** -17 * (np.abs(O.wht(k)) @ np.abs(O.wht(q))).max() / np.sqrt(s.D)
+            tol[h] = (2 * d + 2.0 ** -10) * np.linalg.norm(v, axis=-1).max()
+        assert (np.abs(got[row] - ref) <= 2.0 ** -8 * np.abs(ref) + tol).all(), (row, np.abs(got[row] - ref).max(), tol.max())
+        refs[row] = ref
+    a, b = (np.stack([x[r] for r in sorted(refs)]) for x in (got, refs))
+    err = np.linalg.norm(a - b) / np.linalg.norm(b)
+    assert err <= 2.0 ** -8 + 2.0 ** -9, err
+    return err
+
+
+@pytest.mark.parametrize("heads", ["4b", "tiny_alt", "tiny", "wide", "twelve"])
+@pytest.mark.parametrize("scores", [4.0, 64.0, 1024.0, 4096.0])
+@pytest.mark.parametrize("kind", ["tree", "all", "near"])
+def test_turbo8_scores_of_any_size(heads, scores, kind):
+    s = setup(heads, TURBO8, [500 + 20, 65 + 1, 1300 + 3], [20, 1, 3], page=16)
+    along_one(s, scores)
+    call, see = under(s, kind)
+    check_scores(s, call(), see)
+    assert status(s) == 0
+
+
+@pytest.mark.parametrize("heads", ["4b", "tiny", "tiny_alt"])
+@pytest.mark.parametrize("token", [0, 63, 64, 255, 511, 518, 519])
+@pytest.mark.parametrize("kind", ["tree", "all"])
+def test_turbo8_one_key_far_ahead_of_the_others(heads, token, kind):
+    """The output is its value: other weights are below e^-60."""
+    s = setup(heads, TURBO8, [519 + 2], [2], page=16)
+    u = np.sign(s.rng.standard_normal((s.Hkv, s.D)))
+    k = 0.1 * s.rng.standard_normal((521, s.Hkv, s.D))
+    k[token] = 8 * u
+    put(s, "k", 0, k)
+    s.q = bf16(np.broadcast_to(np.repeat(u, s.H // s.Hkv, 0), (s.n_rows, s.H, s.D))).contiguous()
+    call, see = under(s, kind)
+    got = f64(call())
+    for row in range(2):
+        if token in see(0, row, 519 + row):
+            v = np.repeat(s.stands["v"][s.at(0, token)], s.H // s.Hkv, 0)
+            assert (np.abs(got[row] - v) <= 2.0 ** -8 * np.abs(v) + 2.0 ** -10 * np.linalg.norm(v, axis=-1).max()).all()
+
+
+@pytest.mark.parametrize("heads", ["4b", "tiny_alt", "twelve"])
+@pytest.mark.parametrize("scores", [4.0, 64.0, 1024.0, 4096.0])
+def test_turbo8_chains_are_decode_attention(heads, scores):
+    """Both are within their own bounds of float64 (2^-8 + 2^-9 of the norm each), so within twice that of each other; and the
+    tree's error is not above the decode attention's by more than the roundings of the weights and values, 2^-10."""
+    s = setup(heads, TURBO8, [900, 77], [6, 2], page=16)
+    along_one(s, scores)
+    parents = [[-1, 0, 1, 2, 3, 4], [-1, 0]]
+    see = lambda b, i, p: list(range(p + 1))  # noqa: E731
+    out, other = run_tree(s, parents), blank(s)
+    scratch = B.new_scratch(B.qwen35_cache_scratch_bytes(s.cfg, s.cap, 0, s.n_rows))
+    assert B.qwen35_decode_attention(s.cfg, s.kv, s.r, s.q.cuda(), other, scratch) == 0
+    a, b = check_scores(s, out, see), check_scores(s, other, see)
+    assert a <= b + 2.0 ** -10
+    x, y = f64(out), f64(other)
+    assert np.linalg.norm(x - y) <= 2 * (2.0 ** -8 + 2.0 ** -9) * np.linalg.norm(y)
+
+
+@pytest.mark.parametrize("n_seqs", [1000, 1700, 1800, 2048])
+def test_turbo8_rows_of_many_sequences(n_seqs):
+    """The most rows that a call may have, of sequences of their own: as a call of few of them."""
+    s = setup("twelve", TURBO8, [1 + 5 * i % 90 for i in range(n_seqs)], None, page=16)
+    out = run_window(s, 40, 2)
+    some = list(range(0, n_seqs, 97)) + [n_seqs - 1]
+    few = B.DeviceRows(s.pos[some].contiguous(), None, len(some), s.nb)
+    kv = B.qwen35_kv_cache(s.kv.k, s.kv.v, s.cap, s.kv.dtype, s.kv.k_scales, s.kv.v_scales, None, 16, 0)
+    table = s.table[some].contiguous()
+    kv.block_table = table.data_ptr()
+    other = torch.full((len(some), s.H, s.D), NAN, dtype=torch.bfloat16, device="cuda")
+    assert B.qwen35_window_attention(s.cfg, kv, few, 40, 2, s.q[some].cuda(), other, s.scratch) == 0
+    assert status(s) == 0
+    a, b = f64(out)[some], f64(other)
+    # the parts' cuts differ: two outputs of the same values, rounded once each
+    assert (np.abs(a - b) <= 2 * 2.0 ** -8 * np.abs(b) + 2.0 ** -9 * np.abs(b).max()).all()
+    check(s, torch.where(torch.isin(torch.arange(n_seqs, device="cuda"), torch.tensor(some, device="cuda"))[:, None, None], out,
+                         blank(s)), expect(s, lambda b, i, p: visible_window(p, 40, 2) if b in some else None))
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_the_most_rows_in_short_runs(fmt):
+    """2048 rows of 300 sequences, among them empty ones, with rows of none before and behind."""
+    rows = [i % 14 for i in range(300)]
+    s = setup("twelve", fmt, [r + 7 * i % 100 + 1 for i, r in enumerate(rows)], rows, page=16, lead=3, tail=2048 - 3 - sum(rows))
+    assert s.n_rows == 2048
+    out = run_window(s, 50, 3)
+    check(s, out, expect(s, lambda b, i, p: visible_window(p, 50, 3)))
     assert status(s) == 0
