@@ -1223,7 +1223,7 @@ struct Softmax {
     const size_t first = nat ? (size_t)st.b.row * a.H + st.g * cols : (size_t)blockIdx.x * kM;
     const uint32_t wide = nat ? cols : kM;
     float* to = (nat ? work.nat : work.cont) + first * D + row * 8;
-    float odd = 0.f;  // NaN of an infinity or a NaN
+    float2 odd[2] = {};  // NaN of an infinity or a NaN
     const auto write = [&] {
 #pragma unroll 1
       for (uint32_t c = half * (D / 2); c < (half + 1) * (D / 2); c += 32) {
@@ -1238,14 +1238,16 @@ struct Softmax {
           }
           if (!T8)
 #pragma unroll
-            for (uint32_t i = 0; i < 32; ++i) odd = fmaf(__uint_as_float(r[i]), 0.f, odd);
+            for (uint32_t i = 0; i < 32; i += 2)
+              odd[i / 2 % 2] = __ffma2_rn(make_float2(__uint_as_float(r[i]), __uint_as_float(r[i + 1])), make_float2(0.f, 0.f), odd[i / 2 % 2]);
         }
       }
     };
     write();
     if constexpr (!T8) {
       const bool number = live && !skip && l == l;  // else the row is NaN by its scores, or not written
-      if (__any_sync(0xffffffffu, number && odd != odd)) {
+      const float all = (odd[0].x + odd[0].y) + (odd[1].x + odd[1].y);
+      if (__any_sync(0xffffffffu, number && all != all)) {
         put_infinities<D>(a, st, half, number, p, line0, line1, o_col());
         write();
       }
