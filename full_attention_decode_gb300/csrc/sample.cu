@@ -432,16 +432,16 @@ __global__ void __launch_bounds__(kThreads, 1) sample_kernel(const __grid_consta
     if (bw <= goal && goal < bw + w * c) {
       sh.key = key;
       sh.nth = (uint32_t)((goal - bw) / w);
-      if (a.prob && me == 0) {
-        uint32_t e;
-        const u64 m = weight(g.table, scale, key, e);
-        a.prob[r] = ldexpf((float)m, kOne - 63 - (int)e) / (float)kept;
-      }
     }
   });
   // ---- its index: the nth token of that value, in the CTA that holds it
   auto read = cl.barrier_arrive();  // this CTA reads no other's counts any more
   const uint32_t key = sh.key;
+  if (a.prob && me == C - 1 && tid == kThreads - 1) {  // 53 bits, rounded once
+    uint32_t e;
+    const u64 m = weight(g.table, scale, key, e);
+    a.prob[r] = (float)(ldexp((double)m, kOne - 63 - (int)e) / (double)kept);
+  }
   uint32_t nth = sh.nth, before = 0, here = 0;
   for (uint32_t c = 0; c <= me; ++c) {
     before += here;

@@ -678,7 +678,8 @@ QWEN35_API int qwen35_cache_keep(const qwen35_config* cfg, const qwen35_kv_cache
  *    all n_rows draws), as qwen35_lm_head_greedy writes them; vocab at most 524160, n_rows at most 65536 (UNSUPPORTED above).
  *  - u fp32 [n_rows], from [0, 1) (outside: as its nearest end; NaN: 0); temperature, top_p, min_p fp32 [n_rows], top_k
  *    int32 [n_rows], each or NULL: 1, 1, 0 and 0. All in device memory, read when the kernel runs.
- *  - token int32 [n_rows], written; prob NULL, or fp32 [n_rows]: the token's probability among what was left.
+ *  - token int32 [n_rows], written; prob NULL, or fp32 [n_rows]: the token's probability among what was left, its weight over
+ *    their sum rounded once.
  * logits 16-byte aligned, the others 4-byte aligned. No scratch. Errors: INVALID_ARGUMENT, UNSUPPORTED, CUDA. */
 QWEN35_API int qwen35_sample(const qwen35_bf16* logits, uint32_t n_rows, uint32_t vocab, uint64_t row_stride,
                              const float* u, const float* temperature, const int32_t* top_k, const float* top_p,

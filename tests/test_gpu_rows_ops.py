@@ -1203,3 +1203,19 @@ def test_the_most_rows_in_short_runs(fmt):
     out = run_window(s, 50, 3)
     check(s, out, expect(s, lambda b, i, p: visible_window(p, 50, 3)))
     assert status(s) == 0
+
+
+@pytest.mark.parametrize("vocab", [3, 1000, 20000])
+def test_probabilities_are_rounded_once(vocab):
+    """A weight is good to 2^-40 of itself and the sum of what is left to 2^-45 a token, at least 1: with the one rounding to
+    fp32 2^-24 + 2^-40 + vocab 2^-45 of the probability; 2^-24 + 2^-30 for all vocabularies here."""
+    n = 400
+    rng = np.random.default_rng(vocab)
+    x = bf16(2 * rng.standard_normal((n, vocab))).cuda()
+    u, t, k = rng.random(n), (0.5 + rng.random(n)).astype(np.float32), rng.integers(0, vocab, n)
+    token, prob = run_sample(x, u, t=t, k=k)
+    host = f64(x)
+    for r in range(n):
+        want, q = plain_sample(host[r], float(np.float32(u[r])), float(t[r]), int(k[r]))
+        assert token[r] == want
+        assert abs(float(prob[r]) - q) <= (2.0 ** -24 + 2.0 ** -30) * q, (r, prob[r], q)
