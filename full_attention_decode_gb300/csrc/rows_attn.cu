@@ -17,8 +17,8 @@
 //
 // The line of all items' tiles is cut into equal stretches, one CTA an SM. A stretch leaves its sums and maxima in the
 // scratch, and an item's parts are added up in the order of the CTAs, so equal calls give equal bits. Few columns are
-// joined by the last of the item's CTAs; those of a block of many rows by a second launch, spread over the GPU: one CTA that
-// joined a block of 128 columns would read 2.5 MB.
+// joined by the last of the item's CTAs; those of a block of many rows, and of many items, by a second launch, spread over the GPU: one
+// CTA that joined a block of 128 columns would read 2.5 MB.
 //
 // What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 76 us,
 // 5.4 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8191 tokens: 31 us, 273 TFLOP/s, where
@@ -1562,9 +1562,11 @@ cudaError_t rows_attend_attributes() {
 
 cudaError_t rows_attend(const RowsAttend& args, cudaStream_t st) {
   RowsAttend a = args;
-  // Eight columns, one for each warp of the softmax, are joined where their last part is made (one row through a window of 512:
-  // 13.7 us, by a second launch 15.1; 32 rows through windows of 128 15.2 and 18.1; 1024 rows through windows of 64 273 and 263); more columns by CTAs of their own.
-  a.here = a.H / a.c.Hkv * (a.r.row_start ? a.r.n_rows : 1) <= 8;
+  // Eight columns, one for each warp of the softmax, are joined where their last part is made, as long as an SM has few items; more
+  // columns, and the many items of an SM, by CTAs of their own. Single rows (bf16, 4 kv-heads of 256) through windows of 64 and 512, here and by a
+  // second launch: 8 rows 12.7, 15.1 and 14.9, 16.4 us, 64 rows 23.2, 25.3 and 45.0, 46.5, 128 rows (3.4 items an SM) 39.7, 39.1 and 80.0, 78.0, 1024
+  // rows 245, 227 and 517, 494; one kv-head of 64, windows of 64: 256 rows 18.8, 19.9, 512 rows 32.0, 30.1.
+  a.here = a.H / a.c.Hkv * (a.r.row_start ? a.r.n_rows : 1) <= 8 && a.r.n_rows * a.c.Hkv < 3 * a.sms;
   const bool t8 = a.c.ks != nullptr;
 #define CALL(DD) return t8 ? launch<DD, true>(a, st) : launch<DD, false>(a, st)
   switch (a.c.D) {

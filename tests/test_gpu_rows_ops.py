@@ -1219,3 +1219,15 @@ def test_probabilities_are_rounded_once(vocab):
         want, q = plain_sample(host[r], float(np.float32(u[r])), float(t[r]), int(k[r]))
         assert token[r] == want
         assert abs(float(prob[r]) - q) <= (2.0 ** -24 + 2.0 ** -30) * q, (r, prob[r], q)
+
+
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("n", [151, 152, 153, 455, 456, 457])
+def test_single_rows_on_either_side_of_the_join(fmt, n):
+    """Few items an SM are joined inside the launch, many by a second one: the outputs of the same rows."""
+    s = setup("tiny", fmt, [1 + 37 * i % 400 for i in range(n)], None, page=16)
+    out = run_window(s, 150, 2)
+    check(s, out, expect(s, lambda b, i, p: visible_window(p, 150, 2)))
+    assert status(s) == 0
+    for _ in range(2):
+        assert torch.equal(run_window(s, 150, 2).view(torch.int16), out.view(torch.int16))
