@@ -804,49 +804,73 @@ __device__ __noinline__ void mend(const RowsAttend& a, const Block& b, uint32_t 
 
 // O of a stretch over a bf16 cache where infinities among V that its tiles hold as they lie have left NaN (hi and lo of a
 // weight times one, and 0 or less times one): every infinity and NaN among the values that a row sees is added to it, whatever its
-// weight, the first in the NaN's place. A warp's 32 rows and its half of O's columns, D / 64 a lane as V is looked through, a token
-// at a time; a column that every row holds for good is passed over. Rare, so plain and slow.
+// weight, the first in the NaN's place. A warp's 32 rows and its half of O's columns, D / 64 a lane as V is looked through, eight
+// tokens at a time (the CTA's other warps wait meanwhile, so a long stretch must not take their time limit); a column that every
+// row holds for good is passed over. Rare, so plain.
 template <int D>
 __device__ __noinline__ void put_infinities(const RowsAttend& a, const Stretch& st, uint32_t half, bool live, uint32_t p,
                                             uint64_t line0, uint64_t line1, uint32_t o_col) {
   constexpr uint32_t K = D / 64;
+  struct alignas(2 * K) Values {
+    uint16_t v[K];
+  };
   const Block& b = st.b;
   const uint32_t lane = threadIdx.x % 32, c0 = half * (D / 2);
   constexpr uint32_t kNone = 0x7fc00001u;  // a NaN that is the sum's own; the matrix unit's is 0x7fffffff
   uint32_t held = 0;  // two bits a column of the lane: what all rows have there, 1 and 2 an infinity of a sign, 3 NaN
-#pragma unroll 1
-  for (uint32_t i = st.t0 * kTile; i < min(st.t1 * kOctets, b.octets) * 8; ++i) {
-    const uint32_t tok = b.token(i / 8) + i % 8;
-    bool see;
+  const auto sees = [&](uint32_t tok) {
+    if (!live) return false;
     if (a.parent) {
       const uint32_t start = b.pos - b.index, off = tok - start;
-      see = tok < start || (off < 64 ? line0 >> off & 1 : off < 128 && (line1 >> (off - 64) & 1));
-    } else {
-      see = tok <= p && ((uint64_t)tok + a.window > p || tok < a.n_first);
+      return tok < start || (off < 64 ? line0 >> off & 1 : off < 128 && (line1 >> (off - 64) & 1));
     }
-    see &= live;
-    size_t row;
-    if (!__any_sync(0xffffffffu, see) || !cache_row(a.c, b.seq, tok, row)) continue;
-    const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v) + (row * a.c.Hkv + st.g) * D + c0 + lane * K;
+    return tok <= p && ((uint64_t)tok + a.window > p || tok < a.n_first);
+  };
 #pragma unroll 1
-    for (uint32_t e = 0; e < K; ++e) {
-      const float x = bf16f(v[e]);
-      const uint32_t has = held >> (2 * e) & 3u, want = x != x ? 3u : x > 0.f ? 1u : 2u;
-      uint32_t who = __ballot_sync(0xffffffffu, !(fabsf(x) < INFINITY) && has != 3u && has != want);
-      while (who) {
-        const uint32_t from = __ffs(who) - 1, col = o_col + c0 + from * K + e;
-        who &= who - 1;
-        const float y = __shfl_sync(0xffffffffu, x, from);
-        uint32_t u = tm_ld1(col);
-        if (see && u != kNone) {
-          const float o = __uint_as_float(u), sum = o == o ? o + y : y;
-          u = sum == sum ? __float_as_uint(sum) : kNone;
+  for (uint32_t o = st.t0 * kOctets; o < min(st.t1 * kOctets, b.octets); ++o) {
+    const uint32_t t0 = b.token(o);
+    size_t row;
+    if (!cache_row(a.c, b.seq, t0, row)) continue;  // pages hold whole octets
+    const uint16_t* v = reinterpret_cast<const uint16_t*>(a.c.v) + (row * a.c.Hkv + st.g) * D + c0 + lane * K;
+    Values x[8];
+    uint32_t seen = 0;
+    bool any = false;
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j) {
+      const bool one = __any_sync(0xffffffffu, sees(t0 + j));  // so the token is in the cache
+      seen |= (uint32_t)one << j;
+      x[j] = one ? *reinterpret_cast<const Values*>(v + (size_t)j * a.c.Hkv * D) : Values{};
+    }
+#pragma unroll
+    for (uint32_t j = 0; j < 8; ++j)
+#pragma unroll
+      for (uint32_t e = 0; e < K; ++e) any |= (x[j].v[e] & 0x7f80u) == 0x7f80u && (held >> (2 * e) & 3u) != 3u;
+    if (!__any_sync(0xffffffffu, any)) continue;
+#pragma unroll 1
+    for (uint32_t j = 0; j < 8; ++j) {
+      if (!(seen >> j & 1)) continue;
+      const bool see = sees(t0 + j);
+      const Values u8 = *reinterpret_cast<const Values*>(v + (size_t)j * a.c.Hkv * D);
+#pragma unroll
+      for (uint32_t e = 0; e < K; ++e) {
+        const float x = bf16f(u8.v[e]);
+        const uint32_t has = held >> (2 * e) & 3u, want = x != x ? 3u : x > 0.f ? 1u : 2u;
+        uint32_t who = __ballot_sync(0xffffffffu, !(fabsf(x) < INFINITY) && has != 3u && has != want);
+        while (who) {
+          const uint32_t from = __ffs(who) - 1, col = o_col + c0 + from * K + e;
+          who &= who - 1;
+          const float y = __shfl_sync(0xffffffffu, x, from);
+          uint32_t u = tm_ld1(col);
+          if (see && u != kNone) {
+            const float o = __uint_as_float(u), sum = o == o ? o + y : y;
+            u = sum == sum ? __float_as_uint(sum) : kNone;
+          }
+          tm_st1(col, u);
+          tm_stored();
+          const bool nan = __all_sync(0xffffffffu, !live || u == kNone);
+          const bool same = __all_sync(0xffffffffu, !live || __uint_as_float(u) == y);
+          if (lane == from) held = (held & ~(3u << (2 * e))) | (nan ? 3u : !same ? 0u : y > 0.f ? 1u : 2u) << (2 * e);
         }
-        tm_st1(col, u);
-        tm_stored();
-        const bool nan = __all_sync(0xffffffffu, !live || u == kNone);
-        const bool same = __all_sync(0xffffffffu, !live || __uint_as_float(u) == y);
-        if (lane == from) held = (held & ~(3u << (2 * e))) | (nan ? 3u : !same ? 0u : y > 0.f ? 1u : 2u) << (2 * e);
       }
     }
   }

@@ -1231,3 +1231,25 @@ def test_single_rows_on_either_side_of_the_join(fmt, n):
     assert status(s) == 0
     for _ in range(2):
         assert torch.equal(run_window(s, 150, 2).view(torch.int16), out.view(torch.int16))
+
+
+@pytest.mark.parametrize("value", [float("inf"), NAN])
+@pytest.mark.parametrize("last", [False, True])
+def test_long_stretches_without_a_number(value, last):
+    """700 000 tokens a sequence, one kv-head, ten rows: stretches of 46 000 tokens, all of whose values are no number, or
+    whose last one is. No wait runs out, and the outputs are those of the formula."""
+    H, Hkv, D = HEADS["tiny"]
+    cfg = B.make_config(synth.config("tiny") | dict(num_heads=H, num_kv_heads=Hkv, head_dim=D))
+    n, cap = 10, 700_000
+    k = torch.zeros(n * cap, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    v = torch.zeros_like(k) if last else torch.full_like(k, value)
+    pos = torch.full((n,), cap - 1, dtype=torch.int32, device="cuda")
+    if last:
+        v.view(n, cap, Hkv, D)[:, cap - 100] = value  # in a tile that is seen whole
+    kv = B.qwen35_kv_cache(k.data_ptr(), v.data_ptr(), cap, B.QWEN35_KV_BF16, None, None, None, 0, 0)
+    scratch = B.new_scratch(B.qwen35_rows_scratch_bytes(cfg, n))
+    q, out = torch.ones(n, H, D, dtype=torch.bfloat16, device="cuda"), torch.zeros(n, H, D, dtype=torch.bfloat16, device="cuda")
+    assert B.qwen35_window_attention(cfg, kv, B.DeviceRows(pos, None, n, 0), cap, 0, q, out, scratch) == 0
+    torch.cuda.synchronize()
+    assert B.qwen35_read_device_status(scratch) == 0
+    assert torch.isnan(out).all() if np.isnan(value) else (out == value).all()
