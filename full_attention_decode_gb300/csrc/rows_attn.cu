@@ -1186,8 +1186,11 @@ struct Softmax {
       tm_before_sync();
     }
     bool dirty = false;
+    // Before the arrival: behind it the slot may be filled again. Turbo8: of all warps, whether they have columns or not. With one place for V
+    // its arrival says that the product of the tile before is complete; without that a wait for this tile's product, which tells phases
+    // by their parity, could take the one before for it, and the next item's q would lie in O before O is made.
+    if (T8 || (busy && !all)) wait(&sh.full[pv.slot], pv.turn & 1);
     if (busy && (T8 || !all)) {  // bf16: the other tiles have not been looked through
-      wait(&sh.full[pv.slot], pv.turn & 1);  // before the arrival: behind it the slot may be filled again
       const uint2 u = *reinterpret_cast<const uint2*>(sh.dirty[n % Ring<D, T8>::info]);
       dirty = (u.x | u.y) != 0;
     }

@@ -1253,3 +1253,17 @@ def test_long_stretches_without_a_number(value, last):
     torch.cuda.synchronize()
     assert B.qwen35_read_device_status(scratch) == 0
     assert torch.isnan(out).all() if np.isnan(value) else (out == value).all()
+
+
+@pytest.mark.parametrize("heads", ["twelve", "4b", "tiny_alt"])
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+def test_equal_calls_give_equal_bits(heads, fmt):
+    """Blocks of few and of many columns one after another on a CTA, many times: a warp that has columns of one block and none of
+    the block before waits for the same products as the others."""
+    rows = [i % 14 * 3 % 40 for i in range(100)]
+    s = setup(heads, fmt, [r + 7 * i % 100 + 1 for i, r in enumerate(rows)], rows, page=16, lead=3)
+    assert s.n_rows <= 2048
+    first = run_window(s, 50, 3)
+    check(s, first, expect(s, lambda b, i, p: visible_window(p, 50, 3)))
+    differ = sum(not torch.equal(run_window(s, 50, 3).view(torch.int16), first.view(torch.int16)) for _ in range(200))
+    assert differ == 0 and status(s) == 0
