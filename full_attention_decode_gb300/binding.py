@@ -427,6 +427,11 @@ def qwen35_decode_attention(cfg, kv, rows, q, out, scratch, gate=None, gate_stri
                                          _ptr(scratch), scratch.numel(), _stream(stream))
 
 
+def _side_by_side(t, n):
+    if isinstance(t, torch.Tensor) and (t.numel() < n or not t.is_contiguous()):
+        raise ValueError(f"a value for each of {n} rows, side by side, not {tuple(t.shape)} at {t.stride()}")
+
+
 def qwen35_rows_scratch_bytes(cfg, max_rows: int) -> int:
     return lib().qwen35_rows_scratch_bytes(C.byref(cfg), max_rows)
 
@@ -434,6 +439,8 @@ def qwen35_rows_scratch_bytes(cfg, max_rows: int) -> int:
 def qwen35_cache_append_rope(cfg, kv, rows, q, k, v, q_out, scratch, q_norm=None, k_norm=None, q_stride: int = 0,
                              rope_pos=None, bounds=None, k_out=None, stream=None):
     """q, q_out may be None (keys and values alone). q_stride 0: the queries' rows lie head_dim apart."""
+    if rope_pos is not None:
+        _side_by_side(rope_pos, rows.struct.n_rows)
     return lib().qwen35_cache_append_rope(C.byref(cfg), C.byref(kv), C.byref(rows.struct), _ptr(rope_pos),
                                           C.byref(bounds.struct) if bounds is not None else None, _ptr(q),
                                           q_stride or cfg.head_dim, _ptr(q_norm), _ptr(k), _ptr(k_norm), _ptr(v),
@@ -441,6 +448,7 @@ def qwen35_cache_append_rope(cfg, kv, rows, q, k, v, q_out, scratch, q_norm=None
 
 
 def qwen35_cache_keep(cfg, kv, rows, path, scratch, bounds=None, stream=None):
+    _side_by_side(path, rows.struct.n_rows)
     return lib().qwen35_cache_keep(C.byref(cfg), C.byref(kv), C.byref(rows.struct),
                                    C.byref(bounds.struct) if bounds is not None else None, _ptr(path), _ptr(scratch),
                                    scratch.numel(), _stream(stream))
@@ -448,6 +456,7 @@ def qwen35_cache_keep(cfg, kv, rows, path, scratch, bounds=None, stream=None):
 
 def qwen35_tree_attention(cfg, kv, rows, parent, q, out, scratch, gate=None, gate_stride: int = 0, stream=None):
     """gate_stride 0: the gate's rows lie head_dim apart."""
+    _side_by_side(parent, rows.struct.n_rows)
     return lib().qwen35_tree_attention(C.byref(cfg), C.byref(kv), C.byref(rows.struct), _ptr(parent), _ptr(q),
                                        _ptr(gate), gate_stride or cfg.head_dim, _ptr(out), _ptr(scratch),
                                        scratch.numel(), _stream(stream))
@@ -473,6 +482,9 @@ def qwen35_sample(logits, u, token, temperature=None, top_k=None, top_p=None, mi
         stride = logits.stride(0) if n_rows > 1 else vocab
     else:  # a stand-in without a tensor's strides
         stride = max(logits.stride(0), vocab)
+    for t in (u, token, temperature, top_k, top_p, min_p, prob):
+        if t is not None:
+            _side_by_side(t, n_rows)
     return lib().qwen35_sample(_ptr(logits), n_rows, vocab, stride, _ptr(u), _ptr(temperature), _ptr(top_k), _ptr(top_p),
                                _ptr(min_p), _ptr(token), _ptr(prob), _stream(stream))
 

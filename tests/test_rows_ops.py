@@ -186,3 +186,38 @@ def test_sample_strides():
     assert call(3, 1) == call(3, 499) == call(1, 499) == BAD
     x = torch.zeros(1000).as_strided((3, 500), (250, 1))
     assert B.qwen35_sample(x, Y, Z, stream=0) == BAD
+
+
+@pytest.mark.parametrize("name", ["u", "token", "temperature", "top_k", "top_p", "min_p", "prob"])
+def test_sample_refuses_settings_that_do_not_lie_side_by_side(monkeypatch, name):
+    """One value expanded to all rows, every other value of a tensor, too few values: the C entry reads n_rows side by side."""
+    class _Lib:
+        qwen35_sample = staticmethod(lambda *_: 0)
+
+    monkeypatch.setattr(B, "lib", lambda: _Lib)
+
+    def call(t):
+        a = dict(u=torch.zeros(4), token=torch.zeros(4, dtype=torch.int32))
+        a[name] = t
+        return B.qwen35_sample(torch.zeros(4, 100), a.pop("u"), a.pop("token"), stream=0, **a)
+
+    one = torch.zeros(1, dtype=torch.int32 if name in ("token", "top_k") else torch.float32)
+    for bad in (one.expand(4), one, one.expand(8)[:4], torch.zeros(8)[::2], torch.zeros(4, 3)[:, 0], torch.zeros(3)):
+        with pytest.raises(ValueError):
+            call(bad)
+    assert call(torch.zeros(4)) == call(torch.zeros(9)[2:7]) == call(torch.zeros(4, 1)) == 0
+    assert B.qwen35_sample(torch.zeros(100), one.float(), one.int(), stream=0) == 0
+
+
+@no_device
+@pytest.mark.parametrize("bad", [torch.zeros(1, 3, dtype=torch.int32).expand(3, -1), torch.zeros(18, dtype=torch.int32)[::2],
+                                 torch.zeros(8, dtype=torch.int32)])
+def test_a_value_a_row_lies_side_by_side(bad):
+    """Parents, paths and positions of nine rows: one tree expanded to three sequences, every other value, too few."""
+    s, rows = _Fake(0x9000000, 1 << 40), _rows(n_rows=9, row_start=0x7100000)
+    for call in (lambda t: B.qwen35_tree_attention(_cfg(), _kv(), rows, t, Y, Z, s, stream=0),
+                 lambda t: B.qwen35_cache_keep(_cfg(), _kv(), rows, t, s, stream=0),
+                 lambda t: B.qwen35_cache_append_rope(_cfg(), _kv(), rows, X, Y, Z, W, s, rope_pos=t, stream=0)):
+        with pytest.raises(ValueError):
+            call(bad)
+        assert call(torch.zeros(3, 3, dtype=torch.int32)) == call(W) == OK_BUT_NO_DEVICE
