@@ -23,9 +23,10 @@
 // What bounds it (152 SMs, 16 q-heads over 4 kv-heads of 256). One token a sequence through windows of 4096, 32 sequences: 76 us,
 // 5.4 TB/s, 412 MB of K and V in pieces of 16 bytes. A tree of 64 nodes over 8191 tokens: 31 us, 273 TFLOP/s, where
 // seven tiles a CTA share with the way in and the join. Turbo8, 16 trees: 157 us, the chain of loader, products and softmax a
-// tile, 3.3 us: conversions and exponentials share a pipe (1 us), shared memory's bandwidth takes 1.4, the products 1.3. Scores of
-// one f16 q and one f16 K took 139: q's lower part costs 6 us, K's second part 4, the wait for P's product under the next S and
-// the way of q about 8.
+// tile, 3.3 us, with K and V in one place each beside q's lower part: shared memory's data path is busy half of the time, the issue
+// slots 40%, the tensor cores a third. With one f16 of q and of K it took 139: q's lower part costs 6 us, K's second part 4, two halves of a
+// tile ahead instead of three 1.5, the way of q into tensor memory 4, the wait for P's product before the next S over it the rest.
+// (K's second part in a place of its own, written in a second pass 174 us, held in registers 269.)
 //
 // Roundings. bf16: Q, K, V exactly, P as hi + lo bf16 (2^-16). Turbo8: the rotated q as hi + lo f16 over the power of two of its
 // largest value (2^-22 of a value or 2^-25 of the largest); K's codes times scale / 2^E, E the exponent of the token's largest
@@ -59,8 +60,8 @@ constexpr int kRegsLaunch = 96;
 constexpr int kRegsSoft = 112, kRegsLoad = 80;
 static_assert(8 * (kRegsSoft + kRegsLoad) <= 16 * kRegsLaunch, "no more than the block was launched with");
 constexpr uint32_t kHalf = kTile / 2;  // tokens of a thread
-// What an item's beginning and end cost a CTA, in tiles (1, 2, 4, 6: 64 nodes over 8191 tokens 33.3, 32.0, 29.3, 29.7 us, 16
-// Turbo8 trees 149, 143, 139, 141, 32 rows through windows of 4096 80.2, 78.6, 76.3, 77.0, of 128 -, 15.2, 18.7, 18.5), and the tiles of
+// What an item's beginning and end cost a CTA, in tiles (1, 2, 4, 6: 64 nodes over 8191 tokens 35.1, 33.5, 30.9, 31.3 us, 16
+// Turbo8 trees 164, 160, 156, 159, 32 rows through windows of 4096 79.8, 78.8, 76.7, 77.7, of 128 -, 15.2, 18.7, 18.5), and the tiles of
 // a stretch at least (1, 2, 3: a row through a window of 512 13.0, 13.5, 14.2, eight nodes over 1000 tokens 14.0, 14.7, 15.9).
 constexpr uint32_t kLead = 4, kLeast = 1;
 // How far a score may lie above what P and l refer to before O, in tensor memory, is read, scaled and written back: weights up to

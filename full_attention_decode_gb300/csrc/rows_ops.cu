@@ -92,9 +92,10 @@ constexpr uint32_t kTeams = kThreads / 4;
 constexpr uint32_t kRopeRows = 8;  // rows of a CTA at most
 
 // A CTA takes a few rows: their places and angles once for all heads, then four lanes a head's row, q-heads, then k, then v.
-// Bound by the instructions of norm, rotation and quantiser where there are many rows (five prompts of 700 to 4097 tokens into
-// Turbo8, 24 heads of 256: 99 us; a warp a head's row with its own angles 159), by the launch and the chain of loads of the place
-// where there are few (8 rows: 6.7 us).
+// Bound by the instructions of norm, rotation and quantiser and, as a team's items after its first are fetched where they are used, by
+// their loads' latency where there are many rows (five prompts of 700 to 4097 tokens into Turbo8, 24 heads of 256: 86 us, 99 with the
+// rows read back by qwen35_cache_read; a warp a head's row with its own angles 159 with it), by the launch and the chain of loads of the
+// place where there are few (8 rows: 6.0 us a call, 2.5 of them on the GPU).
 template <int D, bool T8>
 __global__ void __launch_bounds__(kThreads, 2) rope_kernel(const __grid_constant__ RopeAppend a, uint32_t rows) {
   constexpr int P = D / 64;

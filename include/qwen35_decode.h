@@ -585,7 +585,9 @@ QWEN35_API int qwen35_decode_attention(const qwen35_config* cfg, const qwen35_kv
  * the accepted path's rows moved together, attention through a sliding window, and the
  * next tokens sampled from logits. One step: qwen35_cache_append_rope (the tree's rows, rope_pos =
  * position of each node's level), qwen35_tree_attention, the head, qwen35_sample for every node, the
- * caller's choice of a path, qwen35_cache_keep. The pages leave all of it to the caller. Dims,
+ * caller's choice of a path, qwen35_cache_keep. That is a step of full-attention layers: the forwards of
+ * linear-attention layers advance one state in place, and nothing here runs them over a tree's branches or takes
+ * their state back to an accepted node. The pages leave all of it to the caller. Dims,
  * caches and rows are as for the cache operators above, with the same limits and errors.
  *
  * Scratch: qwen35_rows_scratch_bytes(cfg, rows of the largest call), made with
