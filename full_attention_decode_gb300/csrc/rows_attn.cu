@@ -715,7 +715,7 @@ __device__ __forceinline__ void join_columns(const RowsAttend& a, const Work& wo
   const float down = T8 ? finite_or_0(V) : 0.f;
   const auto factor = [&](const float4& y) {
     if (y.x == -INFINITY || (T8 && y.z == -INFINITY)) return 0.f;
-    return fmaxf(ex2(exponent(y) - down), T8 ? 0.f : 1.4e-45f);  // bf16: an infinity counts, however small its weight
+    return fmaxf(ex2(exponent(y) - down), 1.4e-45f);  // an infinity counts, however small its weight
   };
   const float own = factor(mine);
   float x[8] = {};

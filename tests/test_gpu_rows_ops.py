@@ -1267,3 +1267,34 @@ def test_equal_calls_give_equal_bits(heads, fmt):
     check(s, first, expect(s, lambda b, i, p: visible_window(p, 50, 3)))
     differ = sum(not torch.equal(run_window(s, 50, 3).view(torch.int16), first.view(torch.int16)) for _ in range(200))
     assert differ == 0 and status(s) == 0
+
+
+@pytest.mark.parametrize("heads", ["tiny", "4b"])
+@pytest.mark.parametrize("fmt", [BF16, TURBO8])
+@pytest.mark.parametrize("kind", ["tree", "all"])
+def test_infinite_values_of_parts_without_weight(heads, fmt, kind):
+    """The first half of the tokens scores 400 below the rest, so parts of it weigh nothing in 32 bits; one of its values is
+    infinite all the same: bf16 gives the infinity, Turbo8 no number in its head."""
+    s = setup(heads, fmt, [4000 + 3], [3], page=16)
+    call, see = under(s, kind)
+    s.q = bf16(np.full(s.q.shape, 2.0))
+    k = s.rng.standard_normal((4003, s.Hkv, s.D))
+    k[:2000] = -400.0 / 2 / np.sqrt(s.D)
+    put(s, "k", 0, k)
+    want = expect(s, see)
+    at, dim = int(s.at(0, 5)), s.D // 2 + 5
+    if fmt == BF16:
+        s.t["v"][at, 0, dim] = -float("inf")
+    else:
+        s.t["vs"][at, dim // 16] = bf16([float("inf")]).view(torch.int16).item()
+    got, g = f64(call()), s.H // s.Hkv
+    for r, (ref, tol) in want.items():
+        ok = np.abs(got[r] - ref) <= 2.0 ** -8 * np.abs(ref) + tol
+        if fmt == BF16:
+            assert (got[r, :g, dim] == -np.inf).all()
+            ok[:g, dim] = True
+        else:
+            assert not np.isfinite(got[r, :g]).any()
+            ok[:g] = True
+        assert ok.all()
+    assert status(s) == 0
