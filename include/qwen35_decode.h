@@ -631,8 +631,8 @@ QWEN35_API int qwen35_cache_append_rope(const qwen35_config* cfg, const qwen35_k
  * behind those, or with a parent that is none on the way to -1, sets QWEN35_ERR_DEVICE_RANGE and is
  * skipped. Keys and values that a row does not see leave no trace in it, infinities and NaN among them. A NaN
  * score makes the row's head NaN. An infinity that a row sees among the values of a bf16 cache is its output there, however
- * small its weight (NaN beside one of the other sign or a NaN; in qwen35_decode_attention it may be NaN alone); with a Turbo8
- * cache the head then holds what is no number.
+ * small its weight (NaN beside one of the other sign or a NaN; qwen35_decode_attention may give NaN for it); with a Turbo8
+ * cache the head then holds no number.
  * Scores, maxima and sums are held in fp32 and the output is rounded to bf16 once. The weights enter the
  * products with V as two bf16 parts (2^-16) with a bf16 cache. With a Turbo8 cache the rotated q is held
  * to 2^-22 of a value or 2^-25 of its largest, codes times scales exactly (to 2^-25 of the power of two of the token's largest
